@@ -18,6 +18,10 @@ EAGLE_MAX_CHILDREN = 16
 EAGLE_MAX_LAYERS = 128
 EAGLE_MAX_VOCAB = 32768
 
+EAGLE_MAX_ROPE_PAIRS = 64
+
+DTYPE_BF16, DTYPE_F32 = 0, 1
+ROPE_LINEAR, ROPE_BANDS, ROPE_RAMP = 1, 2, 3
 PHASE_ROOT, PHASE_FRONTIER, PHASE_FINAL = 0, 1, 2
 
 STATUS = {0: "EAGLE_OK", 1: "EAGLE_ERR_INVALID_ARG", 2: "EAGLE_ERR_SHAPE", 3: "EAGLE_ERR_ALIGN",
@@ -27,7 +31,7 @@ STATUS_CODE = {v: k for k, v in STATUS.items()}
 
 KERNEL_ID = {"all": -1, "gemm_fc": 0, "gemm_qkv": 1, "gemm_o": 2, "gemm_gateup": 3, "gemm_down": 4,
              "gemm_lm": 5, "draft_attn": 6, "select": 7, "tree": 8, "verify_attn": 9, "accept": 10,
-             "commit": 11, "prep": 12, "refresh": 13, "fuse": 14}
+             "commit": 11, "prep": 12, "refresh": 13, "fuse": 14, "append": 15, "chunk_attn": 16, "pages": 17}
 
 P = C.c_void_p
 I = C.c_int
@@ -107,6 +111,35 @@ class eagle_commit_out(C.Structure):
                 ("draft_len", P)]
 
 
+class eagle_rows(C.Structure):
+    _fields_ = [("row_start", P), ("n_rows", I)]
+
+
+class eagle_rope(C.Structure):
+    _fields_ = [("rot_dim", I), ("interleaved", I), ("mscale", C.c_float),
+                ("turn", C.c_uint64 * EAGLE_MAX_ROPE_PAIRS)]
+
+
+class eagle_rope_scaling(C.Structure):
+    _fields_ = [("kind", I), ("factor", C.c_double), ("low", C.c_double), ("high", C.c_double),
+                ("original_len", I), ("mscale", C.c_double)]
+
+
+class eagle_pages(C.Structure):
+    _fields_ = [("block_table", P), ("len", P), ("ref", P), ("scratch", P), ("n_seqs", I), ("per_seq", I),
+                ("block_size", I), ("n_blocks", I)]
+
+
+class eagle_pools(C.Structure):
+    """The layers' block pools, from lists of device addresses (empty: the tables alone)."""
+    _fields_ = [("n_layers", I), ("k", P), ("v", P)]
+
+    def __init__(self, k_layers=(), v_layers=()):
+        n = len(k_layers)
+        self.arrays = (P * max(n, 1))(*k_layers), (P * max(n, 1))(*v_layers)   # live as long as the struct
+        super().__init__(n, C.cast(self.arrays[0], P), C.cast(self.arrays[1], P))
+
+
 _lib = None
 
 
@@ -159,6 +192,15 @@ def _declare(L):
                                 C.POINTER(eagle_commit_out), P, C.POINTER(eagle_kv), P, P, P],
         "eagle_stamps_disable": [P, C.POINTER(I), I, C.POINTER(I)],
         "eagle_wait_selftest": [P, P, P],
+        "eagle_rope_plan": [C.POINTER(eagle_rope), I, I, I, C.c_double, C.POINTER(eagle_rope_scaling)],
+        "eagle_kv_append": [P, I, C.POINTER(eagle_rows), C.POINTER(eagle_rope), I, P, I, P, I, P, I, P, I,
+                            C.POINTER(eagle_kv), P, P, P, P],
+        "eagle_chunk_attn": [P, I, C.POINTER(eagle_rows), P, I, C.POINTER(eagle_kv), I, C.c_float, P, I, P, P],
+        "eagle_pages_init": [P, C.POINTER(eagle_pages), P, P],
+        "eagle_pages_fork": [P, C.POINTER(eagle_pages), I, P, P, P, P],
+        "eagle_pages_reserve": [P, C.POINTER(eagle_pages), C.POINTER(eagle_pools), P, P, P],
+        "eagle_pages_release": [P, C.POINTER(eagle_pages), P, P, P],
+        "eagle_pages_compact": [P, C.POINTER(eagle_pages), C.POINTER(eagle_pools), P, P],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -176,7 +218,9 @@ EXPORTED = ["eagle_create", "eagle_destroy", "eagle_workspace_init", "eagle_read
             "eagle_accept", "eagle_accept_from_probs",
             "eagle_commit", "eagle_trace_enable", "eagle_trace_read", "eagle_trace_disable",
             "eagle_stamps_enable", "eagle_stamps_disable", "eagle_draft_refresh", "eagle_fuse_features",
-            "eagle_launch_count", "eagle_wait_selftest"]
+            "eagle_launch_count", "eagle_wait_selftest", "eagle_rope_plan", "eagle_kv_append",
+            "eagle_chunk_attn", "eagle_pages_init", "eagle_pages_fork", "eagle_pages_reserve",
+            "eagle_pages_release", "eagle_pages_compact"]
 
 
 def _check(name: str, code: int):
@@ -294,6 +338,47 @@ def eagle_draft_refresh(ctx, batch, w, acc, cm, pos0, draft_kv, len_out, ws_ptr,
     _check("eagle_draft_refresh",
            lib().eagle_draft_refresh(ctx, batch, C.byref(w), C.byref(acc), C.byref(cm), pos0, C.byref(draft_kv),
                                      len_out, ws_ptr, stream))
+
+
+def eagle_rope_plan(head_dim: int, rot_dim: int, interleaved: int, theta: float, scaling=None) -> eagle_rope:
+    r = eagle_rope()
+    _check("eagle_rope_plan", lib().eagle_rope_plan(C.byref(r), head_dim, rot_dim, interleaved, theta,
+                                                    _ref(scaling)))
+    return r
+
+
+def eagle_kv_append(ctx, batch, rows, rope, dtype, q, ld_q, q_out, ld_q_out, k, ld_k, v, ld_v, kv, pos, len_out,
+                    ws_ptr, stream):
+    _check("eagle_kv_append",
+           lib().eagle_kv_append(ctx, batch, C.byref(rows), _ref(rope), dtype, q, ld_q, q_out, ld_q_out, k, ld_k, v,
+                                 ld_v, C.byref(kv), pos, len_out, ws_ptr, stream))
+
+
+def eagle_chunk_attn(ctx, batch, rows, q, ld_q, kv, window, scale, out, ld_out, ws_ptr, stream):
+    _check("eagle_chunk_attn",
+           lib().eagle_chunk_attn(ctx, batch, C.byref(rows), q, ld_q, C.byref(kv), window, scale, out, ld_out, ws_ptr,
+                                  stream))
+
+
+def eagle_pages_init(ctx, pages, ws_ptr, stream):
+    _check("eagle_pages_init", lib().eagle_pages_init(ctx, C.byref(pages), ws_ptr, stream))
+
+
+def eagle_pages_fork(ctx, pages, n, src, dst, ws_ptr, stream):
+    _check("eagle_pages_fork", lib().eagle_pages_fork(ctx, C.byref(pages), n, src, dst, ws_ptr, stream))
+
+
+def eagle_pages_reserve(ctx, pages, pools, n_new, ws_ptr, stream):
+    _check("eagle_pages_reserve",
+           lib().eagle_pages_reserve(ctx, C.byref(pages), C.byref(pools), n_new, ws_ptr, stream))
+
+
+def eagle_pages_release(ctx, pages, keep, ws_ptr, stream):
+    _check("eagle_pages_release", lib().eagle_pages_release(ctx, C.byref(pages), keep, ws_ptr, stream))
+
+
+def eagle_pages_compact(ctx, pages, pools, ws_ptr, stream):
+    _check("eagle_pages_compact", lib().eagle_pages_compact(ctx, C.byref(pages), C.byref(pools), ws_ptr, stream))
 
 
 def eagle_trace_enable(ctx, kernel: str, capacity: int):

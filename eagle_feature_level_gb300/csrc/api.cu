@@ -118,6 +118,7 @@ void layout(eagle_ctx* c) {
   }
   W.attn_part = take(records * (D.head_dim + 4) * 4);
   W.attn_cnt = take(static_cast<size_t>(2) * L.max_batch * D.n_kv_heads * 4);
+  W.pages = take(static_cast<size_t>(PAGES_LISTS) * L.max_batch * 4 + 256);
   W.total = off;
 }
 
@@ -184,6 +185,42 @@ eagle_status check_kv(const eagle_ctx* c, const eagle_kv* kv, bool paged = false
   EAGLE_REQUIRE(kv->cap <= c->lim.max_prefix, EAGLE_ERR_CAPACITY);
   EAGLE_REQUIRE(paged || kv->paging.block_table == nullptr, EAGLE_ERR_INVALID_ARG);
   return check_paging(&kv->paging, kv->cap);
+}
+
+// Packed rows of at least `width` elements at pitch ld.
+eagle_status check_packed(const void* p, int ld, long long width, int dtype) {
+  EAGLE_PTR(p);
+  EAGLE_REQUIRE(ld >= width, EAGLE_ERR_SHAPE);
+  EAGLE_REQUIRE(ld % (dtype == EAGLE_DTYPE_F32 ? 4 : 8) == 0, EAGLE_ERR_ALIGN);
+  return EAGLE_OK;
+}
+
+eagle_status check_rows(const eagle_rows* r) {
+  EAGLE_REQUIRE(r, EAGLE_ERR_INVALID_ARG);
+  EAGLE_PTR(r->row_start);
+  EAGLE_REQUIRE(r->n_rows >= 1, EAGLE_ERR_INVALID_ARG);
+  return EAGLE_OK;
+}
+
+eagle_status check_pages(const eagle_ctx* c, const eagle_pages* p) {
+  EAGLE_REQUIRE(p, EAGLE_ERR_INVALID_ARG);
+  EAGLE_PTR(p->block_table); EAGLE_PTR(p->len); EAGLE_PTR(p->ref); EAGLE_PTR(p->scratch);
+  EAGLE_REQUIRE(p->n_seqs >= 1 && p->n_seqs <= c->lim.max_batch, EAGLE_ERR_CAPACITY);
+  const int bs = p->block_size;
+  EAGLE_REQUIRE(bs >= 1 && (bs & (bs - 1)) == 0, EAGLE_ERR_INVALID_ARG);
+  EAGLE_REQUIRE(p->per_seq >= 1 && p->n_blocks >= 1 && p->n_blocks <= (1 << 30), EAGLE_ERR_INVALID_ARG);
+  EAGLE_REQUIRE(static_cast<long long>(p->per_seq) * bs <= c->lim.max_prefix, EAGLE_ERR_CAPACITY);
+  return EAGLE_OK;
+}
+
+eagle_status check_pools(const eagle_pools* p) {
+  EAGLE_REQUIRE(p, EAGLE_ERR_INVALID_ARG);
+  EAGLE_REQUIRE(p->n_layers >= 0 && p->n_layers <= EAGLE_MAX_LAYERS, EAGLE_ERR_CAPACITY);
+  EAGLE_REQUIRE(p->n_layers == 0 || (p->k && p->v), EAGLE_ERR_INVALID_ARG);
+  for (int l = 0; l < p->n_layers; ++l) {
+    EAGLE_PTR(p->k[l]); EAGLE_PTR(p->v[l]);
+  }
+  return EAGLE_OK;
 }
 
 eagle_status check_ws(const void* ws) {
@@ -705,8 +742,183 @@ eagle_status eagle_commit(eagle_ctx* ctx, int batch, const eagle_accept_out* acc
   return EAGLE_OK;
 }
 
+eagle_status eagle_rope_plan(eagle_rope* out, int head_dim, int rot_dim, int interleaved, double theta,
+                             const eagle_rope_scaling* sc) {
+  EAGLE_REQUIRE(out, EAGLE_ERR_INVALID_ARG);
+  EAGLE_REQUIRE(head_dim >= 2 && head_dim <= 2 * EAGLE_MAX_ROPE_PAIRS, EAGLE_ERR_SHAPE);
+  EAGLE_REQUIRE(rot_dim >= 2 && rot_dim <= head_dim && rot_dim % 2 == 0, EAGLE_ERR_SHAPE);
+  EAGLE_REQUIRE(std::isfinite(theta) && theta > 1.0, EAGLE_ERR_INVALID_ARG);
+  const double two_pi = 6.283185307179586476925286766559;
+  double mscale = 1.0, lo = 0.0, hi = 0.0;
+  if (sc) {
+    EAGLE_REQUIRE(sc->kind >= EAGLE_ROPE_LINEAR && sc->kind <= EAGLE_ROPE_RAMP, EAGLE_ERR_INVALID_ARG);
+    EAGLE_REQUIRE(std::isfinite(sc->factor) && sc->factor >= 1.0, EAGLE_ERR_INVALID_ARG);
+    EAGLE_REQUIRE(std::isfinite(sc->mscale) && sc->mscale >= 0.0, EAGLE_ERR_INVALID_ARG);
+    if (sc->kind != EAGLE_ROPE_LINEAR) {
+      EAGLE_REQUIRE(std::isfinite(sc->high) && sc->low > 0.0 && sc->low < sc->high, EAGLE_ERR_INVALID_ARG);
+      EAGLE_REQUIRE(sc->original_len >= 1, EAGLE_ERR_INVALID_ARG);
+    }
+    if (sc->kind == EAGLE_ROPE_RAMP) {
+      mscale = 1.0 + 0.1 * std::log(sc->factor);
+      const auto pair_of = [&](double turns) {
+        return rot_dim * std::log(sc->original_len / (two_pi * turns)) / (2.0 * std::log(theta));
+      };
+      lo = std::max(std::floor(pair_of(sc->high)), 0.0);
+      hi = std::min(std::ceil(pair_of(sc->low)), rot_dim - 1.0);
+    }
+    if (sc->mscale > 0.0) mscale = sc->mscale;
+  }
+  eagle_rope r;
+  std::memset(&r, 0, sizeof(r));
+  r.rot_dim = rot_dim;
+  r.interleaved = interleaved ? 1 : 0;
+  r.mscale = static_cast<float>(mscale);
+  for (int j = 0; j < rot_dim / 2; ++j) {
+    double f = std::pow(theta, -2.0 * j / rot_dim);
+    if (sc) {
+      double keep = 0.0;                     // share of the frequency that is not slowed
+      if (sc->kind == EAGLE_ROPE_BANDS)
+        keep = (sc->original_len * f / two_pi - sc->low) / (sc->high - sc->low);
+      else if (sc->kind == EAGLE_ROPE_RAMP)
+        keep = 1.0 - (j - lo) / std::max(hi - lo, 1e-3);
+      keep = std::min(std::max(keep, 0.0), 1.0);
+      f = f * keep + f / sc->factor * (1.0 - keep);
+    }
+    // f <= 1 radian a position: below half a turn
+    r.turn[j] = static_cast<uint64_t>(std::ldexp(f / two_pi, 64));
+  }
+  *out = r;
+  return EAGLE_OK;
+}
+
+eagle_status eagle_kv_append(eagle_ctx* ctx, int batch, const eagle_rows* rows, const eagle_rope* rope, int dtype,
+                             const void* q, int ld_q, void* q_out, int ld_q_out, const void* k, int ld_k,
+                             const void* v, int ld_v, const eagle_kv* kv, const int32_t* pos, int32_t* len_out,
+                             void* workspace, cudaStream_t stream) {
+  EAGLE_REQUIRE(ctx, EAGLE_ERR_INVALID_ARG);
+  EAGLE_REQUIRE(batch >= 1 && batch <= ctx->lim.max_batch, EAGLE_ERR_CAPACITY);
+  eagle_status st = check_rows(rows);
+  if (st != EAGLE_OK) return st;
+  const eagle_dims& D = ctx->dims;
+  EAGLE_REQUIRE(dtype == EAGLE_DTYPE_BF16 || dtype == EAGLE_DTYPE_F32, EAGLE_ERR_INVALID_ARG);
+  if (rope)
+    EAGLE_REQUIRE(rope->rot_dim >= 2 && rope->rot_dim <= D.head_dim && rope->rot_dim % 2 == 0, EAGLE_ERR_SHAPE);
+  const long long qd = static_cast<long long>(D.n_q_heads) * D.head_dim;
+  const long long kd = static_cast<long long>(D.n_kv_heads) * D.head_dim;
+  if (q) {
+    if ((st = check_packed(q, ld_q, qd, dtype)) != EAGLE_OK) return st;
+    if ((st = check_packed(q_out, ld_q_out, qd, dtype)) != EAGLE_OK) return st;
+    EAGLE_REQUIRE(q_out != q || ld_q_out == ld_q, EAGLE_ERR_INVALID_ARG);
+  } else {
+    EAGLE_REQUIRE(!q_out, EAGLE_ERR_INVALID_ARG);
+  }
+  if ((st = check_packed(k, ld_k, kd, dtype)) != EAGLE_OK) return st;
+  if ((st = check_packed(v, ld_v, kd, dtype)) != EAGLE_OK) return st;
+  if ((st = check_kv(ctx, kv, true)) != EAGLE_OK) return st;
+  if (pos) EAGLE_PTR(pos);
+  EAGLE_PTR(len_out);
+  EAGLE_REQUIRE(len_out != kv->len, EAGLE_ERR_INVALID_ARG);
+  if ((st = check_ws(workspace)) != EAGLE_OK) return st;
+  AppendLaunch A{};
+  A.batch = batch;
+  A.rows = rows;
+  A.rope = rope;
+  A.dtype = dtype;
+  A.q = q;
+  A.ld_q = ld_q;
+  A.q_out = q_out;
+  A.ld_qo = ld_q_out;
+  A.k = k;
+  A.ld_k = ld_k;
+  A.v = v;
+  A.ld_v = ld_v;
+  A.kv = kv;
+  A.pos = pos;
+  A.len_out = len_out;
+  A.status = ws_ptr<int>(workspace, ctx->ws.status);
+  EAGLE_CUDA(launch_append(ctx, A, stream));
+  return EAGLE_OK;
+}
+
+eagle_status eagle_chunk_attn(eagle_ctx* ctx, int batch, const eagle_rows* rows, const uint16_t* q, int ld_q,
+                              const eagle_kv* kv, int window, float scale, uint16_t* out, int ld_out,
+                              void* workspace, cudaStream_t stream) {
+  EAGLE_REQUIRE(ctx, EAGLE_ERR_INVALID_ARG);
+  EAGLE_REQUIRE(batch >= 1 && batch <= ctx->lim.max_batch, EAGLE_ERR_CAPACITY);
+  eagle_status st = check_rows(rows);
+  if (st != EAGLE_OK) return st;
+  const long long qd = static_cast<long long>(ctx->dims.n_q_heads) * ctx->dims.head_dim;
+  if ((st = check_packed(q, ld_q, qd, EAGLE_DTYPE_BF16)) != EAGLE_OK) return st;
+  if ((st = check_packed(out, ld_out, qd, EAGLE_DTYPE_BF16)) != EAGLE_OK) return st;
+  EAGLE_REQUIRE(out != q, EAGLE_ERR_INVALID_ARG);
+  if ((st = check_kv(ctx, kv, true)) != EAGLE_OK) return st;
+  EAGLE_REQUIRE(window >= 0, EAGLE_ERR_INVALID_ARG);
+  EAGLE_REQUIRE(std::isfinite(scale) && scale > 0.f, EAGLE_ERR_INVALID_ARG);
+  if ((st = check_ws(workspace)) != EAGLE_OK) return st;
+  EAGLE_CUDA(launch_chunk_attn(ctx, batch, rows, q, ld_q, kv, window, scale, out, ld_out, workspace, stream));
+  return EAGLE_OK;
+}
+
+eagle_status eagle_pages_init(eagle_ctx* ctx, const eagle_pages* pages, void* workspace, cudaStream_t stream) {
+  EAGLE_REQUIRE(ctx, EAGLE_ERR_INVALID_ARG);
+  eagle_status st = check_pages(ctx, pages);
+  if (st != EAGLE_OK) return st;
+  if ((st = check_ws(workspace)) != EAGLE_OK) return st;
+  EAGLE_CUDA(cudaMemsetAsync(pages->block_table, 0xff, static_cast<size_t>(pages->n_seqs) * pages->per_seq * 4, stream));
+  EAGLE_CUDA(cudaMemsetAsync(pages->len, 0, static_cast<size_t>(pages->n_seqs) * 4, stream));
+  EAGLE_CUDA(cudaMemsetAsync(pages->ref, 0, static_cast<size_t>(pages->n_blocks) * 4, stream));
+  return EAGLE_OK;
+}
+
+eagle_status eagle_pages_fork(eagle_ctx* ctx, const eagle_pages* pages, int n, const int32_t* src, const int32_t* dst,
+                              void* workspace, cudaStream_t stream) {
+  EAGLE_REQUIRE(ctx, EAGLE_ERR_INVALID_ARG);
+  eagle_status st = check_pages(ctx, pages);
+  if (st != EAGLE_OK) return st;
+  EAGLE_REQUIRE(n >= 1, EAGLE_ERR_INVALID_ARG);
+  EAGLE_REQUIRE(n <= pages->n_seqs, EAGLE_ERR_CAPACITY);
+  EAGLE_PTR(src); EAGLE_PTR(dst);
+  if ((st = check_ws(workspace)) != EAGLE_OK) return st;
+  EAGLE_CUDA(launch_pages_fork(ctx, *pages, n, src, dst, workspace, stream));
+  return EAGLE_OK;
+}
+
+eagle_status eagle_pages_reserve(eagle_ctx* ctx, const eagle_pages* pages, const eagle_pools* pools,
+                                 const int32_t* n_new, void* workspace, cudaStream_t stream) {
+  EAGLE_REQUIRE(ctx, EAGLE_ERR_INVALID_ARG);
+  eagle_status st = check_pages(ctx, pages);
+  if (st != EAGLE_OK) return st;
+  if ((st = check_pools(pools)) != EAGLE_OK) return st;
+  EAGLE_PTR(n_new);
+  if ((st = check_ws(workspace)) != EAGLE_OK) return st;
+  EAGLE_CUDA(launch_pages_reserve(ctx, *pages, *pools, n_new, workspace, stream));
+  return EAGLE_OK;
+}
+
+eagle_status eagle_pages_release(eagle_ctx* ctx, const eagle_pages* pages, const int32_t* keep, void* workspace,
+                                 cudaStream_t stream) {
+  EAGLE_REQUIRE(ctx, EAGLE_ERR_INVALID_ARG);
+  eagle_status st = check_pages(ctx, pages);
+  if (st != EAGLE_OK) return st;
+  EAGLE_PTR(keep);
+  if ((st = check_ws(workspace)) != EAGLE_OK) return st;
+  EAGLE_CUDA(launch_pages_release(ctx, *pages, keep, workspace, stream));
+  return EAGLE_OK;
+}
+
+eagle_status eagle_pages_compact(eagle_ctx* ctx, const eagle_pages* pages, const eagle_pools* pools, void* workspace,
+                                 cudaStream_t stream) {
+  EAGLE_REQUIRE(ctx, EAGLE_ERR_INVALID_ARG);
+  eagle_status st = check_pages(ctx, pages);
+  if (st != EAGLE_OK) return st;
+  if ((st = check_pools(pools)) != EAGLE_OK) return st;
+  if ((st = check_ws(workspace)) != EAGLE_OK) return st;
+  EAGLE_CUDA(launch_pages_compact(ctx, *pages, *pools, workspace, stream));
+  return EAGLE_OK;
+}
+
 eagle_status eagle_trace_enable(eagle_ctx* ctx, int kernel_id, int capacity) {
-  EAGLE_REQUIRE(ctx && capacity >= 1 && kernel_id >= -1 && kernel_id <= EAGLE_K_FUSE, EAGLE_ERR_INVALID_ARG);
+  EAGLE_REQUIRE(ctx && capacity >= 1 && kernel_id >= -1 && kernel_id <= EAGLE_K_PAGES, EAGLE_ERR_INVALID_ARG);
   TraceState& t = ctx->trace;
   while (static_cast<int>(t.events.size()) < 2 * capacity) {
     cudaEvent_t e;

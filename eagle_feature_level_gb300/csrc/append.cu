@@ -1,0 +1,287 @@
+// eagle_kv_append: rotary positions of a batch's new rows and their append to
+// a (paged) KV cache.
+//
+// Pair j of a head turns by position * f_j.  With f_j as a 64-bit fraction of
+// a turn the product mod 2^64 is the angle's exact fraction, one integer
+// multiplication; its top 32 bits as a signed number of turns in [-1/2, 1/2)
+// go to sincospif, whose error (2^-24 or so) is then all of the angle's.
+//
+// The work is a pass over the rows: each element read once, written once.  A
+// CTA takes a few rows: one warp per row finds its request and cache row, the
+// threads compute the rows' sines and cosines once into shared memory (every
+// head of a row shares them), then each thread moves units of 16 elements of
+// a head (8 pairs), 16 bytes a load.
+#include <algorithm>
+
+#include "internal.h"
+#include "common.cuh"
+#include "rows.cuh"
+
+namespace eagle {
+namespace {
+
+constexpr int AP_THREADS = 256;
+constexpr int AP_WARPS = AP_THREADS / 32;
+constexpr int AP_ROWS = AP_WARPS;            // rows of a CTA at most: a warp sets up each
+
+struct AppendParams {
+  PackedRows rows;
+  int tile;                // rows a CTA takes
+  int row_ctas;            // CTAs for rows; the rest set len_out, a warp per request
+  int hq, hkv, dh;
+  int rot, interleaved;
+  float mscale;
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  long long ld_q, ld_qo, ld_k, ld_v;
+  uint16_t* kc;
+  uint16_t* vc;
+  int cap;
+  const int32_t* len;
+  PagedKv paged;
+  const int32_t* pos;
+  int32_t* len_out;
+  int* status;
+  uint64_t* stamp;
+  uint64_t turn[EAGLE_MAX_ROPE_PAIRS];
+};
+
+__device__ __forceinline__ void load8(const uint16_t* p, float (&x)[8]) {
+  const uint4 w = *reinterpret_cast<const uint4*>(p);
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(u[i] << 16);
+    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), z = *reinterpret_cast<const float4*>(p + 4);
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = z.x; x[5] = z.y; x[6] = z.z; x[7] = z.w;
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  return f32_to_bf16(a) | (static_cast<uint32_t>(f32_to_bf16(b)) << 16);
+}
+__device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+}
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ float load1(const uint16_t* p) { return bf16_to_f32(*p); }
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+__device__ __forceinline__ void store1(uint16_t* p, float x) { *p = f32_to_bf16(x); }
+__device__ __forceinline__ void store1(float* p, float x) { *p = x; }
+
+// (cos, sin) * mscale of the pair at a position.
+__device__ __forceinline__ float2 turn_of(uint64_t turn, int pos, float mscale) {
+  const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(pos)) * turn;
+  const float half_turns = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f;
+  float s, c;
+  sincospif(half_turns, &s, &c);
+  return make_float2(c * mscale, s * mscale);
+}
+
+// One unit of a head from `in` to `out`: elements [16 u, 16 u + 16) when they
+// pass through or interleave; for the split layout the pairs [8 u, 8 u + 8).
+// A and B are the unit's two runs of 8 elements.
+template <typename TI, typename TO>
+__device__ __forceinline__ void unit16(const AppendParams& p, const float2* cs, const TI* in, TO* out, int u) {
+  const bool turn = 16 * u < p.rot;
+  const bool split = turn && !p.interleaved;
+  const int a = split ? 8 * u : 16 * u, b = split ? p.rot / 2 + 8 * u : 16 * u + 8;
+  float x[8], y[8];
+  load8(in + a, x);
+  load8(in + b, y);
+  if (split) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 t = cs[8 * u + i];
+      const float x1 = x[i], x2 = y[i];
+      x[i] = x1 * t.x - x2 * t.y;
+      y[i] = x2 * t.x + x1 * t.y;
+    }
+  } else if (turn) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 t = cs[8 * u + i], z = cs[8 * u + 4 + i];
+      const float x1 = x[2 * i], x2 = x[2 * i + 1], y1 = y[2 * i], y2 = y[2 * i + 1];
+      x[2 * i] = x1 * t.x - x2 * t.y;
+      x[2 * i + 1] = x2 * t.x + x1 * t.y;
+      y[2 * i] = y1 * z.x - y2 * z.y;
+      y[2 * i + 1] = y2 * z.x + y1 * z.y;
+    }
+  }
+  store8(out + a, x);
+  store8(out + b, y);
+}
+
+// One pair (u < rot / 2) or two elements that pass through: for a rot_dim
+// that is no multiple of 16.
+template <typename TI, typename TO>
+__device__ __forceinline__ void unit2(const AppendParams& p, const float2* cs, const TI* in, TO* out, int u) {
+  const bool turn = 2 * u < p.rot;
+  const bool split = turn && !p.interleaved;
+  const int a = split ? u : 2 * u, b = split ? p.rot / 2 + u : 2 * u + 1;
+  float x = load1(in + a), y = load1(in + b);
+  if (turn) {
+    const float2 t = cs[u];
+    const float x1 = x, x2 = y;
+    x = x1 * t.x - x2 * t.y;
+    y = x2 * t.x + x1 * t.y;
+  }
+  store1(out + a, x);
+  store1(out + b, y);
+}
+
+// T: element type of the rows (uint16_t: bf16 bits, or float); WIDE: units of
+// 16 elements (rot_dim a multiple of 16) or of 2.
+template <typename T, bool WIDE>
+__global__ void __launch_bounds__(AP_THREADS) append_kernel(const __grid_constant__ AppendParams p) {
+  const LaunchStamp ls(p.stamp);
+  __shared__ float2 s_cs[AP_ROWS][EAGLE_MAX_ROPE_PAIRS];
+  __shared__ long long s_at[AP_ROWS];        // cache row, -1: not written
+  __shared__ int s_pos[AP_ROWS];
+  __shared__ int s_any[AP_ROWS];             // the row belongs to a request
+  pdl_wait();
+  ls.waited();
+  pdl_trigger();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (static_cast<int>(blockIdx.x) >= p.row_ctas) {
+    // the requests' new lengths
+    const int b = (static_cast<int>(blockIdx.x) - p.row_ctas) * AP_WARPS + warp;
+    if (b >= p.rows.B) return;
+    int lo, hi;
+    const bool ok = request_rows(p.rows, b, lo, hi);
+    const int L = p.len[b];
+    const bool room = cache_takes(p.paged, p.cap, b, L, hi - lo, lane);
+    if (lane == 0) {
+      p.len_out[b] = room ? L + (hi - lo) : L;
+      if (!ok) set_status(p.status, EAGLE_ERR_INVALID_ARG);
+      if (!room) set_status(p.status, EAGLE_ERR_CAPACITY);
+    }
+    return;
+  }
+  const int r0 = blockIdx.x * p.tile;
+  const int rows = min(p.tile, p.rows.n_rows - r0);
+  if (warp < rows) {
+    const int r = r0 + warp;
+    const int b = request_of_row(p.rows, r, lane);
+    long long at = -1;
+    int pos = 0;
+    if (b >= 0) {
+      int lo, hi;
+      request_rows(p.rows, b, lo, hi);
+      const int L = p.len[b], i = r - lo;
+      pos = p.pos ? p.pos[r] : L + i;
+      if (cache_takes(p.paged, p.cap, b, L, hi - lo, lane))
+        at = p.paged.table ? paged_row(p.paged, b, L + i) : static_cast<long long>(b) * p.cap + L + i;
+    }
+    if (lane == 0) {
+      s_at[warp] = at;
+      s_pos[warp] = pos;
+      s_any[warp] = b >= 0;
+    }
+  }
+  __syncthreads();
+  const int pairs = p.rot / 2;
+  for (int i = tid; i < rows * pairs; i += AP_THREADS) {
+    const int r = i / pairs, j = i - r * pairs;
+    s_cs[r][j] = turn_of(p.turn[j], s_pos[r], p.mscale);
+  }
+  __syncthreads();
+  constexpr int W = WIDE ? 16 : 2;
+  const int upr = p.dh / W;                  // units of a head
+  const int hq = p.q ? p.hq : 0;
+  const int units = (hq + 2 * p.hkv) * upr;
+  for (int r = 0; r < rows; ++r) {
+    if (!s_any[r]) continue;
+    const size_t row = static_cast<size_t>(r0) + r;
+    const long long at = s_at[r];
+    for (int i = tid; i < units; i += AP_THREADS) {
+      const int h = i / upr, u = i - h * upr;
+      if (h < hq) {
+        const T* in = static_cast<const T*>(p.q) + row * p.ld_q + h * p.dh;
+        T* out = static_cast<T*>(p.q_out) + row * p.ld_qo + h * p.dh;
+        if (WIDE) unit16(p, s_cs[r], in, out, u);
+        else unit2(p, s_cs[r], in, out, u);
+      } else if (at >= 0) {
+        const bool is_v = h >= hq + p.hkv;
+        const int hk = h - hq - (is_v ? p.hkv : 0);
+        const T* in = static_cast<const T*>(is_v ? p.v : p.k) + row * (is_v ? p.ld_v : p.ld_k) + hk * p.dh;
+        uint16_t* out = (is_v ? p.vc : p.kc) + (static_cast<size_t>(at) * p.hkv + hk) * p.dh;
+        if (is_v) {
+          if (WIDE) {
+            float x[8], y[8];
+            load8(in + 16 * u, x);
+            load8(in + 16 * u + 8, y);
+            store8(out + 16 * u, x);
+            store8(out + 16 * u + 8, y);
+          } else {
+            store1(out + 2 * u, load1(in + 2 * u));
+            store1(out + 2 * u + 1, load1(in + 2 * u + 1));
+          }
+        } else {
+          if (WIDE) unit16(p, s_cs[r], in, out, u);
+          else unit2(p, s_cs[r], in, out, u);
+        }
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_append(eagle_ctx* ctx, const AppendLaunch& A, cudaStream_t st) {
+  const eagle_dims& D = ctx->dims;
+  AppendParams p{};
+  p.rows = PackedRows{A.rows->row_start, A.rows->n_rows, A.batch};
+  p.hq = D.n_q_heads;
+  p.hkv = D.n_kv_heads;
+  p.dh = D.head_dim;
+  if (A.rope) {
+    p.rot = A.rope->rot_dim;
+    p.interleaved = A.rope->interleaved;
+    p.mscale = A.rope->mscale;
+    for (int j = 0; j < EAGLE_MAX_ROPE_PAIRS; ++j) p.turn[j] = A.rope->turn[j];
+  }
+  p.q = A.q;
+  p.k = A.k;
+  p.v = A.v;
+  p.q_out = A.q_out;
+  p.ld_q = A.ld_q;
+  p.ld_qo = A.ld_qo;
+  p.ld_k = A.ld_k;
+  p.ld_v = A.ld_v;
+  p.kc = A.kv->k;
+  p.vc = A.kv->v;
+  p.cap = A.kv->cap;
+  p.len = A.kv->len;
+  p.paged = paged_of(&A.kv->paging, A.kv->cap);
+  p.pos = A.pos;
+  p.len_out = A.len_out;
+  p.status = A.status;
+  // few rows: one a CTA, so that a decoding step spreads over the SMs
+  p.tile = A.rows->n_rows <= 2 * ctx->sm_count ? 1 : AP_ROWS;
+  p.row_ctas = ceil_div(A.rows->n_rows, p.tile);
+  p.stamp = stamp_slot(ctx, EAGLE_K_APPEND);
+  const dim3 grid(static_cast<unsigned>(p.row_ctas) + ceil_div(A.batch, AP_WARPS));
+  const bool wide = p.rot % 16 == 0;
+  trace_before(ctx, EAGLE_K_APPEND, st);
+  cudaError_t e;
+  if (A.dtype == EAGLE_DTYPE_F32)
+    e = wide ? launch_pdl(append_kernel<float, true>, grid, dim3(AP_THREADS), 0, st, p)
+             : launch_pdl(append_kernel<float, false>, grid, dim3(AP_THREADS), 0, st, p);
+  else
+    e = wide ? launch_pdl(append_kernel<uint16_t, true>, grid, dim3(AP_THREADS), 0, st, p)
+             : launch_pdl(append_kernel<uint16_t, false>, grid, dim3(AP_THREADS), 0, st, p);
+  ctx->launches++;
+  trace_after(ctx, EAGLE_K_APPEND, st);
+  return e;
+}
+
+}  // namespace eagle

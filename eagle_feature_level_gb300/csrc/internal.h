@@ -32,6 +32,9 @@ inline int padded_rows(int n) {
   return (n + 15) / 16 * 16;
 }
 
+// Per-sequence lists of the page calls in the workspace.
+constexpr int PAGES_LISTS = 5;
+
 struct Workspace {
   size_t status;                 // int status word
   size_t b_fc, b_qkv, b_o, b_gu, b_down, b_lm, b_fuse;   // bf16 [2*NPmax][Kpad]
@@ -43,6 +46,7 @@ struct Workspace {
   size_t gemm_cnt;               // int [N_EPI][max_mtiles]
   size_t attn_part;              // fp32 partial (m, l, acc[dh]) records
   size_t attn_cnt;               // int [2][max_batch * Hkv]
+  size_t pages;                  // int lists of the page calls (PAGES_LISTS per sequence) and their counts
   size_t total;
   int max_mtiles;
   int npmax;
@@ -245,6 +249,38 @@ struct CommitLaunch {
 };
 cudaError_t launch_commit(eagle_ctx* ctx, const CommitLaunch& C, cudaStream_t st);
 cudaError_t launch_wait_selftest(eagle_ctx* ctx, void* ws, cudaStream_t st);
+
+// eagle_kv_append
+struct AppendLaunch {
+  int batch;
+  const eagle_rows* rows;
+  const eagle_rope* rope;
+  int dtype;
+  const void* q;
+  int ld_q;
+  void* q_out;
+  int ld_qo;
+  const void* k;
+  int ld_k;
+  const void* v;
+  int ld_v;
+  const eagle_kv* kv;
+  const int32_t* pos;
+  int32_t* len_out;
+  int* status;
+};
+cudaError_t launch_append(eagle_ctx* ctx, const AppendLaunch& A, cudaStream_t st);
+cudaError_t launch_chunk_attn(eagle_ctx* ctx, int batch, const eagle_rows* rows, const uint16_t* q, int ld_q,
+                              const eagle_kv* kv, int window, float scale, uint16_t* out, int ld_out, void* ws,
+                              cudaStream_t st);
+cudaError_t launch_pages_fork(eagle_ctx* ctx, const eagle_pages& pg, int n, const int32_t* src, const int32_t* dst,
+                              void* ws, cudaStream_t st);
+cudaError_t launch_pages_reserve(eagle_ctx* ctx, const eagle_pages& pg, const eagle_pools& pools, const int32_t* n_new,
+                                 void* ws, cudaStream_t st);
+cudaError_t launch_pages_release(eagle_ctx* ctx, const eagle_pages& pg, const int32_t* keep, void* ws,
+                                 cudaStream_t st);
+cudaError_t launch_pages_compact(eagle_ctx* ctx, const eagle_pages& pg, const eagle_pools& pools, void* ws,
+                                 cudaStream_t st);
 
 // Prefix splits of the split-KV attention for `pairs` (request, kv head)
 // pairs over a cache of `cap` rows, for a kernel run at per_sm CTAs per SM.

@@ -1,0 +1,60 @@
+// Packed rows of a batch (eagle_rows): which request a row belongs to, and
+// the bounds of a request's rows.
+#pragma once
+#include "internal.h"
+#include "common.cuh"
+
+namespace eagle {
+
+struct PackedRows {
+  const int32_t* start;   // [B + 1]
+  int n_rows, B;
+};
+
+// Rows [lo, hi) of request b; none (and false) when the starts break
+// 0 <= lo <= hi <= n_rows.
+__device__ __forceinline__ bool request_rows(const PackedRows& r, int b, int& lo, int& hi) {
+  lo = r.start[b];
+  hi = r.start[b + 1];
+  if (lo >= 0 && lo <= hi && hi <= r.n_rows) return true;
+  hi = lo = 0;
+  return false;
+}
+
+// The request that holds packed row `row` (every lane of a warp calls it; the
+// result is the same in all), or -1: the first whose end passes the row, by
+// a 32-way search of the ends, confirmed against that request's bounds.
+__device__ __forceinline__ int request_of_row(const PackedRows& r, int row, int lane) {
+  int lo = 0, n = r.B;    // the answer is in [lo, lo + n], r.B when no end passes the row
+  while (n > 0) {
+    const int step = (n + 31) / 32;
+    const int probe = lo + min((lane + 1) * step, n) - 1;
+    const bool in = lane * step < n;
+    const unsigned below = __ballot_sync(0xffffffffu, in && r.start[probe + 1] <= row);
+    const int c = __popc(below);              // whole steps whose last end does not pass the row
+    const int next = min(lo + c * step, lo + n);
+    n = step == 1 ? 0 : min(step - 1, lo + n - next);
+    lo = next;
+  }
+  if (lo >= r.B) return -1;
+  int a, z;
+  return request_rows(r, lo, a, z) && row >= a && row < z ? lo : -1;
+}
+
+// Whether a cache takes n more rows of request b at length L: within cap and,
+// when paged, in allocated blocks (every lane of a warp calls it; the result
+// is the same in all).
+__device__ __forceinline__ bool cache_takes(const PagedKv& pg, int cap, int b, int L, int n, int lane) {
+  if (L < 0 || static_cast<long long>(L) + n > cap) return false;
+  bool ok = true;
+  if (pg.table && n > 0) {
+    const int last = (L + n - 1) >> pg.shift;
+    for (int c = (L >> pg.shift) + lane; c <= last; c += 32) {
+      const int blk = pg.table[static_cast<size_t>(b) * pg.per_req + c];
+      ok = ok && blk >= 0 && blk < pg.n_blocks;
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+}  // namespace eagle

@@ -312,3 +312,114 @@ class Round:
             target_fn(self)
         self.accept()
         self.commit()
+
+
+def rope_for(dims: Dict[str, float], rot_dim: int = 0, interleaved: bool = False, theta: float = 0.0,
+             scaling: Optional[B.eagle_rope_scaling] = None) -> B.eagle_rope:
+    """The rotary plan of a model's heads (rot_dim 0: the whole head; theta 0: the model's own base)."""
+    dh = int(dims["head_dim"])
+    return B.eagle_rope_plan(dh, rot_dim or dh, int(interleaved),
+                             float(theta or dims.get("rope_theta", 10000.0)), scaling)
+
+
+class PagedCache:
+    """A paged KV cache of the target model: block pools of every layer, the
+    block table and reference counts all layers share, and the calls on them.
+
+    One step of a target model over a batch's new rows:
+        cache.reserve(n_new)                      # blocks, and private copies of shared tails
+        for each layer: cache.append(...); cache.attend(...)
+        cache.advance()                           # the lengths now count the new rows
+    `paging` and `kv(layer)` are what the round's verification attention and
+    commit take, with the sequences as the batch (capacity `cap`)."""
+
+    def __init__(self, eng: Engine, n_seqs: int, block_size: int, n_blocks: int, per_seq: int, n_layers: int = 1):
+        self.eng, self.n_seqs, self.bs, self.n_blocks, self.per = eng, n_seqs, block_size, n_blocks, per_seq
+        self.n_layers = n_layers
+        self.cap = per_seq * block_size
+        dev = eng.device
+        Hkv, dh = eng.dims["n_kv_heads"], eng.dims["head_dim"]
+        pool = lambda: torch.zeros(n_blocks, block_size, Hkv, dh, dtype=torch.bfloat16, device=dev)
+        self.k = [pool() for _ in range(n_layers)]
+        self.v = [pool() for _ in range(n_layers)]
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.table = torch.full((n_seqs, per_seq), -1, **i32)
+        self.len = torch.zeros(n_seqs, **i32)
+        self.len_next = torch.zeros(n_seqs, **i32)
+        self.ref = torch.zeros(n_blocks, **i32)
+        self.scratch = torch.zeros(2 * n_blocks, **i32)
+        self.pages_c = B.eagle_pages(_p(self.table), _p(self.len), _p(self.ref), _p(self.scratch), n_seqs, per_seq,
+                                     block_size, n_blocks)
+        self.pools_c = B.eagle_pools([_p(t) for t in self.k], [_p(t) for t in self.v])
+        self.paging = B.eagle_paging(_p(self.table), block_size, n_blocks)
+        self._kv = [B.eagle_kv(_p(k), _p(v), self.cap, _p(self.len), self.paging) for k, v in zip(self.k, self.v)]
+        self._kv_next = [B.eagle_kv(_p(k), _p(v), self.cap, _p(self.len_next), self.paging)
+                         for k, v in zip(self.k, self.v)]
+
+    def kv(self, layer: int = 0) -> B.eagle_kv:
+        return self._kv[layer]
+
+    def _ws(self):
+        return self.eng.ws.data_ptr(), self.eng.stream()
+
+    # ---- pages ----------------------------------------------------------------
+    def clear(self):
+        B.eagle_pages_init(self.eng.ctx, self.pages_c, *self._ws())
+
+    def fork(self, src: torch.Tensor, dst: torch.Tensor):
+        """Sequences dst share the rows of sequences src (int32, device)."""
+        B.eagle_pages_fork(self.eng.ctx, self.pages_c, src.numel(), _p(src), _p(dst), *self._ws())
+
+    def reserve(self, n_new: torch.Tensor):
+        """Room for n_new[s] more rows of every sequence (int32, device)."""
+        B.eagle_pages_reserve(self.eng.ctx, self.pages_c, self.pools_c, _p(n_new), *self._ws())
+
+    def release(self, keep: torch.Tensor):
+        """Cuts sequence s to its first keep[s] rows (int32, device; < 0: left alone)."""
+        B.eagle_pages_release(self.eng.ctx, self.pages_c, _p(keep), *self._ws())
+
+    def compact(self):
+        B.eagle_pages_compact(self.eng.ctx, self.pages_c, self.pools_c, *self._ws())
+
+    # ---- rows -----------------------------------------------------------------
+    @staticmethod
+    def _packed(t: torch.Tensor):
+        """Address and pitch of packed rows [n][H][dh] whose heads are contiguous (a slice of a fused projection
+        has a larger pitch)."""
+        if t.dim() != 3 or t.stride(2) != 1 or t.stride(1) != t.shape[2]:
+            raise ValueError("packed rows are [n][heads][head_dim] with contiguous heads")
+        return _p(t), t.stride(0)
+
+    def append(self, layer: int, row_start: torch.Tensor, rope: Optional[B.eagle_rope], q: Optional[torch.Tensor],
+               k: torch.Tensor, v: torch.Tensor, q_out: Optional[torch.Tensor] = None,
+               pos: Optional[torch.Tensor] = None):
+        """Rotates q (into q_out, default q itself) and k of the new rows and appends k, v behind the sequences'
+        rows in `layer`; len_next counts them."""
+        if q is not None and q_out is None:
+            q_out = q
+        dtype = B.DTYPE_F32 if k.dtype == torch.float32 else B.DTYPE_BF16
+        for t in (q, v, q_out):
+            if t is not None and t.dtype != k.dtype:
+                raise ValueError("q, k, v and q_out have one type")
+        if k.dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError("rows are bf16 or fp32")
+        none = (0, 0)
+        B.eagle_kv_append(self.eng.ctx, self.n_seqs, B.eagle_rows(_p(row_start), k.shape[0]), rope, dtype,
+                          *(self._packed(q) if q is not None else none),
+                          *(self._packed(q_out) if q is not None else none), *self._packed(k), *self._packed(v),
+                          self._kv[layer], _p(pos), _p(self.len_next), *self._ws())
+
+    def attend(self, layer: int, row_start: torch.Tensor, q: torch.Tensor, out: torch.Tensor, window: int = 0,
+               scale: Optional[float] = None):
+        """Causal attention of the appended rows (bf16 q, out) over `layer`'s rows up to len_next."""
+        if q.dtype != torch.bfloat16 or out.dtype != torch.bfloat16:
+            raise ValueError("q and out are bf16")
+        qp, ldq = self._packed(q)
+        op, ldo = self._packed(out)
+        B.eagle_chunk_attn(self.eng.ctx, self.n_seqs, B.eagle_rows(_p(row_start), q.shape[0]), qp, ldq,
+                           self._kv_next[layer], window, scale or 1.0 / math.sqrt(self.eng.dims["head_dim"]), op, ldo,
+                           *self._ws())
+
+    def advance(self):
+        """The appended rows become the sequences' own."""
+        self.len.copy_(self.len_next)

@@ -78,6 +78,7 @@ typedef enum {
 #define EAGLE_MAX_CHILDREN 16  /* drawn children per expanded node */
 #define EAGLE_MAX_LAYERS 128   /* target layers one commit can append */
 #define EAGLE_MAX_VOCAB 32768  /* keeps every exact sampling product below 2^128 */
+#define EAGLE_MAX_ROPE_PAIRS 64 /* rotating pairs of a head (head_dim <= 128) */
 
 typedef struct eagle_ctx eagle_ctx;
 
@@ -509,6 +510,182 @@ eagle_status eagle_fuse_features(eagle_ctx* ctx, const uint16_t* w_fuse, int ld_
                                  int n_rows, const float* lmh, float* g_out, void* workspace,
                                  cudaStream_t stream);
 
+/* ---- the target's cache --------------------------------------------------- */
+/*
+ * The round reads and extends KV caches that the target model has filled.
+ * These calls are that filling, for target models run beside the round: the
+ * new rows of a batch (a prompt, a chunk of one, or one token a request) get
+ * their rotary positions and go into the cache (eagle_kv_append), attend to
+ * everything before them (eagle_chunk_attn), and the blocks that hold a paged
+ * cache are handed out, shared, taken back and packed on the device
+ * (eagle_pages_*), with no host round trip: every call can be captured in a
+ * CUDA graph and replayed on other lengths.
+ */
+
+/* New rows of a batch, packed: request b's are the rows row_start[b] ..
+ * row_start[b + 1] - 1 of the packed buffers, 0 <= row_start[b] <=
+ * row_start[b + 1] <= n_rows.  Requests may have no rows; rows outside every
+ * request are neither read nor written.  Starts that break these bounds set
+ * EAGLE_ERR_INVALID_ARG in the status word; the requests they concern are
+ * treated as having no rows. */
+typedef struct {
+  const int32_t* row_start;  /* [B + 1] (device) */
+  int n_rows;                /* rows of the packed buffers, >= 1 */
+} eagle_rows;
+
+/* Element type of packed rows. */
+typedef enum { EAGLE_DTYPE_BF16 = 0, EAGLE_DTYPE_F32 = 1 } eagle_dtype;
+
+/* Rotary positions (host struct, built by eagle_rope_plan): the leading
+ * rot_dim elements of a head rotate in pairs j = 0 .. rot_dim / 2 - 1, pair j
+ * by position * turn[j] / 2^64 full turns, scaled by mscale:
+ *   y1 = m (x1 cos - x2 sin),  y2 = m (x2 cos + x1 sin);
+ * the elements from rot_dim on pass through.  interleaved 0: pair j is the
+ * elements (j, j + rot_dim / 2); 1: (2j, 2j + 1).  A frequency is held as a
+ * 64-bit fraction of a turn, so that position * turn mod 2^64 is the angle's
+ * exact fraction at any position (fp32 angles lose it: 2^-24 of position
+ * 131072 is 0.008 radians). */
+typedef struct {
+  int rot_dim;
+  int interleaved;
+  float mscale;
+  uint64_t turn[EAGLE_MAX_ROPE_PAIRS];
+} eagle_rope;
+
+/* Scaling of the frequencies f_j = theta^(-2j / rot_dim) for contexts longer
+ * than the original_len positions a model was trained on:
+ *   LINEAR  f / factor (interpolated positions);
+ *   BANDS   by wavelength: a pair that makes at least `high` turns in the
+ *           original length keeps f, at most `low` takes f / factor, between
+ *           them t f + (1 - t) f / factor, t = (turns - low) / (high - low);
+ *   RAMP    by pair number: with c(r) = rot_dim ln(original_len / (2 pi r)) /
+ *           (2 ln theta) the pair that makes r turns, f below floor(c(high)),
+ *           f / factor above ceil(c(low)), linear in j between (both ends
+ *           clamped to [0, rot_dim - 1]).
+ * mscale: the factor on the rotated elements; 0 takes the kind's own (RAMP:
+ * 1 + 0.1 ln factor, otherwise 1). */
+typedef enum { EAGLE_ROPE_LINEAR = 1, EAGLE_ROPE_BANDS = 2, EAGLE_ROPE_RAMP = 3 } eagle_rope_kind;
+typedef struct {
+  int kind;
+  double factor;        /* >= 1 */
+  double low, high;     /* BANDS, RAMP: 0 < low < high, in turns */
+  int original_len;     /* BANDS, RAMP: >= 1 */
+  double mscale;
+} eagle_rope_scaling;
+
+/* Builds `out` (host only).  rot_dim even, 2 <= rot_dim <= head_dim <= 128
+ * (EAGLE_ERR_SHAPE); theta > 1 finite; scaling NULL: none. */
+eagle_status eagle_rope_plan(eagle_rope* out, int head_dim, int rot_dim, int interleaved, double theta,
+                             const eagle_rope_scaling* scaling);
+
+/* eagle_kv_append -- rotates the new rows' q and k and appends k and v to the
+ * cache: for row r = row_start[b] + i at position p = pos[r] (pos NULL:
+ * kv.len[b] + i), q_out[r] = RoPE(q[r], p), and cache row kv.len[b] + i takes
+ * bf16(RoPE(k[r], p)) and bf16(v[r]); len_out[b] = kv.len[b] + the request's
+ * rows.  rope NULL: nothing rotates.  q NULL: keys and values only.
+ * q [n_rows][ld_q] (Hq heads of head_dim each), k and v alike with Hkv heads,
+ * all of `dtype`; q_out of the same type.  Pitches in elements, >= the row and
+ * multiples of 8 (bf16) or 4 (fp32) elements, so that the three can be slices
+ * of one fused projection.  q_out may be q itself (with its pitch); no other
+ * overlap of outputs and inputs.  The arithmetic is fp32 from an exact angle,
+ * rounded once.
+ * The cache may be paged (kv.paging) and the draft's or a tree's own arena
+ * (a contiguous cache of as many rows per request).  A request whose cache
+ * cannot take all its rows (beyond kv.cap, or in unallocated blocks) writes
+ * none of them and keeps its length (EAGLE_ERR_CAPACITY in the status word);
+ * its q rows are rotated all the same.  len_out must not alias kv.len
+ * (EAGLE_ERR_INVALID_ARG).  Rows a block table maps to the same place -- a
+ * block that two requests hold -- must be made private first
+ * (eagle_pages_reserve). */
+eagle_status eagle_kv_append(eagle_ctx* ctx, int batch, const eagle_rows* rows, const eagle_rope* rope, int dtype,
+                             const void* q, int ld_q, void* q_out, int ld_q_out, const void* k, int ld_k,
+                             const void* v, int ld_v, const eagle_kv* kv, const int32_t* pos, int32_t* len_out,
+                             void* workspace, cudaStream_t stream);
+
+/* eagle_chunk_attn -- causal attention of the new rows over a cache that
+ * already holds them (kv.len[b] counts them: eagle_kv_append's len_out).  With
+ * n the request's rows, row i stands at p = kv.len[b] - n + i and
+ *   out[i][h] = softmax_j(scale q[i][h] . K[j]) V,
+ *   max(0, p - window + 1) <= j <= p   (window 0: from 0), kv head h / (Hq / Hkv).
+ * A row that sees no key (a length shorter than the rows) is zero.  One row
+ * is a decoding step, n = kv.len[b] a whole prompt; requests of both kinds
+ * mix in one call.  q [n_rows][ld_q] and out [n_rows][ld_out] bf16, pitches
+ * multiples of 8 elements; out must not overlap q or the cache.  Scores,
+ * maxima and sums are fp32; the probabilities enter the product with V
+ * rounded to bf16.  The cache may be paged: rows of an unallocated block
+ * read as zeros and set EAGLE_ERR_INVALID_ARG in the status word; a length
+ * beyond kv.cap is read as kv.cap and sets EAGLE_ERR_CAPACITY.  The contents
+ * of cache rows at or past a request's length never matter; every row below
+ * it must be finite. */
+eagle_status eagle_chunk_attn(eagle_ctx* ctx, int batch, const eagle_rows* rows, const uint16_t* q, int ld_q,
+                              const eagle_kv* kv, int window, float scale, uint16_t* out, int ld_out,
+                              void* workspace, cudaStream_t stream);
+
+/* The pages of a paged cache, shared by all layers: sequence s holds the
+ * blocks block_table[s][0 .. ceil(len[s] / block_size)) -- and possibly more,
+ * reserved ahead -- and ref counts, for every block, the table entries that
+ * map it.  A block is free when its count is 0; there is no other allocator
+ * state, and the calls below always take the lowest free ids first, so equal
+ * states give equal tables.  block_table is what eagle_paging takes, with
+ * kv.cap = per_seq * block_size and the sequences as the batch. */
+typedef struct {
+  int32_t* block_table;  /* [n_seqs][per_seq]; < 0: none */
+  int32_t* len;          /* [n_seqs] rows */
+  int32_t* ref;          /* [n_blocks] */
+  int32_t* scratch;      /* [2 * n_blocks], contents arbitrary */
+  int n_seqs;            /* <= max_batch */
+  int per_seq;           /* per_seq * block_size <= max_prefix */
+  int block_size;        /* a power of two */
+  int n_blocks;
+} eagle_pages;
+
+/* The block pools a page call copies in: HOST arrays of n_layers device
+ * pointers to [n_blocks][block_size][Hkv][dh] bf16, n_layers <=
+ * EAGLE_MAX_LAYERS (0: the tables alone). */
+typedef struct {
+  int n_layers;
+  uint16_t* const* k;
+  uint16_t* const* v;
+} eagle_pools;
+
+/* Every block free, every sequence empty. */
+eagle_status eagle_pages_init(eagle_ctx* ctx, const eagle_pages* pages, void* workspace, cudaStream_t stream);
+
+/* eagle_pages_fork -- for i < n: sequence dst[i] gives its blocks back and
+ * shares those of src[i] that hold its rows; len[dst] = len[src].  No row is
+ * copied.  src, dst: [n] (device).  A pair that is out of range, whose
+ * destination is some pair's source, or whose destination an earlier pair
+ * has is refused (EAGLE_ERR_INVALID_ARG in the status word), the others
+ * take effect. */
+eagle_status eagle_pages_fork(eagle_ctx* ctx, const eagle_pages* pages, int n, const int32_t* src,
+                              const int32_t* dst, void* workspace, cudaStream_t stream);
+
+/* eagle_pages_reserve -- makes room for n_new[s] more rows of every sequence
+ * (n_new[s] <= 0: none): blocks for the rows len[s] .. len[s] + n_new[s] - 1,
+ * in sequence order, and copy on write: a partly filled last block that other
+ * sequences hold too is replaced by a copy of its len[s] % block_size rows in
+ * every layer's pools -- except for the last holder when all of a block's
+ * holders are writing.  Lengths do not change (eagle_kv_append and
+ * eagle_commit move them).  All or nothing: when the free blocks do not
+ * suffice for the whole call, or a sequence's rows pass per_seq blocks,
+ * nothing changes and EAGLE_ERR_CAPACITY is set in the status word. */
+eagle_status eagle_pages_reserve(eagle_ctx* ctx, const eagle_pages* pages, const eagle_pools* pools,
+                                 const int32_t* n_new, void* workspace, cudaStream_t stream);
+
+/* eagle_pages_release -- cuts every sequence s with keep[s] >= 0 to its first
+ * keep[s] rows: blocks past ceil(keep[s] / block_size) are given back (free
+ * once no table maps them) and len[s] = min(len[s], keep[s]).  0 frees a
+ * sequence, keep[s] < 0 leaves it alone. */
+eagle_status eagle_pages_release(eagle_ctx* ctx, const eagle_pages* pages, const int32_t* keep, void* workspace,
+                                 cudaStream_t stream);
+
+/* eagle_pages_compact -- moves the live blocks to the front of the pools: with
+ * u blocks live, the live ids >= u move, in ascending order, to the free ids
+ * < u, in every layer's pools; tables and counts follow.  Afterwards the
+ * blocks from u on are free. */
+eagle_status eagle_pages_compact(eagle_ctx* ctx, const eagle_pages* pages, const eagle_pools* pools,
+                                 void* workspace, cudaStream_t stream);
+
 /* ---- measurement --------------------------------------------------------- */
 
 /* Kernel timing hook: while enabled, the library records a CUDA event before
@@ -519,7 +696,8 @@ typedef enum {
   EAGLE_K_ALL = -1, EAGLE_K_GEMM_FC = 0, EAGLE_K_GEMM_QKV = 1, EAGLE_K_GEMM_O = 2,
   EAGLE_K_GEMM_GATEUP = 3, EAGLE_K_GEMM_DOWN = 4, EAGLE_K_GEMM_LM = 5, EAGLE_K_DRAFT_ATTN = 6,
   EAGLE_K_SELECT = 7, EAGLE_K_TREE = 8, EAGLE_K_VERIFY_ATTN = 9, EAGLE_K_ACCEPT = 10,
-  EAGLE_K_COMMIT = 11, EAGLE_K_PREP = 12, EAGLE_K_REFRESH = 13, EAGLE_K_FUSE = 14
+  EAGLE_K_COMMIT = 11, EAGLE_K_PREP = 12, EAGLE_K_REFRESH = 13, EAGLE_K_FUSE = 14,
+  EAGLE_K_APPEND = 15, EAGLE_K_CHUNK_ATTN = 16, EAGLE_K_PAGES = 17
 } eagle_kernel_id;
 eagle_status eagle_trace_enable(eagle_ctx* ctx, int kernel_id, int capacity);
 /* Synchronises the recorded events; writes up to `cap` durations in ms, the
