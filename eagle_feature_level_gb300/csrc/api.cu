@@ -116,8 +116,10 @@ void layout(eagle_ctx* c) {
     records = std::max(records, static_cast<size_t>(L.max_rows) * D.n_q_heads * s1);
     records = std::max(records, static_cast<size_t>(b) * L.max_tree * D.n_q_heads * s1);
   }
-  W.attn_part = take(records * (D.head_dim + 4) * 4);
+  // the chunk attention's partials take their place in its calls
+  W.attn_part = take(std::max(records * (D.head_dim + 4) * 4, chunk_part_bytes(c->sm_count, D.head_dim)));
   W.attn_cnt = take(static_cast<size_t>(2) * L.max_batch * D.n_kv_heads * 4);
+  W.chunk_cnt = take(static_cast<size_t>(c->sm_count) * 4);
   W.pages = take(static_cast<size_t>(PAGES_LISTS) * L.max_batch * 4 + 256);
   W.total = off;
 }

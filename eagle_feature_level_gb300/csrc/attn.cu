@@ -1167,71 +1167,6 @@ constexpr int WS_BAR_GROUP = 2;
 __device__ __forceinline__ uint32_t ws_sw(int row, int chunk) {
   return static_cast<uint32_t>((row >> 3) * 1024 + (row & 7) * 128 + ((chunk ^ (row & 7)) << 4));
 }
-// 32 lanes x 32 consecutive 32-bit columns (thread i: lane quarter * 32 + i).
-__device__ __forceinline__ void ws_tmem_ld32(uint32_t taddr, float (&v)[32]) {
-  uint32_t r[32];
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-               : "r"(taddr));
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-// 32 lanes x 16 consecutive 32-bit columns.
-__device__ __forceinline__ void ws_tmem_ld16(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-               : "r"(taddr));
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-// 32 lanes x 4 consecutive 32-bit columns, stored.
-__device__ __forceinline__ void ws_tmem_st4(uint32_t taddr, const uint32_t (&w)[4]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(w[0]), "r"(w[1]),
-               "r"(w[2]), "r"(w[3])
-               : "memory");
-}
-// 32 lanes x 8 consecutive 32-bit columns, stored.
-__device__ __forceinline__ void ws_tmem_st8(uint32_t taddr, const uint32_t (&w)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(w[0]),
-               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
-// 32 lanes x 16 consecutive 32-bit columns, stored.
-__device__ __forceinline__ void ws_tmem_st16(uint32_t taddr, const uint32_t (&w)[16]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]), "r"(w[9]), "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15])
-               : "memory");
-}
-// Shared-memory descriptors as two 32-bit words.  The high word (8-row group
-// stride 1024 bytes, version 1, 128-byte swizzle) is the same for every
-// operand here; the low word is (address >> 4) | (leading byte offset >> 4)
-// << 16, so an operand that many bytes on is the low word plus (bytes >> 4)
-// (the address field never carries: operands end below 256 KB).
-constexpr uint32_t WS_DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint32_t ws_desc_lo(uint32_t saddr, uint32_t lbo) {
-  return ((saddr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16);
-}
-// The two MMA forms from 32-bit descriptor words; `acc` false only for the
-// first MMA of an accumulation.
-__device__ __forceinline__ void ws_mma_ss32(uint32_t d_tmem, uint32_t alo, uint32_t blo, uint32_t hi, uint32_t idesc,
-                                            uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}\n" ::"r"(d_tmem),
-      "r"(alo), "r"(blo), "r"(hi), "r"(idesc), "r"(acc));
-}
-__device__ __forceinline__ void ws_mma_ts32(uint32_t d_tmem, uint32_t a_tmem, uint32_t blo, uint32_t hi, uint32_t idesc,
-                                            uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %3};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "r"(blo), "r"(hi), "r"(idesc), "r"(acc));
-}
-__device__ __forceinline__ float ws_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // (x, y) -> bf16x2 hi = RN(x, y) and lo = RN of the remainders, x in the low
 // half (the same values as split_pair, two conversions per pair).
 __device__ __forceinline__ void ws_split2(float x, float y, uint32_t& hi, uint32_t& lo) {
@@ -1393,9 +1328,9 @@ __device__ __forceinline__ bool ws_softmax_tile(bool work, bool rows, uint32_t t
   }
   if (work && rows) {
     if constexpr (KPT == 32) {
-      ws_tmem_ld32(tmem + WS_TM_S + 64u * G + lane_base + j0, sv);
+      sm100::tmem_ld32(tmem + WS_TM_S + 64u * G + lane_base + j0, sv);
     } else {
-      ws_tmem_ld16(tmem + WS_TM_S + 64u * G + lane_base + j0, sv);
+      sm100::tmem_ld16(tmem + WS_TM_S + 64u * G + lane_base + j0, sv);
     }
     sm100::tmem_wait_ld();
     // this warp is done with S buffer G: S(t + 2) may be issued into it
@@ -1431,17 +1366,17 @@ __device__ __forceinline__ bool ws_softmax_tile(bool work, bool rows, uint32_t t
     // O_G of the warp's rows times 2^(m_old - m_new) (a finite reference
     // comes from an earlier tile of the group); this warpgroup's half of the columns
     sm100::tc_fence_after();
-    const float f = rescale ? ws_exp2(m_ref - mt) : 1.f;
+    const float f = rescale ? sm100::exp2(m_ref - mt) : 1.f;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       float v16[16];
       const uint32_t ta = tmem + WS_TM_O + WS_TM_O_STEP * G + lane_base + 64 * w + 16 * q;
-      ws_tmem_ld16(ta, v16);
+      sm100::tmem_ld16(ta, v16);
       sm100::tmem_wait_ld();
       uint32_t x[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(v16[j] * f);
-      ws_tmem_st16(ta, x);
+      sm100::tmem_st16(ta, x);
     }
     sm100::tmem_wait_st();
     if (rescale) l_part *= f;
@@ -1454,18 +1389,18 @@ __device__ __forceinline__ bool ws_softmax_tile(bool work, bool rows, uint32_t t
   uint32_t hw[KPT / 2], lw[KPT / 2];
 #pragma unroll
   for (int i = 0; i < KPT / 2; ++i) {
-    const float e0 = ws_exp2(fmaf(sv[2 * i], ec, nm)), e1 = ws_exp2(fmaf(sv[2 * i + 1], ec, nm));
+    const float e0 = sm100::exp2(fmaf(sv[2 * i], ec, nm)), e1 = sm100::exp2(fmaf(sv[2 * i + 1], ec, nm));
     part[0] += e0;
     part[1] += e1;
     ws_split2(e0, e1, hw[i], lw[i]);
   }
   l_part += part[0] + part[1];
   if constexpr (KPT == 32) {
-    ws_tmem_st16(pcol, hw);
-    ws_tmem_st16(pcol + 32, lw);
+    sm100::tmem_st16(pcol, hw);
+    sm100::tmem_st16(pcol + 32, lw);
   } else {
-    ws_tmem_st8(pcol, hw);
-    ws_tmem_st8(pcol + 32, lw);
+    sm100::tmem_st8(pcol, hw);
+    sm100::tmem_st8(pcol + 32, lw);
   }
   sm100::tmem_wait_st();
   return true;
@@ -1652,23 +1587,23 @@ __global__ void __launch_bounds__(WS_THREADS, 1)
       // lean -- descriptors formed once per tile, every MMA's offset a
       // constant -- since a dependent MMA chain issues at the rate this
       // thread reaches it.
-      const uint32_t hi = WS_DESC_HI;
-      const uint32_t qlo = ws_desc_lo(sbase, 16);                 // Q hi, k-block 0
+      const uint32_t hi = sm100::DESC_SW128_HI;
+      const uint32_t qlo = sm100::desc_lo(sbase, 16);                 // Q hi, k-block 0
       // stage base of tile t's K and V; stage and phase tracked incrementally
       auto issue_s = [&](int t, int st) {
         sm100::tc_fence_after();
         const uint32_t stg = rbase + static_cast<uint32_t>(st) * WS_STAGE;
         const uint32_t d = tmem + WS_TM_S + 64u * static_cast<uint32_t>(t & 1);
-        const uint32_t klo = ws_desc_lo(stg, 16);
+        const uint32_t klo = sm100::desc_lo(stg, 16);
         if (!(draft && t >= T.n_pre)) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)                 // Q hi against K
-            ws_mma_ss32(d, qlo + (((kk >> 2) * WS_QHALF + (kk & 3) * 32) >> 4),
+            sm100::mma_ss32(d, qlo + (((kk >> 2) * WS_QHALF + (kk & 3) * 32) >> 4),
                         klo + (((kk >> 2) * WS_HALF + (kk & 3) * 32) >> 4), hi, id_s64, kk > 0 ? 1u : 0u);
           if (draft) {
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)               // Q lo against K
-              ws_mma_ss32(d, qlo + ((2 * WS_QHALF + (kk >> 2) * WS_QHALF + (kk & 3) * 32) >> 4),
+              sm100::mma_ss32(d, qlo + ((2 * WS_QHALF + (kk >> 2) * WS_QHALF + (kk & 3) * 32) >> 4),
                           klo + (((kk >> 2) * WS_HALF + (kk & 3) * 32) >> 4), hi, id_s64, 1u);
           }
         } else {
@@ -1676,7 +1611,7 @@ __global__ void __launch_bounds__(WS_THREADS, 1)
           for (int pr = 0; pr < 3; ++pr)                 // Qhi Khi, Qlo Khi, Qhi Klo
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              ws_mma_ss32(d, qlo + (((pr == 1 ? 2 * WS_QHALF : 0u) + (kk >> 2) * WS_QHALF + (kk & 3) * 32) >> 4),
+              sm100::mma_ss32(d, qlo + (((pr == 1 ? 2 * WS_QHALF : 0u) + (kk >> 2) * WS_QHALF + (kk & 3) * 32) >> 4),
                           klo + (((pr == 2 ? WS_HALF : 0u) + (kk >> 2) * WS_FHALF + (kk & 3) * 32) >> 4), hi, id_s32,
                           (pr | kk) != 0 ? 1u : 0u);
         }
@@ -1689,17 +1624,17 @@ __global__ void __launch_bounds__(WS_THREADS, 1)
         const uint32_t od = tmem + WS_TM_O + WS_TM_O_STEP * static_cast<uint32_t>(t & 1);
         const uint32_t first = t >= 2 ? 1u : 0u;            // the first tile of each group starts its O
         if (!(draft && t >= T.n_pre)) {
-          const uint32_t vlo = ws_desc_lo(stg + 2 * WS_HALF, WS_HALF);
+          const uint32_t vlo = sm100::desc_lo(stg + 2 * WS_HALF, WS_HALF);
 #pragma unroll
           for (int i = 0; i < 8; ++i)                    // P hi, then P lo, against V
-            ws_mma_ts32(od, pt + 32u * (i >> 2) + 8u * (i & 3), vlo + (((i & 3) * 2048) >> 4), hi, id_pv,
+            sm100::mma_ts32(od, pt + 32u * (i >> 2) + 8u * (i & 3), vlo + (((i & 3) * 2048) >> 4), hi, id_pv,
                         i > 0 ? 1u : first);
         } else {
-          const uint32_t vlo = ws_desc_lo(stg + 2 * WS_HALF, WS_FHALF);
+          const uint32_t vlo = sm100::desc_lo(stg + 2 * WS_HALF, WS_FHALF);
 #pragma unroll
           for (int i = 0; i < 6; ++i) {                  // Phi Vhi, Plo Vhi, Phi Vlo
             const int pr = i >> 1, kk = i & 1;
-            ws_mma_ts32(od, pt + (pr == 1 ? 32u : 0u) + 8u * kk,
+            sm100::mma_ts32(od, pt + (pr == 1 ? 32u : 0u) + 8u * kk,
                         vlo + (((pr == 2 ? WS_HALF : 0u) + kk * 2048) >> 4), hi, id_pv, i > 0 ? 1u : first);
           }
         }
@@ -1783,7 +1718,7 @@ __global__ void __launch_bounds__(WS_THREADS, 1)
     sm100::named_barrier(WS_BAR_SOFT, WS_SOFT_THREADS);
     const float m0 = s_m[0][row], m1 = s_m[1][row];
     const float M = fmaxf(m0, m1);
-    const float a0 = m0 == -INFINITY ? 0.f : ws_exp2(m0 - M), a1 = m1 == -INFINITY ? 0.f : ws_exp2(m1 - M);
+    const float a0 = m0 == -INFINITY ? 0.f : sm100::exp2(m0 - M), a1 = m1 == -INFINITY ? 0.f : sm100::exp2(m1 - M);
     m_run = M;
     l_run = a0 * (s_l[0][0][row] + s_l[0][1][row]) + a1 * (s_l[1][0][row] + s_l[1][1][row]);
     // output columns c0 .. c0 + OC - 1: a0 O_0 + a1 O_1 (an O with weight 0 is not read: it may never have been written)
@@ -1794,7 +1729,7 @@ __global__ void __launch_bounds__(WS_THREADS, 1)
         const float a = gi ? a1 : a0;
         if (__any_sync(0xffffffffu, a != 0.f)) {
           float v[OC];
-          ws_tmem_ld32(tmem + WS_TM_O + WS_TM_O_STEP * gi + lane_base + c0, v);
+          sm100::tmem_ld32(tmem + WS_TM_O + WS_TM_O_STEP * gi + lane_base + c0, v);
           sm100::tmem_wait_ld();
           if (a != 0.f) {
 #pragma unroll
@@ -1878,7 +1813,7 @@ __global__ void __launch_bounds__(WS_THREADS, 1)
 #pragma unroll
       for (int q = 0; q < 4; ++q) vals[u][q] = u < ns ? __ldcg(src + u * rec + 4 + lane + 32 * q) : 0.f;
     const float M = warp_max(ms);
-    const float wgt = ms == -INFINITY ? 0.f : ws_exp2(ms - M);
+    const float wgt = ms == -INFINITY ? 0.f : sm100::exp2(ms - M);
     const float Lsum = warp_sum(wgt * lsv);
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll

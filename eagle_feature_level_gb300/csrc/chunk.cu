@@ -1,89 +1,839 @@
 // eagle_chunk_attn: causal attention of a batch's new rows over the cache
-// that holds them.  One warp per (row, query head): online softmax over the
-// row's keys, the head's elements spread over the lanes.
+// that holds them, from one token a request to whole prompts.
+//
+// Rows and items.  The query heads of a kv head share its keys, so a 128-row
+// tensor-core tile holds T = 128 / GB tokens x GB heads (GB = the heads per
+// kv head, at most 128).  An item is two such tiles (one when the request has
+// few rows left) of one request and kv head, against the tiles of 128 keys
+// its rows can see: max(0, first row's position - window + 1) up to its last
+// row's position.
+//
+// Schedule.  Items differ by orders of magnitude (a decoding token over 64 key
+// tiles, a prompt's first rows over one), and their sizes are known on the
+// device only.  So the key tiles of all items, laid end to end, are dealt out
+// evenly: CTA c of n takes the units [U c / n, U (c + 1) / n).  Each CTA finds
+// its start itself (two passes of one warp over the batch's lengths), walks
+// on from there, and writes the rows of items it holds whole; an item that
+// crosses CTAs leaves (max, sum, unnormalised output) partials, which the
+// last CTA to arrive combines in CTA order (the same bits whoever is last).
+//
+// One CTA per SM, 384 threads:
+//   warp 0      loader: Q tiles, then K and V tiles by TMA into a ring (boxes
+//               of 64 elements x one block's rows, out-of-range blocks read as
+//               zeros); rows of V past the request's length are zeroed.
+//   warp 1      one thread issues the MMAs: S_w = Q_w K^T into tensor memory,
+//               O_w += P_w V with P_w (bf16) written over S_w.
+//   warp 2      scheduler: the walk over items, a few segments ahead.
+//   warps 4-11  two softmax warpgroups, thread = query row = tensor-memory
+//               lane.  With two tiles warpgroup w has tile w and every key
+//               tile; with one, warpgroup w has the key tiles t = w (mod 2) and
+//               an O of its own, joined at the item's end.  So the tensor
+//               cores always have the other group's products to run while one
+//               group is at its exponentials.
+// The running maximum of a row is raised (O and the sum rescaled) only when a
+// tile's maximum passes it by more than 8 in log2 units: P stays below 2^8 and
+// O / l does not depend on when it was raised.  P in bf16 (2^-9 of each
+// probability) is this operator's one rounding besides its output's: with P as
+// a hi + lo pair the P V products double, which the fp32 outputs of the tree
+// attention need and a bf16 output does not.
 #include <algorithm>
+#include <cstring>
 
 #include "internal.h"
 #include "common.cuh"
 #include "rows.cuh"
+#include "sm100.cuh"
 
 namespace eagle {
 namespace {
 
+constexpr int CH_THREADS = 384;
+constexpr int CH_LOAD_WARP = 0, CH_MMA_WARP = 1, CH_SCHED_WARP = 2, CH_SOFT_WARP0 = 4;
+constexpr int CH_SOFT_WARPS = 8;
+constexpr int CH_KEYS = 128;                 // keys per tile
+constexpr int CH_ROWS = 128;                 // query rows per tile
+constexpr uint32_t CH_HALF = CH_KEYS * 128;  // bytes of 128 rows x 64 elements
+constexpr int CH_SEGS = 4;                   // segments the scheduler runs ahead
+constexpr float CH_RAISE = 8.0f;
+constexpr uint32_t CH_TM_S = 0, CH_TM_O = 256, CH_TM_COLS = 512;   // S_w / P_w at 128 w, O_w at 256 + 128 w
+constexpr int CH_REGS_FEW = 80, CH_REGS_SOFT = 208;
+static_assert(128 * CH_REGS_FEW + 256 * CH_REGS_SOFT <= CH_THREADS * 168, "the split fits the launch's registers");
+
+// D: elements of a head as staged (64, or 128); ring slots of one K or V tile.
+template <int D>
+struct Shape {
+  static constexpr int HALVES = D / 64;
+  static constexpr uint32_t TILE = HALVES * CH_HALF;       // bytes of a Q, K or V tile
+  static constexpr int SLOTS = D == 128 ? 5 : 10;
+  static constexpr uint32_t TILES = (2 + SLOTS) * TILE;    // two Q tiles, then the ring
+};
+
 struct ChunkParams {
   PackedRows rows;
-  int hq, hkv, dh, G;
-  const uint16_t* q;
+  int hkv, G, GB, T, nsub;                   // heads: kv, per kv head, per tile; tokens per tile; tiles' heads per kv head
+  int dh;
+  long long ld_o;
   uint16_t* out;
-  long long ld_q, ld_o;
-  const uint16_t* k;
-  const uint16_t* v;
   int cap, window;
   const int32_t* len;
   PagedKv paged;
-  float c;                 // scale * log2 e
+  int box;                                   // rows of a K / V box
+  float c;                                   // scale * log2 e
+  float* part;                               // [2 grid][CH_PART] partials
+  int* cnt;                                  // [grid] arrivals at a split item, by its first CTA
   int* status;
   uint64_t* stamp;
 };
 
-__global__ void __launch_bounds__(128) chunk_simple_kernel(const ChunkParams p) {
+// A run of an item's key tiles that one CTA takes.
+struct Segment {
+  int row0;        // packed row of the item's first token
+  int tokens;      // of the item
+  int pos0;        // position of the first token
+  int len;         // rows of the request in the cache
+  int b, hk;       // request, kv head
+  int head0, heads;     // first query head, and how many of them the tile's GB hold
+  int kt0, nt;     // key tiles [kt0, kt0 + nt)
+  int two;         // two query tiles
+  int whole;       // the item's only segment
+  int part;        // partial slot
+  int first_cta, n_parts;
+  int last;        // no segment: the CTA is done
+};
+
+// What the warps share, behind the tiles.
+template <int SLOTS>
+struct Shared {
+  uint64_t full[SLOTS], empty[SLOTS], seg_full[CH_SEGS], seg_empty[CH_SEGS];
+  uint64_t q_full, q_empty, v_raw, s_full[2], p_full[2], o_full[2], join, done;
+  Segment seg[CH_SEGS];
+  float m[2][CH_ROWS], l[2][CH_ROWS];
+  uint32_t tmem;
+  int abort, never, prev;
+};
+template <int D>
+constexpr size_t chunk_smem() {
+  return Shape<D>::TILES + sizeof(Shared<Shape<D>::SLOTS>);
+}
+static_assert(chunk_smem<128>() <= (227u << 10) && chunk_smem<64>() <= (227u << 10), "one CTA's shared memory");
+
+// ---- the walk over items (one warp) -------------------------------------------
+
+struct Request {
+  int row0, n, len, per, items;              // tokens per item, items per kv head part
+  bool bad, over;
+};
+
+__device__ __forceinline__ Request request_of(const ChunkParams& p, int b) {
+  Request r;
+  int lo, hi;
+  r.bad = !request_rows(p.rows, b, lo, hi);
+  const int L = p.len[b];
+  r.over = L > p.cap;
+  r.len = max(0, min(L, p.cap));
+  r.row0 = lo;
+  r.n = hi - lo;
+  r.per = r.n <= p.T ? p.T : 2 * p.T;
+  r.items = (r.n + r.per - 1) / r.per;
+  return r;
+}
+
+// Key tiles [kt0, kt1) of item q (kt1 <= kt0: none of its rows sees a key).
+__device__ __forceinline__ void item_tiles(const ChunkParams& p, const Request& r, int q, int& kt0, int& kt1) {
+  const long long first = static_cast<long long>(r.len) - r.n + static_cast<long long>(q) * r.per;
+  const long long end = min(static_cast<long long>(r.len), first + r.per);
+  const long long lo = p.window > 0 ? max(0ll, first - p.window + 1) : 0ll;
+  kt0 = static_cast<int>(lo / CH_KEYS);
+  kt1 = end > lo ? static_cast<int>((end + CH_KEYS - 1) / CH_KEYS) : kt0;
+}
+__device__ __forceinline__ int item_units(const ChunkParams& p, const Request& r, int q) {
+  int a, z;
+  item_tiles(p, r, q, a, z);
+  return max(1, z - a);
+}
+
+// Units of one kv head part of the lane's own request (every lane calls it;
+// requests of many items are summed by the whole warp).
+__device__ __forceinline__ long long request_units(const ChunkParams& p, const Request& r, int lane) {
+  constexpr int ALONE = 4;
+  long long w = 0;
+  if (r.items <= ALONE)
+    for (int q = 0; q < r.items; ++q) w += item_units(p, r, q);
+  for (unsigned todo = __ballot_sync(0xffffffffu, r.items > ALONE); todo; todo &= todo - 1) {
+    const int l = __ffs(todo) - 1;
+    Request s;
+    s.n = __shfl_sync(0xffffffffu, r.n, l);
+    s.len = __shfl_sync(0xffffffffu, r.len, l);
+    s.per = __shfl_sync(0xffffffffu, r.per, l);
+    s.items = __shfl_sync(0xffffffffu, r.items, l);
+    long long part = 0;
+    for (int q = lane; q < s.items; q += 32) part += item_units(p, s, q);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+    if (lane == l) w = part;
+  }
+  return w;
+}
+__device__ __forceinline__ long long warp_scan(long long v, int lane) {   // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  return v;
+}
+
+// The walk's place: item q of kv head part hs of request b, whose first unit
+// is `unit` of all.
+struct Walk {
+  Request r;
+  int b, hs, q;
+  long long unit;
+};
+
+// Requests' units over the batch; optionally (u0 >= 0) the item that holds
+// unit u0.  Returns the sum.
+__device__ long long scan_batch(const ChunkParams& p, int lane, long long u0, bool report, Walk& w) {
+  const int parts = p.hkv * p.nsub;
+  long long sum = 0;
+  for (int b0 = 0; b0 < p.rows.B; b0 += 32) {
+    const int b = b0 + lane;
+    Request r{};
+    r.per = 1;
+    if (b < p.rows.B) r = request_of(p, b);
+    if (report && r.bad) set_status(p.status, EAGLE_ERR_INVALID_ARG);
+    if (report && r.over && r.n > 0) set_status(p.status, EAGLE_ERR_CAPACITY);
+    const long long units = request_units(p, r, lane);
+    const long long end = sum + warp_scan(units * parts, lane);
+    if (u0 >= 0) {
+      const unsigned past = __ballot_sync(0xffffffffu, end > u0);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        w.b = b0 + l;
+        w.r.row0 = __shfl_sync(0xffffffffu, r.row0, l);
+        w.r.n = __shfl_sync(0xffffffffu, r.n, l);
+        w.r.len = __shfl_sync(0xffffffffu, r.len, l);
+        w.r.per = __shfl_sync(0xffffffffu, r.per, l);
+        w.r.items = __shfl_sync(0xffffffffu, r.items, l);
+        const long long W = __shfl_sync(0xffffffffu, units, l);
+        const long long begin = __shfl_sync(0xffffffffu, end - units * parts, l);
+        w.hs = static_cast<int>((u0 - begin) / W);
+        long long at = begin + W * w.hs;             // first unit of the part
+        for (int q0 = 0;; q0 += 32) {
+          const int q = q0 + lane;
+          const long long v = q < w.r.items ? item_units(p, w.r, q) : 0;
+          const long long upto = at + warp_scan(v, lane);
+          const unsigned hit = __ballot_sync(0xffffffffu, upto > u0 && q < w.r.items);
+          if (hit) {
+            const int k = __ffs(hit) - 1;
+            w.q = q0 + k;
+            w.unit = __shfl_sync(0xffffffffu, upto - v, k);
+            return sum;
+          }
+          at = __shfl_sync(0xffffffffu, upto, 31);
+          if (q0 + 32 >= w.r.items) break;            // (not reached: the part's units end past u0)
+        }
+        w.q = w.r.items - 1;
+        w.unit = at;
+        return sum;
+      }
+    }
+    sum = __shfl_sync(0xffffffffu, end, 31);
+  }
+  return sum;
+}
+
+// To the next item; false at the batch's end.
+__device__ __forceinline__ bool walk_on(const ChunkParams& p, Walk& w, int lane) {
+  if (++w.q < w.r.items) return true;
+  w.q = 0;
+  if (++w.hs < p.hkv * p.nsub) return true;
+  w.hs = 0;
+  for (int b0 = w.b + 1; b0 < p.rows.B; b0 += 32) {
+    Request r{};
+    if (b0 + lane < p.rows.B) r = request_of(p, b0 + lane);
+    const unsigned some = __ballot_sync(0xffffffffu, r.n > 0);
+    if (some) {
+      const int l = __ffs(some) - 1;
+      w.b = b0 + l;
+      w.r.row0 = __shfl_sync(0xffffffffu, r.row0, l);
+      w.r.n = __shfl_sync(0xffffffffu, r.n, l);
+      w.r.len = __shfl_sync(0xffffffffu, r.len, l);
+      w.r.per = __shfl_sync(0xffffffffu, r.per, l);
+      w.r.items = __shfl_sync(0xffffffffu, r.items, l);
+      return true;
+    }
+  }
+  return false;
+}
+
+// ---- softmax of one tile -------------------------------------------------------
+
+// This thread's row of S_w: maximum, exponentials, P_w into tensor memory over
+// S_w, the row sum; O_w rescaled when the maximum was raised.  Column j is
+// visible when lo <= j <= hi (masked tiles), or all are.
+template <int D>
+__device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, bool masked, int lo, int hi, bool valid,
+                                             float c, float& m_ref, float& l_sum) {
+  float sv[4][32];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) sm100::tmem_ld32(s_addr + 32u * k, sv[k]);
+  sm100::tmem_wait_ld();
+  if (masked) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int j = 0; j < 32; ++j) sv[k][j] = (32 * k + j >= lo && 32 * k + j <= hi) ? sv[k][j] : -INFINITY;
+  }
+  float mx[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    mx[k] = sv[k][0];
+#pragma unroll
+    for (int j = 1; j < 32; ++j) mx[k] = fmaxf(mx[k], sv[k][j]);
+  }
+  const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+  const bool raise = valid && (mt > m_ref + CH_RAISE || (m_ref == -INFINITY && mt != -INFINITY));
+  const bool rescale = raise && m_ref != -INFINITY;
+  if (__any_sync(0xffffffffu, rescale)) {
+    // S_w of this tile was complete after every earlier P_w V: O_w is at rest
+    const float f = rescale ? sm100::exp2(m_ref - mt) : 1.f;
+#pragma unroll
+    for (int q = 0; q < D / 16; ++q) {
+      float o[16];
+      sm100::tmem_ld16(o_addr + 16u * q, o);
+      sm100::tmem_wait_ld();
+      uint32_t x[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(o[j] * f);
+      sm100::tmem_st16(o_addr + 16u * q, x);
+    }
+    l_sum *= f;
+  }
+  if (raise) m_ref = mt;
+  const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
+  float part[2] = {0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t pw[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const float e0 = sm100::exp2(fmaf(sv[k][2 * j], c, nm)), e1 = sm100::exp2(fmaf(sv[k][2 * j + 1], c, nm));
+      part[0] += e0;
+      part[1] += e1;
+      const __nv_bfloat162 h = __floats2bfloat162_rn(e0, e1);
+      pw[j] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    sm100::tmem_st16(s_addr + 16u * k, pw);    // columns below those still to be read: all are in registers
+  }
+  l_sum += part[0] + part[1];
+  sm100::tmem_wait_st();
+}
+
+// ---- the kernel ------------------------------------------------------------------
+
+template <int D>
+__global__ void __launch_bounds__(CH_THREADS, 1)
+    chunk_attn_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUtensorMap qmap,
+                      const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  using S = Shape<D>;
+  constexpr int SLOTS = S::SLOTS;
+  constexpr int PART = 2 * CH_ROWS * (D + 2);            // floats of a partial
   const LaunchStamp ls(p.stamp);
+  // no static shared memory: the tiles start at the CTA's window, 1024-byte aligned (checked)
+  extern __shared__ __align__(1024) uint8_t sm[];
+  uint8_t* ring = sm + 2 * S::TILE;
+  Shared<SLOTS>& sh = *reinterpret_cast<Shared<SLOTS>*>(sm + S::TILES);
+  if (sm100::smem_u32(sm) & 1023u) {
+    if (threadIdx.x == 0 && blockIdx.x == 0) set_status(p.status, EAGLE_ERR_UNSUPPORTED);
+    return;
+  }
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort_flag = &sh.abort;
+  volatile int* never = &sh.never;
+  if (tid == 0) {
+    for (int i = 0; i < SLOTS; ++i) {
+      sm100::mbar_init(&sh.full[i], 1);
+      sm100::mbar_init(&sh.empty[i], 1);
+    }
+    for (int i = 0; i < CH_SEGS; ++i) {
+      sm100::mbar_init(&sh.seg_full[i], 1);
+      sm100::mbar_init(&sh.seg_empty[i], 2 + CH_SOFT_WARPS);   // loader, MMA thread, softmax warps
+    }
+    sm100::mbar_init(&sh.q_full, 1);
+    sm100::mbar_init(&sh.q_empty, 1);
+    sm100::mbar_init(&sh.v_raw, 1);
+    for (int i = 0; i < 2; ++i) {
+      sm100::mbar_init(&sh.s_full[i], 1);
+      sm100::mbar_init(&sh.p_full[i], 4);
+      sm100::mbar_init(&sh.o_full[i], 1);
+    }
+    sm100::mbar_init(&sh.join, CH_SOFT_WARPS);
+    sm100::mbar_init(&sh.done, 1);
+    sh.abort = 0;
+    sh.never = 0;
+    sm100::fence_barrier_init();
+  }
   pdl_wait();
   ls.waited();
+  if (warp == CH_MMA_WARP) {
+    sm100::tmem_alloc(&sh.tmem, CH_TM_COLS);
+    sm100::tmem_relinquish();
+  }
+  sm100::tc_fence_before();
+  __syncthreads();
+  sm100::tc_fence_after();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (blockIdx.x == 0 && blockIdx.y == 0)
-    for (int b = threadIdx.x; b < p.rows.B; b += blockDim.x) {
-      int lo, hi;
-      if (!request_rows(p.rows, b, lo, hi)) set_status(p.status, EAGLE_ERR_INVALID_ARG);
-    }
-  const int row = blockIdx.x, h = blockIdx.y * 4 + warp;
-  if (h >= p.hq) return;
-  const int b = request_of_row(p.rows, row, lane);
-  if (b < 0) return;
-  int lo, hi;
-  request_rows(p.rows, b, lo, hi);
-  int L = p.len[b];
-  if (L > p.cap) {
-    if (lane == 0) set_status(p.status, EAGLE_ERR_CAPACITY);
-    L = p.cap;
-  }
-  const int pos = L - (hi - lo) + (row - lo);
-  const int first = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-  const int hk = h / p.G;
-  float q[4], o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    q[i] = lane + 32 * i < p.dh ? bf16_to_f32(p.q[row * p.ld_q + h * p.dh + lane + 32 * i]) * p.c : 0.f;
-  float m = -INFINITY, l = 0.f;
-  for (int j = first; j <= pos; ++j) {
-    const long long at = p.paged.table ? paged_row(p.paged, b, j) : static_cast<long long>(b) * p.cap + j;
-    float s = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
-    if (at >= 0) {
-      const size_t base = (static_cast<size_t>(at) * p.hkv + hk) * p.dh;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (lane + 32 * i < p.dh) {
-          s += q[i] * bf16_to_f32(p.k[base + lane + 32 * i]);
-          v[i] = bf16_to_f32(p.v[base + lane + 32 * i]);
+  const uint32_t tmem = sh.tmem;
+  const uint32_t sbase = sm100::smem_u32(sm);
+  const uint32_t rbase = sbase + 2 * S::TILE;
+
+  auto give_up = [&]() {
+    set_status(p.status, EAGLE_ERR_TIMEOUT);
+    sh.abort = 1;
+  };
+  // every lane waits; the answer is the warp's
+  auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
+    return static_cast<bool>(__all_sync(0xffffffffu, sm100::mbar_wait(bar, parity, abort_flag)));
+  };
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CH_REGS_FEW));
+    if (warp == CH_SCHED_WARP) {
+      // ---- scheduler ----
+      Walk w{};
+      const int parts = p.hkv * p.nsub;
+      const long long U = scan_batch(p, lane, -1, blockIdx.x == 0, w);
+      const long long n = min(static_cast<long long>(gridDim.x), U);     // CTAs with work
+      const long long c = blockIdx.x;
+      long long at = c < n ? U * c / n : 0, end = c < n ? U * (c + 1) / n : 0;
+      if (at < end) scan_batch(p, lane, at, false, w);
+      bool ok = true;
+      for (int i = 0; ok; ++i) {
+        const int slot = i % CH_SEGS;
+        if (i >= CH_SEGS) ok = warp_wait(&sh.seg_empty[slot], static_cast<uint32_t>((i / CH_SEGS - 1) & 1));
+        if (!ok) break;
+        Segment g{};
+        g.last = at >= end;
+        if (!g.last) {
+          int kt0, kt1;
+          item_tiles(p, w.r, w.q, kt0, kt1);
+          const int units = max(1, kt1 - kt0);
+          const int x0 = static_cast<int>(at - w.unit);
+          const int x1 = static_cast<int>(min(static_cast<long long>(units), end - w.unit));
+          const int hk = w.hs / p.nsub, sub = w.hs - hk * p.nsub;
+          const int t0 = w.q * w.r.per;
+          g.row0 = w.r.row0 + t0;
+          g.tokens = min(w.r.per, w.r.n - t0);
+          g.pos0 = w.r.len - w.r.n + t0;
+          g.len = w.r.len;
+          g.b = w.b;
+          g.hk = hk;
+          g.head0 = hk * p.G + sub * p.GB;
+          g.heads = min(p.GB, p.G - sub * p.GB);
+          g.kt0 = kt0 + x0;
+          g.nt = kt1 > kt0 ? x1 - x0 : 0;
+          g.two = g.tokens > p.T;
+          g.whole = x0 == 0 && x1 == units;
+          if (!g.whole) {
+            // the CTA that holds unit u: the largest whose range begins at or before it
+            g.first_cta = static_cast<int>(((w.unit + 1) * n - 1) / U);
+            g.n_parts = static_cast<int>(((w.unit + units) * n - 1) / U) - g.first_cta + 1;
+            g.part = 2 * static_cast<int>(c) + (x0 == 0 ? 1 : 0);
+          }
+          at = w.unit + x1;
+          if (x1 == units) {
+            w.unit += units;
+            if (at < end && !walk_on(p, w, lane)) at = end;
+          }
         }
-    } else if (lane == 0) {
-      set_status(p.status, EAGLE_ERR_INVALID_ARG);
+        if (lane == 0) {
+          sh.seg[slot] = g;
+          sm100::mbar_arrive(&sh.seg_full[slot]);
+        }
+        __syncwarp();
+        if (g.last) break;
+      }
+      if (!ok && lane == 0) give_up();
+      (void)parts;
+    } else if (warp == CH_LOAD_WARP) {
+      // ---- loader ----
+      const bool paged = p.paged.table != nullptr;
+      const int boxes = CH_KEYS / p.box;
+      int e = 0;                               // ring elements so far: K and V tiles alternate
+      int segs = 0;                            // segments with tiles so far
+      uint32_t raw = 0;                        // V tiles that needed zeroing so far
+      bool ok = true;
+      for (int i = 0; ok; ++i) {
+        const int slot = i % CH_SEGS;
+        ok = warp_wait(&sh.seg_full[slot], static_cast<uint32_t>((i / CH_SEGS) & 1));
+        if (!ok) break;
+        const Segment g = sh.seg[slot];
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive(&sh.seg_empty[slot]);
+        if (g.last) break;
+        if (g.nt == 0) continue;
+        const int32_t* table = paged ? p.paged.table + static_cast<size_t>(g.b) * p.paged.per_req : nullptr;
+        // the block of box j of key tile t, out of range where nothing is to be read
+        auto block_at = [&](int t, int j) {
+          const int pos = (g.kt0 + t) * CH_KEYS + j * p.box;
+          if (pos >= g.len) return p.paged.n_blocks;
+          const int blk = table[pos >> p.paged.shift];
+          if (blk >= 0 && blk < p.paged.n_blocks) return blk;
+          set_status(p.status, EAGLE_ERR_INVALID_ARG);
+          return p.paged.n_blocks;
+        };
+        int blk = paged && lane < boxes ? block_at(0, lane) : 0;   // box `lane` of the tile at hand
+        auto load = [&](int t, int m) {
+          const int s = e % SLOTS;
+          if (e >= SLOTS && !warp_wait(&sh.empty[s], static_cast<uint32_t>((e / SLOTS - 1) & 1))) return false;
+          uint8_t* dst = ring + s * S::TILE;
+          const int k0 = (g.kt0 + t) * CH_KEYS;
+          const CUtensorMap* map = m == 0 ? &kmap : &vmap;
+          const bool zero = m == 1 && k0 + CH_KEYS > g.len;
+          uint64_t* bar = zero ? &sh.v_raw : &sh.full[s];
+          if (lane == 0) sm100::mbar_arrive_expect_tx(bar, S::TILE);
+          __syncwarp();
+          for (int j = lane; j < boxes; j += 32) {
+            const int z = !paged ? g.b : j < 32 ? blk : block_at(t, j);
+            const int y = !paged ? k0 : (k0 + j * p.box) & ((1 << p.paged.shift) - 1);
+#pragma unroll
+            for (int h = 0; h < S::HALVES; ++h)
+              sm100::tma_load_4d(dst + h * CH_HALF + j * p.box * 128, map, 64 * h, g.hk, y, z, bar);
+          }
+          if (zero) {
+            // rows past the length may hold anything, and 0 x NaN is NaN: V's become zeros
+            if (!warp_wait(&sh.v_raw, raw & 1)) return false;
+            ++raw;
+            const int first = max(0, g.len - k0);
+            for (int x = lane; x < (CH_KEYS - first) * 8 * S::HALVES; x += 32) {
+              const int h = x / ((CH_KEYS - first) * 8), y = x - h * (CH_KEYS - first) * 8;
+              *reinterpret_cast<uint4*>(dst + h * CH_HALF + first * 128 + y * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            sm100::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) sm100::mbar_arrive(&sh.full[s]);
+          }
+          ++e;
+          return true;
+        };
+        auto load_q = [&]() {
+          if (segs > 0 && !warp_wait(&sh.q_empty, static_cast<uint32_t>((segs - 1) & 1))) return false;
+          ++segs;
+          if (lane == 0) {
+            const uint32_t bytes = static_cast<uint32_t>(p.GB * p.T) * 128u * S::HALVES;
+            const int tiles = g.two ? 2 : 1;
+            sm100::mbar_arrive_expect_tx(&sh.q_full, bytes * tiles);
+            for (int w = 0; w < tiles; ++w)
+              for (int h = 0; h < S::HALVES; ++h)
+                sm100::tma_load_3d(sm + w * S::TILE + h * CH_HALF, &qmap, 64 * h, g.head0, g.row0 + w * p.T, &sh.q_full);
+          }
+          __syncwarp();
+          return true;
+        };
+        // the first K and V while the item before still uses its Q
+        for (int t = 0; ok && t < g.nt; ++t) {
+          ok = load(t, 0) && load(t, 1) && (t > 0 || load_q());
+          if (paged && ok && t + 1 < g.nt && lane < boxes) blk = block_at(t + 1, lane);
+        }
+      }
+      if (!ok && lane == 0) give_up();
+      // no TMA copy may still be landing when the CTA leaves
+      for (int u = max(0, e - SLOTS); u < e; ++u)
+        sm100::mbar_wait(&sh.full[u % SLOTS], static_cast<uint32_t>((u / SLOTS) & 1), never);
+      if (segs > 0) sm100::mbar_wait(&sh.q_full, static_cast<uint32_t>((segs - 1) & 1), never);
+    } else if (warp == CH_MMA_WARP) {
+      // ---- MMA issuer ----
+      if (lane == 0) {
+        constexpr uint32_t HI = sm100::DESC_SW128_HI;
+        const uint32_t id_s = sm100::idesc_bf16_f32(CH_ROWS, CH_KEYS);
+        const uint32_t id_o = sm100::idesc_bf16_f32(CH_ROWS, D) | (1u << 16);     // B (V) MN-major
+        int e0 = 0, segs = 0;
+        uint32_t p_phase[2] = {0u, 0u};
+        bool ok = true;
+        for (int i = 0; ok; ++i) {
+          const int slot = i % CH_SEGS;
+          ok = sm100::mbar_wait(&sh.seg_full[slot], static_cast<uint32_t>((i / CH_SEGS) & 1), abort_flag);
+          if (!ok) break;
+          const int nt = sh.seg[slot].nt, last = sh.seg[slot].last;
+          const bool two = sh.seg[slot].two;
+          sm100::mbar_arrive(&sh.seg_empty[slot]);
+          if (last) break;
+          if (nt == 0) continue;
+          ok = sm100::mbar_wait(&sh.q_full, static_cast<uint32_t>(segs & 1), abort_flag);
+          ++segs;
+          // element x's slot has landed
+          auto landed = [&](int x) {
+            return sm100::mbar_wait(&sh.full[x % SLOTS], static_cast<uint32_t>((x / SLOTS) & 1), abort_flag);
+          };
+          // S_w of key tile t
+          auto issue_s = [&](int w, int t) {
+            const int x = e0 + 2 * t;
+            if (!landed(x)) return false;
+            sm100::tc_fence_after();
+            const uint32_t qlo = sm100::desc_lo(sbase + (two ? w * S::TILE : 0u), 16);
+            const uint32_t klo = sm100::desc_lo(rbase + (x % SLOTS) * S::TILE, 16);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = ((k >> 2) * CH_HALF + (k & 3) * 32) >> 4;
+              sm100::mma_ss32(tmem + CH_TM_S + 128u * w, qlo + off, klo + off, HI, id_s, k > 0 ? 1u : 0u);
+            }
+            sm100::mma_commit(&sh.s_full[w]);
+            if (!two || w == 1) {
+              sm100::mma_commit(&sh.empty[x % SLOTS]);
+              if (t == nt - 1) sm100::mma_commit(&sh.q_empty);
+            }
+            return true;
+          };
+          // O_w += P_w V of key tile t
+          auto issue_o = [&](int w, int t, bool first) {
+            const int x = e0 + 2 * t + 1;
+            if (!sm100::mbar_wait(&sh.p_full[w], p_phase[w] & 1, abort_flag) || !landed(x)) return false;
+            ++p_phase[w];
+            sm100::tc_fence_after();
+            const uint32_t vlo = sm100::desc_lo(rbase + (x % SLOTS) * S::TILE, CH_HALF);
+#pragma unroll
+            for (int k = 0; k < CH_KEYS / 16; ++k)
+              sm100::mma_ts32(tmem + CH_TM_O + 128u * w, tmem + CH_TM_S + 128u * w + 8u * k, vlo + ((k * 2048) >> 4), HI,
+                              id_o, k > 0 || !first ? 1u : 0u);
+            if (!two || w == 1) sm100::mma_commit(&sh.empty[x % SLOTS]);
+            if (t + (two ? 1 : 2) >= nt) sm100::mma_commit(&sh.o_full[w]);
+            return true;
+          };
+          ok = ok && issue_s(0, 0) && (two ? issue_s(1, 0) : nt > 1 ? issue_s(1, 1) : true);
+          for (int j = 0; ok && j < nt; j += two ? 1 : 2)
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              const int t = two ? j : j + w, next = t + (two ? 1 : 2);
+              if (t >= nt || !ok) continue;
+              ok = issue_o(w, t, j == 0) && (next >= nt || issue_s(w, next));
+            }
+          e0 += 2 * nt;
+        }
+        if (!ok) give_up();
+        // every MMA issued here has completed before the tensor memory goes
+        sm100::mma_commit(&sh.done);
+        sm100::mbar_wait(&sh.done, 0u, never);
+      }
+      __syncwarp();
     }
-    s = warp_sum(s);
-    const float mn = fmaxf(m, s), f = exp2f(m - mn), w = exp2f(s - mn);
-    l = l * f + w;
+  } else {
+    // ---- softmax ----
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(CH_REGS_SOFT));
+    const int w = (warp - CH_SOFT_WARP0) >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t s_addr = tmem + CH_TM_S + 128u * w + lane_base, o_addr = tmem + CH_TM_O + 128u * w + lane_base;
+    const int st = tid - 32 * CH_SOFT_WARP0;               // 0 .. 255
+    const int tok = row / p.GB, head = row - tok * p.GB;   // of this row in its tile
+    uint32_t s_phase = 0, o_phase = 0, j_phase = 0;
+    bool ok = true;
+    // all softmax warps: shared memory and tensor memory of the others' last step may be used after it
+    auto join = [&]() {
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(&sh.join);
+      const bool r = warp_wait(&sh.join, j_phase & 1);
+      ++j_phase;
+      return r;
+    };
+    for (int i = 0; ok; ++i) {
+      const int slot = i % CH_SEGS;
+      ok = warp_wait(&sh.seg_full[slot], static_cast<uint32_t>((i / CH_SEGS) & 1));
+      if (!ok) break;
+      const Segment g = sh.seg[slot];
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(&sh.seg_empty[slot]);
+      if (g.last) break;
+      const bool two = g.two;
+      const int t_item = (two ? w * p.T : 0) + tok;        // the row's token in the item
+      const bool valid = tok < p.T && t_item < g.tokens && head < g.heads;
+      const int pos = g.pos0 + t_item;
+      const int lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+      // bounds of the warp's rows, so that a tile they all see whole is not masked
+      const int pos_least = __reduce_min_sync(0xffffffffu, valid ? pos : INT_MAX);
+      const int lo_most = __reduce_max_sync(0xffffffffu, valid ? lo : INT_MIN);
+      const bool some = __any_sync(0xffffffffu, valid);
+      float m_ref = -INFINITY, l_sum = 0.f;
+      const int step = two ? 1 : 2;
+      int mine = 0;
+      for (int t = two ? 0 : w; t < g.nt; t += step) {
+        ok = warp_wait(&sh.s_full[w], s_phase & 1);
+        if (!ok) break;
+        ++s_phase;
+        ++mine;
+        sm100::tc_fence_after();
+        if (some) {
+          const int k0 = (g.kt0 + t) * CH_KEYS;
+          const bool masked = k0 + CH_KEYS - 1 > pos_least || k0 < lo_most;
+          softmax_tile<D>(s_addr, o_addr, masked, lo - k0, pos - k0, valid, p.c, m_ref, l_sum);
+        }
+        sm100::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive(&sh.p_full[w]);
+      }
+      if (ok && mine > 0) {
+        ok = warp_wait(&sh.o_full[w], o_phase & 1);
+        ++o_phase;
+      }
+      if (!ok) break;
+      sm100::tc_fence_after();
+      // The item's rows are 0 .. 255 (two tiles) or 0 .. 127; this thread holds D columns of its own row, or (one
+      // tile, whose key tiles both groups shared) half the columns of the join of O_0 and O_1.
+      const int r_item = two ? w * CH_ROWS + row : row;
+      float a[2] = {1.f, 0.f};
+      float m_row = m_ref, l_row = l_sum;
+      if (!two) {
+        sh.m[w][row] = m_ref;
+        sh.l[w][row] = l_sum;
+        ok = join();
+        if (!ok) break;
+        const float m0 = sh.m[0][row], m1 = sh.m[1][row];
+        m_row = fmaxf(m0, m1);
+        a[0] = m0 == -INFINITY ? 0.f : sm100::exp2(m0 - m_row);
+        a[1] = m1 == -INFINITY ? 0.f : sm100::exp2(m1 - m_row);
+        l_row = a[0] * sh.l[0][row] + a[1] * sh.l[1][row];
+      }
+      const int col0 = two ? 0 : w * (D / 2), cols = two ? D : D / 2;
+      const float inv = g.whole ? (l_row > 0.f ? 1.f / l_row : 0.f) : 1.f;
+      float* part = p.part + static_cast<size_t>(g.part) * PART;
+      if (some) {
+        for (int cc = col0; cc < col0 + cols; cc += 32) {
+          float o[32];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = o[i] * f + w * v[i];
-    m = mn;
+          for (int j = 0; j < 32; ++j) o[j] = 0.f;
+          if (g.nt > 0) {
+            if (two) {
+              sm100::tmem_ld32(o_addr + cc, o);
+              sm100::tmem_wait_ld();
+            } else {
+              // an O whose weight is 0 in every row may never have been written
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                if (__any_sync(0xffffffffu, a[k] != 0.f)) {
+                  float v[32];
+                  sm100::tmem_ld32(tmem + CH_TM_O + 128u * k + lane_base + cc, v);
+                  sm100::tmem_wait_ld();
+                  if (a[k] != 0.f) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = fmaf(a[k], v[j], o[j]);
+                  }
+                }
+            }
+          }
+          if (!valid) continue;
+          if (l_row == 0.f) {                  // no key seen: whatever the tile's products left
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = 0.f;
+          }
+          if (g.whole) {
+            uint16_t* dst = p.out + (static_cast<size_t>(g.row0) + t_item) * p.ld_o + (g.head0 + head) * p.dh + cc;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              if (cc + 8 * q < p.dh) {
+                uint32_t x[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const __nv_bfloat162 h = __floats2bfloat162_rn(o[8 * q + 2 * j] * inv, o[8 * q + 2 * j + 1] * inv);
+                  x[j] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+                *reinterpret_cast<uint4*>(dst + 8 * q) = make_uint4(x[0], x[1], x[2], x[3]);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              reinterpret_cast<float4*>(part)[(cc / 4 + q) * (2 * CH_ROWS) + r_item] =
+                  make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          }
+        }
+      }
+      if (!g.whole && valid && (two || w == 0)) {
+        part[2 * CH_ROWS * D + r_item] = m_row;
+        part[2 * CH_ROWS * D + 2 * CH_ROWS + r_item] = l_row;
+      }
+      sm100::tc_fence_before();
+      if (g.whole) {
+        // one tile: O_0 and O_1 were read by both groups, the next item's products may not overwrite them before
+        if (!two) ok = join();
+        continue;
+      }
+      ok = join();                             // every thread's partials come first
+      if (!ok) break;
+      if (st == 0) {
+        sh.prev = arrive_acq_rel(&p.cnt[g.first_cta]);
+        if (sh.prev == g.n_parts - 1) p.cnt[g.first_cta] = 0;
+      }
+      ok = join();
+      if (!ok) break;
+      const bool merge = sh.prev == g.n_parts - 1;
+      if (!merge) continue;
+      // ---- the last of an item's CTAs: all partials, in CTA order ----
+      const int n_rows = two ? 2 * CH_ROWS : min(CH_ROWS, g.tokens * p.GB);
+      auto slot_of = [&](int k) {
+        return p.part + static_cast<size_t>(k == 0 ? 2 * g.first_cta + 1 : 2 * (g.first_cta + k)) * PART;
+      };
+      for (int x = st; x < n_rows * (D / 4); x += 256) {
+        const int c4 = x / n_rows, r = x - c4 * n_rows;
+        const int rt = r & (CH_ROWS - 1), t = rt / p.GB, h = rt - t * p.GB;
+        const int ti = (r >= CH_ROWS ? p.T : 0) + t;
+        if (t >= p.T || ti >= g.tokens || h >= g.heads || 4 * c4 >= p.dh) continue;
+        float M = -INFINITY;
+        for (int k = 0; k < g.n_parts; ++k) M = fmaxf(M, __ldcg(slot_of(k) + 2 * CH_ROWS * D + r));
+        float l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = 0; k < g.n_parts; ++k) {
+          const float* sp = slot_of(k);
+          const float m = __ldcg(sp + 2 * CH_ROWS * D + r);
+          const float f = m == -INFINITY ? 0.f : sm100::exp2(m - M);
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(sp) + c4 * (2 * CH_ROWS) + r);
+          l = fmaf(f, __ldcg(sp + 2 * CH_ROWS * D + 2 * CH_ROWS + r), l);
+          o.x = fmaf(f, v.x, o.x);
+          o.y = fmaf(f, v.y, o.y);
+          o.z = fmaf(f, v.z, o.z);
+          o.w = fmaf(f, v.w, o.w);
+        }
+        const float z = l > 0.f ? 1.f / l : 0.f;
+        const __nv_bfloat162 h0 = __floats2bfloat162_rn(o.x * z, o.y * z), h1 = __floats2bfloat162_rn(o.z * z, o.w * z);
+        uint2 y;
+        y.x = *reinterpret_cast<const uint32_t*>(&h0);
+        y.y = *reinterpret_cast<const uint32_t*>(&h1);
+        *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(g.row0) + ti) * p.ld_o + (g.head0 + h) * p.dh + 4 * c4) = y;
+      }
+    }
+    if (!ok && lane == 0) give_up();
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (lane + 32 * i < p.dh) p.out[row * p.ld_o + h * p.dh + lane + 32 * i] = f32_to_bf16(o[i] * inv);
+  sm100::tc_fence_before();
+  __syncthreads();
+  if (warp == CH_MMA_WARP) {
+    sm100::tc_fence_after();
+    sm100::tmem_dealloc(tmem, CH_TM_COLS);
+  }
+}
+
+bool encode(eagle_ctx* ctx, CUtensorMap* map, const void* ptr, int rank, const cuuint64_t* dims,
+            const cuuint64_t* strides, const cuuint32_t* box) {
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return ctx->encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void*>(ptr), dims,
+                     strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch_shape(eagle_ctx* ctx, const ChunkParams& p, const CUtensorMap& qm, const CUtensorMap& km,
+                         const CUtensorMap& vm, cudaStream_t st) {
+  const cudaError_t e =
+      smem_limit_once(reinterpret_cast<const void*>(chunk_attn_kernel<D>), static_cast<int>(chunk_smem<D>()));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(chunk_attn_kernel<D>, dim3(ctx->sm_count), dim3(CH_THREADS), chunk_smem<D>(), st, p, qm, km, vm);
 }
 
 }  // namespace
+
+size_t chunk_part_bytes(int sm_count, int head_dim) {
+  return static_cast<size_t>(2) * sm_count * 2 * CH_ROWS * ((head_dim > 64 ? 128 : 64) + 2) * sizeof(float);
+}
 
 cudaError_t launch_chunk_attn(eagle_ctx* ctx, int batch, const eagle_rows* rows, const uint16_t* q, int ld_q,
                               const eagle_kv* kv, int window, float scale, uint16_t* out, int ld_out, void* ws,
@@ -91,25 +841,42 @@ cudaError_t launch_chunk_attn(eagle_ctx* ctx, int batch, const eagle_rows* rows,
   const eagle_dims& D = ctx->dims;
   ChunkParams p{};
   p.rows = PackedRows{rows->row_start, rows->n_rows, batch};
-  p.hq = D.n_q_heads;
   p.hkv = D.n_kv_heads;
   p.dh = D.head_dim;
   p.G = D.n_q_heads / D.n_kv_heads;
-  p.q = q;
+  p.GB = std::min(p.G, CH_ROWS);
+  p.T = CH_ROWS / p.GB;
+  p.nsub = ceil_div(p.G, p.GB);
   p.out = out;
-  p.ld_q = ld_q;
   p.ld_o = ld_out;
-  p.k = kv->k;
-  p.v = kv->v;
   p.cap = kv->cap;
   p.window = window >= kv->cap ? 0 : window;   // a window of the whole cache is none
   p.len = kv->len;
   p.paged = paged_of(&kv->paging, kv->cap);
+  const bool paged = p.paged.table != nullptr;
+  const int bs = paged ? kv->paging.block_size : kv->cap;
+  p.box = paged ? std::min(bs, CH_KEYS) : CH_KEYS;
   p.c = scale * 1.4426950408889634f;
+  p.part = ws_ptr<float>(ws, ctx->ws.attn_part);
+  p.cnt = ws_ptr<int>(ws, ctx->ws.chunk_cnt);
   p.status = ws_ptr<int>(ws, ctx->ws.status);
+  // q as {element, head, row}; a K or V pool as {element, kv head, row of a block, block} (contiguous: row, request)
+  const cuuint64_t e2 = 2, dh = static_cast<cuuint64_t>(p.dh);
+  const cuuint64_t qd[3] = {dh, static_cast<cuuint64_t>(D.n_q_heads), static_cast<cuuint64_t>(rows->n_rows)};
+  const cuuint64_t qs[2] = {dh * e2, static_cast<cuuint64_t>(ld_q) * e2};
+  const cuuint32_t qb[3] = {64, static_cast<cuuint32_t>(p.GB), static_cast<cuuint32_t>(p.T)};
+  const cuuint64_t kd[4] = {dh, static_cast<cuuint64_t>(p.hkv), static_cast<cuuint64_t>(bs),
+                            static_cast<cuuint64_t>(paged ? kv->paging.n_blocks : batch)};
+  const cuuint64_t row = dh * p.hkv * e2;
+  const cuuint64_t ks[3] = {dh * e2, row, row * bs};
+  const cuuint32_t kb[4] = {64, 1, static_cast<cuuint32_t>(p.box), 1};
+  CUtensorMap qm, km, vm;
+  if (!encode(ctx, &qm, q, 3, qd, qs, qb) || !encode(ctx, &km, kv->k, 4, kd, ks, kb) ||
+      !encode(ctx, &vm, kv->v, 4, kd, ks, kb))
+    return cudaErrorInvalidValue;
   p.stamp = stamp_slot(ctx, EAGLE_K_CHUNK_ATTN);
   trace_before(ctx, EAGLE_K_CHUNK_ATTN, st);
-  const cudaError_t e = launch_pdl(chunk_simple_kernel, dim3(rows->n_rows, ceil_div(D.n_q_heads, 4)), dim3(128), 0, st, p);
+  const cudaError_t e = p.dh > 64 ? launch_shape<128>(ctx, p, qm, km, vm, st) : launch_shape<64>(ctx, p, qm, km, vm, st);
   ctx->launches++;
   trace_after(ctx, EAGLE_K_CHUNK_ATTN, st);
   return e;
