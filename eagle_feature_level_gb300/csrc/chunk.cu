@@ -21,8 +21,10 @@
 //   warp 0      loader: Q tiles, then K and V tiles by TMA into a ring (boxes
 //               of 64 elements x one block's rows, out-of-range blocks read as
 //               zeros); rows of V past the request's length are zeroed.
-//   warp 1      one thread issues the MMAs: S_w = Q_w K^T into tensor memory,
-//               O_w += P_w V with P_w (bf16) written over S_w.
+//   warps 1, 3  one thread each issues the MMAs of softmax group w = 0, 1:
+//               S_w = Q_w K^T into tensor memory, O_w += P_w V with P_w (bf16)
+//               written over S_w.  (One thread for both left the tensor cores
+//               idle while it polled barriers and committed: 42% active.)
 //   warp 2      scheduler: the walk over items, a few segments ahead.
 //   warps 4-11  two softmax warpgroups, thread = query row = tensor-memory
 //               lane.  With two tiles warpgroup w has tile w and every key
@@ -48,15 +50,16 @@ namespace eagle {
 namespace {
 
 constexpr int CH_THREADS = 384;
-constexpr int CH_LOAD_WARP = 0, CH_MMA_WARP = 1, CH_SCHED_WARP = 2, CH_SOFT_WARP0 = 4;
+constexpr int CH_LOAD_WARP = 0, CH_MMA_WARP = 1, CH_SCHED_WARP = 2, CH_SOFT_WARP0 = 4;   // MMA: 1 and 3
 constexpr int CH_SOFT_WARPS = 8;
+constexpr int CH_SOFT_THREADS = 32 * CH_SOFT_WARPS;
 constexpr int CH_KEYS = 128;                 // keys per tile
 constexpr int CH_ROWS = 128;                 // query rows per tile
 constexpr uint32_t CH_HALF = CH_KEYS * 128;  // bytes of 128 rows x 64 elements
 constexpr int CH_SEGS = 4;                   // segments the scheduler runs ahead
 constexpr float CH_RAISE = 8.0f;
 constexpr uint32_t CH_TM_S = 0, CH_TM_O = 256, CH_TM_COLS = 512;   // S_w / P_w at 128 w, O_w at 256 + 128 w
-constexpr int CH_REGS_FEW = 80, CH_REGS_SOFT = 208;
+constexpr int CH_REGS_FEW = 56, CH_REGS_SOFT = 224;
 static_assert(128 * CH_REGS_FEW + 256 * CH_REGS_SOFT <= CH_THREADS * 168, "the split fits the launch's registers");
 
 // D: elements of a head as staged (64, or 128); ring slots of one K or V tile.
@@ -105,7 +108,7 @@ struct Segment {
 template <int SLOTS>
 struct Shared {
   uint64_t full[SLOTS], empty[SLOTS], seg_full[CH_SEGS], seg_empty[CH_SEGS];
-  uint64_t q_full, q_empty, v_raw, s_full[2], p_full[2], o_full[2], join, done;
+  uint64_t q_full, q_empty, v_raw, s_full[2], p_full[2][2], o_full[2], join, done;
   Segment seg[CH_SEGS];
   float m[2][CH_ROWS], l[2][CH_ROWS];
   uint32_t tmem;
@@ -269,65 +272,160 @@ __device__ __forceinline__ bool walk_on(const ChunkParams& p, Walk& w, int lane)
 
 // ---- softmax of one tile -------------------------------------------------------
 
-// This thread's row of S_w: maximum, exponentials, P_w into tensor memory over
-// S_w, the row sum; O_w rescaled when the maximum was raised.  Column j is
-// visible when lo <= j <= hi (masked tiles), or all are.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// 64 scores' exponentials 2^(s c + nm) as bf16 pairs, and their sum.
+__device__ __forceinline__ float2 exps64(const float (&a)[32], const float (&b)[32], float c, float nm,
+                                         uint32_t (&pa)[16], uint32_t (&pb)[16]) {
+  const float2 c2 = make_float2(c, c), nm2 = make_float2(nm, nm);
+  float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const float(&s)[32] = k ? b : a;
+    uint32_t(&p)[16] = k ? pb : pa;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const float2 x = __ffma2_rn(make_float2(s[2 * j], s[2 * j + 1]), c2, nm2);
+      const float2 e = make_float2(sm100::exp2(x.x), sm100::exp2(x.y));
+      sum = __fadd2_rn(sum, e);
+      const __nv_bfloat162 h = __floats2bfloat162_rn(e.x, e.y);
+      p[j] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  return sum;
+}
+
+// This thread's row of S_w: P_w into tensor memory over S_w, and the row sum.
+// Column j is visible when lo <= j <= hi (masked tiles), or all are.  The
+// exponentials of the first half start at once, against the reference of the
+// tiles before; only where the tile's maximum passes that by CH_RAISE (and in
+// a row's first tile) is it raised, O_w and the sum rescaled, and the half
+// done again.  P_w is handed over in halves of 64 keys, so that its product
+// with V starts under the second half's exponentials.
 template <int D>
 __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, bool masked, int lo, int hi, bool valid,
-                                             float c, float& m_ref, float& l_sum) {
+                                             float c, float& m_ref, float& l_sum, uint64_t* p_full) {
   float sv[4][32];
 #pragma unroll
   for (int k = 0; k < 4; ++k) sm100::tmem_ld32(s_addr + 32u * k, sv[k]);
   sm100::tmem_wait_ld();
+  auto mask = [&](int k) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) sv[k][j] = (32 * k + j >= lo && 32 * k + j <= hi) ? sv[k][j] : -INFINITY;
+  };
   if (masked) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-      for (int j = 0; j < 32; ++j) sv[k][j] = (32 * k + j >= lo && 32 * k + j <= hi) ? sv[k][j] : -INFINITY;
+    for (int k = 0; k < 4; ++k) mask(k);
   }
   float mx[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    mx[k] = sv[k][0];
+    mx[k] = fmaxf(sv[k][0], sv[k][1]);
 #pragma unroll
-    for (int j = 1; j < 32; ++j) mx[k] = fmaxf(mx[k], sv[k][j]);
+    for (int j = 2; j < 32; j += 2) mx[k] = max3(mx[k], sv[k][j], sv[k][j + 1]);
   }
-  const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+  const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
+  uint32_t pa[16], pb[16];
+  float2 sum = exps64(sv[0], sv[1], c, m_ref == -INFINITY ? 0.f : -m_ref, pa, pb);
   const bool raise = valid && (mt > m_ref + CH_RAISE || (m_ref == -INFINITY && mt != -INFINITY));
-  const bool rescale = raise && m_ref != -INFINITY;
-  if (__any_sync(0xffffffffu, rescale)) {
-    // S_w of this tile was complete after every earlier P_w V: O_w is at rest
-    const float f = rescale ? sm100::exp2(m_ref - mt) : 1.f;
+  if (__any_sync(0xffffffffu, raise)) {
+    const bool rescale = raise && m_ref != -INFINITY;
+    if (__any_sync(0xffffffffu, rescale)) {
+      // S_w of this tile was complete after every earlier P_w V: O_w is at rest
+      const float f = rescale ? sm100::exp2(m_ref - mt) : 1.f;
+#pragma unroll 1
+      for (int q = 0; q < D / 16; ++q) {
+        float o[16];
+        sm100::tmem_ld16(o_addr + 16u * q, o);
+        sm100::tmem_wait_ld();
+        uint32_t x[16];
 #pragma unroll
-    for (int q = 0; q < D / 16; ++q) {
-      float o[16];
-      sm100::tmem_ld16(o_addr + 16u * q, o);
-      sm100::tmem_wait_ld();
-      uint32_t x[16];
-#pragma unroll
-      for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(o[j] * f);
-      sm100::tmem_st16(o_addr + 16u * q, x);
+        for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(o[j] * f);
+        sm100::tmem_st16(o_addr + 16u * q, x);
+      }
+      l_sum *= f;
     }
-    l_sum *= f;
-  }
-  if (raise) m_ref = mt;
-  const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
-  float part[2] = {0.f, 0.f};
+    if (raise) m_ref = mt;
+    // the first half's scores once more (their registers went to P)
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    uint32_t pw[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const float e0 = sm100::exp2(fmaf(sv[k][2 * j], c, nm)), e1 = sm100::exp2(fmaf(sv[k][2 * j + 1], c, nm));
-      part[0] += e0;
-      part[1] += e1;
-      const __nv_bfloat162 h = __floats2bfloat162_rn(e0, e1);
-      pw[j] = *reinterpret_cast<const uint32_t*>(&h);
+    for (int k = 0; k < 2; ++k) sm100::tmem_ld32(s_addr + 32u * k, sv[k]);
+    sm100::tmem_wait_ld();
+    if (masked) {
+      mask(0);
+      mask(1);
     }
-    sm100::tmem_st16(s_addr + 16u * k, pw);    // columns below those still to be read: all are in registers
+    sum = exps64(sv[0], sv[1], c, m_ref == -INFINITY ? 0.f : -m_ref, pa, pb);
   }
-  l_sum += part[0] + part[1];
-  sm100::tmem_wait_st();
+  const int lane = threadIdx.x & 31;
+  auto hand_over = [&](int half) {
+    sm100::tmem_st16(s_addr + 32u * half, pa);
+    sm100::tmem_st16(s_addr + 32u * half + 16u, pb);
+    sm100::tmem_wait_st();
+    sm100::tc_fence_before();
+    __syncwarp();
+    if (lane == 0) sm100::mbar_arrive(&p_full[half]);
+  };
+  hand_over(0);
+  const float2 more = exps64(sv[2], sv[3], c, m_ref == -INFINITY ? 0.f : -m_ref, pa, pb);
+  hand_over(1);
+  l_sum += (sum.x + sum.y) + (more.x + more.y);
+}
+
+// A split item's partials joined in CTA order, by the softmax threads: each
+// takes CN runs of four columns of a row at a time.
+template <int D, int CN>
+__device__ __forceinline__ void merge_parts(const ChunkParams& p, const Segment& g, int n_rows, int st) {
+  constexpr int PART = 2 * CH_ROWS * (D + 2);
+  const int n_parts = g.n_parts;
+  const float* first = p.part + static_cast<size_t>(2 * g.first_cta + 1) * PART;
+  // the parts after the first are two slots apart, from the first's neighbour on
+  auto slot_of = [&](int k) { return first + (k == 0 ? 0 : static_cast<size_t>(2 * k - 1) * PART); };
+  for (int x = st; x < n_rows * (D / 4 / CN); x += CH_SOFT_THREADS) {
+    const int cg = x / n_rows, r = x - cg * n_rows;
+    const int rt = r & (CH_ROWS - 1), t = rt / p.GB, h = rt - t * p.GB;
+    const int ti = (r >= CH_ROWS ? p.T : 0) + t;
+    if (t >= p.T || ti >= g.tokens || h >= g.heads || 4 * CN * cg >= p.dh) continue;
+    float M = -INFINITY;
+#pragma unroll 4
+    for (int k = 0; k < n_parts; ++k) M = fmaxf(M, __ldcg(slot_of(k) + 2 * CH_ROWS * D + r));
+    float l = 0.f;
+    float4 o[CN];
+#pragma unroll
+    for (int j = 0; j < CN; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll(CN == 1 ? 4 : 2)
+    for (int k = 0; k < n_parts; ++k) {
+      const float* sp = slot_of(k);
+      const float m = __ldcg(sp + 2 * CH_ROWS * D + r), lk = __ldcg(sp + 2 * CH_ROWS * D + 2 * CH_ROWS + r);
+      float4 v[CN];
+#pragma unroll
+      for (int j = 0; j < CN; ++j)
+        v[j] = __ldcg(reinterpret_cast<const float4*>(sp) + (CN * cg + j) * (2 * CH_ROWS) + r);
+      const float f = m == -INFINITY ? 0.f : sm100::exp2(m - M);
+      l = fmaf(f, lk, l);
+#pragma unroll
+      for (int j = 0; j < CN; ++j) {
+        o[j].x = fmaf(f, v[j].x, o[j].x);
+        o[j].y = fmaf(f, v[j].y, o[j].y);
+        o[j].z = fmaf(f, v[j].z, o[j].z);
+        o[j].w = fmaf(f, v[j].w, o[j].w);
+      }
+    }
+    const float z = l > 0.f ? 1.f / l : 0.f;
+    uint16_t* dst = p.out + (static_cast<size_t>(g.row0) + ti) * p.ld_o + (g.head0 + h) * p.dh + 4 * CN * cg;
+#pragma unroll
+    for (int j = 0; j < CN; ++j) {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(o[j].x * z, o[j].y * z);
+      const __nv_bfloat162 b = __floats2bfloat162_rn(o[j].z * z, o[j].w * z);
+      uint2 y;
+      y.x = *reinterpret_cast<const uint32_t*>(&a);
+      y.y = *reinterpret_cast<const uint32_t*>(&b);
+      *reinterpret_cast<uint2*>(dst + 4 * j) = y;
+    }
+  }
 }
 
 // ---- the kernel ------------------------------------------------------------------
@@ -355,22 +453,23 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
   if (tid == 0) {
     for (int i = 0; i < SLOTS; ++i) {
       sm100::mbar_init(&sh.full[i], 1);
-      sm100::mbar_init(&sh.empty[i], 1);
+      sm100::mbar_init(&sh.empty[i], 2);          // the MMA threads
     }
     for (int i = 0; i < CH_SEGS; ++i) {
       sm100::mbar_init(&sh.seg_full[i], 1);
-      sm100::mbar_init(&sh.seg_empty[i], 2 + CH_SOFT_WARPS);   // loader, MMA thread, softmax warps
+      sm100::mbar_init(&sh.seg_empty[i], 3 + CH_SOFT_WARPS);   // loader, MMA threads, softmax warps
     }
     sm100::mbar_init(&sh.q_full, 1);
-    sm100::mbar_init(&sh.q_empty, 1);
+    sm100::mbar_init(&sh.q_empty, 2);
     sm100::mbar_init(&sh.v_raw, 1);
     for (int i = 0; i < 2; ++i) {
       sm100::mbar_init(&sh.s_full[i], 1);
-      sm100::mbar_init(&sh.p_full[i], 4);
+      sm100::mbar_init(&sh.p_full[i][0], 4);
+      sm100::mbar_init(&sh.p_full[i][1], 4);
       sm100::mbar_init(&sh.o_full[i], 1);
     }
     sm100::mbar_init(&sh.join, CH_SOFT_WARPS);
-    sm100::mbar_init(&sh.done, 1);
+    sm100::mbar_init(&sh.done, 2);
     sh.abort = 0;
     sh.never = 0;
     sm100::fence_barrier_init();
@@ -543,14 +642,16 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
       for (int u = max(0, e - SLOTS); u < e; ++u)
         sm100::mbar_wait(&sh.full[u % SLOTS], static_cast<uint32_t>((u / SLOTS) & 1), never);
       if (segs > 0) sm100::mbar_wait(&sh.q_full, static_cast<uint32_t>((segs - 1) & 1), never);
-    } else if (warp == CH_MMA_WARP) {
-      // ---- MMA issuer ----
+    } else {
+      // ---- MMA issuers: warp 1 for group 0, warp 3 for group 1 ----
+      const int w = warp >> 1;
       if (lane == 0) {
         constexpr uint32_t HI = sm100::DESC_SW128_HI;
         const uint32_t id_s = sm100::idesc_bf16_f32(CH_ROWS, CH_KEYS);
         const uint32_t id_o = sm100::idesc_bf16_f32(CH_ROWS, D) | (1u << 16);     // B (V) MN-major
+        const uint32_t s_tm = tmem + CH_TM_S + 128u * w, o_tm = tmem + CH_TM_O + 128u * w;
         int e0 = 0, segs = 0;
-        uint32_t p_phase[2] = {0u, 0u};
+        uint32_t p_phase = 0;
         bool ok = true;
         for (int i = 0; ok; ++i) {
           const int slot = i % CH_SEGS;
@@ -563,52 +664,62 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
           if (nt == 0) continue;
           ok = sm100::mbar_wait(&sh.q_full, static_cast<uint32_t>(segs & 1), abort_flag);
           ++segs;
-          // element x's slot has landed
+          const int step = two ? 1 : 2, t0 = two ? 0 : w;
+          const uint32_t qlo = sm100::desc_lo(sbase + (two ? w * S::TILE : 0u), 16);
+          // this thread is done with ring element x's slot once its MMAs so far are; a tile that one group alone
+          // uses counts for both
+          auto release = [&](int x) {
+            sm100::mma_commit(&sh.empty[x % SLOTS]);
+            if (!two) sm100::mbar_arrive(&sh.empty[x % SLOTS]);
+          };
           auto landed = [&](int x) {
             return sm100::mbar_wait(&sh.full[x % SLOTS], static_cast<uint32_t>((x / SLOTS) & 1), abort_flag);
           };
           // S_w of key tile t
-          auto issue_s = [&](int w, int t) {
+          auto issue_s = [&](int t) {
             const int x = e0 + 2 * t;
-            if (!landed(x)) return false;
-            sm100::tc_fence_after();
-            const uint32_t qlo = sm100::desc_lo(sbase + (two ? w * S::TILE : 0u), 16);
             const uint32_t klo = sm100::desc_lo(rbase + (x % SLOTS) * S::TILE, 16);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               const uint32_t off = ((k >> 2) * CH_HALF + (k & 3) * 32) >> 4;
-              sm100::mma_ss32(tmem + CH_TM_S + 128u * w, qlo + off, klo + off, HI, id_s, k > 0 ? 1u : 0u);
+              sm100::mma_ss32(s_tm, qlo + off, klo + off, HI, id_s, k > 0 ? 1u : 0u);
             }
             sm100::mma_commit(&sh.s_full[w]);
-            if (!two || w == 1) {
-              sm100::mma_commit(&sh.empty[x % SLOTS]);
-              if (t == nt - 1) sm100::mma_commit(&sh.q_empty);
-            }
-            return true;
+            release(x);
+            if (t + step >= nt) sm100::mma_commit(&sh.q_empty);
           };
-          // O_w += P_w V of key tile t
-          auto issue_o = [&](int w, int t, bool first) {
+          // O_w += P_w V of key tile t, as the halves of P_w come
+          auto issue_o = [&](int t) {
             const int x = e0 + 2 * t + 1;
-            if (!sm100::mbar_wait(&sh.p_full[w], p_phase[w] & 1, abort_flag) || !landed(x)) return false;
-            ++p_phase[w];
-            sm100::tc_fence_after();
+            if (!landed(x)) return false;
             const uint32_t vlo = sm100::desc_lo(rbase + (x % SLOTS) * S::TILE, CH_HALF);
+            const uint32_t more = t > t0 ? 1u : 0u;
 #pragma unroll
-            for (int k = 0; k < CH_KEYS / 16; ++k)
-              sm100::mma_ts32(tmem + CH_TM_O + 128u * w, tmem + CH_TM_S + 128u * w + 8u * k, vlo + ((k * 2048) >> 4), HI,
-                              id_o, k > 0 || !first ? 1u : 0u);
-            if (!two || w == 1) sm100::mma_commit(&sh.empty[x % SLOTS]);
-            if (t + (two ? 1 : 2) >= nt) sm100::mma_commit(&sh.o_full[w]);
+            for (int half = 0; half < 2; ++half) {
+              // (the next tile's K meanwhile, so that S follows the products at once)
+              if (half == 1 && t + step < nt && !landed(x - 1 + 2 * step)) return false;
+              if (!sm100::mbar_wait(&sh.p_full[w][half], p_phase & 1, abort_flag)) return false;
+              sm100::tc_fence_after();
+#pragma unroll
+              for (int k = 4 * half; k < 4 * half + 4; ++k)
+                sm100::mma_ts32(o_tm, s_tm + 8u * k, vlo + ((k * 2048) >> 4), HI, id_o, k > 0 ? 1u : more);
+            }
+            ++p_phase;
+            if (t + step >= nt) sm100::mma_commit(&sh.o_full[w]);
             return true;
           };
-          ok = ok && issue_s(0, 0) && (two ? issue_s(1, 0) : nt > 1 ? issue_s(1, 1) : true);
-          for (int j = 0; ok && j < nt; j += two ? 1 : 2)
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              const int t = two ? j : j + w, next = t + (two ? 1 : 2);
-              if (t >= nt || !ok) continue;
-              ok = issue_o(w, t, j == 0) && (next >= nt || issue_s(w, next));
-            }
+          if (ok && t0 >= nt) sm100::mbar_arrive(&sh.q_empty);
+          if (ok && t0 < nt) {
+            ok = landed(e0 + 2 * t0);
+            sm100::tc_fence_after();
+            if (ok) issue_s(t0);
+          }
+          for (int t = t0; ok && t < nt; t += step) {
+            ok = issue_o(t);
+            if (!ok) break;
+            if (t + step < nt) issue_s(t + step);
+            release(e0 + 2 * t + 1);
+          }
           e0 += 2 * nt;
         }
         if (!ok) give_up();
@@ -666,11 +777,11 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
         if (some) {
           const int k0 = (g.kt0 + t) * CH_KEYS;
           const bool masked = k0 + CH_KEYS - 1 > pos_least || k0 < lo_most;
-          softmax_tile<D>(s_addr, o_addr, masked, lo - k0, pos - k0, valid, p.c, m_ref, l_sum);
+          softmax_tile<D>(s_addr, o_addr, masked, lo - k0, pos - k0, valid, p.c, m_ref, l_sum, sh.p_full[w]);
+        } else if (lane == 0) {
+          sm100::mbar_arrive(&sh.p_full[w][0]);
+          sm100::mbar_arrive(&sh.p_full[w][1]);
         }
-        sm100::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) sm100::mbar_arrive(&sh.p_full[w]);
       }
       if (ok && mine > 0) {
         ok = warp_wait(&sh.o_full[w], o_phase & 1);
@@ -766,40 +877,11 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
       }
       ok = join();
       if (!ok) break;
-      const bool merge = sh.prev == g.n_parts - 1;
-      if (!merge) continue;
-      // ---- the last of an item's CTAs: all partials, in CTA order ----
-      const int n_rows = two ? 2 * CH_ROWS : min(CH_ROWS, g.tokens * p.GB);
-      auto slot_of = [&](int k) {
-        return p.part + static_cast<size_t>(k == 0 ? 2 * g.first_cta + 1 : 2 * (g.first_cta + k)) * PART;
-      };
-      for (int x = st; x < n_rows * (D / 4); x += 256) {
-        const int c4 = x / n_rows, r = x - c4 * n_rows;
-        const int rt = r & (CH_ROWS - 1), t = rt / p.GB, h = rt - t * p.GB;
-        const int ti = (r >= CH_ROWS ? p.T : 0) + t;
-        if (t >= p.T || ti >= g.tokens || h >= g.heads || 4 * c4 >= p.dh) continue;
-        float M = -INFINITY;
-        for (int k = 0; k < g.n_parts; ++k) M = fmaxf(M, __ldcg(slot_of(k) + 2 * CH_ROWS * D + r));
-        float l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int k = 0; k < g.n_parts; ++k) {
-          const float* sp = slot_of(k);
-          const float m = __ldcg(sp + 2 * CH_ROWS * D + r);
-          const float f = m == -INFINITY ? 0.f : sm100::exp2(m - M);
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(sp) + c4 * (2 * CH_ROWS) + r);
-          l = fmaf(f, __ldcg(sp + 2 * CH_ROWS * D + 2 * CH_ROWS + r), l);
-          o.x = fmaf(f, v.x, o.x);
-          o.y = fmaf(f, v.y, o.y);
-          o.z = fmaf(f, v.z, o.z);
-          o.w = fmaf(f, v.w, o.w);
-        }
-        const float z = l > 0.f ? 1.f / l : 0.f;
-        const __nv_bfloat162 h0 = __floats2bfloat162_rn(o.x * z, o.y * z), h1 = __floats2bfloat162_rn(o.z * z, o.w * z);
-        uint2 y;
-        y.x = *reinterpret_cast<const uint32_t*>(&h0);
-        y.y = *reinterpret_cast<const uint32_t*>(&h1);
-        *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(g.row0) + ti) * p.ld_o + (g.head0 + h) * p.dh + 4 * c4) = y;
+      if (sh.prev == g.n_parts - 1) {
+        // the last of the item's CTAs
+        const int n_rows = two ? 2 * CH_ROWS : min(CH_ROWS, g.tokens * p.GB);
+        if (n_rows >= CH_ROWS) merge_parts<D, 4>(p, g, n_rows, st);
+        else merge_parts<D, 1>(p, g, n_rows, st);
       }
     }
     if (!ok && lane == 0) give_up();

@@ -44,13 +44,15 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 // WAIT_LIMIT_NS (or as soon as *abort is set by another thread), returning false.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
   if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
+  uint64_t t0 = 0;
   uint32_t spins = 0;
   while (true) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((++spins & 63u) == 0) {
+    if ((++spins & 63u) == 0) {              // (the timer is slow to read: not in a short wait)
       if (*abort) return false;
-      if (globaltimer_ns() - t0 > WAIT_LIMIT_NS) return false;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > WAIT_LIMIT_NS) return false;
     }
   }
 }
