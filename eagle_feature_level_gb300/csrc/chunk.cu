@@ -54,6 +54,7 @@ constexpr int CH_LOAD_WARP = 0, CH_MMA_WARP = 1, CH_SCHED_WARP = 2, CH_SOFT_WARP
 constexpr int CH_SOFT_WARPS = 8;
 constexpr int CH_SOFT_THREADS = 32 * CH_SOFT_WARPS;
 constexpr int CH_KEYS = 128;                 // keys per tile
+constexpr int CH_STEP = 64;                  // keys per softmax step
 constexpr int CH_ROWS = 128;                 // query rows per tile
 constexpr uint32_t CH_HALF = CH_KEYS * 128;  // bytes of 128 rows x 64 elements
 constexpr int CH_SEGS = 4;                   // segments the scheduler runs ahead
@@ -108,7 +109,7 @@ struct Segment {
 template <int SLOTS>
 struct Shared {
   uint64_t full[SLOTS], empty[SLOTS], seg_full[CH_SEGS], seg_empty[CH_SEGS];
-  uint64_t q_full, q_empty, v_raw, s_full[2], p_full[2][2], o_full[2], join, done;
+  uint64_t q_full, q_empty, v_raw, s_full[2][2], p_full[2][2], join, done;
   Segment seg[CH_SEGS];
   float m[2][CH_ROWS], l[2][CH_ROWS];
   uint32_t tmem;
@@ -278,64 +279,60 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// 64 scores' exponentials 2^(s c + nm) as bf16 pairs, and their sum.
-__device__ __forceinline__ float2 exps64(const float (&a)[32], const float (&b)[32], float c, float nm,
-                                         uint32_t (&pa)[16], uint32_t (&pb)[16]) {
-  const float2 c2 = make_float2(c, c), nm2 = make_float2(nm, nm);
-  float2 sum = make_float2(0.f, 0.f);
+// This thread's row of one half of S_w (64 columns): P_w into tensor memory
+// over it, and the row sum.  Column j is visible when lo <= j <= hi (masked
+// steps), or all are.  The exponentials start at once, against the reference
+// of the steps before; only where the step's maximum passes that by CH_RAISE
+// (and in a row's first step) is it raised, O_w and the sum rescaled, and the
+// step done again.  `at_rest` waits until every product into O_w so far is
+// complete.
+template <int D, typename Wait>
+__device__ __forceinline__ bool softmax_step(uint32_t s_addr, uint32_t o_addr, bool masked, int lo, int hi, bool valid,
+                                             float c, float& m_ref, float& l_sum, uint64_t* p_full, Wait at_rest) {
+  float sv[2][32];
+  auto load = [&]() {
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const float(&s)[32] = k ? b : a;
-    uint32_t(&p)[16] = k ? pb : pa;
+    for (int k = 0; k < 2; ++k) sm100::tmem_ld32(s_addr + 32u * k, sv[k]);
+    sm100::tmem_wait_ld();
+    if (__builtin_expect(masked, 0)) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const float2 x = __ffma2_rn(make_float2(s[2 * j], s[2 * j + 1]), c2, nm2);
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) sv[k][j] = (32 * k + j >= lo && 32 * k + j <= hi) ? sv[k][j] : -INFINITY;
+    }
+  };
+  uint32_t pw[32];
+  float2 sum;
+  auto exps = [&]() {
+    const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
+    const float2 c2 = make_float2(c, c), nm2 = make_float2(nm, nm);
+    sum = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const float2 x = __ffma2_rn(make_float2(sv[j >> 4][2 * (j & 15)], sv[j >> 4][2 * (j & 15) + 1]), c2, nm2);
       const float2 e = make_float2(sm100::exp2(x.x), sm100::exp2(x.y));
       sum = __fadd2_rn(sum, e);
       const __nv_bfloat162 h = __floats2bfloat162_rn(e.x, e.y);
-      p[j] = *reinterpret_cast<const uint32_t*>(&h);
+      pw[j] = *reinterpret_cast<const uint32_t*>(&h);
     }
-  }
-  return sum;
-}
-
-// This thread's row of S_w: P_w into tensor memory over S_w, and the row sum.
-// Column j is visible when lo <= j <= hi (masked tiles), or all are.  The
-// exponentials of the first half start at once, against the reference of the
-// tiles before; only where the tile's maximum passes that by CH_RAISE (and in
-// a row's first tile) is it raised, O_w and the sum rescaled, and the half
-// done again.  P_w is handed over in halves of 64 keys, so that its product
-// with V starts under the second half's exponentials.
-template <int D>
-__device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, bool masked, int lo, int hi, bool valid,
-                                             float c, float& m_ref, float& l_sum, uint64_t* p_full) {
-  float sv[4][32];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) sm100::tmem_ld32(s_addr + 32u * k, sv[k]);
-  sm100::tmem_wait_ld();
-  auto mask = [&](int k) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) sv[k][j] = (32 * k + j >= lo && 32 * k + j <= hi) ? sv[k][j] : -INFINITY;
   };
-  if (masked) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) mask(k);
-  }
+  load();
   float mx[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    mx[k] = fmaxf(sv[k][0], sv[k][1]);
+    mx[k] = fmaxf(sv[k >> 1][16 * (k & 1)], sv[k >> 1][16 * (k & 1) + 1]);
 #pragma unroll
-    for (int j = 2; j < 32; j += 2) mx[k] = max3(mx[k], sv[k][j], sv[k][j + 1]);
+    for (int j = 2; j < 16; j += 2) mx[k] = max3(mx[k], sv[k >> 1][16 * (k & 1) + j], sv[k >> 1][16 * (k & 1) + j + 1]);
   }
   const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
-  uint32_t pa[16], pb[16];
-  float2 sum = exps64(sv[0], sv[1], c, m_ref == -INFINITY ? 0.f : -m_ref, pa, pb);
   const bool raise = valid && (mt > m_ref + CH_RAISE || (m_ref == -INFINITY && mt != -INFINITY));
-  if (__any_sync(0xffffffffu, raise)) {
+  const bool any = __any_sync(0xffffffffu, raise);
+  exps();
+  if (__builtin_expect(any, 0)) {
     const bool rescale = raise && m_ref != -INFINITY;
     if (__any_sync(0xffffffffu, rescale)) {
-      // S_w of this tile was complete after every earlier P_w V: O_w is at rest
+      if (!at_rest()) return false;
+      sm100::tc_fence_after();
       const float f = rescale ? sm100::exp2(m_ref - mt) : 1.f;
 #pragma unroll 1
       for (int q = 0; q < D / 16; ++q) {
@@ -350,29 +347,22 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, b
       l_sum *= f;
     }
     if (raise) m_ref = mt;
-    // the first half's scores once more (their registers went to P)
-#pragma unroll
-    for (int k = 0; k < 2; ++k) sm100::tmem_ld32(s_addr + 32u * k, sv[k]);
-    sm100::tmem_wait_ld();
-    if (masked) {
-      mask(0);
-      mask(1);
-    }
-    sum = exps64(sv[0], sv[1], c, m_ref == -INFINITY ? 0.f : -m_ref, pa, pb);
+    load();                                  // the scores once more (their registers went to P)
+    exps();
   }
-  const int lane = threadIdx.x & 31;
-  auto hand_over = [&](int half) {
-    sm100::tmem_st16(s_addr + 32u * half, pa);
-    sm100::tmem_st16(s_addr + 32u * half + 16u, pb);
-    sm100::tmem_wait_st();
-    sm100::tc_fence_before();
-    __syncwarp();
-    if (lane == 0) sm100::mbar_arrive(&p_full[half]);
-  };
-  hand_over(0);
-  const float2 more = exps64(sv[2], sv[3], c, m_ref == -INFINITY ? 0.f : -m_ref, pa, pb);
-  hand_over(1);
-  l_sum += (sum.x + sum.y) + (more.x + more.y);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    uint32_t x[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) x[j] = pw[16 * k + j];
+    sm100::tmem_st16(s_addr + 16u * k, x);
+  }
+  sm100::tmem_wait_st();
+  sm100::tc_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) sm100::mbar_arrive(p_full);
+  l_sum += sum.x + sum.y;
+  return true;
 }
 
 // A split item's partials joined in CTA order, by the softmax threads: each
@@ -462,11 +452,9 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
     sm100::mbar_init(&sh.q_full, 1);
     sm100::mbar_init(&sh.q_empty, 2);
     sm100::mbar_init(&sh.v_raw, 1);
-    for (int i = 0; i < 2; ++i) {
-      sm100::mbar_init(&sh.s_full[i], 1);
-      sm100::mbar_init(&sh.p_full[i][0], 4);
-      sm100::mbar_init(&sh.p_full[i][1], 4);
-      sm100::mbar_init(&sh.o_full[i], 1);
+    for (int i = 0; i < 4; ++i) {
+      sm100::mbar_init(&sh.s_full[i >> 1][i & 1], 1);
+      sm100::mbar_init(&sh.p_full[i >> 1][i & 1], 4);
     }
     sm100::mbar_init(&sh.join, CH_SOFT_WARPS);
     sm100::mbar_init(&sh.done, 2);
@@ -647,7 +635,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
       const int w = warp >> 1;
       if (lane == 0) {
         constexpr uint32_t HI = sm100::DESC_SW128_HI;
-        const uint32_t id_s = sm100::idesc_bf16_f32(CH_ROWS, CH_KEYS);
+        const uint32_t id_s = sm100::idesc_bf16_f32(CH_ROWS, CH_STEP);
         const uint32_t id_o = sm100::idesc_bf16_f32(CH_ROWS, D) | (1u << 16);     // B (V) MN-major
         const uint32_t s_tm = tmem + CH_TM_S + 128u * w, o_tm = tmem + CH_TM_O + 128u * w;
         int e0 = 0, segs = 0;
@@ -675,50 +663,56 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
           auto landed = [&](int x) {
             return sm100::mbar_wait(&sh.full[x % SLOTS], static_cast<uint32_t>((x / SLOTS) & 1), abort_flag);
           };
-          // S_w of key tile t
-          auto issue_s = [&](int t) {
-            const int x = e0 + 2 * t;
-            const uint32_t klo = sm100::desc_lo(rbase + (x % SLOTS) * S::TILE, 16);
+          // S_w of half h of the key tile in ring element x
+          auto issue_s = [&](int x, int h) {
+            sm100::tc_fence_after();
+            const uint32_t klo = sm100::desc_lo(rbase + (x % SLOTS) * S::TILE + h * CH_STEP * 128, 16);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               const uint32_t off = ((k >> 2) * CH_HALF + (k & 3) * 32) >> 4;
-              sm100::mma_ss32(s_tm, qlo + off, klo + off, HI, id_s, k > 0 ? 1u : 0u);
+              sm100::mma_ss32(s_tm + 64u * h, qlo + off, klo + off, HI, id_s, k > 0 ? 1u : 0u);
             }
-            sm100::mma_commit(&sh.s_full[w]);
-            release(x);
-            if (t + step >= nt) sm100::mma_commit(&sh.q_empty);
           };
-          // O_w += P_w V of key tile t, as the halves of P_w come
-          auto issue_o = [&](int t) {
-            const int x = e0 + 2 * t + 1;
-            if (!landed(x)) return false;
-            const uint32_t vlo = sm100::desc_lo(rbase + (x % SLOTS) * S::TILE, CH_HALF);
-            const uint32_t more = t > t0 ? 1u : 0u;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              // (the next tile's K meanwhile, so that S follows the products at once)
-              if (half == 1 && t + step < nt && !landed(x - 1 + 2 * step)) return false;
-              if (!sm100::mbar_wait(&sh.p_full[w][half], p_phase & 1, abort_flag)) return false;
-              sm100::tc_fence_after();
-#pragma unroll
-              for (int k = 4 * half; k < 4 * half + 4; ++k)
-                sm100::mma_ts32(o_tm, s_tm + 8u * k, vlo + ((k * 2048) >> 4), HI, id_o, k > 0 ? 1u : more);
-            }
-            ++p_phase;
-            if (t + step >= nt) sm100::mma_commit(&sh.o_full[w]);
-            return true;
-          };
-          if (ok && t0 >= nt) sm100::mbar_arrive(&sh.q_empty);
-          if (ok && t0 < nt) {
-            ok = landed(e0 + 2 * t0);
+          // O_w += P_w V of the same half of the tile's V
+          auto issue_o = [&](int x, int h, uint32_t more) {
             sm100::tc_fence_after();
-            if (ok) issue_s(t0);
+            const uint32_t vlo = sm100::desc_lo(rbase + (x % SLOTS) * S::TILE + h * CH_STEP * 128, CH_HALF);
+#pragma unroll
+            for (int k = 0; k < CH_STEP / 16; ++k)
+              sm100::mma_ts32(o_tm, s_tm + 64u * h + 8u * k, vlo + ((k * 2048) >> 4), HI, id_o, k > 0 ? 1u : more);
+          };
+          if (t0 >= nt) {
+            if (ok) sm100::mbar_arrive(&sh.q_empty);
+          } else if (ok && (ok = landed(e0 + 2 * t0))) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              issue_s(e0 + 2 * t0, h);
+              sm100::mma_commit(&sh.s_full[w][h]);
+            }
+            release(e0 + 2 * t0);
           }
           for (int t = t0; ok && t < nt; t += step) {
-            ok = issue_o(t);
+            const int kx = e0 + 2 * (t + step), vx = e0 + 2 * t + 1;    // the next tile's K, this one's V
+            const bool next = t + step < nt;
+            if (!next) sm100::mma_commit(&sh.q_empty);
+            ok = landed(vx);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              ok = ok && sm100::mbar_wait(&sh.p_full[w][h], p_phase & 1, abort_flag);
+              if (!ok) break;
+              issue_o(vx, h, h == 1 || t > t0 ? 1u : 0u);
+              if (h == 0 && next && !landed(kx)) {
+                ok = false;
+                break;
+              }
+              if (next) issue_s(kx, h);
+              // with no next tile: the sign that O_w has taken this half
+              sm100::mma_commit(&sh.s_full[w][h]);
+            }
             if (!ok) break;
-            if (t + step < nt) issue_s(t + step);
-            release(e0 + 2 * t + 1);
+            ++p_phase;
+            release(vx);
+            if (next) release(kx);
           }
           e0 += 2 * nt;
         }
@@ -738,7 +732,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
     const uint32_t s_addr = tmem + CH_TM_S + 128u * w + lane_base, o_addr = tmem + CH_TM_O + 128u * w + lane_base;
     const int st = tid - 32 * CH_SOFT_WARP0;               // 0 .. 255
     const int tok = row / p.GB, head = row - tok * p.GB;   // of this row in its tile
-    uint32_t s_phase = 0, o_phase = 0, j_phase = 0;
+    uint32_t s_phase = 0, j_phase = 0;
     bool ok = true;
     // all softmax warps: shared memory and tensor memory of the others' last step may be used after it
     auto join = [&]() {
@@ -766,26 +760,30 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
       const int lo_most = __reduce_max_sync(0xffffffffu, valid ? lo : INT_MIN);
       const bool some = __any_sync(0xffffffffu, valid);
       float m_ref = -INFINITY, l_sum = 0.f;
-      const int step = two ? 1 : 2;
-      int mine = 0;
-      for (int t = two ? 0 : w; t < g.nt; t += step) {
-        ok = warp_wait(&sh.s_full[w], s_phase & 1);
-        if (!ok) break;
-        ++s_phase;
-        ++mine;
-        sm100::tc_fence_after();
-        if (some) {
-          const int k0 = (g.kt0 + t) * CH_KEYS;
-          const bool masked = k0 + CH_KEYS - 1 > pos_least || k0 < lo_most;
-          softmax_tile<D>(s_addr, o_addr, masked, lo - k0, pos - k0, valid, p.c, m_ref, l_sum, sh.p_full[w]);
-        } else if (lane == 0) {
-          sm100::mbar_arrive(&sh.p_full[w][0]);
-          sm100::mbar_arrive(&sh.p_full[w][1]);
+      const int step = two ? 1 : 2, t0 = two ? 0 : w;
+      for (int t = t0; ok && t < g.nt; t += step) {
+        for (int h = 0; ok && h < 2; ++h) {
+          ok = warp_wait(&sh.s_full[w][h], s_phase & 1);
+          if (!ok) break;
+          sm100::tc_fence_after();
+          if (some) {
+            const int k0 = (g.kt0 + t) * CH_KEYS + CH_STEP * h;
+            const bool masked = k0 + CH_STEP - 1 > pos_least || k0 < lo_most;
+            // The products before this step are complete when the other half's next scores are, issued after them (in
+            // the last step: the sign in their place); before the first step there are none.
+            auto at_rest = [&]() { return warp_wait(&sh.s_full[w][h ^ 1], (h ? s_phase + 1 : s_phase) & 1); };
+            ok = softmax_step<D>(s_addr + 64u * h, o_addr, masked, lo - k0, pos - k0, valid, p.c, m_ref, l_sum,
+                                 &sh.p_full[w][h], at_rest);
+          } else if (lane == 0) {
+            sm100::mbar_arrive(&sh.p_full[w][h]);
+          }
         }
+        ++s_phase;
       }
-      if (ok && mine > 0) {
-        ok = warp_wait(&sh.o_full[w], o_phase & 1);
-        ++o_phase;
+      if (ok && t0 < g.nt) {
+        // O_w has taken both halves of the last tile
+        ok = warp_wait(&sh.s_full[w][0], s_phase & 1) && warp_wait(&sh.s_full[w][1], s_phase & 1);
+        ++s_phase;
       }
       if (!ok) break;
       sm100::tc_fence_after();
