@@ -119,7 +119,7 @@ void layout(eagle_ctx* c) {
   // the chunk attention's partials take their place in its calls
   W.attn_part = take(std::max(records * (D.head_dim + 4) * 4, chunk_part_bytes(c->sm_count, D.head_dim)));
   W.attn_cnt = take(static_cast<size_t>(2) * L.max_batch * D.n_kv_heads * 4);
-  W.chunk_cnt = take(static_cast<size_t>(c->sm_count) * 4);
+  W.chunk_cnt = take(static_cast<size_t>(chunk_counters(c->sm_count)) * 4);
   W.pages = take(static_cast<size_t>(PAGES_LISTS) * L.max_batch * 4 + 256);
   W.total = off;
 }

@@ -59,6 +59,11 @@ constexpr int CH_ROWS = 128;                 // query rows per tile
 constexpr uint32_t CH_HALF = CH_KEYS * 128;  // bytes of 128 rows x 64 elements
 constexpr int CH_SEGS = 4;                   // segments the scheduler runs ahead
 constexpr float CH_RAISE = 8.0f;
+// the token phase: requests of at most TK_ROWS query rows a kv head
+constexpr int TK_ROWS = 16;
+template <int SLOTS>
+constexpr int TK_STAGES = SLOTS == 5 ? 3 : 5;  // ring stages of a warp (for heads of 128, of 64 elements)
+
 constexpr uint32_t CH_TM_S = 0, CH_TM_O = 256, CH_TM_COLS = 512;   // S_w / P_w at 128 w, O_w at 256 + 128 w
 constexpr int CH_REGS_FEW = 56, CH_REGS_SOFT = 224;
 static_assert(128 * CH_REGS_FEW + 256 * CH_REGS_SOFT <= CH_THREADS * 168, "the split fits the launch's registers");
@@ -76,15 +81,21 @@ struct ChunkParams {
   PackedRows rows;
   int hkv, G, GB, T, nsub;                   // heads: kv, per kv head, per tile; tokens per tile; tiles' heads per kv head
   int dh;
-  long long ld_o;
+  long long ld_q, ld_o;
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
   uint16_t* out;
   int cap, window;
   const int32_t* len;
   PagedKv paged;
   int box;                                   // rows of a K / V box
   float c;                                   // scale * log2 e
-  float* part;                               // [2 grid][CH_PART] partials
+  float* part;                               // [2 grid] partials of split items
   int* cnt;                                  // [grid] arrivals at a split item, by its first CTA
+  int tk_wph, tk_parts;                      // the token phase: warps per kv head, groups of heads
+  float* tk_part;                            // its partials and arrivals
+  int* tk_cnt;
   int* status;
   uint64_t* stamp;
 };
@@ -112,6 +123,9 @@ struct Shared {
   uint64_t q_full, q_empty, v_raw, s_full[2][2], p_full[2][2], join, done;
   Segment seg[CH_SEGS];
   float m[2][CH_ROWS], l[2][CH_ROWS];
+  uint64_t tk_full[CH_SOFT_WARPS * TK_STAGES<SLOTS>];
+  int tk_prev;
+  uint64_t tk_done;
   uint32_t tmem;
   int abort, never, prev;
 };
@@ -128,50 +142,68 @@ struct Request {
   bool bad, over;
 };
 
+// Requests of few rows (a decoding step's) are taken by the token phase, the
+// others by the tensor-memory phase; each walks the requests of its own class.
+enum : int { TENSOR = 0, TOKEN = 1 };
+
+template <int CLASS>
+__device__ __forceinline__ int parts_of(const ChunkParams& p) { return CLASS == TOKEN ? p.tk_parts : p.hkv * p.nsub; }
+
+template <int CLASS>
 __device__ __forceinline__ Request request_of(const ChunkParams& p, int b) {
   Request r;
   int lo, hi;
   r.bad = !request_rows(p.rows, b, lo, hi);
   const int L = p.len[b];
-  r.over = L > p.cap;
+  r.over = L > p.cap && hi > lo;
   r.len = max(0, min(L, p.cap));
   r.row0 = lo;
   r.n = hi - lo;
-  r.per = r.n <= p.T ? p.T : 2 * p.T;
+  const bool token = static_cast<long long>(r.n) * p.G <= TK_ROWS;
+  if (token != (CLASS == TOKEN)) r.n = 0;
+  r.per = CLASS == TOKEN ? max(r.n, 1) : r.n <= p.T ? p.T : 2 * p.T;
   r.items = (r.n + r.per - 1) / r.per;
   return r;
 }
+__device__ __forceinline__ void take_from(Request& to, const Request& from, int l) {
+  to.row0 = __shfl_sync(0xffffffffu, from.row0, l);
+  to.n = __shfl_sync(0xffffffffu, from.n, l);
+  to.len = __shfl_sync(0xffffffffu, from.len, l);
+  to.per = __shfl_sync(0xffffffffu, from.per, l);
+  to.items = __shfl_sync(0xffffffffu, from.items, l);
+}
 
 // Key tiles [kt0, kt1) of item q (kt1 <= kt0: none of its rows sees a key).
+template <int CLASS>
 __device__ __forceinline__ void item_tiles(const ChunkParams& p, const Request& r, int q, int& kt0, int& kt1) {
+  const int KEYS = CLASS == TOKEN ? 16 * p.tk_wph : CH_KEYS;
   const long long first = static_cast<long long>(r.len) - r.n + static_cast<long long>(q) * r.per;
   const long long end = min(static_cast<long long>(r.len), first + r.per);
   const long long lo = p.window > 0 ? max(0ll, first - p.window + 1) : 0ll;
-  kt0 = static_cast<int>(lo / CH_KEYS);
-  kt1 = end > lo ? static_cast<int>((end + CH_KEYS - 1) / CH_KEYS) : kt0;
+  kt0 = static_cast<int>(lo / KEYS);
+  kt1 = end > lo ? static_cast<int>((end + KEYS - 1) / KEYS) : kt0;
 }
+template <int CLASS>
 __device__ __forceinline__ int item_units(const ChunkParams& p, const Request& r, int q) {
   int a, z;
-  item_tiles(p, r, q, a, z);
+  item_tiles<CLASS>(p, r, q, a, z);
   return max(1, z - a);
 }
 
 // Units of one kv head part of the lane's own request (every lane calls it;
 // requests of many items are summed by the whole warp).
+template <int CLASS>
 __device__ __forceinline__ long long request_units(const ChunkParams& p, const Request& r, int lane) {
   constexpr int ALONE = 4;
   long long w = 0;
   if (r.items <= ALONE)
-    for (int q = 0; q < r.items; ++q) w += item_units(p, r, q);
+    for (int q = 0; q < r.items; ++q) w += item_units<CLASS>(p, r, q);
   for (unsigned todo = __ballot_sync(0xffffffffu, r.items > ALONE); todo; todo &= todo - 1) {
     const int l = __ffs(todo) - 1;
     Request s;
-    s.n = __shfl_sync(0xffffffffu, r.n, l);
-    s.len = __shfl_sync(0xffffffffu, r.len, l);
-    s.per = __shfl_sync(0xffffffffu, r.per, l);
-    s.items = __shfl_sync(0xffffffffu, r.items, l);
+    take_from(s, r, l);
     long long part = 0;
-    for (int q = lane; q < s.items; q += 32) part += item_units(p, s, q);
+    for (int q = lane; q < s.items; q += 32) part += item_units<CLASS>(p, s, q);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
     if (lane == l) w = part;
@@ -187,6 +219,31 @@ __device__ __forceinline__ long long warp_scan(long long v, int lane) {   // inc
   return v;
 }
 
+// Units of the batch's requests, by one warp, 32 requests at a time.
+struct Scan {
+  Request r;               // the lane's request of the 32 at hand,
+  long long units, end;    // its units per kv head part, and the sum up to its end
+};
+template <int CLASS>
+__device__ __forceinline__ void scan_32(const ChunkParams& p, int lane, int b0, long long before, Scan& s) {
+  s.r = Request{};
+  s.r.per = 1;
+  if (b0 + lane < p.rows.B) s.r = request_of<CLASS>(p, b0 + lane);
+  s.units = request_units<CLASS>(p, s.r, lane);
+  s.end = before + warp_scan(s.units * parts_of<CLASS>(p), lane);
+}
+template <int CLASS>
+__device__ __forceinline__ long long scan_batch(const ChunkParams& p, int lane, bool report, Scan& s) {
+  long long sum = 0;
+  for (int b0 = 0; b0 < p.rows.B; b0 += 32) {
+    scan_32<CLASS>(p, lane, b0, sum, s);
+    if (report && s.r.bad) set_status(p.status, EAGLE_ERR_INVALID_ARG);
+    if (report && s.r.over) set_status(p.status, EAGLE_ERR_CAPACITY);
+    sum = __shfl_sync(0xffffffffu, s.end, 31);
+  }
+  return sum;
+}
+
 // The walk's place: item q of kv head part hs of request b, whose first unit
 // is `unit` of all.
 struct Walk {
@@ -195,81 +252,114 @@ struct Walk {
   long long unit;
 };
 
-// Requests' units over the batch; optionally (u0 >= 0) the item that holds
-// unit u0.  Returns the sum.
-__device__ long long scan_batch(const ChunkParams& p, int lane, long long u0, bool report, Walk& w) {
-  const int parts = p.hkv * p.nsub;
+// The item that holds unit u0; s is what scan_batch left.
+template <int CLASS>
+__device__ __forceinline__ void walk_to(const ChunkParams& p, int lane, long long u0, Scan& s, Walk& w) {
+  const int parts = parts_of<CLASS>(p);
   long long sum = 0;
   for (int b0 = 0; b0 < p.rows.B; b0 += 32) {
-    const int b = b0 + lane;
-    Request r{};
-    r.per = 1;
-    if (b < p.rows.B) r = request_of(p, b);
-    if (report && r.bad) set_status(p.status, EAGLE_ERR_INVALID_ARG);
-    if (report && r.over && r.n > 0) set_status(p.status, EAGLE_ERR_CAPACITY);
-    const long long units = request_units(p, r, lane);
-    const long long end = sum + warp_scan(units * parts, lane);
-    if (u0 >= 0) {
-      const unsigned past = __ballot_sync(0xffffffffu, end > u0);
-      if (past) {
-        const int l = __ffs(past) - 1;
-        w.b = b0 + l;
-        w.r.row0 = __shfl_sync(0xffffffffu, r.row0, l);
-        w.r.n = __shfl_sync(0xffffffffu, r.n, l);
-        w.r.len = __shfl_sync(0xffffffffu, r.len, l);
-        w.r.per = __shfl_sync(0xffffffffu, r.per, l);
-        w.r.items = __shfl_sync(0xffffffffu, r.items, l);
-        const long long W = __shfl_sync(0xffffffffu, units, l);
-        const long long begin = __shfl_sync(0xffffffffu, end - units * parts, l);
-        w.hs = static_cast<int>((u0 - begin) / W);
-        long long at = begin + W * w.hs;             // first unit of the part
-        for (int q0 = 0;; q0 += 32) {
-          const int q = q0 + lane;
-          const long long v = q < w.r.items ? item_units(p, w.r, q) : 0;
-          const long long upto = at + warp_scan(v, lane);
-          const unsigned hit = __ballot_sync(0xffffffffu, upto > u0 && q < w.r.items);
-          if (hit) {
-            const int k = __ffs(hit) - 1;
-            w.q = q0 + k;
-            w.unit = __shfl_sync(0xffffffffu, upto - v, k);
-            return sum;
-          }
-          at = __shfl_sync(0xffffffffu, upto, 31);
-          if (q0 + 32 >= w.r.items) break;            // (not reached: the part's units end past u0)
+    if (p.rows.B > 32) scan_32<CLASS>(p, lane, b0, sum, s);
+    const unsigned past = __ballot_sync(0xffffffffu, s.end > u0);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      w.b = b0 + l;
+      take_from(w.r, s.r, l);
+      const long long W = __shfl_sync(0xffffffffu, s.units, l);
+      const long long begin = __shfl_sync(0xffffffffu, s.end - s.units * parts, l);
+      w.hs = static_cast<int>((u0 - begin) / W);
+      long long at = begin + W * w.hs;         // first unit of the part
+      for (int q0 = 0; q0 < w.r.items; q0 += 32) {
+        const int q = q0 + lane;
+        const long long v = q < w.r.items ? item_units<CLASS>(p, w.r, q) : 0;
+        const long long upto = at + warp_scan(v, lane);
+        const unsigned hit = __ballot_sync(0xffffffffu, upto > u0 && q < w.r.items);
+        if (hit) {
+          const int k = __ffs(hit) - 1;
+          w.q = q0 + k;
+          w.unit = __shfl_sync(0xffffffffu, upto - v, k);
+          return;
         }
-        w.q = w.r.items - 1;
-        w.unit = at;
-        return sum;
+        at = __shfl_sync(0xffffffffu, upto, 31);
       }
+      return;
     }
-    sum = __shfl_sync(0xffffffffu, end, 31);
+    sum = __shfl_sync(0xffffffffu, s.end, 31);
   }
-  return sum;
 }
 
 // To the next item; false at the batch's end.
+template <int CLASS>
 __device__ __forceinline__ bool walk_on(const ChunkParams& p, Walk& w, int lane) {
   if (++w.q < w.r.items) return true;
   w.q = 0;
-  if (++w.hs < p.hkv * p.nsub) return true;
+  if (++w.hs < parts_of<CLASS>(p)) return true;
   w.hs = 0;
   for (int b0 = w.b + 1; b0 < p.rows.B; b0 += 32) {
     Request r{};
-    if (b0 + lane < p.rows.B) r = request_of(p, b0 + lane);
+    if (b0 + lane < p.rows.B) r = request_of<CLASS>(p, b0 + lane);
     const unsigned some = __ballot_sync(0xffffffffu, r.n > 0);
     if (some) {
       const int l = __ffs(some) - 1;
       w.b = b0 + l;
-      w.r.row0 = __shfl_sync(0xffffffffu, r.row0, l);
-      w.r.n = __shfl_sync(0xffffffffu, r.n, l);
-      w.r.len = __shfl_sync(0xffffffffu, r.len, l);
-      w.r.per = __shfl_sync(0xffffffffu, r.per, l);
-      w.r.items = __shfl_sync(0xffffffffu, r.items, l);
+      take_from(w.r, r, l);
       return true;
     }
   }
   return false;
 }
+
+// One worker's share [at, end) of n workers' units, segment by segment.
+template <int CLASS>
+struct Share {
+  Walk w;
+  long long U, n, c, at, end;
+  __device__ __forceinline__ void begin(const ChunkParams& p, int lane, int worker, int workers, bool report) {
+    Scan s;
+    U = scan_batch<CLASS>(p, lane, report, s);
+    n = min(static_cast<long long>(workers), U);                 // workers with work
+    c = worker;
+    at = c < n ? U * c / n : 0;
+    end = c < n ? U * (c + 1) / n : 0;
+    if (at < end) walk_to<CLASS>(p, lane, at, s, w);
+  }
+  __device__ __forceinline__ Segment next(const ChunkParams& p, int lane) {
+    Segment g{};
+    g.last = at >= end;
+    if (g.last) return g;
+    int kt0, kt1;
+    item_tiles<CLASS>(p, w.r, w.q, kt0, kt1);
+    const int units = max(1, kt1 - kt0);
+    const int x0 = static_cast<int>(at - w.unit);
+    const int x1 = static_cast<int>(min(static_cast<long long>(units), end - w.unit));
+    const int nsub = CLASS == TOKEN ? 1 : p.nsub;     // (a token item's hk: its group of heads)
+    const int hk = w.hs / nsub, sub = w.hs - hk * nsub;
+    const int t0 = w.q * w.r.per;
+    g.row0 = w.r.row0 + t0;
+    g.tokens = min(w.r.per, w.r.n - t0);
+    g.pos0 = w.r.len - w.r.n + t0;
+    g.len = w.r.len;
+    g.b = w.b;
+    g.hk = hk;
+    g.head0 = hk * p.G + sub * p.GB;
+    g.heads = min(p.GB, p.G - sub * p.GB);
+    g.kt0 = kt0 + x0;
+    g.nt = kt1 > kt0 ? x1 - x0 : 0;
+    g.two = g.tokens > p.T;
+    g.whole = x0 == 0 && x1 == units;
+    if (!g.whole) {
+      // the worker that holds unit u: the largest whose range begins at or before it
+      g.first_cta = static_cast<int>(((w.unit + 1) * n - 1) / U);
+      g.n_parts = static_cast<int>(((w.unit + units) * n - 1) / U) - g.first_cta + 1;
+      g.part = 2 * static_cast<int>(c) + (x0 == 0 ? 1 : 0);
+    }
+    at = w.unit + x1;
+    if (x1 == units) {
+      w.unit += units;
+      if (at < end && !walk_on<CLASS>(p, w, lane)) at = end;
+    }
+    return g;
+  }
+};
 
 // ---- softmax of one tile -------------------------------------------------------
 
@@ -418,12 +508,438 @@ __device__ __forceinline__ void merge_parts(const ChunkParams& p, const Segment&
   }
 }
 
+// ---- the token phase --------------------------------------------------------------
+//
+// Requests of at most 16 query rows a kv head (one decoding token and its
+// group) read every key for a handful of rows: the cache's bytes are all that
+// counts.  A cache row holds its kv heads side by side, 256 bytes each, and
+// DRAM serves whole rows better than pieces: with a kv head per worker, 16
+// requests of 8192 keys x 8 heads streamed at 4.1 TB/s.  So the eight softmax
+// warps take eight kv heads over the same keys (with fewer heads, 2, 4 or 8
+// warps share one), 16 keys a step, each warp through a ring of its own, with no
+// barrier between warps and an online softmax of its own.  One lane requests a
+// step by TMA (per-lane 16-byte copies spent 2300 of a step's 3100 cycles on
+// addresses and the block table).  The products are warp-level bf16 tiles with the keys as
+// rows, S^T = K Q^T and O^T += V^T P^T (m16n8k16): eight query rows fill the
+// narrow side, where Q as the 16-row side would be half padding.
+
+template <int D>
+struct TokenShape {
+  static constexpr int STAGES = D == 128 ? 3 : 5;
+  static constexpr int HALVES = D / 64;
+  static constexpr uint32_t HALF = 16 * 128;               // 16 keys x 64 elements
+  static constexpr uint32_t STAGE = 2 * HALVES * HALF;     // K then V
+  static constexpr uint32_t JOIN = CH_SOFT_WARPS * STAGES * STAGE;   // after the rings: [8 warps][8 rows][D] fp32
+  static constexpr int PART = TK_ROWS * (D + 2);           // floats of a head's partial
+  static_assert(JOIN + CH_SOFT_WARPS * 8 * D * 4 <= Shape<D>::TILES, "the tiles' memory");
+};
+
+// A warp's place: kv head `hk`, and the key steps sub, sub + wph, .. of a unit.
+struct TokenWarp {
+  int wph, hslot, sub, lane;
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// The blocks of a warp's next 32 steps, one in each lane (blocks of at least
+// 16 rows: a step lies in one).
+struct TokenBlocks {
+  int base, blk;
+  __device__ __forceinline__ int of(const ChunkParams& p, const Segment& g, const TokenWarp& tw, int u) {
+    if (u < base || u >= base + 32) {
+      base = u;
+      const int key0 = ((g.kt0 + u + tw.lane) * tw.wph + tw.sub) * 16;
+      blk = p.paged.n_blocks;                // out of range: reads as zeros
+      if (u + tw.lane < g.nt && key0 < g.len) {
+        const int x = p.paged.table[static_cast<size_t>(g.b) * p.paged.per_req + (key0 >> p.paged.shift)];
+        if (x >= 0 && x < p.paged.n_blocks) blk = x;
+        else set_status(p.status, EAGLE_ERR_INVALID_ARG);
+      }
+    }
+    return __shfl_sync(0xffffffffu, blk, u - base);
+  }
+};
+
+// Step u of segment g -- 16 keys of kv head hk, K then V -- into `stage`.  Rows
+// past the length within their block arrive as they are, those of blocks that
+// do not exist as zeros.
+template <int D>
+__device__ __forceinline__ void token_load(const ChunkParams& p, const CUtensorMap* kmap, const CUtensorMap* vmap,
+                                           const Segment& g, int hk, uint8_t* stage, uint64_t* bar, TokenBlocks& blocks,
+                                           const TokenWarp& tw, int u) {
+  using T = TokenShape<D>;
+  const int key0 = ((g.kt0 + u) * tw.wph + tw.sub) * 16;
+  const bool paged = p.paged.table != nullptr;
+  const int mask = (1 << p.paged.shift) - 1;
+  auto box = [&](int y, int z, int row) {
+#pragma unroll
+    for (int h = 0; h < T::HALVES; ++h) {
+      sm100::tma_load_4d(stage + h * T::HALF + row * 128, kmap, 64 * h, hk, y, z, bar);
+      sm100::tma_load_4d(stage + (T::HALVES + h) * T::HALF + row * 128, vmap, 64 * h, hk, y, z, bar);
+    }
+  };
+  if (tw.lane == 0) sm100::mbar_arrive_expect_tx(bar, T::STAGE);
+  if (!paged || p.paged.shift >= 4) {
+    const int z = paged ? blocks.of(p, g, tw, u) : g.b;
+    if (tw.lane == 0) box(paged ? key0 & mask : key0, z, 0);
+  } else {
+    __syncwarp();
+    const int rows = 1 << p.paged.shift;
+    if (tw.lane * rows < 16) {
+      const int key = key0 + tw.lane * rows;
+      int z = p.paged.n_blocks;
+      if (key < g.len) {
+        const int x = p.paged.table[static_cast<size_t>(g.b) * p.paged.per_req + (key >> p.paged.shift)];
+        if (x >= 0 && x < p.paged.n_blocks) z = x;
+        else set_status(p.status, EAGLE_ERR_INVALID_ARG);
+      }
+      box(0, z, tw.lane * rows);
+    }
+  }
+  __syncwarp();
+}
+
+// One segment's softmaxes and products by a warp (its nt units are on their
+// way or, the first STAGES of them, already requested).  NT: tiles of 8 query
+// rows.
+template <int D, int NT>
+__device__ __forceinline__ void token_segment(const ChunkParams& p, const CUtensorMap* kmap, const CUtensorMap* vmap,
+                                              const Segment& g, int hk, uint8_t* ring, uint64_t* bars, uint32_t& phases,
+                                              int& slot, volatile int* abort, bool& ok, TokenBlocks& blocks,
+                                              const TokenWarp& tw, float (&o)[NT][D / 16][4], float (&m)[NT][2],
+                                              float (&l)[NT][2]) {
+  using T = TokenShape<D>;
+  const int lane = tw.lane, gq = lane >> 2, tq = lane & 3;
+  const int rows = g.tokens * p.G;
+  // Q^T as the B operand: column = query row, k = elements
+  uint32_t qf[NT][D / 16][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int r = 8 * n + gq, t = r / p.G, h = r - t * p.G;
+    const uint16_t* q = p.q + (static_cast<size_t>(g.row0) + t) * p.ld_q + (hk * p.G + h) * p.dh + 2 * tq;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      const bool there = r < rows && 16 * k < p.dh && hk < p.hkv;
+      qf[n][k][0] = there ? *reinterpret_cast<const uint32_t*>(q + 16 * k) : 0u;
+      qf[n][k][1] = there ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 8) : 0u;
+    }
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[n][j][i] = 0.f;
+    m[n][0] = m[n][1] = -INFINITY;
+    l[n][0] = l[n][1] = 0.f;
+  }
+  // what the thread's rows (8 n + 2 tq, + 1) see: [lo, pos]
+  int pos[NT][2], lo[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = 8 * n + 2 * tq + i;
+      pos[n][i] = r < rows ? g.pos0 + r / p.G : -1;
+      lo[n][i] = p.window > 0 ? max(0, pos[n][i] - p.window + 1) : 0;
+    }
+  const int pos_least = g.pos0, lo_most = p.window > 0 ? max(0, g.pos0 + g.tokens - p.window) : 0;
+  const uint32_t ring_a = sm100::smem_u32(ring);
+  // ldmatrix addresses within a stage: lanes 0-7, 8-15, .. give the rows of the four 8 x 8 blocks
+  const int r8 = lane & 7, q4 = lane >> 3;
+  const int krow = r8 + 8 * (q4 & 1), kch = q4 >> 1;       // K: keys 0-7 / 8-15, elements 0-7 / 8-15
+  const int vrow = r8 + 8 * (q4 >> 1), vch = q4 & 1;       // V: elements 0-7 / 8-15, keys 0-7 / 8-15
+  for (int u = 0; u < g.nt; ++u) {
+    ok = ok && __all_sync(0xffffffffu, sm100::mbar_wait(&bars[slot], (phases >> slot) & 1u, abort));
+    if (ok) phases ^= 1u << slot;
+    const uint32_t stage = ring_a + slot * T::STAGE;
+    const int key0 = ((g.kt0 + u) * tw.wph + tw.sub) * 16;
+    if (key0 + 16 > g.len) {
+      // rows past the length may hold anything, and 0 x NaN is NaN: V's become zeros
+      uint8_t* v = ring + slot * T::STAGE + T::HALVES * T::HALF;
+      for (int x = lane; x < 16 * 8 * T::HALVES; x += 32)
+        if (key0 + ((x >> 3) & 15) >= g.len) *reinterpret_cast<uint4*>(v + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+      sm100::fence_proxy_async_smem();         // (the stage's next writer is TMA)
+      __syncwarp();
+    }
+    float s[NT][4], z[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[n][i] = z[n][i] = 0.f;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      uint32_t a[4];
+      ldsm4(a, stage + (k >> 2) * T::HALF + krow * 128 + ((((2 * k + kch) & 7) ^ (krow & 7)) << 4));
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma_16816(k & 1 ? z[n] : s[n], a, qf[n][k][0], qf[n][k][1]);
+    }
+    const bool masked = key0 + 15 > pos_least || key0 < lo_most;
+    bool ask = false;
+    float mt[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[n][i] = (s[n][i] + z[n][i]) * p.c;
+        if (masked) {
+          const int key = key0 + gq + 8 * (i >> 1);
+          s[n][i] = key >= lo[n][i & 1] && key <= pos[n][i & 1] ? s[n][i] : -INFINITY;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        mt[n][i] = fmaxf(s[n][i], s[n][i + 2]);
+        ask = ask || mt[n][i] > m[n][i] + CH_RAISE || (m[n][i] == -INFINITY && mt[n][i] != -INFINITY);
+      }
+    }
+    if (__any_sync(0xffffffffu, ask)) {
+      // the rows' maxima over the 16 keys; every lane of a row takes the same step
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float x = mt[n][i];
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+          if (x > m[n][i]) {
+            const float f = m[n][i] == -INFINITY ? 0.f : sm100::exp2(m[n][i] - x);
+            m[n][i] = x;
+            l[n][i] *= f;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+              o[n][j][i] *= f;
+              o[n][j][i + 2] *= f;
+            }
+          }
+        }
+    }
+    uint32_t b[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float n0 = m[n][0] == -INFINITY ? 0.f : m[n][0], n1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+      const float e0 = sm100::exp2(s[n][0] - n0), e1 = sm100::exp2(s[n][1] - n1);
+      const float e2 = sm100::exp2(s[n][2] - n0), e3 = sm100::exp2(s[n][3] - n1);
+      l[n][0] += e0 + e2;
+      l[n][1] += e1 + e3;
+      const __nv_bfloat162 x = __floats2bfloat162_rn(e0, e1), y = __floats2bfloat162_rn(e2, e3);
+      b[n][0] = transpose8(*reinterpret_cast<const uint32_t*>(&x));
+      b[n][1] = transpose8(*reinterpret_cast<const uint32_t*>(&y));
+    }
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) {
+      uint32_t a[4];
+      ldsm4_t(a, stage + (T::HALVES + (j >> 2)) * T::HALF + vrow * 128 + ((((2 * j + vch) & 7) ^ (vrow & 7)) << 4));
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma_16816(o[n][j], a, b[n][0], b[n][1]);
+    }
+    __syncwarp();                            // every lane has read the stage
+    if (ok && u + T::STAGES < g.nt)
+      token_load<D>(p, kmap, vmap, g, hk, ring + slot * T::STAGE, &bars[slot], blocks, tw, u + T::STAGES);
+    slot = slot + 1 == T::STAGES ? 0 : slot + 1;
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], d);
+}
+
+// A segment's end: the states of a head's warps joined, 8 query rows at a
+// time, and the rows written (a whole item) or left as a partial, which the
+// last of the item's workers joins in worker order.
+template <int D, int NT>
+__device__ __forceinline__ void token_join(const ChunkParams& p, const Segment& g, int hk, float* mem, float* sm_m,
+                                           float* sm_l, int* sm_prev, const TokenWarp& tw,
+                                           const float (&o)[NT][D / 16][4], const float (&m)[NT][2],
+                                           const float (&l)[NT][2]) {
+  using T = TokenShape<D>;
+  const int lane = tw.lane, gq = lane >> 2, tq = lane & 3, wph = tw.wph;
+  const int tid = tw.sub * 32 + lane, threads = 32 * wph;  // of the head's warps
+  const int rows = hk < p.hkv ? g.tokens * p.G : 0;
+  float* buf = mem + tw.hslot * wph * 8 * D;
+  sm_m += tw.hslot * wph * 8;
+  sm_l += tw.hslot * wph * 8;
+  auto all = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(CH_SOFT_THREADS) : "memory"); };
+  auto sync = [&]() {
+    if (wph == 1) __syncwarp();
+    else all();
+  };
+  auto out_of = [&](int r) {
+    const int t = r / p.G, h = r - t * p.G;
+    return p.out + (static_cast<size_t>(g.row0) + t) * p.ld_o + (hk * p.G + h) * p.dh;
+  };
+  auto store4 = [&](uint16_t* dst, float4 v, float z) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x * z, v.y * z), b = __floats2bfloat162_rn(v.z * z, v.w * z);
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  };
+  auto part_of = [&](int slot) { return p.tk_part + (static_cast<size_t>(slot) * 8 + tw.hslot) * T::PART; };
+  float* part = part_of(g.part);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    sync();                                  // the buffer's last use is over
+    // [warp][row][D], element d of row r at d ^ 8 (r / 2 % 4): the warp's stores fall on different banks
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        buf[(tw.sub * 8 + 2 * tq + (i & 1)) * D + ((16 * j + gq + 8 * (i >> 1)) ^ (8 * tq))] = o[n][j][i];
+    if (gq == 0) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        sm_m[tw.sub * 8 + 2 * tq + i] = m[n][i];
+        sm_l[tw.sub * 8 + 2 * tq + i] = l[n][i];
+      }
+    }
+    sync();
+    for (int x = tid; x < 8 * (D / 4); x += threads) {
+      const int r = x / (D / 4), c4 = x - r * (D / 4), rr = 8 * n + r;
+      if (rr >= rows || 4 * c4 >= p.dh) continue;
+      float M = -INFINITY;
+      for (int w = 0; w < wph; ++w) M = fmaxf(M, sm_m[w * 8 + r]);
+      float L = 0.f;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = 0; w < wph; ++w) {
+        const float f = sm_m[w * 8 + r] == -INFINITY ? 0.f : sm100::exp2(sm_m[w * 8 + r] - M);
+        const float4 y = *reinterpret_cast<const float4*>(buf + (w * 8 + r) * D + ((4 * c4) ^ (8 * ((r >> 1) & 3))));
+        L = fmaf(f, sm_l[w * 8 + r], L);
+        v.x = fmaf(f, y.x, v.x);
+        v.y = fmaf(f, y.y, v.y);
+        v.z = fmaf(f, y.z, v.z);
+        v.w = fmaf(f, y.w, v.w);
+      }
+      if (g.whole) {
+        store4(out_of(rr) + 4 * c4, v, L > 0.f ? 1.f / L : 0.f);
+      } else {
+        *reinterpret_cast<float4*>(part + rr * D + 4 * c4) = v;
+        if (c4 == 0) {
+          part[TK_ROWS * D + rr] = M;
+          part[TK_ROWS * (D + 1) + rr] = L;
+        }
+      }
+    }
+  }
+  if (g.whole) return;
+  all();                                     // every head's partial comes before the arrival
+  if (tw.hslot == 0 && tid == 0) {
+    *sm_prev = arrive_acq_rel(&p.tk_cnt[g.first_cta]);
+    if (*sm_prev == g.n_parts - 1) p.tk_cnt[g.first_cta] = 0;
+  }
+  all();
+  if (*sm_prev != g.n_parts - 1) return;
+  auto slot_of = [&](int k) { return part_of(k == 0 ? 2 * g.first_cta + 1 : 2 * (g.first_cta + k)); };
+  for (int x = tid; x < rows * (D / 4); x += threads) {
+    const int r = x / (D / 4), c4 = x - r * (D / 4);
+    if (4 * c4 >= p.dh) continue;
+    float M = -INFINITY;
+#pragma unroll 8
+    for (int k = 0; k < g.n_parts; ++k) M = fmaxf(M, __ldcg(slot_of(k) + TK_ROWS * D + r));
+    float L = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int k = 0; k < g.n_parts; ++k) {
+      const float* sp = slot_of(k);
+      const float mk = __ldcg(sp + TK_ROWS * D + r), lk = __ldcg(sp + TK_ROWS * (D + 1) + r);
+      const float4 y = __ldcg(reinterpret_cast<const float4*>(sp + r * D + 4 * c4));
+      const float f = mk == -INFINITY ? 0.f : sm100::exp2(mk - M);
+      L = fmaf(f, lk, L);
+      v.x = fmaf(f, y.x, v.x);
+      v.y = fmaf(f, y.y, v.y);
+      v.z = fmaf(f, y.z, v.z);
+      v.w = fmaf(f, y.w, v.w);
+    }
+    store4(out_of(r) + 4 * c4, v, L > 0.f ? 1.f / L : 0.f);
+  }
+}
+
+template <int D>
+__device__ __forceinline__ bool token_phase(const ChunkParams& p, const CUtensorMap* kmap, const CUtensorMap* vmap,
+                                            uint8_t* mem, uint64_t* bars, volatile int* abort, float* sm_m, float* sm_l,
+                                            int* sm_prev, int sw, int lane) {
+  using T = TokenShape<D>;
+  if (p.G > TK_ROWS) return true;
+  Share<TOKEN> share;
+  share.begin(p, lane, blockIdx.x, gridDim.x, false);
+  const TokenWarp tw{p.tk_wph, sw / p.tk_wph, sw % p.tk_wph, lane};
+  uint8_t* ring = mem + sw * T::STAGES * T::STAGE;
+  bars += sw * T::STAGES;
+  float* buf = reinterpret_cast<float*>(mem + T::JOIN);
+  int slot = 0;
+  uint32_t phases = 0;                         // of the stages' barriers, a bit each
+  bool ok = true;
+  TokenBlocks blocks{0, 0};
+  auto head = [&](const Segment& g) { return g.hk * (CH_SOFT_WARPS / p.tk_wph) + tw.hslot; };
+  // a segment's first steps into the ring, from `slot` on
+  auto request = [&](const Segment& g) {
+    blocks.base = -32;
+    if (!ok || head(g) >= p.hkv) return;
+    for (int u = 0; u < min(T::STAGES, g.nt); ++u) {
+      const int s = (slot + u) % T::STAGES;
+      token_load<D>(p, kmap, vmap, g, head(g), ring + s * T::STAGE, &bars[s], blocks, tw, u);
+    }
+  };
+  Segment g = share.next(p, lane);
+  if (g.last) return true;
+  request(g);
+  // (After a wait that gave up a warp still goes through its segments, waiting and requesting no more: the joins'
+  // barriers count on all of them.)
+  while (true) {
+    Segment next;
+    const int hk = head(g);
+    Segment mine = g;
+    if (hk >= p.hkv) mine.nt = 0;            // a warp without a head: its joins' barriers only
+    if (g.tokens * p.G <= 8) {
+      float o[1][D / 16][4], m[1][2], l[1][2];
+      token_segment<D, 1>(p, kmap, vmap, mine, hk, ring, bars, phases, slot, abort, ok, blocks, tw, o, m, l);
+      next = share.next(p, lane);
+      if (!next.last) request(next);         // on their way while this segment is joined
+      token_join<D, 1>(p, g, hk, buf, sm_m, sm_l, sm_prev, tw, o, m, l);
+    } else {
+      float o[2][D / 16][4], m[2][2], l[2][2];
+      token_segment<D, 2>(p, kmap, vmap, mine, hk, ring, bars, phases, slot, abort, ok, blocks, tw, o, m, l);
+      next = share.next(p, lane);
+      if (!next.last) request(next);
+      token_join<D, 2>(p, g, hk, buf, sm_m, sm_l, sm_prev, tw, o, m, l);
+    }
+    if (next.last) break;
+    g = next;
+  }
+  if (!ok) {
+    // no copy may still be landing when the CTA leaves
+    volatile int never = 0;
+    for (int s = 0; s < T::STAGES; ++s) sm100::mbar_wait(&bars[s], (phases >> s) & 1u, &never);
+  }
+  return ok;
+}
+
 // ---- the kernel ------------------------------------------------------------------
 
 template <int D>
 __global__ void __launch_bounds__(CH_THREADS, 1)
     chunk_attn_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUtensorMap qmap,
-                      const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+                      const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                      const __grid_constant__ CUtensorMap tkmap, const __grid_constant__ CUtensorMap tvmap) {
   using S = Shape<D>;
   constexpr int SLOTS = S::SLOTS;
   constexpr int PART = 2 * CH_ROWS * (D + 2);            // floats of a partial
@@ -457,6 +973,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
       sm100::mbar_init(&sh.p_full[i >> 1][i & 1], 4);
     }
     sm100::mbar_init(&sh.join, CH_SOFT_WARPS);
+    sm100::mbar_init(&sh.tk_done, CH_SOFT_WARPS);
+    for (int i = 0; i < CH_SOFT_WARPS * TK_STAGES<SLOTS>; ++i) sm100::mbar_init(&sh.tk_full[i], 1);
     sm100::mbar_init(&sh.done, 2);
     sh.abort = 0;
     sh.never = 0;
@@ -489,52 +1007,14 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CH_REGS_FEW));
     if (warp == CH_SCHED_WARP) {
       // ---- scheduler ----
-      Walk w{};
-      const int parts = p.hkv * p.nsub;
-      const long long U = scan_batch(p, lane, -1, blockIdx.x == 0, w);
-      const long long n = min(static_cast<long long>(gridDim.x), U);     // CTAs with work
-      const long long c = blockIdx.x;
-      long long at = c < n ? U * c / n : 0, end = c < n ? U * (c + 1) / n : 0;
-      if (at < end) scan_batch(p, lane, at, false, w);
+      Share<TENSOR> share;
+      share.begin(p, lane, blockIdx.x, gridDim.x, blockIdx.x == 0);
       bool ok = true;
       for (int i = 0; ok; ++i) {
         const int slot = i % CH_SEGS;
         if (i >= CH_SEGS) ok = warp_wait(&sh.seg_empty[slot], static_cast<uint32_t>((i / CH_SEGS - 1) & 1));
         if (!ok) break;
-        Segment g{};
-        g.last = at >= end;
-        if (!g.last) {
-          int kt0, kt1;
-          item_tiles(p, w.r, w.q, kt0, kt1);
-          const int units = max(1, kt1 - kt0);
-          const int x0 = static_cast<int>(at - w.unit);
-          const int x1 = static_cast<int>(min(static_cast<long long>(units), end - w.unit));
-          const int hk = w.hs / p.nsub, sub = w.hs - hk * p.nsub;
-          const int t0 = w.q * w.r.per;
-          g.row0 = w.r.row0 + t0;
-          g.tokens = min(w.r.per, w.r.n - t0);
-          g.pos0 = w.r.len - w.r.n + t0;
-          g.len = w.r.len;
-          g.b = w.b;
-          g.hk = hk;
-          g.head0 = hk * p.G + sub * p.GB;
-          g.heads = min(p.GB, p.G - sub * p.GB);
-          g.kt0 = kt0 + x0;
-          g.nt = kt1 > kt0 ? x1 - x0 : 0;
-          g.two = g.tokens > p.T;
-          g.whole = x0 == 0 && x1 == units;
-          if (!g.whole) {
-            // the CTA that holds unit u: the largest whose range begins at or before it
-            g.first_cta = static_cast<int>(((w.unit + 1) * n - 1) / U);
-            g.n_parts = static_cast<int>(((w.unit + units) * n - 1) / U) - g.first_cta + 1;
-            g.part = 2 * static_cast<int>(c) + (x0 == 0 ? 1 : 0);
-          }
-          at = w.unit + x1;
-          if (x1 == units) {
-            w.unit += units;
-            if (at < end && !walk_on(p, w, lane)) at = end;
-          }
-        }
+        const Segment g = share.next(p, lane);
         if (lane == 0) {
           sh.seg[slot] = g;
           sm100::mbar_arrive(&sh.seg_full[slot]);
@@ -543,7 +1023,6 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
         if (g.last) break;
       }
       if (!ok && lane == 0) give_up();
-      (void)parts;
     } else if (warp == CH_LOAD_WARP) {
       // ---- loader ----
       const bool paged = p.paged.table != nullptr;
@@ -551,7 +1030,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
       int e = 0;                               // ring elements so far: K and V tiles alternate
       int segs = 0;                            // segments with tiles so far
       uint32_t raw = 0;                        // V tiles that needed zeroing so far
-      bool ok = true;
+      bool ok = warp_wait(&sh.tk_done, 0u);    // the token phase has used the tiles' memory
       for (int i = 0; ok; ++i) {
         const int slot = i % CH_SEGS;
         ok = warp_wait(&sh.seg_full[slot], static_cast<uint32_t>((i / CH_SEGS) & 1));
@@ -726,6 +1205,14 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
   } else {
     // ---- softmax ----
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(CH_REGS_SOFT));
+    bool tk_ok;
+    {
+      tk_ok = token_phase<D>(p, &tkmap, &tvmap, sm, sh.tk_full, abort_flag, sh.m[0], sh.l[0], &sh.tk_prev,
+                             warp - CH_SOFT_WARP0, lane);
+      sm100::fence_proxy_async_smem();         // the ring's next writer is TMA
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(&sh.tk_done);
+    }
     const int w = (warp - CH_SOFT_WARP0) >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
@@ -733,7 +1220,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
     const int st = tid - 32 * CH_SOFT_WARP0;               // 0 .. 255
     const int tok = row / p.GB, head = row - tok * p.GB;   // of this row in its tile
     uint32_t s_phase = 0, j_phase = 0;
-    bool ok = true;
+    bool ok = warp_wait(&sh.tk_done, 0u) && tk_ok;   // (the token phase used m and l)
     // all softmax warps: shared memory and tensor memory of the others' last step may be used after it
     auto join = [&]() {
       __syncwarp();
@@ -902,18 +1389,24 @@ bool encode(eagle_ctx* ctx, CUtensorMap* map, const void* ptr, int rank, const c
 
 template <int D>
 cudaError_t launch_shape(eagle_ctx* ctx, const ChunkParams& p, const CUtensorMap& qm, const CUtensorMap& km,
-                         const CUtensorMap& vm, cudaStream_t st) {
+                         const CUtensorMap& vm, const CUtensorMap& tkm, const CUtensorMap& tvm, cudaStream_t st) {
   const cudaError_t e =
       smem_limit_once(reinterpret_cast<const void*>(chunk_attn_kernel<D>), static_cast<int>(chunk_smem<D>()));
   if (e != cudaSuccess) return e;
-  return launch_pdl(chunk_attn_kernel<D>, dim3(ctx->sm_count), dim3(CH_THREADS), chunk_smem<D>(), st, p, qm, km, vm);
+  return launch_pdl(chunk_attn_kernel<D>, dim3(ctx->sm_count), dim3(CH_THREADS), chunk_smem<D>(), st, p, qm, km, vm, tkm,
+                    tvm);
 }
 
 }  // namespace
 
-size_t chunk_part_bytes(int sm_count, int head_dim) {
-  return static_cast<size_t>(2) * sm_count * 2 * CH_ROWS * ((head_dim > 64 ? 128 : 64) + 2) * sizeof(float);
+static size_t part_floats(int sm_count, int head_dim) {
+  return static_cast<size_t>(2) * sm_count * 2 * CH_ROWS * ((head_dim > 64 ? 128 : 64) + 2);
 }
+size_t chunk_part_bytes(int sm_count, int head_dim) {
+  return (part_floats(sm_count, head_dim) +
+          static_cast<size_t>(2) * sm_count * 8 * TK_ROWS * ((head_dim > 64 ? 128 : 64) + 2)) * sizeof(float);
+}
+int chunk_counters(int sm_count) { return 2 * sm_count; }
 
 cudaError_t launch_chunk_attn(eagle_ctx* ctx, int batch, const eagle_rows* rows, const uint16_t* q, int ld_q,
                               const eagle_kv* kv, int window, float scale, uint16_t* out, int ld_out, void* ws,
@@ -931,7 +1424,14 @@ cudaError_t launch_chunk_attn(eagle_ctx* ctx, int batch, const eagle_rows* rows,
   p.ld_o = ld_out;
   p.cap = kv->cap;
   p.window = window >= kv->cap ? 0 : window;   // a window of the whole cache is none
+  // eight kv heads side by side when there are as many, else each shared by 2, 4 or 8 warps
+  p.tk_wph = p.hkv >= 8 ? 1 : p.hkv >= 4 ? 2 : p.hkv >= 2 ? 4 : 8;
+  p.tk_parts = ceil_div(p.hkv, CH_SOFT_WARPS / p.tk_wph);
   p.len = kv->len;
+  p.q = q;
+  p.ld_q = ld_q;
+  p.k = kv->k;
+  p.v = kv->v;
   p.paged = paged_of(&kv->paging, kv->cap);
   const bool paged = p.paged.table != nullptr;
   const int bs = paged ? kv->paging.block_size : kv->cap;
@@ -939,6 +1439,8 @@ cudaError_t launch_chunk_attn(eagle_ctx* ctx, int batch, const eagle_rows* rows,
   p.c = scale * 1.4426950408889634f;
   p.part = ws_ptr<float>(ws, ctx->ws.attn_part);
   p.cnt = ws_ptr<int>(ws, ctx->ws.chunk_cnt);
+  p.tk_part = p.part + part_floats(ctx->sm_count, D.head_dim);
+  p.tk_cnt = p.cnt + ctx->sm_count;
   p.status = ws_ptr<int>(ws, ctx->ws.status);
   // q as {element, head, row}; a K or V pool as {element, kv head, row of a block, block} (contiguous: row, request)
   const cuuint64_t e2 = 2, dh = static_cast<cuuint64_t>(p.dh);
@@ -950,13 +1452,16 @@ cudaError_t launch_chunk_attn(eagle_ctx* ctx, int batch, const eagle_rows* rows,
   const cuuint64_t row = dh * p.hkv * e2;
   const cuuint64_t ks[3] = {dh * e2, row, row * bs};
   const cuuint32_t kb[4] = {64, 1, static_cast<cuuint32_t>(p.box), 1};
-  CUtensorMap qm, km, vm;
+  const cuuint32_t tb[4] = {64, 1, static_cast<cuuint32_t>(std::min(p.box, 16)), 1};   // the token phase's steps
+  CUtensorMap qm, km, vm, tkm, tvm;
   if (!encode(ctx, &qm, q, 3, qd, qs, qb) || !encode(ctx, &km, kv->k, 4, kd, ks, kb) ||
-      !encode(ctx, &vm, kv->v, 4, kd, ks, kb))
+      !encode(ctx, &vm, kv->v, 4, kd, ks, kb) || !encode(ctx, &tkm, kv->k, 4, kd, ks, tb) ||
+      !encode(ctx, &tvm, kv->v, 4, kd, ks, tb))
     return cudaErrorInvalidValue;
   p.stamp = stamp_slot(ctx, EAGLE_K_CHUNK_ATTN);
   trace_before(ctx, EAGLE_K_CHUNK_ATTN, st);
-  const cudaError_t e = p.dh > 64 ? launch_shape<128>(ctx, p, qm, km, vm, st) : launch_shape<64>(ctx, p, qm, km, vm, st);
+  const cudaError_t e = p.dh > 64 ? launch_shape<128>(ctx, p, qm, km, vm, tkm, tvm, st)
+                                    : launch_shape<64>(ctx, p, qm, km, vm, tkm, tvm, st);
   ctx->launches++;
   trace_after(ctx, EAGLE_K_CHUNK_ATTN, st);
   return e;

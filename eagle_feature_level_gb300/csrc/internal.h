@@ -46,7 +46,7 @@ struct Workspace {
   size_t gemm_cnt;               // int [N_EPI][max_mtiles]
   size_t attn_part;              // fp32 partial (m, l, acc[dh]) records
   size_t attn_cnt;               // int [2][max_batch * Hkv]
-  size_t chunk_cnt;              // int [SMs]: arrivals at the chunk attention's split items
+  size_t chunk_cnt;              // int [chunk_counters]: arrivals at the chunk attention's split items
   size_t pages;                  // int lists of the page calls (PAGES_LISTS per sequence) and their counts
   size_t total;
   int max_mtiles;
@@ -275,6 +275,7 @@ cudaError_t launch_chunk_attn(eagle_ctx* ctx, int batch, const eagle_rows* rows,
                               const eagle_kv* kv, int window, float scale, uint16_t* out, int ld_out, void* ws,
                               cudaStream_t st);
 size_t chunk_part_bytes(int sm_count, int head_dim);   // its partials
+int chunk_counters(int sm_count);                      // and arrival counters
 cudaError_t launch_pages_fork(eagle_ctx* ctx, const eagle_pages& pg, int n, const int32_t* src, const int32_t* dst,
                               void* ws, cudaStream_t st);
 cudaError_t launch_pages_reserve(eagle_ctx* ctx, const eagle_pages& pg, const eagle_pools& pools, const int32_t* n_new,
