@@ -91,10 +91,10 @@ struct ChunkParams {
   PagedKv paged;
   int box;                                   // rows of a K / V box
   float c;                                   // scale * log2 e
+  int tensor;                                // some request may have more rows than the token phase takes
   float* part;                               // [2 grid] partials of split items
   int* cnt;                                  // [grid] arrivals at a split item, by its first CTA
-  int tk_wph, tk_parts;                      // the token phase: warps per kv head, groups of heads
-  float* tk_part;                            // its partials and arrivals
+  float* tk_part;                            // the token phase's partials by run, arrivals at split items by their first run,
   int* tk_cnt;
   int* status;
   uint64_t* stamp;
@@ -112,7 +112,7 @@ struct Segment {
   int two;         // two query tiles
   int whole;       // the item's only segment
   int part;        // partial slot
-  int first_cta, n_parts;
+  int first_run, n_parts;
   int last;        // no segment: the CTA is done
 };
 
@@ -120,7 +120,7 @@ struct Segment {
 template <int SLOTS>
 struct Shared {
   uint64_t full[SLOTS], empty[SLOTS], seg_full[CH_SEGS], seg_empty[CH_SEGS];
-  uint64_t q_full, q_empty, v_raw, s_full[2][2], p_full[2][2], join, done;
+  uint64_t tm_ready, q_full, q_empty, v_raw, s_full[2][2], p_full[2][2], join, done;
   Segment seg[CH_SEGS];
   float m[2][CH_ROWS], l[2][CH_ROWS];
   uint64_t tk_full[CH_SOFT_WARPS * TK_STAGES<SLOTS>];
@@ -146,8 +146,15 @@ struct Request {
 // others by the tensor-memory phase; each walks the requests of its own class.
 enum : int { TENSOR = 0, TOKEN = 1 };
 
+// a / b of non-negative numbers, in 32 bits where they fit (a 64-bit division
+// is a few hundred instructions).
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (static_cast<unsigned long long>(a | b) >> 32 == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+  return a / b;
+}
+
 template <int CLASS>
-__device__ __forceinline__ int parts_of(const ChunkParams& p) { return CLASS == TOKEN ? p.tk_parts : p.hkv * p.nsub; }
+__device__ __forceinline__ int parts_of(const ChunkParams& p) { return CLASS == TOKEN ? p.hkv : p.hkv * p.nsub; }
 
 template <int CLASS>
 __device__ __forceinline__ Request request_of(const ChunkParams& p, int b) {
@@ -174,36 +181,32 @@ __device__ __forceinline__ void take_from(Request& to, const Request& from, int 
 }
 
 // Key tiles [kt0, kt1) of item q (kt1 <= kt0: none of its rows sees a key).
-template <int CLASS>
 __device__ __forceinline__ void item_tiles(const ChunkParams& p, const Request& r, int q, int& kt0, int& kt1) {
-  const int KEYS = CLASS == TOKEN ? 16 * p.tk_wph : CH_KEYS;
-  const long long first = static_cast<long long>(r.len) - r.n + static_cast<long long>(q) * r.per;
-  const long long end = min(static_cast<long long>(r.len), first + r.per);
-  const long long lo = p.window > 0 ? max(0ll, first - p.window + 1) : 0ll;
-  kt0 = static_cast<int>(lo / KEYS);
-  kt1 = end > lo ? static_cast<int>((end + KEYS - 1) / KEYS) : kt0;
+  const int first = r.len - r.n + q * r.per;                 // the first row's position; no sum here passes 32 bits
+  const int end = q + 1 < r.items ? first + r.per : r.len;
+  const int lo = p.window > 0 && first >= p.window ? first - p.window + 1 : 0;
+  kt0 = lo / CH_KEYS;
+  kt1 = end > lo ? (end - 1) / CH_KEYS + 1 : kt0;
 }
-template <int CLASS>
 __device__ __forceinline__ int item_units(const ChunkParams& p, const Request& r, int q) {
   int a, z;
-  item_tiles<CLASS>(p, r, q, a, z);
+  item_tiles(p, r, q, a, z);
   return max(1, z - a);
 }
 
 // Units of one kv head part of the lane's own request (every lane calls it;
 // requests of many items are summed by the whole warp).
-template <int CLASS>
 __device__ __forceinline__ long long request_units(const ChunkParams& p, const Request& r, int lane) {
   constexpr int ALONE = 4;
   long long w = 0;
   if (r.items <= ALONE)
-    for (int q = 0; q < r.items; ++q) w += item_units<CLASS>(p, r, q);
+    for (int q = 0; q < r.items; ++q) w += item_units(p, r, q);
   for (unsigned todo = __ballot_sync(0xffffffffu, r.items > ALONE); todo; todo &= todo - 1) {
     const int l = __ffs(todo) - 1;
     Request s;
     take_from(s, r, l);
     long long part = 0;
-    for (int q = lane; q < s.items; q += 32) part += item_units<CLASS>(p, s, q);
+    for (int q = lane; q < s.items; q += 32) part += item_units(p, s, q);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
     if (lane == l) w = part;
@@ -219,7 +222,7 @@ __device__ __forceinline__ long long warp_scan(long long v, int lane) {   // inc
   return v;
 }
 
-// Units of the batch's requests, by one warp, 32 requests at a time.
+// Units (and items) of the batch's requests, by one warp, 32 requests at a time.
 struct Scan {
   Request r;               // the lane's request of the 32 at hand,
   long long units, end;    // its units per kv head part, and the sum up to its end
@@ -229,18 +232,23 @@ __device__ __forceinline__ void scan_32(const ChunkParams& p, int lane, int b0, 
   s.r = Request{};
   s.r.per = 1;
   if (b0 + lane < p.rows.B) s.r = request_of<CLASS>(p, b0 + lane);
-  s.units = request_units<CLASS>(p, s.r, lane);
+  s.units = request_units(p, s.r, lane);
   s.end = before + warp_scan(s.units * parts_of<CLASS>(p), lane);
 }
 template <int CLASS>
-__device__ __forceinline__ long long scan_batch(const ChunkParams& p, int lane, bool report, Scan& s) {
+__device__ __forceinline__ long long scan_batch(const ChunkParams& p, int lane, bool report, Scan& s,
+                                                long long& items) {
   long long sum = 0;
+  items = 0;
   for (int b0 = 0; b0 < p.rows.B; b0 += 32) {
     scan_32<CLASS>(p, lane, b0, sum, s);
     if (report && s.r.bad) set_status(p.status, EAGLE_ERR_INVALID_ARG);
     if (report && s.r.over) set_status(p.status, EAGLE_ERR_CAPACITY);
+    items += static_cast<long long>(s.r.items) * parts_of<CLASS>(p);
     sum = __shfl_sync(0xffffffffu, s.end, 31);
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) items += __shfl_xor_sync(0xffffffffu, items, o);
   return sum;
 }
 
@@ -266,11 +274,11 @@ __device__ __forceinline__ void walk_to(const ChunkParams& p, int lane, long lon
       take_from(w.r, s.r, l);
       const long long W = __shfl_sync(0xffffffffu, s.units, l);
       const long long begin = __shfl_sync(0xffffffffu, s.end - s.units * parts, l);
-      w.hs = static_cast<int>((u0 - begin) / W);
+      w.hs = static_cast<int>(quotient(u0 - begin, W));
       long long at = begin + W * w.hs;         // first unit of the part
       for (int q0 = 0; q0 < w.r.items; q0 += 32) {
         const int q = q0 + lane;
-        const long long v = q < w.r.items ? item_units<CLASS>(p, w.r, q) : 0;
+        const long long v = q < w.r.items ? item_units(p, w.r, q) : 0;
         const long long upto = at + warp_scan(v, lane);
         const unsigned hit = __ballot_sync(0xffffffffu, upto > u0 && q < w.r.items);
         if (hit) {
@@ -308,18 +316,28 @@ __device__ __forceinline__ bool walk_on(const ChunkParams& p, Walk& w, int lane)
   return false;
 }
 
-// One worker's share [at, end) of n workers' units, segment by segment.
+// The units in n even runs; run c, [U c / n, U (c + 1) / n), segment by
+// segment.
 template <int CLASS>
-struct Share {
+struct Runs {
+  Scan s;
   Walk w;
-  long long U, n, c, at, end;
-  __device__ __forceinline__ void begin(const ChunkParams& p, int lane, int worker, int workers, bool report) {
-    Scan s;
-    U = scan_batch<CLASS>(p, lane, report, s);
-    n = min(static_cast<long long>(workers), U);                 // workers with work
-    c = worker;
-    at = c < n ? U * c / n : 0;
-    end = c < n ? U * (c + 1) / n : 0;
+  long long U, items, n, c, at, end;
+  __device__ __forceinline__ void scan(const ChunkParams& p, int lane, bool report) {
+    U = scan_batch<CLASS>(p, lane, report, s, items);
+  }
+  // One run a worker; with fewer items than workers, the same number for every item, so that runs of equal items do not
+  // cross them (32 items of 8 units: 152 runs 16.2 us, 128 runs 10.3).  (Two or four runs a worker, claimed one after
+  // another, were slower: more partials.)
+  __device__ __forceinline__ void split(int workers) {
+    n = workers;
+    if (items > 0 && items < workers) n = workers - workers % static_cast<int>(items);
+    n = min(n, U);
+  }
+  __device__ __forceinline__ void begin(const ChunkParams& p, int lane, long long run) {
+    c = run;
+    at = c < n ? quotient(U * c, n) : 0;
+    end = c < n ? quotient(U * (c + 1), n) : 0;
     if (at < end) walk_to<CLASS>(p, lane, at, s, w);
   }
   __device__ __forceinline__ Segment next(const ChunkParams& p, int lane) {
@@ -327,11 +345,11 @@ struct Share {
     g.last = at >= end;
     if (g.last) return g;
     int kt0, kt1;
-    item_tiles<CLASS>(p, w.r, w.q, kt0, kt1);
+    item_tiles(p, w.r, w.q, kt0, kt1);
     const int units = max(1, kt1 - kt0);
     const int x0 = static_cast<int>(at - w.unit);
     const int x1 = static_cast<int>(min(static_cast<long long>(units), end - w.unit));
-    const int nsub = CLASS == TOKEN ? 1 : p.nsub;     // (a token item's hk: its group of heads)
+    const int nsub = CLASS == TOKEN ? 1 : p.nsub;
     const int hk = w.hs / nsub, sub = w.hs - hk * nsub;
     const int t0 = w.q * w.r.per;
     g.row0 = w.r.row0 + t0;
@@ -347,9 +365,9 @@ struct Share {
     g.two = g.tokens > p.T;
     g.whole = x0 == 0 && x1 == units;
     if (!g.whole) {
-      // the worker that holds unit u: the largest whose range begins at or before it
-      g.first_cta = static_cast<int>(((w.unit + 1) * n - 1) / U);
-      g.n_parts = static_cast<int>(((w.unit + units) * n - 1) / U) - g.first_cta + 1;
+      // the run that holds unit u: the largest that begins at or before it
+      g.first_run = static_cast<int>(quotient((w.unit + 1) * n - 1, U));
+      g.n_parts = static_cast<int>(quotient((w.unit + units) * n - 1, U)) - g.first_run + 1;
       g.part = 2 * static_cast<int>(c) + (x0 == 0 ? 1 : 0);
     }
     at = w.unit + x1;
@@ -455,35 +473,31 @@ __device__ __forceinline__ bool softmax_step(uint32_t s_addr, uint32_t o_addr, b
   return true;
 }
 
-// A split item's partials joined in CTA order, by the softmax threads: each
-// takes CN runs of four columns of a row at a time.
+// A split item's partials joined in run order, by the softmax threads: a
+// thread takes CN runs of four columns of its row at a time, from c0 on.
 template <int D, int CN>
-__device__ __forceinline__ void merge_parts(const ChunkParams& p, const Segment& g, int n_rows, int st) {
+__device__ __forceinline__ void merge_row(const ChunkParams& p, const Segment& g, int r, int c0, int cols,
+                                          uint16_t* dst) {
   constexpr int PART = 2 * CH_ROWS * (D + 2);
   const int n_parts = g.n_parts;
-  const float* first = p.part + static_cast<size_t>(2 * g.first_cta + 1) * PART;
+  const float* first = p.part + static_cast<size_t>(2 * g.first_run + 1) * PART;
   // the parts after the first are two slots apart, from the first's neighbour on
   auto slot_of = [&](int k) { return first + (k == 0 ? 0 : static_cast<size_t>(2 * k - 1) * PART); };
-  for (int x = st; x < n_rows * (D / 4 / CN); x += CH_SOFT_THREADS) {
-    const int cg = x / n_rows, r = x - cg * n_rows;
-    const int rt = r & (CH_ROWS - 1), t = rt / p.GB, h = rt - t * p.GB;
-    const int ti = (r >= CH_ROWS ? p.T : 0) + t;
-    if (t >= p.T || ti >= g.tokens || h >= g.heads || 4 * CN * cg >= p.dh) continue;
-    float M = -INFINITY;
-#pragma unroll 4
-    for (int k = 0; k < n_parts; ++k) M = fmaxf(M, __ldcg(slot_of(k) + 2 * CH_ROWS * D + r));
+  float M = -INFINITY;
+#pragma unroll 8
+  for (int k = 0; k < n_parts; ++k) M = fmaxf(M, __ldcg(slot_of(k) + 2 * CH_ROWS * D + r));
+  for (int c = c0; c < c0 + cols; c += CN) {
     float l = 0.f;
     float4 o[CN];
 #pragma unroll
     for (int j = 0; j < CN; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll(CN == 1 ? 4 : 2)
+#pragma unroll(CN == 1 ? 8 : 2)
     for (int k = 0; k < n_parts; ++k) {
       const float* sp = slot_of(k);
       const float m = __ldcg(sp + 2 * CH_ROWS * D + r), lk = __ldcg(sp + 2 * CH_ROWS * D + 2 * CH_ROWS + r);
       float4 v[CN];
 #pragma unroll
-      for (int j = 0; j < CN; ++j)
-        v[j] = __ldcg(reinterpret_cast<const float4*>(sp) + (CN * cg + j) * (2 * CH_ROWS) + r);
+      for (int j = 0; j < CN; ++j) v[j] = __ldcg(reinterpret_cast<const float4*>(sp) + (c + j) * (2 * CH_ROWS) + r);
       const float f = m == -INFINITY ? 0.f : sm100::exp2(m - M);
       l = fmaf(f, lk, l);
 #pragma unroll
@@ -495,33 +509,45 @@ __device__ __forceinline__ void merge_parts(const ChunkParams& p, const Segment&
       }
     }
     const float z = l > 0.f ? 1.f / l : 0.f;
-    uint16_t* dst = p.out + (static_cast<size_t>(g.row0) + ti) * p.ld_o + (g.head0 + h) * p.dh + 4 * CN * cg;
 #pragma unroll
     for (int j = 0; j < CN; ++j) {
+      if (4 * (c + j) >= p.dh) continue;
       const __nv_bfloat162 a = __floats2bfloat162_rn(o[j].x * z, o[j].y * z);
       const __nv_bfloat162 b = __floats2bfloat162_rn(o[j].z * z, o[j].w * z);
-      uint2 y;
-      y.x = *reinterpret_cast<const uint32_t*>(&a);
-      y.y = *reinterpret_cast<const uint32_t*>(&b);
-      *reinterpret_cast<uint2*>(dst + 4 * j) = y;
+      *reinterpret_cast<uint2*>(dst + 4 * (c + j)) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
     }
   }
+}
+template <int D>
+__device__ __forceinline__ void merge_parts(const ChunkParams& p, const Segment& g, int st) {
+  // rows side by side in the threads (their partials are), as many threads a row as there are
+  const int n_rows = g.two ? 2 * CH_ROWS : min(CH_ROWS, g.tokens * p.GB);
+  const int log_rows = 32 - __clz(n_rows - 1);           // of the rows rounded up to a power of two
+  const int r = st & ((1 << log_rows) - 1);
+  const int rt = r & (CH_ROWS - 1), t = rt / p.GB, h = rt - t * p.GB;
+  const int ti = (r >= CH_ROWS ? p.T : 0) + t;
+  const int per = CH_SOFT_THREADS >> log_rows, cols = max(1, D / 4 / per), c0 = (st >> log_rows) * cols;
+  if (t >= p.T || ti >= g.tokens || h >= g.heads || c0 >= D / 4) return;
+  uint16_t* dst = p.out + (static_cast<size_t>(g.row0) + ti) * p.ld_o + (g.head0 + h) * p.dh;
+  if (cols >= 8) merge_row<D, 8>(p, g, r, c0, cols, dst);
+  else merge_row<D, 1>(p, g, r, c0, cols, dst);
 }
 
 // ---- the token phase --------------------------------------------------------------
 //
 // Requests of at most 16 query rows a kv head (one decoding token and its
 // group) read every key for a handful of rows: the cache's bytes are all that
-// counts.  A cache row holds its kv heads side by side, 256 bytes each, and
-// DRAM serves whole rows better than pieces: with a kv head per worker, 16
-// requests of 8192 keys x 8 heads streamed at 4.1 TB/s.  So the eight softmax
-// warps take eight kv heads over the same keys (with fewer heads, 2, 4 or 8
-// warps share one), 16 keys a step, each warp through a ring of its own, with no
-// barrier between warps and an online softmax of its own.  One lane requests a
-// step by TMA (per-lane 16-byte copies spent 2300 of a step's 3100 cycles on
-// addresses and the block table).  The products are warp-level bf16 tiles with the keys as
-// rows, S^T = K Q^T and O^T += V^T P^T (m16n8k16): eight query rows fill the
-// narrow side, where Q as the 16-row side would be half padding.
+// counts.  An item is one kv head of a request; each of the eight softmax warps
+// takes 16 of a tile's 128 keys through a ring of its own, with no barrier
+// between warps and an online softmax of its own, and the eight states are
+// joined at a segment's end.  One lane requests a step by TMA (per-lane 16-byte
+// copies spent 2300 of a step's 3100 cycles on addresses and the block table).
+// The products are warp-level bf16 tiles with the keys as rows, S^T = K Q^T and
+// O^T += V^T P^T (m16n8k16): eight query rows fill the narrow side, where Q as
+// the 16-row side would be half padding.  (Eight kv heads side by side over
+// the same keys, whole cache rows for DRAM, streamed no faster, and one long
+// request then left 152 partials of every head: 128 us where this takes 21.)
 
 template <int D>
 struct TokenShape {
@@ -534,9 +560,12 @@ struct TokenShape {
   static_assert(JOIN + CH_SOFT_WARPS * 8 * D * 4 <= Shape<D>::TILES, "the tiles' memory");
 };
 
-// A warp's place: kv head `hk`, and the key steps sub, sub + wph, .. of a unit.
+// A warp's place among the eight, and the L2 policy of the cache's lines (read
+// once: the first to go, so that a cache larger than L2 does not push out code
+// and tables).
 struct TokenWarp {
-  int wph, hslot, sub, lane;
+  int w, lane;
+  uint64_t policy;
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
@@ -570,7 +599,7 @@ struct TokenBlocks {
   __device__ __forceinline__ int of(const ChunkParams& p, const Segment& g, const TokenWarp& tw, int u) {
     if (u < base || u >= base + 32) {
       base = u;
-      const int key0 = ((g.kt0 + u + tw.lane) * tw.wph + tw.sub) * 16;
+      const int key0 = (g.kt0 + u + tw.lane) * CH_KEYS + 16 * tw.w;
       blk = p.paged.n_blocks;                // out of range: reads as zeros
       if (u + tw.lane < g.nt && key0 < g.len) {
         const int x = p.paged.table[static_cast<size_t>(g.b) * p.paged.per_req + (key0 >> p.paged.shift)];
@@ -582,22 +611,23 @@ struct TokenBlocks {
   }
 };
 
-// Step u of segment g -- 16 keys of kv head hk, K then V -- into `stage`.  Rows
+// Step u of segment g -- the warp's 16 keys of a key tile, K then V -- into
+// `stage`.  Rows
 // past the length within their block arrive as they are, those of blocks that
 // do not exist as zeros.
 template <int D>
 __device__ __forceinline__ void token_load(const ChunkParams& p, const CUtensorMap* kmap, const CUtensorMap* vmap,
-                                           const Segment& g, int hk, uint8_t* stage, uint64_t* bar, TokenBlocks& blocks,
+                                           const Segment& g, uint8_t* stage, uint64_t* bar, TokenBlocks& blocks,
                                            const TokenWarp& tw, int u) {
   using T = TokenShape<D>;
-  const int key0 = ((g.kt0 + u) * tw.wph + tw.sub) * 16;
+  const int key0 = (g.kt0 + u) * CH_KEYS + 16 * tw.w;
   const bool paged = p.paged.table != nullptr;
   const int mask = (1 << p.paged.shift) - 1;
   auto box = [&](int y, int z, int row) {
 #pragma unroll
     for (int h = 0; h < T::HALVES; ++h) {
-      sm100::tma_load_4d(stage + h * T::HALF + row * 128, kmap, 64 * h, hk, y, z, bar);
-      sm100::tma_load_4d(stage + (T::HALVES + h) * T::HALF + row * 128, vmap, 64 * h, hk, y, z, bar);
+      sm100::tma_load_4d_hint(stage + h * T::HALF + row * 128, kmap, 64 * h, g.hk, y, z, bar, tw.policy);
+      sm100::tma_load_4d_hint(stage + (T::HALVES + h) * T::HALF + row * 128, vmap, 64 * h, g.hk, y, z, bar, tw.policy);
     }
   };
   if (tw.lane == 0) sm100::mbar_arrive_expect_tx(bar, T::STAGE);
@@ -626,7 +656,7 @@ __device__ __forceinline__ void token_load(const ChunkParams& p, const CUtensorM
 // rows.
 template <int D, int NT>
 __device__ __forceinline__ void token_segment(const ChunkParams& p, const CUtensorMap* kmap, const CUtensorMap* vmap,
-                                              const Segment& g, int hk, uint8_t* ring, uint64_t* bars, uint32_t& phases,
+                                              const Segment& g, uint8_t* ring, uint64_t* bars, uint32_t& phases,
                                               int& slot, volatile int* abort, bool& ok, TokenBlocks& blocks,
                                               const TokenWarp& tw, float (&o)[NT][D / 16][4], float (&m)[NT][2],
                                               float (&l)[NT][2]) {
@@ -638,10 +668,10 @@ __device__ __forceinline__ void token_segment(const ChunkParams& p, const CUtens
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int r = 8 * n + gq, t = r / p.G, h = r - t * p.G;
-    const uint16_t* q = p.q + (static_cast<size_t>(g.row0) + t) * p.ld_q + (hk * p.G + h) * p.dh + 2 * tq;
+    const uint16_t* q = p.q + (static_cast<size_t>(g.row0) + t) * p.ld_q + (g.head0 + h) * p.dh + 2 * tq;
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
-      const bool there = r < rows && 16 * k < p.dh && hk < p.hkv;
+      const bool there = r < rows && 16 * k < p.dh;
       qf[n][k][0] = there ? *reinterpret_cast<const uint32_t*>(q + 16 * k) : 0u;
       qf[n][k][1] = there ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 8) : 0u;
     }
@@ -672,7 +702,7 @@ __device__ __forceinline__ void token_segment(const ChunkParams& p, const CUtens
     ok = ok && __all_sync(0xffffffffu, sm100::mbar_wait(&bars[slot], (phases >> slot) & 1u, abort));
     if (ok) phases ^= 1u << slot;
     const uint32_t stage = ring_a + slot * T::STAGE;
-    const int key0 = ((g.kt0 + u) * tw.wph + tw.sub) * 16;
+    const int key0 = (g.kt0 + u) * CH_KEYS + 16 * tw.w;
     if (key0 + 16 > g.len) {
       // rows past the length may hold anything, and 0 x NaN is NaN: V's become zeros
       uint8_t* v = ring + slot * T::STAGE + T::HALVES * T::HALF;
@@ -754,7 +784,7 @@ __device__ __forceinline__ void token_segment(const ChunkParams& p, const CUtens
     }
     __syncwarp();                            // every lane has read the stage
     if (ok && u + T::STAGES < g.nt)
-      token_load<D>(p, kmap, vmap, g, hk, ring + slot * T::STAGE, &bars[slot], blocks, tw, u + T::STAGES);
+      token_load<D>(p, kmap, vmap, g, ring + slot * T::STAGE, &bars[slot], blocks, tw, u + T::STAGES);
     slot = slot + 1 == T::STAGES ? 0 : slot + 1;
   }
 #pragma unroll
@@ -765,62 +795,53 @@ __device__ __forceinline__ void token_segment(const ChunkParams& p, const CUtens
       for (int d = 4; d < 32; d <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], d);
 }
 
-// A segment's end: the states of a head's warps joined, 8 query rows at a
-// time, and the rows written (a whole item) or left as a partial, which the
-// last of the item's workers joins in worker order.
+__device__ __forceinline__ void all_soft() { asm volatile("bar.sync 1, %0;" ::"n"(CH_SOFT_THREADS) : "memory"); }
+__device__ __forceinline__ void store_bf16x4(uint16_t* dst, float4 v, float z) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x * z, v.y * z), b = __floats2bfloat162_rn(v.z * z, v.w * z);
+  *reinterpret_cast<uint2*>(dst) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+__device__ __forceinline__ uint16_t* token_row(const ChunkParams& p, const Segment& g, int r) {
+  const int t = r / p.G, h = r - t * p.G;
+  return p.out + (static_cast<size_t>(g.row0) + t) * p.ld_o + (g.head0 + h) * p.dh;
+}
+
+// A segment's end: the warps' states joined, 8 query rows at a time, and the
+// rows written (a whole item) or left as a partial.
 template <int D, int NT>
-__device__ __forceinline__ void token_join(const ChunkParams& p, const Segment& g, int hk, float* mem, float* sm_m,
-                                           float* sm_l, int* sm_prev, const TokenWarp& tw,
-                                           const float (&o)[NT][D / 16][4], const float (&m)[NT][2],
-                                           const float (&l)[NT][2]) {
-  using T = TokenShape<D>;
-  const int lane = tw.lane, gq = lane >> 2, tq = lane & 3, wph = tw.wph;
-  const int tid = tw.sub * 32 + lane, threads = 32 * wph;  // of the head's warps
-  const int rows = hk < p.hkv ? g.tokens * p.G : 0;
-  float* buf = mem + tw.hslot * wph * 8 * D;
-  sm_m += tw.hslot * wph * 8;
-  sm_l += tw.hslot * wph * 8;
-  auto all = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(CH_SOFT_THREADS) : "memory"); };
-  auto sync = [&]() {
-    if (wph == 1) __syncwarp();
-    else all();
-  };
-  auto out_of = [&](int r) {
-    const int t = r / p.G, h = r - t * p.G;
-    return p.out + (static_cast<size_t>(g.row0) + t) * p.ld_o + (hk * p.G + h) * p.dh;
-  };
-  auto store4 = [&](uint16_t* dst, float4 v, float z) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x * z, v.y * z), b = __floats2bfloat162_rn(v.z * z, v.w * z);
-    *reinterpret_cast<uint2*>(dst) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  };
-  auto part_of = [&](int slot) { return p.tk_part + (static_cast<size_t>(slot) * 8 + tw.hslot) * T::PART; };
-  float* part = part_of(g.part);
+__device__ __forceinline__ void token_join(const ChunkParams& p, const Segment& g, float* buf, float* sm_m, float* sm_l,
+                                           const TokenWarp& tw, const float (&o)[NT][D / 16][4],
+                                           const float (&m)[NT][2], const float (&l)[NT][2]) {
+  const int lane = tw.lane, gq = lane >> 2, tq = lane & 3, tid = tw.w * 32 + lane;
+  const int rows = g.tokens * p.G;
+  float* part = p.tk_part + static_cast<size_t>(g.part) * TokenShape<D>::PART;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    sync();                                  // the buffer's last use is over
+    all_soft();                              // the buffer's last use is over
     // [warp][row][D], element d of row r at d ^ 8 (r / 2 % 4): the warp's stores fall on different banks
 #pragma unroll
     for (int j = 0; j < D / 16; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        buf[(tw.sub * 8 + 2 * tq + (i & 1)) * D + ((16 * j + gq + 8 * (i >> 1)) ^ (8 * tq))] = o[n][j][i];
+        buf[(tw.w * 8 + 2 * tq + (i & 1)) * D + ((16 * j + gq + 8 * (i >> 1)) ^ (8 * tq))] = o[n][j][i];
     if (gq == 0) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        sm_m[tw.sub * 8 + 2 * tq + i] = m[n][i];
-        sm_l[tw.sub * 8 + 2 * tq + i] = l[n][i];
+        sm_m[tw.w * 8 + 2 * tq + i] = m[n][i];
+        sm_l[tw.w * 8 + 2 * tq + i] = l[n][i];
       }
     }
-    sync();
-    for (int x = tid; x < 8 * (D / 4); x += threads) {
+    all_soft();
+    for (int x = tid; x < 8 * (D / 4); x += CH_SOFT_THREADS) {
       const int r = x / (D / 4), c4 = x - r * (D / 4), rr = 8 * n + r;
       if (rr >= rows || 4 * c4 >= p.dh) continue;
       float M = -INFINITY;
-      for (int w = 0; w < wph; ++w) M = fmaxf(M, sm_m[w * 8 + r]);
+#pragma unroll
+      for (int w = 0; w < CH_SOFT_WARPS; ++w) M = fmaxf(M, sm_m[w * 8 + r]);
       float L = 0.f;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = 0; w < wph; ++w) {
+#pragma unroll
+      for (int w = 0; w < CH_SOFT_WARPS; ++w) {
         const float f = sm_m[w * 8 + r] == -INFINITY ? 0.f : sm100::exp2(sm_m[w * 8 + r] - M);
         const float4 y = *reinterpret_cast<const float4*>(buf + (w * 8 + r) * D + ((4 * c4) ^ (8 * ((r >> 1) & 3))));
         L = fmaf(f, sm_l[w * 8 + r], L);
@@ -830,7 +851,7 @@ __device__ __forceinline__ void token_join(const ChunkParams& p, const Segment& 
         v.w = fmaf(f, y.w, v.w);
       }
       if (g.whole) {
-        store4(out_of(rr) + 4 * c4, v, L > 0.f ? 1.f / L : 0.f);
+        store_bf16x4(token_row(p, g, rr) + 4 * c4, v, L > 0.f ? 1.f / L : 0.f);
       } else {
         *reinterpret_cast<float4*>(part + rr * D + 4 * c4) = v;
         if (c4 == 0) {
@@ -840,36 +861,46 @@ __device__ __forceinline__ void token_join(const ChunkParams& p, const Segment& 
       }
     }
   }
-  if (g.whole) return;
-  all();                                     // every head's partial comes before the arrival
-  if (tw.hslot == 0 && tid == 0) {
-    *sm_prev = arrive_acq_rel(&p.tk_cnt[g.first_cta]);
-    if (*sm_prev == g.n_parts - 1) p.tk_cnt[g.first_cta] = 0;
-  }
-  all();
-  if (*sm_prev != g.n_parts - 1) return;
-  auto slot_of = [&](int k) { return part_of(k == 0 ? 2 * g.first_cta + 1 : 2 * (g.first_cta + k)); };
-  for (int x = tid; x < rows * (D / 4); x += threads) {
-    const int r = x / (D / 4), c4 = x - r * (D / 4);
-    if (4 * c4 >= p.dh) continue;
-    float M = -INFINITY;
-#pragma unroll 8
-    for (int k = 0; k < g.n_parts; ++k) M = fmaxf(M, __ldcg(slot_of(k) + TK_ROWS * D + r));
-    float L = 0.f;
+}
+
+// A split item's partials joined in run order, a row per warp at a time: lane =
+// part for the row's maximum and sum, then lane = four columns.
+template <int D>
+__device__ __forceinline__ void token_merge(const ChunkParams& p, const Segment& g, const TokenWarp& tw) {
+  using T = TokenShape<D>;
+  const int lane = tw.lane;
+  const float* first = p.tk_part + static_cast<size_t>(2 * g.first_run + 1) * T::PART;
+  // the parts after the first are two slots apart, from the first's neighbour on
+  auto slot_of = [&](int k) { return first + (k == 0 ? 0 : static_cast<size_t>(2 * k - 1) * T::PART); };
+  for (int r = tw.w; r < g.tokens * p.G; r += CH_SOFT_WARPS) {
+    float M = -INFINITY, L = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < g.n_parts; k0 += 32) {
+      const bool there = k0 + lane < g.n_parts;
+      const float* sp = slot_of(there ? k0 + lane : 0) + TK_ROWS * D + r;
+      const float mk = there ? __ldcg(sp) : -INFINITY, lk = there ? __ldcg(sp + TK_ROWS) : 0.f;
+      const float now = fmaxf(M, warp_max(mk));
+      const float old = M == -INFINITY ? 0.f : sm100::exp2(M - now);   // of the 32 parts before
+      const float f = mk == -INFINITY ? 0.f : sm100::exp2(mk - now);
+      M = now;
+      L = fmaf(L, old, warp_sum(f * lk));
+      v.x *= old;
+      v.y *= old;
+      v.z *= old;
+      v.w *= old;
+      const int n = min(32, g.n_parts - k0);
 #pragma unroll 8
-    for (int k = 0; k < g.n_parts; ++k) {
-      const float* sp = slot_of(k);
-      const float mk = __ldcg(sp + TK_ROWS * D + r), lk = __ldcg(sp + TK_ROWS * (D + 1) + r);
-      const float4 y = __ldcg(reinterpret_cast<const float4*>(sp + r * D + 4 * c4));
-      const float f = mk == -INFINITY ? 0.f : sm100::exp2(mk - M);
-      L = fmaf(f, lk, L);
-      v.x = fmaf(f, y.x, v.x);
-      v.y = fmaf(f, y.y, v.y);
-      v.z = fmaf(f, y.z, v.z);
-      v.w = fmaf(f, y.w, v.w);
+      for (int k = 0; k < n; ++k) {
+        const float w = __shfl_sync(0xffffffffu, f, k);
+        const float4 y = 4 * lane < D ? __ldcg(reinterpret_cast<const float4*>(slot_of(k0 + k) + r * D) + lane)
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+        v.x = fmaf(w, y.x, v.x);
+        v.y = fmaf(w, y.y, v.y);
+        v.z = fmaf(w, y.z, v.z);
+        v.w = fmaf(w, y.w, v.w);
+      }
     }
-    store4(out_of(r) + 4 * c4, v, L > 0.f ? 1.f / L : 0.f);
+    if (4 * lane < p.dh) store_bf16x4(token_row(p, g, r) + 4 * lane, v, L > 0.f ? 1.f / L : 0.f);
   }
 }
 
@@ -879,9 +910,11 @@ __device__ __forceinline__ bool token_phase(const ChunkParams& p, const CUtensor
                                             int* sm_prev, int sw, int lane) {
   using T = TokenShape<D>;
   if (p.G > TK_ROWS) return true;
-  Share<TOKEN> share;
-  share.begin(p, lane, blockIdx.x, gridDim.x, false);
-  const TokenWarp tw{p.tk_wph, sw / p.tk_wph, sw % p.tk_wph, lane};
+  Runs<TOKEN> runs;
+  runs.scan(p, lane, false);
+  runs.split(gridDim.x);
+  runs.begin(p, lane, blockIdx.x);
+  const TokenWarp tw{sw, lane, sm100::l2_policy_evict_first()};
   uint8_t* ring = mem + sw * T::STAGES * T::STAGE;
   bars += sw * T::STAGES;
   float* buf = reinterpret_cast<float*>(mem + T::JOIN);
@@ -889,42 +922,64 @@ __device__ __forceinline__ bool token_phase(const ChunkParams& p, const CUtensor
   uint32_t phases = 0;                         // of the stages' barriers, a bit each
   bool ok = true;
   TokenBlocks blocks{0, 0};
-  auto head = [&](const Segment& g) { return g.hk * (CH_SOFT_WARPS / p.tk_wph) + tw.hslot; };
   // a segment's first steps into the ring, from `slot` on
   auto request = [&](const Segment& g) {
     blocks.base = -32;
-    if (!ok || head(g) >= p.hkv) return;
+    if (!ok) return;
     for (int u = 0; u < min(T::STAGES, g.nt); ++u) {
       const int s = (slot + u) % T::STAGES;
-      token_load<D>(p, kmap, vmap, g, head(g), ring + s * T::STAGE, &bars[s], blocks, tw, u);
+      token_load<D>(p, kmap, vmap, g, ring + s * T::STAGE, &bars[s], blocks, tw, u);
     }
   };
-  Segment g = share.next(p, lane);
-  if (g.last) return true;
-  request(g);
+  Segment g = runs.next(p, lane);
+  // the segment after this one, on its way while this one is joined
+  auto advance = [&]() {
+    const Segment next = runs.next(p, lane);
+    if (!next.last) request(next);
+    return next;
+  };
+  if (!g.last) request(g);
   // (After a wait that gave up a warp still goes through its segments, waiting and requesting no more: the joins'
   // barriers count on all of them.)
-  while (true) {
+  // A split item's arrival is one atomic, which takes microseconds on a busy memory: its answer is looked at a segment
+  // later.
+  Segment waiting{};
+  bool waits = false;
+  int arrived = 0;
+  auto settle = [&]() {
+    if (!waits) return;
+    if (sw == 0 && lane == 0) {
+      *sm_prev = arrived;
+      if (arrived == waiting.n_parts - 1) p.tk_cnt[waiting.first_run] = 0;
+    }
+    all_soft();
+    if (*sm_prev == waiting.n_parts - 1) token_merge<D>(p, waiting, tw);   // the last of the item's CTAs
+    waits = false;
+  };
+  while (!g.last) {
     Segment next;
-    const int hk = head(g);
-    Segment mine = g;
-    if (hk >= p.hkv) mine.nt = 0;            // a warp without a head: its joins' barriers only
     if (g.tokens * p.G <= 8) {
       float o[1][D / 16][4], m[1][2], l[1][2];
-      token_segment<D, 1>(p, kmap, vmap, mine, hk, ring, bars, phases, slot, abort, ok, blocks, tw, o, m, l);
-      next = share.next(p, lane);
-      if (!next.last) request(next);         // on their way while this segment is joined
-      token_join<D, 1>(p, g, hk, buf, sm_m, sm_l, sm_prev, tw, o, m, l);
+      token_segment<D, 1>(p, kmap, vmap, g, ring, bars, phases, slot, abort, ok, blocks, tw, o, m, l);
+      next = advance();
+      settle();
+      token_join<D, 1>(p, g, buf, sm_m, sm_l, tw, o, m, l);
     } else {
       float o[2][D / 16][4], m[2][2], l[2][2];
-      token_segment<D, 2>(p, kmap, vmap, mine, hk, ring, bars, phases, slot, abort, ok, blocks, tw, o, m, l);
-      next = share.next(p, lane);
-      if (!next.last) request(next);
-      token_join<D, 2>(p, g, hk, buf, sm_m, sm_l, sm_prev, tw, o, m, l);
+      token_segment<D, 2>(p, kmap, vmap, g, ring, bars, phases, slot, abort, ok, blocks, tw, o, m, l);
+      next = advance();
+      settle();
+      token_join<D, 2>(p, g, buf, sm_m, sm_l, tw, o, m, l);
     }
-    if (next.last) break;
+    if (!g.whole) {
+      all_soft();                            // the partial comes before its arrival
+      if (sw == 0 && lane == 0) arrived = arrive_acq_rel(&p.tk_cnt[g.first_run]);
+      waiting = g;
+      waits = true;
+    }
     g = next;
   }
+  settle();
   if (!ok) {
     // no copy may still be landing when the CTA leaves
     volatile int never = 0;
@@ -965,6 +1020,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
       sm100::mbar_init(&sh.seg_full[i], 1);
       sm100::mbar_init(&sh.seg_empty[i], 3 + CH_SOFT_WARPS);   // loader, MMA threads, softmax warps
     }
+    sm100::mbar_init(&sh.tm_ready, 1);
     sm100::mbar_init(&sh.q_full, 1);
     sm100::mbar_init(&sh.q_empty, 2);
     sm100::mbar_init(&sh.v_raw, 1);
@@ -980,17 +1036,23 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
     sh.never = 0;
     sm100::fence_barrier_init();
   }
+  if (warp == CH_LOAD_WARP && lane < (p.tensor ? 5 : 2))
+    sm100::tma_prefetch_desc(lane == 0 ? &tkmap : lane == 1 ? &tvmap : lane == 2 ? &qmap : lane == 3 ? &kmap : &vmap);
+  __syncthreads();
   pdl_wait();
   ls.waited();
-  if (warp == CH_MMA_WARP) {
+  if (!p.tensor) {
+    pdl_trigger();                             // every request has few rows: the token phase is all
+  } else if (warp == CH_MMA_WARP) {
+    // tensor memory only after the wait (every kernel this one waits for has finished), and dependents start only once
+    // every CTA holds its columns; the token phase runs meanwhile
     sm100::tmem_alloc(&sh.tmem, CH_TM_COLS);
     sm100::tmem_relinquish();
+    sm100::tc_fence_before();
+    __syncwarp();
+    if (lane == 0) sm100::mbar_arrive(&sh.tm_ready);
+    pdl_trigger();
   }
-  sm100::tc_fence_before();
-  __syncthreads();
-  sm100::tc_fence_after();
-  pdl_trigger();
-  const uint32_t tmem = sh.tmem;
   const uint32_t sbase = sm100::smem_u32(sm);
   const uint32_t rbase = sbase + 2 * S::TILE;
 
@@ -1005,16 +1067,26 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CH_REGS_FEW));
+    if (!p.tensor) {
+      if (warp == CH_SCHED_WARP && blockIdx.x == 0) {
+        Scan s;
+        long long items;
+        scan_batch<TENSOR>(p, lane, true, s, items);    // reports what is wrong with the batch
+      }
+      return;
+    }
     if (warp == CH_SCHED_WARP) {
       // ---- scheduler ----
-      Share<TENSOR> share;
-      share.begin(p, lane, blockIdx.x, gridDim.x, blockIdx.x == 0);
+      Runs<TENSOR> runs;
+      runs.scan(p, lane, blockIdx.x == 0);
+      runs.split(gridDim.x);
+      runs.begin(p, lane, blockIdx.x);
       bool ok = true;
       for (int i = 0; ok; ++i) {
         const int slot = i % CH_SEGS;
         if (i >= CH_SEGS) ok = warp_wait(&sh.seg_empty[slot], static_cast<uint32_t>((i / CH_SEGS - 1) & 1));
         if (!ok) break;
-        const Segment g = share.next(p, lane);
+        const Segment g = runs.next(p, lane);
         if (lane == 0) {
           sh.seg[slot] = g;
           sm100::mbar_arrive(&sh.seg_full[slot]);
@@ -1116,10 +1188,11 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
         constexpr uint32_t HI = sm100::DESC_SW128_HI;
         const uint32_t id_s = sm100::idesc_bf16_f32(CH_ROWS, CH_STEP);
         const uint32_t id_o = sm100::idesc_bf16_f32(CH_ROWS, D) | (1u << 16);     // B (V) MN-major
-        const uint32_t s_tm = tmem + CH_TM_S + 128u * w, o_tm = tmem + CH_TM_O + 128u * w;
+        bool ok = sm100::mbar_wait(&sh.tm_ready, 0u, abort_flag);
+        sm100::tc_fence_after();
+        const uint32_t tmem = sh.tmem, s_tm = tmem + CH_TM_S + 128u * w, o_tm = tmem + CH_TM_O + 128u * w;
         int e0 = 0, segs = 0;
         uint32_t p_phase = 0;
-        bool ok = true;
         for (int i = 0; ok; ++i) {
           const int slot = i % CH_SEGS;
           ok = sm100::mbar_wait(&sh.seg_full[slot], static_cast<uint32_t>((i / CH_SEGS) & 1), abort_flag);
@@ -1209,6 +1282,10 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
     {
       tk_ok = token_phase<D>(p, &tkmap, &tvmap, sm, sh.tk_full, abort_flag, sh.m[0], sh.l[0], &sh.tk_prev,
                              warp - CH_SOFT_WARP0, lane);
+      if (!p.tensor) {
+        if (!tk_ok && lane == 0) set_status(p.status, EAGLE_ERR_TIMEOUT);
+        return;
+      }
       sm100::fence_proxy_async_smem();         // the ring's next writer is TMA
       __syncwarp();
       if (lane == 0) sm100::mbar_arrive(&sh.tk_done);
@@ -1216,11 +1293,13 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
     const int w = (warp - CH_SOFT_WARP0) >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t s_addr = tmem + CH_TM_S + 128u * w + lane_base, o_addr = tmem + CH_TM_O + 128u * w + lane_base;
     const int st = tid - 32 * CH_SOFT_WARP0;               // 0 .. 255
     const int tok = row / p.GB, head = row - tok * p.GB;   // of this row in its tile
     uint32_t s_phase = 0, j_phase = 0;
-    bool ok = warp_wait(&sh.tk_done, 0u) && tk_ok;   // (the token phase used m and l)
+    bool ok = warp_wait(&sh.tm_ready, 0u) && warp_wait(&sh.tk_done, 0u) && tk_ok;   // (the token phase used m and l)
+    sm100::tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    const uint32_t s_addr = tmem + CH_TM_S + 128u * w + lane_base, o_addr = tmem + CH_TM_O + 128u * w + lane_base;
     // all softmax warps: shared memory and tensor memory of the others' last step may be used after it
     auto join = [&]() {
       __syncwarp();
@@ -1357,16 +1436,13 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
       ok = join();                             // every thread's partials come first
       if (!ok) break;
       if (st == 0) {
-        sh.prev = arrive_acq_rel(&p.cnt[g.first_cta]);
-        if (sh.prev == g.n_parts - 1) p.cnt[g.first_cta] = 0;
+        sh.prev = arrive_acq_rel(&p.cnt[g.first_run]);
+        if (sh.prev == g.n_parts - 1) p.cnt[g.first_run] = 0;
       }
       ok = join();
       if (!ok) break;
       if (sh.prev == g.n_parts - 1) {
-        // the last of the item's CTAs
-        const int n_rows = two ? 2 * CH_ROWS : min(CH_ROWS, g.tokens * p.GB);
-        if (n_rows >= CH_ROWS) merge_parts<D, 4>(p, g, n_rows, st);
-        else merge_parts<D, 1>(p, g, n_rows, st);
+        merge_parts<D>(p, g, st);              // the last of the item's CTAs
       }
     }
     if (!ok && lane == 0) give_up();
@@ -1375,7 +1451,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
   __syncthreads();
   if (warp == CH_MMA_WARP) {
     sm100::tc_fence_after();
-    sm100::tmem_dealloc(tmem, CH_TM_COLS);
+    sm100::tmem_dealloc(sh.tmem, CH_TM_COLS);
   }
 }
 
@@ -1404,7 +1480,7 @@ static size_t part_floats(int sm_count, int head_dim) {
 }
 size_t chunk_part_bytes(int sm_count, int head_dim) {
   return (part_floats(sm_count, head_dim) +
-          static_cast<size_t>(2) * sm_count * 8 * TK_ROWS * ((head_dim > 64 ? 128 : 64) + 2)) * sizeof(float);
+          static_cast<size_t>(2) * sm_count * TK_ROWS * ((head_dim > 64 ? 128 : 64) + 2)) * sizeof(float);
 }
 int chunk_counters(int sm_count) { return 2 * sm_count; }
 
@@ -1424,9 +1500,6 @@ cudaError_t launch_chunk_attn(eagle_ctx* ctx, int batch, const eagle_rows* rows,
   p.ld_o = ld_out;
   p.cap = kv->cap;
   p.window = window >= kv->cap ? 0 : window;   // a window of the whole cache is none
-  // eight kv heads side by side when there are as many, else each shared by 2, 4 or 8 warps
-  p.tk_wph = p.hkv >= 8 ? 1 : p.hkv >= 4 ? 2 : p.hkv >= 2 ? 4 : 8;
-  p.tk_parts = ceil_div(p.hkv, CH_SOFT_WARPS / p.tk_wph);
   p.len = kv->len;
   p.q = q;
   p.ld_q = ld_q;
@@ -1454,8 +1527,13 @@ cudaError_t launch_chunk_attn(eagle_ctx* ctx, int batch, const eagle_rows* rows,
   const cuuint32_t kb[4] = {64, 1, static_cast<cuuint32_t>(p.box), 1};
   const cuuint32_t tb[4] = {64, 1, static_cast<cuuint32_t>(std::min(p.box, 16)), 1};   // the token phase's steps
   CUtensorMap qm, km, vm, tkm, tvm;
-  if (!encode(ctx, &qm, q, 3, qd, qs, qb) || !encode(ctx, &km, kv->k, 4, kd, ks, kb) ||
-      !encode(ctx, &vm, kv->v, 4, kd, ks, kb) || !encode(ctx, &tkm, kv->k, 4, kd, ks, tb) ||
+  p.tensor = static_cast<long long>(rows->n_rows) * p.G > TK_ROWS;
+  std::memset(&qm, 0, sizeof(qm));
+  std::memset(&km, 0, sizeof(km));
+  std::memset(&vm, 0, sizeof(vm));
+  if ((p.tensor && (!encode(ctx, &qm, q, 3, qd, qs, qb) || !encode(ctx, &km, kv->k, 4, kd, ks, kb) ||
+                    !encode(ctx, &vm, kv->v, 4, kd, ks, kb))) ||
+      !encode(ctx, &tkm, kv->k, 4, kd, ks, tb) ||
       !encode(ctx, &tvm, kv->v, 4, kd, ks, tb))
     return cudaErrorInvalidValue;
   p.stamp = stamp_slot(ctx, EAGLE_K_CHUNK_ATTN);
