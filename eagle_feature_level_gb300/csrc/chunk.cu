@@ -86,6 +86,7 @@ struct ChunkParams {
   const uint16_t* k;
   const uint16_t* v;
   uint16_t* out;
+  int out32;                                 // 32-byte aligned rows of out
   int cap, window;
   const int32_t* len;
   PagedKv paged;
@@ -326,12 +327,16 @@ struct Runs {
   __device__ __forceinline__ void scan(const ChunkParams& p, int lane, bool report) {
     U = scan_batch<CLASS>(p, lane, report, s, items);
   }
-  // One run a worker; with fewer items than workers, the same number for every item, so that runs of equal items do not
-  // cross them (32 items of 8 units: 152 runs 16.2 us, 128 runs 10.3).  (Two or four runs a worker, claimed one after
-  // another, were slower: more partials.)
+  // One run a worker; with fewer items than workers, the same number for every item where that idles at most a fifth of
+  // them, so that runs of equal items do not cross them (32 items of 8 units: 152 runs 16.2 us, 128 runs 10.3; but 80
+  // items of 34 units: 80 runs 100 us, 152 runs 75).  (Two or four runs a worker, claimed one after another, were
+  // slower: more partials.)
   __device__ __forceinline__ void split(int workers) {
     n = workers;
-    if (items > 0 && items < workers) n = workers - workers % static_cast<int>(items);
+    if (items > 0 && items < workers) {
+      const int even = workers - workers % static_cast<int>(items);
+      if (5 * even >= 4 * workers) n = even;
+    }
     n = min(n, U);
   }
   __device__ __forceinline__ void begin(const ChunkParams& p, int lane, long long run) {
@@ -388,25 +393,32 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // This thread's row of one half of S_w (64 columns): P_w into tensor memory
-// over it, and the row sum.  Column j is visible when lo <= j <= hi (masked
-// steps), or all are.  The exponentials start at once, against the reference
-// of the steps before; only where the step's maximum passes that by CH_RAISE
-// (and in a row's first step) is it raised, O_w and the sum rescaled, and the
-// step done again.  `at_rest` waits until every product into O_w so far is
+// over it, and the row sum.  Column j is visible when j <= hi (masked & 1) and
+// j >= lo (masked & 2).  The exponentials start at once, against the reference
+// of the steps before (in a segment's first step, its own maximum); only where
+// the step's maximum passes that by CH_RAISE is it raised, O_w and the sum
+// rescaled, and the step done again.  `at_rest` waits until every product into O_w so far is
 // complete.
 template <int D, typename Wait>
-__device__ __forceinline__ bool softmax_step(uint32_t s_addr, uint32_t o_addr, bool masked, int lo, int hi, bool valid,
-                                             float c, float& m_ref, float& l_sum, uint64_t* p_full, Wait at_rest) {
+__device__ __forceinline__ bool softmax_step(uint32_t s_addr, uint32_t o_addr, bool first, int masked, int lo, int hi,
+                                             bool valid, float c, float& m_ref, float& l_sum, uint64_t* p_full,
+                                             Wait at_rest) {
   float sv[2][32];
   auto load = [&]() {
 #pragma unroll
     for (int k = 0; k < 2; ++k) sm100::tmem_ld32(s_addr + 32u * k, sv[k]);
     sm100::tmem_wait_ld();
-    if (__builtin_expect(masked, 0)) {
+    if (__builtin_expect(masked & 1, 0)) {
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int j = 0; j < 32; ++j) sv[k][j] = (32 * k + j >= lo && 32 * k + j <= hi) ? sv[k][j] : -INFINITY;
+        for (int j = 0; j < 32; ++j) sv[k][j] = 32 * k + j <= hi ? sv[k][j] : -INFINITY;
+    }
+    if (__builtin_expect(masked & 2, 0)) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) sv[k][j] = 32 * k + j >= lo ? sv[k][j] : -INFINITY;
     }
   };
   uint32_t pw[32];
@@ -435,8 +447,9 @@ __device__ __forceinline__ bool softmax_step(uint32_t s_addr, uint32_t o_addr, b
   const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
   const bool raise = valid && (mt > m_ref + CH_RAISE || (m_ref == -INFINITY && mt != -INFINITY));
   const bool any = __any_sync(0xffffffffu, raise);
+  if (first && raise) m_ref = mt;            // nothing summed yet
   exps();
-  if (__builtin_expect(any, 0)) {
+  if (__builtin_expect(any && !first, 0)) {
     const bool rescale = raise && m_ref != -INFINITY;
     if (__any_sync(0xffffffffu, rescale)) {
       if (!at_rest()) return false;
@@ -1334,11 +1347,11 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
           sm100::tc_fence_after();
           if (some) {
             const int k0 = (g.kt0 + t) * CH_KEYS + CH_STEP * h;
-            const bool masked = k0 + CH_STEP - 1 > pos_least || k0 < lo_most;
+            const int masked = (k0 + CH_STEP - 1 > pos_least ? 1 : 0) | (k0 < lo_most ? 2 : 0);
             // The products before this step are complete when the other half's next scores are, issued after them (in
             // the last step: the sign in their place); before the first step there are none.
             auto at_rest = [&]() { return warp_wait(&sh.s_full[w][h ^ 1], (h ? s_phase + 1 : s_phase) & 1); };
-            ok = softmax_step<D>(s_addr + 64u * h, o_addr, masked, lo - k0, pos - k0, valid, p.c, m_ref, l_sum,
+            ok = softmax_step<D>(s_addr + 64u * h, o_addr, t == t0 && h == 0, masked, lo - k0, pos - k0, valid, p.c, m_ref, l_sum,
                                  &sh.p_full[w][h], at_rest);
           } else if (lane == 0) {
             sm100::mbar_arrive(&sh.p_full[w][h]);
@@ -1404,15 +1417,23 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
           if (g.whole) {
             uint16_t* dst = p.out + (static_cast<size_t>(g.row0) + t_item) * p.ld_o + (g.head0 + head) * p.dh + cc;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              if (cc + 8 * q < p.dh) {
-                uint32_t x[4];
+            for (int q = 0; q < 2; ++q) {
+              if (cc + 16 * q < p.dh) {
+                uint32_t x[8];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const __nv_bfloat162 h = __floats2bfloat162_rn(o[8 * q + 2 * j] * inv, o[8 * q + 2 * j + 1] * inv);
+                for (int j = 0; j < 8; ++j) {
+                  const __nv_bfloat162 h = __floats2bfloat162_rn(o[16 * q + 2 * j] * inv, o[16 * q + 2 * j + 1] * inv);
                   x[j] = *reinterpret_cast<const uint32_t*>(&h);
                 }
-                *reinterpret_cast<uint4*>(dst + 8 * q) = make_uint4(x[0], x[1], x[2], x[3]);
+                if (p.out32) {
+                  // every thread's row is a line of its own: half as many passes as 16-byte stores
+                  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + 16 * q), "r"(x[0]),
+                               "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                               : "memory");
+                } else {
+                  *reinterpret_cast<uint4*>(dst + 16 * q) = make_uint4(x[0], x[1], x[2], x[3]);
+                  *reinterpret_cast<uint4*>(dst + 16 * q + 8) = make_uint4(x[4], x[5], x[6], x[7]);
+                }
               }
             }
           } else {
@@ -1498,6 +1519,7 @@ cudaError_t launch_chunk_attn(eagle_ctx* ctx, int batch, const eagle_rows* rows,
   p.nsub = ceil_div(p.G, p.GB);
   p.out = out;
   p.ld_o = ld_out;
+  p.out32 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0 && ld_out % 16 == 0;
   p.cap = kv->cap;
   p.window = window >= kv->cap ? 0 : window;   // a window of the whole cache is none
   p.len = kv->len;
