@@ -22,7 +22,8 @@ namespace {
 
 constexpr int AP_THREADS = 256;
 constexpr int AP_WARPS = AP_THREADS / 32;
-constexpr int AP_ROWS = AP_WARPS;            // rows of a CTA at most: a warp sets up each
+constexpr int AP_ROWS = 8;                  // rows of a CTA at most
+constexpr int AP_UNITS = 3;                  // units of a thread in flight
 
 struct AppendParams {
   PackedRows rows;
@@ -48,29 +49,9 @@ struct AppendParams {
   uint64_t turn[EAGLE_MAX_ROPE_PAIRS];
 };
 
-__device__ __forceinline__ void load8(const uint16_t* p, float (&x)[8]) {
-  const uint4 w = *reinterpret_cast<const uint4*>(p);
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16);
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-  }
-}
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), z = *reinterpret_cast<const float4*>(p + 4);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = z.x; x[5] = z.y; x[6] = z.z; x[7] = z.w;
-}
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
-  return f32_to_bf16(a) | (static_cast<uint32_t>(f32_to_bf16(b)) << 16);
-}
-__device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
-}
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ float load1(const uint16_t* p) { return bf16_to_f32(*p); }
 __device__ __forceinline__ float load1(const float* p) { return *p; }
@@ -86,45 +67,83 @@ __device__ __forceinline__ float2 turn_of(uint64_t turn, int pos, float mscale) 
   return make_float2(c * mscale, s * mscale);
 }
 
-// One unit of a head from `in` to `out`: elements [16 u, 16 u + 16) when they
-// pass through or interleave; for the split layout the pairs [8 u, 8 u + 8).
-// A and B are the unit's two runs of 8 elements.
-template <typename TI, typename TO>
-__device__ __forceinline__ void unit16(const AppendParams& p, const float2* cs, const TI* in, TO* out, int u) {
-  const bool turn = 16 * u < p.rot;
-  const bool split = turn && !p.interleaved;
-  const int a = split ? 8 * u : 16 * u, b = split ? p.rot / 2 + 8 * u : 16 * u + 8;
-  float x[8], y[8];
-  load8(in + a, x);
-  load8(in + b, y);
-  if (split) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 t = cs[8 * u + i];
-      const float x1 = x[i], x2 = y[i];
-      x[i] = x1 * t.x - x2 * t.y;
-      y[i] = x2 * t.x + x1 * t.y;
-    }
-  } else if (turn) {
+// Eight elements as they were loaded, turned in fp32 and rounded once when
+// stored; what passes through bf16 to bf16 is moved as it is.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<uint16_t> {
+  uint4 w;
+  __device__ __forceinline__ void load(const uint16_t* p) { w = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = w; }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 t = cs[8 * u + i], z = cs[8 * u + 4 + i];
-      const float x1 = x[2 * i], x2 = x[2 * i + 1], y1 = y[2 * i], y2 = y[2 * i + 1];
-      x[2 * i] = x1 * t.x - x2 * t.y;
-      x[2 * i + 1] = x2 * t.x + x1 * t.y;
-      y[2 * i] = y1 * z.x - y2 * z.y;
-      y[2 * i + 1] = y2 * z.x + y1 * z.y;
+      x[2 * i] = __uint_as_float(u[i] << 16);
+      x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
     }
   }
-  store8(out + a, x);
-  store8(out + b, y);
+  __device__ __forceinline__ void set(const float (&x)[8]) {
+    w = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+  }
+};
+template <>
+struct Raw<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(p + 4);
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    *reinterpret_cast<float4*>(p) = a;
+    *reinterpret_cast<float4*>(p + 4) = b;
+  }
+  __device__ __forceinline__ void store(uint16_t* p) const {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack2(a.x, a.y), pack2(a.z, a.w), pack2(b.x, b.y), pack2(b.z, b.w));
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+  __device__ __forceinline__ void set(const float (&x)[8]) {
+    a = make_float4(x[0], x[1], x[2], x[3]);
+    b = make_float4(x[4], x[5], x[6], x[7]);
+  }
+};
+
+// A unit's eight pairs: (x_i, y_i) in the split layout, neighbours otherwise.
+template <typename T>
+__device__ __forceinline__ void unit_turn(Raw<T>& rx, Raw<T>& ry, const float2 (&cs)[8], int interleaved) {
+  float x[8], y[8];
+  rx.get(x);
+  ry.get(y);
+  if (!interleaved) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float x1 = x[i], x2 = y[i];
+      x[i] = x1 * cs[i].x - x2 * cs[i].y;
+      y[i] = x2 * cs[i].x + x1 * cs[i].y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x1 = x[2 * i], x2 = x[2 * i + 1], y1 = y[2 * i], y2 = y[2 * i + 1];
+      x[2 * i] = x1 * cs[i].x - x2 * cs[i].y;
+      x[2 * i + 1] = x2 * cs[i].x + x1 * cs[i].y;
+      y[2 * i] = y1 * cs[4 + i].x - y2 * cs[4 + i].y;
+      y[2 * i + 1] = y2 * cs[4 + i].x + y1 * cs[4 + i].y;
+    }
+  }
+  rx.set(x);
+  ry.set(y);
 }
 
 // One pair (u < rot / 2) or two elements that pass through: for a rot_dim
 // that is no multiple of 16.
 template <typename TI, typename TO>
-__device__ __forceinline__ void unit2(const AppendParams& p, const float2* cs, const TI* in, TO* out, int u) {
-  const bool turn = 2 * u < p.rot;
+__device__ __forceinline__ void unit2(const AppendParams& p, const float2* cs, const TI* in, TO* out, int u,
+                                      bool turn) {
   const bool split = turn && !p.interleaved;
   const int a = split ? u : 2 * u, b = split ? p.rot / 2 + u : 2 * u + 1;
   float x = load1(in + a), y = load1(in + b);
@@ -141,7 +160,7 @@ __device__ __forceinline__ void unit2(const AppendParams& p, const float2* cs, c
 // T: element type of the rows (uint16_t: bf16 bits, or float); WIDE: units of
 // 16 elements (rot_dim a multiple of 16) or of 2.
 template <typename T, bool WIDE>
-__global__ void __launch_bounds__(AP_THREADS) append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(AP_THREADS, 3) append_kernel(const __grid_constant__ AppendParams p) {
   const LaunchStamp ls(p.stamp);
   __shared__ float2 s_cs[AP_ROWS][EAGLE_MAX_ROPE_PAIRS];
   __shared__ long long s_at[AP_ROWS];        // cache row, -1: not written
@@ -168,8 +187,8 @@ __global__ void __launch_bounds__(AP_THREADS) append_kernel(const __grid_constan
   }
   const int r0 = blockIdx.x * p.tile;
   const int rows = min(p.tile, p.rows.n_rows - r0);
-  if (warp < rows) {
-    const int r = r0 + warp;
+  for (int w = warp; w < rows; w += AP_WARPS) {
+    const int r = r0 + w;
     const int b = request_of_row(p.rows, r, lane);
     long long at = -1;
     int pos = 0;
@@ -182,9 +201,9 @@ __global__ void __launch_bounds__(AP_THREADS) append_kernel(const __grid_constan
         at = p.paged.table ? paged_row(p.paged, b, L + i) : static_cast<long long>(b) * p.cap + L + i;
     }
     if (lane == 0) {
-      s_at[warp] = at;
-      s_pos[warp] = pos;
-      s_any[warp] = b >= 0;
+      s_at[w] = at;
+      s_pos[w] = pos;
+      s_any[w] = b >= 0;
     }
   }
   __syncthreads();
@@ -194,10 +213,60 @@ __global__ void __launch_bounds__(AP_THREADS) append_kernel(const __grid_constan
     s_cs[r][j] = turn_of(p.turn[j], s_pos[r], p.mscale);
   }
   __syncthreads();
-  constexpr int W = WIDE ? 16 : 2;
-  const int upr = p.dh / W;                  // units of a head
   const int hq = p.q ? p.hq : 0;
-  const int units = (hq + 2 * p.hkv) * upr;
+  const int heads = hq + 2 * p.hkv;
+  if (WIDE) {
+    // A thread keeps one unit's place in a head, and a row's sines and cosines for it in registers, over the row's heads
+    // (dh / 16 is a power of two), AP_UNITS of them in flight.
+    const int upr = p.dh / 16, u = tid & (upr - 1), step = AP_THREADS / upr;
+    const bool in_rot = 16 * u < p.rot;
+    for (int r = 0; r < rows; ++r) {
+      if (!s_any[r]) continue;
+      float2 cs[8];
+      if (in_rot) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) cs[i] = s_cs[r][8 * u + i];
+      }
+      const size_t row = static_cast<size_t>(r0) + r;
+      const long long at = s_at[r];
+      for (int h0 = tid / upr; h0 < heads; h0 += AP_UNITS * step) {
+        Raw<T> x[AP_UNITS], y[AP_UNITS];
+#pragma unroll
+        for (int j = 0; j < AP_UNITS; ++j) {
+          const int h = h0 + j * step;
+          if (h >= heads || (h >= hq && at < 0)) continue;
+          const bool is_v = h >= hq + p.hkv;
+          const T* in = h < hq ? static_cast<const T*>(p.q) + row * p.ld_q + h * p.dh
+                               : is_v ? static_cast<const T*>(p.v) + row * p.ld_v + (h - hq - p.hkv) * p.dh
+                                      : static_cast<const T*>(p.k) + row * p.ld_k + (h - hq) * p.dh;
+          const bool split = !is_v && in_rot && !p.interleaved;
+          x[j].load(in + (split ? 8 * u : 16 * u));
+          y[j].load(in + (split ? p.rot / 2 + 8 * u : 16 * u + 8));
+        }
+#pragma unroll
+        for (int j = 0; j < AP_UNITS; ++j) {
+          const int h = h0 + j * step;
+          if (h >= heads || (h >= hq && at < 0)) continue;
+          const bool is_v = h >= hq + p.hkv, turn = !is_v && in_rot;
+          const bool split = turn && !p.interleaved;
+          const int a = split ? 8 * u : 16 * u, b = split ? p.rot / 2 + 8 * u : 16 * u + 8;
+          if (turn) unit_turn(x[j], y[j], cs, p.interleaved);
+          if (h < hq) {
+            T* out = static_cast<T*>(p.q_out) + row * p.ld_qo + h * p.dh;
+            x[j].store(out + a);
+            y[j].store(out + b);
+          } else {
+            uint16_t* out = is_v ? p.vc + (static_cast<size_t>(at) * p.hkv + (h - hq - p.hkv)) * p.dh
+                                 : p.kc + (static_cast<size_t>(at) * p.hkv + (h - hq)) * p.dh;
+            x[j].store(out + a);
+            y[j].store(out + b);
+          }
+        }
+      }
+    }
+    return;
+  }
+  const int upr = p.dh / 2, units = heads * upr;
   for (int r = 0; r < rows; ++r) {
     if (!s_any[r]) continue;
     const size_t row = static_cast<size_t>(r0) + r;
@@ -205,30 +274,13 @@ __global__ void __launch_bounds__(AP_THREADS) append_kernel(const __grid_constan
     for (int i = tid; i < units; i += AP_THREADS) {
       const int h = i / upr, u = i - h * upr;
       if (h < hq) {
-        const T* in = static_cast<const T*>(p.q) + row * p.ld_q + h * p.dh;
-        T* out = static_cast<T*>(p.q_out) + row * p.ld_qo + h * p.dh;
-        if (WIDE) unit16(p, s_cs[r], in, out, u);
-        else unit2(p, s_cs[r], in, out, u);
+        unit2(p, s_cs[r], static_cast<const T*>(p.q) + row * p.ld_q + h * p.dh,
+              static_cast<T*>(p.q_out) + row * p.ld_qo + h * p.dh, u, 2 * u < p.rot);
       } else if (at >= 0) {
         const bool is_v = h >= hq + p.hkv;
         const int hk = h - hq - (is_v ? p.hkv : 0);
-        const T* in = static_cast<const T*>(is_v ? p.v : p.k) + row * (is_v ? p.ld_v : p.ld_k) + hk * p.dh;
-        uint16_t* out = (is_v ? p.vc : p.kc) + (static_cast<size_t>(at) * p.hkv + hk) * p.dh;
-        if (is_v) {
-          if (WIDE) {
-            float x[8], y[8];
-            load8(in + 16 * u, x);
-            load8(in + 16 * u + 8, y);
-            store8(out + 16 * u, x);
-            store8(out + 16 * u + 8, y);
-          } else {
-            store1(out + 2 * u, load1(in + 2 * u));
-            store1(out + 2 * u + 1, load1(in + 2 * u + 1));
-          }
-        } else {
-          if (WIDE) unit16(p, s_cs[r], in, out, u);
-          else unit2(p, s_cs[r], in, out, u);
-        }
+        unit2(p, s_cs[r], static_cast<const T*>(is_v ? p.v : p.k) + row * (is_v ? p.ld_v : p.ld_k) + hk * p.dh,
+              (is_v ? p.vc : p.kc) + (static_cast<size_t>(at) * p.hkv + hk) * p.dh, u, !is_v && 2 * u < p.rot);
       }
     }
   }
