@@ -74,6 +74,16 @@ __device__ __forceinline__ T block_scan(T v, T* s_warp, T& total) {
   return before + x - v;
 }
 
+// The counts of blocks b .. b + 3 (b a multiple of 4), 0 past the last block.
+__device__ __forceinline__ int4 counts4(const PagesParams& p, int b) {
+  if (b + 4 <= p.n_blocks) return *reinterpret_cast<const int4*>(p.ref + b);
+  int4 c = make_int4(0, 0, 0, 0);
+  if (b < p.n_blocks) c.x = p.ref[b];
+  if (b + 1 < p.n_blocks) c.y = p.ref[b + 1];
+  if (b + 2 < p.n_blocks) c.z = p.ref[b + 2];
+  return c;
+}
+
 // ---- fork -------------------------------------------------------------------
 
 // One CTA per (pair, run of columns).  A pair's standing -- in range, its
@@ -244,10 +254,12 @@ __global__ void __launch_bounds__(PLAN_THREADS) reserve_kernel(const PagesParams
   int found = 0;
   for (int b0 = 0; fits && found < need && b0 < p.n_blocks; b0 += 4 * PLAN_THREADS) {
     const int b = b0 + 4 * tid;
+    const int4 c = counts4(p, b);
+    const int count[4] = {c.x, c.y, c.z, c.w};
     int free[4], n = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      free[i] = b + i < p.n_blocks && p.ref[b + i] == 0;
+      free[i] = b + i < p.n_blocks && count[i] == 0;
       n += free[i];
     }
     int total;
@@ -297,7 +309,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) reserve_kernel(const PagesParams
 // ---- compact: the plan --------------------------------------------------------
 
 // scratch: the moving blocks by rank, from n_blocks / 2 on their places, and
-// from n_blocks on where each id goes (every id from the live count on).
+// from n_blocks on the rank of each id from the live count on (-1: not live).
 __global__ void __launch_bounds__(PLAN_THREADS) compact_kernel(const PagesParams p) {
   const LaunchStamp ls(p.stamp);
   __shared__ int s_warp[32];
@@ -306,32 +318,43 @@ __global__ void __launch_bounds__(PLAN_THREADS) compact_kernel(const PagesParams
   pdl_trigger();
   const int tid = threadIdx.x;
   int live = 0;
-  for (int b = tid; b < p.n_blocks; b += PLAN_THREADS) live += p.ref[b] > 0;
+  for (int b = 4 * tid; b < p.n_blocks; b += 4 * PLAN_THREADS) {
+    const int4 c = counts4(p, b);
+    live += (c.x > 0) + (c.y > 0) + (c.z > 0) + (c.w > 0);
+  }
   int used;
   block_scan(live, s_warp, used);
   int* src = p.scratch;
   int* dst = p.scratch + p.n_blocks / 2;
   int* to = p.scratch + p.n_blocks;
   int movers = 0, holes = 0;
-  for (int b0 = 0; b0 < p.n_blocks; b0 += PLAN_THREADS) {
-    const int b = b0 + tid;
-    const bool in = b < p.n_blocks;
-    const bool lv = in && p.ref[b] > 0;
-    const bool mover = lv && b >= used, hole = in && !lv && b < used;
+  for (int b0 = 0; b0 < p.n_blocks; b0 += 4 * PLAN_THREADS) {
+    const int b = b0 + 4 * tid;
+    const int4 c = counts4(p, b);
+    const int count[4] = {c.x, c.y, c.z, c.w};
+    int n = 0;                               // of these four ids: movers, and holes 16 bits up
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (b + i < p.n_blocks) n += count[i] > 0 ? (b + i >= used ? 1 : 0) : (b + i < used ? 1 << 16 : 0);
     int total;
-    // a run of ids lies on one side of `used` except for the run that holds it
-    const int packed = block_scan((mover ? 1 : 0) + (hole ? 1 << 16 : 0), s_warp, total);
-    if (mover) src[movers + (packed & 0xffff)] = b;
-    if (hole) dst[holes + (packed >> 16)] = b;
-    if (in && b >= used) to[b] = b;
+    int at = block_scan(n, s_warp, total);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (b + i < p.n_blocks) {
+        if (b + i >= used) {
+          const int rank = movers + (at & 0xffff);
+          to[b + i] = count[i] > 0 ? rank : -1;
+          if (count[i] > 0) {
+            src[rank] = b + i;
+            ++at;
+          }
+        } else if (count[i] <= 0) {
+          dst[holes + (at >> 16)] = b + i;
+          at += 1 << 16;
+        }
+      }
     movers += total & 0xffff;
     holes += total >> 16;
-  }
-  __syncthreads();
-  for (int i = tid; i < movers; i += PLAN_THREADS) {
-    to[src[i]] = dst[i];
-    p.ref[dst[i]] = p.ref[src[i]];
-    p.ref[src[i]] = 0;
   }
   if (tid == 0) {
     *p.l.n_copies = movers;
@@ -351,7 +374,7 @@ struct CopyParams {
   long long block_elems;   // of one pool: rows x heads x head_dim
   int row_elems;
   int chunks;              // CP_CHUNK pieces of a block
-  int move;                // rewrite the tables too (compact)
+  int move;                // the tables and counts follow (compact)
   uint16_t* k[EAGLE_MAX_LAYERS];
   uint16_t* v[EAGLE_MAX_LAYERS];
 };
@@ -364,12 +387,16 @@ __global__ void __launch_bounds__(CP_THREADS) copy_kernel(const __grid_constant_
   const int tid = threadIdx.x;
   if (p.move) {
     const int used = p.n_copies[1];
-    const int32_t* to = p.pg.scratch + p.pg.n_blocks;
+    const int32_t* rank = p.pg.scratch + p.pg.n_blocks;
     const long long entries = static_cast<long long>(p.pg.n_seqs) * p.pg.per;
     for (long long i = static_cast<long long>(blockIdx.x) * CP_THREADS + tid; i < entries;
          i += static_cast<long long>(gridDim.x) * CP_THREADS) {
       const int blk = p.pg.table[i];
-      if (blk >= used && blk < p.pg.n_blocks) p.pg.table[i] = to[blk];
+      if (blk >= used && blk < p.pg.n_blocks && rank[blk] >= 0) p.pg.table[i] = p.dst[rank[blk]];
+    }
+    for (int i = blockIdx.x * CP_THREADS + tid; i < *p.n_copies; i += gridDim.x * CP_THREADS) {
+      p.pg.ref[p.dst[i]] = p.pg.ref[p.src[i]];
+      p.pg.ref[p.src[i]] = 0;
     }
   }
   const long long per_copy = static_cast<long long>(p.n_layers) * 2 * p.chunks;
