@@ -42,12 +42,13 @@ __device__ __forceinline__ int request_of_row(const PackedRows& r, int row, int 
 }
 
 // Whether a cache takes n more rows of request b at length L: within cap and,
-// when paged, in allocated blocks (every lane of a warp calls it; the result
-// is the same in all).
+// when paged, in allocated blocks; none, whatever the length (every lane of a
+// warp calls it; the result is the same in all).
 __device__ __forceinline__ bool cache_takes(const PagedKv& pg, int cap, int b, int L, int n, int lane) {
+  if (n == 0) return true;
   if (L < 0 || static_cast<long long>(L) + n > cap) return false;
   bool ok = true;
-  if (pg.table && n > 0) {
+  if (pg.table) {
     const int last = (L + n - 1) >> pg.shift;
     for (int c = (L >> pg.shift) + lane; c <= last; c += 32) {
       const int blk = pg.table[static_cast<size_t>(b) * pg.per_req + c];

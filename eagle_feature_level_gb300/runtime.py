@@ -364,32 +364,40 @@ class PagedCache:
     def _ws(self):
         return self.eng.ws.data_ptr(), self.eng.stream()
 
+    def _ints(self, t: torch.Tensor, n: int) -> int:
+        """Address of n int32 on the cache's device."""
+        if t.dtype != torch.int32 or t.device != self.table.device or t.numel() != n or not t.is_contiguous():
+            raise ValueError(f"needs {n} contiguous int32 on {self.table.device}")
+        return _p(t)
+
     # ---- pages ----------------------------------------------------------------
     def clear(self):
         B.eagle_pages_init(self.eng.ctx, self.pages_c, *self._ws())
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor):
         """Sequences dst share the rows of sequences src (int32, device)."""
-        B.eagle_pages_fork(self.eng.ctx, self.pages_c, src.numel(), _p(src), _p(dst), *self._ws())
+        n = src.numel()
+        B.eagle_pages_fork(self.eng.ctx, self.pages_c, n, self._ints(src, n), self._ints(dst, n), *self._ws())
 
     def reserve(self, n_new: torch.Tensor):
         """Room for n_new[s] more rows of every sequence (int32, device)."""
-        B.eagle_pages_reserve(self.eng.ctx, self.pages_c, self.pools_c, _p(n_new), *self._ws())
+        B.eagle_pages_reserve(self.eng.ctx, self.pages_c, self.pools_c, self._ints(n_new, self.n_seqs),
+                              *self._ws())
 
     def release(self, keep: torch.Tensor):
         """Cuts sequence s to its first keep[s] rows (int32, device; < 0: left alone)."""
-        B.eagle_pages_release(self.eng.ctx, self.pages_c, _p(keep), *self._ws())
+        B.eagle_pages_release(self.eng.ctx, self.pages_c, self._ints(keep, self.n_seqs), *self._ws())
 
     def compact(self):
         B.eagle_pages_compact(self.eng.ctx, self.pages_c, self.pools_c, *self._ws())
 
     # ---- rows -----------------------------------------------------------------
-    @staticmethod
-    def _packed(t: torch.Tensor):
+    def _packed(self, t: torch.Tensor, n: int, heads: str):
         """Address and pitch of packed rows [n][H][dh] whose heads are contiguous (a slice of a fused projection
         has a larger pitch)."""
-        if t.dim() != 3 or t.stride(2) != 1 or t.stride(1) != t.shape[2]:
-            raise ValueError("packed rows are [n][heads][head_dim] with contiguous heads")
+        H, dh = self.eng.dims[heads], self.eng.dims["head_dim"]
+        if t.shape != (n, H, dh) or t.stride(2) != 1 or t.stride(1) != dh or t.device != self.table.device:
+            raise ValueError(f"packed rows are [{n}][{H}][{dh}] with contiguous heads on {self.table.device}")
         return _p(t), t.stride(0)
 
     def append(self, layer: int, row_start: torch.Tensor, rope: Optional[B.eagle_rope], q: Optional[torch.Tensor],
@@ -397,30 +405,32 @@ class PagedCache:
                pos: Optional[torch.Tensor] = None):
         """Rotates q (into q_out, default q itself) and k of the new rows and appends k, v behind the sequences'
         rows in `layer`; len_next counts them."""
+        if q is None and q_out is not None:
+            raise ValueError("q_out without q")
         if q is not None and q_out is None:
             q_out = q
-        dtype = B.DTYPE_F32 if k.dtype == torch.float32 else B.DTYPE_BF16
+        if k.dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError("rows are bf16 or fp32")
         for t in (q, v, q_out):
             if t is not None and t.dtype != k.dtype:
                 raise ValueError("q, k, v and q_out have one type")
-        if k.dtype not in (torch.float32, torch.bfloat16):
-            raise ValueError("rows are bf16 or fp32")
-        none = (0, 0)
-        B.eagle_kv_append(self.eng.ctx, self.n_seqs, B.eagle_rows(_p(row_start), k.shape[0]), rope, dtype,
-                          *(self._packed(q) if q is not None else none),
-                          *(self._packed(q_out) if q is not None else none), *self._packed(k), *self._packed(v),
-                          self._kv[layer], _p(pos), _p(self.len_next), *self._ws())
+        n = k.shape[0]
+        qs = (*self._packed(q, n, "n_q_heads"), *self._packed(q_out, n, "n_q_heads")) if q is not None else (0, 0, 0, 0)
+        B.eagle_kv_append(self.eng.ctx, self.n_seqs, B.eagle_rows(self._ints(row_start, self.n_seqs + 1), n), rope,
+                          B.DTYPE_F32 if k.dtype == torch.float32 else B.DTYPE_BF16, *qs,
+                          *self._packed(k, n, "n_kv_heads"), *self._packed(v, n, "n_kv_heads"), self._kv[layer],
+                          None if pos is None else self._ints(pos, n), _p(self.len_next), *self._ws())
 
     def attend(self, layer: int, row_start: torch.Tensor, q: torch.Tensor, out: torch.Tensor, window: int = 0,
                scale: Optional[float] = None):
         """Causal attention of the appended rows (bf16 q, out) over `layer`'s rows up to len_next."""
         if q.dtype != torch.bfloat16 or out.dtype != torch.bfloat16:
             raise ValueError("q and out are bf16")
-        qp, ldq = self._packed(q)
-        op, ldo = self._packed(out)
-        B.eagle_chunk_attn(self.eng.ctx, self.n_seqs, B.eagle_rows(_p(row_start), q.shape[0]), qp, ldq,
-                           self._kv_next[layer], window, scale or 1.0 / math.sqrt(self.eng.dims["head_dim"]), op, ldo,
-                           *self._ws())
+        n = q.shape[0]
+        B.eagle_chunk_attn(self.eng.ctx, self.n_seqs, B.eagle_rows(self._ints(row_start, self.n_seqs + 1), n),
+                           *self._packed(q, n, "n_q_heads"), self._kv_next[layer], window,
+                           1.0 / math.sqrt(self.eng.dims["head_dim"]) if scale is None else scale,
+                           *self._packed(out, n, "n_q_heads"), *self._ws())
 
     def advance(self):
         """The appended rows become the sequences' own."""

@@ -593,8 +593,9 @@ eagle_status eagle_rope_plan(eagle_rope* out, int head_dim, int rot_dim, int int
  * (a contiguous cache of as many rows per request).  A request whose cache
  * cannot take all its rows (beyond kv.cap, or in unallocated blocks) writes
  * none of them and keeps its length (EAGLE_ERR_CAPACITY in the status word);
- * its q rows are rotated all the same.  len_out must not alias kv.len
- * (EAGLE_ERR_INVALID_ARG).  Rows a block table maps to the same place -- a
+ * its q rows are rotated all the same.  A request without rows keeps its
+ * length, whatever that is (a padded batch's idle entries).  len_out must not
+ * alias kv.len (EAGLE_ERR_INVALID_ARG).  Rows a block table maps to the same place -- a
  * block that two requests hold -- must be made private first
  * (eagle_pages_reserve). */
 eagle_status eagle_kv_append(eagle_ctx* ctx, int batch, const eagle_rows* rows, const eagle_rope* rope, int dtype,
@@ -626,7 +627,9 @@ eagle_status eagle_chunk_attn(eagle_ctx* ctx, int batch, const eagle_rows* rows,
  * reserved ahead -- and ref counts, for every block, the table entries that
  * map it.  A block is free when its count is 0; there is no other allocator
  * state, and the calls below always take the lowest free ids first, so equal
- * states give equal tables.  block_table is what eagle_paging takes, with
+ * states give equal tables.  A length goes up by rows appended to reserved
+ * blocks and down by eagle_pages_release (which gives up what a shorter
+ * sequence may share with others).  block_table is what eagle_paging takes, with
  * kv.cap = per_seq * block_size and the sequences as the batch. */
 typedef struct {
   int32_t* block_table;  /* [n_seqs][per_seq]; < 0: none */

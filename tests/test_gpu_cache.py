@@ -452,6 +452,125 @@ def test_attention_two_streams():
         engs[i].close()
 
 
+@pytest.mark.parametrize("heads", [(24, 1, 64), (17, 1, 128), (144, 1, 64), (300, 1, 64)],
+                         ids=lambda h: "x".join(map(str, h)))
+def test_attention_many_heads_a_group(heads):
+    """More query heads a kv head than the few-row tile has rows, and than a tensor-core tile has."""
+    attention_case(heads, 16, [1, 130, 300], [1, 3, 1], seed=30)
+    attention_case(heads, 0, [260, 40], [37, 0], window=50, seed=31)
+
+
+@pytest.mark.parametrize("heads", [(8, 2, 128), (4, 2, 64)], ids=["dh128", "dh64"])
+def test_attention_small_contiguous_caches(heads):
+    """Caches shorter than a tile of keys."""
+    attention_case(heads, 0, [1], [1], seed=32)
+    attention_case(heads, 0, [3, 2], [3, 1], seed=33)
+    attention_case(heads, 0, [5, 9, 30], [5, 9, 30], seed=34, cap=30)
+
+
+def test_attention_hundreds_of_requests():
+    rng = random.Random(5)
+    eng = R.Engine(dict(d=256, n_q_heads=4, n_kv_heads=2, head_dim=64, d_ff=64, vocab=64), max_batch=301, max_rows=8,
+                   max_expanded=1, max_children=1, max_tree=2, max_prefix=512, device="cuda")
+    lens = [rng.choice([1, 2, 20, 130, 257]) for _ in range(301)]
+    new = [rng.choice([0, 1, 1, 1, min(n, 3), n]) for n in lens]
+    attention_case((4, 2, 64), 16, lens, new, seed=35, eng=eng)
+    attention_case((4, 2, 64), 0, lens, [1] * 301, seed=36, eng=eng)
+    eng.close()
+
+
+def test_idle_requests_may_hold_any_length():
+    """A padded batch: the length of a request without rows is neither used nor reported."""
+    heads = hq, hkv, dh = 8, 2, 128
+    eng = engine(*heads)
+    for bs in (0, 16):
+        c = Cache([6, 0, 40, 0], [12, 12, 41, 12], hkv, dh, bs, seed=37)
+        c.len.copy_(i32([6, -9, 40, 10 ** 9]))
+        x = torch.randn(4, hq + 2 * hkv, dh, device="cuda").to(torch.bfloat16)
+        out = torch.zeros(4, hq, dh, dtype=torch.bfloat16, device="cuda")
+        rs = i32([0, 3, 3, 4, 4])
+        ln = run_append(eng, c, rs, 4, None, x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], x[:, :hq])
+        attend(eng, c, rs, x[:, :hq], out, kv=c.kv(ln))
+        torch.cuda.synchronize()
+        assert eng.status() == 0 and ln.tolist() == [9, -9, 41, 10 ** 9]
+        for b, lo, hi in ((0, 0, 3), (2, 3, 4)):
+            k, v = (np.concatenate([f64(c.rows[b][i]), f64(x[lo:hi, hq + i * hkv:hq + (i + 1) * hkv])]) for i in (0, 1))
+            check_attention(f64(out[lo:hi]), f64(x[lo:hi, :hq]), k, v, 1 / math.sqrt(dh), 0)
+
+
+def test_blocks_beyond_32_bit_offsets():
+    """Pools of more than 2^32 elements: append, attention, the copy of a shared tail and compaction at their end."""
+    hq, hkv, dh, bs = 8, 2, 128, 256
+    eng = engine(hq, hkv, dh)
+    n_blocks = (1 << 32) // (bs * hkv * dh) + 20
+    c = R.PagedCache.__new__(R.PagedCache)
+    zeros, torch.zeros = torch.zeros, lambda *s, **k: torch.empty(*s, **k)     # (the pools need no contents)
+    try:
+        c.__init__(eng, 2, bs, n_blocks, 4)
+    finally:
+        torch.zeros = zeros
+    c.clear()
+    last = n_blocks - 1
+    c.table[0, 0], c.ref[last], c.ref[:last - 3] = last, 1, 1                   # the free blocks are last - 3 .. last - 1
+    x = torch.randn(300, hq + 2 * hkv, dh, device="cuda").to(torch.bfloat16)
+    q, k, v = x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:]
+    out = torch.zeros(300, hq, dh, dtype=torch.bfloat16, device="cuda")
+
+    def step(new):
+        rs = i32(starts(new))
+        c.reserve(i32(new))
+        c.append(0, rs, None, q, k, v)
+        c.attend(0, rs, q, out)
+        c.advance()
+        torch.cuda.synchronize()
+        assert eng.status() == 0
+
+    def check(row0, n, rows):
+        kk, vv = (np.concatenate([f64(t[a:z]) for a, z in rows]) for t in (k, v))
+        check_attention(f64(out[row0:row0 + n]), f64(q[row0:row0 + n]), kk, vv, 1 / math.sqrt(dh), 0)
+
+    step([200, 0])
+    check(0, 200, [(0, 200)])
+    c.fork(i32([0]), i32([1]))
+    step([1, 100])                                         # sequence 0 gets a copy of the tail, 1 keeps the block
+    assert c.table[:, 0].tolist() == [last - 3, last] and c.table[1, 1] == last - 2
+    check(0, 1, [(0, 200), (0, 1)])
+    check(1, 100, [(0, 200), (1, 101)])
+    c.ref[:last - 3] = 0
+    before = [t[i].clone() for t in (c.k[0], c.v[0]) for i in (last - 3, last - 2, last)]
+    c.compact()
+    torch.cuda.synchronize()
+    assert eng.status() == 0
+    assert c.table[:, :2].tolist() == [[0, -1], [2, 1]] and c.ref[:4].tolist() == [1, 1, 1, 0]
+    for t, w in zip([t[i] for t in (c.k[0], c.v[0]) for i in range(3)], before):
+        assert torch.equal(t.view(torch.int16), w.view(torch.int16))
+
+
+def test_two_graphs_on_one_workspace():
+    """Captured calls of different batches share the partials and counters of one workspace, replayed in turn."""
+    heads = (8, 2, 128)
+    eng = engine(*heads, fresh=True)
+    work = []
+    for i, (lens, new) in enumerate([([3000, 700], [1, 300]), ([900, 90, 2000, 5], [1, 1, 1, 1]), ([1500], [1500])]):
+        c = Cache(lens, lens, 2, 128, 16, seed=40 + i)
+        q = torch.randn(sum(new), 8, 128, device="cuda").to(torch.bfloat16)
+        rs, o = i32(starts(new)), torch.empty_like(q)
+        attend(eng, c, rs, q, o)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        again = torch.zeros_like(o)
+        with torch.cuda.graph(g):
+            attend(eng, c, rs, q, again)
+        work.append((c, q, rs, o, again, g))
+    for i in (0, 1, 2, 2, 0, 1, 0, 2, 1):
+        work[i][5].replay()
+    torch.cuda.synchronize()
+    assert eng.status() == 0
+    for c, q, rs, o, again, g in work:
+        assert torch.equal(o, again)
+    eng.close()
+
+
 # ---- refusals before any launch ---------------------------------------------------
 
 def test_arguments_checked_before_launch():

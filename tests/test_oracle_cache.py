@@ -185,3 +185,48 @@ def test_calls_refuse_a_missing_context(binding):
         with pytest.raises(B.EagleError) as e:
             call()
         assert e.value.name == "EAGLE_ERR_INVALID_ARG"
+
+
+def test_paged_cache_checks_its_tensors(monkeypatch):
+    """What PagedCache refuses before it calls the library: types, counts, shapes, strides, devices."""
+    import torch
+    from eagle_feature_level_gb300 import _binding as B
+    from eagle_feature_level_gb300 import runtime as R
+    calls = []
+    for name in ("eagle_kv_append", "eagle_chunk_attn", "eagle_pages_fork", "eagle_pages_reserve", "eagle_pages_release"):
+        monkeypatch.setattr(B, name, lambda *a, name=name: calls.append(name))
+    eng = R.Engine.__new__(R.Engine)
+    eng.ctx, eng.device, eng.dims = None, torch.device("cpu"), dict(n_q_heads=4, n_kv_heads=2, head_dim=64)
+    eng.ws, eng.stream = torch.empty(0), lambda: 0
+    eng.close = lambda: None
+    c = R.PagedCache(eng, 3, 16, 8, 4)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32)
+    rs, b = i32(0, 1, 1, 5), torch.bfloat16
+    x = torch.zeros(5, 8, 64, dtype=b)
+    q, k, v = x[:, :4], x[:, 4:6], x[:, 6:]
+    out = torch.zeros(5, 4, 64, dtype=b)
+    c.append(0, rs, None, q, k, v, pos=i32(0, 1, 2, 3, 4))
+    c.append(0, rs, None, None, k, v)
+    c.attend(0, rs, q, out)
+    c.fork(i32(0, 1), i32(2, 3))
+    c.reserve(i32(0, 1, 2))
+    c.release(i32(-1, 1, 2))
+    assert len(calls) == 6
+    refused = [
+        lambda: c.append(0, i32(0, 1, 5), None, q, k, v), lambda: c.append(0, rs.long(), None, q, k, v),
+        lambda: c.append(0, rs.repeat(2)[::2], None, q, k, v), lambda: c.append(0, rs.to("meta"), None, q, k, v),
+        lambda: c.append(0, rs, None, q[:4], k, v), lambda: c.append(0, rs, None, q, k, v[:4]),
+        lambda: c.append(0, rs, None, k, k, v), lambda: c.append(0, rs, None, q, k, v, q_out=out[:3]),
+        lambda: c.append(0, rs, None, q.float(), k, v), lambda: c.append(0, rs, None, q.half(), k.half(), v.half()),
+        lambda: c.append(0, rs, None, None, k, v, q_out=out), lambda: c.append(0, rs, None, q, k, v, pos=i32(1, 2)),
+        lambda: c.append(0, rs, None, q, k, x[:, 1::4]), lambda: c.append(0, rs, None, q, k, v.to("meta")),
+        lambda: c.attend(0, rs, q, out[:4]), lambda: c.attend(0, rs, q, out.float()),
+        lambda: c.attend(0, rs, q.reshape(5, 2, 128), out), lambda: c.attend(0, rs[:3], q, out),
+        lambda: c.fork(i32(0, 1), i32(2)), lambda: c.fork(i32(0).long(), i32(2)), lambda: c.reserve(i32(1, 1)),
+        lambda: c.reserve(torch.zeros(3)), lambda: c.release(i32(1, 1, 1, 1)),
+    ]
+    for i, call in enumerate(refused):
+        with pytest.raises(ValueError):
+            call()
+            raise AssertionError(i)
+    assert len(calls) == 6
