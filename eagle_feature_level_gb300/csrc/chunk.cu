@@ -59,6 +59,8 @@ constexpr int CH_ROWS = 128;                 // query rows per tile
 constexpr uint32_t CH_HALF = CH_KEYS * 128;  // bytes of 128 rows x 64 elements
 constexpr int CH_SEGS = 4;                   // segments the scheduler runs ahead
 constexpr float CH_RAISE = 8.0f;
+constexpr int CH_HEAD = 2, CH_SNAP = 1;      // units of an item before its tiles'; tiles of its ends that no boundary cuts off
+constexpr int CH_FOLD = 8;                   // units of a worker from which the token phase pays
 // the token phase: requests of at most TK_ROWS query rows a kv head
 constexpr int TK_ROWS = 16;
 template <int SLOTS>
@@ -140,7 +142,7 @@ static_assert(chunk_smem<128>() <= (227u << 10) && chunk_smem<64>() <= (227u << 
 
 struct Request {
   int row0, n, len, per, items;              // tokens per item, items per kv head part
-  bool bad, over;
+  bool bad, over, other;                     // other: rows, but of the other class
 };
 
 // Requests of few rows (a decoding step's) are taken by the token phase, the
@@ -157,8 +159,15 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 template <int CLASS>
 __device__ __forceinline__ int parts_of(const ChunkParams& p) { return CLASS == TOKEN ? p.hkv : p.hkv * p.nsub; }
 
+// In units of a tile of 128 keys, what an item costs beside its tiles (its
+// queries, its output, the empty pipeline at its ends): the first units of an item.
 template <int CLASS>
-__device__ __forceinline__ Request request_of(const ChunkParams& p, int b) {
+constexpr int HEAD = CLASS == TOKEN ? 0 : CH_HEAD;
+template <int CLASS>
+constexpr int SNAP = CLASS == TOKEN ? 0 : CH_SNAP;
+
+template <int CLASS>
+__device__ __forceinline__ Request request_of(const ChunkParams& p, int b, bool fold) {
   Request r;
   int lo, hi;
   r.bad = !request_rows(p.rows, b, lo, hi);
@@ -167,7 +176,8 @@ __device__ __forceinline__ Request request_of(const ChunkParams& p, int b) {
   r.len = max(0, min(L, p.cap));
   r.row0 = lo;
   r.n = hi - lo;
-  const bool token = static_cast<long long>(r.n) * p.G <= TK_ROWS;
+  const bool token = !fold && static_cast<long long>(r.n) * p.G <= TK_ROWS;
+  r.other = token != (CLASS == TOKEN) && r.n > 0;
   if (token != (CLASS == TOKEN)) r.n = 0;
   r.per = CLASS == TOKEN ? max(r.n, 1) : r.n <= p.T ? p.T : 2 * p.T;
   r.items = (r.n + r.per - 1) / r.per;
@@ -189,25 +199,27 @@ __device__ __forceinline__ void item_tiles(const ChunkParams& p, const Request& 
   kt0 = lo / CH_KEYS;
   kt1 = end > lo ? (end - 1) / CH_KEYS + 1 : kt0;
 }
+template <int CLASS>
 __device__ __forceinline__ int item_units(const ChunkParams& p, const Request& r, int q) {
   int a, z;
   item_tiles(p, r, q, a, z);
-  return max(1, z - a);
+  return max(1, z - a) + HEAD<CLASS>;
 }
 
 // Units of one kv head part of the lane's own request (every lane calls it;
 // requests of many items are summed by the whole warp).
+template <int CLASS>
 __device__ __forceinline__ long long request_units(const ChunkParams& p, const Request& r, int lane) {
   constexpr int ALONE = 4;
   long long w = 0;
   if (r.items <= ALONE)
-    for (int q = 0; q < r.items; ++q) w += item_units(p, r, q);
+    for (int q = 0; q < r.items; ++q) w += item_units<CLASS>(p, r, q);
   for (unsigned todo = __ballot_sync(0xffffffffu, r.items > ALONE); todo; todo &= todo - 1) {
     const int l = __ffs(todo) - 1;
     Request s;
     take_from(s, r, l);
     long long part = 0;
-    for (int q = lane; q < s.items; q += 32) part += item_units(p, s, q);
+    for (int q = lane; q < s.items; q += 32) part += item_units<CLASS>(p, s, q);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
     if (lane == l) w = part;
@@ -229,20 +241,22 @@ struct Scan {
   long long units, end;    // its units per kv head part, and the sum up to its end
 };
 template <int CLASS>
-__device__ __forceinline__ void scan_32(const ChunkParams& p, int lane, int b0, long long before, Scan& s) {
+__device__ __forceinline__ void scan_32(const ChunkParams& p, int lane, bool fold, int b0, long long before, Scan& s) {
   s.r = Request{};
   s.r.per = 1;
-  if (b0 + lane < p.rows.B) s.r = request_of<CLASS>(p, b0 + lane);
-  s.units = request_units(p, s.r, lane);
+  if (b0 + lane < p.rows.B) s.r = request_of<CLASS>(p, b0 + lane, fold);
+  s.units = request_units<CLASS>(p, s.r, lane);
   s.end = before + warp_scan(s.units * parts_of<CLASS>(p), lane);
 }
 template <int CLASS>
-__device__ __forceinline__ long long scan_batch(const ChunkParams& p, int lane, bool report, Scan& s,
-                                                long long& items) {
+__device__ __forceinline__ long long scan_batch(const ChunkParams& p, int lane, bool fold, bool report, Scan& s,
+                                                long long& items, bool& others) {
   long long sum = 0;
   items = 0;
+  others = false;
   for (int b0 = 0; b0 < p.rows.B; b0 += 32) {
-    scan_32<CLASS>(p, lane, b0, sum, s);
+    scan_32<CLASS>(p, lane, fold, b0, sum, s);
+    others = others || __any_sync(0xffffffffu, s.r.other);
     if (report && s.r.bad) set_status(p.status, EAGLE_ERR_INVALID_ARG);
     if (report && s.r.over) set_status(p.status, EAGLE_ERR_CAPACITY);
     items += static_cast<long long>(s.r.items) * parts_of<CLASS>(p);
@@ -263,11 +277,11 @@ struct Walk {
 
 // The item that holds unit u0; s is what scan_batch left.
 template <int CLASS>
-__device__ __forceinline__ void walk_to(const ChunkParams& p, int lane, long long u0, Scan& s, Walk& w) {
+__device__ __forceinline__ void walk_to(const ChunkParams& p, int lane, bool fold, long long u0, Scan& s, Walk& w) {
   const int parts = parts_of<CLASS>(p);
   long long sum = 0;
   for (int b0 = 0; b0 < p.rows.B; b0 += 32) {
-    if (p.rows.B > 32) scan_32<CLASS>(p, lane, b0, sum, s);
+    if (p.rows.B > 32) scan_32<CLASS>(p, lane, fold, b0, sum, s);
     const unsigned past = __ballot_sync(0xffffffffu, s.end > u0);
     if (past) {
       const int l = __ffs(past) - 1;
@@ -279,7 +293,7 @@ __device__ __forceinline__ void walk_to(const ChunkParams& p, int lane, long lon
       long long at = begin + W * w.hs;         // first unit of the part
       for (int q0 = 0; q0 < w.r.items; q0 += 32) {
         const int q = q0 + lane;
-        const long long v = q < w.r.items ? item_units(p, w.r, q) : 0;
+        const long long v = q < w.r.items ? item_units<CLASS>(p, w.r, q) : 0;
         const long long upto = at + warp_scan(v, lane);
         const unsigned hit = __ballot_sync(0xffffffffu, upto > u0 && q < w.r.items);
         if (hit) {
@@ -298,14 +312,14 @@ __device__ __forceinline__ void walk_to(const ChunkParams& p, int lane, long lon
 
 // To the next item; false at the batch's end.
 template <int CLASS>
-__device__ __forceinline__ bool walk_on(const ChunkParams& p, Walk& w, int lane) {
+__device__ __forceinline__ bool walk_on(const ChunkParams& p, bool fold, Walk& w, int lane) {
   if (++w.q < w.r.items) return true;
   w.q = 0;
   if (++w.hs < parts_of<CLASS>(p)) return true;
   w.hs = 0;
   for (int b0 = w.b + 1; b0 < p.rows.B; b0 += 32) {
     Request r{};
-    if (b0 + lane < p.rows.B) r = request_of<CLASS>(p, b0 + lane);
+    if (b0 + lane < p.rows.B) r = request_of<CLASS>(p, b0 + lane, fold);
     const unsigned some = __ballot_sync(0xffffffffu, r.n > 0);
     if (some) {
       const int l = __ffs(some) - 1;
@@ -318,14 +332,19 @@ __device__ __forceinline__ bool walk_on(const ChunkParams& p, Walk& w, int lane)
 }
 
 // The units in n even runs; run c, [U c / n, U (c + 1) / n), segment by
-// segment.
+// segment.  A boundary within an item's head or SNAP tiles of its ends moves
+// there: no run takes a head without tiles, or a few tiles at the price of a
+// partial.
 template <int CLASS>
 struct Runs {
   Scan s;
   Walk w;
   long long U, items, n, c, at, end;
-  __device__ __forceinline__ void scan(const ChunkParams& p, int lane, bool report) {
-    U = scan_batch<CLASS>(p, lane, report, s, items);
+  bool others, fold;       // requests of the other class; all of them counted as TENSOR
+  static constexpr int NEAR = HEAD<CLASS> + SNAP<CLASS>;   // boundaries up to here move to the item's start
+  __device__ __forceinline__ void scan(const ChunkParams& p, int lane, bool all_tensor, bool report) {
+    fold = all_tensor;
+    U = scan_batch<CLASS>(p, lane, fold, report, s, items, others);
   }
   // One run a worker; with fewer items than workers, the same number for every item where that idles at most a fifth of
   // them, so that runs of equal items do not cross them (32 items of 8 units: 152 runs 16.2 us, 128 runs 10.3; but 80
@@ -343,17 +362,35 @@ struct Runs {
     c = run;
     at = c < n ? quotient(U * c, n) : 0;
     end = c < n ? quotient(U * (c + 1), n) : 0;
-    if (at < end) walk_to<CLASS>(p, lane, at, s, w);
+    if (at >= end) return;
+    walk_to<CLASS>(p, lane, fold, at, s, w);
+    const int units = item_units<CLASS>(p, w.r, w.q);
+    if (at - w.unit > NEAR && at - w.unit >= units - SNAP<CLASS>) {
+      w.unit += units;
+      if (!walk_on<CLASS>(p, fold, w, lane)) {
+        at = end;
+        return;
+      }
+      at = w.unit;
+    } else if (at - w.unit <= NEAR) {
+      at = w.unit;
+    }
   }
   __device__ __forceinline__ Segment next(const ChunkParams& p, int lane) {
+    constexpr int H = HEAD<CLASS>;
     Segment g{};
     g.last = at >= end;
     if (g.last) return g;
     int kt0, kt1;
     item_tiles(p, w.r, w.q, kt0, kt1);
-    const int units = max(1, kt1 - kt0);
+    const int units = max(1, kt1 - kt0) + H;
     const int x0 = static_cast<int>(at - w.unit);
-    const int x1 = static_cast<int>(min(static_cast<long long>(units), end - w.unit));
+    int x1 = static_cast<int>(min(static_cast<long long>(units), end - w.unit));
+    if (x1 < units) {
+      g.last = x1 <= NEAR;
+      if (g.last) return g;
+      if (x1 >= units - SNAP<CLASS>) x1 = units;
+    }
     const int nsub = CLASS == TOKEN ? 1 : p.nsub;
     const int hk = w.hs / nsub, sub = w.hs - hk * nsub;
     const int t0 = w.q * w.r.per;
@@ -365,24 +402,35 @@ struct Runs {
     g.hk = hk;
     g.head0 = hk * p.G + sub * p.GB;
     g.heads = min(p.GB, p.G - sub * p.GB);
-    g.kt0 = kt0 + x0;
-    g.nt = kt1 > kt0 ? x1 - x0 : 0;
+    const int first = max(x0 - H, 0);        // of the item's tiles
+    g.kt0 = kt0 + first;
+    g.nt = kt1 > kt0 ? x1 - H - first : 0;
     g.two = g.tokens > p.T;
     g.whole = x0 == 0 && x1 == units;
     if (!g.whole) {
-      // the run that holds unit u: the largest that begins at or before it
-      g.first_run = static_cast<int>(quotient((w.unit + 1) * n - 1, U));
-      g.n_parts = static_cast<int>(quotient((w.unit + units) * n - 1, U)) - g.first_run + 1;
+      // the largest run that begins at or before unit u: u the last from where a boundary moves to the item's start, and
+      // the last from where it does not move to its end (a split item is longer than NEAR + SNAP)
+      g.first_run = static_cast<int>(quotient((w.unit + NEAR + 1) * n - 1, U));
+      g.n_parts = static_cast<int>(quotient((w.unit + units - SNAP<CLASS>) * n - 1, U)) - g.first_run + 1;
       g.part = 2 * static_cast<int>(c) + (x0 == 0 ? 1 : 0);
     }
     at = w.unit + x1;
     if (x1 == units) {
       w.unit += units;
-      if (at < end && !walk_on<CLASS>(p, w, lane)) at = end;
+      if (at < end && !walk_on<CLASS>(p, fold, w, lane)) at = end;
     }
     return g;
   }
 };
+
+// Whether requests of few rows go with the others (so that there is no token
+// phase): where there are others, and a worker's share of their units is
+// small.  A token phase of few units is latency, 15 us or so, whereas tiles of
+// 128 rows take them for some 1.5 us a unit; its streaming pays from long
+// prefixes of many requests on.
+__device__ __forceinline__ bool folds(const Runs<TOKEN>& few, int workers) {
+  return few.others && few.U < static_cast<long long>(CH_FOLD) * workers;
+}
 
 // ---- softmax of one tile -------------------------------------------------------
 
@@ -392,15 +440,18 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+// The lowest n bits of a word (none below 1, all from 32 on).
+__device__ __forceinline__ uint32_t first_bits(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
+
 // This thread's row of one half of S_w (64 columns): P_w into tensor memory
-// over it, and the row sum.  Column j is visible when j <= hi (masked & 1) and
-// j >= lo (masked & 2).  The exponentials start at once, against the reference
+// over it, and the row sum.  Column j is visible when lo <= j <= hi (masked; all
+// are otherwise).  The exponentials start at once, against the reference
 // of the steps before (in a segment's first step, its own maximum); only where
 // the step's maximum passes that by CH_RAISE is it raised, O_w and the sum
 // rescaled, and the step done again.  `at_rest` waits until every product into O_w so far is
 // complete.
 template <int D, typename Wait>
-__device__ __forceinline__ bool softmax_step(uint32_t s_addr, uint32_t o_addr, bool first, int masked, int lo, int hi,
+__device__ __forceinline__ bool softmax_step(uint32_t s_addr, uint32_t o_addr, bool first, bool masked, int lo, int hi,
                                              bool valid, float c, float& m_ref, float& l_sum, uint64_t* p_full,
                                              Wait at_rest) {
   float sv[2][32];
@@ -408,17 +459,13 @@ __device__ __forceinline__ bool softmax_step(uint32_t s_addr, uint32_t o_addr, b
 #pragma unroll
     for (int k = 0; k < 2; ++k) sm100::tmem_ld32(s_addr + 32u * k, sv[k]);
     sm100::tmem_wait_ld();
-    if (__builtin_expect(masked & 1, 0)) {
+    if (masked) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t see = first_bits(hi + 1 - 32 * k) & ~first_bits(lo - 32 * k);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) sv[k][j] = 32 * k + j <= hi ? sv[k][j] : -INFINITY;
-    }
-    if (__builtin_expect(masked & 2, 0)) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int j = 0; j < 32; ++j) sv[k][j] = 32 * k + j >= lo ? sv[k][j] : -INFINITY;
+        for (int j = 0; j < 32; ++j) sv[k][j] = see & (1u << j) ? sv[k][j] : -INFINITY;
+      }
     }
   };
   uint32_t pw[32];
@@ -427,14 +474,39 @@ __device__ __forceinline__ bool softmax_step(uint32_t s_addr, uint32_t o_addr, b
     const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
     const float2 c2 = make_float2(c, c), nm2 = make_float2(nm, nm);
     sum = make_float2(0.f, 0.f);
+    float2 ps[2];
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const float2 x = __ffma2_rn(make_float2(sv[j >> 4][2 * (j & 15)], sv[j >> 4][2 * (j & 15) + 1]), c2, nm2);
-      const float2 e = make_float2(sm100::exp2(x.x), sm100::exp2(x.y));
-      sum = __fadd2_rn(sum, e);
-      const __nv_bfloat162 h = __floats2bfloat162_rn(e.x, e.y);
-      pw[j] = *reinterpret_cast<const uint32_t*>(&h);
+    for (int i = 0; i < 2; ++i) ps[i] = make_float2(0.f, 0.f);
+    constexpr int NB = 8;
+    float2 e[2][NB];
+#pragma unroll
+    for (int g = 0; g <= 32 / NB; ++g) {
+      if (g < 32 / NB) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const int j = g * NB + i;
+          e[g & 1][i] = __ffma2_rn(make_float2(sv[j >> 4][2 * (j & 15)], sv[j >> 4][2 * (j & 15) + 1]), c2, nm2);
+        }
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          asm volatile("ex2.approx.ftz.f32 %0, %0;" : "+f"(e[g & 1][i].x));
+          asm volatile("ex2.approx.ftz.f32 %0, %0;" : "+f"(e[g & 1][i].y));
+        }
+      }
+      if (g > 0) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const int j = (g - 1) * NB + i;
+          const float2 y = e[(g & 1) ^ 1][i];
+          ps[i % 2] = __fadd2_rn(ps[i % 2], y);
+          uint32_t w;
+          asm volatile("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(y.y), "f"(y.x));
+          pw[j] = w;
+        }
+      }
     }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) sum = __fadd2_rn(sum, ps[i]);
   };
   load();
   float mx[4];
@@ -924,7 +996,8 @@ __device__ __forceinline__ bool token_phase(const ChunkParams& p, const CUtensor
   using T = TokenShape<D>;
   if (p.G > TK_ROWS) return true;
   Runs<TOKEN> runs;
-  runs.scan(p, lane, false);
+  runs.scan(p, lane, false, false);
+  if (folds(runs, gridDim.x)) return true;
   runs.split(gridDim.x);
   runs.begin(p, lane, blockIdx.x);
   const TokenWarp tw{sw, lane, sm100::l2_policy_evict_first()};
@@ -1027,7 +1100,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
   if (tid == 0) {
     for (int i = 0; i < SLOTS; ++i) {
       sm100::mbar_init(&sh.full[i], 1);
-      sm100::mbar_init(&sh.empty[i], 2);          // the MMA threads
+      sm100::mbar_init(&sh.empty[i], 2);          // a thread of each softmax group
     }
     for (int i = 0; i < CH_SEGS; ++i) {
       sm100::mbar_init(&sh.seg_full[i], 1);
@@ -1082,16 +1155,21 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CH_REGS_FEW));
     if (!p.tensor) {
       if (warp == CH_SCHED_WARP && blockIdx.x == 0) {
-        Scan s;
-        long long items;
-        scan_batch<TENSOR>(p, lane, true, s, items);    // reports what is wrong with the batch
+        Runs<TENSOR> runs;
+        runs.scan(p, lane, false, true);       // reports what is wrong with the batch
       }
       return;
     }
     if (warp == CH_SCHED_WARP) {
       // ---- scheduler ----
+      bool fold = false;
+      if (p.G <= TK_ROWS) {
+        Runs<TOKEN> few;
+        few.scan(p, lane, false, false);
+        fold = folds(few, gridDim.x);
+      }
       Runs<TENSOR> runs;
-      runs.scan(p, lane, blockIdx.x == 0);
+      runs.scan(p, lane, fold, blockIdx.x == 0);
       runs.split(gridDim.x);
       runs.begin(p, lane, blockIdx.x);
       bool ok = true;
@@ -1219,12 +1297,6 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
           ++segs;
           const int step = two ? 1 : 2, t0 = two ? 0 : w;
           const uint32_t qlo = sm100::desc_lo(sbase + (two ? w * S::TILE : 0u), 16);
-          // this thread is done with ring element x's slot once its MMAs so far are; a tile that one group alone
-          // uses counts for both
-          auto release = [&](int x) {
-            sm100::mma_commit(&sh.empty[x % SLOTS]);
-            if (!two) sm100::mbar_arrive(&sh.empty[x % SLOTS]);
-          };
           auto landed = [&](int x) {
             return sm100::mbar_wait(&sh.full[x % SLOTS], static_cast<uint32_t>((x / SLOTS) & 1), abort_flag);
           };
@@ -1246,38 +1318,28 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
             for (int k = 0; k < CH_STEP / 16; ++k)
               sm100::mma_ts32(o_tm, s_tm + 64u * h + 8u * k, vlo + ((k * 2048) >> 4), HI, id_o, k > 0 ? 1u : more);
           };
-          if (t0 >= nt) {
-            if (ok) sm100::mbar_arrive(&sh.q_empty);
-          } else if (ok && (ok = landed(e0 + 2 * t0))) {
+          if (ok && t0 < nt && (ok = landed(e0 + 2 * t0))) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               issue_s(e0 + 2 * t0, h);
               sm100::mma_commit(&sh.s_full[w][h]);
             }
-            release(e0 + 2 * t0);
           }
           for (int t = t0; ok && t < nt; t += step) {
             const int kx = e0 + 2 * (t + step), vx = e0 + 2 * t + 1;    // the next tile's K, this one's V
             const bool next = t + step < nt;
-            if (!next) sm100::mma_commit(&sh.q_empty);
-            ok = landed(vx);
+            ok = landed(vx) && (!next || landed(kx));
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               ok = ok && sm100::mbar_wait(&sh.p_full[w][h], p_phase & 1, abort_flag);
               if (!ok) break;
               issue_o(vx, h, h == 1 || t > t0 ? 1u : 0u);
-              if (h == 0 && next && !landed(kx)) {
-                ok = false;
-                break;
-              }
               if (next) issue_s(kx, h);
               // with no next tile: the sign that O_w has taken this half
               sm100::mma_commit(&sh.s_full[w][h]);
             }
             if (!ok) break;
             ++p_phase;
-            release(vx);
-            if (next) release(kx);
           }
           e0 += 2 * nt;
         }
@@ -1309,6 +1371,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
     const int st = tid - 32 * CH_SOFT_WARP0;               // 0 .. 255
     const int tok = row / p.GB, head = row - tok * p.GB;   // of this row in its tile
     uint32_t s_phase = 0, j_phase = 0;
+    int e0 = 0;                                            // ring element of the segment's first K
+    const bool frees = quarter == 0 && lane == 0;          // tells the loader what the group's products have read
     bool ok = warp_wait(&sh.tm_ready, 0u) && warp_wait(&sh.tk_done, 0u) && tk_ok;   // (the token phase used m and l)
     sm100::tc_fence_after();
     const uint32_t tmem = sh.tmem;
@@ -1337,22 +1401,50 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
       // bounds of the warp's rows, so that a tile they all see whole is not masked
       const int pos_least = __reduce_min_sync(0xffffffffu, valid ? pos : INT_MAX);
       const int lo_most = __reduce_max_sync(0xffffffffu, valid ? lo : INT_MIN);
+      const int pos_most = __reduce_max_sync(0xffffffffu, valid ? pos : INT_MIN);
+      const int lo_least = __reduce_min_sync(0xffffffffu, valid ? lo : INT_MAX);
       const bool some = __any_sync(0xffffffffu, valid);
+      bool fresh = true;                       // the warp has summed nothing yet
       float m_ref = -INFINITY, l_sum = 0.f;
       const int step = two ? 1 : 2, t0 = two ? 0 : w;
+      // ring element x is read; a tile that one group alone uses counts for both
+      auto release = [&](int x) {
+        sm100::mbar_arrive(&sh.empty[x % SLOTS]);
+        if (!two) sm100::mbar_arrive(&sh.empty[x % SLOTS]);
+      };
+      if (frees && g.nt > 0 && t0 >= g.nt) sm100::mbar_arrive(&sh.q_empty);
       for (int t = t0; ok && t < g.nt; t += step) {
         for (int h = 0; ok && h < 2; ++h) {
           ok = warp_wait(&sh.s_full[w][h], s_phase & 1);
           if (!ok) break;
+          if (h == 1 && frees) {               // the tile's scores are complete, and so is what was issued before them
+            if (t > t0) release(e0 + 2 * (t - step) + 1);
+            release(e0 + 2 * t);
+            if (t + step >= g.nt) sm100::mbar_arrive(&sh.q_empty);
+          }
           sm100::tc_fence_after();
           if (some) {
             const int k0 = (g.kt0 + t) * CH_KEYS + CH_STEP * h;
-            const int masked = (k0 + CH_STEP - 1 > pos_least ? 1 : 0) | (k0 < lo_most ? 2 : 0);
+            if (k0 > pos_most || k0 + CH_STEP <= lo_least) {
+              // none of the warp's rows sees a key of the step
+              uint32_t zero[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) zero[j] = 0u;
+              sm100::tmem_st16(s_addr + 64u * h, zero);
+              sm100::tmem_st16(s_addr + 64u * h + 16u, zero);
+              sm100::tmem_wait_st();
+              sm100::tc_fence_before();
+              __syncwarp();
+              if (lane == 0) sm100::mbar_arrive(&sh.p_full[w][h]);
+              continue;
+            }
+            const bool masked = k0 + CH_STEP - 1 > pos_least || k0 < lo_most;
             // The products before this step are complete when the other half's next scores are, issued after them (in
             // the last step: the sign in their place); before the first step there are none.
             auto at_rest = [&]() { return warp_wait(&sh.s_full[w][h ^ 1], (h ? s_phase + 1 : s_phase) & 1); };
-            ok = softmax_step<D>(s_addr + 64u * h, o_addr, t == t0 && h == 0, masked, lo - k0, pos - k0, valid, p.c, m_ref, l_sum,
+            ok = softmax_step<D>(s_addr + 64u * h, o_addr, fresh, masked, lo - k0, pos - k0, valid, p.c, m_ref, l_sum,
                                  &sh.p_full[w][h], at_rest);
+            fresh = false;
           } else if (lane == 0) {
             sm100::mbar_arrive(&sh.p_full[w][h]);
           }
@@ -1363,8 +1455,10 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
         // O_w has taken both halves of the last tile
         ok = warp_wait(&sh.s_full[w][0], s_phase & 1) && warp_wait(&sh.s_full[w][1], s_phase & 1);
         ++s_phase;
+        if (ok && frees) release(e0 + 2 * (t0 + (g.nt - 1 - t0) / step * step) + 1);
       }
       if (!ok) break;
+      e0 += 2 * g.nt;
       sm100::tc_fence_after();
       // The item's rows are 0 .. 255 (two tiles) or 0 .. 127; this thread holds D columns of its own row, or (one
       // tile, whose key tiles both groups shared) half the columns of the join of O_0 and O_1.
