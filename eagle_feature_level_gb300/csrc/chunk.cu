@@ -93,6 +93,7 @@ struct ChunkParams {
   const int32_t* len;
   PagedKv paged;
   int box;                                   // rows of a K / V box
+  int grouped;                               // a box brings whole rows, 8 by 8
   float c;                                   // scale * log2 e
   int tensor;                                // some request may have more rows than the token phase takes
   float* part;                               // [2 grid] partials of split items
@@ -1141,6 +1142,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
   }
   const uint32_t sbase = sm100::smem_u32(sm);
   const uint32_t rbase = sbase + 2 * S::TILE;
+  // K and V tiles: bytes from 8 rows to the next 8, and from elements 0 - 63 to 64 - 127
+  const uint32_t kv_rows = p.grouped ? 1024u * S::HALVES : 1024u, kv_half = p.grouped ? 1024u : CH_HALF;
 
   auto give_up = [&]() {
     set_status(p.status, EAGLE_ERR_TIMEOUT);
@@ -1204,16 +1207,18 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
         if (g.last) break;
         if (g.nt == 0) continue;
         const int32_t* table = paged ? p.paged.table + static_cast<size_t>(g.b) * p.paged.per_req : nullptr;
-        // the block of box j of key tile t, out of range where nothing is to be read
-        auto block_at = [&](int t, int j) {
-          const int pos = (g.kt0 + t) * CH_KEYS + j * p.box;
-          if (pos >= g.len) return p.paged.n_blocks;
-          const int blk = table[pos >> p.paged.shift];
-          if (blk >= 0 && blk < p.paged.n_blocks) return blk;
+        // the table's entry for box j of key tile t, and the block it stands for: out of range (read as zeros) where
+        // nothing is to be read
+        auto pos_of = [&](int t, int j) { return (g.kt0 + t) * CH_KEYS + j * p.box; };
+        auto entry_at = [&](int t, int j) { return pos_of(t, j) < g.len ? table[pos_of(t, j) >> p.paged.shift] : 0; };
+        auto block_of = [&](int t, int j, int x) {
+          if (pos_of(t, j) >= g.len) return p.paged.n_blocks;
+          if (x >= 0 && x < p.paged.n_blocks) return x;
           set_status(p.status, EAGLE_ERR_INVALID_ARG);
           return p.paged.n_blocks;
         };
-        int blk = paged && lane < boxes ? block_at(0, lane) : 0;   // box `lane` of the tile at hand
+        // box `lane` of the tile at hand, and the next tile's entry: looked at a tile later, when it has arrived
+        int blk = paged && lane < boxes ? block_of(0, lane, entry_at(0, lane)) : 0, ahead = 0;
         auto load = [&](int t, int m) {
           const int s = e % SLOTS;
           if (e >= SLOTS && !warp_wait(&sh.empty[s], static_cast<uint32_t>((e / SLOTS - 1) & 1))) return false;
@@ -1225,8 +1230,13 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
           if (lane == 0) sm100::mbar_arrive_expect_tx(bar, S::TILE);
           __syncwarp();
           for (int j = lane; j < boxes; j += 32) {
-            const int z = !paged ? g.b : j < 32 ? blk : block_at(t, j);
+            const int z = !paged ? g.b : j < 32 ? blk : block_of(t, j, entry_at(t, j));
             const int y = !paged ? k0 : (k0 + j * p.box) & ((1 << p.paged.shift) - 1);
+            if (p.grouped) {
+              sm100::tma_load_4d(dst + j * p.box * 128 * S::HALVES, map, 0, 0, g.hk * S::HALVES,
+                                 (z << (p.paged.shift - 3)) + (y >> 3), bar);
+              continue;
+            }
 #pragma unroll
             for (int h = 0; h < S::HALVES; ++h)
               sm100::tma_load_4d(dst + h * CH_HALF + j * p.box * 128, map, 64 * h, g.hk, y, z, bar);
@@ -1238,7 +1248,9 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
             const int first = max(0, g.len - k0);
             for (int x = lane; x < (CH_KEYS - first) * 8 * S::HALVES; x += 32) {
               const int h = x / ((CH_KEYS - first) * 8), y = x - h * (CH_KEYS - first) * 8;
-              *reinterpret_cast<uint4*>(dst + h * CH_HALF + first * 128 + y * 16) = make_uint4(0u, 0u, 0u, 0u);
+              const int r = first + (y >> 3);
+              *reinterpret_cast<uint4*>(dst + h * kv_half + (r >> 3) * kv_rows + (r & 7) * 128 + (y & 7) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
             }
             sm100::fence_proxy_async_smem();
             __syncwarp();
@@ -1263,8 +1275,10 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
         };
         // the first K and V while the item before still uses its Q
         for (int t = 0; ok && t < g.nt; ++t) {
+          const bool more = paged && t + 1 < g.nt && lane < boxes;
+          if (more) ahead = entry_at(t + 1, lane);
           ok = load(t, 0) && load(t, 1) && (t > 0 || load_q());
-          if (paged && ok && t + 1 < g.nt && lane < boxes) blk = block_at(t + 1, lane);
+          if (more) blk = block_of(t + 1, lane, ahead);
         }
       }
       if (!ok && lane == 0) give_up();
@@ -1277,6 +1291,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
       const int w = warp >> 1;
       if (lane == 0) {
         constexpr uint32_t HI = sm100::DESC_SW128_HI;
+        const uint32_t kv_hi = (HI & ~0x3FFFu) | (kv_rows >> 4);
         const uint32_t id_s = sm100::idesc_bf16_f32(CH_ROWS, CH_STEP);
         const uint32_t id_o = sm100::idesc_bf16_f32(CH_ROWS, D) | (1u << 16);     // B (V) MN-major
         bool ok = sm100::mbar_wait(&sh.tm_ready, 0u, abort_flag);
@@ -1303,20 +1318,21 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
           // S_w of half h of the key tile in ring element x
           auto issue_s = [&](int x, int h) {
             sm100::tc_fence_after();
-            const uint32_t klo = sm100::desc_lo(rbase + (x % SLOTS) * S::TILE + h * CH_STEP * 128, 16);
+            const uint32_t klo = sm100::desc_lo(rbase + (x % SLOTS) * S::TILE + h * (CH_STEP / 8) * kv_rows, 16);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
-              const uint32_t off = ((k >> 2) * CH_HALF + (k & 3) * 32) >> 4;
-              sm100::mma_ss32(s_tm + 64u * h, qlo + off, klo + off, HI, id_s, k > 0 ? 1u : 0u);
+              const uint32_t q_off = ((k >> 2) * CH_HALF + (k & 3) * 32) >> 4;
+              const uint32_t k_off = ((k >> 2) * kv_half + (k & 3) * 32) >> 4;
+              sm100::mma_ss32(s_tm + 64u * h, qlo + q_off, HI, klo + k_off, kv_hi, id_s, k > 0 ? 1u : 0u);
             }
           };
           // O_w += P_w V of the same half of the tile's V
           auto issue_o = [&](int x, int h, uint32_t more) {
             sm100::tc_fence_after();
-            const uint32_t vlo = sm100::desc_lo(rbase + (x % SLOTS) * S::TILE + h * CH_STEP * 128, CH_HALF);
+            const uint32_t vlo = sm100::desc_lo(rbase + (x % SLOTS) * S::TILE + h * (CH_STEP / 8) * kv_rows, kv_half);
 #pragma unroll
             for (int k = 0; k < CH_STEP / 16; ++k)
-              sm100::mma_ts32(o_tm, s_tm + 64u * h + 8u * k, vlo + ((k * 2048) >> 4), HI, id_o, k > 0 ? 1u : more);
+              sm100::mma_ts32(o_tm, s_tm + 64u * h + 8u * k, vlo + ((k * 2 * kv_rows) >> 4), kv_hi, id_o, k > 0 ? 1u : more);
           };
           if (ok && t0 < nt && (ok = landed(e0 + 2 * t0))) {
 #pragma unroll
@@ -1641,14 +1657,22 @@ cudaError_t launch_chunk_attn(eagle_ctx* ctx, int batch, const eagle_rows* rows,
   const cuuint64_t row = dh * p.hkv * e2;
   const cuuint64_t ks[3] = {dh * e2, row, row * bs};
   const cuuint32_t kb[4] = {64, 1, static_cast<cuuint32_t>(p.box), 1};
+  // Heads of 128 in blocks of 8 rows or more: a box brings both halves of its rows, 8 rows at a time, from the pool as
+  // {64 elements, 8 rows, half of a kv head, 8-row group}.  One copy a block where two took 95 cycles each to issue (40 heads,
+  // 512 rows after 4096, blocks of 16: 68 -> us).
+  p.grouped = paged && bs >= 8 && p.dh == 128;
+  const cuuint64_t gd[4] = {64, 8, 2 * static_cast<cuuint64_t>(p.hkv), kd[3] * (bs / 8)};
+  const cuuint64_t gs[3] = {row, 128, 8 * row};
+  const cuuint32_t gb[4] = {64, 8, 2, static_cast<cuuint32_t>(p.box / 8)};
   const cuuint32_t tb[4] = {64, 1, static_cast<cuuint32_t>(std::min(p.box, 16)), 1};   // the token phase's steps
   CUtensorMap qm, km, vm, tkm, tvm;
   p.tensor = static_cast<long long>(rows->n_rows) * p.G > TK_ROWS;
   std::memset(&qm, 0, sizeof(qm));
   std::memset(&km, 0, sizeof(km));
   std::memset(&vm, 0, sizeof(vm));
-  if ((p.tensor && (!encode(ctx, &qm, q, 3, qd, qs, qb) || !encode(ctx, &km, kv->k, 4, kd, ks, kb) ||
-                    !encode(ctx, &vm, kv->v, 4, kd, ks, kb))) ||
+  if ((p.tensor && (!encode(ctx, &qm, q, 3, qd, qs, qb) ||
+                    !encode(ctx, &km, kv->k, 4, p.grouped ? gd : kd, p.grouped ? gs : ks, p.grouped ? gb : kb) ||
+                    !encode(ctx, &vm, kv->v, 4, p.grouped ? gd : kd, p.grouped ? gs : ks, p.grouped ? gb : kb))) ||
       !encode(ctx, &tkm, kv->k, 4, kd, ks, tb) ||
       !encode(ctx, &tvm, kv->v, 4, kd, ks, tb))
     return cudaErrorInvalidValue;
