@@ -124,7 +124,8 @@ struct Segment {
 template <int SLOTS>
 struct Shared {
   uint64_t full[SLOTS], empty[SLOTS], seg_full[CH_SEGS], seg_empty[CH_SEGS];
-  uint64_t tm_ready, q_full, q_empty, v_raw, s_full[2][2], p_full[2][2], join, done;
+  uint64_t raw[SLOTS];                     // V tiles that end past the length: landed, not yet zeroed there
+  uint64_t tm_ready, q_full, q_empty, s_full[2][2], p_full[2][2], join, done;
   Segment seg[CH_SEGS];
   float m[2][CH_ROWS], l[2][CH_ROWS];
   uint64_t tk_full[CH_SOFT_WARPS * TK_STAGES<SLOTS>];
@@ -1101,6 +1102,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
   if (tid == 0) {
     for (int i = 0; i < SLOTS; ++i) {
       sm100::mbar_init(&sh.full[i], 1);
+      sm100::mbar_init(&sh.raw[i], 1);
       sm100::mbar_init(&sh.empty[i], 2);          // a thread of each softmax group
     }
     for (int i = 0; i < CH_SEGS; ++i) {
@@ -1110,7 +1112,6 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
     sm100::mbar_init(&sh.tm_ready, 1);
     sm100::mbar_init(&sh.q_full, 1);
     sm100::mbar_init(&sh.q_empty, 2);
-    sm100::mbar_init(&sh.v_raw, 1);
     for (int i = 0; i < 4; ++i) {
       sm100::mbar_init(&sh.s_full[i >> 1][i & 1], 1);
       sm100::mbar_init(&sh.p_full[i >> 1][i & 1], 4);
@@ -1176,18 +1177,46 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
       runs.split(gridDim.x);
       runs.begin(p, lane, blockIdx.x);
       bool ok = true;
-      for (int i = 0; ok; ++i) {
+      int e = 0;                               // ring elements of the segments that are through `finish`
+      uint32_t raw = 0;                        // phases of sh.raw, a bit each
+      // A segment's last V tile, where it ends past the length: rows there may hold anything, and 0 x NaN is NaN, so they
+      // become zeros.  (By the loader, which then waited for the tile, the next segment's loads came 3 to 5 thousand
+      // cycles later.)
+      auto finish = [&](int slot) {
+        const int nt = sh.seg[slot].nt, first = sh.seg[slot].len - (sh.seg[slot].kt0 + nt - 1) * CH_KEYS;
+        e += 2 * nt;
+        if (nt == 0 || first >= CH_KEYS) return true;
+        const int s = (e - 1) % SLOTS;
+        if (!warp_wait(&sh.raw[s], (raw >> s) & 1u)) return false;
+        raw ^= 1u << s;
+        uint8_t* v = ring + s * S::TILE;
+        const int per = (CH_KEYS - first) * 8;
+        for (int x = lane; x < per * S::HALVES; x += 32) {
+          const int h = x >= per ? 1 : 0, y = x - h * per, r = first + (y >> 3);
+          *reinterpret_cast<uint4*>(v + h * kv_half + (r >> 3) * kv_rows + (r & 7) * 128 + (y & 7) * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
+        }
+        sm100::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive(&sh.full[s]);
+        return true;
+      };
+      int i = 0;
+      for (bool more = true; ok && more; ++i) {
         const int slot = i % CH_SEGS;
-        if (i >= CH_SEGS) ok = warp_wait(&sh.seg_empty[slot], static_cast<uint32_t>((i / CH_SEGS - 1) & 1));
-        if (!ok) break;
+        if (i >= CH_SEGS) {
+          ok = warp_wait(&sh.seg_empty[slot], static_cast<uint32_t>((i / CH_SEGS - 1) & 1)) && finish(slot);
+          if (!ok) break;
+        }
         const Segment g = runs.next(p, lane);
         if (lane == 0) {
           sh.seg[slot] = g;
           sm100::mbar_arrive(&sh.seg_full[slot]);
         }
         __syncwarp();
-        if (g.last) break;
+        more = !g.last;
       }
+      for (int j = max(0, i - CH_SEGS); ok && j < i - 1; ++j) ok = finish(j % CH_SEGS);   // (the last one has no tiles)
       if (!ok && lane == 0) give_up();
     } else if (warp == CH_LOAD_WARP) {
       // ---- loader ----
@@ -1195,7 +1224,6 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
       const int boxes = CH_KEYS / p.box;
       int e = 0;                               // ring elements so far: K and V tiles alternate
       int segs = 0;                            // segments with tiles so far
-      uint32_t raw = 0;                        // V tiles that needed zeroing so far
       bool ok = warp_wait(&sh.tk_done, 0u);    // the token phase has used the tiles' memory
       for (int i = 0; ok; ++i) {
         const int slot = i % CH_SEGS;
@@ -1225,8 +1253,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
           uint8_t* dst = ring + s * S::TILE;
           const int k0 = (g.kt0 + t) * CH_KEYS;
           const CUtensorMap* map = m == 0 ? &kmap : &vmap;
-          const bool zero = m == 1 && k0 + CH_KEYS > g.len;
-          uint64_t* bar = zero ? &sh.v_raw : &sh.full[s];
+          const bool zero = m == 1 && k0 + CH_KEYS > g.len;   // (the scheduler's)
+          uint64_t* bar = zero ? &sh.raw[s] : &sh.full[s];
           if (lane == 0) sm100::mbar_arrive_expect_tx(bar, S::TILE);
           __syncwarp();
           for (int j = lane; j < boxes; j += 32) {
@@ -1240,21 +1268,6 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
 #pragma unroll
             for (int h = 0; h < S::HALVES; ++h)
               sm100::tma_load_4d(dst + h * CH_HALF + j * p.box * 128, map, 64 * h, g.hk, y, z, bar);
-          }
-          if (zero) {
-            // rows past the length may hold anything, and 0 x NaN is NaN: V's become zeros
-            if (!warp_wait(&sh.v_raw, raw & 1)) return false;
-            ++raw;
-            const int first = max(0, g.len - k0);
-            for (int x = lane; x < (CH_KEYS - first) * 8 * S::HALVES; x += 32) {
-              const int h = x / ((CH_KEYS - first) * 8), y = x - h * (CH_KEYS - first) * 8;
-              const int r = first + (y >> 3);
-              *reinterpret_cast<uint4*>(dst + h * kv_half + (r >> 3) * kv_rows + (r & 7) * 128 + (y & 7) * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
-            }
-            sm100::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) sm100::mbar_arrive(&sh.full[s]);
           }
           ++e;
           return true;
