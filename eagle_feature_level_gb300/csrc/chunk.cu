@@ -144,7 +144,7 @@ static_assert(chunk_smem<128>() <= (227u << 10) && chunk_smem<64>() <= (227u << 
 
 struct Request {
   int row0, n, len, per, items;              // tokens per item, items per kv head part
-  bool bad, over, other;                     // other: rows, but of the other class
+  bool bad, over;
 };
 
 // Requests of few rows (a decoding step's) are taken by the token phase, the
@@ -179,7 +179,6 @@ __device__ __forceinline__ Request request_of(const ChunkParams& p, int b, bool 
   r.row0 = lo;
   r.n = hi - lo;
   const bool token = !fold && static_cast<long long>(r.n) * p.G <= TK_ROWS;
-  r.other = token != (CLASS == TOKEN) && r.n > 0;
   if (token != (CLASS == TOKEN)) r.n = 0;
   r.per = CLASS == TOKEN ? max(r.n, 1) : r.n <= p.T ? p.T : 2 * p.T;
   r.items = (r.n + r.per - 1) / r.per;
@@ -212,7 +211,7 @@ __device__ __forceinline__ int item_units(const ChunkParams& p, const Request& r
 // requests of many items are summed by the whole warp).
 template <int CLASS>
 __device__ __forceinline__ long long request_units(const ChunkParams& p, const Request& r, int lane) {
-  constexpr int ALONE = 4;
+  constexpr int ALONE = 32;                    // (a sum by the warp takes as long as some 30 items by a lane)
   long long w = 0;
   if (r.items <= ALONE)
     for (int q = 0; q < r.items; ++q) w += item_units<CLASS>(p, r, q);
@@ -252,13 +251,11 @@ __device__ __forceinline__ void scan_32(const ChunkParams& p, int lane, bool fol
 }
 template <int CLASS>
 __device__ __forceinline__ long long scan_batch(const ChunkParams& p, int lane, bool fold, bool report, Scan& s,
-                                                long long& items, bool& others) {
+                                                long long& items) {
   long long sum = 0;
   items = 0;
-  others = false;
   for (int b0 = 0; b0 < p.rows.B; b0 += 32) {
     scan_32<CLASS>(p, lane, fold, b0, sum, s);
-    others = others || __any_sync(0xffffffffu, s.r.other);
     if (report && s.r.bad) set_status(p.status, EAGLE_ERR_INVALID_ARG);
     if (report && s.r.over) set_status(p.status, EAGLE_ERR_CAPACITY);
     items += static_cast<long long>(s.r.items) * parts_of<CLASS>(p);
@@ -342,11 +339,11 @@ struct Runs {
   Scan s;
   Walk w;
   long long U, items, n, c, at, end;
-  bool others, fold;       // requests of the other class; all of them counted as TENSOR
+  bool fold;               // every request counts as TENSOR
   static constexpr int NEAR = HEAD<CLASS> + SNAP<CLASS>;   // boundaries up to here move to the item's start
   __device__ __forceinline__ void scan(const ChunkParams& p, int lane, bool all_tensor, bool report) {
     fold = all_tensor;
-    U = scan_batch<CLASS>(p, lane, fold, report, s, items, others);
+    U = scan_batch<CLASS>(p, lane, fold, report, s, items);
   }
   // One run a worker; with fewer items than workers, the same number for every item where that idles at most a fifth of
   // them, so that runs of equal items do not cross them (32 items of 8 units: 152 runs 16.2 us, 128 runs 10.3; but 80
@@ -425,13 +422,34 @@ struct Runs {
   }
 };
 
-// Whether requests of few rows go with the others (so that there is no token
-// phase): where there are others, and a worker's share of their units is
-// small.  A token phase of few units is latency, 15 us or so, whereas tiles of
-// 128 rows take them for some 1.5 us a unit; its streaming pays from long
-// prefixes of many requests on.
-__device__ __forceinline__ bool folds(const Runs<TOKEN>& few, int workers) {
-  return few.others && few.U < static_cast<long long>(CH_FOLD) * workers;
+// What the batch holds: requests of few rows, and whether they go with the
+// others, without a token phase: where there are others, and a worker's share
+// of their units is small.  A token phase of few units is latency, 15 us or
+// so, whereas tiles of 128 rows take them for some 1.5 us a unit; its
+// streaming pays from long prefixes of many requests on.
+struct Mix {
+  bool few, fold;
+};
+__device__ __forceinline__ Mix mix_of(const ChunkParams& p, int lane) {
+  constexpr int MANY = 1 << 24;
+  int units = 0;
+  bool few = false, others = false;
+  if (p.G <= TK_ROWS) {
+    for (int b = lane; b < p.rows.B; b += 32) {
+      const Request r = request_of<TOKEN>(p, b, false);
+      int lo, hi;
+      request_rows(p.rows, b, lo, hi);
+      few = few || r.n > 0;
+      others = others || hi - lo > r.n;
+      if (r.n > 0)
+        units = static_cast<int>(min(static_cast<long long>(MANY),
+                                     units + static_cast<long long>(item_units<TOKEN>(p, r, 0)) * parts_of<TOKEN>(p)));
+    }
+    few = __any_sync(0xffffffffu, few);
+    others = __any_sync(0xffffffffu, others);
+    units = __reduce_add_sync(0xffffffffu, units);
+  }
+  return Mix{few, few && others && units < CH_FOLD * static_cast<int>(gridDim.x)};
 }
 
 // ---- softmax of one tile -------------------------------------------------------
@@ -996,10 +1014,10 @@ __device__ __forceinline__ bool token_phase(const ChunkParams& p, const CUtensor
                                             uint8_t* mem, uint64_t* bars, volatile int* abort, float* sm_m, float* sm_l,
                                             int* sm_prev, int sw, int lane) {
   using T = TokenShape<D>;
-  if (p.G > TK_ROWS) return true;
+  const Mix mix = mix_of(p, lane);
+  if (!mix.few || mix.fold) return true;
   Runs<TOKEN> runs;
   runs.scan(p, lane, false, false);
-  if (folds(runs, gridDim.x)) return true;
   runs.split(gridDim.x);
   runs.begin(p, lane, blockIdx.x);
   const TokenWarp tw{sw, lane, sm100::l2_policy_evict_first()};
@@ -1166,14 +1184,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
     }
     if (warp == CH_SCHED_WARP) {
       // ---- scheduler ----
-      bool fold = false;
-      if (p.G <= TK_ROWS) {
-        Runs<TOKEN> few;
-        few.scan(p, lane, false, false);
-        fold = folds(few, gridDim.x);
-      }
       Runs<TENSOR> runs;
-      runs.scan(p, lane, fold, blockIdx.x == 0);
+      runs.scan(p, lane, mix_of(p, lane).fold, blockIdx.x == 0);
       runs.split(gridDim.x);
       runs.begin(p, lane, blockIdx.x);
       bool ok = true;
@@ -1286,11 +1298,13 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
           __syncwarp();
           return true;
         };
-        // the first K and V while the item before still uses its Q
+        // the first K and V while the item before still uses its Q; the CTA's first Q at once
+        const bool first = segs == 0;
+        if (first) ok = load_q();
         for (int t = 0; ok && t < g.nt; ++t) {
           const bool more = paged && t + 1 < g.nt && lane < boxes;
           if (more) ahead = entry_at(t + 1, lane);
-          ok = load(t, 0) && load(t, 1) && (t > 0 || load_q());
+          ok = load(t, 0) && load(t, 1) && (t > 0 || first || load_q());
           if (more) blk = block_of(t + 1, lane, ahead);
         }
       }
