@@ -227,13 +227,19 @@ __device__ __forceinline__ long long request_units(const ChunkParams& p, const R
   }
   return w;
 }
-__device__ __forceinline__ long long warp_scan(long long v, int lane) {   // inclusive
+template <typename T>
+__device__ __forceinline__ T scan_of(T v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, v, o);
+    const T y = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += y;
   }
   return v;
+}
+// Inclusive prefix sums of non-negative numbers, in 32 bits where they fit.
+__device__ __forceinline__ long long warp_scan(long long v, int lane) {
+  if (__any_sync(0xffffffffu, v >> 26)) return scan_of(v, lane);
+  return scan_of(static_cast<int>(v), lane);
 }
 
 // Units (and items) of the batch's requests, by one warp, 32 requests at a time.
@@ -251,18 +257,19 @@ __device__ __forceinline__ void scan_32(const ChunkParams& p, int lane, bool fol
 }
 template <int CLASS>
 __device__ __forceinline__ long long scan_batch(const ChunkParams& p, int lane, bool fold, bool report, Scan& s,
-                                                long long& items) {
+                                                int& items) {
+  constexpr int MANY = 1 << 16;                // (more than there are workers)
   long long sum = 0;
   items = 0;
   for (int b0 = 0; b0 < p.rows.B; b0 += 32) {
     scan_32<CLASS>(p, lane, fold, b0, sum, s);
     if (report && s.r.bad) set_status(p.status, EAGLE_ERR_INVALID_ARG);
     if (report && s.r.over) set_status(p.status, EAGLE_ERR_CAPACITY);
-    items += static_cast<long long>(s.r.items) * parts_of<CLASS>(p);
+    items = static_cast<int>(min(static_cast<long long>(MANY),
+                                 items + static_cast<long long>(s.r.items) * parts_of<CLASS>(p)));
     sum = __shfl_sync(0xffffffffu, s.end, 31);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) items += __shfl_xor_sync(0xffffffffu, items, o);
+  items = __reduce_add_sync(0xffffffffu, items);
   return sum;
 }
 
@@ -290,7 +297,9 @@ __device__ __forceinline__ void walk_to(const ChunkParams& p, int lane, bool fol
       const long long begin = __shfl_sync(0xffffffffu, s.end - s.units * parts, l);
       w.hs = static_cast<int>(quotient(u0 - begin, W));
       long long at = begin + W * w.hs;         // first unit of the part
-      for (int q0 = 0; q0 < w.r.items; q0 += 32) {
+      w.q = 0;
+      w.unit = at;
+      for (int q0 = 0; CLASS == TENSOR && q0 < w.r.items; q0 += 32) {   // (TOKEN: one item)
         const int q = q0 + lane;
         const long long v = q < w.r.items ? item_units<CLASS>(p, w.r, q) : 0;
         const long long upto = at + warp_scan(v, lane);
@@ -299,7 +308,7 @@ __device__ __forceinline__ void walk_to(const ChunkParams& p, int lane, bool fol
           const int k = __ffs(hit) - 1;
           w.q = q0 + k;
           w.unit = __shfl_sync(0xffffffffu, upto - v, k);
-          return;
+          break;
         }
         at = __shfl_sync(0xffffffffu, upto, 31);
       }
@@ -338,7 +347,8 @@ template <int CLASS>
 struct Runs {
   Scan s;
   Walk w;
-  long long U, items, n, c, at, end;
+  long long U, n, c, at, end;
+  int items;
   bool fold;               // every request counts as TENSOR
   static constexpr int NEAR = HEAD<CLASS> + SNAP<CLASS>;   // boundaries up to here move to the item's start
   __device__ __forceinline__ void scan(const ChunkParams& p, int lane, bool all_tensor, bool report) {
@@ -352,7 +362,7 @@ struct Runs {
   __device__ __forceinline__ void split(int workers) {
     n = workers;
     if (items > 0 && items < workers) {
-      const int even = workers - workers % static_cast<int>(items);
+      const int even = workers - workers % items;
       if (5 * even >= 4 * workers) n = even;
     }
     n = min(n, U);
@@ -1014,8 +1024,10 @@ __device__ __forceinline__ bool token_phase(const ChunkParams& p, const CUtensor
                                             uint8_t* mem, uint64_t* bars, volatile int* abort, float* sm_m, float* sm_l,
                                             int* sm_prev, int sw, int lane) {
   using T = TokenShape<D>;
-  const Mix mix = mix_of(p, lane);
-  if (!mix.few || mix.fold) return true;
+  if (p.tensor) {
+    const Mix mix = mix_of(p, lane);
+    if (!mix.few || mix.fold) return true;
+  }
   Runs<TOKEN> runs;
   runs.scan(p, lane, false, false);
   runs.split(gridDim.x);
