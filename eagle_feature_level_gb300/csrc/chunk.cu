@@ -57,8 +57,8 @@ constexpr int CH_KEYS = 128;                 // keys per tile
 constexpr int CH_STEP = 64;                  // keys per softmax step
 constexpr int CH_ROWS = 128;                 // query rows per tile
 constexpr uint32_t CH_HALF = CH_KEYS * 128;  // bytes of 128 rows x 64 elements
-constexpr int CH_SEGS = 4;                   // segments the scheduler runs ahead
-constexpr float CH_RAISE = 8.0f;
+constexpr int CH_SEGS = 4;                    // segments the scheduler runs ahead
+constexpr float CH_RAISE = 256.0f, TK_RAISE = 8.0f;
 constexpr int CH_HEAD = 2, CH_SNAP = 1;      // units of an item before its tiles'; tiles of its ends that no boundary cuts off
 constexpr int CH_FOLD = 8;                   // units of a worker from which the token phase pays
 // the token phase: requests of at most TK_ROWS query rows a kv head
@@ -481,7 +481,7 @@ __device__ __forceinline__ uint32_t first_bits(int n) { return n >= 32 ? ~0u : n
 // rescaled, and the step done again.  `at_rest` waits until every product into O_w so far is
 // complete.
 template <int D, typename Wait>
-__device__ __forceinline__ bool softmax_step(uint32_t s_addr, uint32_t o_addr, bool first, bool masked, int lo, int hi,
+__device__ __forceinline__ bool softmax_step(uint32_t s_addr, uint32_t o_addr, bool masked, int lo, int hi,
                                              bool valid, float c, float& m_ref, float& l_sum, uint64_t* p_full,
                                              Wait at_rest) {
   float sv[2][32];
@@ -504,9 +504,9 @@ __device__ __forceinline__ bool softmax_step(uint32_t s_addr, uint32_t o_addr, b
     const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
     const float2 c2 = make_float2(c, c), nm2 = make_float2(nm, nm);
     sum = make_float2(0.f, 0.f);
-    float2 ps[2];
+    float2 ps[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) ps[i] = make_float2(0.f, 0.f);
+    for (int i = 0; i < 4; ++i) ps[i] = make_float2(0.f, 0.f);
     constexpr int NB = 8;
     float2 e[2][NB];
 #pragma unroll
@@ -528,49 +528,51 @@ __device__ __forceinline__ bool softmax_step(uint32_t s_addr, uint32_t o_addr, b
         for (int i = 0; i < NB; ++i) {
           const int j = (g - 1) * NB + i;
           const float2 y = e[(g & 1) ^ 1][i];
-          ps[i % 2] = __fadd2_rn(ps[i % 2], y);
+          ps[i % 4] = __fadd2_rn(ps[i % 4], y);
           uint32_t w;
           asm volatile("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(y.y), "f"(y.x));
           pw[j] = w;
         }
       }
     }
+    sum = __fadd2_rn(__fadd2_rn(ps[0], ps[1]), __fadd2_rn(ps[2], ps[3]));
+  };
+  auto most = [&]() {
+    float mx[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) sum = __fadd2_rn(sum, ps[i]);
+    for (int k = 0; k < 4; ++k) {
+      mx[k] = fmaxf(sv[k >> 1][16 * (k & 1)], sv[k >> 1][16 * (k & 1) + 1]);
+#pragma unroll
+      for (int j = 2; j < 16; j += 2)
+        mx[k] = max3(mx[k], sv[k >> 1][16 * (k & 1) + j], sv[k >> 1][16 * (k & 1) + j + 1]);
+    }
+    return fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
   };
   load();
-  float mx[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    mx[k] = fmaxf(sv[k >> 1][16 * (k & 1)], sv[k >> 1][16 * (k & 1) + 1]);
-#pragma unroll
-    for (int j = 2; j < 16; j += 2) mx[k] = max3(mx[k], sv[k >> 1][16 * (k & 1) + j], sv[k >> 1][16 * (k & 1) + j + 1]);
+  if (__any_sync(0xffffffffu, valid && m_ref == -INFINITY)) {
+    const float mt = most();
+    if (m_ref == -INFINITY) m_ref = mt;        // nothing summed yet
   }
-  const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
-  const bool raise = valid && (mt > m_ref + CH_RAISE || (m_ref == -INFINITY && mt != -INFINITY));
-  const bool any = __any_sync(0xffffffffu, raise);
-  if (first && raise) m_ref = mt;            // nothing summed yet
   exps();
-  if (__builtin_expect(any && !first, 0)) {
-    const bool rescale = raise && m_ref != -INFINITY;
-    if (__any_sync(0xffffffffu, rescale)) {
-      if (!at_rest()) return false;
-      sm100::tc_fence_after();
-      const float f = rescale ? sm100::exp2(m_ref - mt) : 1.f;
+  const bool raise = valid && sum.x + sum.y > CH_RAISE;
+  if (__builtin_expect(__any_sync(0xffffffffu, raise), 0)) {
+    if (!at_rest()) return false;
+    sm100::tc_fence_after();
+    load();                                    // the scores once more (their registers went to P)
+    const float mt = most();
+    const float f = raise ? sm100::exp2(m_ref - mt) : 1.f;
 #pragma unroll 1
-      for (int q = 0; q < D / 16; ++q) {
-        float o[16];
-        sm100::tmem_ld16(o_addr + 16u * q, o);
-        sm100::tmem_wait_ld();
-        uint32_t x[16];
+    for (int q = 0; q < D / 16; ++q) {
+      float o[16];
+      sm100::tmem_ld16(o_addr + 16u * q, o);
+      sm100::tmem_wait_ld();
+      uint32_t x[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(o[j] * f);
-        sm100::tmem_st16(o_addr + 16u * q, x);
-      }
-      l_sum *= f;
+      for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(o[j] * f);
+      sm100::tmem_st16(o_addr + 16u * q, x);
     }
+    l_sum *= f;
     if (raise) m_ref = mt;
-    load();                                  // the scores once more (their registers went to P)
     exps();
   }
 #pragma unroll
@@ -854,7 +856,7 @@ __device__ __forceinline__ void token_segment(const ChunkParams& p, const CUtens
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         mt[n][i] = fmaxf(s[n][i], s[n][i + 2]);
-        ask = ask || mt[n][i] > m[n][i] + CH_RAISE || (m[n][i] == -INFINITY && mt[n][i] != -INFINITY);
+        ask = ask || mt[n][i] > m[n][i] + TK_RAISE || (m[n][i] == -INFINITY && mt[n][i] != -INFINITY);
       }
     }
     if (__any_sync(0xffffffffu, ask)) {
@@ -1459,7 +1461,6 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
       const int pos_most = __reduce_max_sync(0xffffffffu, valid ? pos : INT_MIN);
       const int lo_least = __reduce_min_sync(0xffffffffu, valid ? lo : INT_MAX);
       const bool some = __any_sync(0xffffffffu, valid);
-      bool fresh = true;                       // the warp has summed nothing yet
       float m_ref = -INFINITY, l_sum = 0.f;
       const int step = two ? 1 : 2, t0 = two ? 0 : w;
       // ring element x is read; a tile that one group alone uses counts for both
@@ -1497,9 +1498,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
             // The products before this step are complete when the other half's next scores are, issued after them (in
             // the last step: the sign in their place); before the first step there are none.
             auto at_rest = [&]() { return warp_wait(&sh.s_full[w][h ^ 1], (h ? s_phase + 1 : s_phase) & 1); };
-            ok = softmax_step<D>(s_addr + 64u * h, o_addr, fresh, masked, lo - k0, pos - k0, valid, p.c, m_ref, l_sum,
+            ok = softmax_step<D>(s_addr + 64u * h, o_addr, masked, lo - k0, pos - k0, valid, p.c, m_ref, l_sum,
                                  &sh.p_full[w][h], at_rest);
-            fresh = false;
           } else if (lane == 0) {
             sm100::mbar_arrive(&sh.p_full[w][h]);
           }
