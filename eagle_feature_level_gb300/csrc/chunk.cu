@@ -4,40 +4,57 @@
 // Rows and items.  The query heads of a kv head share its keys, so a 128-row
 // tensor-core tile holds T = 128 / GB tokens x GB heads (GB = the heads per
 // kv head, at most 128).  An item is two such tiles (one when the request has
-// few rows left) of one request and kv head, against the tiles of 128 keys
-// its rows can see: max(0, first row's position - window + 1) up to its last
-// row's position.
+// few rows) of one request and kv head, against the tiles of 128 keys its
+// rows can see: max(0, first row's position - window + 1) up to its last
+// row's position.  Two tiles read K and V once for 256 rows.
 //
 // Schedule.  Items differ by orders of magnitude (a decoding token over 64 key
 // tiles, a prompt's first rows over one), and their sizes are known on the
 // device only.  So the key tiles of all items, laid end to end, are dealt out
-// evenly: CTA c of n takes the units [U c / n, U (c + 1) / n).  Each CTA finds
-// its start itself (two passes of one warp over the batch's lengths), walks
-// on from there, and writes the rows of items it holds whole; an item that
-// crosses CTAs leaves (max, sum, unnormalised output) partials, which the
-// last CTA to arrive combines in CTA order (the same bits whoever is last).
+// evenly: CTA c of n takes the units [U c / n, U (c + 1) / n), where an item
+// counts two units beside its tiles for its ends (queries in, output out, the
+// pipeline empty).  Each CTA finds its start itself (a pass of one warp over
+// the batch's lengths), walks on from there, and writes the rows of items it
+// holds whole; an item that crosses CTAs leaves (max, sum, unnormalised
+// output) partials, which the last CTA to arrive combines in CTA order (the
+// same bits whoever is last).  Counting the ends took a prompt of 8192 (64/8
+// heads) from 819 to 766 us.
 //
 // One CTA per SM, 384 threads:
 //   warp 0      loader: Q tiles, then K and V tiles by TMA into a ring (boxes
-//               of 64 elements x one block's rows, out-of-range blocks read as
-//               zeros); rows of V past the request's length are zeroed.
+//               of one block's rows, out-of-range blocks read as zeros).
 //   warps 1, 3  one thread each issues the MMAs of softmax group w = 0, 1:
-//               S_w = Q_w K^T into tensor memory, O_w += P_w V with P_w (bf16)
-//               written over S_w.  (One thread for both left the tensor cores
-//               idle while it polled barriers and committed: 42% active.)
-//   warp 2      scheduler: the walk over items, a few segments ahead.
+//               S_w = Q_w K^T into tensor memory in two steps of 64 keys, O_w +=
+//               P_w V with P_w (bf16) written over S_w; the next tile's step
+//               of S_w goes out behind the products of this tile's.  So
+//               a group always has its next 64 scores ready while it is at the
+//               exponentials of these.
+//   warp 2      scheduler: the walk over items, a few segments ahead; makes
+//               rows of V past the request's length zeros.
 //   warps 4-11  two softmax warpgroups, thread = query row = tensor-memory
 //               lane.  With two tiles warpgroup w has tile w and every key
 //               tile; with one, warpgroup w has the key tiles t = w (mod 2) and
-//               an O of its own, joined at the item's end.  So the tensor
-//               cores always have the other group's products to run while one
-//               group is at its exponentials.
-// The running maximum of a row is raised (O and the sum rescaled) only when a
-// tile's maximum passes it by more than 8 in log2 units: P stays below 2^8 and
-// O / l does not depend on when it was raised.  P in bf16 (2^-9 of each
-// probability) is this operator's one rounding besides its output's: with P as
-// a hi + lo pair the P V products double, which the fp32 outputs of the tree
-// attention need and a bf16 output does not.
+//               an O of its own, joined at the item's end.  They also free the
+//               ring's slots: scores that are complete show that the products
+//               issued before them are (a commit of the MMA threads for each
+//               slot cost 250 cycles of their time: 364 -> 342 us below).
+//
+// Bound.  At heads of 128 the products of 128 rows x 128 keys take 1024 cycles
+// (measured), in steps of 64 keys 1260: S reads both operands from shared
+// memory, 6 KB for 32 cycles of products, 128 bytes a cycle.  A step of the
+// softmax takes some 1300 cycles of a warp beside its neighbour.  2048 rows after
+// 6144 (64 query / 8 kv heads): 312 us, 1.54 PF/s, 0.79 of a measured bf16 GEMM;
+// tensor pipe 66% active.  S in steps of 128 keys lost more to waiting than it
+// gained (384 to 434 us when this took 364).  At heads of 64 the softmax bounds
+// it: two prompts of 4096 (16/4 heads) 103 us, 0.67 PF/s.
+//
+// The running reference of a row is raised (O and the sum rescaled) only when
+// the 64 exponentials of a step add up to more than 256: P stays below 2^8, O / l
+// does not depend on when it was raised, and the steps in between take no
+// maximum (334 -> 312 us).  P in bf16 (2^-9 of each probability) is this
+// operator's one rounding besides its output's: with P as a hi + lo pair the
+// P V products double, which the fp32 outputs of the tree attention need and a
+// bf16 output does not.
 #include <algorithm>
 #include <cstring>
 
@@ -57,11 +74,14 @@ constexpr int CH_KEYS = 128;                 // keys per tile
 constexpr int CH_STEP = 64;                  // keys per softmax step
 constexpr int CH_ROWS = 128;                 // query rows per tile
 constexpr uint32_t CH_HALF = CH_KEYS * 128;  // bytes of 128 rows x 64 elements
-constexpr int CH_SEGS = 4;                    // segments the scheduler runs ahead
-constexpr float CH_RAISE = 256.0f, TK_RAISE = 8.0f;
-constexpr int CH_HEAD = 2, CH_SNAP = 1;      // units of an item before its tiles'; tiles of its ends that no boundary cuts off
-constexpr int CH_FOLD = 8;                   // units of a worker from which the token phase pays
-// the token phase: requests of at most TK_ROWS query rows a kv head
+constexpr int CH_SEGS = 4;                   // segments the scheduler runs ahead
+constexpr float CH_RAISE = 256.0f;           // a step's sum of exponentials from which its reference is raised
+constexpr float TK_RAISE = 8.0f;             // in the token phase: the excess of a score over it, in log2 units
+constexpr int CH_HEAD = 2;                   // units of an item before its tiles'
+constexpr int CH_SNAP = 1;                   // tiles of its ends that no boundary cuts off
+constexpr int CH_FOLD = 16;                  // units of a worker from which the token phase pays
+// the token phase: requests of at most TK_ROWS query rows a kv head.  At 9 to 16 rows (tiles / token phase): 16 x 2 rows
+// after 8192 (64/8 heads) 156 / 90 us, 4 x 12 after 4096 (40 heads) 95 / 68, 1 x 12 after 1024 20 / 22.
 constexpr int TK_ROWS = 16;
 template <int SLOTS>
 constexpr int TK_STAGES = SLOTS == 5 ? 3 : 5;  // ring stages of a warp (for heads of 128, of 64 elements)
@@ -81,7 +101,7 @@ struct Shape {
 
 struct ChunkParams {
   PackedRows rows;
-  int hkv, G, GB, T, nsub;                   // heads: kv, per kv head, per tile; tokens per tile; tiles' heads per kv head
+  int hkv, G, GB, T, nsub;                   // kv heads, heads of each, heads and tokens of a tile, tiles for G heads
   int dh;
   long long ld_q, ld_o;
   const uint16_t* q;
@@ -98,8 +118,8 @@ struct ChunkParams {
   int tensor;                                // some request may have more rows than the token phase takes
   float* part;                               // [2 grid] partials of split items
   int* cnt;                                  // [grid] arrivals at a split item, by its first CTA
-  float* tk_part;                            // the token phase's partials by run, arrivals at split items by their first run,
-  int* tk_cnt;
+  float* tk_part;                            // the token phase's partials by run,
+  int* tk_cnt;                               // and arrivals at split items by their first run
   int* status;
   uint64_t* stamp;
 };
@@ -417,8 +437,8 @@ struct Runs {
     g.two = g.tokens > p.T;
     g.whole = x0 == 0 && x1 == units;
     if (!g.whole) {
-      // the largest run that begins at or before unit u: u the last from where a boundary moves to the item's start, and
-      // the last from where it does not move to its end (a split item is longer than NEAR + SNAP)
+      // the largest run that begins at or before unit u: u the last from where a boundary moves to the item's start,
+      // and the last from where it does not move to its end (a split item is longer than NEAR + SNAP)
       g.first_run = static_cast<int>(quotient((w.unit + NEAR + 1) * n - 1, U));
       g.n_parts = static_cast<int>(quotient((w.unit + units - SNAP<CLASS>) * n - 1, U)) - g.first_run + 1;
       g.part = 2 * static_cast<int>(c) + (x0 == 0 ? 1 : 0);
@@ -434,9 +454,11 @@ struct Runs {
 
 // What the batch holds: requests of few rows, and whether they go with the
 // others, without a token phase: where there are others, and a worker's share
-// of their units is small.  A token phase of few units is latency, 15 us or
-// so, whereas tiles of 128 rows take them for some 1.5 us a unit; its
-// streaming pays from long prefixes of many requests on.
+// of their units is small.  A token phase of few units is latency, 10 us or
+// so; its streaming pays from long prefixes of many requests on.  512 rows of a
+// prompt beside single tokens (40 heads), with the phase / in tiles: 2.1 units
+// a worker 58 / 50 us, 8.4: 64 / 53, 16.8: 72 / 72, 34: 99 / 109, 135: 264 / 337;
+// 64/8 heads, 13.5: 69 / 68, 27: 88 / 99.
 struct Mix {
   bool few, fold;
 };
@@ -473,13 +495,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // The lowest n bits of a word (none below 1, all from 32 on).
 __device__ __forceinline__ uint32_t first_bits(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
 
-// This thread's row of one half of S_w (64 columns): P_w into tensor memory
+// This thread's row of one step of S_w (64 columns): P_w into tensor memory
 // over it, and the row sum.  Column j is visible when lo <= j <= hi (masked; all
-// are otherwise).  The exponentials start at once, against the reference
-// of the steps before (in a segment's first step, its own maximum); only where
-// the step's maximum passes that by CH_RAISE is it raised, O_w and the sum
-// rescaled, and the step done again.  `at_rest` waits until every product into O_w so far is
-// complete.
+// are otherwise).  The exponentials are against the reference of the steps
+// before; a row that has none yet takes the step's maximum first.  Only where
+// a row's exponentials add up to more than CH_RAISE is its reference raised to
+// the step's maximum, O_w and the sum rescaled, and the step done again.
+// `at_rest` waits until every product into O_w so far is complete.
 template <int D, typename Wait>
 __device__ __forceinline__ bool softmax_step(uint32_t s_addr, uint32_t o_addr, bool masked, int lo, int hi,
                                              bool valid, float c, float& m_ref, float& l_sum, uint64_t* p_full,
@@ -1205,9 +1227,9 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
       bool ok = true;
       int e = 0;                               // ring elements of the segments that are through `finish`
       uint32_t raw = 0;                        // phases of sh.raw, a bit each
-      // A segment's last V tile, where it ends past the length: rows there may hold anything, and 0 x NaN is NaN, so they
-      // become zeros.  (By the loader, which then waited for the tile, the next segment's loads came 3 to 5 thousand
-      // cycles later.)
+      // A segment's last V tile, where it ends past the length: rows there may hold anything, and 0 x NaN is NaN, so
+      // they become zeros.  (By the loader, which then waited for the tile, the next segment's loads came 3 to 5
+      // thousand cycles later.)
       auto finish = [&](int slot) {
         const int nt = sh.seg[slot].nt, first = sh.seg[slot].len - (sh.seg[slot].kt0 + nt - 1) * CH_KEYS;
         e += 2 * nt;
@@ -1307,7 +1329,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
             sm100::mbar_arrive_expect_tx(&sh.q_full, bytes * tiles);
             for (int w = 0; w < tiles; ++w)
               for (int h = 0; h < S::HALVES; ++h)
-                sm100::tma_load_3d(sm + w * S::TILE + h * CH_HALF, &qmap, 64 * h, g.head0, g.row0 + w * p.T, &sh.q_full);
+                sm100::tma_load_3d(sm + w * S::TILE + h * CH_HALF, &qmap, 64 * h, g.head0, g.row0 + w * p.T,
+                                   &sh.q_full);
           }
           __syncwarp();
           return true;
@@ -1373,7 +1396,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
             const uint32_t vlo = sm100::desc_lo(rbase + (x % SLOTS) * S::TILE + h * (CH_STEP / 8) * kv_rows, kv_half);
 #pragma unroll
             for (int k = 0; k < CH_STEP / 16; ++k)
-              sm100::mma_ts32(o_tm, s_tm + 64u * h + 8u * k, vlo + ((k * 2 * kv_rows) >> 4), kv_hi, id_o, k > 0 ? 1u : more);
+              sm100::mma_ts32(o_tm, s_tm + 64u * h + 8u * k, vlo + ((k * 2 * kv_rows) >> 4), kv_hi, id_o,
+                              k > 0 ? 1u : more);
           };
           if (ok && t0 < nt && (ok = landed(e0 + 2 * t0))) {
 #pragma unroll
@@ -1697,8 +1721,8 @@ cudaError_t launch_chunk_attn(eagle_ctx* ctx, int batch, const eagle_rows* rows,
   const cuuint64_t ks[3] = {dh * e2, row, row * bs};
   const cuuint32_t kb[4] = {64, 1, static_cast<cuuint32_t>(p.box), 1};
   // Heads of 128 in blocks of 8 rows or more: a box brings both halves of its rows, 8 rows at a time, from the pool as
-  // {64 elements, 8 rows, half of a kv head, 8-row group}.  One copy a block where two took 95 cycles each to issue (40 heads,
-  // 512 rows after 4096, blocks of 16: 68 -> us).
+  // {64 elements, 8 rows, half of a kv head, 8-row group}.  One copy a block where two took 95 cycles each to issue,
+  // which kept the loader behind (40 heads, 512 rows after 4096, blocks of 16: 68 -> 62 us; of 64: 61 either way).
   p.grouped = paged && bs >= 8 && p.dh == 128;
   const cuuint64_t gd[4] = {64, 8, 2 * static_cast<cuuint64_t>(p.hkv), kd[3] * (bs / 8)};
   const cuuint64_t gs[3] = {row, 128, 8 * row};

@@ -6,7 +6,9 @@
 // reserve and compact are two launches: a plan by one CTA over the tables and
 // counts (a few thousand integers: latency), which writes a list of block
 // copies, and the copy of those blocks in every layer's K and V pools by the
-// whole GPU (bandwidth: each byte read once, written once).
+// whole GPU (bandwidth: each byte read once, written once).  A plan takes 12 us
+// for 16384 blocks; the copy of 1.07 GB of moving blocks 335 us, 6.4 TB/s, 0.94
+// of a measured copy.
 #include <algorithm>
 
 #include "internal.h"

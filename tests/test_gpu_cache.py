@@ -751,6 +751,18 @@ def test_pages_reserved_ahead_stay():
     assert not t.reserve([18, 29])                         # within the columns, out of blocks
 
 
+def test_pages_block_zero_takes_a_copy():
+    """A shared tail copied into block 0 beside sequences that end on a block's end and copy nothing."""
+    t = Twin(9, 4, 4, 24)
+    t.grow([3, 8, 5, 0, 0, 0, 0, 0, 0])
+    t.release([0, -1, -1, -1, -1, -1, -1, -1, -1])
+    assert t.o.ref[0] == 0
+    t.fork([1, 2, 2, 1, 2], [3, 4, 5, 6, 7])
+    assert t.reserve([0, 0, 0, 2, 2, 2, 2, 2, 0])
+    assert t.o.table[4][1] == 0 or t.o.table[3][2] == 0
+    t.compact()
+
+
 def test_pages_tables_alone_and_large_copies():
     """No pools: tables only.  And blocks of many copy chunks, copied part by part."""
     t = Twin(3, 4, 8, 12)
