@@ -612,6 +612,18 @@ __device__ __forceinline__ bool softmax_step(uint32_t s_addr, uint32_t o_addr, b
   return true;
 }
 
+// 16 bf16 elements of a thread's own row, a line that no other thread of the warp writes.
+__device__ __forceinline__ void store16(const ChunkParams& p, uint16_t* dst, const uint32_t* x) {
+  if (p.out32) {                             // half as many passes as 16-byte stores
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                 "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+  } else {
+    *reinterpret_cast<uint4*>(dst) = make_uint4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<uint4*>(dst + 8) = make_uint4(x[4], x[5], x[6], x[7]);
+  }
+}
+
 // A split item's partials joined in run order, by the softmax threads: a
 // thread takes CN runs of four columns of its row at a time, from c0 on.
 template <int D, int CN>
@@ -648,13 +660,20 @@ __device__ __forceinline__ void merge_row(const ChunkParams& p, const Segment& g
       }
     }
     const float z = l > 0.f ? 1.f / l : 0.f;
+    uint32_t x[2 * CN];
 #pragma unroll
     for (int j = 0; j < CN; ++j) {
-      if (4 * (c + j) >= p.dh) continue;
       const __nv_bfloat162 a = __floats2bfloat162_rn(o[j].x * z, o[j].y * z);
       const __nv_bfloat162 b = __floats2bfloat162_rn(o[j].z * z, o[j].w * z);
-      *reinterpret_cast<uint2*>(dst + 4 * (c + j)) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+      x[2 * j] = *reinterpret_cast<const uint32_t*>(&a);
+      x[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    if (CN == 8) {
+#pragma unroll
+      for (int q = 0; q < CN / 4; ++q)
+        if (4 * c + 16 * q < p.dh) store16(p, dst + 4 * c + 16 * q, x + 8 * q);
+    } else if (4 * c < p.dh) {
+      *reinterpret_cast<uint2*>(dst + 4 * c) = make_uint2(x[0], x[1]);
     }
   }
 }
@@ -1598,15 +1617,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                   const __nv_bfloat162 h = __floats2bfloat162_rn(o[16 * q + 2 * j] * inv, o[16 * q + 2 * j + 1] * inv);
                   x[j] = *reinterpret_cast<const uint32_t*>(&h);
                 }
-                if (p.out32) {
-                  // every thread's row is a line of its own: half as many passes as 16-byte stores
-                  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + 16 * q), "r"(x[0]),
-                               "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
-                               : "memory");
-                } else {
-                  *reinterpret_cast<uint4*>(dst + 16 * q) = make_uint4(x[0], x[1], x[2], x[3]);
-                  *reinterpret_cast<uint4*>(dst + 16 * q + 8) = make_uint4(x[4], x[5], x[6], x[7]);
-                }
+                store16(p, dst + 16 * q, x);
               }
             }
           } else {
