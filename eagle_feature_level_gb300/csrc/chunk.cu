@@ -1391,9 +1391,12 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
           sm100::mbar_arrive(&sh.seg_empty[slot]);
           if (last) break;
           if (nt == 0) continue;
+          const int step = two ? 1 : 2, t0 = two ? 0 : w;
+          // Every segment's queries are waited for, and given free in a segment without tiles for this group (else by its
+          // softmax warps), only then: the barriers' phases stay in step with both groups.
           ok = sm100::mbar_wait(&sh.q_full, static_cast<uint32_t>(segs & 1), abort_flag);
           ++segs;
-          const int step = two ? 1 : 2, t0 = two ? 0 : w;
+          if (ok && t0 >= nt) sm100::mbar_arrive(&sh.q_empty);
           const uint32_t qlo = sm100::desc_lo(sbase + (two ? w * S::TILE : 0u), 16);
           auto landed = [&](int x) {
             return sm100::mbar_wait(&sh.full[x % SLOTS], static_cast<uint32_t>((x / SLOTS) & 1), abort_flag);
@@ -1511,7 +1514,6 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
         sm100::mbar_arrive(&sh.empty[x % SLOTS]);
         if (!two) sm100::mbar_arrive(&sh.empty[x % SLOTS]);
       };
-      if (frees && g.nt > 0 && t0 >= g.nt) sm100::mbar_arrive(&sh.q_empty);
       for (int t = t0; ok && t < g.nt; t += step) {
         for (int h = 0; ok && h < 2; ++h) {
           ok = warp_wait(&sh.s_full[w][h], s_phase & 1);

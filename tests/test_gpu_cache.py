@@ -468,6 +468,19 @@ def test_attention_small_contiguous_caches(heads):
     attention_case(heads, 0, [5, 9, 30], [5, 9, 30], seed=34, cap=30)
 
 
+@pytest.mark.parametrize("heads", [(8, 2, 128), (4, 4, 64)], ids=["dh128", "dh64"])
+def test_attention_short_prompts_between_long_ones(heads):
+    """Items of two query tiles and several key tiles beside items of one query tile and one key tile, in turn: one
+    softmax group has nothing to do in the latter and may be a segment ahead of the other."""
+    G = heads[0] // heads[1]
+    T = 128 // G
+    lens, new = [], []
+    for i in range(32):
+        lens += [2 * T + 1 + i, T if T <= 128 else 128]
+        new += [2 * T, T - i % 3]
+    attention_case(heads, 16, lens, new, seed=50)
+
+
 def test_attention_hundreds_of_requests():
     rng = random.Random(5)
     eng = R.Engine(dict(d=256, n_q_heads=4, n_kv_heads=2, head_dim=64, d_ff=64, vocab=64), max_batch=301, max_rows=8,
