@@ -57,6 +57,7 @@
 // bf16 output does not.
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
 #include "internal.h"
 #include "common.cuh"
@@ -80,8 +81,8 @@ constexpr float TK_RAISE = 8.0f;             // in the token phase: the excess o
 constexpr int CH_HEAD = 2;                   // units of an item before its tiles'
 constexpr int CH_SNAP = 1;                   // tiles of its ends that no boundary cuts off
 constexpr int CH_FOLD = 16;                  // units of a worker from which the token phase pays
-// the token phase: requests of at most TK_ROWS query rows a kv head.  At 9 to 16 rows (tiles / token phase): 16 x 2 rows
-// after 8192 (64/8 heads) 156 / 90 us, 4 x 12 after 4096 (40 heads) 95 / 68, 1 x 12 after 1024 20 / 22.
+// the token phase: requests of at most TK_ROWS query rows a kv head.  At 9 to 16 rows, tiles / token phase: 16 x 2
+// rows after 8192 (64/8 heads) 156 / 90 us, 4 x 12 after 4096 (40 heads) 95 / 68, 1 x 12 after 1024 20 / 22.
 constexpr int TK_ROWS = 16;
 template <int SLOTS>
 constexpr int TK_STAGES = SLOTS == 5 ? 3 : 5;  // ring stages of a warp (for heads of 128, of 64 elements)
@@ -145,7 +146,7 @@ template <int SLOTS>
 struct Shared {
   uint64_t full[SLOTS], empty[SLOTS], seg_full[CH_SEGS], seg_empty[CH_SEGS];
   uint64_t raw[SLOTS];                     // V tiles that end past the length: landed, not yet zeroed there
-  uint64_t tm_ready, q_full, q_empty, s_full[2][2], p_full[2][2], join, done;
+  uint64_t tm_ready, q_full, q_empty, s_full[2][2], p_full[2][2], o_half[2], o_full[2], join, done;
   Segment seg[CH_SEGS];
   float m[2][CH_ROWS], l[2][CH_ROWS];
   uint64_t tk_full[CH_SOFT_WARPS * TK_STAGES<SLOTS>];
@@ -1176,7 +1177,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
     for (int i = 0; i < SLOTS; ++i) {
       sm100::mbar_init(&sh.full[i], 1);
       sm100::mbar_init(&sh.raw[i], 1);
-      sm100::mbar_init(&sh.empty[i], 2);          // a thread of each softmax group
+      sm100::mbar_init(&sh.empty[i], 2);          // each group: its softmax warps, or its MMA thread
     }
     for (int i = 0; i < CH_SEGS; ++i) {
       sm100::mbar_init(&sh.seg_full[i], 1);
@@ -1188,6 +1189,10 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
     for (int i = 0; i < 4; ++i) {
       sm100::mbar_init(&sh.s_full[i >> 1][i & 1], 1);
       sm100::mbar_init(&sh.p_full[i >> 1][i & 1], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      sm100::mbar_init(&sh.o_half[i], 1);
+      sm100::mbar_init(&sh.o_full[i], 1);
     }
     sm100::mbar_init(&sh.join, CH_SOFT_WARPS);
     sm100::mbar_init(&sh.tk_done, CH_SOFT_WARPS);
@@ -1391,9 +1396,9 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
           sm100::mbar_arrive(&sh.seg_empty[slot]);
           if (last) break;
           if (nt == 0) continue;
-          const int step = two ? 1 : 2, t0 = two ? 0 : w;
-          // Every segment's queries are waited for, and given free in a segment without tiles for this group (else by its
-          // softmax warps), only then: the barriers' phases stay in step with both groups.
+          const int t0 = two ? 0 : w;
+          // Every segment's queries are waited for, and given free in a segment without tiles for this group (else by
+          // its softmax warps), only then: the barriers' phases stay in step with both groups.
           ok = sm100::mbar_wait(&sh.q_full, static_cast<uint32_t>(segs & 1), abort_flag);
           ++segs;
           if (ok && t0 >= nt) sm100::mbar_arrive(&sh.q_empty);
@@ -1421,29 +1426,56 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
               sm100::mma_ts32(o_tm, s_tm + 64u * h + 8u * k, vlo + ((k * 2 * kv_rows) >> 4), kv_hi, id_o,
                               k > 0 ? 1u : more);
           };
-          if (ok && t0 < nt && (ok = landed(e0 + 2 * t0))) {
+          // a tile of the other group alone: this one is through with it once it is there.  (So every slot's phases
+          // pass both MMA threads in turn, and no wait can take one for the one two before.)
+          auto pass = [&](int t) {
+            for (int x = e0 + 2 * t; ok && x < e0 + 2 * t + 2; ++x) {
+              ok = landed(x);
+              if (ok) sm100::mbar_arrive(&sh.empty[x % SLOTS]);
+            }
+          };
+          // Tiles t0, t0 + STEP, .. of the segment.  (The loop of the two-tile case has nothing in it but waits and
+          // products: tests for the other case in it took 311 to 345 us.)
+          auto run = [&](auto both) {
+            constexpr bool BOTH = decltype(both)::value;
+            constexpr int STEP = BOTH ? 1 : 2;
+            if (!BOTH && t0 == 1) pass(0);
+            if (!ok || t0 >= nt || !(ok = landed(e0 + 2 * t0))) return;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               issue_s(e0 + 2 * t0, h);
               sm100::mma_commit(&sh.s_full[w][h]);
             }
-          }
-          for (int t = t0; ok && t < nt; t += step) {
-            const int kx = e0 + 2 * (t + step), vx = e0 + 2 * t + 1;    // the next tile's K, this one's V
-            const bool next = t + step < nt;
-            ok = landed(vx) && (!next || landed(kx));
+            int t = t0;
+            for (; t + STEP < nt; t += STEP) {
+              const int kx = e0 + 2 * (t + STEP), vx = e0 + 2 * t + 1;    // the next tile's K, this one's V
+              ok = landed(vx);
+              if (!BOTH) pass(t + 1);
+              ok = ok && landed(kx);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                ok = ok && sm100::mbar_wait(&sh.p_full[w][h], p_phase & 1, abort_flag);
+                if (!ok) return;
+                issue_o(vx, h, h == 1 || t > t0 ? 1u : 0u);
+                issue_s(kx, h);
+                sm100::mma_commit(&sh.s_full[w][h]);
+              }
+              ++p_phase;
+            }
+            // the last tile: the signs that O_w has taken its halves
+            ok = landed(e0 + 2 * t + 1);
+            if (!BOTH && t + 1 < nt) pass(t + 1);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               ok = ok && sm100::mbar_wait(&sh.p_full[w][h], p_phase & 1, abort_flag);
-              if (!ok) break;
-              issue_o(vx, h, h == 1 || t > t0 ? 1u : 0u);
-              if (next) issue_s(kx, h);
-              // with no next tile: the sign that O_w has taken this half
-              sm100::mma_commit(&sh.s_full[w][h]);
+              if (!ok) return;
+              issue_o(e0 + 2 * t + 1, h, h == 1 || t > t0 ? 1u : 0u);
+              sm100::mma_commit(h == 0 ? &sh.o_half[w] : &sh.o_full[w]);
             }
-            if (!ok) break;
             ++p_phase;
-          }
+          };
+          if (two) run(std::true_type{});
+          else run(std::false_type{});
           e0 += 2 * nt;
         }
         if (!ok) give_up();
@@ -1473,7 +1505,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const int st = tid - 32 * CH_SOFT_WARP0;               // 0 .. 255
     const int tok = row / p.GB, head = row - tok * p.GB;   // of this row in its tile
-    uint32_t s_phase = 0, j_phase = 0;
+    uint32_t s_phase = 0, o_phase = 0, j_phase = 0;
     int e0 = 0;                                            // ring element of the segment's first K
     const bool frees = quarter == 0 && lane == 0;          // tells the loader what the group's products have read
     bool ok = warp_wait(&sh.tm_ready, 0u) && warp_wait(&sh.tk_done, 0u) && tk_ok;   // (the token phase used m and l)
@@ -1509,11 +1541,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
       const bool some = __any_sync(0xffffffffu, valid);
       float m_ref = -INFINITY, l_sum = 0.f;
       const int step = two ? 1 : 2, t0 = two ? 0 : w;
-      // ring element x is read; a tile that one group alone uses counts for both
-      auto release = [&](int x) {
-        sm100::mbar_arrive(&sh.empty[x % SLOTS]);
-        if (!two) sm100::mbar_arrive(&sh.empty[x % SLOTS]);
-      };
+      auto release = [&](int x) { sm100::mbar_arrive(&sh.empty[x % SLOTS]); };   // ring element x is read
       for (int t = t0; ok && t < g.nt; t += step) {
         for (int h = 0; ok && h < 2; ++h) {
           ok = warp_wait(&sh.s_full[w][h], s_phase & 1);
@@ -1542,7 +1570,10 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
             const bool masked = k0 + CH_STEP - 1 > pos_least || k0 < lo_most;
             // The products before this step are complete when the other half's next scores are, issued after them (in
             // the last step: the sign in their place); before the first step there are none.
-            auto at_rest = [&]() { return warp_wait(&sh.s_full[w][h ^ 1], (h ? s_phase + 1 : s_phase) & 1); };
+            auto at_rest = [&]() {
+              if (h == 1 && t + step >= g.nt) return warp_wait(&sh.o_half[w], o_phase & 1);
+              return warp_wait(&sh.s_full[w][h ^ 1], (h ? s_phase + 1 : s_phase) & 1);
+            };
             ok = softmax_step<D>(s_addr + 64u * h, o_addr, masked, lo - k0, pos - k0, valid, p.c, m_ref, l_sum,
                                  &sh.p_full[w][h], at_rest);
           } else if (lane == 0) {
@@ -1552,9 +1583,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
         ++s_phase;
       }
       if (ok && t0 < g.nt) {
-        // O_w has taken both halves of the last tile
-        ok = warp_wait(&sh.s_full[w][0], s_phase & 1) && warp_wait(&sh.s_full[w][1], s_phase & 1);
-        ++s_phase;
+        ok = warp_wait(&sh.o_full[w], o_phase & 1);        // O_w has taken the last tile
+        ++o_phase;
         if (ok && frees) release(e0 + 2 * (t0 + (g.nt - 1 - t0) / step * step) + 1);
       }
       if (!ok) break;
@@ -1676,8 +1706,8 @@ cudaError_t launch_shape(eagle_ctx* ctx, const ChunkParams& p, const CUtensorMap
   const cudaError_t e =
       smem_limit_once(reinterpret_cast<const void*>(chunk_attn_kernel<D>), static_cast<int>(chunk_smem<D>()));
   if (e != cudaSuccess) return e;
-  return launch_pdl(chunk_attn_kernel<D>, dim3(ctx->sm_count), dim3(CH_THREADS), chunk_smem<D>(), st, p, qm, km, vm, tkm,
-                    tvm);
+  return launch_pdl(chunk_attn_kernel<D>, dim3(ctx->sm_count), dim3(CH_THREADS), chunk_smem<D>(), st, p, qm, km, vm,
+                    tkm, tvm);
 }
 
 }  // namespace
