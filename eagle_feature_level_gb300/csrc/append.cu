@@ -325,9 +325,9 @@ cudaError_t launch_append(eagle_ctx* ctx, const AppendLaunch& A, cudaStream_t st
   p.pos = A.pos;
   p.len_out = A.len_out;
   p.status = A.status;
-  // Few rows spread over the SMs, one or two a CTA; with many a CTA's setup pays from 4 and then 8 on.  64/8 heads, 1 / 2 /
-  // 4 / 8 rows a CTA: 304 rows 5.6 / 5.8 / 8.1 / 13.3 us, 608: 8.5 / 7.6 / 8.8 / 13.2, 1216: 14.6 / 14.0 / 13.1 / 17.7,
-  // 4864: 50 / 43 / 40 / 45, 9728: 93 / 78 / 75 / 74.
+  // Few rows spread over the SMs, one or two a CTA; with many a CTA's setup pays from 4 and then 8 on.  64/8 heads,
+  // 1 / 2 / 4 / 8 rows a CTA: 304 rows 5.6 / 5.8 / 8.1 / 13.3 us, 608: 8.5 / 7.6 / 8.8 / 13.2, 1216: 14.6 / 14.0 /
+  // 13.1 / 17.7, 4864: 50 / 43 / 40 / 45, 9728: 93 / 78 / 75 / 74.
   const int per_sm = ceil_div(A.rows->n_rows, ctx->sm_count);
   p.tile = per_sm <= 2 ? 1 : per_sm <= 4 ? 2 : per_sm <= 48 ? 4 : AP_ROWS;
   p.row_ctas = ceil_div(A.rows->n_rows, p.tile);
