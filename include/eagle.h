@@ -519,7 +519,8 @@ eagle_status eagle_fuse_features(eagle_ctx* ctx, const uint16_t* w_fuse, int ld_
  * everything before them (eagle_chunk_attn), and the blocks that hold a paged
  * cache are handed out, shared, taken back and packed on the device
  * (eagle_pages_*), with no host round trip: every call can be captured in a
- * CUDA graph and replayed on other lengths.
+ * CUDA graph and replayed on other lengths.  As everywhere, calls (and graph
+ * replays) on one workspace are ordered: one stream, or events between them.
  */
 
 /* New rows of a batch, packed: request b's are the rows row_start[b] ..
