@@ -481,6 +481,15 @@ def test_attention_short_prompts_between_long_ones(heads):
     attention_case(heads, 16, lens, new, seed=50)
 
 
+@pytest.mark.parametrize("heads,requests", [((40, 8, 128), 12), ((16, 4, 64), 21)], ids=["dh128", "dh64"])
+def test_attention_long_decoding_beside_prompts(heads, requests):
+    """Enough single tokens over long prefixes that they keep their own phase beside a prompt's tiles."""
+    lens = [4000 - 7 * i for i in range(requests)] + [300, 200]
+    new = [1] * (requests - 1) + [2, 150, 200]
+    attention_case(heads, 16, lens, new, seed=51)
+    attention_case(heads, 0, lens, new, window=3500, seed=52)
+
+
 def test_attention_hundreds_of_requests():
     rng = random.Random(5)
     eng = R.Engine(dict(d=256, n_q_heads=4, n_kv_heads=2, head_dim=64, d_ff=64, vocab=64), max_batch=301, max_rows=8,
