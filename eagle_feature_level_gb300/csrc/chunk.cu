@@ -575,6 +575,7 @@ __device__ __forceinline__ bool softmax_step(uint32_t s_addr, uint32_t o_addr, b
   if (__any_sync(0xffffffffu, valid && m_ref == -INFINITY)) {
     const float mt = most();
     if (m_ref == -INFINITY) m_ref = mt;        // nothing summed yet
+    __syncwarp();
   }
   exps();
   const bool raise = valid && sum.x + sum.y > CH_RAISE;
@@ -596,6 +597,7 @@ __device__ __forceinline__ bool softmax_step(uint32_t s_addr, uint32_t o_addr, b
     }
     l_sum *= f;
     if (raise) m_ref = mt;
+    __syncwarp();
     exps();
   }
 #pragma unroll
@@ -921,6 +923,7 @@ __device__ __forceinline__ void token_segment(const ChunkParams& p, const CUtens
             }
           }
         }
+      __syncwarp();
     }
     uint32_t b[NT][2];
 #pragma unroll
@@ -954,7 +957,10 @@ __device__ __forceinline__ void token_segment(const ChunkParams& p, const CUtens
       for (int d = 4; d < 32; d <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], d);
 }
 
-__device__ __forceinline__ void all_soft() { asm volatile("bar.sync 1, %0;" ::"n"(CH_SOFT_THREADS) : "memory"); }
+__device__ __forceinline__ void all_soft() {
+  __syncwarp();
+  asm volatile("bar.sync 1, %0;" ::"n"(CH_SOFT_THREADS) : "memory");
+}
 __device__ __forceinline__ void store_bf16x4(uint16_t* dst, float4 v, float z) {
   const __nv_bfloat162 a = __floats2bfloat162_rn(v.x * z, v.y * z), b = __floats2bfloat162_rn(v.z * z, v.w * z);
   *reinterpret_cast<uint2*>(dst) =
@@ -1219,6 +1225,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
     if (lane == 0) sm100::mbar_arrive(&sh.tm_ready);
     pdl_trigger();
   }
+  __syncwarp();
   const uint32_t sbase = sm100::smem_u32(sm);
   const uint32_t rbase = sbase + 2 * S::TILE;
   // K and V tiles: bytes from 8 rows to the next 8, and from elements 0 - 63 to 64 - 127
@@ -1551,6 +1558,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
             release(e0 + 2 * t);
             if (t + step >= g.nt) sm100::mbar_arrive(&sh.q_empty);
           }
+          __syncwarp();
           sm100::tc_fence_after();
           if (some) {
             const int k0 = (g.kt0 + t) * CH_KEYS + CH_STEP * h;
@@ -1586,6 +1594,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
         ok = warp_wait(&sh.o_full[w], o_phase & 1);        // O_w has taken the last tile
         ++o_phase;
         if (ok && frees) release(e0 + 2 * (t0 + (g.nt - 1 - t0) / step * step) + 1);
+        __syncwarp();
       }
       if (!ok) break;
       e0 += 2 * g.nt;
@@ -1630,34 +1639,37 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) o[j] = fmaf(a[k], v[j], o[j]);
                   }
+                  __syncwarp();
                 }
             }
           }
-          if (!valid) continue;
-          if (l_row == 0.f) {                  // no key seen: whatever the tile's products left
+          if (valid) {
+            if (l_row == 0.f) {                // no key seen: whatever the tile's products left
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = 0.f;
-          }
-          if (g.whole) {
-            uint16_t* dst = p.out + (static_cast<size_t>(g.row0) + t_item) * p.ld_o + (g.head0 + head) * p.dh + cc;
+              for (int j = 0; j < 32; ++j) o[j] = 0.f;
+            }
+            if (g.whole) {
+              uint16_t* dst = p.out + (static_cast<size_t>(g.row0) + t_item) * p.ld_o + (g.head0 + head) * p.dh + cc;
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              if (cc + 16 * q < p.dh) {
-                uint32_t x[8];
+              for (int q = 0; q < 2; ++q) {
+                if (cc + 16 * q < p.dh) {
+                  uint32_t x[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  const __nv_bfloat162 h = __floats2bfloat162_rn(o[16 * q + 2 * j] * inv, o[16 * q + 2 * j + 1] * inv);
-                  x[j] = *reinterpret_cast<const uint32_t*>(&h);
+                  for (int j = 0; j < 8; ++j) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(o[16 * q + 2 * j] * inv, o[16 * q + 2 * j + 1] * inv);
+                    x[j] = *reinterpret_cast<const uint32_t*>(&h);
+                  }
+                  store16(p, dst + 16 * q, x);
                 }
-                store16(p, dst + 16 * q, x);
               }
-            }
-          } else {
+            } else {
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-              reinterpret_cast<float4*>(part)[(cc / 4 + q) * (2 * CH_ROWS) + r_item] =
-                  make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+              for (int q = 0; q < 8; ++q)
+                reinterpret_cast<float4*>(part)[(cc / 4 + q) * (2 * CH_ROWS) + r_item] =
+                    make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            }
           }
+          __syncwarp();                        // the next columns' load is the whole warp's
         }
       }
       if (!g.whole && valid && (two || w == 0)) {

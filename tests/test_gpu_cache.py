@@ -490,6 +490,19 @@ def test_attention_long_decoding_beside_prompts(heads, requests):
     attention_case(heads, 0, lens, new, window=3500, seed=52)
 
 
+@pytest.mark.parametrize("heads", [(20, 2, 128), (10, 2, 128), (12, 1, 64), (7, 1, 64)],
+                         ids=lambda h: "x".join(map(str, h)))
+def test_attention_rows_that_end_inside_a_warp(heads):
+    """Groups whose tokens do not fill a tile's 128 rows, and items whose tokens end inside a warp's 32: lanes with and
+    without a row read the same accumulator column by column.  Items of one and of two tiles, whole and split."""
+    T = 128 // (heads[0] // heads[1])
+    lens = [2 * T + 5, T - 1, 2500, 1 + T, 129, 700, 4, 300]
+    new = [2 * T + 5, T - 1, T + 3, 1 + T, 2, 333, 4, T // 2 + 1]
+    attention_case(heads, 16, lens, new, seed=60)
+    attention_case(heads, 0, [3000], [2 * T - 1], seed=61)                    # few items, each split over many CTAs
+    attention_case(heads, 16, lens * 4, new * 4, window=150, seed=62)         # many short ones
+
+
 def test_attention_hundreds_of_requests():
     rng = random.Random(5)
     eng = R.Engine(dict(d=256, n_q_heads=4, n_kv_heads=2, head_dim=64, d_ff=64, vocab=64), max_batch=301, max_rows=8,
