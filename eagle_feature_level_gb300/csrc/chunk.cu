@@ -1609,6 +1609,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
         sh.l[w][row] = l_sum;
         ok = join();
         if (!ok) break;
+        sm100::tc_fence_after();               // the other group saw its products complete; its O is read here too
         const float m0 = sh.m[0][row], m1 = sh.m[1][row];
         m_row = fmaxf(m0, m1);
         a[0] = m0 == -INFINITY ? 0.f : sm100::exp2(m0 - m_row);

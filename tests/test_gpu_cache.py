@@ -503,6 +503,17 @@ def test_attention_rows_that_end_inside_a_warp(heads):
     attention_case(heads, 16, lens * 4, new * 4, window=150, seed=62)         # many short ones
 
 
+@pytest.mark.parametrize("heads", [(8, 2, 128), (4, 2, 64)], ids=["dh128", "dh64"])
+def test_attention_one_tile_items_over_many_key_tiles(heads):
+    """Items of one query tile: the softmax groups share the key tiles, and each reads both groups' accumulators.  Long
+    ones back to back on a CTA, of even and odd numbers of key tiles."""
+    T = 128 // (heads[0] // heads[1])
+    lens = [128 * (2 + i % 7) + i for i in range(60)]
+    new = [T - i % 5 for i in range(60)]
+    attention_case(heads, 16, lens, new, seed=63)
+    attention_case(heads, 0, lens[:5], new[:5], seed=64)
+
+
 def test_attention_hundreds_of_requests():
     rng = random.Random(5)
     eng = R.Engine(dict(d=256, n_q_heads=4, n_kv_heads=2, head_dim=64, d_ff=64, vocab=64), max_batch=301, max_rows=8,
