@@ -1548,17 +1548,16 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
       const bool some = __any_sync(0xffffffffu, valid);
       float m_ref = -INFINITY, l_sum = 0.f;
       const int step = two ? 1 : 2, t0 = two ? 0 : w;
-      auto release = [&](int x) { sm100::mbar_arrive(&sh.empty[x % SLOTS]); };   // ring element x is read
+      auto release = [&](int x) { sm100::mbar_arrive_if(&sh.empty[x % SLOTS], frees); };   // ring element x is read
       for (int t = t0; ok && t < g.nt; t += step) {
         for (int h = 0; ok && h < 2; ++h) {
           ok = warp_wait(&sh.s_full[w][h], s_phase & 1);
           if (!ok) break;
-          if (h == 1 && frees) {               // the tile's scores are complete, and so is what was issued before them
+          if (h == 1) {                        // the tile's scores are complete, and so is what was issued before them
             if (t > t0) release(e0 + 2 * (t - step) + 1);
             release(e0 + 2 * t);
-            if (t + step >= g.nt) sm100::mbar_arrive(&sh.q_empty);
+            if (t + step >= g.nt) sm100::mbar_arrive_if(&sh.q_empty, frees);
           }
-          __syncwarp();
           sm100::tc_fence_after();
           if (some) {
             const int k0 = (g.kt0 + t) * CH_KEYS + CH_STEP * h;
@@ -1593,8 +1592,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
       if (ok && t0 < g.nt) {
         ok = warp_wait(&sh.o_full[w], o_phase & 1);        // O_w has taken the last tile
         ++o_phase;
-        if (ok && frees) release(e0 + 2 * (t0 + (g.nt - 1 - t0) / step * step) + 1);
-        __syncwarp();
+        if (ok) release(e0 + 2 * (t0 + (g.nt - 1 - t0) / step * step) + 1);
       }
       if (!ok) break;
       e0 += 2 * g.nt;
