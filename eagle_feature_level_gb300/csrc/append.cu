@@ -29,7 +29,7 @@ namespace {
 
 constexpr int AP_THREADS = 256;
 constexpr int AP_WARPS = AP_THREADS / 32;
-constexpr int AP_ROWS = 8;                  // rows of a CTA at most
+constexpr int AP_ROWS = AP_WARPS;           // rows of a CTA at most
 constexpr int AP_UNITS = 3;                  // units of a thread in flight
 
 struct AppendParams {
@@ -164,64 +164,21 @@ __device__ __forceinline__ void unit2(const AppendParams& p, const float2* cs, c
   store1(out + b, y);
 }
 
-// T: element type of the rows (uint16_t: bf16 bits, or float); WIDE: units of
-// 16 elements (rot_dim a multiple of 16, so that a unit's 16-byte loads are
-// aligned) or of 2 (4864 rows of 64/8 heads: 45 us as 16, 112 as 2).
+// Rows r0 .. r0 + rows - 1, each at its place.  T: element type of the rows
+// (uint16_t: bf16 bits, or float); WIDE: units of 16 elements (rot_dim a
+// multiple of 16, so that a unit's 16-byte loads are aligned) or of 2 (4864
+// rows of 64/8 heads: 45 us as 16, 112 as 2).
 template <typename T, bool WIDE>
-__global__ void __launch_bounds__(AP_THREADS, 3) append_kernel(const __grid_constant__ AppendParams p) {
-  const LaunchStamp ls(p.stamp);
-  __shared__ float2 s_cs[AP_ROWS][EAGLE_MAX_ROPE_PAIRS];
-  __shared__ long long s_at[AP_ROWS];        // cache row, -1: not written
-  __shared__ int s_pos[AP_ROWS];
-  __shared__ int s_any[AP_ROWS];             // the row belongs to a request
-  pdl_wait();
-  ls.waited();
-  pdl_trigger();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (static_cast<int>(blockIdx.x) >= p.row_ctas) {
-    // the requests' new lengths
-    const int b = (static_cast<int>(blockIdx.x) - p.row_ctas) * AP_WARPS + warp;
-    if (b >= p.rows.B) return;
-    int lo, hi;
-    const bool ok = request_rows(p.rows, b, lo, hi);
-    const int L = p.len[b];
-    const bool room = cache_takes(p.paged, p.cap, b, L, hi - lo, lane);
-    if (lane == 0) {
-      p.len_out[b] = room ? L + (hi - lo) : L;
-      if (!ok) set_status(p.status, EAGLE_ERR_INVALID_ARG);
-      if (!room) set_status(p.status, EAGLE_ERR_CAPACITY);
-    }
-    return;
-  }
-  const int r0 = blockIdx.x * p.tile;
-  const int rows = min(p.tile, p.rows.n_rows - r0);
-  for (int w = warp; w < rows; w += AP_WARPS) {
-    const int r = r0 + w;
-    const int b = request_of_row(p.rows, r, lane);
-    long long at = -1;
-    int pos = 0;
-    if (b >= 0) {
-      int lo, hi;
-      request_rows(p.rows, b, lo, hi);
-      const int L = p.len[b], i = r - lo;
-      pos = p.pos ? p.pos[r] : L + i;
-      if (cache_takes(p.paged, p.cap, b, L, hi - lo, lane))
-        at = p.paged.table ? paged_row(p.paged, b, L + i) : static_cast<long long>(b) * p.cap + L + i;
-    }
-    if (lane == 0) {
-      s_at[w] = at;
-      s_pos[w] = pos;
-      s_any[w] = b >= 0;
-    }
-  }
-  __syncthreads();
+__device__ __forceinline__ void append_rows(const AppendParams& p, int r0, int rows, int hq,
+                                            float2 (*s_cs)[EAGLE_MAX_ROPE_PAIRS], const long long* s_at,
+                                            const int* s_pos, const int* s_any) {
+  const int tid = threadIdx.x;
   const int pairs = p.rot / 2;
   for (int i = tid; i < rows * pairs; i += AP_THREADS) {
     const int r = i / pairs, j = i - r * pairs;
     s_cs[r][j] = turn_of(p.turn[j], s_pos[r], p.mscale);
   }
   __syncthreads();
-  const int hq = p.q ? p.hq : 0;
   const int heads = hq + 2 * p.hkv;
   if (WIDE) {
     // A thread keeps one unit's place in a head, and a row's sines and cosines for it in registers, over the row's
@@ -291,6 +248,81 @@ __global__ void __launch_bounds__(AP_THREADS, 3) append_kernel(const __grid_cons
               (is_v ? p.vc : p.kc) + (static_cast<size_t>(at) * p.hkv + hk) * p.dh, u, !is_v && 2 * u < p.rot);
       }
     }
+  }
+}
+
+template <typename T, bool WIDE>
+__global__ void __launch_bounds__(AP_THREADS, 3) append_kernel(const __grid_constant__ AppendParams p) {
+  const LaunchStamp ls(p.stamp);
+  __shared__ float2 s_cs[AP_ROWS][EAGLE_MAX_ROPE_PAIRS];
+  __shared__ long long s_at[AP_ROWS];        // cache row, -1: not written
+  __shared__ int s_pos[AP_ROWS];
+  __shared__ int s_any[AP_ROWS];             // the row belongs to a request
+  pdl_wait();
+  ls.waited();
+  pdl_trigger();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int hq = p.q ? p.hq : 0;
+  // packed row r as the CTA's row w, of request b (-1: none)
+  auto place = [&](int w, int r, int b) {
+    long long at = -1;
+    int pos = 0;
+    if (b >= 0) {
+      int lo, hi;
+      request_rows(p.rows, b, lo, hi);
+      const int L = p.len[b], i = r - lo;
+      pos = p.pos ? p.pos[r] : L + i;
+      if (cache_takes(p.paged, p.cap, b, L, hi - lo, lane))
+        at = p.paged.table ? paged_row(p.paged, b, L + i) : static_cast<long long>(b) * p.cap + L + i;
+    }
+    if (lane == 0) {
+      s_at[w] = at;
+      s_pos[w] = pos;
+      s_any[w] = b >= 0;
+    }
+  };
+  if (static_cast<int>(blockIdx.x) < p.row_ctas) {
+    const int r0 = blockIdx.x * p.tile;
+    const int rows = min(p.tile, p.rows.n_rows - r0);
+    for (int w = warp; w < rows; w += AP_WARPS) place(w, r0 + w, request_of_row(p.rows, r0 + w, lane));
+    __syncthreads();
+    append_rows<T, WIDE>(p, r0, rows, hq, s_cs, s_at, s_pos, s_any);
+    return;
+  }
+  // the requests' new lengths
+  const int b0 = (static_cast<int>(blockIdx.x) - p.row_ctas) * AP_WARPS, b = b0 + warp;
+  bool found = true;                         // the CTAs of rows find the request's rows
+  if (b < p.rows.B) {
+    int lo, hi;
+    const bool ok = request_rows(p.rows, b, lo, hi);
+    const int L = p.len[b];
+    const bool room = cache_takes(p.paged, p.cap, b, L, hi - lo, lane);
+    if (lane == 0) {
+      p.len_out[b] = room ? L + (hi - lo) : L;
+      if (!ok) set_status(p.status, EAGLE_ERR_INVALID_ARG);
+      if (!room) set_status(p.status, EAGLE_ERR_CAPACITY);
+    }
+    if (hi > lo) found = request_of_row(p.rows, lo, lane) == b;
+    if (hi > lo + 1) found = found && request_of_row(p.rows, hi - 1, lane) == b;
+  }
+  if (__syncthreads_and(found)) return;
+  // Other requests' starts mislead the search: the rows it does not give to these requests are appended here, so that
+  // a request always has all its rows.  A query is turned once, here where the search gives its row to no request.
+  for (int e = b0; e < min(b0 + AP_WARPS, p.rows.B); ++e) {
+    int lo, hi;
+    request_rows(p.rows, e, lo, hi);
+    for (int x = lo; x < hi; x += AP_ROWS)
+      for (int q = 0; q < 2; ++q) {
+        const int r = x + warp;
+        if (r < hi) {
+          const int s = request_of_row(p.rows, r, lane);
+          const bool turns = s < 0 && first_request_of_row(p.rows, r, lane) == e;
+          place(warp, r, s != e && turns == (q == 1) ? e : -1);
+        }
+        __syncthreads();
+        append_rows<T, false>(p, x, min(AP_ROWS, hi - x), q ? hq : 0, s_cs, s_at, s_pos, s_any);
+        __syncthreads();
+      }
   }
 }
 

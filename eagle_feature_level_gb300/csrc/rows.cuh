@@ -11,8 +11,8 @@ struct PackedRows {
   int n_rows, B;
 };
 
-// Rows [lo, hi) of request b; none (and false) when the starts break
-// 0 <= lo <= hi <= n_rows.
+// Rows [lo, hi) of request b, by its own two starts; none (and false) when they
+// break 0 <= lo <= hi <= n_rows.
 __device__ __forceinline__ bool request_rows(const PackedRows& r, int b, int& lo, int& hi) {
   lo = r.start[b];
   hi = r.start[b + 1];
@@ -23,7 +23,10 @@ __device__ __forceinline__ bool request_rows(const PackedRows& r, int b, int& lo
 
 // The request that holds packed row `row` (every lane of a warp calls it; the
 // result is the same in all), or -1: the first whose end passes the row, by
-// a 32-way search of the ends, confirmed against that request's bounds.
+// a 32-way search of the ends, confirmed against that request's bounds.  Where
+// starts out of order mislead the search, a row may have a request that it
+// does not find.  The place it arrives at never goes back as the row goes up,
+// so a request it finds for its first and last row it finds for all between.
 __device__ __forceinline__ int request_of_row(const PackedRows& r, int row, int lane) {
   int lo = 0, n = r.B;    // the answer is in [lo, lo + n], r.B when no end passes the row
   while (n > 0) {
@@ -39,6 +42,18 @@ __device__ __forceinline__ int request_of_row(const PackedRows& r, int row, int 
   if (lo >= r.B) return -1;
   int a, z;
   return request_rows(r, lo, a, z) && row >= a && row < z ? lo : -1;
+}
+
+// The first request that holds a row by its own two starts, or -1, whatever
+// the others are.
+__device__ __forceinline__ int first_request_of_row(const PackedRows& r, int row, int lane) {
+  for (int b0 = 0; b0 < r.B; b0 += 32) {
+    int a = 0, z = 0;
+    if (b0 + lane < r.B) request_rows(r, b0 + lane, a, z);
+    const unsigned who = __ballot_sync(0xffffffffu, row >= a && row < z);
+    if (who) return b0 + __ffs(who) - 1;
+  }
+  return -1;
 }
 
 // Whether a cache takes n more rows of request b at length L: within cap and,

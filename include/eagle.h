@@ -527,8 +527,10 @@ eagle_status eagle_fuse_features(eagle_ctx* ctx, const uint16_t* w_fuse, int ld_
  * row_start[b + 1] - 1 of the packed buffers, 0 <= row_start[b] <=
  * row_start[b + 1] <= n_rows.  Requests may have no rows; rows outside every
  * request are neither read nor written.  Starts that break these bounds set
- * EAGLE_ERR_INVALID_ARG in the status word; the requests they concern are
- * treated as having no rows. */
+ * EAGLE_ERR_INVALID_ARG in the status word; the requests they concern -- each by
+ * its own two starts -- are treated as having no rows, the others have theirs.
+ * (Others may then share rows: each appends them, and the row's q_out and its
+ * attention's output are those of one of them.) */
 typedef struct {
   const int32_t* row_start;  /* [B + 1] (device) */
   int n_rows;                /* rows of the packed buffers, >= 1 */

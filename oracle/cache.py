@@ -52,6 +52,12 @@ def rotate(x: np.ndarray, pos: Sequence[int], freq: np.ndarray, interleaved: boo
     return y
 
 
+def rows_of(row_start: Sequence[int], n_rows: int) -> List[Tuple[int, int]]:
+    """The packed rows [lo, hi) of each request by its own two starts; (0, 0), none, where they break
+    0 <= lo <= hi <= n_rows."""
+    return [(a, z) if 0 <= a <= z <= n_rows else (0, 0) for a, z in zip(row_start, row_start[1:])]
+
+
 def chunk_attention(q: np.ndarray, k: np.ndarray, v: np.ndarray, scale: float, window: int = 0
                     ) -> Tuple[np.ndarray, np.ndarray, np.ndarray]:
     """q [n, Hq, dh], k and v [L, Hkv, dh] with the new rows last.  Returns the output, and for error bounds the

@@ -18,7 +18,7 @@ import torch
 from eagle_feature_level_gb300 import _binding as B
 from eagle_feature_level_gb300 import runtime as R
 from eagle_feature_level_gb300.runtime import _p
-from oracle.cache import OutOfBlocks, Pages, chunk_attention, frequencies, rotate
+from oracle.cache import OutOfBlocks, Pages, chunk_attention, frequencies, rotate, rows_of
 
 pytestmark = pytest.mark.gpu
 
@@ -108,7 +108,7 @@ def run_append(eng, c, row_start, n_rows, rope, q, k, v, q_out, pos=None, kv=Non
     return len_out
 
 
-def check_rotated(got, x, pos, freq, inter, m, u):
+def is_rotated(got, x, pos, freq, inter, m, u):
     want = rotate(x, pos, freq, inter, m)
     half = len(freq)
     first = np.arange(half) * 2 if inter else np.arange(half)
@@ -116,7 +116,11 @@ def check_rotated(got, x, pos, freq, inter, m, u):
     size = np.abs(x)
     size[..., first] = size[..., second] = (np.abs(x[..., first]) + np.abs(x[..., second])) * m
     size[..., 2 * half:] = 0.0
-    assert (np.abs(got - want) <= size * 2.0 ** -21 + u * np.abs(want)).all()
+    return np.abs(got - want) <= size * 2.0 ** -21 + u * np.abs(want)
+
+
+def check_rotated(*args):
+    assert is_rotated(*args).all()
 
 
 APPENDS = [  # heads, dtype, rot, interleaved, scaling, block size, lengths before, new rows
@@ -614,6 +618,100 @@ def test_two_graphs_on_one_workspace():
     assert eng.status() == 0
     for c, q, rs, o, again, g in work:
         assert torch.equal(o, again)
+    eng.close()
+
+
+# ---- starts that break their bounds ---------------------------------------------------
+
+def random_starts(seed):
+    """Starts in order but for a few, some of those out of bounds; more than a warp of requests in half of them."""
+    rng = random.Random(seed)
+    nb, n = rng.choice([(3, 6), (7, 12), (40, 60), (64, 50)])
+    rs = sorted(rng.randint(0, n) for _ in range(nb + 1))
+    for _ in range(rng.randint(1, 3)):
+        rs[rng.randrange(nb + 1)] = rng.choice([-1, 0, n, n + 1, 10 ** 9, rng.randint(0, n), rng.randint(0, n)])
+    return rs, n
+
+
+STARTS = [([0, 5, 3], 6), ([0, 100, 2, 6], 6), ([0, 4, 2, 6], 6), ([4, 6, 0, 3], 6), ([-1, 2, 6], 6), ([6, 6, 0, 6], 6),
+          ([2, 5, 1, 4, 6], 6), ([0, 3, 7, 2, 6], 6), ([0, 2, 4, 6], 6)] + [random_starts(i) for i in range(16)]
+
+
+@pytest.mark.parametrize("rs,n", STARTS, ids=lambda x: "_".join(map(str, x[:5])) if isinstance(x, list) else str(x))
+@pytest.mark.parametrize("bs", [0, 16])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_rows_and_lengths_agree_whatever_the_starts(rs, n, bs, in_place):
+    """A request has the rows of its own two starts, all of them, or none: appended, counted and attended alike."""
+    hq, hkv, dh = 4, 2, 64
+    eng = engine(hq, hkv, dh)
+    rope, freq, m = rope_and_freq(dh, dh, False, None)
+    nb, held = len(rs) - 1, rows_of(rs, n)
+    ctx = [(7 * b) % 23 for b in range(nb)]
+    c = Cache(ctx, [a + n for a in ctx], hkv, dh, bs, seed=nb)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    q, k, v = (torch.randn(n, h, dh, generator=g, device="cuda").to(torch.bfloat16) for h in (hq, hkv, hkv))
+    q0, q_out, out = q.clone(), q if in_place else torch.full_like(q, NAN), torch.full_like(q, NAN)
+    before = c.k.clone(), c.v.clone()
+    ln = run_append(eng, c, i32(rs), n, rope, q, k, v, q_out)
+    torch.cuda.synchronize()
+    broken = any(not 0 <= a <= z <= n for a, z in zip(rs, rs[1:]))
+    assert eng.status() == (INVALID_ARG if broken else 0)
+    assert ln.tolist() == [a + hi - lo for a, (lo, hi) in zip(ctx, held)]
+    attend(eng, c, i32(rs), q_out, out, kv=c.kv(ln))
+    torch.cuda.synchronize()
+    assert eng.status() == (INVALID_ARG if broken else 0)
+    owners = np.zeros(n, dtype=int)
+    for lo, hi in held:
+        owners[lo:hi] += 1
+    turned = np.zeros(n, dtype=bool)                       # a row's query turns once, by one of its requests' positions
+    for b, (lo, hi) in enumerate(held):
+        if lo == hi:
+            continue
+        pos, at = np.arange(ctx[b], ctx[b] + hi - lo), c.at(b, ctx[b], ctx[b] + hi - lo)
+        turned[lo:hi] |= is_rotated(f64(q_out[lo:hi]), f64(q0[lo:hi]), pos, freq, False, m, U).all((1, 2))
+        kc, vc = c.k.view(-1, hkv, dh)[at].clone(), c.v.view(-1, hkv, dh)[at].clone()
+        check_rotated(f64(kc), f64(k[lo:hi]), pos, freq, False, m, U)
+        assert torch.equal(vc, v[lo:hi])
+        kk, vv = (np.concatenate([f64(c.rows[b][i]), f64(x)]) for i, x in ((0, kc), (1, vc)))
+        if (owners[lo:hi] == 1).all():
+            check_attention(f64(out[lo:hi]), f64(q_out[lo:hi]), kk, vv, 1 / math.sqrt(dh), 0)
+        for now, old in zip((c.k, c.v), before):           # put back, to compare the rest
+            now.view(-1, hkv, dh)[at] = old.view(-1, hkv, dh)[at]
+    for now, old in zip((c.k, c.v), before):
+        assert torch.equal(now.view(torch.int16), old.view(torch.int16))
+    assert (turned == (owners > 0)).all()
+    free = torch.tensor(owners == 0, device="cuda")
+    assert torch.isnan(out[free]).all() and torch.isfinite(out[~free]).all()
+    assert torch.equal(q_out[free], q0[free]) if in_place else torch.isnan(q_out[free]).all()
+
+
+def test_append_broken_starts_among_many_requests():
+    """More requests than two levels of the search for a row's request reach, some prompts among them."""
+    hq, hkv, dh, nb, n = 4, 2, 64, 1100, 1500
+    eng = R.Engine(dict(d=256, n_q_heads=hq, n_kv_heads=hkv, head_dim=dh, d_ff=64, vocab=64), max_batch=nb, max_rows=8,
+                   max_expanded=1, max_children=1, max_tree=2, max_prefix=512, device="cuda")
+    rng = random.Random(7)
+    for broken in (0, 1, 3, 40):
+        rs = sorted(rng.choice([0, 40, 41, 300, 301, 1400, n, rng.randint(0, n), rng.randint(0, n)]) for _ in range(nb + 1))
+        for _ in range(broken):
+            rs[rng.randrange(nb + 1)] = rng.choice([-5, 0, n, n + 1, rng.randint(0, n), rng.randint(0, n)])
+        held = [(lo, hi) if hi - lo <= 512 else (0, 0) for lo, hi in rows_of(rs, n)]     # (no room for more)
+        k, v = (torch.randn(n, hkv, dh, device="cuda").to(torch.bfloat16) for _ in range(2))
+        kc = torch.full((nb, 512, hkv, dh), NAN, dtype=torch.bfloat16, device="cuda")
+        vc = kc.clone()
+        want_k, want_v = kc.clone(), vc.clone()
+        for b, (lo, hi) in enumerate(held):
+            want_k[b, :hi - lo], want_v[b, :hi - lo] = k[lo:hi], v[lo:hi]
+        ln = i32([0] * nb)
+        out = torch.full_like(ln, -7)
+        B.eagle_kv_append(eng.ctx, nb, B.eagle_rows(_p(i32(rs)), n), None, B.DTYPE_BF16, 0, 0, 0, 0, _p(k), k.stride(0),
+                          _p(v), v.stride(0), B.eagle_kv(_p(kc), _p(vc), 512, _p(ln)), None, _p(out),
+                          eng.ws.data_ptr(), eng.stream())
+        torch.cuda.synchronize()
+        assert (eng.status() == 0) == (held == list(zip(rs, rs[1:])))
+        assert out.tolist() == [hi - lo for lo, hi in held]
+        assert torch.equal(kc.view(torch.int16), want_k.view(torch.int16))
+        assert torch.equal(vc.view(torch.int16), want_v.view(torch.int16))
     eng.close()
 
 
