@@ -69,7 +69,7 @@ class eagle_draft_weights(C.Structure):
 
 
 class eagle_paging(C.Structure):
-    _fields_ = [("block_table", P), ("block_size", I), ("n_blocks", I)]
+    _fields_ = [("block_table", P), ("block_size", I), ("n_blocks", I), ("ref", P)]
 
 
 class eagle_kv(C.Structure):

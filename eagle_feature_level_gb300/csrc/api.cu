@@ -174,6 +174,7 @@ eagle_status check_paging(const eagle_paging* pg, int cap) {
   const int bs = pg->block_size;
   EAGLE_REQUIRE(bs >= 1 && (bs & (bs - 1)) == 0 && cap % bs == 0, EAGLE_ERR_INVALID_ARG);
   EAGLE_REQUIRE(pg->n_blocks >= 1, EAGLE_ERR_INVALID_ARG);
+  if (pg->ref) EAGLE_PTR(pg->ref);
   return EAGLE_OK;
 }
 

@@ -215,6 +215,13 @@ __device__ __forceinline__ long long paged_row(const PagedKv& pg, int b, int pos
   return (static_cast<long long>(blk) << pg.shift) + (pos & ((1 << pg.shift) - 1));
 }
 
+// Whether rows may be written to block `col` of request b's: allocated and,
+// where the counts are given, in no other table entry.
+__device__ __forceinline__ bool block_takes_rows(const PagedKv& pg, int b, int col) {
+  const int blk = pg.table[static_cast<size_t>(b) * pg.per_req + col];
+  return blk >= 0 && blk < pg.n_blocks && (pg.ref == nullptr || pg.ref[blk] <= 1);
+}
+
 __device__ __forceinline__ uint64_t globaltimer_ns() {
   uint64_t t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));

@@ -220,6 +220,7 @@ struct PagedKv {
   int shift;              // log2(block_size)
   int per_req;            // table entries per request (cap / block_size)
   int n_blocks;
+  const int32_t* ref;     // table entries that map each block, null: not looked at
 };
 
 inline PagedKv paged_of(const eagle_paging* pg, int cap) {
@@ -229,6 +230,7 @@ inline PagedKv paged_of(const eagle_paging* pg, int cap) {
   while ((1 << k.shift) < pg->block_size) ++k.shift;
   k.per_req = cap / pg->block_size;
   k.n_blocks = pg->n_blocks;
+  k.ref = pg->ref;
   return k;
 }
 

@@ -332,6 +332,9 @@ class PagedCache:
         cache.reserve(n_new)                      # blocks, and private copies of shared tails
         for each layer: cache.append(...); cache.attend(...)
         cache.advance()                           # the lengths now count the new rows
+    Where a reserve finds too few blocks it changes nothing, the status says so, and the appends behind it refuse the
+    sequences that lack a block or still share the one they would write: those keep their rows and lengths, the others
+    go on.  The page calls stand between such steps.
     `paging` and `kv(layer)` are what the round's verification attention and
     commit take, with the sequences as the batch (capacity `cap`)."""
 
@@ -353,7 +356,7 @@ class PagedCache:
         self.pages_c = B.eagle_pages(_p(self.table), _p(self.len), _p(self.ref), _p(self.scratch), n_seqs, per_seq,
                                      block_size, n_blocks)
         self.pools_c = B.eagle_pools([_p(t) for t in self.k], [_p(t) for t in self.v])
-        self.paging = B.eagle_paging(_p(self.table), block_size, n_blocks)
+        self.paging = B.eagle_paging(_p(self.table), block_size, n_blocks, _p(self.ref))
         self._kv = [B.eagle_kv(_p(k), _p(v), self.cap, _p(self.len), self.paging) for k, v in zip(self.k, self.v)]
         self._kv_next = [B.eagle_kv(_p(k), _p(v), self.cap, _p(self.len_next), self.paging)
                          for k, v in zip(self.k, self.v)]

@@ -159,11 +159,15 @@ typedef struct {
  * the table and the blocks: the library reads the table and never changes it.
  * Rows of an unallocated block inside a request's length read as zeros and set
  * EAGLE_ERR_INVALID_ARG in the status word; a commit whose rows would land in
- * an unallocated block is refused (EAGLE_ERR_CAPACITY, see eagle_commit). */
+ * an unallocated block is refused (EAGLE_ERR_CAPACITY, see eagle_commit).
+ * With ref, the blocks' reference counts (eagle_pages.ref), so is one whose rows
+ * would land in a block that another table entry maps too: after an
+ * eagle_pages_reserve that could not be served nobody's rows are overwritten. */
 typedef struct {
   const int32_t* block_table;  /* [B][cap / block_size] block ids (device), NULL: contiguous */
   int block_size;              /* rows per block */
   int n_blocks;                /* blocks in each pool */
+  const int32_t* ref;          /* [n_blocks] table entries that map each block (device), NULL: not looked at */
 } eagle_paging;
 
 /* A KV cache of one attention layer: [B][cap][Hkv][dh] bf16, or block pools
@@ -455,7 +459,8 @@ typedef struct {
  * no cache row of it is written, prefix_len / draft_len keep the old
  * lengths, its other outputs are unspecified, and EAGLE_ERR_CAPACITY is set
  * in the workspace's status word.  With target_paging, a request any of whose
- * 1 + a rows maps to an unallocated block is refused the same way. */
+ * 1 + a rows maps to an unallocated block is refused the same way, and (with
+ * target_paging->ref) one any of whose rows maps to a shared block. */
 eagle_status eagle_commit(eagle_ctx* ctx, int batch, const eagle_accept_out* acc,
                           const eagle_tree* tree, const float* f_true, int n_layers,
                           const uint16_t* const* k_tree_layers, const uint16_t* const* v_tree_layers,
@@ -594,13 +599,14 @@ eagle_status eagle_rope_plan(eagle_rope* out, int head_dim, int rot_dim, int int
  * rounded once.
  * The cache may be paged (kv.paging) and the draft's or a tree's own arena
  * (a contiguous cache of as many rows per request).  A request whose cache
- * cannot take all its rows (beyond kv.cap, or in unallocated blocks) writes
- * none of them and keeps its length (EAGLE_ERR_CAPACITY in the status word);
+ * cannot take all its rows (beyond kv.cap, in unallocated blocks or, with
+ * kv.paging.ref, in a block that other table entries map too) writes none of
+ * them and keeps its length (EAGLE_ERR_CAPACITY in the status word);
  * its q rows are rotated all the same.  A request without rows keeps its
  * length, whatever that is (a padded batch's idle entries).  len_out must not
  * alias kv.len (EAGLE_ERR_INVALID_ARG).  Rows a block table maps to the same place -- a
  * block that two requests hold -- must be made private first
- * (eagle_pages_reserve). */
+ * (eagle_pages_reserve); without kv.paging.ref that is not checked. */
 eagle_status eagle_kv_append(eagle_ctx* ctx, int batch, const eagle_rows* rows, const eagle_rope* rope, int dtype,
                              const void* q, int ld_q, void* q_out, int ld_q_out, const void* k, int ld_k,
                              const void* v, int ld_v, const eagle_kv* kv, const int32_t* pos, int32_t* len_out,
@@ -674,7 +680,10 @@ eagle_status eagle_pages_fork(eagle_ctx* ctx, const eagle_pages* pages, int n, c
  * holders are writing.  Lengths do not change (eagle_kv_append and
  * eagle_commit move them).  All or nothing: when the free blocks do not
  * suffice for the whole call, or a sequence's rows pass per_seq blocks,
- * nothing changes and EAGLE_ERR_CAPACITY is set in the status word. */
+ * nothing changes and EAGLE_ERR_CAPACITY is set in the status word.  Appends
+ * and commits that follow without a look at the status (a captured step) then
+ * refuse every request that lacks a block or still shares one, given the
+ * counts (eagle_paging.ref); the others go on. */
 eagle_status eagle_pages_reserve(eagle_ctx* ctx, const eagle_pages* pages, const eagle_pools* pools,
                                  const int32_t* n_new, void* workspace, cudaStream_t stream);
 

@@ -1034,6 +1034,170 @@ def test_serving_step_captured():
     m.eng.close()
 
 
+@pytest.mark.parametrize("captured", [False, True], ids=["eager", "captured"])
+@pytest.mark.parametrize("forks", ["one writes", "both write", "all write"])
+def test_a_reserve_that_fails_costs_no_rows(captured, forks):
+    """Too few blocks for a step whose calls go on without a look at the status: sequences that share the block they
+    would write, or lack one, keep their rows and lengths, the others' rows are appended; with room it all works."""
+    heads, bs = (4, 2, 64), 16
+    m = Model(engine(*heads, fresh=True), 5, 8, bs, 7, seed=9)
+    x, out = m.buffers(80)
+    q_out = torch.zeros_like(out)
+    rs, n_new = i32([0] * 6), i32([0] * 5)
+    graph = None
+
+    def step(new):
+        nonlocal graph
+        m.fill(x)
+        rs.copy_(i32(starts(new)))
+        n_new.copy_(i32(new))
+        if graph is not None:
+            graph.replay()
+        else:
+            m.step(x, out, rs, n_new, q_out)
+        torch.cuda.synchronize()
+
+    step([40, 0, 0, 5, 14])                                # 3, 1 and 1 blocks of 7
+    m.check(x, out, q_out, [40, 0, 0, 5, 14])
+    m.c.fork(i32([0, 0]), i32([1, 2]))
+    m.c.release(i32([-1, 33, 40 if forks == "all write" else 0, -1, -1]))     # a shorter row of the shared tail; a third
+    m.hist[1] = [[t[:33] for t in h] for h in m.hist[0]]
+    if forks == "all write":
+        m.hist[2] = [list(h) for h in m.hist[0]]
+    if captured:
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            m.step(x, out, rs, n_new, q_out)
+    # two blocks are free: one for a copy, one for sequence 4's third row; sequence 3 wants 100 rows
+    new = {"one writes": [0, 1, 0, 27, 3], "both write": [2, 3, 0, 27, 3], "all write": [1, 1, 1, 27, 3]}[forks]
+    lens = m.c.len.tolist()
+    table, ref = m.c.table.clone(), m.c.ref.clone()
+    kept = [[t.view(-1, 2, 64)[rows_at(m.c, s, 0, lens[s])].clone() for t in m.c.k + m.c.v] for s in range(5)]
+    new[4] = 40                                            # ... and this one two more blocks: in all more than there are
+    step(new)
+    assert m.eng.status() == CAPACITY
+    assert torch.equal(m.c.table, table) and torch.equal(m.c.ref, ref)
+    assert m.c.len.tolist() == lens                        # every one of them shares its block or lacks one
+    new[3], new[4] = 3, 40                                 # one that needs nothing: its rows go in
+    step(new)
+    assert m.eng.status() == CAPACITY
+    lens[3] += 3
+    assert m.c.len.tolist() == lens
+    lo = sum(new[:3])
+    for l in range(2):
+        k, v = (x[l, lo:lo + 3, 4 + 2 * i:6 + 2 * i] for i in (0, 1))
+        at = rows_at(m.c, 3, lens[3] - 3, lens[3])
+        check_rotated(f64(m.c.k[l].view(-1, 2, 64)[at]), f64(k), np.arange(lens[3] - 3, lens[3]), m.freq, False, m.m, U)
+        assert torch.equal(m.c.v[l].view(-1, 2, 64)[at], v)
+        m.hist[3][l] = [np.concatenate([m.hist[3][l][0], f64(m.c.k[l].view(-1, 2, 64)[at])]),
+                        np.concatenate([m.hist[3][l][1], f64(v)])]
+    for s in range(5):
+        for t, w in zip(m.c.k + m.c.v, kept[s]):
+            assert torch.equal(t.view(-1, 2, 64)[rows_at(m.c, s, 0, w.shape[0])].view(torch.int16), w.view(torch.int16))
+    m.c.release(i32([-1, -1, -1, -1, 0]))                  # room again: the same rows for the forks
+    m.hist[4] = [[np.zeros((0, m.hkv, m.dh))] * 2 for _ in range(2)]
+    new[3], new[4] = 1, 0
+    step(new)
+    m.check(x, out, q_out, new)
+    m.eng.close()
+
+
+def rows_at(c, s, lo, hi):
+    """Flat pool rows of positions lo .. hi - 1 of sequence s of a PagedCache."""
+    j = torch.arange(lo, hi, device="cuda")
+    return c.table[s].long()[j // c.bs] * c.bs + j % c.bs
+
+
+def test_append_looks_at_counts_where_given():
+    """The counts are the caller's to give: without them a shared block is written as it always was."""
+    hq, hkv, dh = 4, 2, 64
+    eng = engine(hq, hkv, dh)
+    c = Cache([6, 3, 0], [12, 12, 12], hkv, dh, 4, seed=80)
+    ref = torch.zeros(c.k.shape[0], dtype=torch.int32, device="cuda")
+    ref[c.table.flatten().long()] = 1
+    k, v = (torch.randn(9, hkv, dh, device="cuda").to(torch.bfloat16) for _ in range(2))
+    before = c.k.clone()
+    for col, want in ((0, [9, 6, 0]), (1, [6, 6, 3]), (2, [6, 6, 3])):
+        c.k.copy_(before)
+        counts = ref.clone()
+        counts[c.table[0, 1 if col == 1 else 2].long()] = 2 if col else 1      # request 0 writes columns 1 and 2
+        counts[c.table[2, 0].long()] = 1 if col else 3                          # request 2 writes column 0
+        paging = B.eagle_paging(_p(c.table), 4, c.k.shape[0], _p(counts))
+        ln = run_append(eng, c, i32([0, 3, 6, 9]), 9, None, None, k, v, None,
+                        kv=B.eagle_kv(_p(c.k), _p(c.v), c.cap, _p(c.len), paging))
+        torch.cuda.synchronize()
+        assert eng.status() == CAPACITY and ln.tolist() == want
+        for b, (n, lo) in enumerate(zip(c.lens, (0, 3, 6))):
+            at = c.at(b, n, n + 3)
+            expect = k[lo:lo + 3] if want[b] > n else before.view(-1, hkv, dh)[at]
+            assert torch.equal(c.k.view(-1, hkv, dh)[at].view(torch.int16), expect.contiguous().view(torch.int16))
+    ln = run_append(eng, c, i32([0, 3, 6, 9]), 9, None, None, k, v, None)
+    torch.cuda.synchronize()
+    assert eng.status() == 0 and ln.tolist() == [9, 6, 3]
+    launches = B.eagle_launch_count(eng.ctx)
+    with pytest.raises(B.EagleError) as e:
+        run_append(eng, c, i32([0, 3, 6, 9]), 9, None, None, k, v, None, kv=B.eagle_kv(
+            _p(c.k), _p(c.v), c.cap, _p(c.len), B.eagle_paging(_p(c.table), 4, c.k.shape[0], _p(ref) + 4)))
+    assert e.value.code == ALIGN and B.eagle_launch_count(eng.ctx) == launches
+
+
+def test_commit_writes_no_shared_block():
+    """A commit after a fork whose reserve was left out: the forks keep their rows, the third request commits; after
+    the reserve all do."""
+    import eagle_synth as S
+    from eagle_feature_level_gb300.workload import dims_of, limits_for, load_round, standin
+    w = S.variant("13b_x8_eagle2", name="served", d=128, n_q_heads=4, n_kv_heads=2, head_dim=64, d_ff=344, vocab=1000,
+                  batch=3, prefix_range=(50, 200), weight_std=0.05, temps=(0.0,))
+    inp = S.round_inputs(w, 78, device="cuda")
+    eng = R.Engine(dims_of(w), max_prefix=512, device="cuda", **limits_for(w))
+    rd = R.Round(eng, R.plan_for(w.tree, w.top_k, w.depth, w.top_m), w.batch, inp["kv_cap"])
+    load_round(rd, inp)
+    rd.run(eng.weights(S.draft_weights(w, 78, device="cuda")), standin(inp))
+    torch.cuda.synchronize()
+    accepted = rd.accept_len.tolist()
+    bs = 64
+    m = Model(eng, 3, 512 // bs, bs, 8, seed=4)
+    new = [70, 67, 0]                                      # any path fits the blocks they have
+    assert rd.path_cap < bs - 6
+    x, out = m.buffers(sum(new))
+    m.fill(x)
+    m.step(x, out, i32(starts(new)), i32(new), torch.zeros_like(out))
+    m.c.fork(i32([1]), i32([2]))
+    lens = [70, 67, 67]
+
+    def commit():
+        kept = [[t.view(-1, 2, 64)[rows_at(m.c, s, 0, lens[s])].clone() for t in m.c.k + m.c.v] for s in range(3)]
+        pools = [t.clone() for t in m.c.k + m.c.v]
+        B.eagle_commit(eng.ctx, 3, rd.acc_c, rd.tree_c, _p(rd.f_true), [_p(rd.tree_k[0])] * 2, [_p(rd.tree_v[0])] * 2,
+                       [_p(t) for t in m.c.k], [_p(t) for t in m.c.v], m.c.cap, _p(m.c.len), rd.out_c, rd.draft_kv_c,
+                       rd.commit_c, eng.ws.data_ptr(), eng.stream(), target_paging=m.c.paging)
+        torch.cuda.synchronize()
+        for s in range(3):
+            for t, w in zip(m.c.k + m.c.v, kept[s]):
+                assert torch.equal(t.view(-1, 2, 64)[rows_at(m.c, s, 0, lens[s])].view(torch.int16), w.view(torch.int16))
+        return pools
+
+    def committed(s):
+        path, at = rd.path[s, :accepted[s] + 1].long(), rows_at(m.c, s, lens[s], lens[s] + accepted[s] + 1)
+        return all(torch.equal(t.view(-1, 2, 64)[at], tree[s][path]) for t, tree in
+                   zip(m.c.k + m.c.v, [rd.tree_k[0]] * 2 + [rd.tree_v[0]] * 2))
+
+    pools = commit()
+    assert eng.status() == CAPACITY
+    assert rd.prefix_len_out.tolist() == [lens[0] + 1 + accepted[0], 67, 67] and committed(0)
+    shared = int(m.c.table[1, 1])
+    for t, old in zip(m.c.k + m.c.v, pools):
+        assert torch.equal(t[shared].view(torch.int16), old[shared].view(torch.int16))
+    m.c.reserve(i32([rd.path_cap] * 3))
+    torch.cuda.synchronize()
+    commit()
+    assert eng.status() == 0
+    assert rd.prefix_len_out.tolist() == [n + 1 + a for n, a in zip(lens, accepted)]
+    assert all(committed(s) for s in range(3))
+    eng.close()
+
+
 def test_round_on_a_served_cache():
     """The cache the calls filled is what the round's verification attention and commit take: the tree's rows attend
     to it through its table, and the accepted path lands in blocks that reserve handed out."""
