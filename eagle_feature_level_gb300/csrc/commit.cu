@@ -58,10 +58,13 @@ __global__ void commit_kernel(const CommitParams p) {
   const int L = p.kv_len[b];
   // a request whose cache cannot take the path commits nothing (checked
   // alike by every CTA of the request; the state CTA reports it): the rows
-  // L .. L + a must exist and, in a paged cache, lie in allocated blocks of its own
+  // L .. L + a must exist and, in a paged cache, lie in allocated blocks, the
+  // first of which is the request's own
   bool room = L >= 0 && static_cast<long long>(L) + 1 + a <= p.kv_cap;
   if (room && p.paged.table)
-    for (int c = L >> p.paged.shift; room && c <= (L + a) >> p.paged.shift; ++c) room = block_takes_rows(p.paged, b, c);
+    for (int pos = L; room && pos <= L + a; pos = ((pos >> p.paged.shift) + 1) << p.paged.shift)
+      room = paged_row(p.paged, b, pos) >= 0;
+  if (room && p.paged.ref) room = !block_shared(p.paged, b, L);
   const bool draft_room = p.dk == nullptr || (p.draft_len[b] >= 0 && p.draft_len[b] < p.draft_cap);
   if (i == p.path_cap) {
     if (!room || !draft_room) {

@@ -215,11 +215,13 @@ __device__ __forceinline__ long long paged_row(const PagedKv& pg, int b, int pos
   return (static_cast<long long>(blk) << pg.shift) + (pos & ((1 << pg.shift) - 1));
 }
 
-// Whether rows may be written to block `col` of request b's: allocated and,
-// where the counts are given, in no other table entry.
-__device__ __forceinline__ bool block_takes_rows(const PagedKv& pg, int b, int col) {
-  const int blk = pg.table[static_cast<size_t>(b) * pg.per_req + col];
-  return blk >= 0 && blk < pg.n_blocks && (pg.ref == nullptr || pg.ref[blk] <= 1);
+// Whether another table entry maps the block that position pos of request b
+// lies in (pg.ref is given).  Of the blocks that new rows go to only the first,
+// partly filled one can have other holders: a fork shares the blocks that hold
+// rows, and those behind them come from eagle_pages_reserve.
+__device__ __forceinline__ bool block_shared(const PagedKv& pg, int b, int pos) {
+  const int blk = pg.table[static_cast<size_t>(b) * pg.per_req + (pos >> pg.shift)];
+  return blk >= 0 && blk < pg.n_blocks && pg.ref[blk] > 1;
 }
 
 __device__ __forceinline__ uint64_t globaltimer_ns() {

@@ -57,16 +57,20 @@ __device__ __forceinline__ int first_request_of_row(const PackedRows& r, int row
 }
 
 // Whether a cache takes n more rows of request b at length L: within cap and,
-// when paged, in allocated blocks that (where the counts are given) no other
-// table entry maps; none, whatever the length (every lane of a warp calls it;
-// the result is the same in all).
+// when paged, in allocated blocks, the first of which (where the counts are
+// given) no other table entry maps; none, whatever the length (every lane of a
+// warp calls it; the result is the same in all).
 __device__ __forceinline__ bool cache_takes(const PagedKv& pg, int cap, int b, int L, int n, int lane) {
   if (n == 0) return true;
   if (L < 0 || static_cast<long long>(L) + n > cap) return false;
   bool ok = true;
   if (pg.table) {
     const int last = (L + n - 1) >> pg.shift;
-    for (int c = (L >> pg.shift) + lane; c <= last; c += 32) ok = block_takes_rows(pg, b, c) && ok;
+    for (int c = (L >> pg.shift) + lane; c <= last; c += 32) {
+      const int blk = pg.table[static_cast<size_t>(b) * pg.per_req + c];
+      ok = ok && blk >= 0 && blk < pg.n_blocks;
+    }
+    if (pg.ref) ok = ok && !block_shared(pg, b, L);
   }
   return __all_sync(0xffffffffu, ok);
 }

@@ -160,9 +160,10 @@ typedef struct {
  * Rows of an unallocated block inside a request's length read as zeros and set
  * EAGLE_ERR_INVALID_ARG in the status word; a commit whose rows would land in
  * an unallocated block is refused (EAGLE_ERR_CAPACITY, see eagle_commit).
- * With ref, the blocks' reference counts (eagle_pages.ref), so is one whose rows
- * would land in a block that another table entry maps too: after an
- * eagle_pages_reserve that could not be served nobody's rows are overwritten. */
+ * With ref, the blocks' reference counts (eagle_pages.ref), so is one whose
+ * first row would land in a block that another table entry maps too (the only
+ * one of its rows' blocks that can be shared): after an eagle_pages_reserve
+ * that could not be served nobody's rows are overwritten. */
 typedef struct {
   const int32_t* block_table;  /* [B][cap / block_size] block ids (device), NULL: contiguous */
   int block_size;              /* rows per block */
@@ -460,7 +461,7 @@ typedef struct {
  * lengths, its other outputs are unspecified, and EAGLE_ERR_CAPACITY is set
  * in the workspace's status word.  With target_paging, a request any of whose
  * 1 + a rows maps to an unallocated block is refused the same way, and (with
- * target_paging->ref) one any of whose rows maps to a shared block. */
+ * target_paging->ref) one whose first row maps to a shared block. */
 eagle_status eagle_commit(eagle_ctx* ctx, int batch, const eagle_accept_out* acc,
                           const eagle_tree* tree, const float* f_true, int n_layers,
                           const uint16_t* const* k_tree_layers, const uint16_t* const* v_tree_layers,
@@ -600,8 +601,8 @@ eagle_status eagle_rope_plan(eagle_rope* out, int head_dim, int rot_dim, int int
  * The cache may be paged (kv.paging) and the draft's or a tree's own arena
  * (a contiguous cache of as many rows per request).  A request whose cache
  * cannot take all its rows (beyond kv.cap, in unallocated blocks or, with
- * kv.paging.ref, in a block that other table entries map too) writes none of
- * them and keeps its length (EAGLE_ERR_CAPACITY in the status word);
+ * kv.paging.ref, the first in a block that other table entries map too) writes
+ * none of them and keeps its length (EAGLE_ERR_CAPACITY in the status word);
  * its q rows are rotated all the same.  A request without rows keeps its
  * length, whatever that is (a padded batch's idle entries).  len_out must not
  * alias kv.len (EAGLE_ERR_INVALID_ARG).  Rows a block table maps to the same place -- a

@@ -1118,16 +1118,15 @@ def test_append_looks_at_counts_where_given():
     ref[c.table.flatten().long()] = 1
     k, v = (torch.randn(9, hkv, dh, device="cuda").to(torch.bfloat16) for _ in range(2))
     before = c.k.clone()
-    for col, want in ((0, [9, 6, 0]), (1, [6, 6, 3]), (2, [6, 6, 3])):
+    for shared, want in (((2, 0), [9, 6, 0]), ((0, 1), [6, 6, 3]), ((0, 0), [9, 6, 3])):
         c.k.copy_(before)
         counts = ref.clone()
-        counts[c.table[0, 1 if col == 1 else 2].long()] = 2 if col else 1      # request 0 writes columns 1 and 2
-        counts[c.table[2, 0].long()] = 1 if col else 3                          # request 2 writes column 0
+        counts[c.table[shared].long()] = 2                                      # of a sequence, in its column
         paging = B.eagle_paging(_p(c.table), 4, c.k.shape[0], _p(counts))
         ln = run_append(eng, c, i32([0, 3, 6, 9]), 9, None, None, k, v, None,
                         kv=B.eagle_kv(_p(c.k), _p(c.v), c.cap, _p(c.len), paging))
         torch.cuda.synchronize()
-        assert eng.status() == CAPACITY and ln.tolist() == want
+        assert eng.status() == (0 if want == [9, 6, 3] else CAPACITY) and ln.tolist() == want
         for b, (n, lo) in enumerate(zip(c.lens, (0, 3, 6))):
             at = c.at(b, n, n + 3)
             expect = k[lo:lo + 3] if want[b] > n else before.view(-1, hkv, dh)[at]
