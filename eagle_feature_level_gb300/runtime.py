@@ -334,7 +334,7 @@ class PagedCache:
         cache.advance()                           # the lengths now count the new rows
     Where a reserve finds too few blocks it changes nothing, the status says so, and the appends behind it refuse the
     sequences that lack a block or still share the one they would write: those keep their rows and lengths, the others
-    go on.  The page calls stand between such steps.
+    go on.  `clear`, `fork` and `release` stand between such steps, not between an append and its advance.
     `paging` and `kv(layer)` are what the round's verification attention and
     commit take, with the sequences as the batch (capacity `cap`)."""
 
@@ -374,13 +374,19 @@ class PagedCache:
         return _p(t)
 
     # ---- pages ----------------------------------------------------------------
+    def _no_new_rows(self):
+        """The lengths changed: nothing is appended to them yet."""
+        self.len_next.copy_(self.len)
+
     def clear(self):
         B.eagle_pages_init(self.eng.ctx, self.pages_c, *self._ws())
+        self._no_new_rows()
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor):
         """Sequences dst share the rows of sequences src (int32, device)."""
         n = src.numel()
         B.eagle_pages_fork(self.eng.ctx, self.pages_c, n, self._ints(src, n), self._ints(dst, n), *self._ws())
+        self._no_new_rows()
 
     def reserve(self, n_new: torch.Tensor):
         """Room for n_new[s] more rows of every sequence (int32, device)."""
@@ -390,6 +396,7 @@ class PagedCache:
     def release(self, keep: torch.Tensor):
         """Cuts sequence s to its first keep[s] rows (int32, device; < 0: left alone)."""
         B.eagle_pages_release(self.eng.ctx, self.pages_c, self._ints(keep, self.n_seqs), *self._ws())
+        self._no_new_rows()
 
     def compact(self):
         B.eagle_pages_compact(self.eng.ctx, self.pages_c, self.pools_c, *self._ws())
@@ -436,5 +443,5 @@ class PagedCache:
                            *self._packed(out, n, "n_q_heads"), *self._ws())
 
     def advance(self):
-        """The appended rows become the sequences' own."""
+        """The appended rows, if any, become the sequences' own."""
         self.len.copy_(self.len_next)

@@ -1009,6 +1009,40 @@ def test_serving_steps(heads, bs):
     step([2, 60, 1, 1, 0])
 
 
+def test_advance_without_rows_changes_nothing():
+    """A step in which nobody has rows, behind calls that changed the lengths: they stay as those calls left them."""
+    m = Model(engine(8, 2, 128), 4, 8, 16, 30, seed=5)
+
+    def rows(new):
+        x, out = m.buffers(max(sum(new), 1))
+        q_out = torch.zeros_like(out)
+        m.fill(x)
+        m.step(x, out, i32(starts(new)), i32(new), q_out)
+        m.check(x, out, q_out, new)
+
+    def idle():
+        m.c.reserve(i32([0] * 4))
+        m.c.advance()
+        torch.cuda.synchronize()
+        assert m.eng.status() == 0 and m.c.len.tolist() == [h[0][0].shape[0] for h in m.hist]
+
+    rows([20, 40, 0, 0])
+    idle()
+    m.c.fork(i32([1]), i32([2]))
+    m.hist[2] = [list(h) for h in m.hist[1]]
+    idle()
+    m.c.release(i32([0, 17, -1, -1]))
+    m.hist[0] = [[np.zeros((0, m.hkv, m.dh))] * 2 for _ in range(2)]
+    m.hist[1] = [[t[:17] for t in h] for h in m.hist[1]]
+    idle()
+    rows([3, 1, 0, 5])
+    m.c.clear()
+    m.hist = [[[np.zeros((0, m.hkv, m.dh))] * 2 for _ in range(2)] for _ in range(4)]
+    idle()
+    assert int(m.c.ref.sum()) == 0
+    rows([2, 0, 1, 0])
+
+
 def test_serving_step_captured():
     """One captured step, replayed on other rows, lengths and tables."""
     m = Model(engine(8, 2, 128, fresh=True), 4, 32, 16, 90, seed=2)
