@@ -574,8 +574,7 @@ __device__ __forceinline__ bool softmax_step(uint32_t s_addr, uint32_t o_addr, b
   load();
   if (__any_sync(0xffffffffu, valid && m_ref == -INFINITY)) {
     const float mt = most();
-    if (m_ref == -INFINITY) m_ref = mt;        // nothing summed yet
-    __syncwarp();
+    m_ref = m_ref == -INFINITY ? mt : m_ref;   // nothing summed yet
   }
   exps();
   const bool raise = valid && sum.x + sum.y > CH_RAISE;
@@ -596,8 +595,7 @@ __device__ __forceinline__ bool softmax_step(uint32_t s_addr, uint32_t o_addr, b
       sm100::tmem_st16(o_addr + 16u * q, x);
     }
     l_sum *= f;
-    if (raise) m_ref = mt;
-    __syncwarp();
+    m_ref = raise ? mt : m_ref;
     exps();
   }
 #pragma unroll
@@ -1571,7 +1569,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
               sm100::tmem_wait_st();
               sm100::tc_fence_before();
               __syncwarp();
-              if (lane == 0) sm100::mbar_arrive(&sh.p_full[w][h]);
+              sm100::mbar_arrive_if(&sh.p_full[w][h], lane == 0);
               continue;
             }
             const bool masked = k0 + CH_STEP - 1 > pos_least || k0 < lo_most;
