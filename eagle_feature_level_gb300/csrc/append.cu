@@ -17,7 +17,10 @@
 // Bound: memory.  10.4 thousand rows of 64 query and 8 kv heads: 76 us for 429
 // MB, 5.6 TB/s, 0.83 of a measured copy; with the sines and cosines read from
 // shared memory for every head 83 us.  More rows a CTA (16, 32) and streaming
-// hints changed nothing.  A few rows (8 of 40 heads) are latency: 4.6 us.
+// hints changed nothing.  A few rows (8 of 40 heads) are latency: 4.6 us.  Each
+// row's warp looks at the table's entries of all its request's new rows, which
+// long prompts into very small blocks feel: 16384 rows of 8/2 heads of 64 take
+// 46 us in blocks of 16 rows, 75 in blocks of one.
 #include <algorithm>
 
 #include "internal.h"
@@ -167,7 +170,8 @@ __device__ __forceinline__ void unit2(const AppendParams& p, const float2* cs, c
 // Rows r0 .. r0 + rows - 1, each at its place.  T: element type of the rows
 // (uint16_t: bf16 bits, or float); WIDE: units of 16 elements (rot_dim a
 // multiple of 16, so that a unit's 16-byte loads are aligned) or of 2 (4864
-// rows of 64/8 heads: 45 us as 16, 112 as 2).
+// rows of 64/8 heads: 41 us as 16, 117 as 2; fp32 rows of 16/4 heads of 64, 25
+// and 24).
 template <typename T, bool WIDE>
 __device__ __forceinline__ void append_rows(const AppendParams& p, int r0, int rows, int hq,
                                             float2 (*s_cs)[EAGLE_MAX_ROPE_PAIRS], const long long* s_at,
@@ -357,7 +361,8 @@ cudaError_t launch_append(eagle_ctx* ctx, const AppendLaunch& A, cudaStream_t st
   p.pos = A.pos;
   p.len_out = A.len_out;
   p.status = A.status;
-  // Few rows spread over the SMs, one or two a CTA; with many a CTA's setup pays from 4 and then 8 on.  64/8 heads,
+  // Few rows spread over the SMs, one or two a CTA; with many a CTA's setup pays from 4 and then 8 on.  64/8 heads (no
+  // others were measured),
   // 1 / 2 / 4 / 8 rows a CTA: 304 rows 5.6 / 5.8 / 8.1 / 13.3 us, 608: 8.5 / 7.6 / 8.8 / 13.2, 1216: 14.6 / 14.0 /
   // 13.1 / 17.7, 4864: 50 / 43 / 40 / 45, 9728: 93 / 78 / 75 / 74.
   const int per_sm = ceil_div(A.rows->n_rows, ctx->sm_count);

@@ -37,21 +37,28 @@
 //               an O of its own, joined at the item's end.  They also free the
 //               ring's slots: scores that are complete show that the products
 //               issued before them are (a commit of the MMA threads for each
-//               slot cost 250 cycles of their time: 364 -> 342 us below).
+//               slot cost 250 cycles of their time: 364 -> 342 us in the case
+//               below).
+// tcgen05, ldmatrix, mma and named barriers take a whole warp: behind a branch
+// that lanes take differently they are preceded by __syncwarp, and single
+// arrivals between them are predicated instead of branched to (327 -> 319 us).
 //
 // Bound.  At heads of 128 the products of 128 rows x 128 keys take 1024 cycles
 // (measured), in steps of 64 keys 1260: S reads both operands from shared
 // memory, 6 KB for 32 cycles of products, 128 bytes a cycle.  A step of the
 // softmax takes some 1300 cycles of a warp beside its neighbour.  2048 rows after
-// 6144 (64 query / 8 kv heads): 312 us, 1.54 PF/s, 0.79 of a measured bf16 GEMM;
+// 6144 (64 query / 8 kv heads): 319 us over two inputs in turn, 1.51 PF/s, 0.77
+// of a measured bf16 GEMM (342 us, 0.72, over inputs that change every pass);
 // tensor pipe 66% active.  S in steps of 128 keys lost more to waiting than it
 // gained (384 to 434 us when this took 364).  At heads of 64 the softmax bounds
-// it: two prompts of 4096 (16/4 heads) 103 us, 0.67 PF/s.
+// it: two prompts of 4096 (16/4 heads) 104 us, 0.66 PF/s.  Heads of 16 and 32
+// are staged, multiplied and read as 64: the same case at 12/4 heads of 16, 32
+// and 64 takes 71 us each.
 //
 // The running reference of a row is raised (O and the sum rescaled) only when
 // the 64 exponentials of a step add up to more than 256: P stays below 2^8, O / l
 // does not depend on when it was raised, and the steps in between take no
-// maximum (334 -> 312 us).  P in bf16 (2^-9 of each probability) is this
+// maximum (334 -> 312 us).  P in bf16 (off by 2^-8 of each probability at most) is this
 // operator's one rounding besides its output's: with P as a hi + lo pair the
 // P V products double, which the fp32 outputs of the tree attention need and a
 // bf16 output does not.
