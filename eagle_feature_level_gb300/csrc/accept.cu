@@ -366,6 +366,7 @@ cudaError_t launch_target_softmax(eagle_ctx* ctx, int batch, const eagle_tree* t
                                    tree->size, tree->stride, ctx->dims.vocab, probs, argmax,
                                    ws_ptr<int>(ws, ctx->ws.status), stamp);
   ctx->launches++;
+  note_ordered(ctx, st);
   trace_after(ctx, EAGLE_K_ACCEPT, st);
   return e;
 }
@@ -402,6 +403,7 @@ cudaError_t launch_accept_walk(eagle_ctx* ctx, const eagle_plan* plan, int batch
   trace_before(ctx, EAGLE_K_ACCEPT, st);
   const cudaError_t e = launch_pdl(accept_walk_kernel, dim3(batch * WALK_CL), dim3(WALK_THREADS), 0, st, p);
   ctx->launches++;
+  note_ordered(ctx, st);
   trace_after(ctx, EAGLE_K_ACCEPT, st);
   return e;
 }

@@ -260,6 +260,8 @@ std::mutex once_mu;
 std::set<std::tuple<unsigned long long, const void*, int>> once_done;
 }  // namespace
 
+std::atomic<unsigned long long> cache_writes{0};
+
 bool current_context_id(unsigned long long* id) {
   static const CtxQuery q;
   if (!q.get_current || !q.get_id) return false;
@@ -553,6 +555,7 @@ eagle_status eagle_draft_refresh(eagle_ctx* ctx, int batch, const eagle_draft_we
   L.ws = workspace;
   L.refresh_kv = draft_kv;
   L.refresh_n = acc->accept_len;
+  note_cache_write();
   EAGLE_CUDA(launch_prep_refresh(ctx, L, cm->f_commit, cm->tok_commit, acc->path_cap, len_out, stream));
   EAGLE_CUDA(launch_gemm(ctx, EPI_FC, L, stream));
   EAGLE_CUDA(launch_gemm(ctx, EPI_KV, L, stream));
@@ -741,6 +744,7 @@ eagle_status eagle_commit(eagle_ctx* ctx, int batch, const eagle_accept_out* acc
   C.draft_kv = draft_kv;
   C.out = out;
   C.status = ws_ptr<int>(workspace, ctx->ws.status);
+  note_cache_write();
   EAGLE_CUDA(launch_commit(ctx, C, stream));
   return EAGLE_OK;
 }
@@ -839,6 +843,7 @@ eagle_status eagle_kv_append(eagle_ctx* ctx, int batch, const eagle_rows* rows, 
   A.pos = pos;
   A.len_out = len_out;
   A.status = ws_ptr<int>(workspace, ctx->ws.status);
+  note_cache_write();
   EAGLE_CUDA(launch_append(ctx, A, stream));
   return EAGLE_OK;
 }
@@ -882,6 +887,7 @@ eagle_status eagle_pages_fork(eagle_ctx* ctx, const eagle_pages* pages, int n, c
   EAGLE_REQUIRE(n <= pages->n_seqs, EAGLE_ERR_CAPACITY);
   EAGLE_PTR(src); EAGLE_PTR(dst);
   if ((st = check_ws(workspace)) != EAGLE_OK) return st;
+  note_cache_write();
   EAGLE_CUDA(launch_pages_fork(ctx, *pages, n, src, dst, workspace, stream));
   return EAGLE_OK;
 }
@@ -894,6 +900,7 @@ eagle_status eagle_pages_reserve(eagle_ctx* ctx, const eagle_pages* pages, const
   if ((st = check_pools(pools)) != EAGLE_OK) return st;
   EAGLE_PTR(n_new);
   if ((st = check_ws(workspace)) != EAGLE_OK) return st;
+  note_cache_write();
   EAGLE_CUDA(launch_pages_reserve(ctx, *pages, *pools, n_new, workspace, stream));
   return EAGLE_OK;
 }
@@ -905,6 +912,7 @@ eagle_status eagle_pages_release(eagle_ctx* ctx, const eagle_pages* pages, const
   if (st != EAGLE_OK) return st;
   EAGLE_PTR(keep);
   if ((st = check_ws(workspace)) != EAGLE_OK) return st;
+  note_cache_write();
   EAGLE_CUDA(launch_pages_release(ctx, *pages, keep, workspace, stream));
   return EAGLE_OK;
 }
@@ -916,6 +924,7 @@ eagle_status eagle_pages_compact(eagle_ctx* ctx, const eagle_pages* pages, const
   if (st != EAGLE_OK) return st;
   if ((st = check_pools(pools)) != EAGLE_OK) return st;
   if ((st = check_ws(workspace)) != EAGLE_OK) return st;
+  note_cache_write();
   EAGLE_CUDA(launch_pages_compact(ctx, *pages, *pools, workspace, stream));
   return EAGLE_OK;
 }

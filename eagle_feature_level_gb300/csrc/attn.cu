@@ -85,6 +85,7 @@ struct AttnParams {
   int tma;                        // tcgen05 kernel: whole prefix tiles by TMA through the launch's tensor maps
   int box_rows;                   // keys per TMA box: 64, or the block size of a paged prefix
   int stages;                     // tcgen05 kernel: K/V ring stages
+  int early;                      // the prefix is at rest: read before the dependency wait
   int* status;                    // device status word (null: not reported)
   uint64_t* stamp;                // launch timestamps (null: off)
 };
@@ -412,7 +413,7 @@ template <int NR>
 __global__ void __launch_bounds__(THREADS, 4) tree_attn_kernel(const AttnParams p) {
   const LaunchStamp ls(p.stamp);
   pdl_trigger();
-  if (p.mode == 1) {
+  if (p.mode == 1 || !p.early) {
     pdl_wait();                              // verification reads the tree's size first
     ls.waited();
   }
@@ -463,8 +464,8 @@ __global__ void __launch_bounds__(THREADS, 4) tree_attn_kernel(const AttnParams 
       stage_bf16(reinterpret_cast<uint16_t*>(buf), p.kp, p.vp,
                  ((static_cast<size_t>(b) * p.kv_cap + t0) * p.Hkv + h) * dh, row_stride, nt, dh, policy);
   };
-  // The prefix KV is not written by the kernels of this draft step: its
-  // first tile is requested before waiting on the predecessor.
+  // The prefix KV is not written by the kernels of this draft step: at rest
+  // before it, its first tile is requested before waiting on the predecessor.
   if (!is_tree && n_tiles > 0) stage(0, 0);
   pdl_wait();                                // q rows, tree K/V and masks come from the predecessors
   ls.waited();
@@ -869,10 +870,11 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1) tree_attn_mma_kernel
   float* mrg = reinterpret_cast<float*>(qhi);   // after a pass's last tile, the query rows are dead
   const bool is_tree = split == p.n_splits;
   const bool tree_f32 = is_tree && p.mode == 0;
-  // The prefix and its length are this round's inputs, written by no kernel
-  // of the round: a prefix split's range and tiles are known (and its tiles
-  // requested) before the dependency wait.  The tree part's size, the query
-  // rows and the tree K/V come from the predecessors.
+  // The prefix and its length are this round's inputs: where no kernel that
+  // may still run writes them, a prefix split's range and tiles are known (and
+  // its tiles requested) before the dependency wait.  The tree part's size, the
+  // query rows and the tree K/V come from the predecessors.
+  if (!p.early) pdl_wait();
   int lo = 0, hi = 0;
   if (!is_tree) {
     const int L = prefix_rows(p, b, split == 0 && threadIdx.x == 0);
@@ -1432,6 +1434,7 @@ __global__ void __launch_bounds__(WS_THREADS, 1)
   volatile int* abort_flag = &s_abort;
   volatile int* never = &s_never;
 
+  if (!p.early) pdl_wait();
   WsTiles T;
   T.draft = draft;
   {
@@ -1458,8 +1461,9 @@ __global__ void __launch_bounds__(WS_THREADS, 1)
     s_abort = 0;
     s_never = 0;
     sm100::fence_barrier_init();
-    // The prefix is this round's input, written by no kernel of the round:
-    // the split's first whole tiles are requested before the dependency wait.
+    // The prefix is this round's input: where no kernel that may still run
+    // writes it, the split's first whole tiles are requested before the
+    // dependency wait.
     int pre = 0;
     for (; pre < min(NST, T.n_pre); ++pre) {
       const int k0 = T.lo + pre * WS_KEYS;
@@ -1945,6 +1949,7 @@ static cudaError_t run_attn_ws(eagle_ctx* ctx, AttnParams& p, int kernel_id, cud
 
 static cudaError_t run_attn(eagle_ctx* ctx, AttnParams& p, int kernel_id, cudaStream_t st) {
   if (p.dh % 16 != 0 || p.dh > MAX_DH) return cudaErrorInvalidValue;
+  p.early = prefix_at_rest(ctx, st);
   if (p.dh == WS_DH && ((p.mode == 1 && p.rows_cap * p.G >= kVerifyTcRows) ||
                         (p.mode == 0 && p.rows_cap * p.G >= kDraftTcRows)))
     return run_attn_ws(ctx, p, kernel_id, st);

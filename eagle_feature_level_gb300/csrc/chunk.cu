@@ -1803,6 +1803,7 @@ cudaError_t launch_chunk_attn(eagle_ctx* ctx, int batch, const eagle_rows* rows,
   const cudaError_t e = p.dh > 64 ? launch_shape<128>(ctx, p, qm, km, vm, tkm, tvm, st)
                                     : launch_shape<64>(ctx, p, qm, km, vm, tkm, tvm, st);
   ctx->launches++;
+  note_ordered(ctx, st);
   trace_after(ctx, EAGLE_K_CHUNK_ATTN, st);
   return e;
 }

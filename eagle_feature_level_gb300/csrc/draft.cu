@@ -575,6 +575,7 @@ cudaError_t launch_select(eagle_ctx* ctx, const DraftLaunch& L, cudaStream_t st)
   trace_before(ctx, EAGLE_K_SELECT, st);
   const cudaError_t e = launch_pdl(select_kernel, dim3(L.n * SEL_CL), dim3(SEL_THREADS), 0, st, p);
   ctx->launches++;
+  note_ordered(ctx, st);
   trace_after(ctx, EAGLE_K_SELECT, st);
   return e;
 }

@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <utility>
@@ -80,6 +81,9 @@ struct eagle_ctx {
   uint64_t* stamps = nullptr;
   int stamp_cap = 0;
   std::vector<int> stamp_ids;        // kernel class of each stamped launch
+  // the cache writes that this context's last ordering kernel stands behind, and its stream (prefix_at_rest)
+  unsigned long long writes_done = 0;
+  cudaStream_t done_on = nullptr;
 };
 
 namespace eagle {
@@ -147,6 +151,25 @@ inline uint64_t* stamp_slot(eagle_ctx* ctx, int kernel_id) {
   uint64_t* s = ctx->stamps + 3 * ctx->stamp_ids.size();
   ctx->stamp_ids.push_back(kernel_id);
   return s;
+}
+
+// Whether an attention kernel may read its prefix (rows, lengths, block table)
+// before its dependency wait.  The wait covers the kernel before it; kernels
+// that trigger their dependents before they wait themselves may pass it on to
+// the one before that.  So nothing that writes caches may have been launched
+// since the last kernel that triggers only behind its own wait (every kernel
+// before that one has then completed).  Kernels of other streams are ordered
+// by events, which are waited for before a launch; writes are counted for the
+// process, since contexts may share a cache.
+extern std::atomic<unsigned long long> cache_writes;
+inline void note_cache_write() { cache_writes.fetch_add(1); }
+inline void note_ordered(eagle_ctx* ctx, cudaStream_t st) {
+  ctx->writes_done = cache_writes.load();
+  ctx->done_on = st;
+}
+inline bool prefix_at_rest(const eagle_ctx* ctx, cudaStream_t st) {
+  const unsigned long long n = cache_writes.load();
+  return n == 0 || (ctx->writes_done == n && ctx->done_on == st);
 }
 
 // Launch bookkeeping: optional CUDA-event trace around kernels of one class.

@@ -405,6 +405,7 @@ cudaError_t launch_tree(eagle_ctx* ctx, const eagle_plan* plan, int phase, int l
   trace_before(ctx, EAGLE_K_TREE, st);
   const cudaError_t e = launch_pdl(tree_kernel, dim3(batch), dim3(TREE_THREADS), smem, st, p);
   ctx->launches++;
+  note_ordered(ctx, st);
   trace_after(ctx, EAGLE_K_TREE, st);
   return e;
 }

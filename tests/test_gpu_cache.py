@@ -1137,6 +1137,117 @@ def test_a_reserve_that_fails_costs_no_rows(captured, forks):
     m.eng.close()
 
 
+@pytest.mark.parametrize("heads", [(8, 2, 128), (32, 8, 128), (4, 2, 64)], ids=lambda h: "x".join(map(str, h)))
+@pytest.mark.parametrize("call", ["append", "append captured", "compact", "release", "fork"])
+def test_verification_directly_behind_a_cache_call(heads, call):
+    """The round's verification attention as the very next launch behind a call that writes its prefix, its length or
+    its table: the same as after that call has finished."""
+    hq, hkv, dh = heads
+    nb, S, bs, per = 6, 8, 16, 128
+    eng = R.Engine(dict(d=hq * dh, n_q_heads=hq, n_kv_heads=hkv, head_dim=dh, d_ff=64, vocab=64), max_batch=nb + 1,
+                   max_rows=8, max_expanded=1, max_children=1, max_tree=S, max_prefix=bs * per, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(90)
+    bf = lambda *shape: torch.randn(*shape, generator=g, device="cuda").to(torch.bfloat16)
+    q, kt, vt = bf(nb, S, hq, dh), bf(nb, S, hkv, dh), bf(nb, S, hkv, dh)
+    anc = torch.tensor([(2 << s) - 1 for s in range(S)], device="cuda").expand(nb, S).contiguous()
+    size, other = i32([S] * nb), torch.zeros(nb * S * 64, dtype=torch.int32, device="cuda")
+    tree = B.eagle_tree(*[_p(other)] * 5, _p(anc), _p(other), _p(size), S)
+    c = R.PagedCache(eng, nb + 1, bs, 2 * nb * per, per)
+    for t in (c.k[0], c.v[0]):
+        t.copy_(bf(*t.shape))
+    rs, n_new = i32([500 * b for b in range(nb + 1)] + [500 * nb]), i32([500] * nb + [0])
+    k, v = bf(500 * nb, hkv, dh), bf(500 * nb, hkv, dh)
+    outs = [torch.zeros(nb, S, hq, dh, device="cuda") for _ in range(2)]
+
+    def verify(out, kv):
+        B.eagle_tree_verify_attn(eng.ctx, nb, _p(q), _p(kt), _p(vt), kv, tree, 1 / math.sqrt(dh), _p(out),
+                                 eng.ws.data_ptr(), eng.stream())
+
+    def cache_call():
+        if call.startswith("append"):
+            c.append(0, rs, None, None, k, v)
+        elif call == "compact":
+            c.compact()
+        elif call == "release":
+            B.eagle_pages_release(eng.ctx, c.pages_c, _p(keep), eng.ws.data_ptr(), eng.stream())
+        else:
+            B.eagle_pages_fork(eng.ctx, c.pages_c, 1, _p(src), _p(dst), eng.ws.data_ptr(), eng.stream())
+
+    keep, src, dst = i32([700] * nb + [-1]), i32([0]), i32([1])
+    kv = c._kv_next[0] if call.startswith("append") else c.kv()
+    graph = None
+    verify(outs[1], c.kv())
+    for turn in range(6):
+        # 1500 rows each, in blocks behind those of a sequence that goes; the blocks' contents differ from turn to turn
+        c.clear()
+        c.reserve(i32([0] * nb + [bs * per]))
+        c.reserve(i32([1500] * nb + [0]))
+        c.len.copy_(i32([1500 - 3 * b for b in range(nb)] + [0]))
+        c.release(i32([-1] * nb + [0]))
+        c.reserve(n_new)
+        for t in (c.k[0], c.v[0]):
+            t.copy_(t.roll(turn + 1, 0))
+        k.copy_(k.roll(turn + 1, 0))
+        c.len_next.copy_(c.len)
+        torch.cuda.synchronize()
+        if call == "append captured":
+            if graph is None:
+                graph = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(graph):
+                    cache_call()
+                    verify(outs[0], kv)
+            graph.replay()
+        else:
+            cache_call()
+            verify(outs[0], kv)
+        torch.cuda.synchronize()
+        assert eng.status() == 0
+        verify(outs[1], kv)
+        torch.cuda.synchronize()
+        assert eng.status() == 0 and torch.isfinite(outs[1]).all()
+        assert torch.equal(outs[0], outs[1])
+    eng.close()
+
+
+def test_drafting_directly_behind_an_append():
+    """A draft step right behind rows appended to the draft's own cache."""
+    import eagle_synth as S
+    from eagle_feature_level_gb300.workload import dims_of, limits_for
+    w = S.variant("13b_x8_eagle2", name="served", d=256, n_q_heads=4, n_kv_heads=4, head_dim=64, d_ff=344, vocab=1000,
+                  batch=3, prefix_range=(50, 200), weight_std=0.05, temps=(0.0,))
+    eng = R.Engine(dims_of(w), max_prefix=1024, device="cuda", **limits_for(w))
+    rd = R.Round(eng, R.plan_for(w.tree, w.top_k, w.depth, w.top_m), w.batch, 1024)
+    wc = eng.weights(S.draft_weights(w, 79, device="cuda"))
+    g = torch.Generator(device="cuda").manual_seed(91)
+    n, lens = 300, [40, 120, 77]
+    rd.t_next.copy_(i32([5, 9, 700]))
+    rd.f_last.copy_(torch.randn(rd.f_last.shape, generator=g, device="cuda"))
+    ln, rs = i32([0] * 3), i32([0, n, 2 * n, 3 * n])
+    st, ws = eng.stream(), eng.ws.data_ptr()
+    for turn in range(6):
+        rd.draft_len.copy_(i32(lens))
+        rd.pos0.copy_(i32([a + n for a in lens]))
+        ln.copy_(i32(lens))
+        for t in (rd.draft_k, rd.draft_v):
+            t.copy_(torch.randn(t.shape, generator=g, device="cuda"))
+        k, v = (torch.randn(3 * n, 4, 64, generator=g, device="cuda") for _ in range(2))
+        B.eagle_tree_expand_rerank(eng.ctx, rd.plan, B.PHASE_ROOT, 0, 3, rd.req_c, None, rd.pool_c, None, ws, st)
+        kv = B.eagle_kv(_p(rd.draft_k), _p(rd.draft_v), 1024, _p(ln))
+        torch.cuda.synchronize()
+        B.eagle_kv_append(eng.ctx, 3, B.eagle_rows(_p(rs), 3 * n), None, B.DTYPE_F32, 0, 0, 0, 0, _p(k), k.stride(0),
+                          _p(v), v.stride(0), rd.draft_kv_c, None, _p(ln), ws, st)
+        logits = []
+        for _ in range(2):
+            B.eagle_draft_step(eng.ctx, rd.plan, 0, 3, wc, rd.req_c, kv, rd.pool_c, rd.out_c, rd.children_c,
+                               rd.sampling_c, ws, st)
+            torch.cuda.synchronize()
+            assert eng.status() == 0
+            logits.append(rd.logits[:, 0].clone())
+        assert ln.tolist() == [a + n for a in lens]
+        assert torch.isfinite(logits[1]).all() and torch.equal(logits[0], logits[1])
+    eng.close()
+
+
 def rows_at(c, s, lo, hi):
     """Flat pool rows of positions lo .. hi - 1 of sequence s of a PagedCache."""
     j = torch.arange(lo, hi, device="cuda")
