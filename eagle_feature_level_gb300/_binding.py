@@ -22,6 +22,10 @@ EAGLE_MAX_ROPE_PAIRS = 64
 
 DTYPE_BF16, DTYPE_F32 = 0, 1
 ROPE_LINEAR, ROPE_BANDS, ROPE_RAMP = 1, 2, 3
+MX_FP8, MX_FP4, NV_FP4 = 1, 2, 3
+ACT_NONE, ACT_SWIGLU = 0, 1
+EAGLE_MAX_NORM_COLS = 32768
+EAGLE_MAX_SAMPLE_VOCAB = 262144
 PHASE_ROOT, PHASE_FRONTIER, PHASE_FINAL = 0, 1, 2
 
 STATUS = {0: "EAGLE_OK", 1: "EAGLE_ERR_INVALID_ARG", 2: "EAGLE_ERR_SHAPE", 3: "EAGLE_ERR_ALIGN",
@@ -31,7 +35,8 @@ STATUS_CODE = {v: k for k, v in STATUS.items()}
 
 KERNEL_ID = {"all": -1, "gemm_fc": 0, "gemm_qkv": 1, "gemm_o": 2, "gemm_gateup": 3, "gemm_down": 4,
              "gemm_lm": 5, "draft_attn": 6, "select": 7, "tree": 8, "verify_attn": 9, "accept": 10,
-             "commit": 11, "prep": 12, "refresh": 13, "fuse": 14, "append": 15, "chunk_attn": 16, "pages": 17}
+             "commit": 11, "prep": 12, "refresh": 13, "fuse": 14, "append": 15, "chunk_attn": 16, "pages": 17, "norm": 18,
+             "quant": 19, "linear": 20, "sample": 21}
 
 P = C.c_void_p
 I = C.c_int
@@ -140,6 +145,20 @@ class eagle_pools(C.Structure):
         super().__init__(n, C.cast(self.arrays[0], P), C.cast(self.arrays[1], P))
 
 
+class eagle_mx(C.Structure):
+    _fields_ = [("data", P), ("scale", P), ("tensor_scale", P), ("rows", I), ("cols", I), ("format", I)]
+
+
+class eagle_norm(C.Structure):
+    _fields_ = [("rows", I), ("cols", I), ("dtype", I), ("x", P), ("ld_x", I), ("res_dtype", I), ("residual", P),
+                ("ld_res", I), ("residual_out", P), ("ld_res_out", I), ("gain", P), ("eps", C.c_float),
+                ("out_dtype", I), ("out", P), ("ld_out", I), ("out_mx", C.POINTER(eagle_mx))]
+
+
+class eagle_filter(C.Structure):
+    _fields_ = [("temperature", P), ("top_k", P), ("top_p", P), ("min_p", P), ("rows_each", I), ("rows_used", P)]
+
+
 _lib = None
 
 
@@ -201,6 +220,12 @@ def _declare(L):
         "eagle_pages_reserve": [P, C.POINTER(eagle_pages), C.POINTER(eagle_pools), P, P, P],
         "eagle_pages_release": [P, C.POINTER(eagle_pages), P, P, P],
         "eagle_pages_compact": [P, C.POINTER(eagle_pages), C.POINTER(eagle_pools), P, P],
+        "eagle_mx_layout": [I, I, I, C.POINTER(C.c_size_t), C.POINTER(C.c_size_t)],
+        "eagle_mx_quantize": [P, I, I, P, I, C.POINTER(eagle_mx), P, P],
+        "eagle_mx_unpack": [P, C.POINTER(eagle_mx), I, P, I, P, P],
+        "eagle_mx_linear": [P, C.POINTER(eagle_mx), C.POINTER(eagle_mx), P, I, P, I, P, P],
+        "eagle_add_norm": [P, C.POINTER(eagle_norm), P, P],
+        "eagle_sample": [P, I, I, I, P, I, C.POINTER(eagle_filter), P, P, P, P, I, P, P],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -220,7 +245,8 @@ EXPORTED = ["eagle_create", "eagle_destroy", "eagle_workspace_init", "eagle_read
             "eagle_stamps_enable", "eagle_stamps_disable", "eagle_draft_refresh", "eagle_fuse_features",
             "eagle_launch_count", "eagle_wait_selftest", "eagle_rope_plan", "eagle_kv_append",
             "eagle_chunk_attn", "eagle_pages_init", "eagle_pages_fork", "eagle_pages_reserve",
-            "eagle_pages_release", "eagle_pages_compact"]
+            "eagle_pages_release", "eagle_pages_compact", "eagle_mx_layout", "eagle_mx_quantize",
+            "eagle_mx_unpack", "eagle_mx_linear", "eagle_add_norm", "eagle_sample"]
 
 
 def _check(name: str, code: int):
@@ -230,6 +256,11 @@ def _check(name: str, code: int):
 
 def _ref(x):
     return C.byref(x) if x is not None else None
+
+
+def ref(x):
+    """A pointer to struct `x` for a struct's field (None: null); it keeps `x`."""
+    return C.pointer(x) if x is not None else None
 
 
 # ---- thin wrappers with the C names -----------------------------------------
@@ -379,6 +410,36 @@ def eagle_pages_release(ctx, pages, keep, ws_ptr, stream):
 
 def eagle_pages_compact(ctx, pages, pools, ws_ptr, stream):
     _check("eagle_pages_compact", lib().eagle_pages_compact(ctx, C.byref(pages), C.byref(pools), ws_ptr, stream))
+
+
+def eagle_mx_layout(fmt: int, rows: int, cols: int):
+    """(bytes of the data, bytes of the scales)."""
+    data, scale = C.c_size_t(), C.c_size_t()
+    _check("eagle_mx_layout", lib().eagle_mx_layout(fmt, rows, cols, C.byref(data), C.byref(scale)))
+    return data.value, scale.value
+
+
+def eagle_mx_quantize(ctx, dtype, act, x, ld_x, out, ws_ptr, stream):
+    _check("eagle_mx_quantize", lib().eagle_mx_quantize(ctx, dtype, act, x, ld_x, C.byref(out), ws_ptr, stream))
+
+
+def eagle_mx_unpack(ctx, x, dtype, y, ld_y, ws_ptr, stream):
+    _check("eagle_mx_unpack", lib().eagle_mx_unpack(ctx, C.byref(x), dtype, y, ld_y, ws_ptr, stream))
+
+
+def eagle_mx_linear(ctx, x, w, bias, dtype, y, ld_y, ws_ptr, stream):
+    _check("eagle_mx_linear",
+           lib().eagle_mx_linear(ctx, C.byref(x), C.byref(w), bias, dtype, y, ld_y, ws_ptr, stream))
+
+
+def eagle_add_norm(ctx, norm, ws_ptr, stream):
+    _check("eagle_add_norm", lib().eagle_add_norm(ctx, C.byref(norm), ws_ptr, stream))
+
+
+def eagle_sample(ctx, n_rows, vocab, dtype, logits, ld, filter, u, token, argmax, probs, ld_probs, ws_ptr, stream):
+    _check("eagle_sample",
+           lib().eagle_sample(ctx, n_rows, vocab, dtype, logits, ld, C.byref(filter), u, token, argmax, probs,
+                              ld_probs, ws_ptr, stream))
 
 
 def eagle_trace_enable(ctx, kernel: str, capacity: int):

@@ -226,6 +226,21 @@ eagle_status check_pools(const eagle_pools* p) {
   return EAGLE_OK;
 }
 
+eagle_status check_dtype(int dtype) {
+  EAGLE_REQUIRE(dtype == EAGLE_DTYPE_BF16 || dtype == EAGLE_DTYPE_F32, EAGLE_ERR_INVALID_ARG);
+  return EAGLE_OK;
+}
+
+eagle_status check_mx(const eagle_mx* m) {
+  EAGLE_REQUIRE(m, EAGLE_ERR_INVALID_ARG);
+  EAGLE_REQUIRE(m->format >= EAGLE_MX_FP8 && m->format <= EAGLE_NV_FP4, EAGLE_ERR_INVALID_ARG);
+  EAGLE_REQUIRE(m->rows >= 1 && m->cols >= 32 && m->cols % 32 == 0, EAGLE_ERR_SHAPE);
+  EAGLE_PTR(m->data); EAGLE_PTR(m->scale);
+  if (m->format == EAGLE_NV_FP4 && m->tensor_scale)
+    EAGLE_REQUIRE((reinterpret_cast<uintptr_t>(m->tensor_scale) & 3u) == 0, EAGLE_ERR_ALIGN);
+  return EAGLE_OK;
+}
+
 eagle_status check_ws(const void* ws) {
   EAGLE_REQUIRE(ws, EAGLE_ERR_INVALID_ARG);
   EAGLE_REQUIRE((reinterpret_cast<uintptr_t>(ws) & 255u) == 0, EAGLE_ERR_ALIGN);
@@ -929,8 +944,128 @@ eagle_status eagle_pages_compact(eagle_ctx* ctx, const eagle_pages* pages, const
   return EAGLE_OK;
 }
 
+eagle_status eagle_mx_layout(int format, int rows, int cols, size_t* data_bytes, size_t* scale_bytes) {
+  EAGLE_REQUIRE(data_bytes && scale_bytes, EAGLE_ERR_INVALID_ARG);
+  EAGLE_REQUIRE(format >= EAGLE_MX_FP8 && format <= EAGLE_NV_FP4, EAGLE_ERR_INVALID_ARG);
+  EAGLE_REQUIRE(rows >= 1 && cols >= 32 && cols % 32 == 0, EAGLE_ERR_SHAPE);
+  const size_t r = static_cast<size_t>(rows), n = static_cast<size_t>(cols) / (format == EAGLE_NV_FP4 ? 16 : 32);
+  *data_bytes = r * static_cast<size_t>(cols) / (format == EAGLE_MX_FP8 ? 1 : 2);
+  *scale_bytes = (r + 127) / 128 * ((n + 3) / 4) * 512;
+  return EAGLE_OK;
+}
+
+eagle_status eagle_mx_quantize(eagle_ctx* ctx, int dtype, int act, const void* x, int ld_x, const eagle_mx* out,
+                               void* workspace, cudaStream_t stream) {
+  EAGLE_REQUIRE(ctx, EAGLE_ERR_INVALID_ARG);
+  eagle_status st = check_dtype(dtype);
+  if (st != EAGLE_OK) return st;
+  EAGLE_REQUIRE(act == EAGLE_ACT_NONE || act == EAGLE_ACT_SWIGLU, EAGLE_ERR_INVALID_ARG);
+  if ((st = check_mx(out)) != EAGLE_OK) return st;
+  if ((st = check_packed(x, ld_x, (act == EAGLE_ACT_SWIGLU ? 2ll : 1ll) * out->cols, dtype)) != EAGLE_OK) return st;
+  EAGLE_REQUIRE(x != out->data, EAGLE_ERR_INVALID_ARG);
+  if ((st = check_ws(workspace)) != EAGLE_OK) return st;
+  EAGLE_CUDA(launch_quantize(ctx, dtype, act, x, ld_x, out, ws_ptr<int>(workspace, ctx->ws.status), stream));
+  return EAGLE_OK;
+}
+
+eagle_status eagle_mx_unpack(eagle_ctx* ctx, const eagle_mx* x, int dtype, void* y, int ld_y, void* workspace,
+                             cudaStream_t stream) {
+  EAGLE_REQUIRE(ctx, EAGLE_ERR_INVALID_ARG);
+  eagle_status st = check_dtype(dtype);
+  if (st != EAGLE_OK) return st;
+  if ((st = check_mx(x)) != EAGLE_OK) return st;
+  if ((st = check_packed(y, ld_y, x->cols, dtype)) != EAGLE_OK) return st;
+  EAGLE_REQUIRE(y != x->data, EAGLE_ERR_INVALID_ARG);
+  if ((st = check_ws(workspace)) != EAGLE_OK) return st;
+  EAGLE_CUDA(launch_unpack(ctx, x, dtype, y, ld_y, stream));
+  return EAGLE_OK;
+}
+
+eagle_status eagle_mx_linear(eagle_ctx* ctx, const eagle_mx* x, const eagle_mx* w, const float* bias, int dtype,
+                             void* y, int ld_y, void* workspace, cudaStream_t stream) {
+  EAGLE_REQUIRE(ctx, EAGLE_ERR_INVALID_ARG);
+  eagle_status st = check_dtype(dtype);
+  if (st != EAGLE_OK) return st;
+  if ((st = check_mx(x)) != EAGLE_OK) return st;
+  if ((st = check_mx(w)) != EAGLE_OK) return st;
+  EAGLE_REQUIRE(x->format == w->format, EAGLE_ERR_INVALID_ARG);
+  EAGLE_REQUIRE(x->cols == w->cols, EAGLE_ERR_SHAPE);
+  if (bias) EAGLE_PTR(bias);
+  if ((st = check_packed(y, ld_y, w->rows, dtype)) != EAGLE_OK) return st;
+  EAGLE_REQUIRE(y != x->data && y != w->data, EAGLE_ERR_INVALID_ARG);
+  if ((st = check_ws(workspace)) != EAGLE_OK) return st;
+  EAGLE_CUDA(launch_linear(ctx, x, w, bias, dtype, y, ld_y, ws_ptr<int>(workspace, ctx->ws.status), stream));
+  return EAGLE_OK;
+}
+
+eagle_status eagle_add_norm(eagle_ctx* ctx, const eagle_norm* n, void* workspace, cudaStream_t stream) {
+  EAGLE_REQUIRE(ctx && n, EAGLE_ERR_INVALID_ARG);
+  EAGLE_REQUIRE(n->rows >= 1 && n->cols >= 8 && n->cols % 8 == 0, EAGLE_ERR_SHAPE);
+  EAGLE_REQUIRE(n->cols <= EAGLE_MAX_NORM_COLS, EAGLE_ERR_CAPACITY);
+  EAGLE_REQUIRE(std::isfinite(n->eps) && n->eps >= 0.f, EAGLE_ERR_INVALID_ARG);
+  eagle_status st = check_dtype(n->dtype);
+  if (st != EAGLE_OK) return st;
+  if ((st = check_packed(n->x, n->ld_x, n->cols, n->dtype)) != EAGLE_OK) return st;
+  if (n->residual || n->residual_out)
+    if ((st = check_dtype(n->res_dtype)) != EAGLE_OK) return st;
+  if (n->residual) {
+    if ((st = check_packed(n->residual, n->ld_res, n->cols, n->res_dtype)) != EAGLE_OK) return st;
+  }
+  if (n->residual_out) {
+    if ((st = check_packed(n->residual_out, n->ld_res_out, n->cols, n->res_dtype)) != EAGLE_OK) return st;
+    EAGLE_REQUIRE(n->residual_out != n->residual || n->ld_res_out == n->ld_res, EAGLE_ERR_INVALID_ARG);
+    EAGLE_REQUIRE(n->residual_out != n->x, EAGLE_ERR_INVALID_ARG);
+  }
+  if (n->gain) EAGLE_PTR(n->gain);
+  if (n->out_mx) {
+    EAGLE_REQUIRE(!n->out, EAGLE_ERR_INVALID_ARG);
+    if ((st = check_mx(n->out_mx)) != EAGLE_OK) return st;
+    EAGLE_REQUIRE(n->out_mx->rows == n->rows && n->out_mx->cols == n->cols, EAGLE_ERR_SHAPE);
+  } else {
+    if ((st = check_dtype(n->out_dtype)) != EAGLE_OK) return st;
+    if ((st = check_packed(n->out, n->ld_out, n->cols, n->out_dtype)) != EAGLE_OK) return st;
+    EAGLE_REQUIRE(n->out != n->x || (n->ld_out == n->ld_x && n->out_dtype == n->dtype), EAGLE_ERR_INVALID_ARG);
+    EAGLE_REQUIRE(n->out != n->residual && n->out != n->residual_out, EAGLE_ERR_INVALID_ARG);
+  }
+  if ((st = check_ws(workspace)) != EAGLE_OK) return st;
+  EAGLE_CUDA(launch_norm(ctx, n, ws_ptr<int>(workspace, ctx->ws.status), stream));
+  return EAGLE_OK;
+}
+
+eagle_status eagle_sample(eagle_ctx* ctx, int n_rows, int vocab, int dtype, const void* logits, int ld,
+                          const eagle_filter* f, const uint32_t* u, int32_t* token, int32_t* argmax, float* probs,
+                          int ld_probs, void* workspace, cudaStream_t stream) {
+  EAGLE_REQUIRE(ctx && f, EAGLE_ERR_INVALID_ARG);
+  EAGLE_REQUIRE(n_rows >= 1 && vocab >= 1, EAGLE_ERR_SHAPE);
+  EAGLE_REQUIRE(vocab <= EAGLE_MAX_SAMPLE_VOCAB, EAGLE_ERR_CAPACITY);
+  eagle_status st = check_dtype(dtype);
+  if (st != EAGLE_OK) return st;
+  EAGLE_PTR(logits);
+  EAGLE_REQUIRE(ld >= vocab, EAGLE_ERR_SHAPE);
+  EAGLE_REQUIRE(f->rows_each >= 1, EAGLE_ERR_INVALID_ARG);
+  const void* each[] = {f->temperature, f->top_k, f->top_p, f->min_p, f->rows_used};
+  for (const void* p : each)
+    if (p) EAGLE_PTR(p);
+  EAGLE_REQUIRE((u == nullptr) == (token == nullptr), EAGLE_ERR_INVALID_ARG);
+  EAGLE_REQUIRE(token || argmax || probs, EAGLE_ERR_INVALID_ARG);
+  if (token) {
+    EAGLE_PTR(u); EAGLE_PTR(token);
+  }
+  if (argmax) EAGLE_PTR(argmax);
+  if (probs) {
+    EAGLE_PTR(probs);
+    EAGLE_REQUIRE(ld_probs >= vocab, EAGLE_ERR_SHAPE);
+    EAGLE_REQUIRE(static_cast<const void*>(probs) != logits, EAGLE_ERR_INVALID_ARG);
+  }
+  if ((st = check_ws(workspace)) != EAGLE_OK) return st;
+  const SampleLaunch S{n_rows, vocab, dtype, logits, ld, f, u, token, argmax, probs, ld_probs,
+                       ws_ptr<int>(workspace, ctx->ws.status)};
+  EAGLE_CUDA(launch_sample(ctx, S, stream));
+  return EAGLE_OK;
+}
+
 eagle_status eagle_trace_enable(eagle_ctx* ctx, int kernel_id, int capacity) {
-  EAGLE_REQUIRE(ctx && capacity >= 1 && kernel_id >= -1 && kernel_id <= EAGLE_K_PAGES, EAGLE_ERR_INVALID_ARG);
+  EAGLE_REQUIRE(ctx && capacity >= 1 && kernel_id >= -1 && kernel_id <= EAGLE_K_SAMPLE, EAGLE_ERR_INVALID_ARG);
   TraceState& t = ctx->trace;
   while (static_cast<int>(t.events.size()) < 2 * capacity) {
     cudaEvent_t e;

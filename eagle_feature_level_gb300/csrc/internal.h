@@ -299,6 +299,26 @@ cudaError_t launch_append(eagle_ctx* ctx, const AppendLaunch& A, cudaStream_t st
 cudaError_t launch_chunk_attn(eagle_ctx* ctx, int batch, const eagle_rows* rows, const uint16_t* q, int ld_q,
                               const eagle_kv* kv, int window, float scale, uint16_t* out, int ld_out, void* ws,
                               cudaStream_t st);
+cudaError_t launch_norm(eagle_ctx* ctx, const eagle_norm* n, int* status, cudaStream_t st);
+cudaError_t launch_quantize(eagle_ctx* ctx, int dtype, int act, const void* x, int ld, const eagle_mx* out, int* status,
+                            cudaStream_t st);
+cudaError_t launch_unpack(eagle_ctx* ctx, const eagle_mx* x, int dtype, void* y, int ld, cudaStream_t st);
+cudaError_t launch_linear(eagle_ctx* ctx, const eagle_mx* x, const eagle_mx* w, const float* bias, int dtype, void* y,
+                          int ld_y, int* status, cudaStream_t st);
+// eagle_sample
+struct SampleLaunch {
+  int rows, vocab, dtype;
+  const void* logits;
+  int ld;
+  const eagle_filter* filter;
+  const uint32_t* u;
+  int32_t* token;
+  int32_t* argmax;
+  float* probs;
+  int ld_probs;
+  int* status;
+};
+cudaError_t launch_sample(eagle_ctx* ctx, const SampleLaunch& S, cudaStream_t st);
 size_t chunk_part_bytes(int sm_count, int head_dim);   // its partials
 int chunk_counters(int sm_count);                      // and arrival counters
 cudaError_t launch_pages_fork(eagle_ctx* ctx, const eagle_pages& pg, int n, const int32_t* src, const int32_t* dst,

@@ -1,0 +1,177 @@
+// Microscaled formats on the device: eight consecutive values of a thread into elements and the scales of their blocks,
+// and back (eagle_mx).
+#pragma once
+#include <cuda_fp8.h>
+
+#include "internal.h"
+#include "common.cuh"
+
+namespace eagle {
+
+// A matrix's addresses as kernels take them.
+struct MxView {
+  uint8_t* data;
+  uint8_t* scale;
+  const float* g;          // tensor factor, null: 1
+  int rows, cols;
+  int groups;              // 4-scale groups of a row
+};
+
+inline MxView mx_view(const eagle_mx* m) {
+  MxView v;
+  v.data = static_cast<uint8_t*>(m->data);
+  v.scale = m->scale;
+  v.g = m->format == EAGLE_NV_FP4 ? m->tensor_scale : nullptr;
+  v.rows = m->rows;
+  v.cols = m->cols;
+  v.groups = (m->cols / (m->format == EAGLE_NV_FP4 ? 16 : 32) + 3) / 4;
+  return v;
+}
+
+template <int FMT>
+constexpr int mx_block() { return FMT == EAGLE_NV_FP4 ? 16 : 32; }
+
+// Byte of scale 4 c of row r.
+__device__ __forceinline__ size_t mx_scale_at(const MxView& m, int r, int c) {
+  return (static_cast<size_t>(r >> 7) * m.groups + c) * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4;
+}
+
+__device__ __forceinline__ float mx_decode_e4m3(uint32_t byte) {
+  const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(byte), __NV_E4M3);
+  return __half2float(__half(h));
+}
+__device__ __forceinline__ uint32_t mx_pack_e2m1(const float (&v)[8]) {
+  uint32_t w;
+  asm("{\n .reg .b8 a, b, c, d;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+      " mov.b32 %0, {a, b, c, d};\n}\n"
+      : "=r"(w)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return w;
+}
+__device__ __forceinline__ uint32_t mx_pack_e4m3(float a, float b, float c, float d) {
+  uint32_t w;
+  asm("{\n .reg .b16 l, h;\n cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n"
+      " mov.b32 %0, {l, h};\n}\n"
+      : "=r"(w)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return w;
+}
+
+// Eight consecutive values of row `row` from column `col` (a multiple of 8) on, held by each lane of a warp for
+// consecutive columns from a multiple of 256 on: elements, and the scales of their blocks.  Lanes past the last column
+// (`in` false) hold zeros.  A block's largest magnitude is the largest of its lanes' bit patterns (a NaN's is above
+// all).  Scales of powers of two are exact, and so is the product with their inverse; for NV_FP4 the fp32 quotient x / d
+// is one Newton step on x (1 / d) (Markstein 1990: the remainder x - q d is exact in one fused operation), so that
+// quotients that meet a tie exactly stay on it.  Returns whether the block has a NaN or an infinity.
+template <int FMT>
+__device__ __forceinline__ bool mx_put(const MxView& m, float g, int row, int col, bool in, const float (&x)[8],
+                                       int lane) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  if (FMT != EAGLE_NV_FP4) top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  const bool bad = top >= 0x7f800000u;
+  uint32_t byte;
+  float v[8];
+  if (FMT == EAGLE_NV_FP4) {
+    byte = bad ? 0x7fu
+           : top == 0u ? 0u
+               : static_cast<uint32_t>(__nv_cvt_float_to_fp8(__uint_as_float(top) / (6.0f * g), __NV_SATFINITE, __NV_E4M3));
+    const float d = mx_decode_e4m3(byte) * g;
+    const float r = d >= 0x1p-126f ? 1.0f / d : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float q = x[i] * r;
+      // (beyond 6 it saturates, and inf has no remainder; a zero keeps its sign)
+      v[i] = copysignf(fabsf(q) < 16.0f ? fmaf(fmaf(-q, d, x[i]), r, q) : q, x[i]);
+    }
+  } else {
+    // the largest element is 1.75 * 2^8 (e4m3) or 1.5 * 2^2 (e2m1)
+    const uint32_t lead = FMT == EAGLE_MX_FP8 ? 0x600000u : 0x400000u;
+    const int whole = FMT == EAGLE_MX_FP8 ? 8 : 2;
+    const int e = static_cast<int>(top >> 23) - whole + ((top & 0x7fffffu) > lead ? 1 : 0);
+    byte = bad ? 255u : static_cast<uint32_t>(max(e, 0));
+    const float inv = __uint_as_float(bad ? 0x7fffffffu : (254u - byte) << 23);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = x[i] * inv;
+  }
+  const int shift = FMT == EAGLE_NV_FP4 ? 1 : 2;                 // lanes a block, as a power of two
+  uint32_t word = byte << (8 * ((lane >> shift) & 3));
+  word |= __shfl_xor_sync(0xffffffffu, word, 1 << shift);
+  word |= __shfl_xor_sync(0xffffffffu, word, 2 << shift);
+  if (in) {
+    if (FMT == EAGLE_MX_FP8) {
+      *reinterpret_cast<uint2*>(m.data + static_cast<size_t>(row) * m.cols + col) =
+          make_uint2(mx_pack_e4m3(v[0], v[1], v[2], v[3]), mx_pack_e4m3(v[4], v[5], v[6], v[7]));
+    } else {
+      *reinterpret_cast<uint32_t*>(m.data + (static_cast<size_t>(row) * m.cols + col) / 2) = mx_pack_e2m1(v);
+    }
+    if ((lane & ((4 << shift) - 1)) == 0)
+      *reinterpret_cast<uint32_t*>(m.scale + mx_scale_at(m, row, col / (4 * mx_block<FMT>()))) = word;
+  }
+  return bad && in;
+}
+
+// The values of eight elements from `col` on.
+template <int FMT>
+__device__ __forceinline__ void mx_get(const MxView& m, float g, int row, int col, float (&v)[8]) {
+  const int block = col / mx_block<FMT>();
+  const uint32_t byte = m.scale[mx_scale_at(m, row, block >> 2) + (block & 3)];
+  float d;
+  if (FMT == EAGLE_NV_FP4) d = mx_decode_e4m3(byte) * g;
+  else d = __uint_as_float(byte == 255u ? 0x7fffffffu : byte == 0u ? 1u << 22 : byte << 23);
+  if (FMT == EAGLE_MX_FP8) {
+    const uint2 w = *reinterpret_cast<const uint2*>(m.data + static_cast<size_t>(row) * m.cols + col);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t two = ((i < 2 ? w.x : w.y) >> (16 * (i & 1))) & 0xffffu;
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
+      const float2 f = __half22float2(__half2(h));
+      v[2 * i] = f.x * d;
+      v[2 * i + 1] = f.y * d;
+    }
+  } else {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(m.data + (static_cast<size_t>(row) * m.cols + col) / 2);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      // sign, two bits of exponent (bias 1) and one of fraction, as a float 2^126 times too small
+      const uint32_t c = w >> (4 * i);
+      const float f = __uint_as_float(((c & 8u) << 28) | ((c & 7u) << 22)) * 0x1p126f;
+      v[i] = f * d;
+    }
+  }
+}
+
+// Eight elements of a row, from bf16 or fp32 and to them.
+__device__ __forceinline__ void load8(const uint16_t* p, float (&x)[8]) {
+  const uint4 w = *reinterpret_cast<const uint4*>(p);
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(u[i] << 16);
+    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+__device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8]) {
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    u[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+}
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+}  // namespace eagle

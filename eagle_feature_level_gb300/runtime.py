@@ -117,6 +117,34 @@ def _packed(specs, device):
     return flat, views
 
 
+_DTYPE = {torch.bfloat16: B.DTYPE_BF16, torch.float32: B.DTYPE_F32}
+
+
+def _rows2d(t: torch.Tensor, rows: int, cols: int, device, types=_DTYPE):
+    """(type, address, pitch) of [rows][cols] with contiguous rows."""
+    if t.dtype not in types or t.shape != (rows, cols) or (cols > 1 and t.stride(1) != 1) or t.device != device:
+        raise ValueError(f"needs [{rows}][{cols}] of {[str(x) for x in types]} with contiguous rows on {device}")
+    return _DTYPE[t.dtype], _p(t), (t.stride(0) if rows > 1 else -(-cols // 8) * 8)
+
+
+def _each(t: Optional[torch.Tensor], n: int, dtype, device) -> Optional[int]:
+    """Address of n contiguous values of a type (None: none)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"needs {n} contiguous {dtype} on {device}")
+    return _p(t)
+
+
+def _filter(temperature, top_k, top_p, min_p, requests: int, rows_each: int, rows_used) -> B.eagle_filter:
+    dev = next((t.device for t in (temperature, top_k, top_p, min_p, rows_used) if t is not None), None)
+    f = B.eagle_filter(_each(temperature, requests, torch.float32, dev), _each(top_k, requests, torch.int32, dev),
+                       _each(top_p, requests, torch.float32, dev), _each(min_p, requests, torch.float32, dev), rows_each,
+                       _each(rows_used, requests, torch.int32, dev))
+    f.tensors = (temperature, top_k, top_p, min_p, rows_used)    # they live as long as the struct does
+    return f
+
+
 class Round:
     """Caller-side buffers and ABI structs of one round (batch B, plan fixed)."""
 
@@ -192,6 +220,7 @@ class Round:
         self.draft_len_out = z(batch, **i32)
         self.draft_len_next = z(batch, **i32)    # after the draft-cache refresh
         self.seed, self.round_id = 0, 0
+        self.filter_c = None
         self._structs()
 
     def _structs(self):
@@ -216,6 +245,16 @@ class Round:
         self.seed, self.round_id = int(seed) & 0xFFFFFFFF, int(round_id) & 0xFFFFFFFF
         self.sampling_c = B.eagle_sampling(_p(self.temps), self.seed, self.round_id)
 
+    def set_filter(self, top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
+                   min_p: Optional[torch.Tensor] = None):
+        """The target's distribution in acceptance, cut per request by top_k (int32), top_p and min_p (fp32, device;
+        see eagle_sample): what the round commits is then distributed as that cut target's own tokens.  None of them:
+        the whole distribution."""
+        if top_k is None and top_p is None and min_p is None:
+            self.filter_c = None
+            return
+        self.filter_c = _filter(self.temps, top_k, top_p, min_p, self.B, self.S, self.t_size)
+
     # ---- the calls ------------------------------------------------------------
     def draft_and_tree(self, w_c: B.eagle_draft_weights):
         e, st, ws = self.eng, self.eng.stream(), self.eng.ws.data_ptr()
@@ -239,6 +278,13 @@ class Round:
 
     def accept(self):
         e = self.eng
+        if self.filter_c is not None:
+            V, ws, st = e.dims["vocab"], e.ws.data_ptr(), e.stream()
+            B.eagle_sample(e.ctx, self.B * self.S, V, B.DTYPE_F32, _p(self.target_logits), V, self.filter_c, None, None,
+                           _p(self.target_argmax), _p(self.target_probs), V, ws, st)
+            B.eagle_accept_from_probs(e.ctx, self.plan, self.B, self.tree_c, self.children_c, _p(self.target_probs),
+                                      _p(self.target_argmax), _p(self.probs), self.sampling_c, self.acc_c, ws, st)
+            return
         B.eagle_accept(e.ctx, self.plan, self.B, self.tree_c, self.children_c, _p(self.target_logits),
                        _p(self.probs), self.sampling_c, _p(self.target_probs), _p(self.target_argmax), self.acc_c,
                        e.ws.data_ptr(), e.stream())
@@ -445,3 +491,104 @@ class PagedCache:
     def advance(self):
         """The appended rows, if any, become the sequences' own."""
         self.len.copy_(self.len_next)
+
+
+# ---- the target's step around its cache ---------------------------------------
+
+MX_FORMATS = {"fp8": B.MX_FP8, "fp4": B.MX_FP4, "nv4": B.NV_FP4}
+
+
+class MxTensor:
+    """A matrix in a microscaled format (eagle_mx): its data, its scales and, for "nv4", the tensor's factor (an fp32
+    tensor of one element, or None for 1)."""
+
+    def __init__(self, eng: Engine, rows: int, cols: int, fmt: str, tensor_scale: Optional[torch.Tensor] = None,
+                 data: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None):
+        """data, scale: memory of another matrix of at least as many rows, to share."""
+        self.eng, self.rows, self.cols, self.fmt = eng, rows, cols, fmt
+        n_data, n_scale = B.eagle_mx_layout(MX_FORMATS[fmt], rows, cols)
+        u8 = dict(dtype=torch.uint8, device=eng.device)
+        self.data = torch.empty(n_data, **u8) if data is None else data
+        self.scale = torch.empty(n_scale, **u8) if scale is None else scale
+        for t, n in ((self.data, n_data), (self.scale, n_scale)):
+            if t.dtype != torch.uint8 or t.numel() < n or not t.is_contiguous():
+                raise ValueError(f"needs {n} contiguous bytes")
+        self.tensor_scale = tensor_scale
+        self.c = B.eagle_mx(_p(self.data), _p(self.scale), _each(tensor_scale, 1, torch.float32, self.data.device), rows,
+                            cols, MX_FORMATS[fmt])
+
+    def first(self, rows: int) -> "MxTensor":
+        """The first `rows` rows of this matrix's memory as a matrix."""
+        if not 1 <= rows <= self.rows:
+            raise ValueError(f"1 to {self.rows} rows")
+        return MxTensor(self.eng, rows, self.cols, self.fmt, self.tensor_scale, self.data, self.scale)
+
+    def quantize(self, x: torch.Tensor, swiglu: bool = False) -> "MxTensor":
+        """This matrix from x [rows][cols] (bf16 or fp32), or from SiLU(gate) * up of x = [gate | up]."""
+        dt, at, ld = _rows2d(x, self.rows, self.cols * (2 if swiglu else 1), self.data.device)
+        B.eagle_mx_quantize(self.eng.ctx, dt, B.ACT_SWIGLU if swiglu else B.ACT_NONE, at, ld, self.c,
+                            self.eng.ws.data_ptr(), self.eng.stream())
+        return self
+
+    def unpack(self, out: torch.Tensor) -> torch.Tensor:
+        dt, at, ld = _rows2d(out, self.rows, self.cols, self.data.device)
+        B.eagle_mx_unpack(self.eng.ctx, self.c, dt, at, ld, self.eng.ws.data_ptr(), self.eng.stream())
+        return out
+
+
+def mx_linear(x: MxTensor, w: MxTensor, out: torch.Tensor, bias: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """out [x.rows][w.rows] (bf16 or fp32) = x w^T + bias."""
+    e = x.eng
+    dt, at, ld = _rows2d(out, x.rows, w.rows, x.data.device)
+    B.eagle_mx_linear(e.ctx, x.c, w.c, _each(bias, w.rows, torch.float32, out.device), dt, at, ld, e.ws.data_ptr(),
+                      e.stream())
+    return out
+
+
+def add_norm(eng: Engine, x: torch.Tensor, out, gain: Optional[torch.Tensor] = None,
+             residual: Optional[torch.Tensor] = None, residual_out: Optional[torch.Tensor] = None,
+             eps: Optional[float] = None):
+    """h = x + residual (into residual_out); out = h / sqrt(mean(h^2) + eps) * gain, `out` a bf16 or fp32 tensor or an
+    MxTensor.  eps: the engine's rms_eps."""
+    rows, cols = x.shape
+    dt, xp, ld = _rows2d(x, rows, cols, x.device)
+    none = (B.DTYPE_F32, None, 0)
+    rd, rp, rl = none if residual is None else _rows2d(residual, rows, cols, x.device)
+    od, op, ol = none if residual_out is None else _rows2d(residual_out, rows, cols, x.device)
+    if residual is not None and residual_out is not None and rd != od:
+        raise ValueError("residual and residual_out have one type")
+    mx = out if isinstance(out, MxTensor) else None
+    yd, yp, yl = none if mx is not None else _rows2d(out, rows, cols, x.device)
+    n = B.eagle_norm(rows, cols, dt, xp, ld, rd if residual is not None else od, rp, rl, op, ol,
+                     _each(gain, cols, torch.float32, x.device), eng.dims_c.rms_eps if eps is None else eps, yd, yp, yl,
+                     B.ref(None if mx is None else mx.c))
+    B.eagle_add_norm(eng.ctx, n, eng.ws.data_ptr(), eng.stream())
+    return out
+
+
+class Sampler:
+    """Sampling controls of a batch (fp32 temperature, int32 top_k, fp32 top_p and min_p on the device, one a request;
+    None: off) and draws under them."""
+
+    def __init__(self, eng: Engine, requests: int, temperature: Optional[torch.Tensor] = None,
+                 top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
+                 min_p: Optional[torch.Tensor] = None, rows_each: int = 1, rows_used: Optional[torch.Tensor] = None):
+        self.eng, self.requests, self.rows_each = eng, requests, rows_each
+        self.c = _filter(temperature, top_k, top_p, min_p, requests, rows_each, rows_used)
+
+    def __call__(self, logits: torch.Tensor, u: Optional[torch.Tensor] = None, token: Optional[torch.Tensor] = None,
+                 argmax: Optional[torch.Tensor] = None, probs: Optional[torch.Tensor] = None):
+        """Row r of logits (bf16 or fp32) is request r // rows_each's: token from the 32-bit words u (int32 bits or
+        uint32), and / or argmax (int32) and probs (fp32)."""
+        n, V = logits.shape
+        if not 1 <= n <= self.requests * self.rows_each:
+            raise ValueError(f"1 to {self.requests * self.rows_each} rows")
+        dev = logits.device
+        dt, zp, ld = _rows2d(logits, n, V, dev)
+        pp, pl = (None, 0) if probs is None else _rows2d(probs, n, V, dev, (torch.float32,))[1:]
+        if u is not None and u.dtype == torch.uint32:
+            u = u.view(torch.int32)
+        B.eagle_sample(self.eng.ctx, n, V, dt, zp, ld, self.c, _each(u, n, torch.int32, dev),
+                       _each(token, n, torch.int32, dev), _each(argmax, n, torch.int32, dev), pp, pl,
+                       self.eng.ws.data_ptr(), self.eng.stream())
+        return token

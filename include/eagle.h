@@ -704,6 +704,146 @@ eagle_status eagle_pages_release(eagle_ctx* ctx, const eagle_pages* pages, const
 eagle_status eagle_pages_compact(eagle_ctx* ctx, const eagle_pages* pages, const eagle_pools* pools,
                                  void* workspace, cudaStream_t stream);
 
+/* ---- the target's step around its cache ----------------------------------- */
+/*
+ * What a target model run beside the round computes besides the attention over
+ * its cache: norms with the residual's addition, linear layers in microscaled
+ * 8 and 4 bits, and tokens or whole distributions out of its logits.  As
+ * everywhere, calls (and graph replays) on one workspace are ordered, every
+ * call can be captured, and nothing is kept from one call for the next.
+ */
+
+/* Microscaled formats: a row's elements in blocks, each block with a scale of
+ * 8 bits, value = element * scale (* tensor_scale).
+ *   FP8: e4m3 (up to 448), FP4: e2m1 (0, .5, 1, 1.5, 2, 3, 4, 6 and sign), both
+ *        in blocks of 32 with a scale 2^(byte - 127): the smallest power of two
+ *        (from 2^-127 on) that brings the block's largest magnitude within the
+ *        element type's range, so that no element saturates;
+ *   NV_FP4: e2m1 in blocks of 16 with an e4m3 scale s and the tensor's fp32 factor
+ *        g: s is the fp32 quotient largest / (6 g) rounded to e4m3 (at most
+ *        448; 0 for a block of zeros), the elements are rounded from the fp32
+ *        quotients x / d, d = s g in fp32 (zeros where d is below 2^-126).
+ * All roundings go to the nearest, ties to even. */
+typedef enum { EAGLE_MX_FP8 = 1, EAGLE_MX_FP4 = 2, EAGLE_NV_FP4 = 3 } eagle_mx_format;
+
+/* A matrix in such a format.  data: [rows][cols] elements, a byte each (FP8)
+ * or two to a byte, the first in its low half.  scale: with n = cols / block
+ * scales a row, groups of 128 rows x 4 scales, [ceil(rows / 128)][ceil(n / 4)]
+ * of 512 bytes, in which scale j of row r is byte
+ *   (r % 32) * 16 + (r % 128) / 32 * 4 + j % 4.
+ * Scales behind a row's last one (up to the multiple of 4) are 0; those of rows
+ * behind the last may hold anything.  tensor_scale (NV_FP4): one positive
+ * fp32 number (device) that the caller sets, NULL: 1; not looked at otherwise.
+ * cols is a multiple of 32. */
+typedef struct {
+  void* data;
+  uint8_t* scale;
+  const float* tensor_scale;
+  int rows, cols;
+  int format;
+} eagle_mx;
+
+/* Bytes of a matrix's data and scales (host only). */
+eagle_status eagle_mx_layout(int format, int rows, int cols, size_t* data_bytes, size_t* scale_bytes);
+
+/* What stands in front of a quantisation.  SWIGLU: x holds 2 cols elements a
+ * row, a gate's and then its partner's, and SiLU(gate) * partner is quantised
+ * (computed in fp32, not rounded in between). */
+typedef enum { EAGLE_ACT_NONE = 0, EAGLE_ACT_SWIGLU = 1 } eagle_act;
+
+/* eagle_mx_quantize -- out = x in its format.  x [out->rows][ld_x] of `dtype`;
+ * pitches as for eagle_kv_append.  A block that holds a NaN or an infinity gets
+ * a NaN for its scale (its row of a product is then NaN) and sets
+ * EAGLE_ERR_NUMERIC in the status word. */
+eagle_status eagle_mx_quantize(eagle_ctx* ctx, int dtype, int act, const void* x, int ld_x, const eagle_mx* out,
+                               void* workspace, cudaStream_t stream);
+
+/* eagle_mx_unpack -- y [x->rows][ld_y] of `dtype`: the values that x stands
+ * for, element * (scale * tensor_scale) in fp32, rounded to `dtype`. */
+eagle_status eagle_mx_unpack(eagle_ctx* ctx, const eagle_mx* x, int dtype, void* y, int ld_y, void* workspace,
+                             cudaStream_t stream);
+
+/* eagle_mx_linear -- y[r][n] = sum_k x[r][k] w[n][k] + bias[n], x and w of one
+ * format and cols: a linear layer's weights w [outputs][inputs] as PyTorch has
+ * them.  Sums are fp32, tensor factors enter them at the end; y [x->rows][ld_y]
+ * of `dtype`, rounded once; ld_y >= w->rows and a multiple of 8 (bf16) or 4
+ * (fp32) elements; elements of y behind w->rows are not written.  bias fp32
+ * [w->rows] or NULL.  y must not overlap the operands. */
+eagle_status eagle_mx_linear(eagle_ctx* ctx, const eagle_mx* x, const eagle_mx* w, const float* bias, int dtype,
+                             void* y, int ld_y, void* workspace, cudaStream_t stream);
+
+/* eagle_add_norm -- for every row
+ *   h = x + residual;  residual_out = h;  out = h / sqrt(mean(h^2) + eps) * gain.
+ * x of `dtype`, residual and residual_out of `res_dtype`, out of `out_dtype`
+ * or, with out_mx instead, in its format (quantised as eagle_mx_quantize does,
+ * with its NaN rule).  The arithmetic is fp32 throughout: h enters the norm and
+ * the products unrounded, each output is rounded once.  residual NULL: h = x;
+ * residual_out NULL: not wanted.  residual_out may be residual itself, out may
+ * be x (each with the same pitch and type); no other overlaps.  gain fp32 [cols]
+ * or NULL (ones).  cols a multiple of 8 (32 with out_mx), at most
+ * EAGLE_MAX_NORM_COLS; eps >= 0. */
+#define EAGLE_MAX_NORM_COLS 32768
+typedef struct {
+  int rows, cols;
+  int dtype;
+  const void* x;
+  int ld_x;
+  int res_dtype;
+  const void* residual;
+  int ld_res;
+  void* residual_out;
+  int ld_res_out;
+  const float* gain;
+  float eps;
+  int out_dtype;
+  void* out;
+  int ld_out;
+  const eagle_mx* out_mx;  /* host struct */
+} eagle_norm;
+eagle_status eagle_add_norm(eagle_ctx* ctx, const eagle_norm* norm, void* workspace, cudaStream_t stream);
+
+/* Controls of eagle_sample, one value a request (device arrays; NULL: the
+ * control is off for all).  Row r of the logits belongs to request
+ * r / rows_each; with rows_used, rows r with r % rows_each >= rows_used[request]
+ * are neither read nor written (a tree's slots behind its size).
+ *   temperature  <= 0: greedy; NULL: 1
+ *   top_k        <= 0: off
+ *   top_p        >= 1: off
+ *   min_p        <= 0: off */
+typedef struct {
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  int rows_each;
+  const int32_t* rows_used;
+} eagle_filter;
+
+/* eagle_sample -- a row's distribution and a draw from it.  With z the row's
+ * logits, m their maximum, t the temperature, token i has the weight
+ *   w_i = floor(2^40 e^((z_i - m) / t))
+ * (as everywhere draws are on whole weights).  In the order of falling z, the
+ * lower id first among equals,
+ *   top_k keeps the first k tokens;
+ *   top_p, of those, the shortest beginning whose weights sum to at least
+ *         ceil(p S), S the sum of all that top_k kept (at least one token);
+ *   min_p, of those, the tokens with w_i >= p 2^40 (the largest, 2^40, always).
+ * With W the sum of what is kept and u the row's 32-bit word, the token is the
+ * first in the order of ids at which the kept weights sum to more than
+ * floor(u W / 2^32); probs are w_i / W, zero where not kept.  A greedy row is
+ * all on its argmax.  Logits may be -inf (weight 0).  A row without a finite
+ * logit, or with a NaN or +inf, gets token -1, argmax -1 and zero probs and
+ * sets EAGLE_ERR_NUMERIC in the status word.
+ * logits [n_rows][ld] of `dtype`, 1 <= vocab <= EAGLE_MAX_SAMPLE_VOCAB; u [n_rows] and
+ * token [n_rows] go together, each may be NULL with the other; argmax [n_rows]
+ * (ties to the lower id) or NULL; probs fp32 [n_rows][ld_probs] or NULL, any
+ * overlap with the logits excepted.  probs and argmax are what
+ * eagle_accept_from_probs takes as the target's. */
+#define EAGLE_MAX_SAMPLE_VOCAB 262144
+eagle_status eagle_sample(eagle_ctx* ctx, int n_rows, int vocab, int dtype, const void* logits, int ld,
+                          const eagle_filter* filter, const uint32_t* u, int32_t* token, int32_t* argmax,
+                          float* probs, int ld_probs, void* workspace, cudaStream_t stream);
+
 /* ---- measurement --------------------------------------------------------- */
 
 /* Kernel timing hook: while enabled, the library records a CUDA event before
@@ -715,7 +855,8 @@ typedef enum {
   EAGLE_K_GEMM_GATEUP = 3, EAGLE_K_GEMM_DOWN = 4, EAGLE_K_GEMM_LM = 5, EAGLE_K_DRAFT_ATTN = 6,
   EAGLE_K_SELECT = 7, EAGLE_K_TREE = 8, EAGLE_K_VERIFY_ATTN = 9, EAGLE_K_ACCEPT = 10,
   EAGLE_K_COMMIT = 11, EAGLE_K_PREP = 12, EAGLE_K_REFRESH = 13, EAGLE_K_FUSE = 14,
-  EAGLE_K_APPEND = 15, EAGLE_K_CHUNK_ATTN = 16, EAGLE_K_PAGES = 17
+  EAGLE_K_APPEND = 15, EAGLE_K_CHUNK_ATTN = 16, EAGLE_K_PAGES = 17, EAGLE_K_NORM = 18, EAGLE_K_QUANT = 19,
+  EAGLE_K_LINEAR = 20, EAGLE_K_SAMPLE = 21
 } eagle_kernel_id;
 eagle_status eagle_trace_enable(eagle_ctx* ctx, int kernel_id, int capacity);
 /* Synchronises the recorded events; writes up to `cap` durations in ms, the

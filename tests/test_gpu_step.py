@@ -1,0 +1,764 @@
+"""The target's step around its cache on the GPU: eagle_add_norm, eagle_mx_quantize, eagle_mx_unpack, eagle_mx_linear and
+eagle_sample against the oracle (oracle/step.py, fp64), alone and strung together with the cache's calls.
+
+Tolerances, fixed before the first run (u(t) = half a step of type t relative to the value: bf16 2^-8 with the last bit of
+fp32 work before it, fp32 2^-24):
+* quantisation of given rows: codes and scales are the definition's, bit for bit; behind fp32 arithmetic (SiLU, norms)
+  that is off by at most REL = 2^-18 of a value, each block's scale is that of a largest magnitude within REL, and each
+  element is a nearest one for that scale to a value within REL (plus the fp32 quotient's 2^-23);
+* norms: one fp32 rounding of the sum; the mean of squares sums at most 8 * 4 terms a thread and 10 levels of pairs, 42
+  roundings of 2^-24 at most, halved by the root, and five more roundings: below 2^-18 in all;
+* products: operands are exact; each of the K additions (and the alignment before it) loses at most 2^-23 of the sum of
+  magnitudes so far, a further 8 for split sums, factors and the bias: (K + 8) 2^-23 sum |x w|, then one rounding;
+* sampling: a weight is off by at most 2 units of 2^-40, so sums by 2 V: a border of top_p or of the draw may fall on either
+  side within that; probabilities by 2^-22 relative."""
+import math
+import random
+
+import numpy as np
+import pytest
+import torch
+
+from eagle_feature_level_gb300 import _binding as B
+from eagle_feature_level_gb300 import runtime as R
+from eagle_feature_level_gb300.runtime import _p
+from oracle import step as O
+from oracle.sampling import draw_one
+
+pytestmark = pytest.mark.gpu
+
+INVALID_ARG, SHAPE, ALIGN, CAPACITY, NUMERIC = 1, 2, 3, 4, 6
+BF16, F32 = torch.bfloat16, torch.float32
+U = {BF16: 2.0 ** -8, F32: 2.0 ** -24}
+REL = 2.0 ** -18
+NAN, INF = float("nan"), float("inf")
+_engine = []
+
+
+def engine():
+    if not _engine:
+        _engine.append(R.Engine(dict(d=512, n_q_heads=4, n_kv_heads=2, head_dim=64, d_ff=64, vocab=64), max_batch=64,
+                                max_rows=8, max_expanded=1, max_children=1, max_tree=2, max_prefix=1024, device="cuda"))
+    return _engine[0]
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def normal(seed, *shape, dtype=F32):
+    return torch.randn(*shape, generator=gen(seed), device="cuda").to(dtype)
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def f32(x):
+    return torch.tensor(x, dtype=F32, device="cuda")
+
+
+def pitched(t, more):
+    """The same values with rows `more` elements further apart, the gaps NaN."""
+    wide = torch.full((t.shape[0], t.shape[1] + more), NAN, dtype=t.dtype, device="cuda")
+    wide[:, :t.shape[1]] = t
+    return wide[:, :t.shape[1]]
+
+
+def mx(fmt, rows, cols, g=None):
+    t = R.MxTensor(engine(), rows, cols, fmt, None if g is None else f32([g]))
+    t.data.fill_(0xa5)
+    t.scale.fill_(0xff)                                  # NaN scales where nothing is written
+    return t
+
+
+def codes(t):
+    n = t.rows * t.cols // (1 if t.fmt == "fp8" else 2)
+    return O.unpack_bytes(t.fmt, t.data[:n].cpu().numpy(), t.scale.cpu().numpy(), t.rows, t.cols)
+
+
+def factor(t):
+    return 1.0 if t.tensor_scale is None else float(t.tensor_scale.reshape(-1)[0])
+
+
+def held(t):
+    c, b = codes(t)
+    return O.values(t.fmt, c, b[:, :t.cols // O.BLOCK[t.fmt]], factor(t))
+
+
+def is_quantized(t, y, rel=0.0):
+    code, byte = codes(t)
+    n = t.cols // O.BLOCK[t.fmt]
+    assert not byte[:, n:].any()
+    byte = byte[:, :n]
+    want_code, want_byte = O.quantize(t.fmt, y, factor(t))
+    if rel == 0.0:
+        assert np.array_equal(byte, want_byte)
+        assert np.array_equal(code, want_code)
+        return
+    near = [O.quantize(t.fmt, y * (1 + d), factor(t))[1] for d in (-rel, rel)]
+    assert ((byte == near[0]) | (byte == near[1])).all()
+    v = O.values(t.fmt, np.zeros_like(code), byte, factor(t))      # shapes
+    s = (O.E4M3[byte].astype(np.float32) * np.float32(factor(t))).astype(np.float64) if t.fmt == "nv4" else \
+        2.0 ** (byte.astype(float) - 127)
+    s = s.repeat(O.BLOCK[t.fmt], 1)
+    q = np.where(s > 0, y / np.where(s > 0, s, 1), 0)
+    table = O.E4M3 if t.fmt == "fp8" else O.E2M1
+    mag, sign = (code & 127, code >> 7) if t.fmt == "fp8" else (code & 7, code >> 3)
+    lo, hi = O.nearest_code(table, np.abs(q) * (1 - rel - 2.0 ** -23)), O.nearest_code(table, np.abs(q) * (1 + rel + 2.0 ** -23))
+    assert ((mag >= lo) & (mag <= hi)).all()
+    assert ((sign == np.signbit(q)) | (mag == 0)).all() and v.shape == code.shape
+
+
+FORMATS = ["fp8", "fp4", "nv4"]
+SHAPES = [(1, 32), (1, 4096), (3, 96), (31, 160), (33, 64), (127, 1056), (129, 256), (260, 288), (700, 32)]
+
+
+# ---- quantisation ---------------------------------------------------------------
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_quantize_and_unpack(fmt, dtype, shape):
+    x = normal(1, *shape) * torch.exp(3 * normal(2, shape[0], 1)) * torch.exp(normal(3, 1, shape[1]))
+    x[0, :32] = 0
+    x[-1, -16:] = x[-1, -16:].sign() * 2.0 ** -20
+    x = pitched(x.to(dtype), 8)
+    g = float(x.abs().max()) / 2688 if fmt == "nv4" else None
+    t = mx(fmt, *shape, g).quantize(x)
+    is_quantized(t, f64(x))
+    for out in (BF16, F32):
+        y = pitched(torch.zeros(shape, dtype=out, device="cuda"), 16)
+        t.unpack(y)
+        want = held(t)
+        assert (np.abs(f64(y) - want) <= U[out] * np.abs(want) + 2.0 ** -24 * np.abs(want)).all()
+    assert engine().status() == 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_quantize_borders(fmt):
+    """Exact ties, largest magnitudes at the scale's borders, tiny and huge blocks, signed zeros."""
+    rows = []
+    for e in (-130, -126, -100, -20, -1, 0, 1, 20, 100, 125):
+        for m in (1.0, 1.25, 1.5, 1.5 + 2.0 ** -23, 1.75, 1.75 + 2.0 ** -23, 2 - 2.0 ** -23):
+            top = m * 2.0 ** e
+            r = np.array([top, -top] + [top * k / 48 for k in range(1, 31)])
+            rows.append(r)
+    for k in range(8):
+        rows.append(np.array([6.0, -5.0, 3.5, -3.5, 2.5, 1.75, 1.25, 0.75, 0.25, -0.25, -0.0, 0.0, 5.0, 4.5, 1e-30, -1e-30] * 2) *
+                    2.0 ** (k - 4))
+    x = torch.tensor(np.array(rows), dtype=F32, device="cuda")
+    t = mx(fmt, *x.shape, 2.0 ** 100 if fmt == "nv4" else None).quantize(x)
+    is_quantized(t, f64(x))
+    if fmt == "nv4":
+        for g in (1.0, 0.37, 2.0 ** -90):
+            t = mx(fmt, *x.shape, g).quantize(x)
+            is_quantized(t, f64(x))
+        t = mx(fmt, *x.shape).quantize(x)                # no factor: 1
+        is_quantized(t, f64(x))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("shape", [(1, 32), (5, 11008), (130, 96)])
+def test_quantize_gated(fmt, dtype, shape):
+    x = (normal(4, shape[0], 2 * shape[1]) * 3).to(dtype)
+    x[0, 0], x[0, 1] = -200.0, 200.0                     # SiLU's far ends
+    t = mx(fmt, *shape, 0.01 if fmt == "nv4" else None).quantize(pitched(x, 24), swiglu=True)
+    y = O.swiglu(f64(x))
+    # exp is off by 2 steps (2^-22), 1 + exp, the quotient and the product by one each
+    is_quantized(t, y, 2.0 ** -21)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("value", [NAN, INF, -INF])
+def test_quantize_reports_non_finite_blocks(fmt, value):
+    x = normal(5, 4, 128)
+    x[2, 70] = value
+    t = mx(fmt, 4, 128, 0.01).quantize(x)
+    assert engine().status() == NUMERIC
+    y = t.unpack(torch.empty(4, 128, device="cuda"))
+    b = O.BLOCK[fmt]
+    bad = torch.zeros(4, 128, dtype=torch.bool, device="cuda")
+    bad[2, 70 // b * b:70 // b * b + b] = True
+    assert torch.equal(torch.isnan(y), bad)
+    w = mx(fmt, 40, 128, 0.01).quantize(normal(6, 40, 128))
+    out = R.mx_linear(t, w, torch.empty(4, 40, device="cuda"))
+    assert torch.isnan(out[2]).all() and torch.isfinite(out[[0, 1, 3]]).all()
+    assert engine().status() == 0
+
+
+# ---- linear layers ----------------------------------------------------------------
+
+def check_linear(fmt, rows, cols, outs, out=BF16, bias=False, seed=0, more=0, g=(0.02, 0.003)):
+    a, b = (g if fmt == "nv4" else (None, None))
+    x = mx(fmt, rows, cols, a).quantize(normal(seed + 1, rows, cols) * torch.exp(0.5 * normal(seed + 2, 1, cols)))
+    w = mx(fmt, outs, cols, b).quantize(normal(seed + 3, outs, cols) * 0.1)
+    bs = normal(seed + 4, outs) if bias else None
+    ld = (outs + 7) // 8 * 8 + more
+    y = torch.full((rows + 1, ld), 77.0, dtype=out, device="cuda")
+    R.mx_linear(x, w, y[:rows, :outs], bs)
+    xv, wv = (torch.tensor(held(t), device="cuda") for t in (x, w))
+    want, size = xv @ wv.t(), xv.abs() @ wv.abs().t()
+    if bias:
+        want, size = want + bs.double(), size + bs.double().abs()
+    err = (y[:rows, :outs].double() - want).abs()
+    assert bool((err <= (cols + 8) * 2.0 ** -23 * size + U[out] * want.abs()).all()), float((err / size).max())
+    # nothing behind the outputs and the rows
+    assert bool((y[rows:] == 77).all()) and bool((y[:, outs:] == 77).all())
+    assert engine().status() == 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("rows", [1, 2, 15, 16, 17, 31, 64, 65, 100, 128, 129, 191, 192, 193, 250, 320, 500])
+def test_linear_rows(fmt, rows):
+    check_linear(fmt, rows, 512, 300, seed=rows)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("cols", [32, 64, 96, 128, 160, 224, 256, 288, 384, 992, 2080, 5120, 11008])
+def test_linear_inner(fmt, cols):
+    check_linear(fmt, 9, cols, 200, F32, seed=cols)
+    check_linear(fmt, 200, cols, 130, F32, seed=cols + 1)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("outs", [1, 7, 8, 127, 128, 129, 1000, 20000])
+def test_linear_outputs(fmt, outs):
+    check_linear(fmt, 5, 1024, outs, BF16, True, seed=outs, more=8)
+    check_linear(fmt, 140, 256, outs, F32, True, seed=outs + 1)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("shape", [(1, 4096, 12288), (8, 8192, 1024), (40, 8192, 4096), (777, 1024, 2500), (2000, 512, 3000),
+                                   (600, 320, 9000), (4097, 96, 257)])
+def test_linear_large(fmt, shape):
+    check_linear(fmt, *shape, bias=True)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_linear_exact_products(fmt):
+    """Whole numbers whose sums fit in fp32: every product and sum is exact, so a wrong scale or element anywhere shows."""
+    rows, cols, outs = 150, 640, 190
+    r = np.random.default_rng(7)
+    def make(n):
+        t = mx(fmt, n, cols)
+        code = r.integers(0, 16, (n, cols)) if fmt != "fp8" else np.where(r.random((n, cols)) < 0.5, 0x38, 0x40) | \
+            (r.integers(0, 2, (n, cols)) << 7)
+        blocks = cols // O.BLOCK[fmt]
+        byte = r.integers(126, 129, (n, blocks)) if fmt != "nv4" else r.choice([0x30, 0x38, 0x40], (n, blocks))
+        data, scale = O.pack_bytes(fmt, code.astype(np.uint8), byte.astype(np.uint8), 0xff if fmt != "nv4" else 0x7f)
+        t.data.copy_(torch.tensor(data.reshape(-1)))
+        t.scale.copy_(torch.tensor(scale))
+        return t
+    x, w = make(rows), make(outs)
+    y = R.mx_linear(x, w, torch.empty(rows, 192, device="cuda")[:, :outs])
+    assert np.array_equal(f64(y), held(x) @ held(w).T)
+
+
+def test_linear_shared_rows_of_a_buffer():
+    """The first rows of a larger buffer, whose other rows hold NaN scales."""
+    big = mx("nv4", 300, 256, 0.02)
+    x = normal(8, 130, 256)
+    part = big.first(130).quantize(x)
+    w = mx("nv4", 64, 256, 0.01).quantize(normal(9, 64, 256) * 0.1)
+    y = R.mx_linear(part, w, torch.empty(130, 64, device="cuda"))
+    want = held(part) @ held(w).T
+    assert np.allclose(f64(y), want, atol=1e-4) and np.isfinite(f64(y)).all()
+
+
+# ---- norms ------------------------------------------------------------------------
+
+def check_norm(rows, cols, dtype, res, out, gain=True, eps=1e-5, seed=0, in_place=False, scale=1.0):
+    x = pitched((normal(seed + 1, rows, cols) * scale).to(dtype), 16)
+    r = None if res is None else pitched((normal(seed + 2, rows, cols) * 3 * scale).to(res), 8)
+    g = 1 + 0.5 * normal(seed + 3, cols) if gain else None
+    xs, rs = f64(x), None if r is None else f64(r)
+    ro = None if r is None else r if in_place else pitched(torch.zeros_like(r), 24)
+    if out in FORMATS:
+        y = mx(out, rows, cols, 0.003 if out == "nv4" else None)
+    else:
+        y = x if in_place and out == dtype else pitched(torch.zeros(rows, cols, dtype=out, device="cuda"), 8)
+    R.add_norm(engine(), x, y, g, r, ro, eps)
+    h, want = O.add_norm(xs, rs, None if g is None else f64(g), eps)
+    if r is not None:
+        assert (np.abs(f64(ro) - h) <= (U[res] + 2.0 ** -24) * np.abs(h)).all()
+    if out in FORMATS:
+        is_quantized(y, want, REL)
+    else:
+        assert (np.abs(f64(y) - want) <= (U[out] + REL) * np.abs(want) + 1e-40).all()
+    assert engine().status() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("res", [None, BF16, F32])
+@pytest.mark.parametrize("out", [BF16, F32] + FORMATS)
+def test_norm_types(dtype, res, out):
+    check_norm(37, 1056, dtype, res, out)
+
+
+@pytest.mark.parametrize("shape", [(1, 32), (7, 64), (300, 256), (9, 288), (5, 1024), (3, 4096), (2, 4128), (3, 8192), (2, 11008),
+                                   (2, 16416), (1, 32768), (1000, 96)])
+@pytest.mark.parametrize("out", [BF16, "fp8", "nv4"])
+def test_norm_shapes(shape, out):
+    check_norm(*shape, BF16, F32, out, seed=shape[1])
+
+
+@pytest.mark.parametrize("cols", [8, 24, 40, 1000, 5128])
+def test_norm_columns_by_eights(cols):
+    check_norm(4, cols, BF16, BF16, BF16)
+    check_norm(4, cols, F32, None, F32, gain=False)
+
+
+def test_norm_in_place_and_extremes():
+    check_norm(20, 512, BF16, F32, BF16, in_place=True)
+    check_norm(20, 512, F32, BF16, F32, in_place=True)
+    check_norm(3, 512, F32, None, F32, eps=0.0, scale=1e-15)
+    check_norm(3, 512, F32, F32, F32, scale=1e15)
+    x = torch.zeros(2, 64, device="cuda")
+    y = R.add_norm(engine(), x, torch.full_like(x, 5.0))
+    assert not y.any()                                   # an all-zero row
+    x[1, 3] = NAN
+    t = mx("fp8", 2, 64)
+    R.add_norm(engine(), x, t)
+    assert engine().status() == NUMERIC
+    y = t.unpack(y)
+    assert not y[0].any() and torch.isnan(y[1]).all()
+
+
+# ---- sampling -----------------------------------------------------------------------
+
+def check_sample(z, t, k=None, p=None, m=None, u=None, each=1, want_probs=True, used=None):
+    """z [rows][vocab] (possibly pitched) against the oracle; t, k, p, m: per-request lists or None."""
+    n, V = z.shape
+    req = n // each
+    u = normal(99, n).view(torch.int32) if u is None else u
+    token, arg = i32([-7] * n), i32([-7] * n)
+    probs = torch.full((n, V), 7.0, device="cuda") if want_probs else None
+    s = R.Sampler(engine(), req, None if t is None else f32(t), None if k is None else i32(k), None if p is None else f32(p),
+                  None if m is None else f32(m), each, None if used is None else i32(used))
+    s(z, u, token, arg, probs)
+    zs, us, tok, am = f64(z), u.cpu().numpy().astype(np.int64) & 0xffffffff, token.cpu().numpy(), arg.cpu().numpy()
+    ps = f64(probs) if want_probs else None
+    at = lambda v, i, d: d if v is None else float(np.float32(v[i // each]))
+    for i in range(n):
+        if used is not None and i % each >= used[i // each]:
+            assert tok[i] == -7 and am[i] == -7 and (ps is None or (ps[i] == 7).all())
+            continue
+        ti = at(t, i, 1.0)
+        w = O.weights(zs[i], ti)
+        slack = 2 * V
+        assert am[i] == np.flatnonzero(zs[i] == zs[i].max())[0]
+        if not ti > 0:
+            lo = hi = 1
+            order = np.array([am[i]])
+        else:
+            order, lo, hi = O.kept(zs[i], w, 0 if k is None else k[i // each], at(p, i, 1.0), slack=slack)
+        mi = min(at(m, i, 0.0), 1.0)
+        ok = False
+        for c in range(lo, hi + 1):                      # the cuts that whole weights within the slack allow
+            x = np.zeros_like(w)
+            x[order[:c]] = w[order[:c]]
+            if ti > 0:
+                x[x < mi * 2.0 ** 40] = 0
+            total = int(x.sum())
+            upto = int(x[:tok[i] + 1].sum())
+            r = (int(us[i]) * total) >> 32
+            near = upto - int(x[tok[i]]) - slack <= r < upto + slack and x[tok[i]] > 0
+            if want_probs:
+                q = x / total
+                # weights of few units may be there or not
+                near = near and (np.abs(ps[i] - q) <= 2.0 ** -22 * q + 4.0 / total).all() and ((ps[i] > 0) == (x > 0))[x != 1].all()
+            ok = ok or bool(near)
+        assert ok, (i, lo, hi, tok[i])
+    assert engine().status() == 0
+    return token, probs
+
+
+VOCABS = [1, 2, 7, 33, 1000, 4095, 4096, 4097, 8192, 16385, 32000, 65537, 131072, 262144]
+
+
+@pytest.mark.parametrize("vocab", VOCABS)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_sample_vocabularies(vocab, dtype):
+    z = (normal(vocab, 4, vocab) * 3).to(dtype)
+    check_sample(z, [0.7, 1.0, 0.0, 1.3], [5, 0, 0, 40], [0.9, 0.8, 0.5, 1.0], [0.0, 0.01, 0.0, 0.05])
+
+
+@pytest.mark.parametrize("case", ["none", "k", "p", "m", "kp", "km", "pm", "kpm"])
+@pytest.mark.parametrize("rows", [1, 40, 200])
+def test_sample_controls(case, rows):
+    r = random.Random(rows)
+    z = normal(rows, rows, 3000) * 2.5
+    check_sample(z, [r.uniform(0.3, 1.5) for _ in range(rows)],
+                 [r.choice([0, 1, 2, 50, 2999, 3000, 9999]) for _ in range(rows)] if "k" in case else None,
+                 [r.choice([0.0, -1.0, 1e-6, 0.3, 0.95, 0.9999, 1.0, 2.0]) for _ in range(rows)] if "p" in case else None,
+                 [r.choice([0.0, -1.0, 1e-9, 0.05, 0.5, 1.0, 3.0]) for _ in range(rows)] if "m" in case else None)
+
+
+def test_sample_ties():
+    """Equal logits: the lower ids stay; whole rows of one value, more than a list or a bin takes."""
+    for V in (64, 5000, 40000):
+        z = torch.zeros(3, V, device="cuda")
+        check_sample(z, [1.0, 0.5, 2.0], [1, 17, V - 3])
+        check_sample(z, [1.0, 0.5, 2.0], None, [0.5, 1e-5, 0.999])
+        z[:, 1::2] = 1.0
+        z[:, 5] = -3.0
+        check_sample(z, [1.0, 0.5, 2.0], [V // 2 + 1, V // 2, 3], [0.7, 1.0, 0.2])
+    z = torch.round(normal(3, 6, 20000) * 4) / 4         # a hundred values or so
+    check_sample(z, [0.8] * 6, [3000, 1, 700, 0, 0, 0], [1.0, 1.0, 0.6, 0.5, 0.99, 0.9])
+    z = normal(4, 4, 30000) * 1e-3                       # all in a hair's breadth of one another
+    check_sample(z, [1.0] * 4, [20000, 0, 5, 0], [0.9, 0.5, 1.0, 0.01])
+    z = 1000 + normal(5, 4, 30000).to(BF16).float() * 0.01
+    check_sample(z, [1.0] * 4, [20000, 0, 5, 0], [0.9, 0.5, 1.0, 0.01])
+
+
+def test_sample_masked_and_extreme():
+    z = normal(6, 8, 9000) * 3
+    z[0, 1:] = -INF                                      # one token left
+    z[1, ::2] = -INF
+    z[2] = -INF
+    z[2, 8999] = -3e38
+    z[3] *= 1e30
+    z[4, 7], z[4, 8] = 3.3e38, -3.3e38
+    z[5] = -0.0
+    z[5, 100] = 0.0
+    lowest = torch.finfo(F32).min
+    z[6, 10:] = lowest
+    check_sample(z, [1.0, 0.7, 1.0, 1.0, 2.0, 1.0, 1.0, 1e-3], [0, 60, 2, 5, 0, 3, 50, 0], [0.9, 0.9, 0.5, 1.0, 1.0, 0.9, 0.99, 0.9])
+    check_sample(z[1:2], [1e30])
+    check_sample(z[7:], [1e-38])
+    u = torch.tensor([0, -1, 1, 1 << 30, -(1 << 31), 5, 6, 7], dtype=torch.int32, device="cuda")
+    check_sample(z, [1.0] * 8, u=u)
+
+
+@pytest.mark.parametrize("bad", ["nan", "inf", "none"])
+def test_sample_reports_rows_without_a_distribution(bad):
+    z = normal(7, 3, 10000)
+    if bad == "none":
+        z[1] = -INF
+    else:
+        z[1, 9999] = NAN if bad == "nan" else INF
+    token, arg, probs = i32([5] * 3), i32([5] * 3), torch.full_like(z, 3.0)
+    R.Sampler(engine(), 3)(z, i32([1, 2, 3]), token, arg, probs)
+    assert engine().status() == NUMERIC
+    assert int(token[1]) == -1 and int(arg[1]) == -1 and not probs[1].any()
+    assert (token[[0, 2]] >= 0).all() and torch.allclose(probs[[0, 2]].sum(-1), torch.ones(2, device="cuda"))
+
+
+def test_sample_tree_rows_and_pitches():
+    used = [5, 0, 1, 3]
+    z = normal(8, 20, 1003) * 3
+    for b, n in enumerate(used):
+        z[b * 5 + n:(b + 1) * 5] = NAN                   # slots behind the trees' sizes
+    check_sample(pitched(z, 0), [0.8, 0.9, 0.0, 1.1], [40] * 4, [0.9] * 4, [0.02] * 4, each=5, used=used)
+    check_sample(pitched(z, 5), [0.8, 0.9, 0.0, 1.1], None, [0.9] * 4, each=5, used=used, want_probs=False)
+    probs = torch.full((20, 1010), 9.0, device="cuda")
+    R.Sampler(engine(), 4, rows_each=5, rows_used=i32(used))(z, probs=probs[:, :1003])
+    assert (probs[:, 1003:] == 9).all() and torch.allclose(probs[:5, :1003].sum(-1), torch.ones(5, device="cuda"))
+    assert engine().status() == 0
+
+
+def test_sample_draws_follow_the_distribution():
+    """One row, many words: every token exactly as often as its weight says (to a word)."""
+    z = (normal(9, 1, 50) * 2).expand(4096, 50).contiguous()
+    u = torch.arange(4096, device="cuda", dtype=torch.int64).mul(1 << 20).to(torch.int64)
+    u = torch.where(u >= 1 << 31, u - (1 << 32), u).int()
+    token = i32([0] * 4096)
+    R.Sampler(engine(), 4096, top_k=i32([20] * 4096))(z, u, token)
+    w = O.distribution(f64(z[0]), 1.0, 20)
+    n = np.bincount(token.cpu().numpy(), minlength=50)
+    assert (np.abs(n - 4096.0 * w / w.sum()) <= 1.0 + 1e-3).all()
+
+
+# ---- refusals -------------------------------------------------------------------------
+
+def refused(code, fn, *args):
+    with pytest.raises(B.EagleError) as e:
+        fn(*args)
+    assert e.value.code == code
+
+
+def test_arguments_checked_before_launch():
+    e = engine()
+    ws, st = e.ws.data_ptr(), e.stream()
+    buf = torch.zeros(1 << 16, device="cuda")
+    a = _p(buf)
+    before = B.eagle_launch_count(e.ctx)
+    X = lambda **kw: B.eagle_mx(*[{**dict(data=a, scale=a + 65536, tensor_scale=None, rows=4, cols=64, format=1), **kw}[f]
+                                  for f in ("data", "scale", "tensor_scale", "rows", "cols", "format")])
+    Q = lambda m, dtype=0, act=0, x=a + 4096, ld=64, w=ws: B.eagle_mx_quantize(e.ctx, dtype, act, x, ld, m, w, st)
+    for fn in (Q, lambda m: B.eagle_mx_unpack(e.ctx, m, 0, a + 4096, 64, ws, st),
+               lambda m: B.eagle_mx_linear(e.ctx, m, X(), None, 0, a + 4096, 64, ws, st),
+               lambda m: B.eagle_mx_linear(e.ctx, X(), m, None, 0, a + 4096, 64, ws, st)):
+        refused(INVALID_ARG, fn, X(format=0))
+        refused(INVALID_ARG, fn, X(format=4))
+        refused(SHAPE, fn, X(cols=48))
+        refused(SHAPE, fn, X(cols=0))
+        refused(SHAPE, fn, X(rows=0))
+        refused(INVALID_ARG, fn, X(data=None))
+        refused(ALIGN, fn, X(scale=a + 4))
+        refused(ALIGN, fn, X(format=3, tensor_scale=a + 2))
+    refused(INVALID_ARG, Q, X(), 2)
+    refused(INVALID_ARG, Q, X(), 0, 2)
+    refused(SHAPE, Q, X(), 0, 0, a, 56)
+    refused(SHAPE, Q, X(), 0, 1, a + 4096, 64)           # the gate and its partner need 128
+    refused(ALIGN, Q, X(), 0, 0, a + 4096, 68)
+    refused(ALIGN, Q, X(), 0, 0, a + 4098, 64)
+    refused(INVALID_ARG, Q, X(), 0, 0, a, 64)            # x is out
+    refused(INVALID_ARG, Q, X(), 0, 0, a + 4096, 64, None)
+    refused(INVALID_ARG, lambda: B.eagle_mx_linear(e.ctx, X(), X(format=2), None, 0, a + 4096, 64, ws, st))
+    refused(SHAPE, lambda: B.eagle_mx_linear(e.ctx, X(), X(cols=96), None, 0, a + 4096, 64, ws, st))
+    refused(SHAPE, lambda: B.eagle_mx_linear(e.ctx, X(), X(rows=72), None, 0, a + 4096, 64, ws, st))
+    refused(ALIGN, lambda: B.eagle_mx_linear(e.ctx, X(), X(rows=9), None, 0, a + 4096, 9, ws, st))
+    refused(ALIGN, lambda: B.eagle_mx_linear(e.ctx, X(), X(), a + 4, 0, a + 4096, 64, ws, st))
+    refused(INVALID_ARG, lambda: B.eagle_mx_linear(e.ctx, X(), X(), None, 0, a, 64, ws, st))
+    refused(INVALID_ARG, lambda: B.eagle_mx_linear(e.ctx, X(), X(), None, 3, a + 4096, 64, ws, st))
+
+    def N(code, **kw):
+        base = dict(rows=4, cols=64, dtype=0, x=a, ld_x=64, res_dtype=1, residual=a + 4096, ld_res=64, residual_out=a + 8192,
+                    ld_res_out=64, gain=a + 16384, eps=1e-5, out_dtype=0, out=a + 32768, ld_out=64, out_mx=None)
+        base.update(kw)
+        refused(code, B.eagle_add_norm, e.ctx, B.eagle_norm(*base.values()), ws, st)
+    N(SHAPE, rows=0)
+    N(SHAPE, cols=60)
+    N(CAPACITY, cols=32776, ld_x=32776, ld_res=32776, ld_res_out=32776, ld_out=32776)
+    N(INVALID_ARG, eps=-1.0)
+    N(INVALID_ARG, eps=NAN)
+    N(INVALID_ARG, dtype=2)
+    N(INVALID_ARG, res_dtype=2)
+    N(INVALID_ARG, out_dtype=2)
+    N(INVALID_ARG, x=None)
+    N(INVALID_ARG, out=None)
+    N(ALIGN, x=a + 2)
+    N(ALIGN, ld_res=66)
+    N(SHAPE, ld_out=56)
+    N(INVALID_ARG, residual_out=a + 4096, ld_res_out=68)
+    N(INVALID_ARG, out=a, ld_out=72)
+    N(INVALID_ARG, out=a, out_dtype=1)
+    N(INVALID_ARG, out=a + 8192)
+    N(INVALID_ARG, out_mx=B.ref(X()))                    # both outputs
+    N(SHAPE, out=None, out_mx=B.ref(X(rows=5)))
+    N(SHAPE, out=None, out_mx=B.ref(X(cols=32)))
+
+    F = lambda each=1: B.eagle_filter(None, None, None, None, each, None)
+    S = lambda n=2, v=64, dtype=1, z=a, ld=64, f=None, u=a + 4096, token=a + 8192, arg=None, probs=None, lp=64: B.eagle_sample(
+        e.ctx, n, v, dtype, z, ld, f or F(), u, token, arg, probs, lp, ws, st)
+    for code, kw in [(SHAPE, dict(n=0)), (SHAPE, dict(v=0)), (CAPACITY, dict(v=262145, ld=262145)), (INVALID_ARG, dict(dtype=2)),
+                     (INVALID_ARG, dict(z=None)), (SHAPE, dict(ld=63)), (INVALID_ARG, dict(f=F(0))),
+                     (INVALID_ARG, dict(token=None)), (INVALID_ARG, dict(u=None)), (INVALID_ARG, dict(u=None, token=None)),
+                     (ALIGN, dict(z=a + 4)), (ALIGN, dict(probs=a + 4100)), (SHAPE, dict(probs=a + 16384, lp=63)),
+                     (INVALID_ARG, dict(probs=a)), (ALIGN, dict(f=B.eagle_filter(a + 4, None, None, None, 1, None)))]:
+        refused(code, lambda: S(**kw))
+    with pytest.raises(B.EagleError):
+        B.eagle_mx_layout(5, 4, 64)
+    assert B.eagle_mx_layout(1, 129, 160) == (129 * 160, 2 * 2 * 512) and B.eagle_mx_layout(3, 1, 32) == (16, 512)
+    assert B.eagle_launch_count(e.ctx) == before and e.status() == 0
+
+
+def test_wrappers_check_their_tensors():
+    e = engine()
+    t = mx("fp8", 4, 64)
+    for x in (torch.zeros(4, 32, device="cuda"), torch.zeros(4, 64), torch.zeros(4, 64, device="cuda", dtype=torch.float16),
+              torch.zeros(64, 4, device="cuda").t()):
+        with pytest.raises(ValueError):
+            t.quantize(x)
+    with pytest.raises(ValueError):
+        t.first(5)
+    with pytest.raises(ValueError):
+        R.MxTensor(e, 4, 64, "nv4", torch.zeros(2, device="cuda"))
+    x = torch.zeros(4, 64, device="cuda")
+    with pytest.raises(ValueError):
+        R.add_norm(e, x, torch.zeros_like(x), residual=x.bfloat16(), residual_out=x.clone())
+    with pytest.raises(ValueError):
+        R.mx_linear(t, t, torch.zeros(4, 4, device="cuda"), torch.zeros(5, device="cuda"))
+    with pytest.raises(ValueError):
+        R.Sampler(e, 4, temperature=torch.zeros(3, device="cuda"))
+    s = R.Sampler(e, 4)
+    with pytest.raises(ValueError):
+        s(torch.zeros(5, 64, device="cuda"), i32([0] * 5), i32([0] * 5))
+
+
+# ---- streams, graphs, runs ---------------------------------------------------------------
+
+def test_other_stream_and_second_engine():
+    """Two engines' calls on two streams at once."""
+    e2 = R.Engine(engine().dims, max_batch=64, max_rows=8, max_expanded=1, max_children=1, max_tree=2, max_prefix=1024,
+                  device="cuda")
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = []
+    x0, w0 = normal(1, 70, 2048), normal(2, 5000, 2048) * 0.1
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, e in ((a, engine()), (b, e2)):
+            with torch.cuda.stream(s):
+                x = R.MxTensor(e, 70, 2048, "fp4").quantize(x0)
+                w = R.MxTensor(e, 5000, 2048, "fp4").quantize(w0)
+                y = R.mx_linear(x, w, torch.empty(70, 5000, device="cuda"))
+                z = R.add_norm(e, y, torch.empty_like(y))
+                t = torch.empty(70, dtype=torch.int32, device="cuda")
+                R.Sampler(e, 70, top_p=torch.full((70,), 0.8, device="cuda"))(z, torch.arange(70, dtype=torch.int32, device="cuda") * 9999991, t)
+                outs.append((y, z, t))
+    torch.cuda.synchronize()
+    for o in outs[1:]:
+        assert all(torch.equal(p, q) for p, q in zip(o, outs[0]))
+    assert e2.status() == 0 and engine().status() == 0
+
+
+def test_weights_quantised_directly_before_their_product():
+    """A product launched behind the calls that write its operands reads what they wrote, again and again."""
+    x = mx("nv4", 3, 4096, 0.01)
+    w = mx("nv4", 2000, 4096, 0.01)
+    y = torch.empty(3, 2000, device="cuda")
+    xs = [normal(i, 3, 4096) for i in range(3)]
+    wsrc = [normal(10 + i, 2000, 4096) * 0.1 for i in range(3)]
+    wants = []
+    for i in range(3):
+        x.quantize(xs[i]); w.quantize(wsrc[i])
+        torch.cuda.synchronize()
+        wants.append(held(x) @ held(w).T)
+    for turn in range(12):
+        i = turn % 3
+        if turn % 2:
+            x.quantize(xs[i]); w.quantize(wsrc[i])
+        else:
+            w.quantize(wsrc[i]); x.quantize(xs[i])
+        R.mx_linear(x, w, y)
+        got = f64(y)
+        assert np.allclose(got, wants[i], atol=4096 * 2.0 ** -20), turn
+
+
+class Step:
+    """One decoder layer and an LM head of a small target over a paged cache: every call of a decoding step."""
+
+    def __init__(self, fmt, seqs, seed=0):
+        self.eng = e = engine()
+        self.fmt, self.seqs = fmt, seqs
+        self.d, self.ff, self.V = 512, 1152, 1000
+        Hq, Hkv, dh = 4, 2, 64
+        self.qkv_n = (Hq + 2 * Hkv) * dh
+        self.cache = R.PagedCache(e, seqs, 16, 40 * seqs, 20)
+        self.cache.clear()
+        self.rope = R.rope_for(e.dims)
+        g = {"nv4": 0.002}.get(fmt)
+        W = lambda n, k, s: mx(fmt, n, k, g).quantize(normal(seed + s, n, k) / math.sqrt(k))
+        self.wqkv, self.wo = W(self.qkv_n, self.d, 1), W(self.d, Hq * dh, 2)
+        self.wgu, self.wd, self.lm = W(2 * self.ff, self.d, 3), W(self.d, self.ff, 4), W(self.V, self.d, 5)
+        self.g1, self.g2, self.g3 = (1 + 0.2 * normal(seed + 6 + i, self.d) for i in range(3))
+        self.embed = normal(seed + 9, self.V, self.d)
+        self.a = 0.003 if fmt == "nv4" else None
+        self.sampler = R.Sampler(e, seqs, f32([0.8] * seqs), i32([50] * seqs), f32([0.9] * seqs))
+
+    def buffers(self, n):
+        e = lambda *s, dtype=F32: torch.empty(*s, dtype=dtype, device="cuda")
+        b = dict(h=e(n, self.d), a=mx(self.fmt, n, self.d, self.a), qkv=e(n, self.qkv_n, dtype=BF16), att=e(n, 4, 64, dtype=BF16),
+                 o=mx(self.fmt, n, 256, self.a), x=e(n, self.d, dtype=BF16), m=mx(self.fmt, n, self.d, self.a),
+                 gu=e(n, 2 * self.ff, dtype=BF16), s=mx(self.fmt, n, self.ff, self.a), y=e(n, self.d, dtype=BF16),
+                 f=mx(self.fmt, n, self.d, self.a), z=e(n, self.V), token=e(self.seqs, dtype=torch.int32), h2=e(n, self.d))
+        return b
+
+    def run(self, b, x, start, n_new, last, u):
+        """New rows x (fp32 embeddings) of every sequence; tokens from each one's last row."""
+        e, c, n = self.eng, self.cache, x.shape[0]
+        c.reserve(n_new)
+        R.add_norm(e, x, b["a"], self.g1)
+        R.mx_linear(b["a"], self.wqkv, b["qkv"])
+        q = b["qkv"].view(n, 8, 64)
+        c.append(0, start, self.rope, q[:, :4], q[:, 4:6], q[:, 6:])
+        c.attend(0, start, q[:, :4], b["att"])
+        c.advance()
+        b["o"].quantize(b["att"].view(n, 256))
+        R.mx_linear(b["o"], self.wo, b["x"])
+        R.add_norm(e, b["x"], b["m"], self.g2, residual=x, residual_out=b["h"])
+        R.mx_linear(b["m"], self.wgu, b["gu"])
+        b["s"].quantize(b["gu"], swiglu=True)
+        R.mx_linear(b["s"], self.wd, b["y"])
+        R.add_norm(e, b["y"], b["f"], self.g3, residual=b["h"], residual_out=b["h2"])
+        R.mx_linear(b["f"], self.lm, b["z"])
+        zl = b["z"].index_select(0, last) if n > self.seqs else b["z"]
+        self.sampler(zl, u, b["token"])
+        return b["token"]
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_target_step(fmt):
+    """A prompt and decoding steps, each call's output against the oracle on that call's own inputs."""
+    seqs = 3
+    st = Step(fmt, seqs)
+    lens = [7, 20, 1]
+    start = i32([0, 7, 27, 28])
+    last = torch.tensor([6, 26, 27], device="cuda")
+    u = i32([123456789, -99999999, 5])
+    x = normal(50, 28, st.d)
+    for turn in range(3):
+        n = x.shape[0]
+        b = st.buffers(n)
+        xs = f64(x)
+        token = st.run(b, x, start, i32(lens), last, u)
+        assert engine().status() == 0
+        is_quantized(b["a"], O.add_norm(xs, None, f64(st.g1), 1e-5)[1], REL)
+        def linear(xq, w, y, dtype):
+            a, c = held(xq), held(w)
+            want, size = a @ c.T, np.abs(a) @ np.abs(c).T
+            assert (np.abs(f64(y) - want) <= (w.cols + 8) * 2.0 ** -23 * size + U[dtype] * np.abs(want)).all()
+        linear(b["o"], st.wo, b["x"], BF16)
+        is_quantized(b["o"], f64(b["att"]).reshape(n, 256))
+        h, y = O.add_norm(f64(b["x"]), xs, f64(st.g2), 1e-5)
+        assert (np.abs(f64(b["h"]) - h) <= 2.0 ** -23 * np.abs(h)).all()
+        is_quantized(b["m"], y, REL)
+        linear(b["m"], st.wgu, b["gu"], BF16)
+        is_quantized(b["s"], O.swiglu(f64(b["gu"])), 2.0 ** -21)
+        linear(b["s"], st.wd, b["y"], BF16)
+        h2, y = O.add_norm(f64(b["y"]), f64(b["h"]), f64(st.g3), 1e-5)
+        is_quantized(b["f"], y, REL)
+        linear(b["f"], st.lm, b["z"], F32)
+        z = f64(b["z"])[last.cpu().numpy()] if n > seqs else f64(b["z"])
+        for i in range(seqs):
+            w = O.distribution(z[i], float(np.float32(0.8)), 50, float(np.float32(0.9)))
+            assert draw_one(w, int(u[i]) & 0xffffffff) == int(token[i])
+        # the next step: one token each
+        x = st.embed[token.long()]
+        lens, start, last = [1] * seqs, i32([0, 1, 2, 3]), torch.arange(3, device="cuda")
+    assert st.cache.len.tolist() == [9, 22, 3]
+
+
+def test_target_step_captured():
+    """The decoding step as a CUDA graph: replays on other inputs give what eager calls give; two graphs share the
+    workspace."""
+    seqs = 4
+    runs = []
+    for captured in (False, True):
+        st = Step("nv4", seqs)
+        b = st.buffers(seqs)
+        start, ones, last = i32(list(range(seqs + 1))), i32([1] * seqs), torch.arange(seqs, device="cuda")
+        u, x = i32([0] * seqs), torch.empty(seqs, st.d, device="cuda")
+        words = torch.randint(-(1 << 31), (1 << 31) - 1, (6, seqs), generator=gen(3), device="cuda", dtype=torch.int64).int()
+        x.copy_(st.embed[:seqs]); u.copy_(words[0])
+        st.run(b, x, start, ones, last, u)
+        st.cache.release(i32([0] * seqs))
+        st.cache.clear()
+        graphs = []
+        if captured:
+            for _ in range(2):
+                g = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(g):
+                    st.run(b, x, start, ones, last, u)
+                graphs.append(g)
+            st.cache.clear()
+        tokens = []
+        x.copy_(st.embed[:seqs])
+        for i in range(6):
+            u.copy_(words[i])
+            if captured:
+                graphs[i % 2].replay()
+            else:
+                st.run(b, x, start, ones, last, u)
+            tokens.append(b["token"].clone())
+            x.copy_(st.embed[b["token"].long()])
+        runs.append((torch.stack(tokens), b["z"].clone(), b["h2"].clone()))
+        assert engine().status() == 0
+    assert all(torch.equal(p, q) for p, q in zip(*runs))
