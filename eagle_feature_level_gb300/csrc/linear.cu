@@ -8,6 +8,9 @@
 // memory.  Warp roles: TMA producer, MMA issuer, four warps that read the accumulator out; two accumulators, so that
 // a tile is read out under the next one's products.
 //
+// Bound, many rows: an SM takes in 46 KB a stage of 192 rows at the 64 bytes a cycle that L2 gives it, 720 cycles for
+// products of 384.  Few rows: the weights' bytes from memory.
+//
 // Few tiles: a cluster of CTAs splits a tile's inner dimension; each writes its partial to its own shared memory and
 // sums its share of the rows over all of them, in rank order.
 #include <algorithm>
@@ -20,7 +23,7 @@
 namespace eagle {
 namespace {
 
-constexpr int LN_THREADS = 192;
+constexpr int LN_THREADS = 256;
 constexpr int LN_M = 128;                     // outputs of a tile
 constexpr int LN_KB = 128;                    // bytes of a row in a stage
 constexpr int LN_MAX_STAGES = 12;
@@ -55,12 +58,12 @@ struct LinearParams {
 
 struct LinearShared {
   uint64_t full[LN_MAX_STAGES], empty[LN_MAX_STAGES];
+  uint64_t sf_full[2];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t part_full, part_free;
-  uint64_t drained;
+  uint64_t drained[2];
   uint32_t tmem;
   int abort, never;
-  int issued;              // stages that the producer has asked for
 };
 
 template <int FMT>
@@ -77,35 +80,45 @@ __device__ __forceinline__ uint32_t idesc_of(int n, int sf) {
          (scale << 23) | (static_cast<uint32_t>(LN_M >> 4) << 24) | (static_cast<uint32_t>(sf) << 29);
 }
 
+// One product by the lane with `lead`, the operands given as the low words of their descriptors (the high word is
+// sm100::DESC_SW128_HI): a predicate instead of a branch, so that the operands can stay in uniform registers.
 template <int FMT>
-__device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
-                                           uint32_t sfb, uint32_t acc) {
-  if (FMT == EAGLE_MX_FP8)
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
-        : "memory");
-  else if (FMT == EAGLE_MX_FP4)
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
-        : "memory");
-  else
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
-        : "memory");
+__device__ __forceinline__ void mma_scaled(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t sfa,
+                                           uint32_t sfb, uint32_t acc, uint32_t lead) {
+#define EAGLE_MMA_SCALED(KIND)                                                                                         \
+  asm volatile(                                                                                                        \
+      "{\n .reg .pred p, q;\n .reg .b64 a, b;\n setp.ne.b32 p, %7, 0;\n setp.ne.b32 q, %8, 0;\n mov.b64 a, {%1, %6};\n" \
+      " mov.b64 b, {%2, %6};\n @q tcgen05.mma.cta_group::1." KIND " [%0], a, b, %3, [%4], [%5], p;\n}\n" ::"r"(d),     \
+      "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(sm100::DESC_SW128_HI), "r"(acc), "r"(lead)                     \
+      : "memory")
+  if (FMT == EAGLE_MX_FP8) EAGLE_MMA_SCALED("kind::mxf8f6f4.block_scale.scale_vec::1X");
+  else if (FMT == EAGLE_MX_FP4) EAGLE_MMA_SCALED("kind::mxf4nvf4.block_scale.scale_vec::2X");
+  else EAGLE_MMA_SCALED("kind::mxf4nvf4.block_scale.scale_vec::4X");
+#undef EAGLE_MMA_SCALED
+}
+__device__ __forceinline__ void commit_if(uint64_t* bar, uint32_t lead) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(sm100::smem_u32(bar)),
+      "r"(lead)
+      : "memory");
 }
 
-// 512 bytes of scales to four columns, repeated in each quarter of the lanes.
-__device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t saddr) {
-  // 32 rows of 16 bytes without swizzle: 8-row groups 128 bytes apart
-  const uint64_t desc = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128u >> 4) << 32) |
-                        (static_cast<uint64_t>(1u) << 46);
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+// 512 bytes of scales to four columns, repeated in each quarter of the lanes.  (32 rows of 16 bytes without swizzle, 8-row
+// groups 128 bytes apart.)
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t saddr, uint32_t lead) {
+  asm volatile(
+      "{\n .reg .pred q;\n .reg .b64 d;\n setp.ne.b32 q, %3, 0;\n mov.b64 d, {%1, %2};\n"
+      " @q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n}\n" ::"r"(tmem),
+      "r"((saddr >> 4) & 0x3FFFu), "r"((128u >> 4) | (1u << 14)), "r"(lead)
+      : "memory");
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(yes));
+  return yes != 0;
 }
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -161,95 +174,143 @@ __device__ __forceinline__ TileAt tile_at(const LinearParams& p, int tile) {
   return t;
 }
 
-template <int FMT>
-__device__ __forceinline__ void produce(const LinearParams& p, LinearShared& sh, uint8_t* ring, const CUtensorMap* wm,
-                                        const CUtensorMap* xm, int first, int step, int k0, int k1,
-                                        volatile int* abort) {
+// The loops below are gone through by whole warps and issue by predicate: what the instructions take then stays in uniform
+// registers (issued by a lane that had branched off, a product took 90 cycles and a copy of scales 67).  An instruction
+// of the tensor core still takes its warp some 60 cycles, so that the loads of either operand, the copies of scales and
+// the products each have a warp of their own (4096 x 8192 x 10240, NV_FP4: one branched-off lane for each of loads and
+// tensor core 310 us, whole warps 164, these 147).
+
+// Loads the weights (X false) or the rows (X true), and their scales, of this CTA's stages.
+template <int FMT, bool X>
+__device__ __forceinline__ void produce(const LinearParams& p, LinearShared& sh, uint8_t* ring, const CUtensorMap* map,
+                                        int first, int step, int k0, int k1, volatile int* abort) {
   constexpr int GPS = groups_per_stage<FMT>();
   const uint64_t policy = sm100::l2_policy_evict_first();
-  int slot = 0;
+  int slot = 0, issued = 0;
   uint32_t phase = 1;
   for (int tile = first; tile < p.tiles; tile += step) {
     const TileAt at = tile_at(p, tile);
-    const uint8_t* sa = p.w_scale + static_cast<size_t>(at.out0 >> 7) * p.groups * 512;
-    const uint8_t* sb = p.x_scale + static_cast<size_t>(at.rb0) * p.groups * 512;
+    const uint8_t* from = (X ? p.x_scale : p.w_scale) +
+                          (static_cast<size_t>(X ? at.rb0 : at.out0 >> 7) * p.groups + static_cast<size_t>(k0) * GPS) * 512;
+    const size_t next = static_cast<size_t>(p.groups) * 512;
+    int left = p.groups - k0 * GPS;              // groups of scales from here on
     for (int k = k0; k < k1; ++k) {
-      if (!sm100::mbar_wait(&sh.empty[slot], phase, abort)) {
+      if (!__all_sync(0xffffffffu, sm100::mbar_wait(&sh.empty[slot], phase, abort))) {
         *abort = 1;
-        return;
+        break;
       }
-      ++sh.issued;
+      ++issued;
       uint8_t* st = ring + static_cast<size_t>(slot) * p.stage_bytes;
       uint64_t* bar = &sh.full[slot];
-      const uint32_t sf = static_cast<uint32_t>(min(GPS, p.groups - k * GPS)) * 512u;
-      sm100::mbar_arrive_expect_tx(bar, LN_A_BYTES + p.b_bytes + sf * static_cast<uint32_t>(1 + at.n_rb));
-      if (p.once) sm100::tma_load_2d_hint(st, wm, k * LN_KB, at.out0, bar, policy);
-      else sm100::tma_load_2d(st, wm, k * LN_KB, at.out0, bar);
-      sm100::tma_load_2d(st + LN_A_BYTES, xm, k * LN_KB, at.row0, bar);
+      const uint32_t sf = static_cast<uint32_t>(min(GPS, left)) * 512u;
       uint8_t* s = st + LN_A_BYTES + p.b_bytes;
-      bulk_load(s, sa + static_cast<size_t>(k) * GPS * 512, sf, bar);
-      for (int b = 0; b < at.n_rb; ++b)
-        bulk_load(s + (1 + b) * GPS * 512, sb + (static_cast<size_t>(b) * p.groups + static_cast<size_t>(k) * GPS) * 512,
-                  sf, bar);
+      if (elect_one()) {
+        if (X) {
+          sm100::mbar_arrive_expect_tx(bar, p.b_bytes + sf * static_cast<uint32_t>(at.n_rb));
+          sm100::tma_load_2d(st + LN_A_BYTES, map, k * LN_KB, at.row0, bar);
+          bulk_load(s + GPS * 512, from, sf, bar);
+          if (at.n_rb > 1) bulk_load(s + 2 * GPS * 512, from + next, sf, bar);
+        } else {
+          sm100::mbar_arrive_expect_tx(bar, LN_A_BYTES + sf);
+          if (p.once) sm100::tma_load_2d_hint(st, map, k * LN_KB, at.out0, bar, policy);
+          else sm100::tma_load_2d(st, map, k * LN_KB, at.out0, bar);
+          bulk_load(s, from, sf, bar);
+        }
+      }
+      __syncwarp();
+      from += GPS * 512;
+      left -= GPS;
       if (++slot == p.stages) {
         slot = 0;
         phase ^= 1;
       }
     }
+    if (*abort) break;
   }
+  if (*abort)                                    // copies in flight land first (where the other producer asked for its part too)
+    for (int i = max(0, issued - p.stages); i < issued; ++i)
+      sm100::mbar_wait(&sh.full[i % p.stages], (i / p.stages) & 1, &sh.never);
 }
 
-template <int FMT>
-__device__ __forceinline__ void multiply(const LinearParams& p, LinearShared& sh, uint8_t* ring, uint32_t tmem,
-                                         int first, int step, int k0, int k1, volatile int* abort) {
+// Scales to tensor memory, a stage ahead of the products: two places in turn, the products of the stage before last being
+// through with the one that is written.  RB: 128-row blocks of x's scales in a tile.
+template <int FMT, int RB>
+__device__ __forceinline__ void spread_scales(const LinearParams& p, LinearShared& sh, uint8_t* ring, uint32_t tmem,
+                                              int first, int step, int k0, int k1, volatile int* abort) {
   constexpr int GPS = groups_per_stage<FMT>();
-  int slot = 0, n = 0, sf_slot = 0;
-  uint32_t phase = 0;
-  for (int tile = first; tile < p.tiles; tile += step, ++n) {
-    const int buf = n & 1;
-    const uint32_t b_off = static_cast<uint32_t>((tile % p.row_tiles) * p.nt & 127) >> 5;
-    if (!sm100::mbar_wait(&sh.acc_empty[buf], ((n >> 1) & 1) ^ 1, abort)) {
+  const uint32_t ring0 = sm100::smem_u32(ring) + LN_A_BYTES + p.b_bytes;
+  const uint32_t lead = elect_one();
+  int slot = 0, old = p.stages - 2;
+  uint32_t phase = 0, old_phase = 1;
+  const int total = first < p.tiles ? ((p.tiles - first + step - 1) / step) * (k1 - k0) : 0;
+  for (int i = 0; i < total; ++i) {
+    bool ok = sm100::mbar_wait(&sh.full[slot], phase, abort);
+    ok = ok && (i < 2 || sm100::mbar_wait(&sh.empty[old], old_phase, abort));
+    if (!__all_sync(0xffffffffu, ok)) {
       *abort = 1;
       return;
     }
     sm100::tc_fence_after();
+    const uint32_t s = ring0 + static_cast<uint32_t>(slot) * p.stage_bytes;
+    const uint32_t sfa = tmem + p.sf_at + (i & 1) * p.sf_cols, sfb = sfa + 4 * GPS;
+#pragma unroll
+    for (int g = 0; g < GPS; ++g) {
+      copy_scales(sfa + 4 * g, s + 512 * g, lead);
+#pragma unroll
+      for (int b = 0; b < RB; ++b) copy_scales(sfb + 4 * (g * RB + b), s + 512 * ((1 + b) * GPS + g), lead);
+    }
+    commit_if(&sh.sf_full[i & 1], lead);
+    sm100::mbar_arrive_if(&sh.sf_full[i & 1], lead);   // (and that the stage itself is there)
+    if (++slot == p.stages) {
+      slot = 0;
+      phase ^= 1;
+    }
+    if (++old == p.stages) {
+      old = 0;
+      old_phase ^= 1;
+    }
+  }
+}
+
+template <int FMT, int RB>
+__device__ __forceinline__ void multiply(const LinearParams& p, LinearShared& sh, uint8_t* ring, uint32_t tmem,
+                                         int first, int step, int k0, int k1, volatile int* abort) {
+  constexpr int GPS = groups_per_stage<FMT>();
+  const uint32_t ring0 = sm100::smem_u32(ring);
+  const uint32_t lead = elect_one();
+  int slot = 0, n = 0, i = 0;
+  for (int tile = first; tile < p.tiles; tile += step, ++n) {
+    const int buf = n & 1;
+    const uint32_t b_off = static_cast<uint32_t>((tile % p.row_tiles) * p.nt & 127) >> 5;
+    if (!__all_sync(0xffffffffu, sm100::mbar_wait(&sh.acc_empty[buf], ((n >> 1) & 1) ^ 1, abort))) {
+      *abort = 1;
+      return;
+    }
     const uint32_t d = tmem + static_cast<uint32_t>(buf) * p.acc_cols;
     uint32_t acc = 0;
-    for (int k = k0; k < k1; ++k) {
-      if (!sm100::mbar_wait(&sh.full[slot], phase, abort)) {
+    for (int k = k0; k < k1; ++k, ++i) {
+      if (!__all_sync(0xffffffffu, sm100::mbar_wait(&sh.sf_full[i & 1], (i >> 1) & 1, abort))) {
         *abort = 1;
         return;
       }
       sm100::tc_fence_after();
-      const uint32_t st = sm100::smem_u32(ring + static_cast<size_t>(slot) * p.stage_bytes);
-      const uint32_t s = st + LN_A_BYTES + p.b_bytes;
-      const uint32_t sfa = tmem + p.sf_at + static_cast<uint32_t>(sf_slot) * p.sf_cols;
-      const uint32_t sfb = sfa + 4 * GPS;
-#pragma unroll
-      for (int g = 0; g < GPS; ++g) copy_scales(sfa + 4 * g, s + 512 * g);
-      for (int b = 0; b < p.rb; ++b)
-#pragma unroll
-        for (int g = 0; g < GPS; ++g)
-          copy_scales(sfb + 4 * (g * p.rb + b), s + 512 * ((1 + b) * GPS + g));
-      const uint64_t ad = sm100::smem_desc_sw128(st), bd = sm100::smem_desc_sw128(st + LN_A_BYTES);
-      const int left = p.kbytes - k * LN_KB;           // bytes: 32 an MMA
+      const uint32_t st = ring0 + static_cast<uint32_t>(slot) * p.stage_bytes;
+      const uint32_t sfa = tmem + p.sf_at + (i & 1) * p.sf_cols, sfb = sfa + 4 * GPS + b_off;
+      const uint32_t ad = st >> 4, bd = (st + LN_A_BYTES) >> 4;
+      const int left = p.kbytes - k * LN_KB;           // bytes: 32 a product
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if (j > 0 && 32 * j >= left) break;
         const int g = FMT == EAGLE_MX_FP8 ? 0 : FMT == EAGLE_MX_FP4 ? j / 2 : j;
         const int sf = FMT == EAGLE_MX_FP8 ? j : FMT == EAGLE_MX_FP4 ? 2 * (j & 1) : 0;
-        mma_scaled<FMT>(d, ad + 2 * j, bd + 2 * j, idesc_of<FMT>(p.nt, sf), sfa + 4 * g,
-                        sfb + 4 * g * p.rb + b_off, acc);
-        acc = 1;
+        if (j == 0 || 32 * j < left)
+          mma_scaled<FMT>(d, ad + 2 * j, bd + 2 * j, idesc_of<FMT>(p.nt, sf), sfa + 4 * g, sfb + 4 * g * RB,
+                          j == 0 ? acc : 1u, lead);
       }
-      sm100::mma_commit(&sh.empty[slot]);
-      sf_slot ^= 1;
-      if (++slot == p.stages) {
-        slot = 0;
-        phase ^= 1;
-      }
+      commit_if(&sh.empty[slot], lead);
+      if (k + 1 == k1) commit_if(&sh.acc_full[buf], lead);
+      acc = 1;
+      if (++slot == p.stages) slot = 0;
     }
-    sm100::mma_commit(&sh.acc_full[buf]);
   }
 }
 
@@ -342,18 +403,20 @@ __global__ void __launch_bounds__(LN_THREADS, 1)
     sm100::tma_prefetch_desc(&wm);
     sm100::tma_prefetch_desc(&xm);
     for (int i = 0; i < p.stages; ++i) {
-      sm100::mbar_init(&sh.full[i], 1);
+      sm100::mbar_init(&sh.full[i], 2);
       sm100::mbar_init(&sh.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
+      sm100::mbar_init(&sh.sf_full[i], 2);
       sm100::mbar_init(&sh.acc_full[i], 1);
       sm100::mbar_init(&sh.acc_empty[i], 4);
     }
     sm100::mbar_init(&sh.part_full, 4 * p.split);
     sm100::mbar_init(&sh.part_free, 4 * p.split);
-    sm100::mbar_init(&sh.drained, 1);
+    sm100::mbar_init(&sh.drained[0], 1);
+    sm100::mbar_init(&sh.drained[1], 1);
     sm100::fence_barrier_init();
-    sh.abort = sh.never = sh.issued = 0;
+    sh.abort = sh.never = 0;
     // the first ring's weights on their way to L2 (not into shared memory: what precedes may still write them)
     const TileAt at = tile_at(p, min(first, p.tiles - 1));
     for (int k = k0; k < min(k1, k0 + p.stages); ++k) prefetch_2d(&wm, k * LN_KB, at.out0);
@@ -371,19 +434,22 @@ __global__ void __launch_bounds__(LN_THREADS, 1)
   ls.waited();
   pdl_trigger();
   if (warp == 0) {
-    if (lane == 0) {
-      produce<FMT>(p, sh, ring, &wm, &xm, first, step, k0, k1, abort);
-      if (*abort)                                // copies in flight land first
-        for (int i = max(0, sh.issued - p.stages); i < sh.issued; ++i)
-          sm100::mbar_wait(&sh.full[i % p.stages], (i / p.stages) & 1, &sh.never);
+    produce<FMT, false>(p, sh, ring, &wm, first, step, k0, k1, abort);
+  } else if (warp == 3) {
+    produce<FMT, true>(p, sh, ring, &xm, first, step, k0, k1, abort);
+  } else if (warp == 1 || warp == 2) {
+    if (warp == 1) {
+      if (p.rb == 1) multiply<FMT, 1>(p, sh, ring, tmem, first, step, k0, k1, abort);
+      else multiply<FMT, 2>(p, sh, ring, tmem, first, step, k0, k1, abort);
+    } else {
+      if (p.rb == 1) spread_scales<FMT, 1>(p, sh, ring, tmem, first, step, k0, k1, abort);
+      else spread_scales<FMT, 2>(p, sh, ring, tmem, first, step, k0, k1, abort);
     }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      multiply<FMT>(p, sh, ring, tmem, first, step, k0, k1, abort);
-      if (*abort) {                              // and products in flight end
-        sm100::mma_commit(&sh.drained);
-        sm100::mbar_wait(&sh.drained, 0, &sh.never);
-      }
+    __syncwarp();
+    if (*abort) {                                // what is in flight on the tensor core ends
+      if (elect_one()) sm100::mma_commit(&sh.drained[warp - 1]);
+      __syncwarp();
+      sm100::mbar_wait(&sh.drained[warp - 1], 0, &sh.never);
     }
   } else {
     read_out(p, sh, part, tmem, first, step, rank, abort);
