@@ -59,37 +59,66 @@ __device__ __forceinline__ uint32_t mx_pack_e4m3(float a, float b, float c, floa
   return w;
 }
 
+__device__ __forceinline__ float mx_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The tensor's factor as quantisations take it: 6 g and its inverse.
+struct MxFactor {
+  float g, g6, r6;
+};
+__device__ __forceinline__ MxFactor mx_factor(const MxView& m) {
+  MxFactor f;
+  f.g = m.g ? *m.g : 1.0f;
+  f.g6 = 6.0f * f.g;
+  f.r6 = 1.0f / f.g6;
+  return f;
+}
+
+// The fp32 quotient x / d, given r = 1 / d to a step or two: one Newton step on x r (Markstein 1990: the remainder x - q d is
+// exact in one fused operation), so that a quotient that fp32 has, a tie among them, is met exactly.
+__device__ __forceinline__ float mx_quotient(float x, float d, float r) {
+  const float q = x * r;
+  return fmaf(fmaf(-q, d, x), r, q);
+}
+
 // Eight consecutive values of row `row` from column `col` (a multiple of 8) on, held by each lane of a warp for
 // consecutive columns from a multiple of 256 on: elements, and the scales of their blocks.  Lanes past the last column
-// (`in` false) hold zeros.  A block's largest magnitude is the largest of its lanes' bit patterns (a NaN's is above
-// all).  Scales of powers of two are exact, and so is the product with their inverse; for NV_FP4 the fp32 quotient x / d
-// is one Newton step on x (1 / d) (Markstein 1990: the remainder x - q d is exact in one fused operation), so that
-// quotients that meet a tie exactly stay on it.  Returns whether the block has a NaN or an infinity.
+// (`in` false) hold zeros.  Returns whether the block has a NaN or an infinity.
 template <int FMT>
-__device__ __forceinline__ bool mx_put(const MxView& m, float g, int row, int col, bool in, const float (&x)[8],
+__device__ __forceinline__ bool mx_put(const MxView& m, const MxFactor& f, int row, int col, bool in, const float (&x)[8],
                                        int lane) {
-  uint32_t top = 0;
+  float most = fabsf(x[0]);                      // NaN if any is
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  if (FMT != EAGLE_NV_FP4) top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  for (int i = 1; i < 8; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(most) : "f"(fabsf(x[i])));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(most) : "f"(__shfl_xor_sync(0xffffffffu, most, 1)));
+  if (FMT != EAGLE_NV_FP4) asm("max.NaN.f32 %0, %0, %1;" : "+f"(most) : "f"(__shfl_xor_sync(0xffffffffu, most, 2)));
+  const uint32_t top = __float_as_uint(most);
   const bool bad = top >= 0x7f800000u;
   uint32_t byte;
   float v[8];
   if (FMT == EAGLE_NV_FP4) {
+    // (a quotient beyond the type's range saturates: it is held where its remainder stays finite)
+    const float q = fminf(most * f.r6, 1e6f);
+    const float t = f.r6 < INFINITY ? fmaf(fmaf(-q, f.g6, most), f.r6, q) : most / f.g6;
     byte = bad ? 0x7fu
            : top == 0u ? 0u
-               : static_cast<uint32_t>(__nv_cvt_float_to_fp8(__uint_as_float(top) / (6.0f * g), __NV_SATFINITE, __NV_E4M3));
-    const float d = mx_decode_e4m3(byte) * g;
-    const float r = d >= 0x1p-126f ? 1.0f / d : 0.0f;
+                       : static_cast<uint32_t>(__nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3));
+    const float d = mx_decode_e4m3(byte) * f.g;
+    const float r = d >= 0x1p-126f ? mx_rcp(d) : 0.0f;
+    if (__any_sync(0xffffffffu, most * r > 1e30f)) {   // elements far beyond 6, whose remainder may not be finite
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float q = x[i] * r;
-      // (beyond 6 it saturates, and inf has no remainder; a zero keeps its sign)
-      v[i] = copysignf(fabsf(q) < 16.0f ? fmaf(fmaf(-q, d, x[i]), r, q) : q, x[i]);
+      for (int i = 0; i < 8; ++i) v[i] = fabsf(x[i] * r) < 16.0f ? mx_quotient(x[i], d, r) : x[i] * r;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = mx_quotient(x[i], d, r);
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = copysignf(v[i], x[i]);   // (a zero keeps its sign)
   } else {
-    // the largest element is 1.75 * 2^8 (e4m3) or 1.5 * 2^2 (e2m1)
+    // the largest element is 1.75 * 2^8 (e4m3) or 1.5 * 2^2 (e2m1); a power of two and its inverse are exact
     const uint32_t lead = FMT == EAGLE_MX_FP8 ? 0x600000u : 0x400000u;
     const int whole = FMT == EAGLE_MX_FP8 ? 8 : 2;
     const int e = static_cast<int>(top >> 23) - whole + ((top & 0x7fffffu) > lead ? 1 : 0);
@@ -115,26 +144,36 @@ __device__ __forceinline__ bool mx_put(const MxView& m, float g, int row, int co
   return bad && in;
 }
 
-// The values of eight elements from `col` on.
+// Eight elements of a row from `col` on and their scale as they lie in memory, and their values.
 template <int FMT>
-__device__ __forceinline__ void mx_get(const MxView& m, float g, int row, int col, float (&v)[8]) {
-  const int block = col / mx_block<FMT>();
-  const uint32_t byte = m.scale[mx_scale_at(m, row, block >> 2) + (block & 3)];
+struct MxRaw {
+  uint2 w;                 // (4 bits: the first word)
+  uint32_t byte;
+  __device__ __forceinline__ void load(const MxView& m, int row, int col) {
+    const int block = col / mx_block<FMT>();
+    byte = m.scale[mx_scale_at(m, row, block >> 2) + (block & 3)];
+    const size_t at = static_cast<size_t>(row) * m.cols + col;
+    if (FMT == EAGLE_MX_FP8) w = *reinterpret_cast<const uint2*>(m.data + at);
+    else w.x = *reinterpret_cast<const uint32_t*>(m.data + at / 2);
+  }
+};
+template <int FMT>
+__device__ __forceinline__ void mx_get(const MxRaw<FMT>& raw, float g, float (&v)[8]) {
+  const uint32_t byte = raw.byte;
   float d;
   if (FMT == EAGLE_NV_FP4) d = mx_decode_e4m3(byte) * g;
   else d = __uint_as_float(byte == 255u ? 0x7fffffffu : byte == 0u ? 1u << 22 : byte << 23);
   if (FMT == EAGLE_MX_FP8) {
-    const uint2 w = *reinterpret_cast<const uint2*>(m.data + static_cast<size_t>(row) * m.cols + col);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t two = ((i < 2 ? w.x : w.y) >> (16 * (i & 1))) & 0xffffu;
+      const uint32_t two = ((i < 2 ? raw.w.x : raw.w.y) >> (16 * (i & 1))) & 0xffffu;
       const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
       const float2 f = __half22float2(__half2(h));
       v[2 * i] = f.x * d;
       v[2 * i + 1] = f.y * d;
     }
   } else {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(m.data + (static_cast<size_t>(row) * m.cols + col) / 2);
+    const uint32_t w = raw.w.x;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       // sign, two bits of exponent (bias 1) and one of fraction, as a float 2^126 times too small
@@ -145,21 +184,41 @@ __device__ __forceinline__ void mx_get(const MxView& m, float g, int row, int co
   }
 }
 
-// Eight elements of a row, from bf16 or fp32 and to them.
-__device__ __forceinline__ void load8(const uint16_t* p, float (&x)[8]) {
-  const uint4 w = *reinterpret_cast<const uint4*>(p);
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+// Eight elements of a row as they lie in memory, and their values.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<uint16_t> {
+  uint4 w;
+  __device__ __forceinline__ void load(const uint16_t* p) { w = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16);
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(u[i] << 16);
+      x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
   }
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(p + 4);
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+};
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
+  Raw8<T> r;
+  r.load(p);
+  r.get(x);
 }
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
+
 __device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8]) {
   uint32_t u[4];
 #pragma unroll

@@ -1,7 +1,8 @@
 // eagle_add_norm: h = x + residual, out = h / sqrt(mean(h^2) + eps) * gain, out in bf16, fp32 or a microscaled format.
 //
 // One pass: a row's h stays in the registers of its threads (eight consecutive elements a unit, up to four units a
-// thread), its squares are summed over the warps, then the same registers are scaled, rounded and stored.
+// thread, two as a rule), its squares are summed over the warps, then the same registers are scaled, rounded and stored.
+// A block goes on with other rows, the next one's loads under the present one's work and the gains kept.
 #include "internal.h"
 #include "common.cuh"
 #include "mx.cuh"
@@ -24,75 +25,98 @@ struct NormParams {
   uint64_t* stamp;
 };
 
-constexpr int NM_UNITS = 4;
-
 // OUT: 0 bf16, -1 fp32, otherwise a microscaled format.
-template <typename T, typename R, int OUT, int UNITS>
-__global__ void __launch_bounds__(1024) norm_kernel(NormParams p) {
-  __shared__ float s_sum[32];
+template <typename T, typename R, int OUT, int UNITS, int MOST>
+__global__ void __launch_bounds__(MOST, MOST == 512 ? 2 : 1) norm_kernel(NormParams p) {
+  __shared__ float s_sum[2][32];
   LaunchStamp ls(p.stamp);
   pdl_wait();
   ls.waited();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = threadIdx.x & (p.threads - 1);
-  const int row = blockIdx.x * (blockDim.x / p.threads) + threadIdx.x / p.threads;
-  const bool there = row < p.rows;
-  float h[UNITS][8];
-  float sum = 0.0f;
+  const int per_block = blockDim.x / p.threads, step = gridDim.x * per_block;
+  int row = blockIdx.x * per_block + threadIdx.x / p.threads;
+  const int rounds = (p.rows + step - 1) / step;           // the same for a block's threads
+  const MxFactor f = OUT > 0 ? mx_factor(p.m) : MxFactor{1.0f, 1.0f, 1.0f};
+  int col[UNITS];
+  bool own[UNITS];
+  float gain[UNITS][8];
+  Raw8<T> x[UNITS];
+  Raw8<R> res[UNITS];
 #pragma unroll
   for (int u = 0; u < UNITS; ++u) {
-    const int col = (u * p.threads + t) * 8;
+    col[u] = (u * p.threads + t) * 8;
+    own[u] = col[u] < p.cols;
+    if (own[u] && row < p.rows) {
+      x[u].load(static_cast<const T*>(p.x) + row * p.ld_x + col[u]);
+      if (p.res) res[u].load(static_cast<const R*>(p.res) + row * p.ld_res + col[u]);
+    }
+  }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[u][i] = 0.0f;
-    if (there && col < p.cols) {
-      load8(static_cast<const T*>(p.x) + row * p.ld_x + col, h[u]);
-      if (p.res) {
-        float r[8];
-        load8(static_cast<const R*>(p.res) + row * p.ld_res + col, r);
+  for (int u = 0; u < UNITS; ++u) {
+    if (p.gain && own[u]) load8(p.gain + col[u], gain[u]);
+    else
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[u][i] += r[i];
+      for (int i = 0; i < 8; ++i) gain[u][i] = 1.0f;
+  }
+  bool bad = false;
+  for (int k = 0; k < rounds; ++k, row += step) {
+    const bool there = row < p.rows;
+    float h[UNITS][8];
+    float sum = 0.0f;
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) {
+      if (there && own[u]) {
+        x[u].get(h[u]);
+        if (p.res) {
+          float r[8];
+          res[u].get(r);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) h[u][i] += r[i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[u][i] = 0.0f;
       }
     }
-  }
+    // the next row is on its way under this one's work
 #pragma unroll
-  for (int u = 0; u < UNITS; ++u) {
-    const int col = (u * p.threads + t) * 8;
-    if (p.res_out && there && col < p.cols) store8(static_cast<R*>(p.res_out) + row * p.ld_ro + col, h[u]);
+    for (int u = 0; u < UNITS; ++u)
+      if (own[u] && row + step < p.rows) {
+        x[u].load(static_cast<const T*>(p.x) + (row + step) * p.ld_x + col[u]);
+        if (p.res) res[u].load(static_cast<const R*>(p.res) + (row + step) * p.ld_res + col[u]);
+      }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum = fmaf(h[u][i], h[u][i], sum);
-  }
-  sum = warp_sum(sum);
-  if (p.threads > 32) {
-    if (lane == 0) s_sum[warp] = sum;
-    __syncthreads();
-    const int nw = p.threads >> 5, w0 = warp & ~(nw - 1);
-    sum = warp_sum(lane < nw ? s_sum[w0 + lane] : 0.0f);
-  }
-  const float inv = 1.0f / sqrtf(sum / static_cast<float>(p.cols) + p.eps);
-  const float g = p.m.g ? *p.m.g : 1.0f;
-  bool bad = false;
+    for (int u = 0; u < UNITS; ++u) {
+      if (p.res_out && there && own[u]) store8(static_cast<R*>(p.res_out) + row * p.ld_ro + col[u], h[u]);
 #pragma unroll
-  for (int u = 0; u < UNITS; ++u) {
-    const int col = (u * p.threads + t) * 8;
-    const bool in = there && col < p.cols;
-    float y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = h[u][i] * inv;
-    if (p.gain && col < p.cols) {
-      float gain[8];
-      load8(p.gain + col, gain);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] *= gain[i];
+      for (int i = 0; i < 8; ++i) sum = fmaf(h[u][i], h[u][i], sum);
     }
-    if (OUT > 0) {
-      if (!in)
+    sum = warp_sum(sum);
+    if (p.threads > 32) {
+      float* s = s_sum[k & 1];                   // (in turn: the last row's sums may still be read)
+      if (lane == 0) s[warp] = sum;
+      __syncthreads();
+      const int nw = p.threads >> 5, w0 = warp & ~(nw - 1);
+      sum = warp_sum(lane < nw ? s[w0 + lane] : 0.0f);
+    }
+    const float inv = 1.0f / sqrtf(sum / static_cast<float>(p.cols) + p.eps);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = 0.0f;
-      bad |= mx_put<OUT>(p.m, g, row, col, in, y, lane);
-    } else if (in) {
-      if (OUT == 0) store8(static_cast<uint16_t*>(p.out) + row * p.ld_out + col, y);
-      else store8(static_cast<float*>(p.out) + row * p.ld_out + col, y);
+    for (int u = 0; u < UNITS; ++u) {
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = h[u][i] * inv * gain[u][i];
+      const bool in = there && own[u];
+      if (OUT > 0) {
+        if (!in)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = 0.0f;
+        bad |= mx_put<OUT>(p.m, f, row, col[u], in, y, lane);
+      } else if (in) {
+        if (OUT == 0) store8(static_cast<uint16_t*>(p.out) + row * p.ld_out + col[u], y);
+        else store8(static_cast<float*>(p.out) + row * p.ld_out + col[u], y);
+      }
     }
   }
   if (bad) set_status(p.status, EAGLE_ERR_NUMERIC);
@@ -100,17 +124,19 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p) {
 
 typedef void (*NormKernel)(NormParams);
 
+// Rows of up to 8192 columns: 512 threads at most, and registers for them.
 template <typename T, typename R, int OUT>
-NormKernel kernel_of(int units) {
-  return units == 1 ? norm_kernel<T, R, OUT, 1> : units == 2 ? norm_kernel<T, R, OUT, 2> : norm_kernel<T, R, OUT, 4>;
+NormKernel kernel_of(int units, int threads) {
+  if (threads <= 512) return units == 1 ? norm_kernel<T, R, OUT, 1, 512> : norm_kernel<T, R, OUT, 2, 512>;
+  return units <= 2 ? norm_kernel<T, R, OUT, 2, 1024> : norm_kernel<T, R, OUT, 4, 1024>;
 }
 template <typename T, typename R>
-NormKernel kernel_of(const eagle_norm* n, int units) {
-  if (!n->out_mx) return n->out_dtype == EAGLE_DTYPE_F32 ? kernel_of<T, R, -1>(units) : kernel_of<T, R, 0>(units);
+NormKernel kernel_of(const eagle_norm* n, int units, int threads) {
+  if (!n->out_mx) return n->out_dtype == EAGLE_DTYPE_F32 ? kernel_of<T, R, -1>(units, threads) : kernel_of<T, R, 0>(units, threads);
   switch (n->out_mx->format) {
-    case EAGLE_MX_FP8: return kernel_of<T, R, EAGLE_MX_FP8>(units);
-    case EAGLE_MX_FP4: return kernel_of<T, R, EAGLE_MX_FP4>(units);
-    default: return kernel_of<T, R, EAGLE_NV_FP4>(units);
+    case EAGLE_MX_FP8: return kernel_of<T, R, EAGLE_MX_FP8>(units, threads);
+    case EAGLE_MX_FP4: return kernel_of<T, R, EAGLE_MX_FP4>(units, threads);
+    default: return kernel_of<T, R, EAGLE_NV_FP4>(units, threads);
   }
 }
 
@@ -134,16 +160,20 @@ cudaError_t launch_norm(eagle_ctx* ctx, const eagle_norm* n, int* status, cudaSt
   p.status = status;
   const int eights = ceil_div(n->cols, 8);
   p.threads = 32;
-  while (p.threads < 1024 && p.threads * NM_UNITS < eights) p.threads <<= 1;
+  while (p.threads < 1024 && p.threads * 2 < eights) p.threads <<= 1;
   const int need = ceil_div(eights, p.threads);
   const int units = need <= 1 ? 1 : need <= 2 ? 2 : 4;
   const int block = p.threads < 256 ? 256 : p.threads;
   const bool f = n->dtype == EAGLE_DTYPE_F32, rf = n->res_dtype == EAGLE_DTYPE_F32;
-  const NormKernel k = f ? (rf ? kernel_of<float, float>(n, units) : kernel_of<float, uint16_t>(n, units))
-                         : (rf ? kernel_of<uint16_t, float>(n, units) : kernel_of<uint16_t, uint16_t>(n, units));
+  const NormKernel k = f ? (rf ? kernel_of<float, float>(n, units, p.threads) : kernel_of<float, uint16_t>(n, units, p.threads))
+                         : (rf ? kernel_of<uint16_t, float>(n, units, p.threads) : kernel_of<uint16_t, uint16_t>(n, units, p.threads));
   p.stamp = stamp_slot(ctx, EAGLE_K_NORM);
+  // as many blocks as fit the GPU at once, each on with the next rows
+  int per_sm = 1;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, block, 0) != cudaSuccess || per_sm < 1) per_sm = 1;
+  const int blocks = ceil_div(n->rows, block / p.threads), most = per_sm * ctx->sm_count;
   trace_before(ctx, EAGLE_K_NORM, st);
-  const cudaError_t e = launch_pdl(k, dim3(ceil_div(n->rows, block / p.threads)), dim3(block), 0, st, p);
+  const cudaError_t e = launch_pdl(k, dim3(blocks < most ? blocks : most), dim3(block), 0, st, p);
   ctx->launches++;
   trace_after(ctx, EAGLE_K_NORM, st);
   return e;

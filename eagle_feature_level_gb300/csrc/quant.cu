@@ -1,7 +1,9 @@
 // eagle_mx_quantize and eagle_mx_unpack: rows to and from the microscaled formats.
 //
-// A warp takes 256 columns of a row, a lane eight of them: 16 or 32 bytes in, 4 or 8 out, with a block's maximum and
-// the four scales of a group exchanged between its lanes.
+// A warp takes 256 columns and goes down the rows, two in flight; a lane has eight columns: 16 or 32 bytes in, 4 or 8 out,
+// with a block's maximum and the four scales of a group exchanged between its lanes.
+//
+// Bound: memory, and with four bits nearly as much the instructions of an element (NV_FP4: its quotient, 4, and rounding).
 #include "internal.h"
 #include "common.cuh"
 #include "mx.cuh"
@@ -12,18 +14,32 @@ namespace {
 constexpr int QT_THREADS = 256;
 constexpr int QT_WARPS = QT_THREADS / 32;
 
+constexpr int QT_ROWS = 2;              // rows of a warp in flight
+
 struct QuantParams {
   MxView m;
   const void* x;           // quantise: rows in; unpack: rows out
   long long ld;
   int chunks;              // of 256 columns a row
-  long long tasks;         // rows x chunks
+  int step;                // warps of a chunk
   int* status;
   uint64_t* stamp;
 };
 
+// e^(-a) to two steps of fp32: 2^y of y = -a log2(e), the low part of that product put right behind it.
+__device__ __forceinline__ float exp_minus(float a) {
+  constexpr float L = 0x1.715476p+0f, L_LOW = 0x1.4ae0cp-26f, LN2 = 0x1.62e43p-1f;
+  const float y = -a * L;
+  const float low = fmaf(-a, L, -y) - a * L_LOW;
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(y));
+  return fabsf(y) < 126.0f ? fmaf(e, low * LN2, e) : e;
+}
 // SiLU(a) b in fp32.
-__device__ __forceinline__ float gated(float a, float b) { return a / (1.0f + expf(-a)) * b; }
+__device__ __forceinline__ float gated(float a, float b) {
+  const float d = 1.0f + exp_minus(a);
+  return d < 0x1p126f ? mx_quotient(a, d, mx_rcp(d)) * b : a / d * b;
+}
 
 template <int FMT, typename T, bool SWIGLU>
 __global__ void __launch_bounds__(QT_THREADS) quantize_kernel(QuantParams p) {
@@ -31,25 +47,39 @@ __global__ void __launch_bounds__(QT_THREADS) quantize_kernel(QuantParams p) {
   pdl_wait();
   ls.waited();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const float g = p.m.g ? *p.m.g : 1.0f;
+  const int lane = threadIdx.x & 31, warp = blockIdx.x * QT_WARPS + (threadIdx.x >> 5);
+  const MxFactor f = mx_factor(p.m);
+  const int col = warp % p.chunks * 256 + lane * 8;
+  const bool in = col < p.m.cols;
   bool bad = false;
-  for (long long t = static_cast<long long>(blockIdx.x) * QT_WARPS + (threadIdx.x >> 5); t < p.tasks;
-       t += static_cast<long long>(gridDim.x) * QT_WARPS) {
-    const int row = static_cast<int>(t / p.chunks), col = static_cast<int>(t % p.chunks) * 256 + lane * 8;
-    const bool in = col < p.m.cols;
-    float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (in) {
-      const T* from = static_cast<const T*>(p.x) + row * p.ld + col;
-      load8(from, x);
-      if (SWIGLU) {
-        float y[8];
-        load8(from + p.m.cols, y);
+  for (int r0 = warp / p.chunks; r0 < p.m.rows && warp < p.step * p.chunks; r0 += QT_ROWS * p.step) {
+    Raw8<T> a[QT_ROWS], b[QT_ROWS];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = gated(x[i], y[i]);
+    for (int i = 0; i < QT_ROWS; ++i) {
+      const int row = r0 + i * p.step;
+      if (in && row < p.m.rows) {
+        const T* from = static_cast<const T*>(p.x) + row * p.ld + col;
+        a[i].load(from);
+        if (SWIGLU) b[i].load(from + p.m.cols);
       }
     }
-    bad |= mx_put<FMT>(p.m, g, row, col, in, x, lane);
+#pragma unroll
+    for (int i = 0; i < QT_ROWS; ++i) {
+      const int row = r0 + i * p.step;
+      if (row >= p.m.rows) break;
+      float x[8];
+      a[i].get(x);
+      if (SWIGLU) {
+        float y[8];
+        b[i].get(y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = gated(x[j], y[j]);
+      }
+      if (!in)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = 0.0f;
+      bad |= mx_put<FMT>(p.m, f, row, col, in, x, lane);
+    }
   }
   if (bad) set_status(p.status, EAGLE_ERR_NUMERIC);
 }
@@ -60,15 +90,23 @@ __global__ void __launch_bounds__(QT_THREADS) unpack_kernel(QuantParams p) {
   pdl_wait();
   ls.waited();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = blockIdx.x * QT_WARPS + (threadIdx.x >> 5);
   const float g = p.m.g ? *p.m.g : 1.0f;
-  for (long long t = static_cast<long long>(blockIdx.x) * QT_WARPS + (threadIdx.x >> 5); t < p.tasks;
-       t += static_cast<long long>(gridDim.x) * QT_WARPS) {
-    const int row = static_cast<int>(t / p.chunks), col = static_cast<int>(t % p.chunks) * 256 + lane * 8;
-    if (col >= p.m.cols) continue;
-    float v[8];
-    mx_get<FMT>(p.m, g, row, col, v);
-    store8(static_cast<T*>(const_cast<void*>(p.x)) + row * p.ld + col, v);
+  const int col = warp % p.chunks * 256 + lane * 8;
+  if (col >= p.m.cols || warp >= p.step * p.chunks) return;
+  for (int r0 = warp / p.chunks; r0 < p.m.rows; r0 += QT_ROWS * p.step) {
+    MxRaw<FMT> a[QT_ROWS];
+#pragma unroll
+    for (int i = 0; i < QT_ROWS; ++i)
+      if (r0 + i * p.step < p.m.rows) a[i].load(p.m, r0 + i * p.step, col);
+#pragma unroll
+    for (int i = 0; i < QT_ROWS; ++i) {
+      const int row = r0 + i * p.step;
+      if (row >= p.m.rows) break;
+      float v[8];
+      mx_get<FMT>(a[i], g, v);
+      store8(static_cast<T*>(const_cast<void*>(p.x)) + row * p.ld + col, v);
+    }
   }
 }
 
@@ -92,13 +130,14 @@ cudaError_t launch(eagle_ctx* ctx, QuantKernel k, const eagle_mx* m, const void*
   p.x = x;
   p.ld = ld;
   p.chunks = ceil_div(m->cols, 256);
-  p.tasks = static_cast<long long>(m->rows) * p.chunks;
+  // a warp keeps to its 256 columns and goes down the rows; as many warps as there are rows for, up to 96 an SM
+  const int most = 96 * ctx->sm_count / p.chunks;
+  p.step = most < 1 ? 1 : m->rows < most ? m->rows : most;
   p.status = status;
   p.stamp = stamp_slot(ctx, EAGLE_K_QUANT);
-  const long long want = (p.tasks + QT_WARPS - 1) / QT_WARPS;
-  const long long most = 8ll * ctx->sm_count;
   trace_before(ctx, EAGLE_K_QUANT, st);
-  const cudaError_t e = launch_pdl(k, dim3(static_cast<unsigned>(want < most ? want : most)), dim3(QT_THREADS), 0, st, p);
+  const cudaError_t e =
+      launch_pdl(k, dim3(ceil_div(p.step * p.chunks, QT_WARPS)), dim3(QT_THREADS), 0, st, p);
   ctx->launches++;
   trace_after(ctx, EAGLE_K_QUANT, st);
   return e;
