@@ -4,20 +4,24 @@
 // floor(2^40 e^((z - max) / t)) are computed from them wherever one is needed.  Weights are whole numbers and their sums
 // exact, so the order of sums does not matter and a border is where the definition has it.
 //
-// The passes over a thread's tokens are loops of four at a time, not unrolled over registers: each is gone through once a
-// row, and the straight-line form waited for its own instructions (one row of 32000: 48 us).  A warp's lanes stay together
-// in them: which weights need more than fp32 is decided for the whole warp, and computed without branches.
-//
 // Tokens within 17 powers of two of the largest weight (the near ones) are few as a rule: each CTA lists where they are,
-// and all that needs more than fp32's precision goes over that list.  The cut (the last token in falling order that top-k
-// or top-p keeps) is found among fewer still.  Top-k: of the threads' own largest tokens, the k-th largest bounds the
-// row's k-th from below, so a histogram of these alone (1024 bins by the distance to the row's largest) gives a bin up to
-// which there are at least k tokens, and seldom many more.  Top-p: one pass adds up the weight of all tokens and of those
-// within 4, 8, 12 and 17 powers of two of the largest, and the cut lies between two of these.  Where such a part has
-// at most 512 tokens, the cluster's first CTA gathers and sorts it; so top-k needs the weights of its own tokens alone.
-// Otherwise a histogram of the part's tokens, with their number or weight, is summed over the cluster (a slice of the
-// bins a CTA) and scanned by its first CTA; a bin that still has more tokens is split by the bits of the logits, 10 at a
-// time, and tokens of one value by their ids.
+// and all that needs more than fp32's precision goes over that list, so that the work on them is dense.  The passes are
+// loops, not unrolled over registers: each is gone through once a row, and the straight-line form waited for its own
+// instructions (one row of 32000: 48 us).
+//
+// The cut (the last token in falling order that top-k or top-p keeps) is found among fewer still.  Top-k: of the threads'
+// own largest tokens, the k-th largest bounds the row's k-th from below, so a histogram of these alone (1024 bins by the
+// distance to the row's largest) gives a bin up to which there are at least k tokens, and seldom many more.  Top-p: one
+// pass adds up the weight of all tokens and of those within 4, 8, 12 and 17 powers of two of the largest, and the cut lies
+// between two of these.  Where such a part has at most 512 tokens, the cluster's first CTA gathers and sorts it; so
+// top-k needs the weights of its own tokens alone, and that CTA finishes the row.  Otherwise a histogram of the part's
+// tokens, with their number or weight, is summed over the cluster (a slice of the bins a CTA) and scanned by its first
+// CTA; a bin that still has more tokens is split by the bits of the logits, 10 at a time, and tokens of one value by
+// their ids.
+//
+// Bound: instructions (216 rows of 32000: greedy 17 us, top-k of 50 41, top-p of 0.9 83 at t = 0.9), and for one row the
+// latency of the exchanges and of code run once (16.8 us).  CTAs that go over longer pieces of a row from L2 instead of
+// keeping it: greedy 7 us, top-k of 50 17, but top-p 142, a row's work then being one or two CTAs'.
 #include <algorithm>
 
 #include "internal.h"
@@ -403,11 +407,12 @@ __device__ __forceinline__ uint32_t gather(const SampleParams& p, SampleShared& 
 }
 
 // Sorts the threads' e, the first n of them other than 0, largest first: a bitonic network, by shuffles where partners
-// share a warp, else over s.list.
+// share a warp, else over s.list, by as many warps as it takes.
 __device__ __forceinline__ void sort_threads(SampleShared& s, int n, uint64_t& e) {
   const int t = threadIdx.x;
   int width = 32;
   while (width < n) width <<= 1;
+  if (t >= width) return;
 #pragma unroll 1
   for (int size = 2; size <= width; size <<= 1) {
 #pragma unroll 1
@@ -416,9 +421,9 @@ __device__ __forceinline__ void sort_threads(SampleShared& s, int n, uint64_t& e
       if (stride < 32) {
         o = __shfl_xor_sync(0xffffffffu, e, stride);
       } else {
-        __syncthreads();
+        sm100::named_barrier(1, width);
         s.list[t] = e;
-        __syncthreads();
+        sm100::named_barrier(1, width);
         o = s.list[t ^ stride];
       }
       const bool larger = ((t & stride) == 0) == ((t & size) == 0);   // of the two, this thread keeps the larger
@@ -571,13 +576,13 @@ __device__ __noinline__ void count_cut(const SampleParams& p, SampleShared& s, R
 __device__ __forceinline__ uint32_t gather_top(const SampleParams& p, SampleShared& s, Row r, const Tokens& tk, float mine,
                                                uint32_t k, uint32_t rank) {
   r.from = 0.0f;
-  r.to = SP_FAR;
-  r.bins = static_cast<float>(SP_BINS) / SP_FAR;
+  r.to = 41.0f;
+  r.bins = static_cast<float>(SP_BINS) / 41.0f;
   for (int b = threadIdx.x; b < SP_BINS; b += SP_THREADS) s.count[b] = 0;
   __syncthreads();
   if (distance(r, mine) < r.to) atomicAdd(&s.count[bin_of(r, mine)], 1u);
   if (k * static_cast<uint32_t>(p.cluster) <= SP_LIST / 2) {
-    if (threadIdx.x == 0) s.digit = SP_BINS - 1;   // fewer than k: all the near ones
+    if (threadIdx.x == 0) s.digit = SP_BINS - 1;   // fewer than k: all that have weight
     __syncthreads();
     const uint2 two = *reinterpret_cast<const uint2*>(&s.count[2 * threadIdx.x]);
     static_assert(SP_BINS == 2 * SP_THREADS, "two bins a thread");
@@ -604,7 +609,7 @@ __device__ __forceinline__ uint32_t gather_top(const SampleParams& p, SampleShar
     }
   }
   const float end = static_cast<float>(s.digit + 1);
-  const uint32_t n = gather(p, s, tk, false, rank, [&](float z) { return distance(r, z) * r.bins < end; });
+  const uint32_t n = gather(p, s, tk, false, rank, [&](float z) { return distance(r, z) < 41.0f && distance(r, z) * r.bins < end; });
   return n >= k && n <= SP_LIST ? n : 0;
 }
 
@@ -646,27 +651,20 @@ __device__ __forceinline__ void top_p_cut(const SampleParams& p, SampleShared& s
     st_all_u32(p, &s.parts[rank].count[c], b);
   }
   meet(p);
-  // the first part whose weight, with those before it, reaches what is needed
-  uint32_t before_n = 0, there = 0xffffffffu;
-  uint64_t before_w = 0;
-  {
-    uint64_t all = 0;
-    for (int c = 0; c < p.cluster; ++c) all += s.parts[c].weight[SP_PARTS];
-    if (need == 0) need = needed(top_p, all);
-  }
-  r.from = 0.0f;
-#pragma unroll 1
-  for (int i = 0; i <= SP_PARTS; ++i) {
-    uint64_t a = 0;
-    uint32_t b = 0;
-    for (int c = 0; c < p.cluster; ++c) a += s.parts[c].weight[i], b += s.parts[c].count[i];
-    r.to = part_reach(i);
-    there = i < SP_PARTS ? b - before_n : 0xffffffffu;
-    if (a >= need || i == SP_PARTS) break;
-    r.from = r.to;
-    before_n = b;
-    before_w = a;
-  }
+  // the first part whose weight, with those before it, reaches what is needed: a lane a part
+  uint64_t a = 0;
+  uint32_t b = 0;
+  if (lane <= SP_PARTS)
+    for (int c = 0; c < p.cluster; ++c) a += s.parts[c].weight[lane], b += s.parts[c].count[lane];
+  if (need == 0) need = needed(top_p, __shfl_sync(0xffffffffu, a, SP_PARTS));
+  const uint32_t enough = __ballot_sync(0xffffffffu, lane < SP_PARTS && a >= need) | 1u << SP_PARTS;
+  const int part = __ffs(enough) - 1, last = max(part - 1, 0);
+  const uint64_t before_w = part ? __shfl_sync(0xffffffffu, a, last) : 0;
+  const uint32_t before_n = part ? __shfl_sync(0xffffffffu, b, last) : 0;
+  const uint32_t upto = __shfl_sync(0xffffffffu, b, part);
+  const uint32_t there = part < SP_PARTS ? upto - before_n : 0xffffffffu;
+  r.from = part ? part_reach(last) : 0.0f;
+  r.to = part_reach(part);
   if (there > SP_LIST) {
     count_cut(p, s, r, tk, true, need, before_n, before_w, rank);
     return;
