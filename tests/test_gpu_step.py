@@ -762,3 +762,67 @@ def test_target_step_captured():
         runs.append((torch.stack(tokens), b["z"].clone(), b["h2"].clone()))
         assert engine().status() == 0
     assert all(torch.equal(p, q) for p, q in zip(*runs))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("outs", [1, 8, 15, 33, 191, 193, 260, 1000])
+def test_linear_many_rows_any_outputs(fmt, outs):
+    """Rows as the first operand: 16 outputs a store, 8, and single ones; pitches that are and are not whole sectors."""
+    for rows, more, out in ((129, 0, BF16), (300, 8, BF16), (300, 16, F32), (1025, 4, F32)):
+        check_linear(fmt, rows, 288, outs, out, True, seed=rows + outs, more=more)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_linear_many_rows_with_a_non_finite_block(fmt):
+    x = normal(21, 700, 512)
+    x[431, 100] = INF
+    t = mx(fmt, 700, 512, 0.01).quantize(x)
+    assert engine().status() == NUMERIC
+    w = mx(fmt, 600, 512, 0.01).quantize(normal(22, 600, 512))
+    y = R.mx_linear(t, w, torch.empty(700, 600, device="cuda"))
+    bad = torch.zeros(700, dtype=torch.bool, device="cuda")
+    bad[431] = True
+    assert torch.isnan(y[bad]).all() and torch.isfinite(y[~bad]).all()
+    assert engine().status() == 0
+
+
+def test_offsets_beyond_32_bits():
+    """Matrices, rows of logits and outputs of more than 2^32 bytes or 2^31 elements: their far ends."""
+    rows, cols = 66000, 65536
+    x = torch.zeros(rows, cols, dtype=BF16, device="cuda")
+    x[-3:] = normal(1, 3, cols, dtype=BF16)
+    w = mx("fp8", rows, cols).quantize(x)
+    y = w.unpack(x.fill_(5.0))
+    code, byte = O.quantize("fp8", f64(normal(1, 3, cols, dtype=BF16)))
+    assert np.array_equal(f64(y[-3:]), O.values("fp8", code, byte)) and not y[:-3:997].any()
+    a = mx("fp8", 5, cols).quantize(normal(2, 5, cols) * 0.1)
+    out = R.mx_linear(a, w, torch.empty(5, rows, device="cuda"))
+    av, wv = held(a), O.values("fp8", code, byte)
+    assert (np.abs(f64(out[:, -3:]) - av @ wv.T) <= (cols + 8) * 2.0 ** -23 * (np.abs(av) @ np.abs(wv).T)).all()
+    assert not out[:, :-3].any()
+    del x, y, w, out
+    # many rows by many outputs
+    a = mx("nv4", 70000, 64, 0.01).quantize(normal(3, 70000, 64))
+    b = mx("nv4", 65000, 64, 0.01).quantize(normal(4, 65000, 64))
+    y = R.mx_linear(a, b, torch.empty(70000, 65000, dtype=BF16, device="cuda"))
+    bv = torch.tensor(held(b), device="cuda")
+    for r in (0, 33333, 69999):
+        want = torch.tensor(held(a)[r:r + 1], device="cuda") @ bv.t()
+        assert torch.allclose(y[r:r + 1].double(), want, rtol=2.0 ** -8, atol=1e-4)
+    del y
+    n = 70000
+    x = torch.zeros(n, 32768, dtype=BF16, device="cuda")
+    x[-1] = normal(5, 32768, dtype=BF16)
+    y = R.add_norm(engine(), x, torch.empty_like(x))
+    want = O.add_norm(f64(x[-1:]), None, None, 1e-5)[1]
+    assert (np.abs(f64(y[-1:]) - want) <= (U[BF16] + REL) * np.abs(want)).all() and not y[:-1:999].any()
+    del x, y
+    n, V = 17000, 131072
+    z = torch.zeros(n, V, device="cuda")
+    z[-1, V - 2] = 90.0
+    token = i32([0] * n)
+    probs = torch.empty(n, V, device="cuda")
+    R.Sampler(engine(), n, top_k=i32([3] * n))(z, i32([0] * n), token, None, probs)
+    assert token[:-1].unique().tolist() == [0] and int(token[-1]) == V - 2
+    assert probs[-1, V - 2] == 1 and probs[0, :4].tolist() == pytest.approx([1 / 3, 1 / 3, 1 / 3, 0.0])
+    assert engine().status() == 0
