@@ -116,10 +116,12 @@ void layout(eagle_ctx* c) {
     records = std::max(records, static_cast<size_t>(L.max_rows) * D.n_q_heads * s1);
     records = std::max(records, static_cast<size_t>(b) * L.max_tree * D.n_q_heads * s1);
   }
-  // the chunk attention's partials take their place in its calls
-  W.attn_part = take(std::max(records * (D.head_dim + 4) * 4, chunk_part_bytes(c->sm_count, D.head_dim)));
+  // the chunk attention's partials take their place in its calls, the state of the sampled rows in eagle_sample's
+  W.attn_part = take(std::max({records * (D.head_dim + 4) * 4, chunk_part_bytes(c->sm_count, D.head_dim),
+                               SAMPLE_ROWS * sample_row_bytes()}));
   W.attn_cnt = take(static_cast<size_t>(2) * L.max_batch * D.n_kv_heads * 4);
   W.chunk_cnt = take(static_cast<size_t>(chunk_counters(c->sm_count)) * 4);
+  W.sample_cnt = take(2 * SAMPLE_ROWS * sizeof(int));
   W.pages = take(static_cast<size_t>(PAGES_LISTS) * L.max_batch * 4 + 256);
   W.total = off;
 }
@@ -1059,7 +1061,7 @@ eagle_status eagle_sample(eagle_ctx* ctx, int n_rows, int vocab, int dtype, cons
   }
   if ((st = check_ws(workspace)) != EAGLE_OK) return st;
   const SampleLaunch S{n_rows, vocab, dtype, logits, ld, f, u, token, argmax, probs, ld_probs,
-                       ws_ptr<int>(workspace, ctx->ws.status)};
+                       ws_ptr<int>(workspace, ctx->ws.status), ws_ptr<void>(workspace, ctx->ws.attn_part), ws_ptr<int>(workspace, ctx->ws.sample_cnt)};
   EAGLE_CUDA(launch_sample(ctx, S, stream));
   return EAGLE_OK;
 }

@@ -48,6 +48,7 @@ struct Workspace {
   size_t attn_part;              // fp32 partial (m, l, acc[dh]) records
   size_t attn_cnt;               // int [2][max_batch * Hkv]
   size_t chunk_cnt;              // int [chunk_counters]: arrivals at the chunk attention's split items
+  size_t sample_cnt;             // int [2][SAMPLE_ROWS]: arrivals of a sampled row's CTAs
   size_t pages;                  // int lists of the page calls (PAGES_LISTS per sequence) and their counts
   size_t total;
   int max_mtiles;
@@ -305,7 +306,9 @@ cudaError_t launch_quantize(eagle_ctx* ctx, int dtype, int act, const void* x, i
 cudaError_t launch_unpack(eagle_ctx* ctx, const eagle_mx* x, int dtype, void* y, int ld, cudaStream_t st);
 cudaError_t launch_linear(eagle_ctx* ctx, const eagle_mx* x, const eagle_mx* w, const float* bias, int dtype, void* y,
                           int ld_y, int* status, cudaStream_t st);
-// eagle_sample
+// eagle_sample; rows_state: SAMPLE_ROWS of sample_row_bytes() each, of no value between calls; arrived: 2 * SAMPLE_ROWS
+constexpr int SAMPLE_ROWS = 512;
+size_t sample_row_bytes();
 struct SampleLaunch {
   int rows, vocab, dtype;
   const void* logits;
@@ -317,6 +320,8 @@ struct SampleLaunch {
   float* probs;
   int ld_probs;
   int* status;
+  void* rows_state;
+  int* arrived;
 };
 cudaError_t launch_sample(eagle_ctx* ctx, const SampleLaunch& S, cudaStream_t st);
 size_t chunk_part_bytes(int sm_count, int head_dim);   // its partials

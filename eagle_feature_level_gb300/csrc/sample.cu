@@ -1,27 +1,30 @@
 // eagle_sample: a row's distribution under temperature, top-k, top-p and min-p, and a draw from it.
 //
-// A cluster of CTAs holds a row's logits in shared memory, so that they are read once; the weights
-// floor(2^40 e^((z - max) / t)) are computed from them wherever one is needed.  Weights are whole numbers and their sums
-// exact, so the order of sums does not matter and a border is where the definition has it.
+// Weights are whole numbers, floor(2^40 e^((z - max) / t)), and their sums exact, so the order of sums does not matter and
+// a border is where the definition has it.
 //
-// Tokens within 17 powers of two of the largest weight (the near ones) are few as a rule: each CTA lists where they are,
-// and all that needs more than fp32's precision goes over that list, so that the work on them is dense.  The passes are
-// loops, not unrolled over registers: each is gone through once a row, and the straight-line form waited for its own
-// instructions (one row of 32000: 48 us).
+// Rows are gone over in chunks of 4096 tokens, a few to a CTA, whatever the number of rows and their length, so that the
+// work is even; what the chunks find out meets in the row's state, where the last CTA to arrive draws the conclusion:
+//   1. the largest logit, and with it the scale of the row;
+//   2. bins of the tokens by their distance from the largest: their number (top-k, eighths of a power of two) or weight
+//      (top-p, sixteenths), and from these the bin with the cut, the last token in falling order that is kept;
+//   3. the weight of each chunk before that bin, and a list of the bin's tokens (with top-k and top-p both, of all up to
+//      it: top-p's part is of those k);
+//   4. a CTA a row sorts the list, which gives the cut and the weight of each chunk, and draws: the chunk, then the token;
+//   5. the probabilities, where wanted.
+// The logits come from memory once and then from L2.  512 tokens are sorted at a time; where a bin has more, they are told
+// apart by 1024 bins of the bin, then by the bits of the logits, 10 at a time, then by their ids (many of one value).  A
+// list holds 4096; past that (or where the cut is behind 22 powers of two, where weight has no bins) the CTA goes over the
+// row itself.
 //
-// The cut (the last token in falling order that top-k or top-p keeps) is found among fewer still.  Top-k: of the threads'
-// own largest tokens, the k-th largest bounds the row's k-th from below, so a histogram of these alone (1024 bins by the
-// distance to the row's largest) gives a bin up to which there are at least k tokens, and seldom many more.  Top-p: one
-// pass adds up the weight of all tokens and of those within 4, 8, 12 and 17 powers of two of the largest, and the cut lies
-// between two of these.  Where such a part has at most 512 tokens, the cluster's first CTA gathers and sorts it; so
-// top-k needs the weights of its own tokens alone, and that CTA finishes the row.  Otherwise a histogram of the part's
-// tokens, with their number or weight, is summed over the cluster (a slice of the bins a CTA) and scanned by its first
-// CTA; a bin that still has more tokens is split by the bits of the logits, 10 at a time, and tokens of one value by
-// their ids.
+// Weights from 2^23 on (the near tokens') take fixed point and pairs of floats, the others fp32.  Near tokens are a small
+// part of a row as a rule: a warp lists its own first, so that the work on them is dense.
 //
-// Bound: instructions (216 rows of 32000: greedy 17 us, top-k of 50 41, top-p of 0.9 83 at t = 0.9), and for one row the
-// latency of the exchanges and of code run once (16.8 us).  CTAs that go over longer pieces of a row from L2 instead of
-// keeping it: greedy 7 us, top-k of 50 17, but top-p 142, a row's work then being one or two CTAs'.
+// Bound: instructions where rows are flat (64 rows of 131072 in bf16: top-p of 0.95 at t = 1.3 86 us, issue slots 41 %
+// full), else the launches and the latency of each kernel's exchanges (greedy 14 us, top-k of 50 39, min-p of 0.05 27; one
+// row of 32000: top-k of 400 and top-p 18).  A cluster of CTAs that keeps a row in shared memory through all steps reads it
+// once and saves launches, but leaves the SMs waiting for its exchanges: one row 17 us, those 64 rows 209 (flat), 26, 66
+// and 56, and a batch of all sorts 113 us where this takes 59.
 #include <algorithm>
 
 #include "internal.h"
@@ -33,11 +36,51 @@ namespace {
 
 constexpr int SP_THREADS = 512;
 constexpr int SP_WARPS = SP_THREADS / 32;
-constexpr int SP_BINS = 1024;
-constexpr int SP_LIST = SP_THREADS;
-constexpr int SP_MAX_CLUSTER = 16;
-constexpr int SP_RUN = 8 * SP_THREADS;          // tokens a CTA takes with eight a thread
-constexpr int SP_MAX_RUNS = 4;
+constexpr int SP_LIST = 8 * SP_THREADS;         // of a row
+constexpr int SP_SORT = SP_THREADS;             // sorted at a time
+constexpr int SP_CHUNK = 8 * SP_THREADS;        // eight tokens a thread
+constexpr int SP_MAX_CHUNKS = EAGLE_MAX_SAMPLE_VOCAB / SP_CHUNK;
+constexpr int SP_MAX_PIECES = 3;                // chunks of a CTA
+static_assert(SP_MAX_CHUNKS <= 64, "two chunks a lane");
+
+// From this distance on a weight (2^23 or less) needs no more than fp32, and from the other it is nothing.
+constexpr float SP_FAR = 17.0f, SP_NONE = 41.0f;
+// A row's bins: where tokens are counted, up to SP_NONE; where they are weighed, up to SP_WEIGHED (the tokens behind it
+// have 2^-22 of the largest's weight at most: a cut among them takes a row as flat as it is long).
+constexpr float SP_COUNT_BINS = 8.0f, SP_WEIGHT_BINS = 16.0f, SP_WEIGHED = 22.0f;
+constexpr int SP_LANE_BINS = 11;                 // of a lane, where a warp goes over them
+constexpr int SP_ROW_BINS = 32 * SP_LANE_BINS;
+static_assert(SP_NONE * SP_COUNT_BINS <= SP_ROW_BINS && SP_WEIGHED * SP_WEIGHT_BINS <= SP_ROW_BINS, "all bins");
+constexpr int SP_BINS = 2 * SP_THREADS;          // of a bin
+
+// What there is to do for a row: nothing, as it has no distribution or is greedy, or to draw from all its weights, from a
+// beginning by number or by weight, or from what min_p keeps.
+enum RowKind : int { ROW_NONE, ROW_GREEDY, ROW_WHOLE, ROW_COUNT, ROW_WEIGH, ROW_REACH };
+
+// The largest key of some chunks and its first id, and whether any logit is NaN or +inf.
+struct alignas(16) Extent {
+  uint32_t top, id, bad, pad;
+};
+
+// A row's state between the kernels.
+struct alignas(16) SampleRow {
+  // by the first kernel's last CTA; `from`, `end` by the second's where the row has bins
+  float top, c_hi, c_lo;                        // its Row
+  int kind;
+  float from, end;                              // tokens nearer than `from` are kept, those from `end` on not
+  float reach;                                  // distance up to which min_p may keep a token
+  uint32_t id;                                  // the argmax
+  uint64_t least;                               // min_p's weight
+  uint64_t need, before;                        // the cut's number or weight, and the number or weight before `from`
+  uint64_t far;                                 // weight of the tokens behind the bins, where those are weighed
+  uint32_t listed;                              // tokens in `list`, or more than it takes
+  uint32_t cut_key, cut_id;                     // by the fourth: the last token kept (0: all), and one over the weight
+  float inverse;
+  Extent extent[SP_MAX_CHUNKS];                 // of each CTA's chunks
+  uint64_t total[SP_MAX_CHUNKS];                // weight of each chunk before `from`
+  uint64_t bins[SP_ROW_BINS];                   // number or weight of the tokens in each
+  uint64_t list[SP_LIST];                       // tokens from `from` to `end`: key << 32 | ~id
+};
 
 struct SampleParams {
   const void* logits;
@@ -54,8 +97,11 @@ struct SampleParams {
   int32_t* argmax;
   float* probs;
   long long ld_probs;
-  int cluster;
-  int each;                // tokens of a thread
+  SampleRow* state;
+  int* arrived;            // [2][SAMPLE_ROWS]: of a row's CTAs in the first two kernels, zero between calls
+  int row0;                // the launch's first row, whose state is the first
+  int chunks, pieces;      // of a row, and of a CTA of it
+  int groups;              // CTAs of a row
   int* status;
   uint64_t* stamp;
 };
@@ -80,57 +126,9 @@ struct __align__(16) Pow2 {
   float hi, lo;
 };
 
-// What a CTA tells the others about its part of the row: the largest key and its first id, and whether any logit is NaN
-// or +inf.
-struct Extent {
-  uint32_t top, id, bad, pad;
-};
-// From this distance on a weight (2^23 or less) needs no more than fp32.
-constexpr float SP_FAR = 17.0f;
-constexpr uint64_t SP_FAR_WEIGHT = 1ull << 23;   // the largest there
-
-// Number and weight of a CTA's tokens within each of the parts' distances, and the weight of all.
-constexpr int SP_PARTS = 4;
-struct Parts {
-  uint64_t weight[SP_PARTS + 1];
-  uint32_t count[SP_PARTS + 1];
-};
-__device__ __forceinline__ float part_reach(int i) {
-  return i == 0 ? 4.0f : i == 1 ? 8.0f : i == 2 ? 12.0f : i == 3 ? SP_FAR : 41.0f;
-}
-
-struct SampleShared {
-  // bins of this CTA's tokens: how many, and their weight in two words
-  alignas(16) uint32_t count[SP_BINS];
-  uint32_t lo[SP_BINS], hi[SP_BINS];
-  // (first CTA) bins of the whole row; tokens, largest first once sorted: key << 32 | ~id
-  uint32_t all_count[SP_BINS];
-  uint64_t all_weight[SP_BINS];
-  uint64_t list[SP_LIST], kept[SP_LIST];
-  Parts parts[SP_MAX_CLUSTER], warp_parts[SP_WARPS];
-  Pow2 pow2[64];
-  Extent extent[SP_MAX_CLUSTER];
-  uint64_t total[SP_MAX_CLUSTER];
-  uint64_t warp_total[SP_WARPS];
-  uint32_t warp_lo[SP_WARPS], warp_hi[SP_WARPS];
-  uint64_t scan[SP_WARPS];
-  uint32_t scan_n[SP_WARPS];
-  Extent warp_extent[SP_WARPS];
-  // a search's state, written by the first CTA to all
-  uint32_t near_n;               // near tokens of this CTA
-  uint32_t listed;               // tokens in this CTA's list
-  uint32_t digit, in_digit;      // where the cut falls, and how many tokens fall there
-  uint32_t before_n;             // tokens and weight before it
-  uint64_t before_w;
-  uint32_t cut_key, cut_id;
-  uint64_t need_w;
-  uint32_t tie[SP_MAX_CLUSTER];  // tokens of the cut's value in each CTA
-};
-
 // The row's constants.
 struct Row {
   float top, c_hi, c_lo;
-  float from, to, bins;          // the part's distances, and bins of one
 };
 
 // (top - z) log2(e) / t to fp32's precision; large for what has no weight at all.
@@ -156,7 +154,7 @@ __device__ __forceinline__ uint32_t far_weight(const Row& r, float z) {
 // log2(e) / t are pairs of floats; y = k / 64 + r, |r| <= 1 / 128, and 2^(-r) - 1 = u + u^2 / 2 + u^3 / 6 + u^4 / 24 with
 // u = -r ln 2 (the next term is below 2^-44), the linear term a pair, the rest (2^-16) a float; table entry and product
 // then meet in 46-bit fixed point.
-__device__ __forceinline__ uint64_t near_weight(const SampleShared& s, const Row& r, float z) {
+__device__ __forceinline__ uint64_t near_weight(const Pow2* pow2, const Row& r, float z) {
   constexpr float MAGIC = 12582912.0f;           // 1.5 2^23: the sum's low bits are the rounded integer
   constexpr int MAGIC_BITS = 0x4B400000;
   const float dh = r.top - z;
@@ -170,7 +168,7 @@ __device__ __forceinline__ uint64_t near_weight(const SampleShared& s, const Row
   const float uh = -rs * LN2_HI;
   const float ul = fmaf(-rs, LN2_HI, -uh) - fmaf(rs, LN2_LO, rl * LN2_HI);
   const float v = fmaf(uh * uh, fmaf(uh, fmaf(uh, 1.0f / 24.0f, 1.0f / 6.0f), 0.5f), ul);
-  const Pow2 t = s.pow2[k & 63];
+  const Pow2 t = pow2[k & 63];
   const float a = t.hi * uh;
   const float b = fmaf(t.hi, uh, -a) + fmaf(t.hi, v, t.lo * uh);
   const float c = a + b, cl = b - (c - a);
@@ -182,112 +180,21 @@ __device__ __forceinline__ uint64_t near_weight(const SampleShared& s, const Row
   return static_cast<uint64_t>(w) >> (6 + (k >> 6));
 }
 
-__device__ __forceinline__ uint64_t weight(const SampleShared& s, const Row& r, float z) {
+__device__ __forceinline__ uint64_t weight(const Pow2* pow2, const Row& r, float z) {
   const float y = distance(r, z);
-  return y < SP_FAR ? near_weight(s, r, z) : far_weight(r, z);
+  return y < SP_FAR ? near_weight(pow2, r, z) : far_weight(r, z);
 }
 
-// The weights of four tokens, those not wanted 0 (the whole warp calls it).
-__device__ __forceinline__ void weights4(const SampleShared& s, const Row& r, const float (&z)[4], const bool (&wanted)[4],
-                                         uint64_t (&w)[4]) {
-  float y[4];
-  bool near = false;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    y[q] = distance(r, z[q]);
-    w[q] = wanted[q] ? far_weight(r, z[q]) : 0;
-    near |= wanted[q] && y[q] < SP_FAR;
-  }
+// The same, 0 where not wanted, without paths that no thread of the warp needs (the whole warp calls it).
+__device__ __forceinline__ uint64_t weight_of(const Pow2* pow2, const Row& r, float z, bool wanted) {
+  const bool near = wanted && distance(r, z) < SP_FAR;
+  uint64_t w = wanted && !near ? far_weight(r, z) : 0;
   if (__any_sync(0xffffffffu, near)) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint64_t x = near_weight(s, r, z[q]);
-      if (wanted[q] && y[q] < SP_FAR) w[q] = x;
-    }
+    const uint64_t x = near_weight(pow2, r, z);
+    if (near) w = x;
   }
+  return w;
 }
-
-__device__ __forceinline__ uint32_t bin_of(const Row& r, float z) {
-  return static_cast<uint32_t>(fminf((distance(r, z) - r.from) * r.bins, static_cast<float>(SP_BINS - 1)));
-}
-
-// The digit of a search's pass `level`: the bin, then 10, 10, 10 and 2 bits of the logit's order.
-__device__ __forceinline__ int key_shift(int level) { return level >= 4 ? 0 : 32 - 10 * level; }
-__device__ __forceinline__ uint32_t digit_of(const Row& r, float z, int level) {
-  if (level == 0) return bin_of(r, z);
-  return (order_key(z) >> key_shift(level)) & (level == 4 ? 3u : SP_BINS - 1u);
-}
-
-// Exclusive sums over the block of a pair, in thread order.
-__device__ __forceinline__ void block_before(SampleShared& s, uint32_t n, uint64_t w, uint32_t& n0, uint64_t& w0) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t in = n;
-  uint64_t iw = w;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t a = __shfl_up_sync(0xffffffffu, in, o);
-    const uint64_t b = __shfl_up_sync(0xffffffffu, iw, o);
-    if (lane >= o) in += a, iw += b;
-  }
-  if (lane == 31) s.scan_n[warp] = in, s.scan[warp] = iw;
-  __syncthreads();
-  n0 = in - n;
-  w0 = iw - w;
-#pragma unroll
-  for (int i = 0; i < SP_WARPS; ++i)
-    if (i < warp) n0 += s.scan_n[i], w0 += s.scan[i];
-}
-
-__device__ __forceinline__ void st_all_u32(const SampleParams& p, void* local, uint32_t v) {
-  for (int c = 0; c < p.cluster; ++c) sm100::dsmem_st_s32(sm100::dsmem_addr(local, c), static_cast<int>(v));
-}
-__device__ __forceinline__ void st_all_u64(const SampleParams& p, void* local, uint64_t v) {
-  for (int c = 0; c < p.cluster; ++c) sm100::dsmem_st_u64(sm100::dsmem_addr(local, c), v);
-}
-__device__ __forceinline__ uint32_t dsmem_ld_u32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
-
-// Every thread of the cluster; shared-memory accesses before, local or remote, come before those after.
-__device__ __forceinline__ void meet(const SampleParams& p) {
-  if (p.cluster > 1) sm100::cluster_sync();
-  else __syncthreads();
-}
-
-// A CTA's tokens in shared memory.  Token i of thread t is at place i * threads + t and is id base(t) + (i / 8) * 256 +
-// i % 8: a warp has a run of consecutive ids.
-struct Tokens {
-  float* all;
-  uint16_t* near;          // places of the near tokens
-  int n;                   // tokens of a thread
-  int first;               // the CTA's first id
-  __device__ __forceinline__ float& z(int i) const { return all[i * SP_THREADS + threadIdx.x]; }
-  __device__ __forceinline__ int base(int t) const { return first + (t >> 5) * n * 32 + (t & 31) * 8; }
-  __device__ __forceinline__ int id(int i) const { return base(threadIdx.x) + (i >> 3) * 256 + (i & 7); }
-  __device__ __forceinline__ int id_at(int place) const {
-    const int i = place / SP_THREADS;
-    return base(place % SP_THREADS) + (i >> 3) * 256 + (i & 7);
-  }
-  // Calls f(place, z, there) for every near token (dense) or every token, by whole warps.
-  template <typename F>
-  __device__ __forceinline__ void each(bool dense, uint32_t near_n, F f) const {
-    if (!dense) {
-#pragma unroll 4
-      for (int i = 0; i < n; ++i) f(i * SP_THREADS + static_cast<int>(threadIdx.x), z(i), true);
-      return;
-    }
-    const uint32_t end = near_n;
-#pragma unroll 1
-    for (uint32_t at = threadIdx.x; at - (threadIdx.x & 31) < end; at += SP_THREADS) {
-      const bool there = at < end;
-      const uint32_t place = there ? near[at] : 0;
-      f(static_cast<int>(place), all[place], there);
-      __syncwarp();
-    }
-  }
-};
 
 // Eight logits from id `at` on, those past the end -inf.
 __device__ __forceinline__ void load_logits(const float* row, int at, int vocab, bool wide, float (&z)[8]) {
@@ -315,95 +222,416 @@ __device__ __forceinline__ void load_logits(const uint16_t* row, int at, int voc
   }
 }
 
-// Sums the CTAs' bins into the first CTA's all_*.
-__device__ __forceinline__ void sum_bins(const SampleParams& p, SampleShared& s, bool weighted, uint32_t rank) {
-  meet(p);
-  const int slice = SP_BINS / p.cluster;
-  for (int b = static_cast<int>(rank) * slice + threadIdx.x; b < (static_cast<int>(rank) + 1) * slice; b += SP_THREADS) {
-    uint32_t n = 0;
-    uint64_t sum = 0;
-#pragma unroll 4
-    for (int c = 0; c < p.cluster; ++c) {
-      n += dsmem_ld_u32(sm100::dsmem_addr(&s.count[b], c));
-      if (weighted)
-        sum += (static_cast<uint64_t>(dsmem_ld_u32(sm100::dsmem_addr(&s.hi[b], c))) << 32) +
-               dsmem_ld_u32(sm100::dsmem_addr(&s.lo[b], c));
-    }
-    sm100::dsmem_st_s32(sm100::dsmem_addr(&s.all_count[b], 0), static_cast<int>(n));
-    if (weighted) sm100::dsmem_st_u64(sm100::dsmem_addr(&s.all_weight[b], 0), sum);
+__device__ __forceinline__ void store_probs(float* row, int id, int vocab, bool wide, const float (&v)[8]) {
+  if (wide && id + 8 <= vocab) {
+    *reinterpret_cast<float4*>(row + id) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(row + id + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    return;
   }
-  meet(p);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (id + i < vocab) row[id + i] = v[i];
 }
 
-// Where the count or the weight reaches `need` in the first CTA's bins (rising: in their order, else from the last down):
-// digit, in_digit (0: nowhere), before_n and before_w of every CTA, the latter on top of those given.
-__device__ __forceinline__ void scan_bins(const SampleParams& p, SampleShared& s, bool by_weight, bool rising, uint64_t need,
-                                          uint32_t before_n, uint64_t before_w, uint32_t rank) {
-  if (rank == 0) {
-    constexpr int OWN = SP_BINS / SP_THREADS;
-    uint32_t n = 0, cn[OWN];
-    uint64_t sum = 0, cw[OWN];
+// Exclusive sums over the block, in thread order.
+struct BlockScan {
+  uint64_t of[SP_WARPS];
+};
+__device__ __forceinline__ uint64_t block_before(BlockScan& s, uint64_t w) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint64_t upto = w;
 #pragma unroll
-    for (int q = 0; q < OWN; ++q) {
-      const int at = threadIdx.x * OWN + q, b = rising ? at : SP_BINS - 1 - at;
-      cn[q] = s.all_count[b];
-      cw[q] = by_weight ? s.all_weight[b] : 0;
-      n += cn[q];
-      sum += cw[q];
-    }
-    uint32_t n0;
-    uint64_t w0;
-    block_before(s, n, sum, n0, w0);
-    n0 += before_n;
-    w0 += before_w;
-    if (threadIdx.x == SP_THREADS - 1 && (by_weight ? w0 + sum : n0 + n) < need) st_all_u32(p, &s.in_digit, 0);
-#pragma unroll
-    for (int q = 0; q < OWN; ++q) {
-      if (by_weight ? w0 < need && w0 + cw[q] >= need : n0 < need && n0 + cn[q] >= need) {
-        const int at = threadIdx.x * OWN + q;
-        st_all_u32(p, &s.digit, rising ? at : SP_BINS - 1 - at);
-        st_all_u32(p, &s.in_digit, cn[q]);
-        st_all_u32(p, &s.before_n, n0);
-        st_all_u64(p, &s.before_w, w0);
-      }
-      n0 += cn[q];
-      w0 += cw[q];
-    }
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t b = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += b;
   }
-  meet(p);
-}
-
-// The chosen tokens (near ones alone where dense) of all CTAs into the first one's list; how many there are (to every
-// CTA), none gathered where they pass SP_LIST.
-template <typename Chosen>
-__device__ __forceinline__ uint32_t gather(const SampleParams& p, SampleShared& s, const Tokens& tk, bool dense,
-                                           uint32_t rank, Chosen chosen) {
-  if (threadIdx.x == 0) s.listed = 0;
+  __syncthreads();                               // (the last scan's sums are read)
+  if (lane == 31) s.of[warp] = upto;
   __syncthreads();
-  tk.each(dense, s.near_n, [&](int place, float z, bool there) {
-    if (there && chosen(z)) {
-      const uint32_t at = atomicAdd(&s.listed, 1u);
-      if (at < SP_LIST)
-        s.list[at] = static_cast<uint64_t>(order_key(z)) << 32 | (0xffffffffu - static_cast<uint32_t>(tk.id_at(place)));
+  upto -= w;
+#pragma unroll
+  for (int i = 0; i < SP_WARPS; ++i)
+    if (i < warp) upto += s.of[i];
+  return upto;
+}
+
+// ceil(p S), at least 1 and at most S < 2^60: the 24 bits of p times S, shifted down.
+__device__ __forceinline__ uint64_t needed(float top_p, uint64_t all) {
+  if (!(top_p > 0.0f)) return 1;
+  const uint32_t bits = __float_as_uint(top_p), e = bits >> 23;
+  const uint64_t m = e ? (bits & 0x7fffffu) | 0x800000u : bits & 0x7fffffu;
+  const int sh = 150 - static_cast<int>(e ? e : 1u);             // top_p = m 2^-sh, sh >= 24
+  const uint64_t lo = m * all, hi = __umul64hi(m, all);
+  uint64_t need, rest;
+  if (sh < 64) {
+    need = (hi << (64 - sh)) | (lo >> sh);
+    rest = lo & ((1ull << sh) - 1);
+  } else {
+    need = sh < 128 ? hi >> (sh - 64) : 0;
+    rest = lo | hi;                              // (need is 0 or small: one more at most)
+    if (sh < 128 && sh > 64) rest = lo | (hi & ((1ull << (sh - 64)) - 1));
+    if (sh == 64) rest = lo;
+  }
+  need += rest ? 1 : 0;
+  return need < 1 ? 1 : min(need, all);
+}
+
+__device__ __forceinline__ Row row_of(const SampleRow& st) { return Row{st.top, st.c_hi, st.c_lo}; }
+
+__device__ __forceinline__ void fill_pow2(Pow2* pow2) {
+  if (threadIdx.x < 64) {
+    const uint64_t v = kPow2[threadIdx.x];
+    const float h = static_cast<float>(v);
+    pow2[threadIdx.x] =
+        Pow2{v, h * 0x1p-46f, static_cast<float>(static_cast<int64_t>(v) - static_cast<int64_t>(h)) * 0x1p-46f};
+  }
+}
+
+// A row behind those that its request uses.
+__device__ __forceinline__ bool unused(const SampleParams& p, int row, int request) {
+  return p.rows_used && row - request * p.rows_each >= p.rows_used[request];
+}
+
+// Of the first id of a thread's eight in a chunk: a warp's are in a row.
+__device__ __forceinline__ int chunk_id(int chunk) { return chunk * SP_CHUNK + static_cast<int>(threadIdx.x) * 8; }
+
+__device__ __forceinline__ Extent warp_extent(Extent e) {
+  const uint32_t t = __reduce_max_sync(0xffffffffu, e.top);
+  e.id = __reduce_min_sync(0xffffffffu, e.top == t ? e.id : 0xffffffffu);
+  e.bad = __reduce_or_sync(0xffffffffu, e.bad);
+  e.top = t;
+  return e;
+}
+
+// Whether this CTA is the last of its row's to arrive: it then sees what all of them stored (every thread calls it).
+__device__ __forceinline__ bool last_of_row(int* arrived, int ctas) {
+  __shared__ int last;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    last = ctas == 1 || arrive_acq_rel(arrived) == ctas - 1;
+    if (last && ctas > 1) *arrived = 0;
+  }
+  __syncthreads();
+  return last;
+}
+
+__device__ __forceinline__ void add_u64(uint64_t* to, uint64_t v) {
+  atomicAdd(reinterpret_cast<unsigned long long*>(to), static_cast<unsigned long long>(v));
+}
+__device__ __forceinline__ uint64_t ldcg_u64(const uint64_t* at) {
+  return __ldcg(reinterpret_cast<const unsigned long long*>(at));
+}
+
+// 1. The largest logit of every chunk; a row's last CTA takes the row's and its controls, and finishes greedy tokens.
+template <typename T>
+__global__ void __launch_bounds__(SP_THREADS) sample_top_kernel(SampleParams p) {
+  __shared__ Extent warps[SP_WARPS];
+  LaunchStamp ls(p.stamp);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int at = blockIdx.x / p.groups, row = p.row0 + at;
+  const int chunk0 = (blockIdx.x - at * p.groups) * p.pieces, chunk1 = min(chunk0 + p.pieces, p.chunks);
+  pdl_wait();
+  ls.waited();
+  pdl_trigger();
+  const int request = row / p.rows_each;
+  if (unused(p, row, request)) return;
+  SampleRow& st = p.state[at];
+  const T* logits = static_cast<const T*>(p.logits) + row * p.ld;
+  const bool wide = (reinterpret_cast<uintptr_t>(logits) & 15) == 0;
+  float top = -INFINITY;                         // NaN if any is
+  uint32_t id = 0xffffffffu;
+#pragma unroll 2
+  for (int chunk = chunk0; chunk < chunk1; ++chunk) {
+    float z[8], most = -INFINITY;
+    load_logits(logits, chunk_id(chunk), p.vocab, wide, z);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(most) : "f"(z[i]));
+    if (chunk == chunk0 || most > top) {         // (the first of equals stays; with a NaN the id is not used)
+#pragma unroll
+      for (int i = 7; i >= 0; --i)
+        if (z[i] == most) id = static_cast<uint32_t>(chunk_id(chunk) + i);
     }
-  });
-  if (p.cluster == 1) {
-    __syncthreads();
-    return s.listed;
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(most));
   }
-  meet(p);
-  uint32_t at = 0;                               // this CTA's place, and all
+  Extent e = warp_extent(Extent{order_key(top), id, top < INFINITY ? 0u : 1u, 0u});
+  if (lane == 0) warps[warp] = e;
+  __syncthreads();
+  if (warp == 0) {
+    e = warp_extent(warps[lane % SP_WARPS]);
+    if (lane == 0) *reinterpret_cast<uint4*>(&st.extent[blockIdx.x - at * p.groups]) = make_uint4(e.top, e.id, e.bad, 0);
+  }
+  if (!last_of_row(p.arrived + at, p.groups)) return;
+  if (threadIdx.x < SP_ROW_BINS) st.bins[threadIdx.x] = 0;
+  static_assert(SP_ROW_BINS <= SP_THREADS, "a bin a thread");
+  if (warp > 0) return;
+  e = Extent{0, 0xffffffffu, 0, 0};
+#pragma unroll
+  for (int c = 0; c < SP_MAX_CHUNKS; c += 32) {
+    if (c + lane < p.groups) {
+      const uint4 v = __ldcg(reinterpret_cast<const uint4*>(&st.extent[c + lane]));
+      if (v.x > e.top) e.top = v.x, e.id = v.y;   // (the later CTA's ids are larger)
+      e.bad |= v.z;
+    }
+  }
+  e = warp_extent(e);
+  if (lane > 0) return;
+  const float temp = p.temperature ? p.temperature[request] : 1.0f;
+  const int k = p.top_k ? p.top_k[request] : 0;
+  const float top_p = p.top_p ? p.top_p[request] : 1.0f;
+  const float min_p = p.min_p ? fminf(p.min_p[request], 1.0f) : 0.0f;
+  const bool none = e.bad || !(key_value(e.top) > -INFINITY), greedy = !(temp > 0.0f);
+  const bool by_k = k > 0 && k < p.vocab, by_p = top_p < 1.0f;
+  // log2(e) / t as a pair of floats: the quotient and, over t, what it leaves
+  constexpr float LOG2E_HI = 0x1.715476p+0f, LOG2E_LO = 0x1.4ae0cp-26f;
+  const float t = fmaxf(temp, 1e-30f), c_hi = LOG2E_HI / t;
+  st.top = key_value(e.top);
+  st.c_hi = c_hi;
+  st.c_lo = t < 1e30f ? (fmaf(-c_hi, t, LOG2E_HI) + LOG2E_LO) / t : 0.0f;
+  st.kind = none ? ROW_NONE : greedy ? ROW_GREEDY : by_k ? ROW_COUNT : by_p ? ROW_WEIGH : min_p > 0.0f ? ROW_REACH
+                                                                                                      : ROW_WHOLE;
+  st.from = st.end = SP_NONE;
+  const uint64_t least = min_p > 0.0f ? static_cast<uint64_t>(ceilf(min_p * 0x1p40f)) : 1;
+  st.least = least;
+  st.reach = least > 1 ? 40.01f - log2f(static_cast<float>(least)) : SP_NONE;   // (generously)
+  st.id = e.id;
+  st.far = 0;
+  st.listed = 0;
+  if (p.argmax) p.argmax[row] = none ? -1 : static_cast<int32_t>(e.id);
+  if (none) set_status(p.status, EAGLE_ERR_NUMERIC);
+  if ((none || greedy) && p.token) p.token[row] = none ? -1 : static_cast<int32_t>(e.id);
+}
+
+// Lists those of a warp's tokens that are nearer than `from` (SP_FAR at most); how many.
+__device__ __forceinline__ uint32_t list_near(const Row& r, const float (&z)[8], float from, float* list) {
+  const uint32_t before = (1u << (threadIdx.x & 31)) - 1;
   uint32_t n = 0;
-  for (int c = 0; c < p.cluster; ++c) {
-    const uint32_t x = dsmem_ld_u32(sm100::dsmem_addr(&s.listed, c));
-    if (c < static_cast<int>(rank)) at += x;
-    n += x;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const bool near = distance(r, z[i]) < from;
+    const uint32_t who = __ballot_sync(0xffffffffu, near);
+    if (near) list[n + __popc(who & before)] = z[i];
+    n += __popc(who);
   }
-  if (n <= SP_LIST && rank > 0)
-    for (uint32_t i = threadIdx.x; i < s.listed; i += SP_THREADS)
-      sm100::dsmem_st_u64(sm100::dsmem_addr(&s.list[at + i], 0), s.list[i]);
-  meet(p);
+  __syncwarp();
   return n;
+}
+
+// 2. The bins of every chunk; a row's last CTA finds the bin with the cut.
+template <typename T>
+__global__ void __launch_bounds__(SP_THREADS, 3) sample_bins_kernel(SampleParams p) {
+  __shared__ Pow2 pow2[64];
+  __shared__ float near_z[SP_WARPS][256];        // a warp's near tokens
+  // bins of every four warps: fewer than 4096 tokens' numbers, or weights in parts of 20 bits and 21, stay below 2^32
+  constexpr int COPIES = SP_WARPS / 4;
+  static_assert(SP_MAX_PIECES * SP_CHUNK / COPIES < 4096, "no sum passes 32 bits");
+  __shared__ uint32_t lo[COPIES][SP_ROW_BINS], hi[COPIES][SP_ROW_BINS];
+  __shared__ uint64_t sums[SP_WARPS];
+  LaunchStamp ls(p.stamp);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int at = blockIdx.x / p.groups, row = p.row0 + at;
+  const int chunk0 = (blockIdx.x - at * p.groups) * p.pieces, chunk1 = min(chunk0 + p.pieces, p.chunks);
+  fill_pow2(pow2);
+  for (int b = threadIdx.x; b < COPIES * SP_ROW_BINS; b += SP_THREADS) (&lo[0][0])[b] = (&hi[0][0])[b] = 0;
+  __syncthreads();
+  pdl_wait();
+  ls.waited();
+  pdl_trigger();
+  const int request = row / p.rows_each;
+  if (unused(p, row, request)) return;
+  SampleRow& st = p.state[at];
+  const T* logits = static_cast<const T*>(p.logits) + row * p.ld;
+  const bool wide = (reinterpret_cast<uintptr_t>(logits) & 15) == 0;
+  const int kind = st.kind;
+  if (kind != ROW_COUNT && kind != ROW_WEIGH) return;
+  const Row r = row_of(st);
+  uint32_t* my_lo = lo[warp % COPIES];
+  uint32_t* my_hi = hi[warp % COPIES];
+  uint64_t far_all = 0;
+#pragma unroll 1
+  for (int chunk = chunk0; chunk < chunk1; ++chunk) {
+    float z[8];
+    load_logits(logits, chunk_id(chunk), p.vocab, wide, z);
+    if (kind == ROW_COUNT) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float y = distance(r, z[i]);
+        if (y < SP_NONE) atomicAdd(&my_lo[static_cast<int>(y * SP_COUNT_BINS)], 1u);
+      }
+      continue;
+    }
+    uint32_t far = 0;                            // (256 of less than 2^18)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float y = distance(r, z[i]);
+      const uint32_t w = far_weight(r, z[i]);
+      if (y >= SP_FAR && y < SP_WEIGHED) {
+        const int bin = static_cast<int>(y * SP_WEIGHT_BINS);
+        atomicAdd(&my_lo[bin], w & 0xfffffu);
+        if (w >> 20) atomicAdd(&my_hi[bin], w >> 20);
+      }
+      far += y < SP_WEIGHED ? 0u : w;
+    }
+    far_all += __reduce_add_sync(0xffffffffu, far);
+    const uint32_t n = list_near(r, z, SP_FAR, near_z[warp]);
+#pragma unroll 1
+    for (uint32_t b = lane; b < n; b += 32) {
+      const float x = near_z[warp][b];
+      const uint64_t w = near_weight(pow2, r, x);
+      const int bin = static_cast<int>(distance(r, x) * SP_WEIGHT_BINS);
+      atomicAdd(&my_lo[bin], static_cast<uint32_t>(w) & 0xfffffu);
+      atomicAdd(&my_hi[bin], static_cast<uint32_t>(w >> 20));
+    }
+    __syncwarp();                                // (the list is read)
+  }
+  if (lane == 0) sums[warp] = far_all;
+  __syncthreads();
+  if (threadIdx.x < SP_ROW_BINS) {
+    const int b = threadIdx.x;
+    uint64_t in = 0;
+#pragma unroll
+    for (int i = 0; i < COPIES; ++i) in += (static_cast<uint64_t>(hi[i][b]) << 20) + lo[i][b];
+    if (in) add_u64(&st.bins[b], in);
+  } else if (warp == SP_WARPS - 1 && kind == ROW_WEIGH) {
+    const uint64_t all = warp_sum_u64(lane < SP_WARPS ? sums[lane] : 0);
+    if (lane == 0 && all) add_u64(&st.far, all);
+  }
+  static_assert(SP_ROW_BINS + 32 <= SP_THREADS, "the last warp has no bins");
+  if (!last_of_row(p.arrived + SAMPLE_ROWS + at, p.groups) || warp > 0) return;
+  uint64_t own[SP_LANE_BINS], mine = 0;
+#pragma unroll
+  for (int q = 0; q < SP_LANE_BINS; ++q) {
+    own[q] = ldcg_u64(&st.bins[lane * SP_LANE_BINS + q]);
+    mine += own[q];
+  }
+  uint64_t upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  const uint64_t binned = __shfl_sync(0xffffffffu, upto, 31);
+  const uint64_t need = kind == ROW_COUNT ? static_cast<uint64_t>(p.top_k[request])
+                                          : needed(p.top_p[request], binned + ldcg_u64(&st.far));
+  const bool both = kind == ROW_COUNT && p.top_p && p.top_p[request] < 1.0f;   // (then all k are listed)
+  uint64_t before = upto - mine;
+  if (lane == 0) {
+    st.need = need;
+    if (binned < need) {                         // all that have weight are kept, or the cut is behind the bins
+      st.before = kind == ROW_COUNT ? 0 : binned;
+      if (kind == ROW_WEIGH) st.from = SP_WEIGHED;
+      else if (both) st.from = 0.0f;
+    }
+  }
+  if (before < need && upto >= need) {           // in one of this lane's bins
+    int bin = -1;
+#pragma unroll
+    for (int q = 0; q < SP_LANE_BINS; ++q) {
+      if (bin < 0 && before + own[q] >= need) bin = lane * SP_LANE_BINS + q;
+      if (bin < 0) before += own[q];
+    }
+    const float bins = kind == ROW_COUNT ? SP_COUNT_BINS : SP_WEIGHT_BINS;
+    st.before = both ? 0 : before;
+    st.from = both ? 0.0f : static_cast<float>(bin) / bins;
+    st.end = static_cast<float>(bin + 1) / bins;
+  }
+}
+
+// 3. The weight of every chunk's tokens before the bin with the cut, and a list of that bin's tokens.
+template <typename T>
+__global__ void __launch_bounds__(SP_THREADS, 3) sample_list_kernel(SampleParams p) {
+  __shared__ Pow2 pow2[64];
+  __shared__ float near_z[SP_WARPS][256];
+  __shared__ uint64_t sums[SP_MAX_PIECES][SP_WARPS];
+  LaunchStamp ls(p.stamp);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int at = blockIdx.x / p.groups, row = p.row0 + at;
+  const int chunk0 = (blockIdx.x - at * p.groups) * p.pieces, chunk1 = min(chunk0 + p.pieces, p.chunks);
+  fill_pow2(pow2);
+  __syncthreads();
+  pdl_wait();
+  ls.waited();
+  pdl_trigger();
+  if (unused(p, row, row / p.rows_each)) return;
+  SampleRow& st = p.state[at];
+  if (st.kind < ROW_WHOLE) return;
+  const T* logits = static_cast<const T*>(p.logits) + row * p.ld;
+  const bool wide = (reinterpret_cast<uintptr_t>(logits) & 15) == 0;
+  const Row r = row_of(st);
+  const float from = st.from, end = st.end, reach = st.reach;
+  const uint64_t least = st.least;
+#pragma unroll 1
+  for (int chunk = chunk0; chunk < chunk1; ++chunk) {
+    const int id0 = chunk_id(chunk);
+    float z[8];
+    load_logits(logits, id0, p.vocab, wide, z);
+    uint64_t sum = 0;
+    if (from > SP_FAR && reach > SP_FAR) {       // far tokens too
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float y = distance(r, z[i]);
+        const uint32_t w = far_weight(r, z[i]);
+        sum += y >= SP_FAR && y < from && w >= least ? w : 0u;
+      }
+    }
+    const uint32_t n = list_near(r, z, fminf(fminf(from, reach), SP_FAR), near_z[warp]);
+#pragma unroll 1
+    for (uint32_t b = lane; b < n; b += 32) {
+      const uint64_t w = near_weight(pow2, r, near_z[warp][b]);
+      sum += w >= least ? w : 0;
+    }
+    if (__any_sync(0xffffffffu, sum != 0)) sum = warp_sum_u64(sum);   // (the list is read)
+    if (lane == 0) sums[chunk - chunk0][warp] = sum;
+    uint32_t in = 0;                             // a bit a token
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float y = distance(r, z[i]);
+      in |= y >= from && y < end ? 1u << i : 0u;
+    }
+    if (!__any_sync(0xffffffffu, in != 0)) continue;
+    uint32_t upto = static_cast<uint32_t>(__popc(in));
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    uint32_t to = 0;
+    if (lane == 31) to = atomicAdd(&st.listed, upto);
+    to = __shfl_sync(0xffffffffu, to, 31) + upto - static_cast<uint32_t>(__popc(in));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (in >> i & 1u) {
+        if (to < SP_LIST)
+          st.list[to] = static_cast<uint64_t>(order_key(z[i])) << 32 | (0xffffffffu - static_cast<uint32_t>(id0 + i));
+        ++to;
+      }
+    }
+  }
+  __syncthreads();
+  for (int chunk = chunk0 + warp; chunk < chunk1; chunk += SP_WARPS) {
+    const uint64_t sum = warp_sum_u64(lane < SP_WARPS ? sums[chunk - chunk0][lane] : 0);
+    if (lane == 0) st.total[chunk] = sum;
+  }
+}
+
+struct SampleShared {
+  Pow2 pow2[64];
+  // bins of a bin: how many tokens, and their weight in two words
+  uint32_t count[SP_BINS], lo[SP_BINS], hi[SP_BINS];
+  uint64_t list[SP_SORT];        // key << 32 | ~id
+  uint32_t total_lo[SP_MAX_CHUNKS], total_hi[SP_MAX_CHUNKS];   // weight of each chunk, in two words
+  BlockScan scan;
+  uint64_t sum;
+  uint32_t listed;
+  uint32_t digit, in_digit;      // where the cut falls, and how many tokens fall there
+  uint64_t before;               // number or weight before it
+  uint32_t cut_key, cut_id;
+};
+
+// Adds to a sum in two words of shared memory (its atomic additions are of 32 bits).
+__device__ __forceinline__ void add_words(uint32_t& lo, uint32_t& hi, uint64_t w) {
+  const uint32_t l = static_cast<uint32_t>(w), old = atomicAdd(&lo, l);
+  const uint32_t h = static_cast<uint32_t>(w >> 32) + (old + l < old ? 1u : 0u);
+  if (h) atomicAdd(&hi, h);
 }
 
 // Sorts the threads' e, the first n of them other than 0, largest first: a bitonic network, by shuffles where partners
@@ -432,610 +660,322 @@ __device__ __forceinline__ void sort_threads(SampleShared& s, int n, uint64_t& e
   }
 }
 
-// Sorts the n <= SP_LIST tokens of this CTA's list, largest first: thread t gets the t-th and its weight, and the weight
-// before it.
-__device__ __forceinline__ void sort_list(SampleShared& s, const Row& r, int n, uint64_t& e, uint64_t& w, uint64_t& before) {
-  e = static_cast<int>(threadIdx.x) < n ? s.list[threadIdx.x] : 0;
-  sort_threads(s, n, e);
-  w = e ? weight(s, r, key_value(static_cast<uint32_t>(e >> 32))) : 0;
-  uint32_t none;
-  block_before(s, 0, w, none, before);
-}
+__device__ __forceinline__ float z_of(uint64_t e) { return key_value(static_cast<uint32_t>(e >> 32)); }
+__device__ __forceinline__ uint32_t id_of(uint64_t e) { return 0xffffffffu - static_cast<uint32_t>(e); }
 
-__device__ __forceinline__ void tell_cut(const SampleParams& p, SampleShared& s, uint64_t e) {
-  st_all_u32(p, &s.cut_key, static_cast<uint32_t>(e >> 32));
-  st_all_u32(p, &s.cut_id, 0xffffffffu - static_cast<uint32_t>(e));
-}
-
-// ceil(p S), at least 1 and at most S < 2^60: the 24 bits of p times S, shifted down.
-__device__ __forceinline__ uint64_t needed(float top_p, uint64_t all) {
-  if (!(top_p > 0.0f)) return 1;
-  const uint32_t bits = __float_as_uint(top_p), e = bits >> 23;
-  const uint64_t m = e ? (bits & 0x7fffffu) | 0x800000u : bits & 0x7fffffu;
-  const int sh = 150 - static_cast<int>(e ? e : 1u);             // top_p = m 2^-sh, sh >= 24
-  const uint64_t lo = m * all, hi = __umul64hi(m, all);
-  uint64_t need, rest;
-  if (sh < 64) {
-    need = (hi << (64 - sh)) | (lo >> sh);
-    rest = lo & ((1ull << sh) - 1);
-  } else {
-    need = sh < 128 ? hi >> (sh - 64) : 0;
-    rest = lo | hi;                              // (need is 0 or small: one more at most)
-    if (sh < 128 && sh > 64) rest = lo | (hi & ((1ull << (sh - 64)) - 1));
-    if (sh == 64) rest = lo;
+// Whether the cut keeps a token.
+struct Cut {
+  float z;
+  uint32_t id;
+  __device__ __forceinline__ Cut(uint32_t key, uint32_t i)   // (key 0: it keeps all)
+      : z(key ? key_value(key) : -INFINITY), id(key ? i : 0xffffffffu) {}
+  __device__ __forceinline__ bool keeps(float x, int i) const {
+    return x > z || (x == z && static_cast<uint32_t>(i) <= id);
   }
-  need += rest ? 1 : 0;
-  return need < 1 ? 1 : min(need, all);
-}
+};
 
-// The cut in the part of the row at distances r.from to r.to, by counting: where the number (by_weight false) or the
-// weight of the tokens, on top of those before the part, reaches `need`.  cut_key and cut_id of every CTA; cut_key 0 where
-// it never does.
-__device__ __noinline__ void count_cut(const SampleParams& p, SampleShared& s, Row r, const Tokens tk, bool by_weight,
-                                       uint64_t need, uint32_t before_n, uint64_t before_w, uint32_t rank) {
-  uint32_t bin = 0, prefix = 0, there = 0;
-  int level = 0;
-  r.bins = static_cast<float>(SP_BINS) / (r.to - r.from);
-  const bool dense = r.to <= SP_FAR;
-  auto chosen = [&](float z) {
-    const float y = distance(r, z);
-    if (!(y < r.to) || y < r.from) return false;
-    if (level == 0) return true;
-    if (bin_of(r, z) != bin) return false;
-    return level == 1 || order_key(z) >> key_shift(level - 1) == prefix;
-  };
-  do {
-    for (int b = threadIdx.x; b < SP_BINS; b += SP_THREADS) s.count[b] = s.lo[b] = s.hi[b] = 0;
-    __syncthreads();
-    tk.each(dense, s.near_n, [&](int, float z, bool there) {
-      if (!there || !chosen(z)) return;
-      const uint32_t d = digit_of(r, z, level);
-      atomicAdd(&s.count[d], 1u);
-      if (by_weight) {
-        const uint64_t wi = weight(s, r, z);
-        const uint32_t l = static_cast<uint32_t>(wi), old = atomicAdd(&s.lo[d], l);
-        const uint32_t h = static_cast<uint32_t>(wi >> 32) + (old + l < old ? 1u : 0u);
-        if (h) atomicAdd(&s.hi[d], h);
-      }
-    });
-    sum_bins(p, s, by_weight, rank);
-    // the digits in falling order of z: bins as they are, bits from the largest down
-    scan_bins(p, s, by_weight, level == 0, need, before_n, before_w, rank);
-    there = s.in_digit;
-    if (there == 0) {
-      if (threadIdx.x == 0) s.cut_key = 0;
-      meet(p);
+// A row's tokens, or those of its list, where that holds all that are asked for.
+template <typename T>
+struct Tokens {
+  const T* logits;
+  int vocab;
+  const uint64_t* list;
+  uint32_t listed;               // 0: the row's
+  // Calls f(id, z) for each.
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+    if (listed) {
+#pragma unroll 1
+      for (uint32_t i = threadIdx.x; i < listed; i += SP_THREADS) f(static_cast<int>(id_of(list[i])), z_of(list[i]));
       return;
     }
-    before_n = s.before_n;
-    before_w = s.before_w;
+    const bool wide = (reinterpret_cast<uintptr_t>(logits) & 15) == 0;
+#pragma unroll 1
+    for (int chunk = 0; chunk * SP_CHUNK < vocab; ++chunk) {
+      float z[8];
+      load_logits(logits, chunk_id(chunk), vocab, wide, z);
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) {
+        const float x = z[0];
+        f(chunk_id(chunk) + i, x);
+#pragma unroll
+        for (int q = 0; q < 7; ++q) z[q] = z[q + 1];
+      }
+    }
+  }
+};
+
+// The cut among the tokens at distances from `from` to `to`, by going over them: where their number (by_weight false) or
+// weight, on top of that before them, reaches `need`.  s.cut_*; the key is 0 where it never does.
+template <typename T>
+__device__ __noinline__ void find_cut(SampleShared& s, const Row r, const Tokens<T> tk, float from, float to,
+                                      bool by_weight, uint64_t need, uint64_t before) {
+  const float bins = static_cast<float>(SP_BINS) / (to - from);
+  const int t = threadIdx.x;
+  uint32_t bin = 0, prefix = 0, there = 0;
+  int level = 0;                                 // the bin, then 10, 10, 10 and 2 bits of the logit's order
+  auto bin_of = [&](float z) {
+    return static_cast<uint32_t>(fminf((distance(r, z) - from) * bins, static_cast<float>(SP_BINS - 1)));
+  };
+  auto shift = [](int l) { return l >= 4 ? 0 : 32 - 10 * l; };
+  auto chosen = [&](float z) {
+    const float y = distance(r, z);
+    if (!(y < to) || y < from) return false;
+    if (level == 0) return true;
+    if (bin_of(z) != bin) return false;
+    return level == 1 || order_key(z) >> shift(level - 1) == prefix;
+  };
+  do {
+    for (int b = t; b < SP_BINS; b += SP_THREADS) s.count[b] = s.lo[b] = s.hi[b] = 0;
+    if (t == 0) s.in_digit = 0;
+    __syncthreads();
+    tk.each([&](int, float z) {
+      if (!chosen(z)) return;
+      const uint32_t d = level == 0 ? bin_of(z) : (order_key(z) >> shift(level)) & (level == 4 ? 3u : SP_BINS - 1u);
+      atomicAdd(&s.count[d], 1u);
+      if (by_weight) add_words(s.lo[d], s.hi[d], weight(s.pow2, r, z));
+    });
+    __syncthreads();
+    // the digits in falling order of z: bins as they are, bits from the largest down
+    uint64_t own[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int b = level == 0 ? 2 * t + q : SP_BINS - 1 - 2 * t - q;
+      own[q] = by_weight ? static_cast<uint64_t>(s.hi[b]) << 32 | s.lo[b] : s.count[b];
+    }
+    uint64_t sofar = before + block_before(s.scan, own[0] + own[1]);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      if (sofar < need && sofar + own[q] >= need) {
+        const int b = level == 0 ? 2 * t + q : SP_BINS - 1 - 2 * t - q;
+        s.digit = b;
+        s.in_digit = s.count[b];
+        s.before = sofar;
+      }
+      sofar += own[q];
+    }
+    __syncthreads();
+    there = s.in_digit;
+    if (there == 0) {
+      if (t == 0) s.cut_key = 0;
+      __syncthreads();
+      return;
+    }
+    before = s.before;
     if (level == 0) bin = s.digit;
     else prefix = level == 4 ? prefix << 2 | s.digit : prefix << 10 | s.digit;
     ++level;
-    meet(p);                                     // the state is read before the next pass writes it
-  } while (there > SP_LIST && level < 5);
-  if (there <= SP_LIST) {
-    gather(p, s, tk, dense, rank, chosen);
-    if (rank == 0) {
-      uint64_t e, w, before;
-      sort_list(s, r, static_cast<int>(there), e, w, before);
-      before += before_w;
-      if (e && (by_weight ? before < need && before + w >= need : before_n + threadIdx.x + 1 == need)) tell_cut(p, s, e);
-    }
-    meet(p);
+    __syncthreads();                             // the state is read before the next pass writes it
+  } while (there > SP_SORT && level < 5);
+  if (there <= SP_SORT) {
+    if (t == 0) s.listed = 0;
+    __syncthreads();
+    tk.each([&](int id, float z) {
+      if (chosen(z))
+        s.list[atomicAdd(&s.listed, 1u)] =
+            static_cast<uint64_t>(order_key(z)) << 32 | (0xffffffffu - static_cast<uint32_t>(id));
+    });
+    __syncthreads();
+    uint64_t e = t < static_cast<int>(there) ? s.list[t] : 0;
+    sort_threads(s, static_cast<int>(there), e);
+    const uint64_t w = !e ? 0 : by_weight ? weight(s.pow2, r, z_of(e)) : 1;
+    const uint64_t upto = before + block_before(s.scan, w);
+    if (upto < need && upto + w >= need) s.cut_key = static_cast<uint32_t>(e >> 32), s.cut_id = id_of(e);
+    __syncthreads();
     return;
   }
   // Tokens of one value, more than the list takes: the cut is the m-th of them by id.
-  const uint64_t one = weight(s, r, key_value(prefix));
-  const uint32_t m = by_weight ? static_cast<uint32_t>((need - before_w + one - 1) / one)
-                               : static_cast<uint32_t>(need) - before_n;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t mine = 0;
+  const uint64_t one = by_weight ? weight(s.pow2, r, key_value(prefix)) : 1, m = (need - before + one - 1) / one;
+  uint64_t sofar = 0;
+  const bool wide = (reinterpret_cast<uintptr_t>(tk.logits) & 15) == 0;
 #pragma unroll 1
-  for (int i = 0; i < tk.n; ++i) mine += chosen(tk.z(i)) ? 1u : 0u;
-  const uint32_t in_warp = __reduce_add_sync(0xffffffffu, mine);
-  if (lane == 0) s.scan_n[warp] = in_warp;
-  __syncthreads();
-  uint32_t before = 0, in_cta = 0;
-  for (int i = 0; i < SP_WARPS; ++i) {
-    if (i < warp) before += s.scan_n[i];
-    in_cta += s.scan_n[i];
-  }
-  if (threadIdx.x == 0) st_all_u32(p, &s.tie[rank], in_cta);
-  meet(p);
-  for (uint32_t c = 0; c < rank; ++c) before += s.tie[c];
-  if (before < m && before + in_warp >= m) {     // in this warp: its runs of 256 ids, then its lanes, then a lane's eight
-#pragma unroll 1
-    for (int j = 0; j < tk.n / 8; ++j) {
-      uint32_t bits = 0;
-#pragma unroll 1
-      for (int i = 0; i < 8; ++i)
-        if (chosen(tk.z(8 * j + i))) bits |= 1u << i;
-      uint32_t c = static_cast<uint32_t>(__popc(bits)), upto = c;
+  for (int chunk = 0; chunk * SP_CHUNK < tk.vocab && sofar < m; ++chunk) {
+    float z[8];
+    load_logits(tk.logits, chunk_id(chunk), tk.vocab, wide, z);
+    uint32_t in = 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t x = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += x;
+    for (int i = 0; i < 8; ++i) in |= chosen(z[i]) ? 1u << i : 0u;
+    uint64_t k = sofar + block_before(s.scan, __popc(in));
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (in >> i & 1u) {
+        if (++k == m) s.cut_key = prefix, s.cut_id = static_cast<uint32_t>(chunk_id(chunk) + i);
       }
-      uint32_t k = before + upto - c;
-#pragma unroll 1
-      for (int i = 0; i < 8; ++i)
-        if (bits >> i & 1u) {
-          if (++k == m)
-            tell_cut(p, s, static_cast<uint64_t>(prefix) << 32 | (0xffffffffu - static_cast<uint32_t>(tk.id(8 * j + i))));
-        }
-      before += __shfl_sync(0xffffffffu, upto, 31);
-    }
-  }
-  meet(p);
-}
-
-// Gathers the tokens that may be among the row's k largest into the first CTA's list, by a thread's largest, `mine`; how
-// many there are (0: too many, or too few).  With few tokens to keep each CTA bounds them by its own threads' largest
-// (up to k tokens and some more a CTA are gathered), else all do together.
-__device__ __forceinline__ uint32_t gather_top(const SampleParams& p, SampleShared& s, Row r, const Tokens& tk, float mine,
-                                               uint32_t k, uint32_t rank) {
-  r.from = 0.0f;
-  r.to = 41.0f;
-  r.bins = static_cast<float>(SP_BINS) / 41.0f;
-  for (int b = threadIdx.x; b < SP_BINS; b += SP_THREADS) s.count[b] = 0;
-  __syncthreads();
-  if (distance(r, mine) < r.to) atomicAdd(&s.count[bin_of(r, mine)], 1u);
-  if (k * static_cast<uint32_t>(p.cluster) <= SP_LIST / 2) {
-    if (threadIdx.x == 0) s.digit = SP_BINS - 1;   // fewer than k: all that have weight
+    if (t == SP_THREADS - 1) s.sum = k;
     __syncthreads();
-    const uint2 two = *reinterpret_cast<const uint2*>(&s.count[2 * threadIdx.x]);
-    static_assert(SP_BINS == 2 * SP_THREADS, "two bins a thread");
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t upto = two.x + two.y;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t x = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += x;
-    }
-    if (lane == 31) s.scan_n[warp] = upto;
+    sofar = s.sum;
     __syncthreads();
-    uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? s.scan_n[lane] : 0u);
-    before += upto - two.x - two.y;
-    if (before < k && before + two.x >= k) s.digit = 2 * threadIdx.x;
-    else if (before + two.x < k && before + two.x + two.y >= k) s.digit = 2 * threadIdx.x + 1;
-    __syncthreads();
-  } else {
-    sum_bins(p, s, false, rank);
-    scan_bins(p, s, false, true, k, 0, 0, rank);
-    if (s.in_digit == 0) {
-      meet(p);                                   // (the state is read)
-      return 0;
-    }
   }
-  const float end = static_cast<float>(s.digit + 1);
-  const uint32_t n = gather(p, s, tk, false, rank, [&](float z) { return distance(r, z) < 41.0f && distance(r, z) * r.bins < end; });
-  return n >= k && n <= SP_LIST ? n : 0;
 }
 
-// The cut of top-p: where the weight reaches `need` (0: top_p of the weight of all).
-// far: the weight of this thread's other than near tokens (32 of 2^23 at most).
-__device__ __forceinline__ void top_p_cut(const SampleParams& p, SampleShared& s, Row r, const Tokens& tk, uint32_t far,
-                                          uint64_t need, float top_p, uint32_t rank) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t n[SP_PARTS] = {0, 0, 0, 0};
-  uint64_t w[SP_PARTS] = {0, 0, 0, 0};
-  tk.each(true, s.near_n, [&](int, float z, bool there) {
-    const float y = there ? distance(r, z) : 100.0f;
-    const uint64_t x = near_weight(s, r, z);
-#pragma unroll
-    for (int c = 0; c < SP_PARTS; ++c)
-      if (y < part_reach(c)) w[c] += x, ++n[c];
-  });
-#pragma unroll
-  for (int c = 0; c < SP_PARTS; ++c) {
-    n[c] = __reduce_add_sync(0xffffffffu, n[c]);
-    w[c] = n[c] ? warp_sum_u64(w[c]) : 0;
-  }
-  const uint64_t far_all = warp_sum_u64(far);
-  if (lane == 0) {
-    Parts& x = s.warp_parts[warp];
-#pragma unroll
-    for (int c = 0; c < SP_PARTS; ++c) x.weight[c] = w[c], x.count[c] = n[c];
-    x.weight[SP_PARTS] = w[SP_PARTS - 1] + far_all;
-    x.count[SP_PARTS] = 0;
-  }
-  __syncthreads();
-  if (threadIdx.x <= SP_PARTS) {                 // a thread a part, told to every CTA
-    const int c = threadIdx.x;
-    uint64_t a = 0;
-    uint32_t b = 0;
-#pragma unroll
-    for (int i = 0; i < SP_WARPS; ++i) a += s.warp_parts[i].weight[c], b += s.warp_parts[i].count[c];
-    st_all_u64(p, &s.parts[rank].weight[c], a);
-    st_all_u32(p, &s.parts[rank].count[c], b);
-  }
-  meet(p);
-  // the first part whose weight, with those before it, reaches what is needed: a lane a part
-  uint64_t a = 0;
-  uint32_t b = 0;
-  if (lane <= SP_PARTS)
-    for (int c = 0; c < p.cluster; ++c) a += s.parts[c].weight[lane], b += s.parts[c].count[lane];
-  if (need == 0) need = needed(top_p, __shfl_sync(0xffffffffu, a, SP_PARTS));
-  const uint32_t enough = __ballot_sync(0xffffffffu, lane < SP_PARTS && a >= need) | 1u << SP_PARTS;
-  const int part = __ffs(enough) - 1, last = max(part - 1, 0);
-  const uint64_t before_w = part ? __shfl_sync(0xffffffffu, a, last) : 0;
-  const uint32_t before_n = part ? __shfl_sync(0xffffffffu, b, last) : 0;
-  const uint32_t upto = __shfl_sync(0xffffffffu, b, part);
-  const uint32_t there = part < SP_PARTS ? upto - before_n : 0xffffffffu;
-  r.from = part ? part_reach(last) : 0.0f;
-  r.to = part_reach(part);
-  if (there > SP_LIST) {
-    count_cut(p, s, r, tk, true, need, before_n, before_w, rank);
-    return;
-  }
-  gather(p, s, tk, true, rank, [&](float z) {
-    const float y = distance(r, z);
-    return y < r.to && y >= r.from;
-  });
-  if (rank == 0) {
-    uint64_t e, we, before;
-    sort_list(s, r, static_cast<int>(there), e, we, before);
-    before += before_w;
-    if (e && before < need && before + we >= need) tell_cut(p, s, e);
-  }
-  meet(p);
-}
-
-__device__ __forceinline__ void store_probs(float* row, int id, int vocab, bool wide, const float (&v)[8]) {
-  if (wide && id + 8 <= vocab) {
-    *reinterpret_cast<float4*>(row + id) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4*>(row + id + 4) = make_float4(v[4], v[5], v[6], v[7]);
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (id + i < vocab) row[id + i] = v[i];
-}
-
+// 4. A row's cut, the weight of each chunk up to it, and the draw.
 template <typename T>
-__global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SampleParams p) {
-  extern __shared__ __align__(16) uint8_t raw_shared[];
-  SampleShared& s = *reinterpret_cast<SampleShared*>(raw_shared);
+__global__ void __launch_bounds__(SP_THREADS, 2) sample_draw_kernel(SampleParams p) {
+  __shared__ SampleShared s;
   LaunchStamp ls(p.stamp);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row = blockIdx.x / p.cluster;
-  const uint32_t rank = p.cluster > 1 ? sm100::cluster_rank() : 0;
-  if (threadIdx.x < 64) {
-    const uint64_t v = kPow2[threadIdx.x];
-    const float h = static_cast<float>(v);
-    s.pow2[threadIdx.x] =
-        Pow2{v, h * 0x1p-46f, static_cast<float>(static_cast<int64_t>(v) - static_cast<int64_t>(h)) * 0x1p-46f};
-  }
-  if (threadIdx.x == 0) s.near_n = 0;
+  const int t = threadIdx.x, lane = t & 31;
+  const int row = p.row0 + blockIdx.x;
+  fill_pow2(s.pow2);
+  if (t == 0) s.cut_key = s.cut_id = 0;
   pdl_wait();
   ls.waited();
   pdl_trigger();
   const int request = row / p.rows_each;
-  if (p.rows_used && row - request * p.rows_each >= p.rows_used[request]) return;
-  if (p.cluster > 1) sm100::cluster_arrive_relaxed();   // (the others are there before anything is written to them)
-  const float temp = p.temperature ? p.temperature[request] : 1.0f;
-  const int k = p.top_k ? p.top_k[request] : 0;
-  const float top_p = p.top_p ? p.top_p[request] : 1.0f;
-  const float min_p = p.min_p ? fminf(p.min_p[request], 1.0f) : 0.0f;
-  const uint32_t u = p.token ? p.u[row] : 0;
-  const bool greedy = !(temp > 0.0f);
-
+  if (unused(p, row, request)) return;
+  SampleRow& st = p.state[blockIdx.x];
+  const int kind = st.kind;
+  if (kind < ROW_WHOLE) return;
   const T* logits = static_cast<const T*>(p.logits) + row * p.ld;
-  const bool wide = (reinterpret_cast<uintptr_t>(logits) & 15) == 0;
-  Tokens tk;
-  tk.all = reinterpret_cast<float*>(raw_shared + sizeof(SampleShared));
-  tk.n = p.each;
-  tk.near = reinterpret_cast<uint16_t*>(tk.all + tk.n * SP_THREADS);
-  tk.first = static_cast<int>(rank) * tk.n * SP_THREADS;
-  const int id0 = tk.base(threadIdx.x);
-  // the largest logit, and whether any is NaN or +inf
-  float top = -INFINITY;                         // NaN if any is
-#pragma unroll 2
-  for (int j = 0; j < tk.n / 8; ++j) {
-    float z[8];
-    load_logits(logits, id0 + j * 256, p.vocab, wide, z);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      tk.z(8 * j + i) = z[i];
-      asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(z[i]));
-    }
+  const Row r = row_of(st);
+  const uint64_t least = st.least, need = st.need, before = st.before;
+  const float from = st.from, end = st.end;
+  const uint32_t n = st.listed;
+  const float top_p = kind == ROW_COUNT && p.top_p ? p.top_p[request] : 1.0f;
+  const uint32_t u = p.token ? p.u[row] : 0;
+  if (t < SP_MAX_CHUNKS) {
+    const uint64_t sum = t < p.chunks ? st.total[t] : 0;
+    s.total_lo[t] = static_cast<uint32_t>(sum);
+    s.total_hi[t] = static_cast<uint32_t>(sum >> 32);
   }
-  {
-    const uint32_t key = order_key(top), warp_top = __reduce_max_sync(0xffffffffu, key);
-    uint32_t id = 0xffffffffu;
-    if (p.argmax || greedy) {
-      if (key == warp_top) {
-#pragma unroll 1
-        for (int i = tk.n - 1; i >= 0; --i)
-          if (tk.z(i) == top) id = static_cast<uint32_t>(tk.id(i));
-      }
-      id = __reduce_min_sync(0xffffffffu, id);
-    }
-    const bool any = __any_sync(0xffffffffu, !(top < INFINITY));
-    if (lane == 0) s.warp_extent[warp] = Extent{warp_top, id, any ? 1u : 0u, 0u};
-  }
+  uint64_t e = t < static_cast<int>(min(n, static_cast<uint32_t>(SP_SORT))) ? st.list[t] : 0;
   __syncthreads();
-  if (warp == 0) {
-    Extent e = s.warp_extent[lane % SP_WARPS];
-    const uint32_t t = __reduce_max_sync(0xffffffffu, e.top);
-    e.id = __reduce_min_sync(0xffffffffu, e.top == t ? e.id : 0xffffffffu);
-    e.bad = __reduce_or_sync(0xffffffffu, e.bad);
-    if (p.cluster > 1) sm100::cluster_wait();
-    if (lane < p.cluster) {
-      const uint32_t a = sm100::dsmem_addr(&s.extent[rank], lane);
-      sm100::dsmem_st_u64(a, t | (static_cast<uint64_t>(e.id) << 32));
-      sm100::dsmem_st_u64(a + 8, e.bad);
+  if (n > SP_SORT) {
+    const Tokens<T> tk{logits, p.vocab, st.list, n <= SP_LIST ? n : 0};
+    find_cut(s, r, tk, from, end, kind == ROW_WEIGH, need, before);
+    if (top_p < 1.0f) {                          // of the weight of those k
+      const Cut cut(s.cut_key, s.cut_id);
+      uint64_t mine = 0;
+      tk.each([&](int id, float z) {
+        if (cut.keeps(z, id)) mine += weight(s.pow2, r, z);
+      });
+      const uint64_t upto = block_before(s.scan, mine) + mine;
+      if (t == SP_THREADS - 1) s.sum = upto;
+      __syncthreads();
+      find_cut(s, r, tk, 0.0f, SP_NONE, true, needed(top_p, s.sum), 0);
     }
-    __syncwarp();
-  } else if (p.cluster > 1) {
-    sm100::cluster_wait();
-  }
-  meet(p);
-  Extent all{0, 0xffffffffu, 0, 0};
-  for (int c = 0; c < p.cluster; ++c) {
-    const Extent e = s.extent[c];
-    if (e.top > all.top) all.top = e.top, all.id = e.id;
-    all.bad |= e.bad;
-  }
-  const float zmax = key_value(all.top);
-  const bool none = all.bad || !(zmax > -INFINITY);
-  float* probs = p.probs ? p.probs + row * p.ld_probs : nullptr;
-  const bool wide_out = (reinterpret_cast<uintptr_t>(probs) & 15) == 0;
-  if (threadIdx.x == 0 && rank == 0) {
-    if (p.argmax) p.argmax[row] = none ? -1 : static_cast<int32_t>(all.id);
-    if (none) set_status(p.status, EAGLE_ERR_NUMERIC);
-    if ((none || greedy) && p.token) p.token[row] = none ? -1 : static_cast<int32_t>(all.id);
-  }
-  auto write_probs = [&]() {
-#pragma unroll 1
-    for (int j = 0; j < tk.n / 8; ++j) {
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = tk.z(8 * j + i);
-      store_probs(probs, id0 + j * 256, p.vocab, wide_out, v);
-    }
-  };
-  if (none || greedy) {
-    if (probs) {
-#pragma unroll 4
-      for (int i = 0; i < tk.n; ++i) tk.z(i) = !none && static_cast<uint32_t>(tk.id(i)) == all.id ? 1.0f : 0.0f;
-      write_probs();
-    }
-    return;
-  }
-  if (!p.token && !probs) return;
-
-  Row r;
-  r.top = zmax;
-  {
-    // log2(e) / t as a pair of floats: the quotient and, over t, what it leaves
-    constexpr float LOG2E_HI = 0x1.715476p+0f, LOG2E_LO = 0x1.4ae0cp-26f;
-    const float t = fmaxf(temp, 1e-30f);
-    r.c_hi = LOG2E_HI / t;
-    r.c_lo = (fmaf(-r.c_hi, t, LOG2E_HI) + LOG2E_LO) / t;
-    if (!(t < 1e30f)) r.c_lo = 0.0f;
-  }
-  r.from = r.to = r.bins = 0.0f;
-  const bool by_k = k > 0 && k < p.vocab;
-  float cut_z = -INFINITY;
-  uint32_t cut_id = 0xffffffffu;
-  const uint64_t least = min_p > 0.0f ? static_cast<uint64_t>(ceilf(min_p * 0x1p40f)) : 1;
-  // the weights of tokens i to i + 3 where the cut (and `floor`) keeps them
-  auto kept4 = [&](int i, uint64_t floor, uint64_t (&w)[4]) {
-    float z[4];
-    bool in[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      z[q] = tk.z(i + q);
-      in[q] = z[q] > cut_z || (z[q] == cut_z && static_cast<uint32_t>(tk.id(i + q)) <= cut_id);
-    }
-    w[0] = w[1] = w[2] = w[3] = 0;
-    if (!__any_sync(0xffffffffu, in[0] || in[1] || in[2] || in[3])) return;
-    weights4(s, r, z, in, w);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) w[q] = w[q] >= floor ? w[q] : 0;
-  };
-  // the weight of what is kept: before this warp, in it, and in the row
-  uint64_t before = 0, in_warp = 0, W = 0;
-  auto add_up = [&]() {                          // from s.warp_total
-    __syncthreads();
-    uint64_t in_cta = 0;
-    before = 0;
-#pragma unroll
-    for (int i = 0; i < SP_WARPS; ++i) {
-      const uint64_t t = s.warp_total[i];
-      if (i < warp) before += t;
-      in_cta += t;
-    }
-    in_warp = s.warp_total[warp];
-    if (threadIdx.x == 0) st_all_u64(p, &s.total[rank], in_cta);
-    meet(p);
-    W = 0;
-    for (int c = 0; c < p.cluster; ++c) {
-      if (c < static_cast<int>(rank)) before += s.total[c];
-      W += s.total[c];
-    }
-  };
-  auto take_cut = [&]() {
-    if (s.cut_key != 0) {
-      cut_z = key_value(s.cut_key);
-      cut_id = s.cut_id;
-    }
-  };
-  if (by_k) {
-    const uint32_t n = gather_top(p, s, r, tk, top, static_cast<uint32_t>(k), rank);
-    if (n) {                                     // the first CTA has all that is kept
-      if (probs) {
-#pragma unroll 1
-        for (int j = 0; j < tk.n / 8; ++j) {
-          const float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-          store_probs(probs, id0 + j * 256, p.vocab, wide_out, v);
-        }
-        meet(p);
+    const Cut cut(s.cut_key, s.cut_id);
+    tk.each([&](int id, float z) {
+      const float y = distance(r, z);
+      if (y >= from && y < SP_NONE && cut.keeps(z, id)) {
+        const uint64_t w = weight(s.pow2, r, z);
+        if (w && w >= least) add_words(s.total_lo[id / SP_CHUNK], s.total_hi[id / SP_CHUNK], w);
       }
-      if (rank > 0) return;
-      const int t = threadIdx.x;
-      uint64_t e, w, before_t;
-      sort_list(s, r, static_cast<int>(n), e, w, before_t);
-      bool in = t < k;
-      if (top_p < 1.0f) {
-        if (t + 1 == k) s.need_w = needed(top_p, before_t + w);   // of the weight up to the k-th
+    });
+  } else if (n > 0) {
+    sort_threads(s, static_cast<int>(n), e);
+    const uint64_t w = e ? weight(s.pow2, r, z_of(e)) : 0;
+    bool in = e != 0;
+    if (kind == ROW_COUNT) in = in && before + t < need;
+    if (kind == ROW_WEIGH || top_p < 1.0f) {     // the weight before each
+      uint64_t sofar = block_before(s.scan, in ? w : 0), enough = need;
+      if (kind == ROW_COUNT) {
+        if (t == SP_THREADS - 1) s.sum = sofar + (in ? w : 0);
         __syncthreads();
-        in = in && before_t < s.need_w;
+        enough = needed(top_p, s.sum);
+      } else {
+        sofar += before;
       }
-      in = in && w >= least;
-      // those kept by their ids
-      s.kept[t] = in ? w : 0;
-      e = in ? (e << 32) | static_cast<uint32_t>(SP_THREADS - 1 - t) : 0;
-      __syncthreads();
-      sort_threads(s, static_cast<int>(n), e);
-      w = e ? s.kept[SP_THREADS - 1 - static_cast<uint32_t>(e)] : 0;
-      uint32_t none;
-      __syncthreads();
-      block_before(s, 0, w, none, before_t);
-      if (t == SP_THREADS - 1) s.need_w = before_t + w;
-      __syncthreads();
-      const uint64_t W = s.need_w, at = scale_uniform(u, W);
-      if (w) {
-        const int token = static_cast<int>(0xffffffffu - static_cast<uint32_t>(e >> 32));
-        if (p.token && before_t <= at && at < before_t + w) p.token[row] = token;
-        if (probs) probs[token] = static_cast<float>(w) * (1.0f / static_cast<float>(W));
-      }
-      return;
+      in = in && sofar < enough;
     }
-  }
-  // the near tokens' places; the weight of this thread's others where all may count
-  bool by_p = top_p < 1.0f;
-  const bool want_far = !by_k && (by_p || least <= 1);
-  uint32_t far = 0;
-#pragma unroll 4
-  for (int i = 0; i < tk.n; ++i) {
-    const float z = tk.z(i);
-    const bool near = distance(r, z) < SP_FAR;
-    const uint32_t who = __ballot_sync(0xffffffffu, near);
-    if (want_far) far += near ? 0u : far_weight(r, z);
-    if (who) {
-      uint32_t at = 0;
-      if (lane == 0) at = atomicAdd(&s.near_n, static_cast<uint32_t>(__popc(who)));
-      at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1));
-      if (near) tk.near[at] = static_cast<uint16_t>(i * SP_THREADS + threadIdx.x);
-    }
+    // the last of those that are in (they are the first)
+    const int kept = __syncthreads_count(in);
+    if (t == kept - 1) s.cut_key = static_cast<uint32_t>(e >> 32), s.cut_id = id_of(e);
+    if (in && w >= least) add_words(s.total_lo[id_of(e) / SP_CHUNK], s.total_hi[id_of(e) / SP_CHUNK], w);
   }
   __syncthreads();
-  // whether the cut keeps the token at a place, and its weight; a token too far for `floor` needs no weight
-  auto kept_at = [&](int place, float z, uint64_t floor, float reach) -> uint64_t {
-    if (distance(r, z) > reach || z < cut_z || (z == cut_z && static_cast<uint32_t>(tk.id_at(place)) > cut_id)) return 0;
-    const uint64_t wi = near_weight(s, r, z);
-    return wi >= floor ? wi : 0;
-  };
-  // the weight of what is kept, in s.warp_total by the warps that have the tokens: `others`, this thread's far ones, and
-  // the near ones from the list
-  auto weigh = [&](uint32_t others, uint64_t floor, float reach) {
-    const uint64_t t = warp_sum_u64(others);
-    if (lane == 0) s.warp_lo[warp] = static_cast<uint32_t>(t), s.warp_hi[warp] = static_cast<uint32_t>(t >> 32);
-    __syncthreads();
-    tk.each(true, s.near_n, [&](int place, float z, bool there) {
-      const uint64_t wi = there ? kept_at(place, z, floor, reach) : 0;
-      if (wi) {
-        const int owner = (place % SP_THREADS) >> 5;
-        const uint32_t l = static_cast<uint32_t>(wi), old = atomicAdd(&s.warp_lo[owner], l);
-        const uint32_t h = static_cast<uint32_t>(wi >> 32) + (old + l < old ? 1u : 0u);
-        if (h) atomicAdd(&s.warp_hi[owner], h);
-      }
-    });
-    __syncthreads();
-    if (threadIdx.x < SP_WARPS)
-      s.warp_total[threadIdx.x] = static_cast<uint64_t>(s.warp_hi[threadIdx.x]) << 32 | s.warp_lo[threadIdx.x];
-    add_up();
-  };
-  // this thread's far tokens that the cut keeps
-  auto far_kept = [&](uint64_t floor) {
-    uint32_t sum = 0;
-    if (distance(r, cut_z) < SP_FAR) return sum;
-#pragma unroll 2
-    for (int i = 0; i < tk.n; ++i) {
-      const float z = tk.z(i);
-      const bool in = !(distance(r, z) < SP_FAR) && (z > cut_z || (z == cut_z && static_cast<uint32_t>(tk.id(i)) <= cut_id));
-      const uint32_t wi = far_weight(r, z);
-      sum += in && wi >= floor ? wi : 0u;
-    }
-    return sum;
-  };
-  if (by_k) {
-    Row whole = r;
-    whole.from = 0.0f;
-    whole.to = 41.0f;
-    count_cut(p, s, whole, tk, false, static_cast<uint64_t>(k), 0, 0, rank);
-    take_cut();
-    if (by_p) {                                  // the weight of those k
-      weigh(far_kept(1), 1, SP_FAR);
-      meet(p);                                   // (s.total and s.cut_* are read)
-      top_p_cut(p, s, r, tk, 0, needed(top_p, W), top_p, rank);
-      take_cut();
-    }
-  } else if (by_p) {
-    top_p_cut(p, s, r, tk, far, 0, top_p, rank);
-    take_cut();
+  const Cut cut(s.cut_key, s.cut_id);
+  // the chunk with the draw
+  static_assert(SP_MAX_CHUNKS == 64, "two chunks a lane");
+  const uint64_t a = static_cast<uint64_t>(s.total_hi[2 * lane]) << 32 | s.total_lo[2 * lane];
+  const uint64_t b = static_cast<uint64_t>(s.total_hi[2 * lane + 1]) << 32 | s.total_lo[2 * lane + 1];
+  uint64_t upto = a + b;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
   }
-  // min_p's reach, generously
-  const float reach = least > 1 ? 40.01f - log2f(static_cast<float>(least)) : SP_FAR;
-  const bool far_too = least <= SP_FAR_WEIGHT && !(distance(r, cut_z) < SP_FAR);
-  weigh(!far_too ? 0u : want_far && !by_p ? far : far_kept(least), least, reach);
-  if (p.token) {
-    const uint64_t at = scale_uniform(u, W);
-    if (before <= at && at < before + in_warp) {
-#pragma unroll 1
-      for (int i = 0; i < tk.n; i += 8) {
-        uint64_t w[8];
-        kept4(i, least, reinterpret_cast<uint64_t(&)[4]>(w[0]));
-        kept4(i + 4, least, reinterpret_cast<uint64_t(&)[4]>(w[4]));
-        uint64_t mine = 0;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) mine += w[q];
-        uint64_t upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint64_t x = __shfl_up_sync(0xffffffffu, upto, o);
-          if (lane >= o) upto += x;
-        }
-        uint64_t sofar = before + upto - mine;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          if (sofar <= at && at < sofar + w[q]) p.token[row] = tk.id(i + q);
-          sofar += w[q];
-        }
-        before += __shfl_sync(0xffffffffu, upto, 31);
-      }
-    }
+  const uint64_t W = __shfl_sync(0xffffffffu, upto, 31);
+  if (p.probs && t == 0) {
+    st.cut_key = s.cut_key;
+    st.cut_id = s.cut_id;
+    st.inverse = 1.0f / static_cast<float>(W);
   }
-  if (probs) {
-    const float inv = 1.0f / static_cast<float>(W);
-#pragma unroll 1
-    for (int j = 0; j < tk.n / 8; ++j) {         // the far tokens' (zeros, where none is kept), then the near ones'
-      float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-      if (far_too) {
+  if (!p.token) return;
+  const uint64_t at = scale_uniform(u, W);       // (below W)
+  const int l = __ffs(__ballot_sync(0xffffffffu, upto > at)) - 1;
+  uint64_t sofar = __shfl_sync(0xffffffffu, upto - a - b, l);
+  const uint64_t first = __shfl_sync(0xffffffffu, a, l);
+  const int chunk = 2 * l + (sofar + first > at ? 0 : 1);
+  if (chunk & 1) sofar += first;
+  const int id = chunk_id(chunk);
+  float z[8];
+  load_logits(logits, id, p.vocab, (reinterpret_cast<uintptr_t>(logits) & 15) == 0, z);
+  uint64_t w[8], mine = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float z = tk.z(8 * j + i);
-          const uint32_t wi = far_weight(r, z);
-          const bool in = z > cut_z || (z == cut_z && static_cast<uint32_t>(tk.id(8 * j + i)) <= cut_id);
-          v[i] = in && wi >= least ? static_cast<float>(wi) * inv : 0.0f;
-        }
+  for (int i = 0; i < 8; ++i) {
+    w[i] = weight_of(s.pow2, r, z[i], cut.keeps(z[i], id + i));
+    w[i] = w[i] >= least ? w[i] : 0;
+    mine += w[i];
+  }
+  sofar += block_before(s.scan, mine);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (sofar <= at && at < sofar + w[i]) p.token[row] = id + i;
+    sofar += w[i];
+  }
+}
+
+// 5. The probabilities.
+template <typename T>
+__global__ void __launch_bounds__(SP_THREADS, 3) sample_probs_kernel(SampleParams p) {
+  __shared__ Pow2 pow2[64];
+  LaunchStamp ls(p.stamp);
+  const int at = blockIdx.x / p.groups, row = p.row0 + at;
+  const int chunk0 = (blockIdx.x - at * p.groups) * p.pieces, chunk1 = min(chunk0 + p.pieces, p.chunks);
+  fill_pow2(pow2);
+  __syncthreads();
+  pdl_wait();
+  ls.waited();
+  pdl_trigger();
+  if (unused(p, row, row / p.rows_each)) return;
+  const SampleRow& st = p.state[at];
+  const T* logits = static_cast<const T*>(p.logits) + row * p.ld;
+  float* probs = p.probs + row * p.ld_probs;
+  const bool wide = (reinterpret_cast<uintptr_t>(logits) & 15) == 0;
+  const bool wide_out = (reinterpret_cast<uintptr_t>(probs) & 15) == 0;
+  const int kind = st.kind;
+  const Row r = row_of(st);
+  const Cut cut(st.cut_key, st.cut_id);
+  const float inverse = st.inverse;
+  const uint64_t least = st.least;
+  const uint32_t one = kind == ROW_GREEDY ? st.id : 0xffffffffu;
+#pragma unroll 1
+  for (int chunk = chunk0; chunk < chunk1; ++chunk) {
+    const int id = chunk_id(chunk);
+    float v[8];
+    if (kind < ROW_WHOLE) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = static_cast<uint32_t>(id + i) == one ? 1.0f : 0.0f;
+    } else {
+      float z[8];
+      load_logits(logits, id, p.vocab, wide, z);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool in = cut.keeps(z[i], id + i);
+        v[i] = 0.0f;
+        if (!__any_sync(0xffffffffu, in)) continue;
+        const uint64_t w = weight_of(pow2, r, z[i], in);
+        v[i] = w >= least ? static_cast<float>(w) * inverse : 0.0f;
       }
-      store_probs(probs, id0 + j * 256, p.vocab, wide_out, v);
     }
-    __syncthreads();
-    tk.each(true, s.near_n, [&](int place, float z, bool there) {
-      const uint64_t wi = there ? kept_at(place, z, least, reach) : 0;
-      if (wi) probs[tk.id_at(place)] = static_cast<float>(wi) * inv;
-      else if (there && far_too) probs[tk.id_at(place)] = 0.0f;
-    });
+    store_probs(probs, id, p.vocab, wide_out, v);
   }
 }
 
 typedef void (*SampleKernel)(SampleParams);
 }  // namespace
+
+size_t sample_row_bytes() { return sizeof(SampleRow); }
 
 cudaError_t launch_sample(eagle_ctx* ctx, const SampleLaunch& S, cudaStream_t st) {
   SampleParams p{};
@@ -1053,44 +993,38 @@ cudaError_t launch_sample(eagle_ctx* ctx, const SampleLaunch& S, cudaStream_t st
   p.argmax = S.argmax;
   p.probs = S.probs;
   p.ld_probs = S.ld_probs;
+  p.state = static_cast<SampleRow*>(S.rows_state);
+  p.arrived = S.arrived;
   p.status = S.status;
-  // A CTA takes 4096 or 8192 tokens, two CTAs an SM, or 16384, one: whichever gets through the rows in the least time, a
-  // round of CTAs counting its tokens and as much again as 8192 for its exchanges.
-  int runs = 0;
-  auto clusters = [&](int n) {
-    int c = 1;
-    while (c * SP_RUN * n < S.vocab) c <<= 1;
-    return c;
-  };
-  long long best = 0;
-  for (int n = 1; n <= SP_MAX_RUNS; n <<= 1) {
-    if (clusters(n) > SP_MAX_CLUSTER) continue;
-    const int slots = (n == SP_MAX_RUNS ? 1 : 2) * ctx->sm_count;
-    const long long rounds = (static_cast<long long>(clusters(n)) * S.rows + slots - 1) / slots;
-    if (runs == 0 || rounds * (n + 2) < best) {
-      runs = n;
-      best = rounds * (n + 2);
+  p.chunks = (S.vocab + SP_CHUNK - 1) / SP_CHUNK;
+  const bool f32 = S.dtype == EAGLE_DTYPE_F32;
+  const SampleKernel kernels[5] = {f32 ? sample_top_kernel<float> : sample_top_kernel<uint16_t>,
+                                   f32 ? sample_bins_kernel<float> : sample_bins_kernel<uint16_t>,
+                                   f32 ? sample_list_kernel<float> : sample_list_kernel<uint16_t>,
+                                   f32 ? sample_draw_kernel<float> : sample_draw_kernel<uint16_t>,
+                                   f32 ? sample_probs_kernel<float> : sample_probs_kernel<uint16_t>};
+  // bins serve a cut, lists and draws a token or probabilities
+  const bool cuts = S.filter->top_k || S.filter->top_p, rest = S.token || S.probs;
+  const bool wanted[5] = {true, rest && cuts, rest, rest, S.probs != nullptr};
+  for (p.row0 = 0; p.row0 < S.rows; p.row0 += SAMPLE_ROWS) {   // (the state is that of SAMPLE_ROWS rows)
+    const int rows = std::min(S.rows - p.row0, SAMPLE_ROWS);
+    // As many chunks a CTA as let all CTAs, three an SM, take two rounds: rows differ in their work (64 rows of 131072 of
+    // all sorts, and 216 of 32000: one round 79 and 81 us, two 59 and 71, three 56 and 72, five 62 and 76).
+    const int slots = 2 * 3 * ctx->sm_count;
+    p.pieces = std::min((rows * p.chunks + slots - 1) / slots, SP_MAX_PIECES);
+    p.groups = (p.chunks + p.pieces - 1) / p.pieces;
+    for (int i = 0; i < 5; ++i) {
+      if (!wanted[i]) continue;
+      p.stamp = stamp_slot(ctx, EAGLE_K_SAMPLE);
+      trace_before(ctx, EAGLE_K_SAMPLE, st);
+      const cudaError_t e = launch_pdl(kernels[i], dim3(static_cast<unsigned>(rows) * (i == 3 ? 1 : p.groups)),
+                                       dim3(SP_THREADS), 0, st, p);
+      if (e != cudaSuccess) return e;
+      ctx->launches++;
+      trace_after(ctx, EAGLE_K_SAMPLE, st);
     }
   }
-  p.cluster = clusters(runs);
-  p.each = 8 * runs;
-  const SampleKernel k = S.dtype == EAGLE_DTYPE_F32 ? sample_kernel<float> : sample_kernel<uint16_t>;
-  const size_t smem = sizeof(SampleShared) + static_cast<size_t>(runs) * SP_RUN * 6;
-  cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(k),
-                                  static_cast<int>(sizeof(SampleShared) + static_cast<size_t>(SP_MAX_RUNS) * SP_RUN * 6));
-  if (e != cudaSuccess) return e;
-  if (p.cluster > 8) {
-    e = cluster_nonportable_once(reinterpret_cast<const void*>(k));
-    if (e != cudaSuccess) return e;
-  }
-  p.stamp = stamp_slot(ctx, EAGLE_K_SAMPLE);
-  trace_before(ctx, EAGLE_K_SAMPLE, st);
-  const dim3 grid(static_cast<unsigned>(S.rows) * p.cluster);
-  e = p.cluster > 1 ? launch_pdl_cluster(k, grid, dim3(SP_THREADS), smem, st, p.cluster, p)
-                    : launch_pdl(k, grid, dim3(SP_THREADS), smem, st, p);
-  ctx->launches++;
-  trace_after(ctx, EAGLE_K_SAMPLE, st);
-  return e;
+  return cudaSuccess;
 }
 
 }  // namespace eagle

@@ -417,6 +417,33 @@ def test_sample_ties():
     check_sample(z, [1.0] * 4, [20000, 0, 5, 0], [0.9, 0.5, 1.0, 0.01])
 
 
+def test_sample_long_lists():
+    """Cuts among more tokens than are sorted at a time, or than a list holds, and behind the bins of weight."""
+    z = normal(11, 8, 131072) * 2.5
+    check_sample(z, [1.3] * 8, [0, 0, 3000, 3000, 20000, 20000, 130000, 0], [0.97, 0.9999, 1.0, 0.8, 0.9, 1.0, 0.999, 0.6],
+                 [0.0, 0.0, 0.0, 0.0, 1e-7, 1e-5, 0.0, 1e-4])
+    check_sample((z * 4).to(BF16), [2.5, 2.5, 2.0, 2.0, 3.0, 3.0, 0.1, 2.5], [0, 0, 0, 70000, 70000, 0, 600, 0],
+                 [0.9999, 0.99999, 0.9999, 0.9999, 1.0, 0.999999, 0.9, 1.0], [0.0, 1e-9, 0.0, 0.0, 0.0, 0.0, 0.0, 1e-6])
+
+
+def test_sample_outputs_alone():
+    """Each output without the others, and no filter at all."""
+    z = normal(12, 5, 9001) * 3
+    u = i32([1, -5, 1 << 30, 7, -(1 << 31)])
+    s = R.Sampler(engine(), 5, f32([0.8, 0.0, 1.2, 1.0, 0.6]), i32([0, 3, 40, 0, 700]), f32([0.9, 0.9, 0.9, 1.0, 1.0]))
+    token, arg, probs = i32([-7] * 5), i32([-7] * 5), torch.full_like(z, 7.0)
+    s(z, u, token, arg, probs)
+    a, b, c = i32([-7] * 5), i32([-7] * 5), torch.full_like(z, 7.0)
+    s(z, u, a)
+    s(z, argmax=b)
+    s(z, probs=c)
+    assert torch.equal(a, token) and torch.equal(b, arg) and torch.equal(c, probs)
+    s(z, u, a, probs=c.fill_(7.0))
+    assert torch.equal(a, token) and torch.equal(c, probs)
+    check_sample(z, None)
+    assert engine().status() == 0
+
+
 def test_sample_masked_and_extreme():
     z = normal(6, 8, 9000) * 3
     z[0, 1:] = -INF                                      # one token left
