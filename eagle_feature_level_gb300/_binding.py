@@ -24,6 +24,7 @@ DTYPE_BF16, DTYPE_F32 = 0, 1
 ROPE_LINEAR, ROPE_BANDS, ROPE_RAMP = 1, 2, 3
 MX_FP8, MX_FP4, NV_FP4 = 1, 2, 3
 ACT_NONE, ACT_SWIGLU = 0, 1
+EAGLE_MAX_EXTENT = 1 << 30
 EAGLE_MAX_NORM_COLS = 32768
 EAGLE_MAX_SAMPLE_VOCAB = 262144
 PHASE_ROOT, PHASE_FRONTIER, PHASE_FINAL = 0, 1, 2

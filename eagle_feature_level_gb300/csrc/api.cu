@@ -237,6 +237,7 @@ eagle_status check_mx(const eagle_mx* m) {
   EAGLE_REQUIRE(m, EAGLE_ERR_INVALID_ARG);
   EAGLE_REQUIRE(m->format >= EAGLE_MX_FP8 && m->format <= EAGLE_NV_FP4, EAGLE_ERR_INVALID_ARG);
   EAGLE_REQUIRE(m->rows >= 1 && m->cols >= 32 && m->cols % 32 == 0, EAGLE_ERR_SHAPE);
+  EAGLE_REQUIRE(m->rows <= EAGLE_MAX_EXTENT && m->cols <= EAGLE_MAX_EXTENT, EAGLE_ERR_CAPACITY);
   EAGLE_PTR(m->data); EAGLE_PTR(m->scale);
   if (m->format == EAGLE_NV_FP4 && m->tensor_scale)
     EAGLE_REQUIRE((reinterpret_cast<uintptr_t>(m->tensor_scale) & 3u) == 0, EAGLE_ERR_ALIGN);
@@ -950,6 +951,7 @@ eagle_status eagle_mx_layout(int format, int rows, int cols, size_t* data_bytes,
   EAGLE_REQUIRE(data_bytes && scale_bytes, EAGLE_ERR_INVALID_ARG);
   EAGLE_REQUIRE(format >= EAGLE_MX_FP8 && format <= EAGLE_NV_FP4, EAGLE_ERR_INVALID_ARG);
   EAGLE_REQUIRE(rows >= 1 && cols >= 32 && cols % 32 == 0, EAGLE_ERR_SHAPE);
+  EAGLE_REQUIRE(rows <= EAGLE_MAX_EXTENT && cols <= EAGLE_MAX_EXTENT, EAGLE_ERR_CAPACITY);
   const size_t r = static_cast<size_t>(rows), n = static_cast<size_t>(cols) / (format == EAGLE_NV_FP4 ? 16 : 32);
   *data_bytes = r * static_cast<size_t>(cols) / (format == EAGLE_MX_FP8 ? 1 : 2);
   *scale_bytes = (r + 127) / 128 * ((n + 3) / 4) * 512;
@@ -1003,7 +1005,7 @@ eagle_status eagle_mx_linear(eagle_ctx* ctx, const eagle_mx* x, const eagle_mx* 
 eagle_status eagle_add_norm(eagle_ctx* ctx, const eagle_norm* n, void* workspace, cudaStream_t stream) {
   EAGLE_REQUIRE(ctx && n, EAGLE_ERR_INVALID_ARG);
   EAGLE_REQUIRE(n->rows >= 1 && n->cols >= 8 && n->cols % 8 == 0, EAGLE_ERR_SHAPE);
-  EAGLE_REQUIRE(n->cols <= EAGLE_MAX_NORM_COLS, EAGLE_ERR_CAPACITY);
+  EAGLE_REQUIRE(n->rows <= EAGLE_MAX_EXTENT && n->cols <= EAGLE_MAX_NORM_COLS, EAGLE_ERR_CAPACITY);
   EAGLE_REQUIRE(std::isfinite(n->eps) && n->eps >= 0.f, EAGLE_ERR_INVALID_ARG);
   eagle_status st = check_dtype(n->dtype);
   if (st != EAGLE_OK) return st;
@@ -1039,7 +1041,7 @@ eagle_status eagle_sample(eagle_ctx* ctx, int n_rows, int vocab, int dtype, cons
                           int ld_probs, void* workspace, cudaStream_t stream) {
   EAGLE_REQUIRE(ctx && f, EAGLE_ERR_INVALID_ARG);
   EAGLE_REQUIRE(n_rows >= 1 && vocab >= 1, EAGLE_ERR_SHAPE);
-  EAGLE_REQUIRE(vocab <= EAGLE_MAX_SAMPLE_VOCAB, EAGLE_ERR_CAPACITY);
+  EAGLE_REQUIRE(n_rows <= EAGLE_MAX_EXTENT && vocab <= EAGLE_MAX_SAMPLE_VOCAB, EAGLE_ERR_CAPACITY);
   eagle_status st = check_dtype(dtype);
   if (st != EAGLE_OK) return st;
   EAGLE_PTR(logits);

@@ -710,8 +710,10 @@ eagle_status eagle_pages_compact(eagle_ctx* ctx, const eagle_pages* pages, const
  * its cache: norms with the residual's addition, linear layers in microscaled
  * 8 and 4 bits, and tokens or whole distributions out of its logits.  As
  * everywhere, calls (and graph replays) on one workspace are ordered, every
- * call can be captured, and nothing is kept from one call for the next.
+ * call can be captured, and nothing is kept from one call for the next.  Rows
+ * and columns of every matrix: at most EAGLE_MAX_EXTENT.
  */
+#define EAGLE_MAX_EXTENT (1 << 30)
 
 /* Microscaled formats: a row's elements in blocks, each block with a scale of
  * 8 bits, value = element * scale (* tensor_scale).

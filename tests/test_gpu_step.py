@@ -587,6 +587,22 @@ def test_arguments_checked_before_launch():
     assert B.eagle_launch_count(e.ctx) == before and e.status() == 0
 
 
+def test_refuses_extents_that_pass_32_bits():
+    e = engine()
+    a, ws, st, before = torch.zeros(1 << 16, dtype=torch.uint8, device="cuda").data_ptr(), e.ws.data_ptr(), e.stream(), \
+        B.eagle_launch_count(e.ctx)
+    most = B.EAGLE_MAX_EXTENT
+    for rows, cols in ((most + 1, 32), (1, most + 32), ((1 << 31) - 1, 32), (1, (1 << 31) - 32)):
+        m = B.eagle_mx(a, a + 32768, None, rows, cols, B.MX_FP8)
+        refused(CAPACITY, B.eagle_mx_quantize, e.ctx, 0, 0, a + 4096, (1 << 31) - 8, m, ws, st)
+        refused(CAPACITY, B.eagle_mx_unpack, e.ctx, m, 0, a + 4096, (1 << 31) - 8, ws, st)
+        refused(CAPACITY, B.eagle_mx_linear, e.ctx, m, m, None, 0, a + 4096, (1 << 31) - 8, ws, st)
+    refused(CAPACITY, B.eagle_add_norm, e.ctx, B.eagle_norm(most + 1, 8, 0, a, 8, 0, None, 0, None, 0, None, 0.0, 0, a + 4096, 8, None), ws, st)
+    refused(CAPACITY, B.eagle_sample, e.ctx, most + 1, 1, 0, a, 1, B.eagle_filter(None, None, None, None, 1, None), None, None,
+            a + 4096, None, 1, ws, st)
+    assert B.eagle_launch_count(e.ctx) == before and e.status() == 0
+
+
 def test_wrappers_check_their_tensors():
     e = engine()
     t = mx("fp8", 4, 64)
