@@ -5,17 +5,21 @@
 // holds [128 outputs][rows] and a lane stores its output's column, 32 neighbours a warp.  Many rows: x is operand A and
 // the weights B, a lane has a row and stores 16 outputs of it at once (in whole sectors; 4096 x 4096 x 4096
 // 42 to 32 us); where it pays, two CTAs work on a tile of 256 rows of A, each loading half of B (tcgen05's pairs), so
-// that an SM takes in less for as many products.  A stage of the ring holds 128 bytes of every row of both (256 four-bit or 128 eight-bit
-// elements, 4 MMAs) and their scales, which lie in memory as the 512-byte groups that one tcgen05.cp spreads over tensor
-// memory.  Warp roles: TMA producer, MMA issuer, four warps that read the accumulator out; two accumulators, so that
-// a tile is read out under the next one's products.
+// that an SM takes in less for as many products.  A stage of the ring holds 128 bytes of every row of both (256 four-bit or
+// 128 eight-bit elements, 4 MMAs) and their scales, which lie in memory as the 512-byte groups that one tcgen05.cp spreads
+// over tensor memory.  Warp roles: a producer for A and one for B (with the scales), one warp that issues the products and
+// one the scales' copies (an instruction of either takes some 60 cycles to issue: 4096 x 8192 x 10240 in one warp 310 us,
+// apart 148), four that read the accumulator out; two accumulators, so that a tile is read out under the next one's
+// products.
 //
 // Bound, many rows: what an SM takes in, 64 bytes a cycle: a stage of 192 rows of B is 46 KB for a CTA alone and 34 KB for
-// one of a pair (4096 x 8192 x 10240, NV_FP4: 148 and 124 us, 5.6 PFLOP/s), 720 and 530 cycles for products of 384.  Few
-// rows: the weights' bytes from memory (16 x 8192 x 32000: 24.5 us, 6.0 TB/s).
+// one of a pair (4096 x 8192 x 10240, NV_FP4: 148 and 120 us, 5.7 PFLOP/s), 720 and 530 cycles for products of 384.  Few
+// rows: the weights' bytes from memory (16 x 8192 x 32000: 25 us, 6.0 TB/s; 1 x 4096 x 12288: 7.8, 3.6 TB/s, of which some
+// 4 us until the first products and behind the last).
 //
-// Few tiles: a cluster of CTAs splits a tile's inner dimension; each writes its partial to its own shared memory and
-// sums its share of the rows over all of them, in rank order.
+// Few tiles: a cluster of 2, 4 or 8 CTAs splits a tile's inner dimension; each writes its partial to its own shared memory
+// and sums its share of the rows over all of them, in rank order (8 x 8192 x 8192 in 8 bits: 14.8 us; 3, 5 or 6 ways were
+// nowhere the best).
 #include <algorithm>
 
 #include "internal.h"
@@ -27,7 +31,7 @@ namespace eagle {
 namespace {
 
 constexpr int LN_THREADS = 256;
-constexpr int LN_M = 128;                     // outputs of a tile
+constexpr int LN_M = 128;                     // A's rows of a tile
 constexpr int LN_KB = 128;                    // bytes of a row in a stage
 constexpr int LN_MAX_STAGES = 12;
 constexpr int LN_A_BYTES = LN_M * LN_KB;
@@ -310,7 +314,7 @@ __device__ __forceinline__ void produce(const LinearParams& p, LinearShared& sh,
     }
     if (*abort) break;
   }
-  if (*abort && rank == 0)                       // copies in flight land first (where the other producers asked for theirs too)
+  if (*abort && rank == 0)                       // copies in flight land first (if the others asked for theirs too)
     for (int i = max(0, issued - p.stages); i < issued; ++i)
       sm100::mbar_wait(&sh.full[i % p.stages], (i / p.stages) & 1, &sh.never);
 }
@@ -589,7 +593,8 @@ __global__ void __launch_bounds__(LN_THREADS, 1)
     sh.abort = sh.never = 0;
     // the first ring's weights on their way to L2 (not into shared memory: what precedes may still write them)
     const TileAt at = tile_at<PAIR>(p, min(first, p.tiles - 1), rank);
-    for (int k = k0; k < min(k1, k0 + p.stages); ++k) prefetch_2d(p.by_row ? &bm : &am, k * LN_KB, p.by_row ? at.b0 : at.a0);
+    for (int k = k0; k < min(k1, k0 + p.stages); ++k)
+      prefetch_2d(p.by_row ? &bm : &am, k * LN_KB, p.by_row ? at.b0 : at.a0);
   }
   if (PAIR) {                                    // (the allocation takes both CTAs)
     __syncwarp();
