@@ -40,7 +40,7 @@ constexpr int SP_LIST = 8 * SP_THREADS;         // of a row
 constexpr int SP_SORT = SP_THREADS;             // sorted at a time
 constexpr int SP_CHUNK = 8 * SP_THREADS;        // eight tokens a thread
 constexpr int SP_MAX_CHUNKS = EAGLE_MAX_SAMPLE_VOCAB / SP_CHUNK;
-constexpr int SP_MAX_PIECES = 3;                // chunks of a CTA
+constexpr int SP_MAX_PIECES = 3;                // chunks of a CTA from the second kernel on
 static_assert(SP_MAX_CHUNKS <= 64, "two chunks a lane");
 
 // From this distance on a weight (2^23 or less) needs no more than fp32, and from the other it is nothing.
@@ -196,30 +196,53 @@ __device__ __forceinline__ uint64_t weight_of(const Pow2* pow2, const Row& r, fl
   return w;
 }
 
-// Eight logits from id `at` on, those past the end -inf.
-__device__ __forceinline__ void load_logits(const float* row, int at, int vocab, bool wide, float (&z)[8]) {
-  if (wide && at + 8 <= vocab) {
-    const float4 a = *reinterpret_cast<const float4*>(row + at), b = *reinterpret_cast<const float4*>(row + at + 4);
+// Eight logits from id `at` on, those past the end -inf, as they are loaded: what is converted is waited for, so a chunk's
+// are loaded under the one before and converted when it is their turn.
+template <typename T>
+struct Logits;
+template <>
+struct Logits<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* row, int at, int vocab, bool wide) {
+    if (wide && at + 8 <= vocab) {
+      a = *reinterpret_cast<const float4*>(row + at);
+      b = *reinterpret_cast<const float4*>(row + at + 4);
+    } else {
+      auto one = [&](int i) { return at + i < vocab ? row[at + i] : -INFINITY; };
+      a = make_float4(one(0), one(1), one(2), one(3));
+      b = make_float4(one(4), one(5), one(6), one(7));
+    }
+  }
+  __device__ __forceinline__ void get(float (&z)[8]) const {
     z[0] = a.x; z[1] = a.y; z[2] = a.z; z[3] = a.w;
     z[4] = b.x; z[5] = b.y; z[6] = b.z; z[7] = b.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = at + i < vocab ? row[at + i] : -INFINITY;
   }
-}
-__device__ __forceinline__ void load_logits(const uint16_t* row, int at, int vocab, bool wide, float (&z)[8]) {
-  if (wide && at + 8 <= vocab) {
-    const uint4 v = *reinterpret_cast<const uint4*>(row + at);
+};
+template <>
+struct Logits<uint16_t> {
+  uint4 v;
+  __device__ __forceinline__ void load(const uint16_t* row, int at, int vocab, bool wide) {
+    if (wide && at + 8 <= vocab) {
+      v = *reinterpret_cast<const uint4*>(row + at);
+    } else {
+      auto one = [&](int i) { return at + i < vocab ? static_cast<uint32_t>(row[at + i]) : 0xff80u; };
+      v = make_uint4(one(0) | one(1) << 16, one(2) | one(3) << 16, one(4) | one(5) << 16, one(6) | one(7) << 16);
+    }
+  }
+  __device__ __forceinline__ void get(float (&z)[8]) const {
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       z[2 * i] = __uint_as_float(u[i] << 16);
       z[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = at + i < vocab ? bf16_to_f32(row[at + i]) : -INFINITY;
   }
+};
+template <typename T>
+__device__ __forceinline__ void load_logits(const T* row, int at, int vocab, bool wide, float (&z)[8]) {
+  Logits<T> x;
+  x.load(row, at, vocab, wide);
+  x.get(z);
 }
 
 __device__ __forceinline__ void store_probs(float* row, int id, int vocab, bool wide, const float (&v)[8]) {
@@ -303,6 +326,41 @@ __device__ __forceinline__ Extent warp_extent(Extent e) {
   return e;
 }
 
+__device__ __forceinline__ float largest(const float (&z)[8]) {
+  return fmaxf(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])), fmaxf(fmaxf(z[4], z[5]), fmaxf(z[6], z[7])));
+}
+
+// The bin where the sum of a row's bins reaches `need` (-1: nowhere), and the sum before it (or of all); a whole warp.
+template <typename F>
+__device__ __forceinline__ int find_bin(uint64_t need, F bin_at, uint64_t& before) {
+  const int lane = threadIdx.x & 31;
+  uint64_t own[SP_LANE_BINS], mine = 0;
+#pragma unroll
+  for (int q = 0; q < SP_LANE_BINS; ++q) {
+    own[q] = bin_at(lane * SP_LANE_BINS + q);
+    mine += own[q];
+  }
+  uint64_t upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  uint64_t sofar = upto - mine;
+  int bin = -1;
+  if (sofar < need && upto >= need) {            // in one of this lane's
+#pragma unroll
+    for (int q = 0; q < SP_LANE_BINS; ++q) {
+      if (bin < 0 && sofar + own[q] >= need) bin = lane * SP_LANE_BINS + q;
+      if (bin < 0) sofar += own[q];
+    }
+  }
+  const uint32_t who = __ballot_sync(0xffffffffu, bin >= 0);
+  const int from = who ? __ffs(who) - 1 : 31;
+  before = __shfl_sync(0xffffffffu, who ? sofar : upto, from);
+  return __shfl_sync(0xffffffffu, bin, from);
+}
+
 // Whether this CTA is the last of its row's to arrive: it then sees what all of them stored (every thread calls it).
 __device__ __forceinline__ bool last_of_row(int* arrived, int ctas) {
   __shared__ int last;
@@ -340,10 +398,13 @@ __global__ void __launch_bounds__(SP_THREADS) sample_top_kernel(SampleParams p) 
   const bool wide = (reinterpret_cast<uintptr_t>(logits) & 15) == 0;
   float top = -INFINITY;                         // NaN if any is
   uint32_t id = 0xffffffffu;
-#pragma unroll 2
+  Logits<T> next;
+  next.load(logits, chunk_id(chunk0), p.vocab, wide);
+#pragma unroll 1
   for (int chunk = chunk0; chunk < chunk1; ++chunk) {
     float z[8], most = -INFINITY;
-    load_logits(logits, chunk_id(chunk), p.vocab, wide, z);
+    next.get(z);
+    if (chunk + 1 < chunk1) next.load(logits, chunk_id(chunk + 1), p.vocab, wide);
 #pragma unroll
     for (int i = 0; i < 8; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(most) : "f"(z[i]));
     if (chunk == chunk0 || most > top) {         // (the first of equals stays; with a NaN the id is not used)
@@ -441,6 +502,8 @@ __global__ void __launch_bounds__(SP_THREADS, 3) sample_bins_kernel(SampleParams
   SampleRow& st = p.state[at];
   const T* logits = static_cast<const T*>(p.logits) + row * p.ld;
   const bool wide = (reinterpret_cast<uintptr_t>(logits) & 15) == 0;
+  Logits<T> next;
+  next.load(logits, chunk_id(chunk0), p.vocab, wide);
   const int kind = st.kind;
   if (kind != ROW_COUNT && kind != ROW_WEIGH) return;
   const Row r = row_of(st);
@@ -450,7 +513,8 @@ __global__ void __launch_bounds__(SP_THREADS, 3) sample_bins_kernel(SampleParams
 #pragma unroll 1
   for (int chunk = chunk0; chunk < chunk1; ++chunk) {
     float z[8];
-    load_logits(logits, chunk_id(chunk), p.vocab, wide, z);
+    next.get(z);
+    if (chunk + 1 < chunk1) next.load(logits, chunk_id(chunk + 1), p.vocab, wide);
     if (kind == ROW_COUNT) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -497,42 +561,28 @@ __global__ void __launch_bounds__(SP_THREADS, 3) sample_bins_kernel(SampleParams
   }
   static_assert(SP_ROW_BINS + 32 <= SP_THREADS, "the last warp has no bins");
   if (!last_of_row(p.arrived + SAMPLE_ROWS + at, p.groups) || warp > 0) return;
-  uint64_t own[SP_LANE_BINS], mine = 0;
-#pragma unroll
-  for (int q = 0; q < SP_LANE_BINS; ++q) {
-    own[q] = ldcg_u64(&st.bins[lane * SP_LANE_BINS + q]);
-    mine += own[q];
+  auto bin_at = [&](int b) { return ldcg_u64(&st.bins[b]); };
+  uint64_t need, before;
+  bool both = false;
+  if (kind == ROW_COUNT) {
+    need = static_cast<uint64_t>(p.top_k[request]);
+    both = p.top_p && p.top_p[request] < 1.0f;   // (then all k are listed)
+  } else {
+    find_bin(~0ull, bin_at, before);
+    need = needed(p.top_p[request], before + ldcg_u64(&st.far));
   }
-  uint64_t upto = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t x = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += x;
-  }
-  const uint64_t binned = __shfl_sync(0xffffffffu, upto, 31);
-  const uint64_t need = kind == ROW_COUNT ? static_cast<uint64_t>(p.top_k[request])
-                                          : needed(p.top_p[request], binned + ldcg_u64(&st.far));
-  const bool both = kind == ROW_COUNT && p.top_p && p.top_p[request] < 1.0f;   // (then all k are listed)
-  uint64_t before = upto - mine;
-  if (lane == 0) {
-    st.need = need;
-    if (binned < need) {                         // all that have weight are kept, or the cut is behind the bins
-      st.before = kind == ROW_COUNT ? 0 : binned;
-      if (kind == ROW_WEIGH) st.from = SP_WEIGHED;
-      else if (both) st.from = 0.0f;
-    }
-  }
-  if (before < need && upto >= need) {           // in one of this lane's bins
-    int bin = -1;
-#pragma unroll
-    for (int q = 0; q < SP_LANE_BINS; ++q) {
-      if (bin < 0 && before + own[q] >= need) bin = lane * SP_LANE_BINS + q;
-      if (bin < 0) before += own[q];
-    }
-    const float bins = kind == ROW_COUNT ? SP_COUNT_BINS : SP_WEIGHT_BINS;
+  const int bin = find_bin(need, bin_at, before);
+  if (lane > 0) return;
+  st.need = need;
+  const float bins = kind == ROW_COUNT ? SP_COUNT_BINS : SP_WEIGHT_BINS;
+  if (bin >= 0) {
     st.before = both ? 0 : before;
     st.from = both ? 0.0f : static_cast<float>(bin) / bins;
     st.end = static_cast<float>(bin + 1) / bins;
+  } else {                                       // all that have weight are kept, or the cut is behind the bins
+    st.before = kind == ROW_COUNT ? 0 : before;
+    if (kind == ROW_WEIGH) st.from = SP_WEIGHED;
+    else if (both) st.from = 0.0f;
   }
 }
 
@@ -553,9 +603,11 @@ __global__ void __launch_bounds__(SP_THREADS, 3) sample_list_kernel(SampleParams
   pdl_trigger();
   if (unused(p, row, row / p.rows_each)) return;
   SampleRow& st = p.state[at];
-  if (st.kind < ROW_WHOLE) return;
   const T* logits = static_cast<const T*>(p.logits) + row * p.ld;
   const bool wide = (reinterpret_cast<uintptr_t>(logits) & 15) == 0;
+  Logits<T> next;
+  next.load(logits, chunk_id(chunk0), p.vocab, wide);
+  if (st.kind < ROW_WHOLE) return;
   const Row r = row_of(st);
   const float from = st.from, end = st.end, reach = st.reach;
   const uint64_t least = st.least;
@@ -563,7 +615,12 @@ __global__ void __launch_bounds__(SP_THREADS, 3) sample_list_kernel(SampleParams
   for (int chunk = chunk0; chunk < chunk1; ++chunk) {
     const int id0 = chunk_id(chunk);
     float z[8];
-    load_logits(logits, id0, p.vocab, wide, z);
+    next.get(z);
+    if (chunk + 1 < chunk1) next.load(logits, chunk_id(chunk + 1), p.vocab, wide);
+    if (!__any_sync(0xffffffffu, distance(r, largest(z)) < fmaxf(from, end))) {
+      if (lane == 0) sums[chunk - chunk0][warp] = 0;
+      continue;
+    }
     uint64_t sum = 0;
     if (from > SP_FAR && reach > SP_FAR) {       // far tokens too
 #pragma unroll
@@ -943,6 +1000,8 @@ __global__ void __launch_bounds__(SP_THREADS, 3) sample_probs_kernel(SampleParam
   float* probs = p.probs + row * p.ld_probs;
   const bool wide = (reinterpret_cast<uintptr_t>(logits) & 15) == 0;
   const bool wide_out = (reinterpret_cast<uintptr_t>(probs) & 15) == 0;
+  Logits<T> next;
+  next.load(logits, chunk_id(chunk0), p.vocab, wide);
   const int kind = st.kind;
   const Row r = row_of(st);
   const Cut cut(st.cut_key, st.cut_id);
@@ -958,12 +1017,14 @@ __global__ void __launch_bounds__(SP_THREADS, 3) sample_probs_kernel(SampleParam
       for (int i = 0; i < 8; ++i) v[i] = static_cast<uint32_t>(id + i) == one ? 1.0f : 0.0f;
     } else {
       float z[8];
-      load_logits(logits, id, p.vocab, wide, z);
+      next.get(z);
+      if (chunk + 1 < chunk1) next.load(logits, chunk_id(chunk + 1), p.vocab, wide);
+      const bool some = __any_sync(0xffffffffu, largest(z) >= cut.z);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const bool in = cut.keeps(z[i], id + i);
+        const bool in = some && cut.keeps(z[i], id + i);
         v[i] = 0.0f;
-        if (!__any_sync(0xffffffffu, in)) continue;
+        if (!some || !__any_sync(0xffffffffu, in)) continue;
         const uint64_t w = weight_of(pow2, r, z[i], in);
         v[i] = w >= least ? static_cast<float>(w) * inverse : 0.0f;
       }
@@ -1008,13 +1069,14 @@ cudaError_t launch_sample(eagle_ctx* ctx, const SampleLaunch& S, cudaStream_t st
   const bool wanted[5] = {true, rest && cuts, rest, rest, S.probs != nullptr};
   for (p.row0 = 0; p.row0 < S.rows; p.row0 += SAMPLE_ROWS) {   // (the state is that of SAMPLE_ROWS rows)
     const int rows = std::min(S.rows - p.row0, SAMPLE_ROWS);
-    // As many chunks a CTA as let all CTAs, three an SM, take two rounds: rows differ in their work (64 rows of 131072 of
-    // all sorts, and 216 of 32000: one round 79 and 81 us, two 59 and 71, three 56 and 72, five 62 and 76).
-    const int slots = 2 * 3 * ctx->sm_count;
-    p.pieces = std::min((rows * p.chunks + slots - 1) / slots, SP_MAX_PIECES);
-    p.groups = (p.chunks + p.pieces - 1) / p.pieces;
     for (int i = 0; i < 5; ++i) {
       if (!wanted[i]) continue;
+      // As many chunks a CTA as let all CTAs, three an SM, take one round in the first kernel, whose rows are alike, and
+      // three in the others, where flat rows have more work (64 rows of 131072 of all sorts: one round throughout 79 us,
+      // two 59, these 55; the first in two 1.3 more; six in the second 2.5 more).
+      const int slots = (i == 0 ? 1 : 3) * 3 * ctx->sm_count, even = (rows * p.chunks + slots - 1) / slots;
+      p.pieces = i == 0 ? even : std::min(even, SP_MAX_PIECES);
+      p.groups = (p.chunks + p.pieces - 1) / p.pieces;
       p.stamp = stamp_slot(ctx, EAGLE_K_SAMPLE);
       trace_before(ctx, EAGLE_K_SAMPLE, st);
       const cudaError_t e = launch_pdl(kernels[i], dim3(static_cast<unsigned>(rows) * (i == 3 ? 1 : p.groups)),
