@@ -20,11 +20,11 @@
 // Weights from 2^23 on (the near tokens') take fixed point and pairs of floats, the others fp32.  Near tokens are a small
 // part of a row as a rule: a warp lists its own first, so that the work on them is dense.
 //
-// Bound: instructions where rows are flat (64 rows of 131072 in bf16: top-p of 0.95 at t = 1.3 86 us, issue slots 41 %
-// full), else the launches and the latency of each kernel's exchanges (greedy 14 us, top-k of 50 39, min-p of 0.05 27; one
-// row of 32000: top-k of 400 and top-p 18).  A cluster of CTAs that keeps a row in shared memory through all steps reads it
-// once and saves launches, but leaves the SMs waiting for its exchanges: one row 17 us, those 64 rows 209 (flat), 26, 66
-// and 56, and a batch of all sorts 113 us where this takes 59.
+// Bound: instructions where rows are flat (64 rows of 131072 in bf16: top-p of 0.95 at t = 1.3 85 us, issue slots of the
+// busy SMs full), else the latency of each kernel's loads and exchanges (greedy 15 us, top-k of 50 33, top-p of 0.7 at
+// t = 0.5 41, min-p of 0.05 28, no cut 43; one row of 32000: top-k of 400 and top-p 18).  A cluster of CTAs that keeps a row
+// in shared memory through all steps saves launches, but leaves the SMs waiting for its exchanges: those 64
+// rows 209, 26, 66, 89, 56 and 66 us, the one row 17, and 64 rows of all sorts 113 where this takes 55.
 #include <algorithm>
 
 #include "internal.h"
@@ -71,6 +71,7 @@ struct alignas(16) SampleRow {
   float reach;                                  // distance up to which min_p may keep a token
   uint32_t id;                                  // the argmax
   uint64_t least;                               // min_p's weight
+  float top_p;
   uint64_t need, before;                        // the cut's number or weight, and the number or weight before `from`
   uint64_t far;                                 // weight of the tokens behind the bins, where those are weighed
   uint32_t listed;                              // tokens in `list`, or more than it takes
@@ -396,6 +397,11 @@ __global__ void __launch_bounds__(SP_THREADS) sample_top_kernel(SampleParams p) 
   SampleRow& st = p.state[at];
   const T* logits = static_cast<const T*>(p.logits) + row * p.ld;
   const bool wide = (reinterpret_cast<uintptr_t>(logits) & 15) == 0;
+  // (for the last CTA, which would wait for them)
+  const float temp = p.temperature ? p.temperature[request] : 1.0f;
+  const int k = p.top_k ? p.top_k[request] : 0;
+  const float top_p = p.top_p ? p.top_p[request] : 1.0f;
+  const float min_p = p.min_p ? fminf(p.min_p[request], 1.0f) : 0.0f;
   float top = -INFINITY;                         // NaN if any is
   uint32_t id = 0xffffffffu;
   Logits<T> next;
@@ -436,10 +442,6 @@ __global__ void __launch_bounds__(SP_THREADS) sample_top_kernel(SampleParams p) 
   }
   e = warp_extent(e);
   if (lane > 0) return;
-  const float temp = p.temperature ? p.temperature[request] : 1.0f;
-  const int k = p.top_k ? p.top_k[request] : 0;
-  const float top_p = p.top_p ? p.top_p[request] : 1.0f;
-  const float min_p = p.min_p ? fminf(p.min_p[request], 1.0f) : 0.0f;
   const bool none = e.bad || !(key_value(e.top) > -INFINITY), greedy = !(temp > 0.0f);
   const bool by_k = k > 0 && k < p.vocab, by_p = top_p < 1.0f;
   // log2(e) / t as a pair of floats: the quotient and, over t, what it leaves
@@ -455,6 +457,8 @@ __global__ void __launch_bounds__(SP_THREADS) sample_top_kernel(SampleParams p) 
   st.least = least;
   st.reach = least > 1 ? 40.01f - log2f(static_cast<float>(least)) : SP_NONE;   // (generously)
   st.id = e.id;
+  st.need = by_k ? static_cast<uint64_t>(k) : 0;
+  st.top_p = top_p;
   st.far = 0;
   st.listed = 0;
   if (p.argmax) p.argmax[row] = none ? -1 : static_cast<int32_t>(e.id);
@@ -507,6 +511,8 @@ __global__ void __launch_bounds__(SP_THREADS, 3) sample_bins_kernel(SampleParams
   const int kind = st.kind;
   if (kind != ROW_COUNT && kind != ROW_WEIGH) return;
   const Row r = row_of(st);
+  const uint64_t k = st.need;
+  const float top_p = st.top_p;
   uint32_t* my_lo = lo[warp % COPIES];
   uint32_t* my_hi = hi[warp % COPIES];
   uint64_t far_all = 0;
@@ -562,15 +568,12 @@ __global__ void __launch_bounds__(SP_THREADS, 3) sample_bins_kernel(SampleParams
   static_assert(SP_ROW_BINS + 32 <= SP_THREADS, "the last warp has no bins");
   if (!last_of_row(p.arrived + SAMPLE_ROWS + at, p.groups) || warp > 0) return;
   auto bin_at = [&](int b) { return ldcg_u64(&st.bins[b]); };
-  uint64_t need, before;
-  bool both = false;
-  if (kind == ROW_COUNT) {
-    need = static_cast<uint64_t>(p.top_k[request]);
-    both = p.top_p && p.top_p[request] < 1.0f;   // (then all k are listed)
-  } else {
+  uint64_t need = k, before;
+  if (kind == ROW_WEIGH) {
     find_bin(~0ull, bin_at, before);
-    need = needed(p.top_p[request], before + ldcg_u64(&st.far));
+    need = needed(top_p, before + ldcg_u64(&st.far));
   }
+  const bool both = kind == ROW_COUNT && top_p < 1.0f;   // (then all k are listed)
   const int bin = find_bin(need, bin_at, before);
   if (lane > 0) return;
   st.need = need;
@@ -887,7 +890,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_draw_kernel(SampleParams
   const uint64_t least = st.least, need = st.need, before = st.before;
   const float from = st.from, end = st.end;
   const uint32_t n = st.listed;
-  const float top_p = kind == ROW_COUNT && p.top_p ? p.top_p[request] : 1.0f;
+  const float top_p = kind == ROW_COUNT ? st.top_p : 1.0f;
   const uint32_t u = p.token ? p.u[row] : 0;
   if (t < SP_MAX_CHUNKS) {
     const uint64_t sum = t < p.chunks ? st.total[t] : 0;
