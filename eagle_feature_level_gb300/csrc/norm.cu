@@ -6,7 +6,7 @@
 //
 // Bound: memory where rows are many (8192 x 8192 to 8 bits with the residual: 86 us, 470 MB, 5.5 TB/s; with blocks that end
 // with their rows 96), else the latency of a launch, of loads and of two sums (8 x 4096: 2.2 us; 777 x 5120 in fp32:
-// 13.5 us for 56 MB).  Blocks of up to 512 threads are held to 64 registers, so that an SM has two: one waits for
+// 12.8 us for 56 MB; past 16384 columns a block is alone on its SM: 777 x 28672 80 us, 313 MB).  Blocks of up to 512 threads are held to 64 registers, so that an SM has two: one waits for
 // its sums while the other works.
 #include "internal.h"
 #include "common.cuh"
@@ -25,7 +25,7 @@ struct NormParams {
   const float* gain;
   float eps;
   int rows, cols;
-  int threads;             // of a row, a power of two from 32 on
+  int threads;             // of a row: a power of two from 32 on, or a block of 256 or more
   int* status;
   uint64_t* stamp;
 };
@@ -33,43 +33,54 @@ struct NormParams {
 // OUT: 0 bf16, -1 fp32, otherwise a microscaled format.
 template <typename T, typename R, int OUT, int UNITS, int MOST>
 __global__ void __launch_bounds__(MOST, MOST == 512 ? 2 : 1) norm_kernel(NormParams p) {
+  // (four units leave no registers for gains and the next row)
+  constexpr bool AHEAD = UNITS <= 2;
   __shared__ float s_sum[2][32];
   LaunchStamp ls(p.stamp);
   pdl_wait();
   ls.waited();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t = threadIdx.x & (p.threads - 1);
+  const int t = p.threads < 256 ? threadIdx.x & (p.threads - 1) : threadIdx.x;
   const int per_block = blockDim.x / p.threads, step = gridDim.x * per_block;
   int row = blockIdx.x * per_block + threadIdx.x / p.threads;
   const int rounds = (p.rows + step - 1) / step;           // the same for a block's threads
   const MxFactor f = OUT > 0 ? mx_factor(p.m) : MxFactor{1.0f, 1.0f, 1.0f};
   int col[UNITS];
   bool own[UNITS];
-  float gain[UNITS][8];
+  float gain[AHEAD ? UNITS : 1][8];
   Raw8<T> x[UNITS];
   Raw8<R> res[UNITS];
 #pragma unroll
   for (int u = 0; u < UNITS; ++u) {
     col[u] = (u * p.threads + t) * 8;
     own[u] = col[u] < p.cols;
-    if (own[u] && row < p.rows) {
+    if (AHEAD && own[u] && row < p.rows) {
       x[u].load(static_cast<const T*>(p.x) + row * p.ld_x + col[u]);
       if (p.res) res[u].load(static_cast<const R*>(p.res) + row * p.ld_res + col[u]);
     }
   }
-#pragma unroll
-  for (int u = 0; u < UNITS; ++u) {
-    if (p.gain && own[u]) load8(p.gain + col[u], gain[u]);
+  auto gains = [&](int u, float (&g)[8]) {
+    if (p.gain && own[u]) load8(p.gain + col[u], g);
     else
 #pragma unroll
-      for (int i = 0; i < 8; ++i) gain[u][i] = 1.0f;
-  }
+      for (int i = 0; i < 8; ++i) g[i] = 1.0f;
+  };
+  if (AHEAD)
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) gains(u, gain[AHEAD ? u : 0]);
   bool bad = false;
   for (int k = 0; k < rounds; ++k, row += step) {
     const bool there = row < p.rows;
     float h[UNITS][8];
     float sum = 0.0f;
+    if (!AHEAD)
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u)
+        if (there && own[u]) {
+          x[u].load(static_cast<const T*>(p.x) + row * p.ld_x + col[u]);
+          if (p.res) res[u].load(static_cast<const R*>(p.res) + row * p.ld_res + col[u]);
+        }
 #pragma unroll
     for (int u = 0; u < UNITS; ++u) {
       if (there && own[u]) {
@@ -88,7 +99,7 @@ __global__ void __launch_bounds__(MOST, MOST == 512 ? 2 : 1) norm_kernel(NormPar
     // the next row is on its way under this one's work
 #pragma unroll
     for (int u = 0; u < UNITS; ++u)
-      if (own[u] && row + step < p.rows) {
+      if (AHEAD && own[u] && row + step < p.rows) {
         x[u].load(static_cast<const T*>(p.x) + (row + step) * p.ld_x + col[u]);
         if (p.res) res[u].load(static_cast<const R*>(p.res) + (row + step) * p.ld_res + col[u]);
       }
@@ -103,15 +114,16 @@ __global__ void __launch_bounds__(MOST, MOST == 512 ? 2 : 1) norm_kernel(NormPar
       float* s = s_sum[k & 1];                   // (in turn: the last row's sums may still be read)
       if (lane == 0) s[warp] = sum;
       __syncthreads();
-      const int nw = p.threads >> 5, w0 = warp & ~(nw - 1);
+      const int nw = p.threads >> 5, w0 = p.threads < 256 ? warp & ~(nw - 1) : 0;
       sum = warp_sum(lane < nw ? s[w0 + lane] : 0.0f);
     }
     const float inv = 1.0f / sqrtf(sum / static_cast<float>(p.cols) + p.eps);
 #pragma unroll
     for (int u = 0; u < UNITS; ++u) {
       float y[8];
+      if (!AHEAD) gains(u, gain[0]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = h[u][i] * inv * gain[u][i];
+      for (int i = 0; i < 8; ++i) y[i] = h[u][i] * inv * gain[AHEAD ? u : 0][i];
       const bool in = there && own[u];
       if (OUT > 0) {
         if (!in)
@@ -165,8 +177,11 @@ cudaError_t launch_norm(eagle_ctx* ctx, const eagle_norm* n, int* status, cudaSt
   p.cols = n->cols;
   p.status = status;
   const int eights = ceil_div(n->cols, 8);
+  // two units a thread (four past 16384 columns): as many whole warps as that takes, where a row has a block to itself (777
+  // x 5120: 320 threads, three blocks an SM, 12.7 us; 512, the next power of two, 13.5; 8192 rows to NV_FP4 85 and 104)
   p.threads = 32;
-  while (p.threads < 1024 && p.threads * 2 < eights) p.threads <<= 1;
+  while (p.threads < 256 && p.threads * 2 < eights) p.threads <<= 1;
+  if (p.threads * 2 < eights) p.threads = ceil_div(ceil_div(eights, eights <= 2048 ? 2 : 4), 32) * 32;
   const int need = ceil_div(eights, p.threads);
   const int units = need <= 1 ? 1 : need <= 2 ? 2 : 4;
   const int block = p.threads < 256 ? 256 : p.threads;
