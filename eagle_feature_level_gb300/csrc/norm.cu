@@ -6,8 +6,8 @@
 //
 // Bound: memory where rows are many (8192 x 8192 to 8 bits with the residual: 86 us, 470 MB, 5.5 TB/s; with blocks that end
 // with their rows 96), else the latency of a launch, of loads and of two sums (8 x 4096: 2.2 us; 777 x 5120 in fp32:
-// 12.8 us for 56 MB; past 16384 columns a block is alone on its SM: 777 x 28672 80 us, 313 MB).  Blocks of up to 512 threads are held to 64 registers, so that an SM has two: one waits for
-// its sums while the other works.
+// 12.8 us for 56 MB; past 16384 columns a block is alone on its SM: 777 x 28672 80 us, 313 MB).  Blocks of up to 512
+// threads are held to 64 registers, so that an SM has two: one waits for its sums while the other works.
 #include "internal.h"
 #include "common.cuh"
 #include "mx.cuh"

@@ -869,3 +869,57 @@ def test_offsets_beyond_32_bits():
     assert token[:-1].unique().tolist() == [0] and int(token[-1]) == V - 2
     assert probs[-1, V - 2] == 1 and probs[0, :4].tolist() == pytest.approx([1 / 3, 1 / 3, 1 / 3, 0.0])
     assert engine().status() == 0
+
+
+def test_two_streams_each_with_its_workspace():
+    """Calls of two contexts at once, and graphs of one context in turn, give what each alone gives."""
+    engines = [R.Engine(dict(d=512, n_q_heads=4, n_kv_heads=2, head_dim=64, d_ff=64, vocab=64), max_batch=64, max_rows=8,
+                        max_expanded=1, max_children=1, max_tree=2, max_prefix=64, device="cuda") for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in engines]
+
+    def job(e, i, seed):
+        """A norm into 4 bits, a product and a sampling of its rows, of sizes that differ from seed to seed."""
+        rows, outs = [(40, 5000), (7, 20000), (130, 1000), (1, 32000)][seed % 4]
+        t, w, z = R.MxTensor(e, rows, 256, "fp4"), R.MxTensor(e, outs, 256, "fp4"), torch.empty(rows, outs, device="cuda")
+        x, res, h = normal(seed, rows, 256), normal(seed + 20, rows, 256), torch.empty(rows, 256, device="cuda")
+        w.quantize(normal(seed + 50, outs, 256) * 0.2)
+        out = i32([-7] * rows), torch.empty(rows, outs, device="cuda")
+        u = normal(seed + 99, rows).view(torch.int32)
+        s = R.Sampler(e, rows, f32([0.5 + 0.1 * (r % 7) for r in range(rows)]), i32([[0, 40, 700][r % 3] for r in range(rows)]),
+                      f32([[0.9, 1.0][r % 2] for r in range(rows)]))
+
+        def run():
+            R.add_norm(e, x, t, None, res, h)
+            R.mx_linear(t, w, z)
+            s(z, u, out[0], None, out[1])
+        return run, out
+
+    def results(alone):
+        jobs = [[job(e, i, 4 * i + k) for k in range(4)] for i, e in enumerate(engines)]
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for k in range(4):
+                for i, st in enumerate(streams):
+                    with torch.cuda.stream(st):
+                        jobs[i][k][0]()
+                    if alone:
+                        torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        assert all(e.status() == 0 for e in engines)
+        return [o for js in jobs for _, out in js for o in out], jobs
+    expected, _ = results(True)
+    together, jobs = results(False)
+    assert all(torch.equal(a, b) for a, b in zip(expected, together))
+    graphs = []
+    for run, out in jobs[0]:
+        for o in out:
+            o.fill_(-3)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run()
+        graphs.append(g)
+    for k in (2, 0, 3, 1, 1, 2, 0, 3):
+        graphs[k].replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(expected[:8], [o for _, out in jobs[0] for o in out]))
+    assert engines[0].status() == 0
