@@ -122,8 +122,8 @@ _DTYPE = {torch.bfloat16: B.DTYPE_BF16, torch.float32: B.DTYPE_F32}
 
 def _rows2d(t: torch.Tensor, rows: int, cols: int, device, types=_DTYPE):
     """(type, address, pitch) of [rows][cols] with contiguous rows."""
-    if t.dtype not in types or t.shape != (rows, cols) or (cols > 1 and t.stride(1) != 1) or t.device != device:
-        raise ValueError(f"needs [{rows}][{cols}] of {[str(x) for x in types]} with contiguous rows on {device}")
+    if t.dtype not in types or t.shape != (rows, cols) or (cols > 1 and t.stride(1) != 1) or t.device != device or not t.is_cuda:
+        raise ValueError(f"needs [{rows}][{cols}] of {[str(x) for x in types]} with contiguous rows on {device}, a GPU")
     return _DTYPE[t.dtype], _p(t), (t.stride(0) if rows > 1 else -(-cols // 8) * 8)
 
 
@@ -131,8 +131,8 @@ def _each(t: Optional[torch.Tensor], n: int, dtype, device) -> Optional[int]:
     """Address of n contiguous values of a type (None: none)."""
     if t is None:
         return None
-    if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"needs {n} contiguous {dtype} on {device}")
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or t.device != device or not t.is_cuda:
+        raise ValueError(f"needs {n} contiguous {dtype} on {device}, a GPU")
     return _p(t)
 
 
@@ -511,8 +511,8 @@ class MxTensor:
         self.data = torch.empty(n_data, **u8) if data is None else data
         self.scale = torch.empty(n_scale, **u8) if scale is None else scale
         for t, n in ((self.data, n_data), (self.scale, n_scale)):
-            if t.dtype != torch.uint8 or t.numel() < n or not t.is_contiguous():
-                raise ValueError(f"needs {n} contiguous bytes")
+            if t.dtype != torch.uint8 or t.numel() < n or not t.is_contiguous() or not t.is_cuda:
+                raise ValueError(f"needs {n} contiguous bytes on a GPU")
         self.tensor_scale = tensor_scale
         self.c = B.eagle_mx(_p(self.data), _p(self.scale), _each(tensor_scale, 1, torch.float32, self.data.device), rows,
                             cols, MX_FORMATS[fmt])

@@ -626,6 +626,25 @@ def test_wrappers_check_their_tensors():
         s(torch.zeros(5, 64, device="cuda"), i32([0] * 5), i32([0] * 5))
 
 
+def test_wrappers_refuse_host_memory():
+    """Tensors of the host among the arguments, or all of them: nothing is launched."""
+    e = engine()
+    x, t, z = torch.zeros(4, 64), mx("fp8", 4, 64), torch.zeros(4, 64, device="cuda")
+    before = B.eagle_launch_count(e.ctx)
+    s = R.Sampler(e, 4)
+    for call in (lambda: R.add_norm(e, x, torch.zeros_like(x)), lambda: R.add_norm(e, x, t), lambda: R.add_norm(e, z, x),
+                 lambda: R.add_norm(e, z, t, torch.ones(64)), lambda: R.mx_linear(t, t, torch.zeros(4, 8)),
+                 lambda: R.mx_linear(t, t, torch.zeros(4, 8, device="cuda")[:, :4], torch.zeros(4)), lambda: t.unpack(x),
+                 lambda: R.Sampler(e, 4, torch.ones(4)), lambda: R.Sampler(e, 4, torch.ones(4, device="cuda"), top_p=torch.ones(4)),
+                 lambda: s(x, torch.zeros(4, dtype=torch.int32), torch.zeros(4, dtype=torch.int32)), lambda: s(z, probs=x),
+                 lambda: s(z, torch.zeros(4, dtype=torch.int32), i32([0] * 4)),
+                 lambda: R.MxTensor(e, 4, 64, "fp8", data=torch.zeros(256, dtype=torch.uint8)),
+                 lambda: R.MxTensor(e, 4, 64, "nv4", torch.ones(1))):
+        with pytest.raises(ValueError):
+            call()
+    assert B.eagle_launch_count(e.ctx) == before
+
+
 # ---- streams, graphs, runs ---------------------------------------------------------------
 
 def test_other_stream_and_second_engine():
