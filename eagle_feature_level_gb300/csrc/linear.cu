@@ -61,6 +61,7 @@ struct LinearParams {
   int stages;
   uint32_t stage_bytes, b_bytes;
   uint32_t acc_cols, sf_at, sf_cols, tmem_cols;
+  int sf_log;              // places for a stage's scales in tensor memory, two or four, as a power of two
   int once;                // A is read once
   int* status;
   uint64_t* stamp;
@@ -68,7 +69,7 @@ struct LinearParams {
 
 struct LinearShared {
   uint64_t full[LN_MAX_STAGES], empty[LN_MAX_STAGES];
-  uint64_t sf_full[2];
+  uint64_t sf_full[4];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t part_full, part_free;
   uint64_t drained[2];
@@ -319,35 +320,37 @@ __device__ __forceinline__ void produce(const LinearParams& p, LinearShared& sh,
       sm100::mbar_wait(&sh.full[i % p.stages], (i / p.stages) & 1, &sh.never);
 }
 
-// Scales to tensor memory, a stage ahead of the products: two places in turn, the products of the stage before last being
-// through with the one that is written.  RB: 128-row blocks of x's scales in a tile.
+// Scales to tensor memory, ahead of the products: places in turn, the products of as many stages before being through with the
+// one that is written.  RB: 128-row blocks of x's scales in a tile.
 template <int FMT, int RB, bool PAIR>
 __device__ __forceinline__ void spread_scales(const LinearParams& p, LinearShared& sh, uint8_t* ring, uint32_t tmem,
                                               int first, int step, int k0, int k1, volatile int* abort) {
   constexpr int GPS = groups_per_stage<FMT>();
   const uint32_t ring0 = sm100::smem_u32(ring) + LN_A_BYTES + p.b_bytes;
   const uint32_t lead = elect_one();
-  int slot = 0, old = p.stages - 2;
+  const int places = 1 << p.sf_log;
+  int slot = 0, old = p.stages - places;
   uint32_t phase = 0, old_phase = 1;
   const int total = first < p.tiles ? ((p.tiles - first + step - 1) / step) * (k1 - k0) : 0;
   for (int i = 0; i < total; ++i) {
     bool ok = sm100::mbar_wait(&sh.full[slot], phase, abort);
-    ok = ok && (i < 2 || sm100::mbar_wait(&sh.empty[old], old_phase, abort));
+    ok = ok && (i < places || sm100::mbar_wait(&sh.empty[old], old_phase, abort));
     if (!__all_sync(0xffffffffu, ok)) {
       *abort = 1;
       return;
     }
     sm100::tc_fence_after();
     const uint32_t s = ring0 + static_cast<uint32_t>(slot) * p.stage_bytes;
-    const uint32_t sfa = tmem + p.sf_at + (i & 1) * p.sf_cols, sfb = sfa + 4 * GPS;
+    const int place = i & (places - 1);
+    const uint32_t sfa = tmem + p.sf_at + place * p.sf_cols, sfb = sfa + 4 * GPS;
 #pragma unroll
     for (int g = 0; g < GPS; ++g) {
       copy_scales<PAIR>(sfa + 4 * g, s + 512 * g, lead);
 #pragma unroll
       for (int b = 0; b < RB; ++b) copy_scales<PAIR>(sfb + 4 * (g * RB + b), s + 512 * ((1 + b) * GPS + g), lead);
     }
-    commit_if<PAIR, false>(&sh.sf_full[i & 1], lead);
-    sm100::mbar_arrive_if(&sh.sf_full[i & 1], lead);   // (and that the stage itself is there)
+    commit_if<PAIR, false>(&sh.sf_full[place], lead);
+    sm100::mbar_arrive_if(&sh.sf_full[place], lead);   // (and that the stage itself is there)
     if (++slot == p.stages) {
       slot = 0;
       phase ^= 1;
@@ -378,13 +381,14 @@ __device__ __forceinline__ void multiply(const LinearParams& p, LinearShared& sh
     const uint32_t d = tmem + static_cast<uint32_t>(buf) * p.acc_cols;
     uint32_t acc = 0;
     for (int k = k0; k < k1; ++k, ++i) {
-      if (!__all_sync(0xffffffffu, sm100::mbar_wait(&sh.sf_full[i & 1], (i >> 1) & 1, abort))) {
+      const int place = i & ((1 << p.sf_log) - 1);
+      if (!__all_sync(0xffffffffu, sm100::mbar_wait(&sh.sf_full[place], (i >> p.sf_log) & 1, abort))) {
         *abort = 1;
         return;
       }
       sm100::tc_fence_after();
       const uint32_t st = ring0 + static_cast<uint32_t>(slot) * p.stage_bytes;
-      const uint32_t sfa = tmem + p.sf_at + (i & 1) * p.sf_cols, sfb = sfa + 4 * GPS + b_off;
+      const uint32_t sfa = tmem + p.sf_at + place * p.sf_cols, sfb = sfa + 4 * GPS + b_off;
       const uint32_t ad = st >> 4, bd = (st + LN_A_BYTES) >> 4;
       const int left = p.kbytes - k * LN_KB;           // bytes: 32 a product
 #pragma unroll
@@ -580,8 +584,8 @@ __global__ void __launch_bounds__(LN_THREADS, 1)
       sm100::mbar_init(&sh.full[i], 2);
       sm100::mbar_init(&sh.empty[i], 1);
     }
+    for (int i = 0; i < 4; ++i) sm100::mbar_init(&sh.sf_full[i], 2);
     for (int i = 0; i < 2; ++i) {
-      sm100::mbar_init(&sh.sf_full[i], 2);
       sm100::mbar_init(&sh.acc_full[i], 1);
       sm100::mbar_init(&sh.acc_empty[i], PAIR ? 8 : 4);
     }
@@ -714,10 +718,11 @@ cudaError_t launch_linear(eagle_ctx* ctx, const eagle_mx* x, const eagle_mx* w, 
     p.sf_cols = static_cast<uint32_t>(4 * gps * (1 + p.rb));
     p.n_acc = 2 * p.acc_cols + 2 * p.sf_cols <= 512 ? 2 : 1;
     p.sf_at = static_cast<uint32_t>(p.n_acc) * p.acc_cols;
-    p.tmem_cols = 32;
-    while (p.tmem_cols < p.sf_at + 2 * p.sf_cols) p.tmem_cols <<= 1;
     const size_t part = c.split > 1 ? static_cast<size_t>(c.nt) * LN_M * 4 : 0;
     p.stages = static_cast<int>(std::min<size_t>(LN_MAX_STAGES, (LN_SMEM - 1024 - part) / p.stage_bytes));
+    p.sf_log = p.stages >= 4 && p.sf_at + 4 * p.sf_cols <= 512 ? 2 : 1;
+    p.tmem_cols = 32;
+    while (p.tmem_cols < p.sf_at + (p.sf_cols << p.sf_log)) p.tmem_cols <<= 1;
     smem = 1024 + static_cast<size_t>(p.stages) * p.stage_bytes + part;
   };
   // The one that a rough count of an SM's cycles gives the least time: a stage costs its products (2 cycles a row of B),
