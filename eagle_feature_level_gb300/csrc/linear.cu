@@ -17,9 +17,10 @@
 // rows: the weights' bytes from memory (16 x 8192 x 32000: 25 us, 6.0 TB/s; 1 x 4096 x 12288: 7.8, 3.6 TB/s, of which some
 // 4 us until the first products and behind the last).
 //
-// Few tiles: a cluster of 2, 4 or 8 CTAs splits a tile's inner dimension; each writes its partial to its own shared memory
-// and sums its share of the rows over all of them, in rank order (8 x 8192 x 8192 in 8 bits: 14.8 us; 3, 5 or 6 ways were
-// nowhere the best).
+// Few tiles: a cluster of up to 8 CTAs splits a tile's inner dimension; each writes its partial to its own shared memory
+// and sums its share of the rows over all of them, in rank order (8 x 8192 x 8192 in 8 bits: 14.9 us by two, 20.5 by one;
+// 96 x 27648 x 5120 in FP4 20.5 by three, 26 by two, 35 by one; 442 x 16640 x 1072 in 8 bits, tiles of 128 rows by four
+// 19.5, of 64 by two 25.7).
 #include <algorithm>
 
 #include "internal.h"
@@ -320,8 +321,8 @@ __device__ __forceinline__ void produce(const LinearParams& p, LinearShared& sh,
       sm100::mbar_wait(&sh.full[i % p.stages], (i / p.stages) & 1, &sh.never);
 }
 
-// Scales to tensor memory, ahead of the products: places in turn, the products of as many stages before being through with the
-// one that is written.  RB: 128-row blocks of x's scales in a tile.
+// Scales to tensor memory, ahead of the products: places in turn, the products of as many stages before being through with
+// the one that is written.  RB: 128-row blocks of x's scales in a tile.
 template <int FMT, int RB, bool PAIR>
 __device__ __forceinline__ void spread_scales(const LinearParams& p, LinearShared& sh, uint8_t* ring, uint32_t tmem,
                                               int first, int step, int k0, int k1, volatile int* abort) {
@@ -725,16 +726,20 @@ cudaError_t launch_linear(eagle_ctx* ctx, const eagle_mx* x, const eagle_mx* w, 
     while (p.tmem_cols < p.sf_at + (p.sf_cols << p.sf_log)) p.tmem_cols <<= 1;
     smem = 1024 + static_cast<size_t>(p.stages) * p.stage_bytes + part;
   };
-  // The one that a rough count of an SM's cycles gives the least time: a stage costs its products (2 cycles a row of B),
-  // its bytes from L2 (64 a cycle) or, where the weights are read once, those from memory (24), whichever is more; a tile
-  // is read out under the next one's products where there are two accumulators; the slowest cluster counts.
+  // The one that a rough count of an SM's cycles gives the least time.  A stage costs its products (2 cycles a row of B),
+  // its bytes (64 a cycle, and 40), 550 cycles in any case or, where the weights are read once, those that come from memory
+  // (24 bytes a cycle and SM with all SMs at it, 33 at most), whichever is the most; a tile is read out under the next one's
+  // products where there are two accumulators; the slowest cluster counts.  (Over 25 shapes from 1 to 1001 rows its choice
+  // was within 10 % of the best of all.)
   Choice best{false, 0, false, 1};
   double least = 1e30;
   auto consider = [&](const Choice& c) {
     settle(c);
     const int clusters = ctx->sm_count / (c.pair ? 2 : c.split);
     const double bytes = p.stage_bytes;
-    const double stage = std::max({2.0 * c.nt, bytes / 64.0 + 40.0, p.once ? bytes / 24.0 : 0.0});
+    const double active = std::min(p.tiles, clusters) * (c.pair ? 2.0 : c.split) / ctx->sm_count;
+    const double weights = p.once ? (LN_A_BYTES + 512.0 * gps) * std::max(active / 24.0, 1.0 / 33.0) : 0.0;
+    const double stage = std::max({2.0 * c.nt, bytes / 64.0 + 40.0, weights, 550.0});
     const double work = ceil_div(p.steps, c.split) * stage, read = (c.by_row ? 25.0 : 45.0) * c.nt + 400.0;
     const double tile = c.split > 1 ? work + read + 2500.0 : p.n_acc == 1 ? work + read + 2500.0 : std::max(work, read);
     const double cost = ceil_div(p.tiles, clusters) * tile + read;
@@ -744,11 +749,11 @@ cudaError_t launch_linear(eagle_ctx* ctx, const eagle_mx* x, const eagle_mx* w, 
     }
   };
   const int all = ceil_div(x->rows, 16) * 16, outs = ceil_div(w->rows, 16) * 16;
-  for (int split = 1; split <= 8 && split <= p.steps; split *= 2)
+  for (int split = 1; split <= 8 && split <= p.steps; ++split)
     for (int q = 0; q < 4; ++q) {
       const int nt = q == 0 ? all : 64 * q;
       if (q == 0 ? nt > 192 : nt >= x->rows) continue;
-      if (split == 1 || nt <= 64) consider({false, nt, false, split});
+      if (split == 1 || nt <= 128) consider({false, nt, false, split});
     }
   for (int by_row = 0; by_row < 2; ++by_row) {   // (B's tiles: places of scales 64 rows apart)
     const int b = by_row ? outs : all, a = by_row ? x->rows : w->rows;
