@@ -8,8 +8,8 @@
 // that an SM takes in less for as many products.  A stage of the ring holds 128 bytes of every row of both (256 four-bit or
 // 128 eight-bit elements, 4 MMAs) and their scales, which lie in memory as the 512-byte groups that one tcgen05.cp spreads
 // over tensor memory.  Warp roles: a producer for A and one for B (with the scales), one warp that issues the products and
-// one the scales' copies (an instruction of either takes some 60 cycles to issue: 4096 x 8192 x 10240 in one warp 310 us,
-// apart 148), four that read the accumulator out; two accumulators, so that a tile is read out under the next one's
+// one the scales' copies (an instruction of either takes some 60 cycles to issue, 90 from a branch of one lane: 4096 x 8192
+// x 10240 310 us so, 154 by a whole warp, 147 by two), four that read the accumulator out; two accumulators, so that a tile is read out under the next one's
 // products.
 //
 // Bound, many rows: what an SM takes in, 64 bytes a cycle: a stage of 192 rows of B is 46 KB for a CTA alone and 34 KB for

@@ -835,6 +835,14 @@ def test_linear_many_rows_any_outputs(fmt, outs):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("rows,cols,outs", [(16, 8192, 3840), (9, 8192, 3200), (3, 8192, 2688), (100, 8192, 6400), (128, 16384, 2600),
+                                            (77, 12288, 3330), (250, 8192, 1500), (40, 4128, 900)])
+def test_linear_inner_dimension_in_parts(fmt, rows, cols, outs):
+    """Few tiles and many columns: the inner dimension in up to eight parts, of unlike numbers of stages."""
+    check_linear(fmt, rows, cols, outs, F32, True, seed=rows + outs)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_linear_many_rows_with_a_non_finite_block(fmt):
     x = normal(21, 700, 512)
     x[431, 100] = INF
