@@ -22,7 +22,7 @@
 //
 // Bound: instructions where rows are flat (64 rows of 131072 in bf16: top-p of 0.95 at t = 1.3 85 us, issue slots of the
 // busy SMs full), else the latency of each kernel's loads and exchanges (greedy 15 us, top-k of 50 33, top-p of 0.7 at
-// t = 0.5 41, min-p of 0.05 28, no cut 43; one row of 32000: top-k of 400 and top-p 18).  A cluster of CTAs that keeps a row
+// t = 0.5 41, min-p of 0.05 28, no cut 43; one row of 32000: top-k of 400 and top-p 17).  A cluster of CTAs that keeps a row
 // in shared memory through all steps saves launches, but leaves the SMs waiting for its exchanges: those 64
 // rows 209, 26, 66, 89, 56 and 66 us, the one row 17, and 64 rows of all sorts 113 where this takes 55.
 #include <algorithm>
@@ -694,29 +694,48 @@ __device__ __forceinline__ void add_words(uint32_t& lo, uint32_t& hi, uint64_t w
   if (h) atomicAdd(&hi, h);
 }
 
-// Sorts the threads' e, the first n of them other than 0, largest first: a bitonic network, by shuffles where partners
-// share a warp, else over s.list, by as many warps as it takes.
+// Sorts the threads' e, the first n of them other than 0 and unlike one another, largest first: a warp's own by a bitonic
+// network of shuffles, then runs by twos, each element's place being its own and the number of the other run's before it.
+// (One row of 32000 with 430 tokens listed: 17.1 us, 17.4 with the network all the way.)  It overwrites s.list and s.count.
 __device__ __forceinline__ void sort_threads(SampleShared& s, int n, uint64_t& e) {
-  const int t = threadIdx.x;
+  const int t = threadIdx.x, lane = t & 31;
   int width = 32;
   while (width < n) width <<= 1;
   if (t >= width) return;
 #pragma unroll 1
-  for (int size = 2; size <= width; size <<= 1) {
+  for (int size = 2; size <= 32; size <<= 1) {
 #pragma unroll 1
     for (int stride = size >> 1; stride > 0; stride >>= 1) {
-      uint64_t o;
-      if (stride < 32) {
-        o = __shfl_xor_sync(0xffffffffu, e, stride);
-      } else {
-        sm100::named_barrier(1, width);
-        s.list[t] = e;
-        sm100::named_barrier(1, width);
-        o = s.list[t ^ stride];
-      }
-      const bool larger = ((t & stride) == 0) == ((t & size) == 0);   // of the two, this thread keeps the larger
+      const uint64_t o = __shfl_xor_sync(0xffffffffu, e, stride);
+      const bool larger = ((lane & stride) == 0) == ((lane & size) == 0);   // of the two, this thread keeps the larger
       e = (e > o) == larger ? e : o;
     }
+  }
+  if (width == 32) return;
+  static_assert(sizeof(s.count) >= sizeof(s.list), "a second list");
+  uint64_t* from = s.list;
+  uint64_t* to = reinterpret_cast<uint64_t*>(s.count);
+  from[t] = e;
+  sm100::named_barrier(1, width);
+#pragma unroll 1
+  for (int run = 32; run < width; run <<= 1) {
+    const uint64_t* other = from + ((t & ~(run - 1)) ^ run);
+    const bool later = (t & run) != 0;           // this run stands behind the other: equals (zeros) of that come first
+    int before = 0;
+#pragma unroll 1
+    for (int step = run; step > 0; step >>= 1) {
+      const int at = before + step - 1;
+      if (at < run) {
+        const uint64_t o = other[at];
+        if (o > e || (later && o == e)) before += step;
+      }
+    }
+    to[(t & ~(2 * run - 1)) + (t & (run - 1)) + before] = e;
+    sm100::named_barrier(1, width);
+    e = to[t];
+    uint64_t* spare = from;
+    from = to;
+    to = spare;
   }
 }
 
@@ -883,21 +902,24 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_draw_kernel(SampleParams
   const int request = row / p.rows_each;
   if (unused(p, row, request)) return;
   SampleRow& st = p.state[blockIdx.x];
+  // (everything at once: what is not there is not used)
+  uint64_t e, sum = 0;
+  asm volatile("ld.global.u64 %0, [%1];" : "=l"(e) : "l"(&st.list[t]) : "memory");
+  if (t < p.chunks) asm volatile("ld.global.u64 %0, [%1];" : "=l"(sum) : "l"(&st.total[t]) : "memory");
   const int kind = st.kind;
-  if (kind < ROW_WHOLE) return;
-  const T* logits = static_cast<const T*>(p.logits) + row * p.ld;
   const Row r = row_of(st);
   const uint64_t least = st.least, need = st.need, before = st.before;
   const float from = st.from, end = st.end;
   const uint32_t n = st.listed;
   const float top_p = kind == ROW_COUNT ? st.top_p : 1.0f;
   const uint32_t u = p.token ? p.u[row] : 0;
+  if (kind < ROW_WHOLE) return;
+  const T* logits = static_cast<const T*>(p.logits) + row * p.ld;
   if (t < SP_MAX_CHUNKS) {
-    const uint64_t sum = t < p.chunks ? st.total[t] : 0;
     s.total_lo[t] = static_cast<uint32_t>(sum);
     s.total_hi[t] = static_cast<uint32_t>(sum >> 32);
   }
-  uint64_t e = t < static_cast<int>(min(n, static_cast<uint32_t>(SP_SORT))) ? st.list[t] : 0;
+  if (t >= static_cast<int>(min(n, static_cast<uint32_t>(SP_SORT)))) e = 0;
   __syncthreads();
   if (n > SP_SORT) {
     const Tokens<T> tk{logits, p.vocab, st.list, n <= SP_LIST ? n : 0};
