@@ -132,7 +132,8 @@ cudaError_t launch(eagle_ctx* ctx, QuantKernel k, const eagle_mx* m, const void*
   p.x = x;
   p.ld = ld;
   p.chunks = ceil_div(m->cols, 256);
-  // a warp keeps to its 256 columns and goes down the rows; as many warps as there are rows for, up to 96 an SM
+  // a warp keeps to its 256 columns and goes down the rows; as many warps as there are rows for, up to 96 an SM (4096 x 8192
+  // to NV_FP4: two rows in flight 26.1 us, one 29.5, four 26.5; 48 warps an SM 29.4, 160 26.4)
   const int most = 96 * ctx->sm_count / p.chunks;
   p.step = most < 1 ? 1 : m->rows < most ? m->rows : most;
   p.status = status;

@@ -22,7 +22,7 @@
 //
 // Bound: instructions where rows are flat (64 rows of 131072 in bf16: top-p of 0.95 at t = 1.3 85 us, issue slots of the
 // busy SMs full), else the latency of each kernel's loads and exchanges (greedy 15 us, top-k of 50 33, top-p of 0.7 at
-// t = 0.5 41, min-p of 0.05 28, no cut 43; one row of 32000: top-k of 400 and top-p 17).  A cluster of CTAs that keeps a row
+// t = 0.5 41, min-p of 0.05 28, no cut 43; a row of 32000: top-k of 400 and top-p 17).  A cluster of CTAs that keeps a row
 // in shared memory through all steps saves launches, but leaves the SMs waiting for its exchanges: those 64
 // rows 209, 26, 66, 89, 56 and 66 us, the one row 17, and 64 rows of all sorts 113 where this takes 55.
 #include <algorithm>
