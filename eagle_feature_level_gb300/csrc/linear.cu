@@ -249,6 +249,13 @@ __device__ __forceinline__ TileAt tile_at(const LinearParams& p, int tile, uint3
 // the products each have a warp of their own (4096 x 8192 x 10240, NV_FP4: one branched-off lane for each of loads and
 // tensor core 310 us, whole warps 164, these 147).
 
+// Whose barriers count a CTA's loads: its own, but for a pair the first one's for both.  The CTA with the barriers asks for
+// the bytes, and where a wait ran out it stays until the loads under way have landed: the shared memory of a CTA that has
+// left may be another's.  (The CTAs of a split load for themselves, whatever their rank.)
+constexpr bool counts_loads(bool pair, uint32_t rank) { return !pair || rank == 0; }
+static_assert(counts_loads(false, 0) && counts_loads(false, 1) && counts_loads(false, 7), "every CTA of a split waits");
+static_assert(counts_loads(true, 0) && !counts_loads(true, 1), "a pair's first CTA waits for both");
+
 // Loads A (X false) or B (X true), and their scales, of this CTA's stages.  A pair's CTAs load 128 rows of A and half of
 // the tile's rows of B each (and all of those rows' scales), counted on the first one's barriers; their
 // scales come by a map too, whose box may reach into the next 128 rows' groups (no product takes those).
@@ -279,7 +286,7 @@ __device__ __forceinline__ void produce(const LinearParams& p, LinearShared& sh,
       if (PAIR) {
         if (elect_one()) {
           const uint32_t both = sm100::dsmem_addr(bar, 0);
-          if (rank == 0)
+          if (counts_loads(PAIR, rank))
             sm100::mbar_arrive_expect_tx(bar, 2 * (X ? p.b_bytes + GPS * 512u * p.rb : LN_A_BYTES + GPS * 512u));
           if (X) {
             pair_load_2d(st + LN_A_BYTES, map, k * LN_KB, at.b0 + static_cast<int>(rank) * (p.nt / 2), both);
@@ -316,7 +323,7 @@ __device__ __forceinline__ void produce(const LinearParams& p, LinearShared& sh,
     }
     if (*abort) break;
   }
-  if (*abort && rank == 0)                       // copies in flight land first (if the others asked for theirs too)
+  if (*abort && counts_loads(PAIR, rank))        // copies in flight land first (if the others asked for theirs too)
     for (int i = max(0, issued - p.stages); i < issued; ++i)
       sm100::mbar_wait(&sh.full[i % p.stages], (i / p.stages) & 1, &sh.never);
 }
