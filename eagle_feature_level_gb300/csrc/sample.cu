@@ -132,49 +132,56 @@ struct Row {
   float top, c_hi, c_lo;
 };
 
+// A token has one weight, whichever kernel computes it: a row's sums are of one kernel and its draw of another.  So every
+// product here that a sum takes is rounded by itself (__fmul_rn) or fused in so many words (fmaf), and none of it is left to
+// the compiler.
+
 // (top - z) log2(e) / t to fp32's precision; large for what has no weight at all.
-__device__ __forceinline__ float distance(const Row& r, float z) { return fminf((r.top - z) * r.c_hi, 100.0f); }
+__device__ __forceinline__ float distance(const Row& r, float z) { return fminf(__fmul_rn(r.top - z, r.c_hi), 100.0f); }
 
 // The difference to the top and its product with log2(e) / t as pairs of floats: the low part of y, given the high one.
 __device__ __forceinline__ float low_part(const Row& r, float z, float dh, float yh) {
   const float bb = dh - r.top;
   const float dl = (r.top - (dh - bb)) - (z + bb);
-  return fmaf(dh, r.c_hi, -yh) + fmaf(dh, r.c_lo, dl * r.c_hi);
+  return fmaf(dh, r.c_hi, -yh) + fmaf(dh, r.c_lo, __fmul_rn(dl, r.c_hi));
 }
 
-// floor(2^40 2^(-y)) from SP_FAR on, off by two units of 2^23 at most: y to both its parts, exp2 to 2 steps of fp32.
+// floor(2^40 2^(-y)) from SP_FAR on, off by two units of 2^23 at most (by one in half a million tokens): y to both its parts,
+// exp2 to 2^-22.7 over all of 40 - y's values, which fp32 has, and a product fused into its sum.
 __device__ __forceinline__ uint32_t far_weight(const Row& r, float z) {
-  const float dh = r.top - z, yh = dh * r.c_hi;
+  const float dh = r.top - z, yh = __fmul_rn(dh, r.c_hi);
   const float e = sm100::exp2(40.0f - yh);
-  const float x = fmaf(e, -0x1.62e43p-1f * low_part(r, z, dh, yh), e);
+  const float x = fmaf(e, __fmul_rn(-0x1.62e43p-1f, low_part(r, z, dh, yh)), e);
   const uint32_t w = __float_as_uint(__fadd_rd(fminf(x, 8388607.0f), 8388608.0f)) & 0x7fffffu;
   return yh < 41.0f ? w : 0u;
 }
 
-// floor(2^40 2^(-y)), off by a unit where the fraction is near a border.  The difference to the top and its product with
-// log2(e) / t are pairs of floats; y = k / 64 + r, |r| <= 1 / 128, and 2^(-r) - 1 = u + u^2 / 2 + u^3 / 6 + u^4 / 24 with
-// u = -r ln 2 (the next term is below 2^-44), the linear term a pair, the rest (2^-16) a float; table entry and product
-// then meet in 46-bit fixed point.
+// floor(2^40 2^(-y)), or one off where that is within 2^-5 of a whole number.  The difference to the top and its product with
+// log2(e) / t are pairs of floats; y = k / 64 + r, |r| <= 1 / 128, and u = -r ln 2 is a pair again, x + l, |l| <= 2^-22 |y|.
+// 2^(-r) - 1 = x + x^2 / 2 + x^3 / 6 + x^4 / 24 + (1 + x + x^2 / 2) l + ...: x and x^2 / 2 (up to 2^-16: as one float it
+// would cost half a unit) meet in a pair, what is left (2^-25) is a float; x^5 / 120 is taken with x^3 as its best multiple
+// of it up to ln(2) / 128, 0.87 (ln(2) / 128)^2 x^3 / 120, to 2^-47.  Table entry and product then meet in 46-bit fixed
+// point.  In units of 2^-40: the table and the fixed point 2^-7 each, the series 2^-7, the sums of 2^-25 three times 2^-10.
 __device__ __forceinline__ uint64_t near_weight(const Pow2* pow2, const Row& r, float z) {
   constexpr float MAGIC = 12582912.0f;           // 1.5 2^23: the sum's low bits are the rounded integer
   constexpr int MAGIC_BITS = 0x4B400000;
   const float dh = r.top - z;
-  const float yh = fminf(dh * r.c_hi, SP_FAR);   // (beyond: not used)
+  const float yh = fminf(__fmul_rn(dh, r.c_hi), SP_FAR);   // (beyond: not used)
   const float yl = low_part(r, z, dh, yh);
   const float kt = fmaf(yh, 64.0f, MAGIC);
   const int k = __float_as_int(kt) - MAGIC_BITS;
   const float rh = fmaf(kt - MAGIC, -0x1p-6f, yh);
-  const float rs = rh + yl, rl = yl - (rs - rh);
   constexpr float LN2_HI = 0x1.62e43p-1f, LN2_LO = -0x1.05c61p-29f;
-  const float uh = -rs * LN2_HI;
-  const float ul = fmaf(-rs, LN2_HI, -uh) - fmaf(rs, LN2_LO, rl * LN2_HI);
-  const float v = fmaf(uh * uh, fmaf(uh, fmaf(uh, 1.0f / 24.0f, 1.0f / 6.0f), 0.5f), ul);
+  const float x = __fmul_rn(-rh, LN2_HI);
+  const float l = fmaf(-rh, LN2_HI, -x) - fmaf(rh, LN2_LO, __fmul_rn(yl, LN2_HI));
+  const float h = 0.5f * x, p = __fmul_rn(h, x), eh = x + p;
+  const float rest = fmaf(__fmul_rn(p, x), fmaf(x, 1.0f / 12.0f, 1.0f / 3.0f + 4.25e-7f), fmaf(h, x, -(eh - x)));
+  const float el = fmaf(eh, l, rest) + l;
   const Pow2 t = pow2[k & 63];
-  const float a = t.hi * uh;
-  const float b = fmaf(t.hi, uh, -a) + fmaf(t.hi, v, t.lo * uh);
-  const float c = a + b, cl = b - (c - a);
-  const float c1 = fmaf(c, 0x1p24f, MAGIC);
-  const float rem = fmaf(c1 - MAGIC, -0x1p-24f, c) + cl;
+  const float a = __fmul_rn(t.hi, eh);
+  const float b = fmaf(t.hi, eh, -a) + fmaf(t.hi, el, __fmul_rn(t.lo, eh));
+  const float c1 = fmaf(a + b, 0x1p24f, MAGIC);
+  const float rem = fmaf(c1 - MAGIC, -0x1p-24f, a) + b;
   const int64_t w = static_cast<int64_t>(t.whole) +
                     (static_cast<int64_t>(__float_as_int(c1) - MAGIC_BITS) << 22) +
                     (__float_as_int(fmaf(rem, 0x1p46f, MAGIC)) - MAGIC_BITS);

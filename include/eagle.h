@@ -824,7 +824,10 @@ typedef struct {
 /* eagle_sample -- a row's distribution and a draw from it.  With z the row's
  * logits, m their maximum, t the temperature, token i has the weight
  *   w_i = floor(2^40 e^((z_i - m) / t))
- * (as everywhere draws are on whole weights).  In the order of falling z, the
+ * (as everywhere draws are on whole weights), as computed: a weight of 2^23 or
+ * more may be one off where the value under the floor is within 2^-4 of a whole
+ * number, a smaller one may be two off; a token has one weight in all that a
+ * call uses it for.  In the order of falling z, the
  * lower id first among equals,
  *   top_k keeps the first k tokens;
  *   top_p, of those, the shortest beginning whose weights sum to at least

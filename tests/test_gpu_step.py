@@ -950,3 +950,55 @@ def test_two_streams_each_with_its_workspace():
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(expected[:8], [o for _, out in jobs[0] for o in out]))
     assert engines[0].status() == 0
+
+
+# ---- single weights, words over whole rows, products on every path ------------------------------------
+
+def border(c, most, r):
+    """(n, m, u): of n tokens with the largest weight and m behind them of weight w, the word u draws one of the m exactly
+    if w >= c."""
+    one = 1 << 40
+    for _ in range(200000):
+        m = r.randint(1, most - 1)
+        n = min(max(int(m * c / one * r.uniform(0.3, 3.0)), 1), most - m)
+        u = -(-(n << 72) // (n * one + m * c))
+        if u < 1 << 32 and u * (n * one + m * (c - 1)) < n << 72:
+            return n, m, u
+    raise AssertionError(c)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_sample_single_weights(dtype):
+    """Weights between the largest and 2^23 of 2^40 are the definition's but within 1/16 of a whole number, where they may be
+    one off; below they are off by at most two.  (fp64's value is off by 2^-11 here.  From 2^23 on: the table's entries and the
+    fixed point of 46 bits cost 2^-7 each, the exponent's pair of floats and the series less: below 2^-5 in all.  Below 2^23:
+    exp2 by 2^-22.7 at most over all exponents that occur, a fused product by 2^-24: 1.75 in all.)"""
+    r = random.Random(5)
+    rows, V = [], 2000
+    for i in range(260):
+        t = [1.0, 1.3, 0.5, 0.05, 2.7, 1e-3][i % 6]
+        t = float(np.float32(t))
+        top = float(torch.tensor([3.0, -7.25, 100.125, 0.0, 0.7109375][i % 5], dtype=dtype))
+        far = i % 4 == 3
+        y = r.uniform(17.01, 30.0) if far else r.uniform(0.0, 16.9) if i % 2 else math.exp(-r.uniform(0.0, 9.0))
+        z = float(torch.tensor(top - y * math.log(2) * t, dtype=dtype))
+        w = math.exp((z - top) / t) * 2.0 ** 40
+        if z == top or w < 64 or ((w < 2.0 ** 23) != far) or abs(w / 2.0 ** 23 - 1) < 1e-3:
+            continue
+        slack = 2.0 if far else 1 / 16
+        low, high = math.floor(w - slack), math.floor(w + slack)
+        for c, above in ((low, True), (high + 1, False)):
+            rows.append((t, top, z, above, w) + border(c, V, r))
+    assert len(rows) > 300
+    z = torch.full((len(rows), V), -INF)
+    for i, (_, top, x, _, _, n, m, _) in enumerate(rows):
+        z[i, :n], z[i, n:n + m] = top, x
+    u = torch.tensor([q[-1] for q in rows], dtype=torch.int64)
+    u = torch.where(u >= 1 << 31, u - (1 << 32), u).int().cuda()
+    token = i32([-7] * len(rows))
+    R.Sampler(engine(), len(rows), f32([q[0] for q in rows]))(z.to(dtype).cuda(), u, token)
+    token = token.tolist()
+    wrong = [q[:5] for q, k in zip(rows, token) if (k >= q[5]) != q[3]]
+    assert not wrong, (len(wrong), len(rows), wrong[:5])
+    assert all(0 <= k < q[5] + q[6] for q, k in zip(rows, token))
+    assert engine().status() == 0
