@@ -1002,3 +1002,37 @@ def test_sample_single_weights(dtype):
     assert not wrong, (len(wrong), len(rows), wrong[:5])
     assert all(0 <= k < q[5] + q[6] for q, k in zip(rows, token))
     assert engine().status() == 0
+
+
+@pytest.mark.parametrize("vocab", [1, 2, 4097, 8191, 65537, 131072, 262144])
+@pytest.mark.parametrize("cut", ["none", "k", "p", "kp", "m"])
+def test_sample_words_over_whole_rows(vocab, cut):
+    """One flat row under words from the first to the last: every chunk of it is drawn from, and every draw is the
+    definition's but for the weights' slack."""
+    r = np.random.default_rng(vocab)
+    n = 224
+    words = np.concatenate(([0, 1, 2, 2 ** 31 - 1, 2 ** 31, 2 ** 31 + 1, 2 ** 32 - 2, 2 ** 32 - 1],
+                            (np.arange(160) * 2 ** 32 + 2 ** 31) // 160, r.integers(0, 2 ** 32, 56))).astype(np.int64)
+    dtype = F32 if vocab % 2 else BF16
+    row = normal(vocab, 1, vocab, dtype=dtype)
+    z = row.expand(n, vocab).contiguous()
+    k = max(vocab // 2, 1) if "k" in cut else 0
+    p = float(np.float32(0.9)) if "p" in cut else 1.0
+    m = 2.0 ** -5 if cut == "m" else 0.0
+    token = i32([-7] * n)
+    u = torch.tensor(np.where(words >= 2 ** 31, words - 2 ** 32, words), dtype=torch.int32, device="cuda")
+    R.Sampler(engine(), n, top_k=i32([k] * n), top_p=f32([p] * n), min_p=f32([m] * n))(z, u, token)
+    token, w, slack = token.cpu().numpy(), O.weights(f64(row[0]), 1.0), 2 * vocab
+    assert (token >= 0).all() and (token < vocab).all()
+    order, lo, hi = O.kept(f64(row[0]), w, k, p, slack=slack)
+    fits = []
+    for c in range(lo, hi + 1):
+        x = np.zeros_like(w)
+        x[order[:c]] = w[order[:c]]
+        x[x < m * 2.0 ** 40] = 0
+        cum = np.cumsum(x)
+        at = np.array([(int(a) * int(cum[-1])) >> 32 for a in words])
+        fits.append(bool(((cum[token] - x[token] - slack <= at) & (at < cum[token] + slack) & (x[token] > 0)).all()))
+    assert any(fits)
+    assert len(np.unique(token // 4096)) >= vocab // 4096
+    assert engine().status() == 0
