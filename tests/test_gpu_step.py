@@ -1036,3 +1036,41 @@ def test_sample_words_over_whole_rows(vocab, cut):
     assert any(fits)
     assert len(np.unique(token // 4096)) >= vocab // 4096
     assert engine().status() == 0
+
+
+PATHS = [(140, 1216, 6338), (31, 3840, 8587), (1086, 2304, 3143), (157, 3424, 2226), (153, 3584, 1989), (15, 12096, 5812),
+         (1003, 4832, 221), (36, 7904, 3758), (50, 7168, 3009), (41, 9280, 2936), (1391, 11040, 69), (73, 5888, 2445),
+         (496, 12320, 175), (40, 10272, 2428), (626, 13536, 127), (70, 7744, 1869), (299, 10976, 6012), (561, 2336, 6163),
+         (672, 1728, 924), (1341, 3296, 46), (396, 864, 4931), (727, 832, 1809), (929, 3392, 4352), (1162, 960, 2083)]
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("rows,cols,outs", PATHS)
+def test_linear_exact_products_on_every_path(fmt, rows, cols, outs):
+    """Whole numbers of at most 16 a product, sums below 2^18: every sum is exact, so one block lost, doubled or under
+    another's scale shows.  Shapes for both operand orders, single CTAs and pairs, tiles of 16 to 256 rows (64 and 192: scales
+    that start inside a group), and 1 to 8 parts of the inner dimension, the last stage of them part of one."""
+    r = gen(rows + cols)
+    def make(n):
+        t = mx(fmt, n, cols)
+        one, two, shift = {"fp8": (0x38, 0x40, 7)}.get(fmt, (2, 4, 3))
+        pick = lambda *s: torch.randint(0, 2, s, generator=r, device="cuda", dtype=torch.uint8)
+        code = one + (two - one) * pick(n, cols) | pick(n, cols) << shift
+        data = code if fmt == "fp8" else code[:, 0::2] | code[:, 1::2] << 4
+        blocks = cols // O.BLOCK[fmt]
+        low = {"nv4": 0x38}.get(fmt, 127)                # scales 1 and 2
+        byte = low + (8 if fmt == "nv4" else 1) * pick(n, blocks)
+        scale = torch.full((t.scale.numel(),), 0x7f if fmt == "nv4" else 0xff, dtype=torch.uint8, device="cuda")
+        at = torch.tensor(O.scale_layout(n, blocks), device="cuda")
+        scale[at.reshape(-1)] = 0
+        scale[at[:, :blocks].reshape(-1)] = byte.reshape(-1)
+        t.data.copy_(data.reshape(-1))
+        t.scale.copy_(scale)
+        value = torch.where(code & (two if fmt != "fp8" else 0x40) != 0, 2.0, 1.0) * (1.0 - 2.0 * (code >> shift))
+        step = torch.where(byte == low, 1.0, 2.0).repeat_interleave(O.BLOCK[fmt], 1)
+        return t, (value * step).double()
+    (x, xv), (w, wv) = make(rows), make(outs)
+    y = torch.full((rows, (outs + 7) // 8 * 8), 0.5, device="cuda")
+    R.mx_linear(x, w, y[:, :outs])
+    assert torch.equal(y[:, :outs].double(), xv @ wv.t())
+    assert bool((y[:, outs:] == 0.5).all()) and engine().status() == 0
