@@ -85,6 +85,8 @@ struct eagle_ctx {
   // the cache writes that this context's last ordering kernel stands behind, and its stream (prefix_at_rest)
   unsigned long long writes_done = 0;
   cudaStream_t done_on = nullptr;
+  // clusters of a size that the GPU holds at once (launch_linear): by format, pairs or not, and size; 0: not asked yet
+  int clusters[3][2][9] = {};
 };
 
 namespace eagle {

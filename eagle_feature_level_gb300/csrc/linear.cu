@@ -679,6 +679,39 @@ template <int FMT>
 LinearKernel kernel_of(bool pair) {
   return pair ? linear_kernel<FMT, true> : linear_kernel<FMT, false>;
 }
+LinearKernel kernel_of(int format, bool pair) {
+  return format == EAGLE_MX_FP8   ? kernel_of<EAGLE_MX_FP8>(pair)
+         : format == EAGLE_MX_FP4 ? kernel_of<EAGLE_MX_FP4>(pair)
+                                  : kernel_of<EAGLE_NV_FP4>(pair);
+}
+
+// Clusters that the GPU holds at once.  A cluster lies within a group of SMs, so that sizes that do not divide a group's
+// leave SMs over: 152 SMs hold 46 clusters of 3 CTAs, 36 of 4, 28 of 5, 23 of 6, 15 of 7 or 8.  One more begins when the
+// others have gone through all their tiles (3 x 15488 x 3633 in 8 bits, 29 tiles: by 30 clusters of 5, of which 28 run,
+// 25.2 us, by 29 of 4 15.5).
+int clusters_of(eagle_ctx* ctx, int format, bool pair, int ctas) {
+  if (ctas == 1) return ctx->sm_count;
+  int& known = ctx->clusters[format - 1][pair][ctas];
+  if (known == 0) {
+    const LinearKernel k = kernel_of(format, pair);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctx->sm_count / ctas * ctas);
+    cfg.blockDim = dim3(LN_THREADS);
+    cfg.dynamicSmemBytes = LN_SMEM;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (smem_limit_once(reinterpret_cast<const void*>(k), static_cast<int>(LN_SMEM)) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&known, k, &cfg) != cudaSuccess || known < 1) {
+      cudaGetLastError();
+      known = ctx->sm_count / ctas;
+    }
+  }
+  return known;
+}
 
 }  // namespace
 
@@ -742,7 +775,7 @@ cudaError_t launch_linear(eagle_ctx* ctx, const eagle_mx* x, const eagle_mx* w, 
   double least = 1e30;
   auto consider = [&](const Choice& c) {
     settle(c);
-    const int clusters = ctx->sm_count / (c.pair ? 2 : c.split);
+    const int clusters = clusters_of(ctx, fmt, c.pair, c.pair ? 2 : c.split);
     const double bytes = p.stage_bytes;
     const double active = std::min(p.tiles, clusters) * (c.pair ? 2.0 : c.split) / ctx->sm_count;
     const double weights = p.once ? (LN_A_BYTES + 512.0 * gps) * std::max(active / 24.0, 1.0 / 33.0) : 0.0;
@@ -784,13 +817,11 @@ cudaError_t launch_linear(eagle_ctx* ctx, const eagle_mx* x, const eagle_mx* w, 
   if (best.pair && (!encode_scales(ctx, &asc, a->scale, p.a_blocks, p.groups, gps) ||
                     !encode_scales(ctx, &bsc, b->scale, p.b_blocks, p.groups, gps)))
     return cudaErrorInvalidValue;
-  const LinearKernel k = fmt == EAGLE_MX_FP8   ? kernel_of<EAGLE_MX_FP8>(best.pair)
-                         : fmt == EAGLE_MX_FP4 ? kernel_of<EAGLE_MX_FP4>(best.pair)
-                                               : kernel_of<EAGLE_NV_FP4>(best.pair);
+  const LinearKernel k = kernel_of(fmt, best.pair);
   cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(k), static_cast<int>(LN_SMEM));
   if (e != cudaSuccess) return e;
   const int ctas = best.pair ? 2 : p.split;
-  const int clusters = std::min(p.tiles, ctx->sm_count / ctas);
+  const int clusters = std::min(p.tiles, clusters_of(ctx, fmt, best.pair, ctas));
   p.stamp = stamp_slot(ctx, EAGLE_K_LINEAR);
   trace_before(ctx, EAGLE_K_LINEAR, st);
   e = ctas > 1 ? launch_pdl_cluster(k, dim3(clusters * ctas), dim3(LN_THREADS), smem, st, ctas, am, bm, asc, bsc, p)

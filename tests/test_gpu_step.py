@@ -1074,3 +1074,13 @@ def test_linear_exact_products_on_every_path(fmt, rows, cols, outs):
     R.mx_linear(x, w, y[:, :outs])
     assert torch.equal(y[:, :outs].double(), xv @ wv.t())
     assert bool((y[:, outs:] == 0.5).all()) and engine().status() == 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("rows,cols,outs", [(130, 6528, 3787), (579, 4800, 912), (18, 1344, 3149), (134, 6240, 2149), (1, 1408, 2959),
+                                            (67, 2368, 955), (1008, 4416, 267), (842, 8512, 261), (52, 2176, 146), (17, 1600, 130),
+                                            (52, 1568, 139), (609, 11360, 259), (1, 1024, 131), (17, 1952, 129), (1, 1600, 131),
+                                            (52, 1824, 132), (3, 15488, 3633), (10, 13728, 3692)])
+def test_linear_exact_products_in_parts(fmt, rows, cols, outs):
+    """The same by 2 to 8 CTAs a tile, a single stage each at the least, with as many clusters as the GPU holds and fewer."""
+    test_linear_exact_products_on_every_path(fmt, rows, cols, outs)
