@@ -136,8 +136,8 @@ def _each(t: Optional[torch.Tensor], n: int, dtype, device) -> Optional[int]:
     return _p(t)
 
 
-def _filter(temperature, top_k, top_p, min_p, requests: int, rows_each: int, rows_used) -> B.eagle_filter:
-    dev = next((t.device for t in (temperature, top_k, top_p, min_p, rows_used) if t is not None), None)
+def _filter(eng: Engine, temperature, top_k, top_p, min_p, requests: int, rows_each: int, rows_used) -> B.eagle_filter:
+    dev = eng.ws.device
     f = B.eagle_filter(_each(temperature, requests, torch.float32, dev), _each(top_k, requests, torch.int32, dev),
                        _each(top_p, requests, torch.float32, dev), _each(min_p, requests, torch.float32, dev), rows_each,
                        _each(rows_used, requests, torch.int32, dev))
@@ -253,7 +253,7 @@ class Round:
         if top_k is None and top_p is None and min_p is None:
             self.filter_c = None
             return
-        self.filter_c = _filter(self.temps, top_k, top_p, min_p, self.B, self.S, self.t_size)
+        self.filter_c = _filter(self.eng, self.temps, top_k, top_p, min_p, self.B, self.S, self.t_size)
 
     # ---- the calls ------------------------------------------------------------
     def draft_and_tree(self, w_c: B.eagle_draft_weights):
@@ -507,14 +507,15 @@ class MxTensor:
         """data, scale: memory of another matrix of at least as many rows, to share."""
         self.eng, self.rows, self.cols, self.fmt = eng, rows, cols, fmt
         n_data, n_scale = B.eagle_mx_layout(MX_FORMATS[fmt], rows, cols)
-        u8 = dict(dtype=torch.uint8, device=eng.device)
+        dev = eng.ws.device
+        u8 = dict(dtype=torch.uint8, device=dev)
         self.data = torch.empty(n_data, **u8) if data is None else data
         self.scale = torch.empty(n_scale, **u8) if scale is None else scale
         for t, n in ((self.data, n_data), (self.scale, n_scale)):
-            if t.dtype != torch.uint8 or t.numel() < n or not t.is_contiguous() or not t.is_cuda:
-                raise ValueError(f"needs {n} contiguous bytes on a GPU")
+            if t.dtype != torch.uint8 or t.numel() < n or not t.is_contiguous() or t.device != dev or not t.is_cuda:
+                raise ValueError(f"needs {n} contiguous bytes on {dev}, a GPU")
         self.tensor_scale = tensor_scale
-        self.c = B.eagle_mx(_p(self.data), _p(self.scale), _each(tensor_scale, 1, torch.float32, self.data.device), rows,
+        self.c = B.eagle_mx(_p(self.data), _p(self.scale), _each(tensor_scale, 1, torch.float32, dev), rows,
                             cols, MX_FORMATS[fmt])
 
     def first(self, rows: int) -> "MxTensor":
@@ -536,9 +537,15 @@ class MxTensor:
         return out
 
 
+def _same_gpu(eng: Engine, m: MxTensor):
+    if m.data.device != eng.ws.device:
+        raise ValueError(f"needs a matrix on {eng.ws.device}")
+
+
 def mx_linear(x: MxTensor, w: MxTensor, out: torch.Tensor, bias: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """out [x.rows][w.rows] (bf16 or fp32) = x w^T + bias."""
+    """out [x.rows][w.rows] (bf16 or fp32) = x w^T + bias, on x's engine."""
     e = x.eng
+    _same_gpu(e, w)
     dt, at, ld = _rows2d(out, x.rows, w.rows, x.data.device)
     B.eagle_mx_linear(e.ctx, x.c, w.c, _each(bias, w.rows, torch.float32, out.device), dt, at, ld, e.ws.data_ptr(),
                       e.stream())
@@ -551,16 +558,19 @@ def add_norm(eng: Engine, x: torch.Tensor, out, gain: Optional[torch.Tensor] = N
     """h = x + residual (into residual_out); out = h / sqrt(mean(h^2) + eps) * gain, `out` a bf16 or fp32 tensor or an
     MxTensor.  eps: the engine's rms_eps."""
     rows, cols = x.shape
-    dt, xp, ld = _rows2d(x, rows, cols, x.device)
+    dev = eng.ws.device
+    dt, xp, ld = _rows2d(x, rows, cols, dev)
     none = (B.DTYPE_F32, None, 0)
-    rd, rp, rl = none if residual is None else _rows2d(residual, rows, cols, x.device)
-    od, op, ol = none if residual_out is None else _rows2d(residual_out, rows, cols, x.device)
+    rd, rp, rl = none if residual is None else _rows2d(residual, rows, cols, dev)
+    od, op, ol = none if residual_out is None else _rows2d(residual_out, rows, cols, dev)
     if residual is not None and residual_out is not None and rd != od:
         raise ValueError("residual and residual_out have one type")
     mx = out if isinstance(out, MxTensor) else None
-    yd, yp, yl = none if mx is not None else _rows2d(out, rows, cols, x.device)
+    if mx is not None:
+        _same_gpu(eng, mx)
+    yd, yp, yl = none if mx is not None else _rows2d(out, rows, cols, dev)
     n = B.eagle_norm(rows, cols, dt, xp, ld, rd if residual is not None else od, rp, rl, op, ol,
-                     _each(gain, cols, torch.float32, x.device), eng.dims_c.rms_eps if eps is None else eps, yd, yp, yl,
+                     _each(gain, cols, torch.float32, dev), eng.dims_c.rms_eps if eps is None else eps, yd, yp, yl,
                      B.ref(None if mx is None else mx.c))
     B.eagle_add_norm(eng.ctx, n, eng.ws.data_ptr(), eng.stream())
     return out
@@ -574,7 +584,7 @@ class Sampler:
                  top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
                  min_p: Optional[torch.Tensor] = None, rows_each: int = 1, rows_used: Optional[torch.Tensor] = None):
         self.eng, self.requests, self.rows_each = eng, requests, rows_each
-        self.c = _filter(temperature, top_k, top_p, min_p, requests, rows_each, rows_used)
+        self.c = _filter(eng, temperature, top_k, top_p, min_p, requests, rows_each, rows_used)
 
     def __call__(self, logits: torch.Tensor, u: Optional[torch.Tensor] = None, token: Optional[torch.Tensor] = None,
                  argmax: Optional[torch.Tensor] = None, probs: Optional[torch.Tensor] = None):
@@ -583,7 +593,7 @@ class Sampler:
         n, V = logits.shape
         if not 1 <= n <= self.requests * self.rows_each:
             raise ValueError(f"1 to {self.requests * self.rows_each} rows")
-        dev = logits.device
+        dev = self.eng.ws.device
         dt, zp, ld = _rows2d(logits, n, V, dev)
         pp, pl = (None, 0) if probs is None else _rows2d(probs, n, V, dev, (torch.float32,))[1:]
         if u is not None and u.dtype == torch.uint32:
