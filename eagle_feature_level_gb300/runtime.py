@@ -118,13 +118,18 @@ def _packed(specs, device):
 
 
 _DTYPE = {torch.bfloat16: B.DTYPE_BF16, torch.float32: B.DTYPE_F32}
+_INT_MAX = (1 << 31) - 1
 
 
 def _rows2d(t: torch.Tensor, rows: int, cols: int, device, types=_DTYPE):
-    """(type, address, pitch) of [rows][cols] with contiguous rows."""
+    """(type, address, pitch) of [rows][cols] with contiguous rows.  The ABI's sizes are ints of 32 bits, and ctypes would
+    cut off what is more."""
     if t.dtype not in types or t.shape != (rows, cols) or (cols > 1 and t.stride(1) != 1) or t.device != device or not t.is_cuda:
         raise ValueError(f"needs [{rows}][{cols}] of {[str(x) for x in types]} with contiguous rows on {device}, a GPU")
-    return _DTYPE[t.dtype], _p(t), (t.stride(0) if rows > 1 else -(-cols // 8) * 8)
+    pitch = t.stride(0) if rows > 1 else -(-cols // 8) * 8
+    if max(rows, cols, pitch) > _INT_MAX:
+        raise ValueError(f"{rows} rows of {cols}, {pitch} apart: at most {_INT_MAX} of each")
+    return _DTYPE[t.dtype], _p(t), pitch
 
 
 def _each(t: Optional[torch.Tensor], n: int, dtype, device) -> Optional[int]:
@@ -138,6 +143,8 @@ def _each(t: Optional[torch.Tensor], n: int, dtype, device) -> Optional[int]:
 
 def _filter(eng: Engine, temperature, top_k, top_p, min_p, requests: int, rows_each: int, rows_used) -> B.eagle_filter:
     dev = eng.ws.device
+    if rows_each > _INT_MAX:
+        raise ValueError(f"at most {_INT_MAX} rows each")
     f = B.eagle_filter(_each(temperature, requests, torch.float32, dev), _each(top_k, requests, torch.int32, dev),
                        _each(top_p, requests, torch.float32, dev), _each(min_p, requests, torch.float32, dev), rows_each,
                        _each(rows_used, requests, torch.int32, dev))

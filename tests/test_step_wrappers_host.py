@@ -1,5 +1,5 @@
-"""What the wrappers of the target's step refuse before they call the library: tensors of another GPU than the engine's.  On
-the host alone, with stand-ins for tensors."""
+"""What the wrappers of the target's step refuse before they call the library: tensors of another GPU than the engine's, and
+sizes that an int of 32 bits does not hold.  On the host alone, with stand-ins for tensors."""
 import math
 
 import pytest
@@ -105,3 +105,24 @@ def test_a_rounds_filter_is_on_its_engines_gpu(env):
     rd.temps, rd.t_size = Tensor(4, gpu=1), Tensor(4, dtype=torch.int32, gpu=1)
     with pytest.raises(ValueError):
         rd.set_filter(top_p=Tensor(4, gpu=1))
+
+
+def test_sizes_that_an_int_does_not_hold(env):
+    """As 32 bits they would look like the right ones."""
+    R, eng, reached = env
+    big = 1 << 32
+    a = matrix(R, eng, 4, 64)
+    far = lambda dtype=torch.float32: Tensor(4, 64, dtype=dtype, pitch=big + 64)
+    s = R.Sampler(eng, 4)
+    for call in (lambda: a.quantize(far()), lambda: a.unpack(far(torch.bfloat16)),
+                 lambda: R.mx_linear(a, matrix(R, eng, 64, 64), far()),
+                 lambda: R.add_norm(eng, far(), Tensor(4, 64)), lambda: R.add_norm(eng, Tensor(4, 64), far()),
+                 lambda: R.add_norm(eng, Tensor(4, 64), Tensor(4, 64), residual=far()),
+                 lambda: s(far(), argmax=Tensor(4, dtype=torch.int32)), lambda: s(Tensor(4, 64), probs=far()),
+                 lambda: R.add_norm(eng, Tensor(big + 4, 64), Tensor(big + 4, 64)),
+                 lambda: R.Sampler(eng, 1, rows_each=big + 4)):
+        with pytest.raises(ValueError):
+            call()
+    assert reached == []
+    a.quantize(Tensor(4, 64, pitch=(1 << 31) - 64))
+    assert reached == ["eagle_mx_quantize"]
