@@ -127,8 +127,8 @@ def _rows2d(t: torch.Tensor, rows: int, cols: int, device, types=_DTYPE):
     if t.dtype not in types or t.shape != (rows, cols) or (cols > 1 and t.stride(1) != 1) or t.device != device or not t.is_cuda:
         raise ValueError(f"needs [{rows}][{cols}] of {[str(x) for x in types]} with contiguous rows on {device}, a GPU")
     pitch = t.stride(0) if rows > 1 else -(-cols // 8) * 8
-    if max(rows, cols, pitch) > _INT_MAX:
-        raise ValueError(f"{rows} rows of {cols}, {pitch} apart: at most {_INT_MAX} of each")
+    if pitch > _INT_MAX or rows > _INT_MAX:              # (a pitch below cols is refused behind this)
+        raise ValueError(f"{rows} rows, {pitch} apart: at most {_INT_MAX} of either")
     return _DTYPE[t.dtype], _p(t), pitch
 
 
