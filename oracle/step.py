@@ -53,7 +53,8 @@ def quantize(fmt: str, x: np.ndarray, g: float = 1.0) -> Tuple[np.ndarray, np.nd
         byte = np.where(top > 0, nearest_code(E4M3, t), 0)
         d = E4M3[byte].astype(np.float32) * g
         with np.errstate(over="ignore"):
-            q = np.where(d[..., None] > 0, b.astype(np.float32) / np.where(d > 0, d, np.float32(1))[..., None],
+            some = d >= np.float32(2.0 ** -126)      # (elements are zeros where d is less)
+            q = np.where(some[..., None], b.astype(np.float32) / np.where(some, d, np.float32(1))[..., None],
                          np.float32(0)).astype(np.float64)
     else:
         byte = np.searchsorted(2.0 ** np.arange(-127, 128), top / (448.0 if fmt == "fp8" else 6.0), side="left")

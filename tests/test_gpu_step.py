@@ -1084,3 +1084,16 @@ def test_linear_exact_products_on_every_path(fmt, rows, cols, outs):
 def test_linear_exact_products_in_parts(fmt, rows, cols, outs):
     """The same by 2 to 8 CTAs a tile, a single stage each at the least, with as many clusters as the GPU holds and fewer."""
     test_linear_exact_products_on_every_path(fmt, rows, cols, outs)
+
+
+def test_quantize_factors_near_the_smallest():
+    """NV_FP4 under factors so small that scale * factor passes below the normal numbers, where elements are zeros."""
+    r = np.random.default_rng(2)
+    x = (r.standard_normal((40, 64)) * 2.0 ** r.integers(-126, -110, (40, 4)).repeat(16, 1)).astype(np.float32)
+    x[0] = 2.0 ** -124
+    for e in (-110, -117, -120, -124, -126, -127, -130, -140, -149):
+        t = mx("nv4", 40, 64, 2.0 ** e).quantize(torch.tensor(x, device="cuda"))
+        is_quantized(t, x.astype(np.float64))
+        y = t.unpack(torch.empty(40, 64, device="cuda"))
+        assert np.array_equal(f64(y), held(t))
+    assert engine().status() == 0

@@ -69,3 +69,20 @@ def test_distribution_is_the_filters_in_turn():
         assert np.allclose(w / w.sum(), np.where(np.isin(np.arange(60), alive), q, 0) / q[alive].sum(), atol=1e-9)
     w = O.distribution([1.0, 3.0, 3.0], 0.0)
     assert list(w) == [0, 1 << 40, 0] and draw_one(w, 0xffffffff) == 1
+
+
+def test_nv4_elements_under_the_smallest_normal_scale_are_zeros():
+    """d = scale * factor below 2^-126: the elements are zeros, with their signs, whatever the block holds."""
+    x = np.full((3, 16), 2.0 ** -124)
+    x[:, 1::2] *= -1
+    x[1:] *= [[2.0], [16.0]]
+    for e in (-127, -130, -149):
+        g = 2.0 ** e
+        code, byte = O.quantize("nv4", x, g)
+        assert byte.all() and np.array_equal(code >> 3, np.signbit(x).astype(int))
+        d = (O.E4M3[byte].astype(np.float32) * np.float32(g)).astype(np.float64)[:, 0]
+        assert np.array_equal((code & 7).any(1), d >= 2.0 ** -126)
+    code, byte = O.quantize("nv4", x[:1], 2.0 ** -127)   # largest / (6 g) = 4 / 3: the scale 1.375, its d 1.375 2^-127
+    assert O.E4M3[byte[0, 0]] == 1.375 and not (code & 7).any()
+    code, byte = O.quantize("nv4", x[1:2], 2.0 ** -127)  # 8 / 3: the scale 2.75, d 1.375 2^-126, elements 8 / 1.375
+    assert O.E4M3[byte[0, 0]] == 2.75 and (O.E2M1[code & 7] == 6.0).all()
