@@ -65,7 +65,13 @@ __device__ __forceinline__ float mx_rcp(float x) {
   return y;
 }
 
-// The tensor's factor as quantisations take it: 6 g and its inverse.
+// Divisors under which a Newton step's remainder may have bits below fp32's smallest number, 2^-149 (a quotient's last bit
+// times the divisor's: from 2^-10 on, the smallest border of a scale, 2^-33 2^-23 d), so that near a border the quotient would
+// not be the rounded one; above the inverse of it the inverse loses its own.  There a scale's quotient is a division, and
+// elements and their divisor are taken 2^64 times larger.
+constexpr float MX_SMALL = 0x1p-80f;
+
+// The tensor's factor as quantisations take it: 6 g and its inverse, infinite where quotients are divisions.
 struct MxFactor {
   float g, g6, r6;
 };
@@ -73,7 +79,7 @@ __device__ __forceinline__ MxFactor mx_factor(const MxView& m) {
   MxFactor f;
   f.g = m.g ? *m.g : 1.0f;
   f.g6 = 6.0f * f.g;
-  f.r6 = 1.0f / f.g6;
+  f.r6 = f.g6 >= MX_SMALL && f.g6 <= 1.0f / MX_SMALL ? 1.0f / f.g6 : INFINITY;
   return f;
 }
 
@@ -108,9 +114,13 @@ __device__ __forceinline__ bool mx_put(const MxView& m, const MxFactor& f, int r
                        : static_cast<uint32_t>(__nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3));
     const float d = mx_decode_e4m3(byte) * f.g;
     const float r = d >= 0x1p-126f ? mx_rcp(d) : 0.0f;
-    if (__any_sync(0xffffffffu, most * r > 1e30f)) {   // elements far beyond 6, whose remainder may not be finite
+    // elements far beyond 6, whose remainder may not be finite, and small divisors
+    if (__any_sync(0xffffffffu, fmaxf(most, 1e30f * MX_SMALL) * r > 1e30f)) {
+      const bool small = r > 1.0f / MX_SMALL;
+      const float up = small ? 0x1p64f : 1.0f, down = small ? 0x1p-64f : 1.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = fabsf(x[i] * r) < 16.0f ? mx_quotient(x[i], d, r) : x[i] * r;
+      for (int i = 0; i < 8; ++i)
+        v[i] = fabsf(x[i] * r) < 16.0f ? mx_quotient(x[i] * up, d * up, r * down) : x[i] * r;
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = mx_quotient(x[i], d, r);

@@ -1097,3 +1097,30 @@ def test_quantize_factors_near_the_smallest():
         y = t.unpack(torch.empty(40, 64, device="cuda"))
         assert np.array_equal(f64(y), held(t))
     assert engine().status() == 0
+
+
+@pytest.mark.parametrize("e", [-126, -124, -118, -110, -102, -90, -81, -79, -60, 0, 60, 90, 110])
+def test_quantize_next_to_ties_under_any_factor(e):
+    """NV_FP4 quotients on a tie and up to two steps beside it, of elements and of scales, whose remainders under small factors
+    are below fp32's smallest number; and factors whose multiple of six fp32 does not hold."""
+    r = np.random.default_rng(200 + e)
+    for turn in range(6):
+        g = np.float32((1 + r.random()) * 2.0 ** e)
+        ties = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+        x = (r.choice(ties, (64, 256)) * float(g)).astype(np.float32)
+        x = (x.view(np.int32) + r.integers(-2, 3, x.shape, dtype=np.int32)).view(np.float32)
+        x[:, ::16] = np.float32(6) * g                   # the block's largest: its scale is 1
+        x *= r.choice(np.float32([-1, 1]), x.shape)
+        is_quantized(mx("nv4", 64, 256, g).quantize(torch.tensor(x, device="cuda")), x.astype(np.float64))
+        border = (O.E4M3[1:] + O.E4M3[:-1]) / 2
+        with np.errstate(over="ignore"):
+            x = (r.choice(border, (64, 16)) * 6 * float(g)).astype(np.float32)
+        x = np.where(np.isfinite(x), x, np.float32(3e38))
+        x = (x.view(np.int32) + r.integers(-2, 3, x.shape, dtype=np.int32)).view(np.float32)
+        y = np.zeros((64, 256), np.float32)
+        y[:, 3::16] = x
+        is_quantized(mx("nv4", 64, 256, g).quantize(torch.tensor(y, device="cuda")), y.astype(np.float64))
+    for g in (5e37, 6e37, 3.4e38):                       # 6 g up to infinity, a quotient of 0
+        y[0, :16] = 3e38
+        is_quantized(mx("nv4", 64, 256, g).quantize(torch.tensor(y, device="cuda")), y.astype(np.float64))
+    assert engine().status() == 0
