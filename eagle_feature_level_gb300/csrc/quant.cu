@@ -28,14 +28,15 @@ struct QuantParams {
   uint64_t* stamp;
 };
 
-// e^(-a) to two steps of fp32: 2^y of y = -a log2(e), the low part of that product put right behind it.
+// e^(-a) to two steps of fp32: 2^y of y = -a log2(e), the low part of that product put right behind it (up to the largest
+// number: a half step of y is 2^-18.5 of the power there).
 __device__ __forceinline__ float exp_minus(float a) {
   constexpr float L = 0x1.715476p+0f, L_LOW = 0x1.4ae0cp-26f, LN2 = 0x1.62e43p-1f;
   const float y = -a * L;
   const float low = fmaf(-a, L, -y) - a * L_LOW;
   float e;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(y));
-  return fabsf(y) < 126.0f ? fmaf(e, low * LN2, e) : e;
+  return fabsf(y) < 128.0f ? fmaf(e, low * LN2, e) : e;
 }
 // SiLU(a) b in fp32.
 __device__ __forceinline__ float gated(float a, float b) {

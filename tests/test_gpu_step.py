@@ -1124,3 +1124,15 @@ def test_quantize_next_to_ties_under_any_factor(e):
         y[0, :16] = 3e38
         is_quantized(mx("nv4", 64, 256, g).quantize(torch.tensor(y, device="cuda")), y.astype(np.float64))
     assert engine().status() == 0
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+def test_quantize_gated_near_the_largest_exponential(fmt):
+    """Gates whose e^(-a) is near fp32's largest number, partners that bring the products back: as near as elsewhere."""
+    r = gen(31)
+    a = -87.34 - 1.37 * torch.rand(256, 11008, generator=r, device="cuda")
+    b = torch.randn(256, 11008, generator=r, device="cuda") * 2.0 ** 120
+    x = torch.cat((a, b), 1)
+    t = mx(fmt, 256, 11008).quantize(x, swiglu=True)
+    is_quantized(t, O.swiglu(f64(x)), 2.0 ** -21)
+    assert engine().status() == 0
