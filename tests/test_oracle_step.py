@@ -86,3 +86,23 @@ def test_nv4_elements_under_the_smallest_normal_scale_are_zeros():
     assert O.E4M3[byte[0, 0]] == 1.375 and not (code & 7).any()
     code, byte = O.quantize("nv4", x[1:2], 2.0 ** -127)  # 8 / 3: the scale 2.75, d 1.375 2^-126, elements 8 / 1.375
     assert O.E4M3[byte[0, 0]] == 2.75 and (O.E2M1[code & 7] == 6.0).all()
+
+
+def test_draws_are_as_frequent_as_their_weights():
+    """Over all 2^32 words a token is drawn as often as its weight says, to one word: counted from where the draw changes."""
+    rng = np.random.default_rng(6)
+    for t, k, p, m in ((1.0, 0, 1.0, 0.0), (0.7, 5, 1.0, 0.0), (1.4, 0, 0.8, 0.0), (1.0, 0, 1.0, 0.1), (0.9, 12, 0.9, 0.02)):
+        w = O.distribution(rng.standard_normal(25) * 2, t, k, p, m)
+        total, first, before = int(w.sum()), 0, 0
+        for i in np.flatnonzero(w):
+            before += int(w[i])
+            end = -(-(before << 32) // total)            # the first word whose share reaches the weights up to i
+            assert draw_one(w, first) == i and draw_one(w, end - 1) == i
+            assert abs((end - first) - 2 ** 32 * int(w[i]) / total) <= 1
+            first = end
+        assert first == 2 ** 32
+    words = rng.integers(0, 2 ** 32, 40000)
+    n = np.bincount([draw_one(w, int(u)) for u in words], minlength=25)
+    share = w / w.sum()
+    assert not n[w == 0].any()
+    assert (np.abs(n - 40000 * share) <= 6 * np.sqrt(40000 * share) + 1).all()
