@@ -1136,3 +1136,21 @@ def test_quantize_gated_near_the_largest_exponential(fmt):
     t = mx(fmt, 256, 11008).quantize(x, swiglu=True)
     is_quantized(t, O.swiglu(f64(x)), 2.0 ** -21)
     assert engine().status() == 0
+
+
+def test_linear_first_call_is_captured():
+    """A context's first products under capture: what a plan asks the runtime for may be asked there."""
+    e = R.Engine(engine().dims, max_batch=64, max_rows=8, max_expanded=1, max_children=1, max_tree=2, max_prefix=64, device="cuda")
+    for rows, cols, outs in ((17, 1600, 130), (1162, 960, 2083), (31, 3840, 8587)):
+        x, w = R.MxTensor(e, rows, cols, "fp8"), R.MxTensor(e, outs, cols, "fp8")
+        x.quantize(normal(rows, rows, cols)), w.quantize(normal(outs, outs, cols) * 0.1)
+        y, z = (torch.zeros(rows, (outs + 7) // 8 * 8, device="cuda") for _ in range(2))
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            R.mx_linear(x, w, y[:, :outs])
+        g.replay()
+        R.mx_linear(x, w, z[:, :outs])
+        assert torch.equal(y, z) and bool(z[:, :outs].any())
+    assert e.status() == 0
+    e.close()
