@@ -13,12 +13,13 @@
 // products.
 //
 // Bound, many rows: what an SM takes in, 64 bytes a cycle: a stage of 192 rows of B is 46 KB for a CTA alone and 34 KB for
-// one of a pair (4096 x 8192 x 10240, NV_FP4: 148 and 120 us, 5.7 PFLOP/s), 720 and 530 cycles for products of 384.  Few
-// rows: the weights' bytes from memory (16 x 8192 x 32000: 25 us, 6.0 TB/s; 1 x 4096 x 12288: 7.8, 3.6 TB/s, of which some
-// 4 us until the first products and behind the last).
+// one of a pair (4096 x 8192 x 10240, NV_FP4: 148 and 120 us, 5.7 PFLOP/s), 720 and 530 cycles for products of 384; in 8 bits the
+// same bytes are half the products, 233 us, 2.95 PFLOP/s).  Few rows: the weights' bytes from memory (16 x 8192 x 32000,
+// NV_FP4: 26 us, 5.8 TB/s, 8 bits 45, 6.1; 1 x 4096 x 12288: 7.9, 3.6 TB/s, of which some 4 us until the first products and
+// behind the last).
 //
 // Few tiles: a cluster of up to 8 CTAs splits a tile's inner dimension; each writes its partial to its own shared memory
-// and sums its share of the rows over all of them, in rank order (8 x 8192 x 8192 in 8 bits: 14.9 us by two, 20.5 by one;
+// and sums its share of the rows over all of them, in rank order (8 x 8192 x 8192 in 8 bits: 16.1 us by two, 20.5 by one;
 // 96 x 27648 x 5120 in FP4 20.5 by three, 26 by two, 35 by one; 442 x 16640 x 1072 in 8 bits, tiles of 128 rows by four
 // 19.5, of 64 by two 25.7).
 #include <algorithm>

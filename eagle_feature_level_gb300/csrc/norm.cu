@@ -7,7 +7,9 @@
 // Bound: memory where rows are many (8192 x 8192 to 8 bits with the residual: 86 us, 470 MB, 5.5 TB/s; with blocks that end
 // with their rows 96), else the latency of a launch, of loads and of two sums (8 x 4096: 2.2 us; 777 x 5120 in fp32:
 // 12.8 us for 56 MB; past 16384 columns a block is alone on its SM: 777 x 28672 80 us, 313 MB).  Blocks of up to 512
-// threads are held to 64 registers, so that an SM has two: one waits for its sums while the other works.
+// threads are held to 64 registers, so that an SM has two: one waits for its sums while the other works.  Rows past 256
+// columns pay for that with spills: none from bf16 with a bf16 residual to bf16 or fp32, 64 bytes a thread with an fp32
+// residual, 32 to 104 from bf16 to a microscaled format, up to 216 where all is fp32; past 16384 columns 148 to 596.
 #include "internal.h"
 #include "common.cuh"
 #include "mx.cuh"

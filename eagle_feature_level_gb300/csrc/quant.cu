@@ -3,9 +3,10 @@
 // A warp takes 256 columns and goes down the rows, two in flight; a lane has eight columns: 16 or 32 bytes in, 4 or 8 out,
 // with a block's maximum and the four scales of a group exchanged between its lanes.
 //
-// Bound: memory, and with four bits nearly as much the instructions of an element (NV_FP4: its quotient, 4, and rounding):
-// 4096 x 8192 to NV_FP4 26 us (86 MB, 3.3 TB/s, issue slots 57 % full), 1001 x 11008 gated pairs to FP4 15.5 us (50 MB);
-// unpacking 8192 x 8192 in 8 bits 33.7 us (203 MB, 6.0 TB/s).
+// Bound: the latency of loads, which are waited for in the turn of the loop that asks for them: 4096 x 8192 to NV_FP4 26 us
+// (86 MB, 3.3 TB/s) with the issue slots 57 % full and half of the warps there, 1001 x 11008 gated pairs to FP4 15.6 us (50
+// MB, slots 52 % full).  Unpacking, which has nothing to exchange, is bound by memory: 8192 x 8192 in 8 bits 33.8 us (203 MB,
+// 6.0 TB/s).
 #include "internal.h"
 #include "common.cuh"
 #include "mx.cuh"

@@ -20,11 +20,16 @@
 // Weights from 2^23 on (the near tokens') take fixed point and pairs of floats, the others fp32.  Near tokens are a small
 // part of a row as a rule: a warp lists its own first, so that the work on them is dense.
 //
-// Bound: instructions where rows are flat (64 rows of 131072 in bf16: top-p of 0.95 at t = 1.3 85 us, issue slots of the
-// busy SMs full), else the latency of each kernel's loads and exchanges (greedy 15 us, top-k of 50 33, top-p of 0.7 at
-// t = 0.5 41, min-p of 0.05 28, no cut 43; a row of 32000: top-k of 400 and top-p 17).  A cluster of CTAs that keeps a row
-// in shared memory through all steps saves launches, but leaves the SMs waiting for its exchanges: those 64
-// rows 209, 26, 66, 89, 56 and 66 us, the one row 17, and 64 rows of all sorts 113 where this takes 55.
+// Bound: instructions where rows are flat (64 rows of 131072 in bf16: top-p of 0.95 at t = 1.3 89 us, issue slots of the
+// busy SMs full), else the latency of each kernel's loads and exchanges (greedy 11 us, 15 among controls, top-k of 50 33, top-p
+// of 0.7 at t = 0.5 41, min-p of 0.05 28, no cut 43; a row of 32000: top-k of 400 and top-p 17).  A cluster of CTAs that keeps
+// a row in shared memory through all steps saves launches, but leaves the SMs waiting for its exchanges: those 64
+// rows 209, 26, 66, 89, 56 and 66 us, the one row 17, and 64 rows of all sorts 113 where this takes 56.
+//
+// Where a list does not hold a row's tokens, one CTA goes over the row once for each of up to five levels of digits and a few
+// times more, and that takes as long as it is long: those 64 rows with top-k of 20000 and top-p of 0.9 520 us (one such row
+// 312), of 4000 at t = 2 436, top-p at t = 100 469, rows of one value throughout 1700; top-k of 20000 alone, whose list holds
+// its bin, 55.
 #include <algorithm>
 
 #include "internal.h"
