@@ -688,7 +688,7 @@ LinearKernel kernel_of(int format, bool pair) {
 
 // Clusters that the GPU holds at once.  A cluster lies within a group of SMs, so that sizes that do not divide a group's
 // leave SMs over: 152 SMs hold 46 clusters of 3 CTAs, 36 of 4, 28 of 5, 23 of 6, 15 of 7 or 8.  One more begins when the
-// others have gone through all their tiles (3 x 15488 x 3633 in 8 bits, 29 tiles: by 30 clusters of 5, of which 28 run,
+// others have gone through all their tiles (3 x 15488 x 3633 in 8 bits, 29 tiles: by clusters of 5, of which 28 run,
 // 25.2 us, by 29 of 4 15.5).
 int clusters_of(eagle_ctx* ctx, int format, bool pair, int ctas) {
   if (ctas == 1) return ctx->sm_count;
